@@ -28,3 +28,21 @@ from ._binding import (  # noqa: F401
     vc_reduce_scatter,
     vc_shard_count,
 )
+from .training import (  # noqa: F401
+    ACTIVATIONS,
+    COEFFICIENTS,
+    PreparedMuon,
+    PreparedOperator,
+    linear_backward_workspace,
+    linear_forward_workspace,
+    orthogonalize_workspace,
+    prepare_linear_backward,
+    prepare_linear_forward,
+    prepare_muon_step,
+    prepare_orthogonalize,
+    train_timeouts,
+    vc_linear_backward,
+    vc_linear_forward,
+    vc_muon_step,
+    vc_orthogonalize,
+)

@@ -20,8 +20,10 @@ BUILD = PKG / "_build"
 LIBDIR = PKG / "_lib"
 LIB = LIBDIR / "libvc.so"
 
-SOURCES = ["vc_api.cu", "vc_reduce_dispatch.cu", "vc_noalloc.cu", "vc_copy.cu", "vc_bucket.cu"]
-HEADERS = ["vc_device.cuh", "vc_launch.cuh", "vc_bucket_kernel.cuh"]
+SOURCES = ["vc_api.cu", "vc_reduce_dispatch.cu", "vc_noalloc.cu", "vc_copy.cu", "vc_bucket.cu",
+           "vc_gemm.cu", "vc_train_linear.cu", "vc_train_muon.cu"]
+HEADERS = ["vc_device.cuh", "vc_launch.cuh", "vc_bucket_kernel.cuh", "vc_gemm.cuh",
+           "vc_train_common.cuh"]
 # vc_reduce_inst.cu compiled once per (element type, op, order group):
 # (object, -D flags).  Groups: 0 ring + recursive halving, 1 tree, 2 double
 # binary tree.  The integer types have group 0 only (ring): their results
@@ -59,7 +61,7 @@ def _stale() -> bool:
         return True
     t = LIB.stat().st_mtime
     deps = [CSRC / s for s in SOURCES + HEADERS + [INSTANCE_SOURCE, BUCKET_SOURCE]] + [
-        INCLUDE / "vc.h", Path(__file__)]
+        INCLUDE / "vc.h", INCLUDE / "vc_train.h", Path(__file__)]
     return any(d.stat().st_mtime > t for d in deps)
 
 

@@ -1,0 +1,90 @@
+// Host side of the product kernel: tensor maps, and the count of waits that
+// ran out.
+#include <mutex>
+
+#include "vc_gemm.cuh"
+#include "vc_train.h"
+
+namespace vc {
+
+int sm_count();  // vc_api.cu
+
+namespace gemm {
+
+namespace {
+__device__ unsigned g_timeouts = 0;
+}
+
+// Looked up once per device (as sm_count does).
+unsigned* timeout_counter() {
+    constexpr int kMaxDevices = 64;
+    static std::mutex mu;
+    static unsigned* where[kMaxDevices] = {nullptr};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    if (where[dev] == nullptr) {
+        void* p = nullptr;
+        if (cudaGetSymbolAddress(&p, g_timeouts) != cudaSuccess) return nullptr;
+        where[dev] = static_cast<unsigned*>(p);
+    }
+    return where[dev];
+}
+
+int device_sms() { return sm_count(); }
+
+namespace {
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled through the runtime (the library does not link the
+// driver); looked up once.
+EncodeFn encoder() {
+    static std::once_flag once;
+    static EncodeFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(p);
+    });
+    return fn;
+}
+
+}  // namespace
+
+bool encode_operand(CUtensorMap* map, const Operand& o, int batch, int box_rows) {
+    EncodeFn fn = encoder();
+    if (fn == nullptr) return false;
+    // A stride is only meaningful with a second row (or matrix); the encoder
+    // still wants a multiple of 16 bytes.
+    const cuuint64_t row = o.outer > 1 ? (cuuint64_t)o.ld * 2 : (cuuint64_t)((o.inner + 7) / 8 * 16);
+    const cuuint64_t mat = batch > 1 ? (cuuint64_t)o.batch_stride * 2 : row;
+    const cuuint64_t dims[3] = {(cuuint64_t)o.inner, (cuuint64_t)o.outer, (cuuint64_t)batch};
+    const cuuint64_t strides[2] = {row, mat};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return fn(map, o.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void*>(o.data), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace gemm
+}  // namespace vc
+
+extern "C" vc_status_t vc_train_timeouts(unsigned* count) {
+    if (count == nullptr) return VC_ERR_INVALID_ARGUMENT;
+    const char* v = getenv("VC_TEST_FAIL_LAUNCH");
+    if (v != nullptr && v[0] != '\0' && v[0] != '0') return VC_ERR_CUDA;
+    const unsigned* p = vc::gemm::timeout_counter();
+    if (p == nullptr) return VC_ERR_CUDA;
+    return cudaMemcpy(count, p, sizeof *count, cudaMemcpyDeviceToHost) == cudaSuccess
+               ? VC_SUCCESS
+               : VC_ERR_CUDA;
+}

@@ -1,0 +1,394 @@
+// The linear layer with bias, activation and residual in its epilogue, and
+// its gradient.
+#include <algorithm>
+
+#include "vc_train_common.cuh"
+
+namespace vc {
+namespace train {
+namespace {
+
+using gemm::Operand;
+using gemm::Shape;
+using gemm::View;
+
+// ------------------------------------------------------------- epilogues --
+
+// y = act(acc + bias) + residual; z = acc + bias kept on request.
+struct EpiForward {
+    static constexpr bool kSym = false, kRows = true;
+    struct Params {
+        const __nv_bfloat16* bias;
+        View residual, y, preact;
+        int has_residual, has_preact, act, bias_vec;
+    };
+    struct Col {
+        float4 bias;
+    };
+    struct Aux {
+        float4 residual;
+    };
+    __device__ static void regs(const Params&, const Shape&, int, int, int, float (&)[32], bool) {}
+    __device__ static Col cols(const Params& p, const Shape&, int, int col, int n) {
+        Col c = {make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (p.bias != nullptr) c.bias = gemm::load4(p.bias + col, n, p.bias_vec);
+        return c;
+    }
+    __device__ static Aux load(const Params& p, const Shape&, int, int row, int col, int n) {
+        Aux a = {make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (p.has_residual) a.residual = gemm::view_load(p.residual, 0, row, col, n);
+        return a;
+    }
+    __device__ static void store(const Params& p, const Shape&, int, int row, int col, int n,
+                                 float4 v, const Aux& a, const Col& c) {
+        v.x += c.bias.x;
+        v.y += c.bias.y;
+        v.z += c.bias.z;
+        v.w += c.bias.w;
+        if (p.has_preact) gemm::view_store(p.preact, 0, row, col, n, v);
+        v.x = act_value(v.x, p.act) + a.residual.x;
+        v.y = act_value(v.y, p.act) + a.residual.y;
+        v.z = act_value(v.z, p.act) + a.residual.z;
+        v.w = act_value(v.w, p.act) + a.residual.w;
+        gemm::view_store(p.y, 0, row, col, n, v);
+    }
+};
+
+// out = acc, or out += acc.
+struct EpiStore {
+    static constexpr bool kSym = false, kRows = true;
+    struct Params {
+        View out;
+        int add;
+    };
+    struct Col {};
+    struct Aux {
+        float4 old;
+    };
+    __device__ static void regs(const Params&, const Shape&, int, int, int, float (&)[32], bool) {}
+    __device__ static Col cols(const Params&, const Shape&, int, int, int) { return {}; }
+    __device__ static Aux load(const Params& p, const Shape&, int, int row, int col, int n) {
+        Aux a = {make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (p.add) a.old = gemm::view_load(p.out, 0, row, col, n);
+        return a;
+    }
+    __device__ static void store(const Params& p, const Shape&, int, int row, int col, int n,
+                                 float4 v, const Aux& a, const Col&) {
+        v.x += a.old.x;
+        v.y += a.old.y;
+        v.z += a.old.z;
+        v.w += a.old.w;
+        gemm::view_store(p.out, 0, row, col, n, v);
+    }
+};
+
+template <class Epi>
+cudaError_t product(const Operand& a, const Operand& b, int M, int N, int K,
+                    const typename Epi::Params& ep, cudaStream_t st) {
+    return gemm::launch_tile<1, 128, Epi>(a, b, M, N, K, 1, ep, st);
+}
+
+// ------------------------------------------------------------ copy, dz, db --
+
+// A bf16 matrix copied to rows of ld_out values (a multiple of 8), so that
+// TMA can read it.  One warp per row step; element-wise reads.
+__global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* src, long long ld,
+                                                   __nv_bfloat16* dst, long long ld_out,
+                                                   long long rows, long long cols) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const long long warps = (long long)gridDim.x * 8;
+    for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
+        const __nv_bfloat16* s = src + r * ld;
+        __nv_bfloat16* d = dst + r * ld_out;
+        for (long long c = lane * 2; c < cols; c += 64) {
+            __nv_bfloat162 v;
+            v.x = s[c];
+            v.y = c + 1 < cols ? s[c + 1] : __float2bfloat16(0.0f);
+            *reinterpret_cast<__nv_bfloat162*>(d + c) = v;
+        }
+    }
+}
+
+struct DzParams {
+    View dy, preact;
+    __nv_bfloat16* dz;  // NULL: not written
+    long long ld_dz;
+    float* sums;  // [gridDim.y][N], or NULL
+    long long rows, cols;
+    int act;
+};
+
+// dz = dy * act'(z) and the column sums of each block's rows.  A warp covers
+// 128 columns of a row; the block's eight warps take its rows in turn.
+__global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzParams p) {
+    __shared__ float4 part[8][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long col = (long long)blockIdx.x * 128 + lane * 4;
+    const int n = (int)min(4ll, p.cols - col);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n > 0) {
+        for (long long row = (long long)blockIdx.y * 8 + warp; row < p.rows;
+             row += (long long)gridDim.y * 8) {
+            float4 v = gemm::view_load(p.dy, 0, row, (int)col, n);
+            if (p.act != VC_ACT_NONE) {
+                const float4 z = gemm::view_load(p.preact, 0, row, (int)col, n);
+                v.x *= act_slope(z.x, p.act);
+                if (n > 1) v.y *= act_slope(z.y, p.act);
+                if (n > 2) v.z *= act_slope(z.z, p.act);
+                if (n > 3) v.w *= act_slope(z.w, p.act);
+            }
+            if (p.dz != nullptr) gemm::store4(p.dz + row * p.ld_dz + col, v, n, true);
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+        }
+    }
+    if (p.sums == nullptr) return;
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && n > 0) {
+        for (int w = 1; w < 8; ++w) {
+            const float4 o = part[w][lane];
+            sum.x += o.x;
+            sum.y += o.y;
+            sum.z += o.z;
+            sum.w += o.w;
+        }
+        gemm::store4(p.sums + (long long)blockIdx.y * p.cols + col, sum, n, false);
+    }
+}
+
+// db (+)= the sum of the blocks' partial sums, in block order.
+__global__ void __launch_bounds__(256) db_kernel(const float* sums, int parts, long long cols,
+                                                 void* db, int f32, int add) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long col = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (col >= cols) return;
+    float v = 0.0f;
+    for (int i = 0; i < parts; ++i) v += sums[(long long)i * cols + col];
+    if (f32) {
+        float* d = static_cast<float*>(db) + col;
+        *d = add ? *d + v : v;
+    } else {
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(db) + col;
+        *d = __float2bfloat16(add ? __bfloat162float(*d) + v : v);
+    }
+}
+
+int dz_row_blocks(long long rows, long long cols) {
+    const long long across = (cols + 127) / 128;
+    const long long want = (152 * 8 + across - 1) / across;
+    return (int)std::max(1ll, std::min(want, (rows + 31) / 32));
+}
+
+// ----------------------------------------------------------- the operands --
+
+bool operand_ready(const vc_matrix_t* m) {
+    return gemm::tma_ready(m->data, m->rows > 1 ? m->ld : 0, 1, 0);
+}
+
+size_t packed_bytes(const vc_matrix_t* m) {
+    return operand_ready(m) ? 0 : round256((size_t)m->rows * padded_ld(m->cols) * 2);
+}
+
+// Where TMA reads the matrix: in place, or packed at *ws (advanced).
+cudaError_t ready_operand(const vc_matrix_t* m, unsigned char** ws, cudaStream_t st,
+                          const void** data, long long* ld) {
+    if (operand_ready(m) || m->rows == 0 || m->cols == 0) {
+        *data = m->data;
+        *ld = m->rows > 1 ? m->ld : padded_ld(m->cols);
+        return cudaSuccess;
+    }
+    *data = *ws;
+    *ld = padded_ld(m->cols);
+    const int blocks = (int)std::min(152 * 8ll, (m->rows + 7) / 8);
+    const cudaError_t e = launch_pdl(
+        pack_kernel, dim3(blocks), dim3(256), st, static_cast<const __nv_bfloat16*>(m->data),
+        m->rows > 1 ? m->ld : 0, reinterpret_cast<__nv_bfloat16*>(*ws), *ld, m->rows, m->cols);
+    *ws += packed_bytes(m);
+    return e;
+}
+
+bool is_bf16(const vc_matrix_t* m) { return m->dtype == VC_BFLOAT16; }
+
+bool plain_matrix(const vc_matrix_t* m, long long rows, long long cols) {
+    return valid_matrix(m) && m->batch == 1 && m->rows == rows && m->cols == cols;
+}
+
+bool valid_act(vc_act_t act) { return act >= VC_ACT_NONE && act <= VC_ACT_SILU; }
+
+bool workspace_ok(const void* ws, size_t have, size_t need) {
+    return need == 0 || (ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 15) == 0 && have >= need);
+}
+
+size_t backward_workspace(const vc_matrix_t* dy, const vc_matrix_t* x, const vc_matrix_t* weight,
+                          vc_act_t act, bool has_dbias) {
+    size_t need = packed_bytes(x) + packed_bytes(weight);
+    if (act != VC_ACT_NONE || !operand_ready(dy))
+        need += round256((size_t)dy->rows * padded_ld(dy->cols) * 2);
+    if (has_dbias) need += round256((size_t)dz_row_blocks(dy->rows, dy->cols) * dy->cols * 4);
+    return need;
+}
+
+}  // namespace
+}  // namespace train
+}  // namespace vc
+
+using namespace vc;
+using namespace vc::train;
+
+extern "C" {
+
+size_t vc_linear_forward_workspace(const vc_matrix_t* x, const vc_matrix_t* weight) {
+    if (!valid_matrix(x) || !valid_matrix(weight)) return 0;
+    return packed_bytes(x) + packed_bytes(weight);
+}
+
+vc_status_t vc_linear_forward(const vc_matrix_t* x, const vc_matrix_t* weight, const void* bias,
+                              const vc_matrix_t* residual, const vc_matrix_t* y,
+                              const vc_matrix_t* preact, vc_act_t act, void* workspace,
+                              size_t workspace_bytes, vc_stream_t stream) {
+    if (!valid_matrix(x) || !valid_matrix(weight) || !valid_act(act)) return VC_ERR_INVALID_ARGUMENT;
+    const long long M = x->rows, K = x->cols, N = weight->rows;
+    if (!plain_matrix(x, M, K) || !plain_matrix(weight, N, K) || !plain_matrix(y, M, N) ||
+        (residual != nullptr && !plain_matrix(residual, M, N)) ||
+        (preact != nullptr && !plain_matrix(preact, M, N)))
+        return VC_ERR_INVALID_ARGUMENT;
+    if (!is_bf16(x) || !is_bf16(weight) || !is_bf16(y) || (residual != nullptr && !is_bf16(residual)) ||
+        (preact != nullptr && !is_bf16(preact)))
+        return VC_ERR_INVALID_ARGUMENT;
+    if ((reinterpret_cast<uintptr_t>(bias) & 1) != 0) return VC_ERR_INVALID_ARGUMENT;
+    const size_t need = packed_bytes(x) + packed_bytes(weight);
+    if (!workspace_ok(workspace, workspace_bytes, need)) return VC_ERR_INVALID_ARGUMENT;
+    const Span outs[3] = {span_of(y), span_of(preact), span_of(workspace, need)};
+    const Span ins[4] = {span_of(x), span_of(weight), span_of(bias, (size_t)N * 2), span_of(residual)};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 4; ++i)
+            if (overlap(outs[o], ins[i]) &&
+                !(o == 0 && i == 3 && same_matrix(y, residual)))
+                return VC_ERR_ALIAS;
+        for (int q = 0; q < o; ++q)
+            if (overlap(outs[o], outs[q])) return VC_ERR_ALIAS;
+    }
+    if (M == 0 || N == 0) return VC_SUCCESS;
+    if (test_launch_failure()) return VC_ERR_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    Operand a = {nullptr, K, M, 0, 0, true, false}, b = {nullptr, K, N, 0, 0, true, false};
+    if (ready_operand(x, &ws, st, &a.data, &a.ld) != cudaSuccess ||
+        ready_operand(weight, &ws, st, &b.data, &b.ld) != cudaSuccess)
+        return VC_ERR_CUDA;
+    EpiForward::Params ep = {};
+    ep.bias = static_cast<const __nv_bfloat16*>(bias);
+    ep.bias_vec = (reinterpret_cast<uintptr_t>(bias) & 7) == 0;
+    ep.residual = view_of(residual);
+    ep.y = view_of(y);
+    ep.preact = view_of(preact);
+    ep.has_residual = residual != nullptr;
+    ep.has_preact = preact != nullptr;
+    ep.act = act;
+    const cudaError_t e = product<EpiForward>(a, b, (int)M, (int)N, (int)K, ep, st);
+    return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
+}
+
+size_t vc_linear_backward_workspace(const vc_matrix_t* dy, const vc_matrix_t* x,
+                                    const vc_matrix_t* weight, vc_act_t act, int has_dbias) {
+    if (!valid_matrix(dy) || !valid_matrix(x) || !valid_matrix(weight)) return 0;
+    return backward_workspace(dy, x, weight, act, has_dbias != 0);
+}
+
+vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
+                               const vc_matrix_t* weight, const vc_matrix_t* preact, vc_act_t act,
+                               const vc_matrix_t* dx, const vc_matrix_t* dweight, void* dbias,
+                               vc_dtype_t dbias_dtype, int accumulate, void* workspace,
+                               size_t workspace_bytes, vc_stream_t stream) {
+    if (!valid_matrix(dy) || !valid_matrix(x) || !valid_matrix(weight) || !valid_act(act))
+        return VC_ERR_INVALID_ARGUMENT;
+    const long long M = x->rows, K = x->cols, N = weight->rows;
+    const bool has_act = act != VC_ACT_NONE;
+    if (!plain_matrix(x, M, K) || !plain_matrix(weight, N, K) || !plain_matrix(dy, M, N) ||
+        (has_act && (preact == nullptr || !plain_matrix(preact, M, N) || !is_bf16(preact))) ||
+        (dx != nullptr && (!plain_matrix(dx, M, K) || !is_bf16(dx))) ||
+        (dweight != nullptr && !plain_matrix(dweight, N, K)))
+        return VC_ERR_INVALID_ARGUMENT;
+    if (!is_bf16(x) || !is_bf16(weight) || !is_bf16(dy)) return VC_ERR_INVALID_ARGUMENT;
+    const int bias_size = elem_size(dbias_dtype);
+    if (dbias != nullptr &&
+        (bias_size == 0 || reinterpret_cast<uintptr_t>(dbias) % bias_size != 0))
+        return VC_ERR_INVALID_ARGUMENT;
+    const size_t need = backward_workspace(dy, x, weight, act, dbias != nullptr);
+    if (!workspace_ok(workspace, workspace_bytes, need)) return VC_ERR_INVALID_ARGUMENT;
+    const Span outs[4] = {span_of(dx), span_of(dweight), span_of(dbias, (size_t)N * bias_size),
+                          span_of(workspace, need)};
+    const Span ins[4] = {span_of(dy), span_of(x), span_of(weight),
+                         has_act ? span_of(preact) : Span{0, 0}};
+    for (int o = 0; o < 4; ++o) {
+        for (int i = 0; i < 4; ++i)
+            if (overlap(outs[o], ins[i])) return VC_ERR_ALIAS;
+        for (int q = 0; q < o; ++q)
+            if (overlap(outs[o], outs[q])) return VC_ERR_ALIAS;
+    }
+    if (dx == nullptr && dweight == nullptr && dbias == nullptr) return VC_SUCCESS;
+    if (N == 0 && M * K == 0) return VC_SUCCESS;
+    if (test_launch_failure()) return VC_ERR_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+
+    const bool write_dz = has_act || !operand_ready(dy);
+    const void* dz = dy->data;
+    long long ld_dz = M > 1 ? dy->ld : padded_ld(N);
+    float* sums = nullptr;
+    const int parts = dz_row_blocks(M, N);
+    if (dbias != nullptr) {
+        sums = reinterpret_cast<float*>(ws);
+        ws += round256((size_t)parts * N * 4);
+    }
+    if (write_dz) {
+        dz = ws;
+        ld_dz = padded_ld(N);
+        ws += round256((size_t)M * ld_dz * 2);
+    }
+    cudaError_t e = cudaSuccess;
+    if (N > 0 && (sums != nullptr || (write_dz && M > 0))) {
+        DzParams p = {};
+        p.dy = view_of(dy);
+        p.preact = view_of(has_act ? preact : nullptr);
+        p.dz = write_dz ? static_cast<__nv_bfloat16*>(const_cast<void*>(dz)) : nullptr;
+        p.ld_dz = ld_dz;
+        p.sums = sums;
+        p.rows = M;
+        p.cols = N;
+        p.act = act;
+        e = launch_pdl(dz_kernel, dim3((unsigned)((N + 127) / 128), parts), dim3(256), st, p);
+        if (e != cudaSuccess) return VC_ERR_CUDA;
+        if (sums != nullptr) {
+            e = launch_pdl(db_kernel, dim3((unsigned)((N + 255) / 256)), dim3(256), st,
+                           (const float*)sums, parts, N, dbias, dbias_dtype == VC_FLOAT32 ? 1 : 0,
+                           accumulate != 0 ? 1 : 0);
+            if (e != cudaSuccess) return VC_ERR_CUDA;
+        }
+    }
+    if (dx != nullptr && M > 0 && K > 0) {
+        Operand a = {dz, N, M, ld_dz, 0, true, false}, b = {nullptr, K, N, 0, 0, true, true};
+        if (ready_operand(weight, &ws, st, &b.data, &b.ld) != cudaSuccess) return VC_ERR_CUDA;
+        EpiStore::Params ep = {view_of(dx), 0};
+        e = product<EpiStore>(a, b, (int)M, (int)K, (int)N, ep, st);
+        if (e != cudaSuccess) return VC_ERR_CUDA;
+    }
+    if (dweight != nullptr && N > 0 && K > 0) {
+        Operand a = {dz, N, M, ld_dz, 0, true, true}, b = {nullptr, K, M, 0, 0, true, true};
+        if (ready_operand(x, &ws, st, &b.data, &b.ld) != cudaSuccess) return VC_ERR_CUDA;
+        EpiStore::Params ep = {view_of(dweight), accumulate != 0};
+        e = product<EpiStore>(a, b, (int)N, (int)K, (int)M, ep, st);
+        if (e != cudaSuccess) return VC_ERR_CUDA;
+    }
+    return VC_SUCCESS;
+}
+
+}  // extern "C"

@@ -1,0 +1,501 @@
+// Newton-Schulz orthogonalisation of matrices, and the Muon step around it.
+//
+// With r the smaller and c the larger side, one pass of the iteration is
+//   A = X X^T        (r x r, symmetric: half of the tiles)
+//   B = b A + c A^2  (r x r, symmetric)
+//   X <- a X + B X   (r x c)
+// on whichever side the smaller dimension is: a tall matrix uses X^T X and
+// X B, which only changes which operands are K-major.
+//
+// Numbers.  The products' operands are fp16: their values are bounded (|X| at
+// most about 1.2 in the spectral norm), so fp16's 11 significant bits are
+// worth more than bf16's range.  Three measures keep the result within about
+// 1e-3 of the exact iteration, below the bf16 rounding of the output (bf16
+// operands: 1e-2):
+//   - X is stored times a power of two near sqrt(c), so that its values are
+//     about 1 at the end and normal fp16 numbers at the start;
+//   - the diagonals of A and B, which are far larger than the rest, are kept
+//     apart in 32 bits; with A = D + O,
+//       A^2 = D^2 + D O + O D + O^2,   B X = diag(B) X + offdiag(B) X;
+//   - X itself is kept as a sum of two fp16 values, of which the a X and
+//     diag(B) X terms use both and the products the larger one.  Without it,
+//     directions with small singular values, which the iteration raises by
+//     up to 500, would be raised from the rounding noise of the large ones.
+#include <algorithm>
+#include <math.h>
+
+#include "vc_train_common.cuh"
+
+namespace vc {
+namespace train {
+namespace {
+
+using gemm::Operand;
+using gemm::Shape;
+using gemm::View;
+
+// ---------------------------------------------------- momentum and scaling --
+
+constexpr int kMaxParts = 1024;  // partial sums of squares per matrix
+
+struct PrepareParams {
+    View g, m;
+    int has_momentum, nesterov;
+    float beta;
+    float* parts;  // [batch][gridDim.x]
+    __half *hi, *lo;
+    long long ld, batch_stride;  // of hi and lo
+    float size, eps;             // X is stored times size / (norm + eps)
+    int rows, cols, vpr;         // vpr: groups of four columns per row
+};
+
+// The update's values: g, or the momentum, or g + beta momentum.
+__device__ __forceinline__ float4 update_of(const PrepareParams& p, float4 g, float4 m) {
+    if (!p.has_momentum) return g;
+    if (!p.nesterov) return m;
+    return make_float4(fmaf(p.beta, m.x, g.x), fmaf(p.beta, m.y, g.y), fmaf(p.beta, m.z, g.z),
+                       fmaf(p.beta, m.w, g.w));
+}
+
+__device__ __forceinline__ float block_sum(float v, float* tmp) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += tmp[w];
+    __syncthreads();
+    return s;
+}
+
+__device__ __forceinline__ float rounded(const View& v, float x) {
+    return v.f32 ? x : __bfloat162float(__float2bfloat16(x));
+}
+
+// M <- beta M + G, and this block's part of the sum of the update's squares.
+__global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ PrepareParams p) {
+    __shared__ float tmp[8];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const unsigned total = (unsigned)p.rows * (unsigned)p.vpr;
+    const int b = blockIdx.y;
+    float sum = 0.0f;
+    for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+        const unsigned row = i / (unsigned)p.vpr;
+        const int col = (int)(i - row * (unsigned)p.vpr) * 4, n = min(4, p.cols - col);
+        const float4 g = gemm::view_load(p.g, b, row, col, n);
+        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.has_momentum) {
+            m = gemm::view_load(p.m, b, row, col, n);
+            m = make_float4(fmaf(p.beta, m.x, g.x), fmaf(p.beta, m.y, g.y),
+                            fmaf(p.beta, m.z, g.z), fmaf(p.beta, m.w, g.w));
+            gemm::view_store(p.m, b, row, col, n, m);
+            // the second pass reads what was stored
+            m = make_float4(rounded(p.m, m.x), rounded(p.m, m.y), rounded(p.m, m.z),
+                            rounded(p.m, m.w));
+        }
+        const float4 u = update_of(p, g, m);  // zero beyond n
+        sum += u.x * u.x + u.y * u.y + u.z * u.z + u.w * u.w;
+    }
+    sum = block_sum(sum, tmp);
+    if (threadIdx.x == 0) p.parts[b * gridDim.x + blockIdx.x] = sum;
+}
+
+// X_0 = update size / (norm + eps), as two fp16 values.  Every block adds up
+// the partial sums, in the same order.
+__global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ PrepareParams p) {
+    __shared__ float tmp[8];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const unsigned total = (unsigned)p.rows * (unsigned)p.vpr;
+    const int b = blockIdx.y;
+    float sum = 0.0f;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) sum += p.parts[b * gridDim.x + i];
+    const float scale = p.size / (sqrtf(block_sum(sum, tmp)) + p.eps);
+    for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+        const unsigned row = i / (unsigned)p.vpr;
+        const int col = (int)(i - row * (unsigned)p.vpr) * 4, n = min(4, p.cols - col);
+        const float4 g = gemm::view_load(p.g, b, row, col, n);
+        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.has_momentum) m = gemm::view_load(p.m, b, row, col, n);
+        float4 u = update_of(p, g, m);
+        u = make_float4(u.x * scale, u.y * scale, u.z * scale, u.w * scale);
+        const long long at = (long long)b * p.batch_stride + (long long)row * p.ld + col;
+        const float4 hi = make_float4(__half2float(__float2half_rn(u.x)), __half2float(__float2half_rn(u.y)),
+                                      __half2float(__float2half_rn(u.z)), __half2float(__float2half_rn(u.w)));
+        gemm::store4(p.hi + at, hi, n, true);
+        gemm::store4(p.lo + at, make_float4(u.x - hi.x, u.y - hi.y, u.z - hi.z, u.w - hi.w), n, true);
+    }
+}
+
+// ------------------------------------------------------------- epilogues --
+
+// A = X X^T: the diagonal to 32 bits, the rest to fp16 on both sides.
+struct EpiGram {
+    static constexpr bool kSym = true, kRows = true;
+    struct Params {
+        __half* o;
+        float* d;
+        long long ld, batch_stride;
+        float scale;
+    };
+    struct Col {};
+    struct Aux {};
+    __device__ static void regs(const Params& p, const Shape& s, int b, int row, int col0,
+                                float (&v)[32], bool off) {
+        __half* const o = p.o + (long long)b * p.batch_stride;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            v[j] *= p.scale;
+            if (!off && row == col0 + j && row < s.M) {
+                p.d[(long long)b * s.M + row] = v[j];
+                v[j] = 0.0f;
+            }
+        }
+        if (off && row < s.M) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col0 + j < s.N) o[(col0 + j) * p.ld + row] = __float2half_rn(v[j]);
+        }
+    }
+    __device__ static Col cols(const Params&, const Shape&, int, int, int) { return {}; }
+    __device__ static Aux load(const Params&, const Shape&, int, int, int, int) { return {}; }
+    __device__ static void store(const Params& p, const Shape&, int b, int row, int col, int n,
+                                 float4 v, const Aux&, const Col&) {
+        gemm::store4(p.o + (long long)b * p.batch_stride + (long long)row * p.ld + col, v, n, true);
+    }
+};
+
+// B = b A + c A^2 from the product O O of A's off-diagonal part.
+struct EpiPoly {
+    static constexpr bool kSym = true, kRows = true;
+    struct Params {
+        const __half* o;
+        const float* d;
+        __half* ob;
+        float* db;
+        long long ld, batch_stride;
+        float cb, cc;
+    };
+    struct Col {};
+    struct Aux {};
+    __device__ static void regs(const Params& p, const Shape& s, int b, int row, int col0,
+                                float (&v)[32], bool off) {
+        const __half* const o = p.o + (long long)b * p.batch_stride;
+        __half* const ob = p.ob + (long long)b * p.batch_stride;
+        const float* const d = p.d + (long long)b * s.M;
+        if (row < s.M) {
+            const float di = d[row];
+            float a[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)  // the same value as o[row][col0 + j], read along rows
+                a[j] = col0 + j < s.N ? __half2float(o[(col0 + j) * p.ld + row]) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float dj = col0 + j < s.N ? d[col0 + j] : 0.0f;
+                if (!off && row == col0 + j) {
+                    p.db[(long long)b * s.M + row] = p.cb * di + p.cc * (di * di + v[j]);
+                    v[j] = 0.0f;
+                } else {
+                    v[j] = (p.cb + p.cc * (di + dj)) * a[j] + p.cc * v[j];
+                }
+            }
+            if (off) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (col0 + j < s.N) ob[(col0 + j) * p.ld + row] = __float2half_rn(v[j]);
+            }
+        }
+    }
+    __device__ static Col cols(const Params&, const Shape&, int, int, int) { return {}; }
+    __device__ static Aux load(const Params&, const Shape&, int, int, int, int) { return {}; }
+    __device__ static void store(const Params& p, const Shape&, int b, int row, int col, int n,
+                                 float4 v, const Aux&, const Col&) {
+        gemm::store4(p.ob + (long long)b * p.batch_stride + (long long)row * p.ld + col, v, n, true);
+    }
+};
+
+// X <- (a + diag B) X + offdiag(B) X, and on the last pass the operator's
+// output instead of X.
+struct UpdateCommon {
+    const __half* hi;
+    __half* lo;
+    __half* hi_out;
+    const float* db;  // of B, [batch][r]
+    long long ld, batch_stride;
+    float a;
+    int tall;  // B stands on the right: its diagonal goes with the columns
+    int r;
+};
+struct UpdateAux {
+    float4 x;
+    float row;
+};
+struct UpdateCol {
+    float4 k;
+};
+__device__ __forceinline__ UpdateCol update_cols(const UpdateCommon& p, int b, int col, int n) {
+    UpdateCol c = {make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (p.tall) c.k = gemm::load4(p.db + (long long)b * p.r + col, n, false);
+    return c;
+}
+__device__ __forceinline__ UpdateAux update_load(const UpdateCommon& p, int b, int row, int col,
+                                                 int n) {
+    const long long at = (long long)b * p.batch_stride + (long long)row * p.ld + col;
+    const float4 h = gemm::load4(p.hi + at, n, true), l = gemm::load4(p.lo + at, n, true);
+    UpdateAux a;
+    a.x = make_float4(h.x + l.x, h.y + l.y, h.z + l.z, h.w + l.w);
+    a.row = p.a + (p.tall ? 0.0f : p.db[(long long)b * p.r + row]);
+    return a;
+}
+__device__ __forceinline__ float4 update_value(float4 v, const UpdateAux& a, const UpdateCol& c) {
+    return make_float4(fmaf(a.row + c.k.x, a.x.x, v.x), fmaf(a.row + c.k.y, a.x.y, v.y),
+                       fmaf(a.row + c.k.z, a.x.z, v.z), fmaf(a.row + c.k.w, a.x.w, v.w));
+}
+
+struct EpiUpdate {
+    static constexpr bool kSym = false, kRows = true;
+    using Params = UpdateCommon;
+    using Col = UpdateCol;
+    using Aux = UpdateAux;
+    __device__ static void regs(const Params&, const Shape&, int, int, int, float (&)[32], bool) {}
+    __device__ static Col cols(const Params& p, const Shape&, int b, int col, int n) {
+        return update_cols(p, b, col, n);
+    }
+    __device__ static Aux load(const Params& p, const Shape&, int b, int row, int col, int n) {
+        return update_load(p, b, row, col, n);
+    }
+    __device__ static void store(const Params& p, const Shape&, int b, int row, int col, int n,
+                                 float4 v, const Aux& a, const Col& c) {
+        const float4 y = update_value(v, a, c);
+        const long long at = (long long)b * p.batch_stride + (long long)row * p.ld + col;
+        const float4 h = make_float4(__half2float(__float2half_rn(y.x)), __half2float(__float2half_rn(y.y)),
+                                     __half2float(__float2half_rn(y.z)), __half2float(__float2half_rn(y.w)));
+        gemm::store4(p.hi_out + at, h, n, true);
+        gemm::store4(p.lo + at, make_float4(y.x - h.x, y.y - h.y, y.z - h.z, y.w - h.w), n, true);
+    }
+};
+
+struct EpiFinal {
+    static constexpr bool kSym = false, kRows = true;
+    struct Params {
+        UpdateCommon u;
+        View out;     // the output, or the weights
+        int weights;  // out <- keep out + scale y, else out <- scale y
+        float keep, scale;
+    };
+    using Col = UpdateCol;
+    struct Aux {
+        UpdateAux u;
+        float4 w;
+    };
+    __device__ static void regs(const Params&, const Shape&, int, int, int, float (&)[32], bool) {}
+    __device__ static Col cols(const Params& p, const Shape&, int b, int col, int n) {
+        return update_cols(p.u, b, col, n);
+    }
+    __device__ static Aux load(const Params& p, const Shape&, int b, int row, int col, int n) {
+        Aux a;
+        a.u = update_load(p.u, b, row, col, n);
+        a.w = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.weights) a.w = gemm::view_load(p.out, b, row, col, n);
+        return a;
+    }
+    __device__ static void store(const Params& p, const Shape&, int b, int row, int col, int n,
+                                 float4 v, const Aux& a, const Col& c) {
+        float4 y = update_value(v, a.u, c);
+        if (p.weights)
+            y = make_float4(fmaf(p.keep, a.w.x, p.scale * y.x), fmaf(p.keep, a.w.y, p.scale * y.y),
+                            fmaf(p.keep, a.w.z, p.scale * y.z), fmaf(p.keep, a.w.w, p.scale * y.w));
+        else
+            y = make_float4(p.scale * y.x, p.scale * y.y, p.scale * y.z, p.scale * y.w);
+        gemm::view_store(p.out, b, row, col, n, y);
+    }
+};
+
+template <class Epi>
+cudaError_t product(const Operand& a, const Operand& b, int M, int N, int K, int batch,
+                    const typename Epi::Params& ep, cudaStream_t st) {
+    return gemm::launch_tile<1, 128, Epi>(a, b, M, N, K, batch, ep, st);
+}
+
+// -------------------------------------------------------------- host side --
+
+struct Layout {
+    long long r, c;        // smaller and larger side
+    long long ldx, ldr;    // row lengths of X and of the r x r matrices
+    long long xs, as;      // values from one matrix of the batch to the next
+    int parts;
+    size_t hi0, hi1, lo, a, b, da, db, sums, bytes;
+};
+
+bool layout_of(long long batch, long long rows, long long cols, Layout* l) {
+    if (batch < 0 || rows < 0 || cols < 0) return false;
+    if (batch > (1 << 16) - 1 || rows > (1ll << 24) || cols > (1ll << 24)) return false;
+    const long long vpr = (cols + 3) / 4;
+    if (rows * vpr > 0x7FFFFFFFll || batch * rows > 0x3FFFFFFFll) return false;
+    l->r = std::min(rows, cols);
+    l->c = std::max(rows, cols);
+    l->ldx = padded_ld(cols);
+    l->ldr = padded_ld(l->r);
+    l->xs = rows * l->ldx;
+    l->as = l->r * l->ldr;
+    const long long want = (rows * vpr + 1023) / 1024, fit = std::max(1ll, 152 * 8 / std::max(1ll, batch));
+    l->parts = (int)std::max(1ll, std::min({want, fit, (long long)kMaxParts}));
+    const size_t x = round256((size_t)batch * l->xs * 2), a = round256((size_t)batch * l->as * 2);
+    const size_t d = round256((size_t)batch * l->r * 4);
+    size_t at = 0;
+    l->hi0 = at, at += x;
+    l->hi1 = at, at += x;
+    l->lo = at, at += x;
+    l->a = at, at += a;
+    l->b = at, at += a;
+    l->da = at, at += d;
+    l->db = at, at += d;
+    l->sums = at, at += round256((size_t)batch * l->parts * 4);
+    l->bytes = at;
+    return true;
+}
+
+bool valid_ns(const vc_newton_schulz_t* ns) {
+    return ns != nullptr && ns->steps >= 1 && ns->steps <= 100 && isfinite(ns->a) &&
+           isfinite(ns->b) && isfinite(ns->c) && isfinite(ns->eps) && ns->eps >= 0.0f;
+}
+
+// The whole iteration; ends in `fin` (out, weights, keep, scale set).
+cudaError_t iterate(const Layout& l, long long batch, long long rows, long long cols,
+                    PrepareParams p, const vc_newton_schulz_t& ns, EpiFinal::Params fin,
+                    unsigned char* ws, cudaStream_t st) {
+    const bool tall = rows > cols;
+    int e2 = 0;  // X is stored times 2^e2, about sqrt(c)
+    while (e2 < 12 && (1ll << (2 * e2)) < l.c) ++e2;
+    const float size = (float)(1 << e2);
+    __half* x[2] = {reinterpret_cast<__half*>(ws + l.hi0), reinterpret_cast<__half*>(ws + l.hi1)};
+    __half *const lo = reinterpret_cast<__half*>(ws + l.lo), *const oa = reinterpret_cast<__half*>(ws + l.a),
+                  *const ob = reinterpret_cast<__half*>(ws + l.b);
+    float *const da = reinterpret_cast<float*>(ws + l.da), *const db = reinterpret_cast<float*>(ws + l.db);
+    p.parts = reinterpret_cast<float*>(ws + l.sums);
+    p.hi = x[0];
+    p.lo = lo;
+    p.ld = l.ldx;
+    p.batch_stride = l.xs;
+    p.size = size;
+    p.eps = ns.eps;
+    p.rows = (int)rows;
+    p.cols = (int)cols;
+    p.vpr = (int)((cols + 3) / 4);
+    const dim3 grid(l.parts, (unsigned)batch);
+    cudaError_t e = launch_pdl(momentum_kernel, grid, dim3(256), st, p);
+    if (e == cudaSuccess) e = launch_pdl(scale_kernel, grid, dim3(256), st, p);
+    const int r = (int)l.r, c = (int)l.c, nb = (int)batch;
+    for (int i = 0; i < ns.steps && e == cudaSuccess; ++i) {
+        const Operand xk = {x[0], cols, rows, l.ldx, l.xs, false, false};
+        Operand xm = xk;
+        xm.mn_major = true;
+        EpiGram::Params gp = {oa, da, l.ldr, l.as, 1.0f / (size * size)};
+        const Operand& side = tall ? xm : xk;
+        e = product<EpiGram>(side, side, r, r, c, nb, gp, st);
+        if (e != cudaSuccess) break;
+        const Operand ao = {oa, r, r, l.ldr, l.as, false, false};
+        EpiPoly::Params pp = {oa, da, ob, db, l.ldr, l.as, ns.b, ns.c};
+        e = product<EpiPoly>(ao, ao, r, r, r, nb, pp, st);
+        if (e != cudaSuccess) break;
+        const Operand bo = {ob, r, r, l.ldr, l.as, false, false};
+        const UpdateCommon u = {x[0], lo, x[1], db, l.ldx, l.xs, ns.a, tall, r};
+        const Operand &left = tall ? xk : bo, &right = tall ? bo : xm;
+        if (i + 1 < ns.steps) {
+            e = product<EpiUpdate>(left, right, (int)rows, (int)cols, r, nb, u, st);
+        } else {
+            fin.u = u;
+            fin.scale /= size;
+            e = product<EpiFinal>(left, right, (int)rows, (int)cols, r, nb, fin, st);
+        }
+        std::swap(x[0], x[1]);
+    }
+    return e;
+}
+
+bool same_sizes(const vc_matrix_t* a, const vc_matrix_t* b) {
+    return a->batch == b->batch && a->rows == b->rows && a->cols == b->cols;
+}
+
+bool workspace_ok(const void* ws, size_t have, size_t need) {
+    return ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && have >= need;
+}
+
+}  // namespace
+}  // namespace train
+}  // namespace vc
+
+using namespace vc;
+using namespace vc::train;
+
+extern "C" {
+
+size_t vc_orthogonalize_workspace(long long batch, long long rows, long long cols) {
+    Layout l;
+    if (!layout_of(batch, rows, cols, &l)) return 0;
+    return batch == 0 || rows == 0 || cols == 0 ? 0 : l.bytes;
+}
+
+vc_status_t vc_orthogonalize(const vc_matrix_t* g, const vc_matrix_t* out,
+                             const vc_newton_schulz_t* ns, void* workspace, size_t workspace_bytes,
+                             vc_stream_t stream) {
+    if (!valid_matrix(g) || !valid_matrix(out) || !same_sizes(g, out) ||
+        out->dtype != VC_BFLOAT16 || !valid_ns(ns))
+        return VC_ERR_INVALID_ARGUMENT;
+    Layout l;
+    if (!layout_of(g->batch, g->rows, g->cols, &l)) return VC_ERR_INVALID_ARGUMENT;
+    if (g->batch == 0 || g->rows == 0 || g->cols == 0) return VC_SUCCESS;
+    if (!workspace_ok(workspace, workspace_bytes, l.bytes)) return VC_ERR_INVALID_ARGUMENT;
+    const Span ws = span_of(workspace, l.bytes);
+    if ((overlap(span_of(g), span_of(out)) && !same_matrix(g, out)) || overlap(span_of(g), ws) ||
+        overlap(span_of(out), ws))
+        return VC_ERR_ALIAS;
+    if (test_launch_failure()) return VC_ERR_CUDA;
+    PrepareParams p = {};
+    p.g = view_of(g);
+    EpiFinal::Params fin = {};
+    fin.out = view_of(out);
+    fin.scale = 1.0f;
+    const cudaError_t e = iterate(l, g->batch, g->rows, g->cols, p, *ns, fin,
+                                  static_cast<unsigned char*>(workspace),
+                                  static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
+}
+
+vc_status_t vc_muon_step(const vc_matrix_t* weight, const vc_matrix_t* grad,
+                         const vc_matrix_t* momentum, const vc_muon_t* args, void* workspace,
+                         size_t workspace_bytes, vc_stream_t stream) {
+    if (!valid_matrix(weight) || !valid_matrix(grad) || !valid_matrix(momentum) ||
+        args == nullptr || !same_sizes(weight, grad) || !same_sizes(weight, momentum) ||
+        !valid_ns(&args->ns) || !isfinite(args->lr) || !isfinite(args->beta) ||
+        !isfinite(args->weight_decay) || !isfinite(args->scale))
+        return VC_ERR_INVALID_ARGUMENT;
+    Layout l;
+    if (!layout_of(grad->batch, grad->rows, grad->cols, &l)) return VC_ERR_INVALID_ARGUMENT;
+    if (grad->batch == 0 || grad->rows == 0 || grad->cols == 0) return VC_SUCCESS;
+    if (!workspace_ok(workspace, workspace_bytes, l.bytes)) return VC_ERR_INVALID_ARGUMENT;
+    const Span s[4] = {span_of(weight), span_of(grad), span_of(momentum), span_of(workspace, l.bytes)};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(s[i], s[j])) return VC_ERR_ALIAS;
+    if (test_launch_failure()) return VC_ERR_CUDA;
+    PrepareParams p = {};
+    p.g = view_of(grad);
+    p.m = view_of(momentum);
+    p.has_momentum = 1;
+    p.nesterov = args->nesterov != 0;
+    p.beta = args->beta;
+    EpiFinal::Params fin = {};
+    fin.out = view_of(weight);
+    fin.weights = 1;
+    fin.keep = 1.0f - args->lr * args->weight_decay;
+    fin.scale = -args->lr * args->scale;
+    const cudaError_t e = iterate(l, grad->batch, grad->rows, grad->cols, p, args->ns, fin,
+                                  static_cast<unsigned char*>(workspace),
+                                  static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
+}
+
+}  // extern "C"
