@@ -1,6 +1,8 @@
 // Host side of the product kernel: tensor maps, and the count of waits that
 // ran out.
 #include <mutex>
+#include <set>
+#include <utility>
 
 #include "vc_gemm.cuh"
 #include "vc_train.h"
@@ -57,6 +59,19 @@ EncodeFn encoder() {
 }
 
 }  // namespace
+
+cudaError_t allow_smem(const void* kernel) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::mutex mu;
+    static std::set<std::pair<int, const void*>> done;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({dev, kernel}) != 0) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerBlock);
+    if (e == cudaSuccess) done.insert({dev, kernel});
+    return e;
+}
 
 bool encode_operand(CUtensorMap* map, const Operand& o, int batch, int box_rows) {
     EncodeFn fn = encoder();

@@ -1,18 +1,24 @@
-// The product kernel of the training-step operators: D = A B on the tcgen05
+// The product kernels of the training-step operators: D = A B on the tcgen05
 // tensor cores, 16-bit operands (bf16 or fp16), 32-bit accumulators, with the
 // operator's own arithmetic in the epilogue.
 //
-// One persistent kernel: a block (or a pair of blocks that share one 256-row
-// product) walks over the output tiles.  Its warps have roles:
+// Warps have roles:
 //   warp 0     loads the tiles of A and B through TMA into a ring of shared
 //              memory stages (64 deep along K, 128-byte swizzle);
 //   warp 1     issues the matrix instructions, which accumulate in tensor
-//              memory (two accumulators, so that the next tile's products
-//              run while this tile's epilogue reads);
-//   the others read the accumulators and run the epilogue.  Each warp owns 32 rows (a warp
-//              may only read the tensor-memory lanes of its quarter) and one
-//              half of the columns; a 32 x 32 chunk goes through shared
-//              memory so that global accesses run along the rows.
+//              memory;
+//   the others read the accumulators and run the epilogue.  Each warp reads
+//              32 rows (a warp may only read the tensor-memory lanes of its
+//              quarter), 32 x 32 values at a time.
+// Two kernels share this:
+//   pair_kernel   for products with many tiles: persistent pairs of blocks,
+//                 one 256 x 256 tile per pair (each block holds half of A's
+//                 rows and half of B's, which halves the operands' traffic),
+//                 two accumulators, so that the next tile's products run
+//                 while this tile's epilogue reads;
+//   split_kernel  for products with few tiles: 128-row tiles, each computed by
+//                 a cluster of blocks that share out K and add their partial
+//                 tiles through distributed shared memory, in rank order.
 // Every wait is bounded: a wait that runs out marks the block as dead, which
 // ends all of its loops, and counts it in a device word that the host can read.
 //
@@ -33,28 +39,42 @@ namespace gemm {
 
 constexpr int kBlockK = 64;            // 64 16-bit values: one 128-byte swizzle row
 constexpr int kRowsPerCta = 128;       // tensor-memory lanes
-constexpr int kStageRow = 36;          // floats per row of an epilogue chunk (32 + 4: no bank
+constexpr int kChunkRow = 36;          // floats per row of an epilogue chunk (32 + 4: no bank
                                        // conflicts in either direction)
+constexpr int kWarpStage = 2048;       // bytes of shared memory of an epilogue warp
+constexpr int kGroup = 8;              // tile rows walked together, for reuse in L2
+constexpr int kChunkRows = 8;          // rows of a chunk at a time
 constexpr int kEpilogueWarps = 8;
-constexpr int kGemmThreads = 32 * (2 + kEpilogueWarps);
+constexpr int kPairThreads = 32 * (2 + kEpilogueWarps);
+constexpr int kSmemPerBlock = 232448;  // 227 KB
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 
 struct Shape {
     int M, N, K;            // of one product
-    int batch;
-    int tiles_m, tiles_n;   // tiles of one product (tiles_m counts block-pair tiles in pair mode)
+    int tiles_m, tiles_n;   // tiles of one product
     int tiles;              // tiles of one product that are computed
+    int total;              // tiles of all products of the batch
     int kblocks;            // ceil(K / 64)
-    int group;              // tile rows walked together, for reuse in L2
+    int segment;            // K blocks summed in tensor memory at a time
     int a_mn, b_mn;         // operand is MN-major
     unsigned idesc;         // instruction descriptor
-    unsigned* timeouts;     // counts blocks whose waits ran out
 };
 
 // ------------------------------------------------------------------ PTX --
 
 __device__ __forceinline__ unsigned smem_u32(const void* p) {
     return (unsigned)__cvta_generic_to_shared(p);
+}
+
+// One lane of a converged warp, the same one each time.  (The instructions
+// that one thread issues for the warp take their operands from uniform
+// registers; under this predicate the compiler knows that there is only one.)
+__device__ __forceinline__ bool elect_one() {
+    unsigned ok;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b32 r;\nelect.sync r|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok));
+    return ok != 0;
 }
 
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -114,6 +134,11 @@ __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, volatil
         }
     }
     return true;
+}
+
+// The same for a whole converged warp: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(unsigned bar, unsigned parity, volatile int* dead) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, dead));
 }
 
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
@@ -223,6 +248,21 @@ __device__ __forceinline__ void tmem_load32(unsigned addr, float (&v)[32]) {
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
 }
 
+// 16 columns.
+__device__ __forceinline__ void tmem_load16(unsigned addr, float (&v)[16]) {
+    unsigned r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+}
+
 // Shared-memory descriptor of a 128-byte-swizzled operand tile.  K-major: rows
 // of 128 bytes (64 values of K), groups of 8 rows 1024 bytes apart.  MN-major:
 // rows of 64 values of M or N, one row per k; groups of 8 k 1024 bytes apart,
@@ -237,6 +277,34 @@ __device__ __forceinline__ uint64_t smem_desc(unsigned addr, bool mn_major) {
 __device__ __forceinline__ unsigned desc_step(bool mn_major) { return mn_major ? 2048 >> 4 : 32 >> 4; }
 
 // ------------------------------------------------------- memory helpers --
+
+// Two float operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ uint64_t pack2(float2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+    return unpack2(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // Up to four consecutive values as float; `vec`: the address is aligned to
 // the four (and n is 4 wherever a vector is taken).
@@ -321,6 +389,7 @@ struct View {
     long long ld, batch_stride;
     int f32;
     int vec;  // four values starting at a column that is a multiple of four are one aligned vector
+    int vec16;  // rows are on 16 bytes
 };
 __device__ __forceinline__ float4 view_load(const View& v, int b, long long row, int col, int n) {
     const long long at = (long long)b * v.batch_stride + row * v.ld + col;
@@ -336,75 +405,400 @@ __device__ __forceinline__ void view_store(const View& v, int b, long long row, 
         store4(static_cast<__nv_bfloat16*>(v.data) + at, x, n, v.vec);
 }
 
-// --------------------------------------------------------------- kernel --
+// ------------------------------------------------------------- epilogues --
 
-// Shared memory: stages (1024-byte aligned), epilogue chunks, barriers.
-template <int kPair, int kBN>
-struct Config {
-    static constexpr int kBRows = kBN / kPair;  // rows of B (columns of D) that this block loads
-    static constexpr int kABytes = kRowsPerCta * kBlockK * 2;
-    static constexpr int kBBytes = kBRows * kBlockK * 2;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kChunkBytes = kEpilogueWarps * 32 * kStageRow * 4;
-    static constexpr int kBarBytes = 256;
-    static constexpr int kStages = (232448 - 1024 - kBarBytes - kChunkBytes) / kStageBytes > 8
-                                       ? 8
-                                       : (232448 - 1024 - kBarBytes - kChunkBytes) / kStageBytes;
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + kChunkBytes + kBarBytes;
-    static constexpr int kTmemCols = 2 * kBN;  // two accumulators; a power of two >= 32
-    static_assert(kStages >= 3, "too few stages");
-    static_assert((2 * kStages + 4) * 8 + 8 <= kBarBytes, "barriers");
+// Where a warp's 32 x 32 chunk of a product lies.
+struct Place {
+    int b, row0, col0;  // product of the batch, first row, first column
+    int M, N;           // its extents
+    int lane;
+    bool off;              // the tile lies off the diagonal (of a symmetric product)
+    unsigned char* stage;  // the warp's piece of shared memory, kWarpStage bytes
+    __device__ __forceinline__ int row() const { return row0 + lane; }
+    __device__ __forceinline__ bool whole() const { return col0 + 32 <= N; }
 };
 
-// Tile t of a product: its tile row and tile column.  Symmetric products
-// compute the tiles on and below the diagonal only, row by row; others walk
-// down `group` tile rows before they move to the next tile column.
-template <bool kSym>
-__device__ __forceinline__ void tile_at(const Shape& s, int t, int& tm, int& tn) {
-    if constexpr (kSym) {
-        int r = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-        while ((r + 1) * (r + 2) / 2 <= t) ++r;
-        while (r * (r + 1) / 2 > t) --r;
-        tm = r;
-        tn = t - r * (r + 1) / 2;
-    } else {
-        const int per = s.group * s.tiles_n;
-        const int g = t / per, in = t - g * per;
-        const int rows = min(s.group, s.tiles_m - g * s.group);
-        tn = in / rows;
-        tm = g * s.group + (in - tn * rows);
+// A chunk of 16-bit values passes between its two forms through the warp's
+// piece of shared memory: one row per lane, which the accumulators have, and
+// 64 bytes of a row per four lanes, which global memory wants.  The 16-byte
+// pieces are permuted within each 128 bytes so that neither side has bank
+// conflicts.
+struct Chunk16 {
+    uint4 u[4];  // across: piece lane % 4 of row 8 i + lane / 4; own: piece i of row lane
+};
+__device__ __forceinline__ uint4* piece_of(unsigned char* stage, int row, int c) {
+    return reinterpret_cast<uint4*>(stage + (row >> 1) * 128 + (row & 1) * 64 +
+                                    ((c ^ ((row >> 1) & 3)) * 16));
+}
+__device__ __forceinline__ void across_to_own(const Place& q, Chunk16& x) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *piece_of(q.stage, 8 * i + (q.lane >> 2), q.lane & 3) = x.u[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.u[i] = *piece_of(q.stage, q.lane, i);
+}
+__device__ __forceinline__ void own_to_across(const Place& q, Chunk16& x) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *piece_of(q.stage, q.lane, i) = x.u[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.u[i] = *piece_of(q.stage, 8 * i + (q.lane >> 2), q.lane & 3);
+}
+// `corner`: the chunk's first value; ld and the 16-byte pieces in bytes.
+__device__ __forceinline__ void load_across(const void* corner, long long ld_bytes, const Place& q,
+                                            Chunk16& x) {
+    const unsigned char* p = static_cast<const unsigned char*>(corner) +
+                             (long long)(q.lane >> 2) * ld_bytes + (q.lane & 3) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (q.row0 + 8 * i + (q.lane >> 2) < q.M)
+            x.u[i] = *reinterpret_cast<const uint4*>(p + 8 * i * ld_bytes);
+}
+__device__ __forceinline__ void store_across(void* corner, long long ld_bytes, const Place& q,
+                                             const Chunk16& x) {
+    unsigned char* p = static_cast<unsigned char*>(corner) + (long long)(q.lane >> 2) * ld_bytes +
+                       (q.lane & 3) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (q.row0 + 8 * i + (q.lane >> 2) < q.M)
+            *reinterpret_cast<uint4*>(p + 8 * i * ld_bytes) = x.u[i];
+}
+
+__device__ __forceinline__ unsigned word_of(const Chunk16& x, int i) {
+    const uint4 u = x.u[i >> 2];
+    return (i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w;
+}
+// Values 2 i and 2 i + 1 of the lane's row.
+__device__ __forceinline__ float2 pair_at(const Chunk16& x, int i, __nv_bfloat16) {
+    const unsigned w = word_of(x, i);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 pair_at(const Chunk16& x, int i, __half) {
+    const unsigned w = word_of(x, i);
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ unsigned packed(float a, float b, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const unsigned*>(&h);
+}
+__device__ __forceinline__ unsigned packed(float a, float b, __half) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const unsigned*>(&h);
+}
+template <class T>
+__device__ __forceinline__ void store_chunk(T* corner, long long ld, const Place& q,
+                                            const float (&v)[32]) {
+    Chunk16 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x.u[i] = make_uint4(packed(v[8 * i], v[8 * i + 1], T()), packed(v[8 * i + 2], v[8 * i + 3], T()),
+                            packed(v[8 * i + 4], v[8 * i + 5], T()),
+                            packed(v[8 * i + 6], v[8 * i + 7], T()));
+    own_to_across(q, x);
+    store_across(corner, ld * (long long)sizeof(T), q, x);
+}
+
+// Whether the chunk can be accessed in 16-byte pieces.
+__device__ __forceinline__ bool in_pieces(const View& v, const Place& q) {
+    return v.vec16 && q.whole();
+}
+__device__ __forceinline__ long long corner_of(const View& v, const Place& q) {
+    return (long long)q.b * v.batch_stride + (long long)q.row0 * v.ld + q.col0;
+}
+
+// The chunk of a matrix, one row per lane: v[j] = X[row0 + lane][col0 + j].
+// All lanes call it.  Chunks that 16-byte pieces do not cover (odd row lengths,
+// the last columns) go through shared memory as floats, eight rows at a time.
+__device__ __forceinline__ void get_rows(const View& x, const Place& q, float (&v)[32]) {
+    if (in_pieces(x, q)) {
+        Chunk16 c;
+        if (x.f32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                load_across(static_cast<const float*>(x.data) + corner_of(x, q) + 16 * h, x.ld * 4, q, c);
+                across_to_own(q, c);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[16 * h + i] = __uint_as_float(word_of(c, i));
+            }
+        } else {
+            load_across(static_cast<const __nv_bfloat16*>(x.data) + corner_of(x, q), x.ld * 2, q, c);
+            across_to_own(q, c);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 f = pair_at(c, i, __nv_bfloat16());
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+        return;
+    }
+    float* const chunk = reinterpret_cast<float*>(q.stage);
+    const int lr = q.lane >> 3, lc = (q.lane & 7) * 4, n = min(4, q.N - q.col0 - lc);
+#pragma unroll
+    for (int h = 0; h < 32 / kChunkRows; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kChunkRows / 4; ++u) {
+            const int r = 4 * u + lr, row = q.row0 + h * kChunkRows + r;
+            if (n > 0 && row < q.M)
+                *reinterpret_cast<float4*>(chunk + r * kChunkRow + lc) =
+                    view_load(x, q.b, row, q.col0 + lc, n);
+        }
+        __syncwarp();
+        if (q.lane / kChunkRows == h) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(
+                    chunk + (q.lane % kChunkRows) * kChunkRow + j);
+                v[j] = f.x;
+                v[j + 1] = f.y;
+                v[j + 2] = f.z;
+                v[j + 3] = f.w;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void put_rows(const View& x, const Place& q, const float (&v)[32]) {
+    if (in_pieces(x, q)) {
+        if (x.f32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Chunk16 c;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    c.u[i] = make_uint4(
+                        __float_as_uint(v[16 * h + 4 * i]), __float_as_uint(v[16 * h + 4 * i + 1]),
+                        __float_as_uint(v[16 * h + 4 * i + 2]), __float_as_uint(v[16 * h + 4 * i + 3]));
+                own_to_across(q, c);
+                store_across(static_cast<float*>(x.data) + corner_of(x, q) + 16 * h, x.ld * 4, q, c);
+            }
+        } else {
+            store_chunk(static_cast<__nv_bfloat16*>(x.data) + corner_of(x, q), x.ld, q, v);
+        }
+        return;
+    }
+    float* const chunk = reinterpret_cast<float*>(q.stage);
+    const int lr = q.lane >> 3, lc = (q.lane & 7) * 4, n = min(4, q.N - q.col0 - lc);
+#pragma unroll
+    for (int h = 0; h < 32 / kChunkRows; ++h) {
+        __syncwarp();
+        if (q.lane / kChunkRows == h) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<float4*>(chunk + (q.lane % kChunkRows) * kChunkRow + j) =
+                    make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kChunkRows / 4; ++u) {
+            const int r = 4 * u + lr, row = q.row0 + h * kChunkRows + r;
+            if (n > 0 && row < q.M)
+                view_store(x, q.b, row, q.col0 + lc, n,
+                           *reinterpret_cast<const float4*>(chunk + r * kChunkRow + lc));
+        }
+    }
+}
+
+// Transposed: v[j] = X[col0 + j][row0 + lane], which a warp accesses along
+// X's rows.  M and N are still the product's, so X has N rows.
+__device__ __forceinline__ void get_columns(const View& x, const Place& q, float (&v)[32]) {
+    const long long at = (long long)q.b * x.batch_stride + (long long)q.col0 * x.ld + q.row();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        v[j] = 0.0f;
+        if (q.row() < q.M && q.col0 + j < q.N)
+            v[j] = x.f32 ? static_cast<const float*>(x.data)[at + j * x.ld]
+                         : __bfloat162float(static_cast<const __nv_bfloat16*>(x.data)[at + j * x.ld]);
+    }
+}
+__device__ __forceinline__ void put_columns(const View& x, const Place& q, const float (&v)[32]) {
+    const long long at = (long long)q.b * x.batch_stride + (long long)q.col0 * x.ld + q.row();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if (q.row() < q.M && q.col0 + j < q.N) {
+            if (x.f32)
+                static_cast<float*>(x.data)[at + j * x.ld] = v[j];
+            else
+                static_cast<__nv_bfloat16*>(x.data)[at + j * x.ld] = __float2bfloat16(v[j]);
+        }
     }
 }
 
 // Epi: the operator's epilogue.
-//   kSym            the product is symmetric
-//   regs(p, s, b, row, col0, v, off): v[j] = D[row][col0 + j], one row per lane, all lanes
-//                   call it; `off`: the tile lies off the diagonal (of a symmetric product)
-//   kRows           whether the row pass below follows, with
-//   Col cols(p, s, b, col, n)            what depends on the columns alone
-//   Aux load(p, s, b, row, col, n)       what is read before anything is written
-//   store(p, s, b, row, col, n, acc, aux, colv)
-template <int kPair, int kBN, class Epi>
-__global__ void __launch_bounds__(kGemmThreads, 1)
-gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-            const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep) {
-    using C = Config<kPair, kBN>;
+//   kSym                  the product is symmetric: only the tiles on and
+//                         below the diagonal are computed
+//   Pre                   what the epilogue of a chunk reads, as loaded
+//   prefetch(p, q, pre)   starts these loads; called before the chunk's products are read
+//   apply(p, q, pre, v)   v[j] = D[row0 + lane][col0 + j]; all lanes call it
+// and, for sums that are promoted to registers,
+//   start(p, q, sum)      the value that the sum begins with
+//   finish(p, q, sum)     stores it
+template <class Epi>
+__device__ __forceinline__ bool inside(const Place& q) {
+    return q.row0 < q.M && q.col0 < q.N;  // the same for the whole warp
+}
+
+// ------------------------------------------------------- loads and products --
+
+// Tile t of a product: its tile row and tile column.  Symmetric products
+// compute the tiles that reach the diagonal or lie below it, row by row (a
+// tile row holds kAcross tiles per tile height); others walk down kGroup tile
+// rows before they move to the next tile column.
+template <bool kSym, int kAcross>
+__device__ __forceinline__ void tile_at(const Shape& s, int t, int& tm, int& tn) {
+    if constexpr (kSym) {
+        const int u = t / kAcross;
+        int r = (int)((sqrtf(8.0f * (float)u + 1.0f) - 1.0f) * 0.5f);
+        while ((long long)(r + 1) * (r + 2) / 2 <= u) ++r;
+        while ((long long)r * (r + 1) / 2 > u) --r;
+        tm = r;
+        tn = t - (int)((long long)r * (r + 1) / 2) * kAcross;
+    } else {
+        const int per = kGroup * s.tiles_n;
+        const int g = t / per, in = t - g * per;
+        const int rows = min(kGroup, s.tiles_m - g * kGroup);
+        tn = in / rows;
+        tm = g * kGroup + (in - tn * rows);
+    }
+}
+
+// A place in the ring of stages.
+template <int kStages>
+struct Ring {
+    int stage = 0;
+    unsigned phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == kStages) stage = 0, phase ^= 1;
+    }
+};
+
+// One stage: 128 rows of A and kBRows of B, 64 values of K.
+template <int kPair, int kBRows>
+__device__ __forceinline__ void load_stage(unsigned sa, const CUtensorMap* map_a,
+                                           const CUtensorMap* map_b, const Shape& s, unsigned bar,
+                                           int m0, int n0, int k0, int b) {
+    const unsigned sb = sa + kRowsPerCta * kBlockK * 2;
+    if (s.a_mn) {
+#pragma unroll
+        for (int i = 0; i < kRowsPerCta / 64; ++i)
+            tma_load<kPair>(sa + i * kBlockK * 128, map_a, bar, m0 + 64 * i, k0, b);
+    } else {
+        tma_load<kPair>(sa, map_a, bar, k0, m0, b);
+    }
+    if (s.b_mn) {
+#pragma unroll
+        for (int i = 0; i < (kBRows + 63) / 64; ++i)
+            tma_load<kPair>(sb + i * kBlockK * 128, map_b, bar, n0 + 64 * i, k0, b);
+    } else {
+        tma_load<kPair>(sb, map_b, bar, k0, n0, b);
+    }
+}
+
+template <int kPair>
+__device__ __forceinline__ void multiply_stage(unsigned d, unsigned sa, const Shape& s, bool add) {
+    uint64_t da = smem_desc(sa, s.a_mn), db = smem_desc(sa + kRowsPerCta * kBlockK * 2, s.b_mn);
+    const unsigned step_a = desc_step(s.a_mn), step_b = desc_step(s.b_mn);
+#pragma unroll
+    for (int k = 0; k < kBlockK / 16; ++k) {
+        mma_f16<kPair>(d, da, db, s.idesc, add || k > 0);
+        da += step_a;
+        db += step_b;
+    }
+}
+
+// A dead block waits until its copies and products in flight, which end
+// within microseconds, can no longer touch its memory; and is counted.
+__device__ __forceinline__ void bury(volatile int* dead, unsigned* timeouts) {
+    if (*dead) {
+        if (threadIdx.x == 0) atomicAdd(timeouts, 1u);
+        const long long t0 = clock64();
+        while (clock64() - t0 < 4000000) {
+        }
+    }
+}
+
+// ------------------------------------------------------------- pair kernel --
+
+struct Pair {
+    static constexpr int kBN = 256, kBM = 256;
+    static constexpr int kBRows = kBN / 2;  // rows of B (columns of D) that a block loads
+    static constexpr int kStageBytes = (kRowsPerCta + kBRows) * kBlockK * 2;
+    static constexpr int kChunkBytes = kEpilogueWarps * kWarpStage;
+    static constexpr int kBarBytes = 256;
+    static constexpr int kStages = 6;
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kChunkBytes + kBarBytes;
+    static constexpr int kTmemCols = 2 * kBN;  // two accumulators
+    static_assert(kSmem <= kSmemPerBlock, "shared memory");
+};
+
+// One or two products in one launch (the second one's tiles may be 0), whose
+// blocks then share the work of both: the first has the longer tiles.
+template <class Epi>
+struct PairWork {
+    Shape s[2];
+    typename Epi::Params ep[2];
+    int extra;  // second product's tiles that a pair without a last tile of the first takes first
+    unsigned* timeouts;
+};
+
+// The i-th tile of pair `slot`: false when there is none.  First the first
+// product's tiles in turn; where these do not come out even, the pairs that
+// are one short take `extra` tiles of the second product, about as long
+// together; then the rest of it in turn.
+template <class Epi>
+__device__ __forceinline__ bool work_item(const PairWork<Epi>& w, int slot, int slots, int i, int& which,
+                                          int& t) {
+    const int n0 = w.s[0].total, n1 = w.s[1].total;
+    const int c0 = slot < n0 ? (n0 - slot + slots - 1) / slots : 0;
+    which = 0;
+    t = slot + i * slots;
+    if (i < c0) return true;
+    if (n1 == 0) return false;
+    which = 1;
+    i -= c0;
+    const int r = n0 % slots;
+    if (r == 0) {
+        t = slot + i * slots;
+        return t < n1;
+    }
+    if (slot >= r) {
+        if (i < w.extra) {
+            t = i * (slots - r) + (slot - r);
+            return t < n1;
+        }
+        i -= w.extra;
+    }
+    t = (slots - r) * w.extra + slot + i * slots;
+    return t < n1;
+}
+
+// kPromote: sums in tensor memory are cut to `segment` K blocks, which the
+// epilogue warps add in registers, rounding to nearest.  (The tensor cores
+// cut accumulated sums off instead: measured 1e-6 relative, towards zero, for
+// sums of 1024 products, and growing with their number.)
+template <class Epi, int kCount, bool kPromote>
+__global__ void __launch_bounds__(kPairThreads, 1)
+pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_b0,
+            const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b1,
+            const __grid_constant__ PairWork<Epi> w) {
+    using C = Pair;
     extern __shared__ unsigned char smem_raw[];
     const unsigned base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* const gen = smem_raw + (base - smem_u32(smem_raw));
-    float* const chunks = reinterpret_cast<float*>(gen + C::kStages * C::kStageBytes);
-    const unsigned bars = base + C::kStages * C::kStageBytes + C::kChunkBytes;
-    const unsigned full = bars, empty = full + 8 * C::kStages, tfull = empty + 8 * C::kStages,
-                   tempty = tfull + 16;
+    unsigned char* const chunks = gen + C::kStages * C::kStageBytes;
+    const unsigned full = base + C::kStages * C::kStageBytes + C::kChunkBytes;
+    const unsigned empty = full + 8 * C::kStages, tfull = empty + 8 * C::kStages, tempty = tfull + 16;
     unsigned char* const tail = gen + (tempty + 16 - base);
     unsigned* const tmem_slot = reinterpret_cast<unsigned*>(tail);
     volatile int* const dead = reinterpret_cast<volatile int*>(tail + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const unsigned rank = kPair == 2 ? cluster_rank() : 0;
+    const unsigned rank = cluster_rank();
     const bool leader = rank == 0;
-    const int first = blockIdx.x / kPair, step = gridDim.x / kPair;
-    const int total = s.tiles * s.batch;
+    const int slot = blockIdx.x / 2, slots = gridDim.x / 2;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -413,19 +807,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + 8 * i, 1);
-            mbar_init(tempty + 8 * i, kPair * kEpilogueWarps);
+            mbar_init(tempty + 8 * i, 2 * kEpilogueWarps);
         }
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        tma_prefetch(&map_a);
-        tma_prefetch(&map_b);
+        tma_prefetch(&map_a0);
+        tma_prefetch(&map_b0);
     }
-    if (warp == 1) tmem_alloc<kPair>(smem_u32(tmem_slot), C::kTmemCols);
+    if (warp == 1) tmem_alloc<2>(smem_u32(tmem_slot), C::kTmemCols);
     tcgen05_fence_before();
-    if constexpr (kPair == 2)
-        cluster_sync_all();
-    else
-        __syncthreads();
+    cluster_sync_all();
     tcgen05_fence_after();
     const unsigned tmem = *tmem_slot;
     // The next kernel on the stream may be set up from here on; this one
@@ -433,178 +824,365 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    int which, t;
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            unsigned phase = 0;
-            bool alive = true;
-            const int arows = kRowsPerCta * kPair;
-            for (int t = first; t < total && alive; t += step) {
-                const int b = t / s.tiles;
-                int tm, tn;
-                tile_at<Epi::kSym>(s, t - b * s.tiles, tm, tn);
-                const int m0 = tm * arows + (int)rank * kRowsPerCta;
-                const int n0 = tn * kBN + (int)rank * C::kBRows;
-                for (int kb = 0; kb < s.kblocks; ++kb) {
-                    if (!mbar_wait(empty + 8 * stage, phase ^ 1, dead)) {
-                        alive = false;
-                        break;
-                    }
-                    const unsigned sa = base + stage * C::kStageBytes, sb = sa + C::kABytes;
-                    const unsigned bar = kPair == 2 ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
-                    if (leader) mbar_expect(full + 8 * stage, kPair * C::kStageBytes);
-                    const int k0 = kb * kBlockK;
-                    if (s.a_mn) {
-#pragma unroll
-                        for (int i = 0; i < kRowsPerCta / 64; ++i)
-                            tma_load<kPair>(sa + i * kBlockK * 128, &map_a, bar, m0 + 64 * i, k0, b);
-                    } else {
-                        tma_load<kPair>(sa, &map_a, bar, k0, m0, b);
-                    }
-                    if (s.b_mn) {
-#pragma unroll
-                        for (int i = 0; i < C::kBRows / 64; ++i)
-                            tma_load<kPair>(sb + i * kBlockK * 128, &map_b, bar, n0 + 64 * i, k0, b);
-                    } else {
-                        tma_load<kPair>(sb, &map_b, bar, k0, n0, b);
-                    }
-                    if (++stage == C::kStages) stage = 0, phase ^= 1;
-                }
-            }
-            // No copy of this block's may be in flight when it ends: wait
-            // until every stage has been consumed.
-            for (int i = 0; i < C::kStages && alive; ++i) {
-                alive = mbar_wait(empty + 8 * stage, phase ^ 1, dead);
-                if (++stage == C::kStages) stage = 0, phase ^= 1;
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            int stage = 0, it = 0;
-            unsigned phase = 0;
-            bool alive = true;
-            const unsigned step_a = desc_step(s.a_mn), step_b = desc_step(s.b_mn);
-            for (int t = first; t < total && alive; t += step, ++it) {
-                const int acc = it & 1;
-                if (!mbar_wait(tempty + 8 * acc, ((it >> 1) & 1) ^ 1, dead)) break;
-                tcgen05_fence_after();
-                const unsigned d = tmem + acc * kBN;
-                for (int kb = 0; kb < s.kblocks; ++kb) {
-                    if (!mbar_wait(full + 8 * stage, phase, dead)) {
-                        alive = false;
-                        break;
-                    }
-                    tcgen05_fence_after();
-                    const unsigned sa = base + stage * C::kStageBytes;
-                    uint64_t da = smem_desc(sa, s.a_mn), db = smem_desc(sa + C::kABytes, s.b_mn);
-#pragma unroll
-                    for (int k = 0; k < kBlockK / 16; ++k) {
-                        mma_f16<kPair>(d, da, db, s.idesc, kb > 0 || k > 0);
-                        da += step_a;
-                        db += step_b;
-                    }
-                    mma_commit<kPair>(empty + 8 * stage);
-                    if (++stage == C::kStages) stage = 0, phase ^= 1;
-                }
-                mma_commit<kPair>(tfull + 8 * acc);
-            }
-        }
-        __syncwarp();
-    } else {
-        const int ew = warp - 2;
-        const int quarter = warp & 3;       // the tensor-memory lanes this warp may read
-        const int half = ew >> 2;           // and its half of the columns
-        float* const chunk = chunks + ew * 32 * kStageRow;
-        const unsigned tempty_lead = kPair == 2 ? map_rank(tempty, 0) : tempty;
-        int it = 0;
-        for (int t = first; t < total; t += step, ++it) {
+        Ring<C::kStages> ring;
+        bool alive = true;
+        for (int i = 0; alive && work_item(w, slot, slots, i, which, t); ++i) {
+            const Shape s = w.s[kCount == 1 ? 0 : which];
+            const CUtensorMap* ma = which ? &map_a1 : &map_a0;
+            const CUtensorMap* mb = which ? &map_b1 : &map_b0;
             const int b = t / s.tiles;
             int tm, tn;
-            tile_at<Epi::kSym>(s, t - b * s.tiles, tm, tn);
-            const int acc = it & 1;
-            const int row0 = tm * kRowsPerCta * kPair + (int)rank * kRowsPerCta + quarter * 32;
-            const int col_first = tn * kBN + half * (kBN / 2);
-            // (every lane waits, and all lanes of a warp get the same answer
-            // before the warp-wide instructions below)
-            const bool ok = mbar_wait(tfull + 8 * acc, (it >> 1) & 1, dead);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            tcgen05_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < kBN / 64; ++c) {
-                const int col0 = col_first + 32 * c;
-                float v[32];
-                tmem_load32(tmem + ((unsigned)(quarter * 32) << 16) + acc * kBN + half * (kBN / 2) +
-                                32 * c,
-                            v);
-                if (c == kBN / 64 - 1) {
+            tile_at<Epi::kSym, C::kBM / C::kBN>(s, t - b * s.tiles, tm, tn);
+            const int m0 = tm * C::kBM + (int)rank * kRowsPerCta;
+            const int n0 = tn * C::kBN + (int)rank * C::kBRows;
+            for (int kb = 0; kb < s.kblocks; ++kb) {
+                alive = warp_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead);
+                if (!alive) break;
+                if (elect_one()) {
+                    // both blocks' copies count on the leading block's barrier
+                    if (leader) mbar_expect(full + 8 * ring.stage, 2 * C::kStageBytes);
+                    load_stage<2, C::kBRows>(base + ring.stage * C::kStageBytes, ma, mb, s,
+                                             map_rank(full + 8 * ring.stage, 0), m0, n0,
+                                             kb * kBlockK, b);
+                }
+                __syncwarp();
+                ring.next();
+            }
+        }
+        // No copy of this block's may be in flight when it ends: wait until
+        // every stage has been consumed.
+        for (int i = 0; i < C::kStages && alive; ++i) {
+            alive = warp_wait(empty + 8 * ring.stage, ring.phase ^ 1, dead);
+            ring.next();
+        }
+    } else if (warp == 1) {
+        if (leader) {
+            Ring<C::kStages> ring;
+            Ring<2> acc;
+            bool alive = true;
+            for (int i = 0; alive && work_item(w, slot, slots, i, which, t); ++i) {
+                const Shape s = w.s[kCount == 1 ? 0 : which];
+                int kb = 0;
+                do {
+                    const int stop = kPromote ? min(kb + s.segment, s.kblocks) : s.kblocks;
+                    alive = warp_wait(tempty + 8 * acc.stage, acc.phase ^ 1, dead);
+                    if (!alive) break;
+                    tcgen05_fence_after();
+                    for (bool add = false; kb < stop; ++kb, add = true) {
+                        alive = warp_wait(full + 8 * ring.stage, ring.phase, dead);
+                        if (!alive) break;
+                        tcgen05_fence_after();
+                        if (elect_one()) {
+                            multiply_stage<2>(tmem + acc.stage * C::kBN,
+                                              base + ring.stage * C::kStageBytes, s, add);
+                            mma_commit<2>(empty + 8 * ring.stage);
+                        }
+                        __syncwarp();
+                        ring.next();
+                    }
+                    if (elect_one()) mma_commit<2>(tfull + 8 * acc.stage);
+                    __syncwarp();
+                    acc.next();
+                } while (alive && kb < s.kblocks);
+            }
+        }
+    } else {
+        const int ew = warp - 2;
+        const int quarter = warp & 3;  // the tensor-memory lanes this warp may read
+        const int half = ew >> 2;      // and its half of the columns
+        constexpr int kChunks = C::kBN / 64;
+        const unsigned lanes = tmem + ((unsigned)(quarter * 32) << 16) + half * (C::kBN / 2);
+        const unsigned tempty_lead = map_rank(tempty, 0);
+        Ring<2> acc;
+        bool alive = true;
+        // (the parameters of each product are read at fixed places, which the
+        // compiler turns into operands of the instructions)
+        auto tile = [&](const Shape& s, const typename Epi::Params& ep) {
+            const int b = t / s.tiles;
+            int tm, tn;
+            tile_at<Epi::kSym, C::kBM / C::kBN>(s, t - b * s.tiles, tm, tn);
+            Place q;
+            q.b = b;
+            q.row0 = tm * C::kBM + (int)rank * kRowsPerCta + quarter * 32;
+            q.col0 = tn * C::kBN + half * (C::kBN / 2);
+            q.M = s.M;
+            q.N = s.N;
+            q.lane = lane;
+            q.off = tm != tn;
+            q.stage = chunks + ew * kWarpStage;
+            if constexpr (kPromote) {
+                float sum[kChunks][32];
+                Place at = q;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c, at.col0 += 32) Epi::start(ep, at, sum[c]);
+                int kb = 0;
+                do {
+                    kb += s.segment;
+                    alive = warp_wait(tfull + 8 * acc.stage, acc.phase, dead);
+                    if (!alive) break;
+                    tcgen05_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 2 * kChunks; ++c) {
+                        float v[16];
+                        tmem_load16(lanes + acc.stage * C::kBN + 16 * c, v);
+                        if (s.kblocks > 0) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[c / 2][(c & 1) * 16 + j] += v[j];
+                        }
+                    }
                     tcgen05_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(tempty_lead + 8 * acc);
+                    if (lane == 0) mbar_arrive_cluster(tempty_lead + 8 * acc.stage);
+                    acc.next();
+                } while (kb < s.kblocks);
+                if (!alive) return;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c, q.col0 += 32) {
+                    if (inside<Epi>(q)) Epi::finish(ep, q, sum[c]);
                 }
-                if (s.kblocks == 0) {
+            } else {
+                typename Epi::Pre pre;
+                if (inside<Epi>(q)) Epi::prefetch(ep, q, pre);
+                alive = warp_wait(tfull + 8 * acc.stage, acc.phase, dead);
+                if (!alive) return;
+                tcgen05_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    float v[32];
+                    tmem_load32(lanes + acc.stage * C::kBN + 32 * c, v);
+                    if (c == kChunks - 1) {
+                        tcgen05_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(tempty_lead + 8 * acc.stage);
+                    }
+                    if (s.kblocks == 0) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    }
+                    if (inside<Epi>(q)) Epi::apply(ep, q, pre, v);
+                    q.col0 += 32;
+                    if (c < kChunks - 1 && inside<Epi>(q)) Epi::prefetch(ep, q, pre);
+                }
+                acc.next();
+            }
+        };
+        for (int i = 0; alive && work_item(w, slot, slots, i, which, t); ++i) {
+            if (kCount == 1 || which == 0)
+                tile(w.s[0], w.ep[0]);
+            else
+                tile(w.s[1], w.ep[1]);
+        }
+    }
+    tcgen05_fence_before();
+    cluster_sync_all();
+    tcgen05_fence_after();
+    bury(dead, w.timeouts);
+    if (warp == 1) tmem_free<2>(tmem, C::kTmemCols);
+}
+
+// ------------------------------------------------------------ split kernel --
+
+template <int kTileN>
+struct Split {
+    static constexpr int kBM = kRowsPerCta, kBN = kTileN;
+    static constexpr int kStageBytes = (kRowsPerCta + kBN) * kBlockK * 2;
+    static constexpr int kWarps = 4;  // of the epilogue
+    static constexpr int kThreads = 32 * (2 + kWarps);
+    // partial chunks that the cluster's blocks (up to 8) send to this one
+    static constexpr int kPartBytes = kBN < 64 ? 8 * 4096 : kRowsPerCta * kBN * 4;
+    static constexpr int kChunkBytes = kWarps * kWarpStage;
+    static constexpr int kBarBytes = 256;
+    static constexpr int kMaxStages = 8;
+    static constexpr int kFixed = 1024 + kPartBytes + kChunkBytes + kBarBytes;
+    static constexpr int kTmemCols = kBN;
+    // Two blocks fit an SM with few stages, so that one's set-up, or the
+    // next launch's, runs beside the other's work; with one block per SM,
+    // more stages cover the latency of the memory.
+    static constexpr int kFewStages = (kSmemPerBlock / 2 - 1024 - kFixed) / kStageBytes;
+    static constexpr int kManyStages =
+        (kSmemPerBlock - kFixed) / kStageBytes < kMaxStages ? (kSmemPerBlock - kFixed) / kStageBytes : kMaxStages;
+    static_assert(kFewStages >= 2, "shared memory");
+    static_assert((2 * kMaxStages + 1) * 8 + 8 <= kBarBytes, "barriers");
+};
+
+// A cluster of blocks computes one 128 x kBN tile; block `rank` takes the
+// rank-th part of K.  The tile's 32 x 32 chunks are shared out over the
+// blocks: each sends its partial chunks to their owners, who add them in rank
+// order and run the epilogue.
+template <int kBN, class Epi>
+__global__ void __launch_bounds__(Split<kBN>::kThreads, 2)
+split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+             const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep,
+             unsigned* timeouts, int ranks, int stages) {
+    using C = Split<kBN>;
+    extern __shared__ unsigned char smem_raw[];
+    const unsigned base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char* const gen = smem_raw + (base - smem_u32(smem_raw));
+    float4* const part = reinterpret_cast<float4*>(gen + stages * C::kStageBytes);
+    unsigned char* const chunks = gen + stages * C::kStageBytes + C::kPartBytes;
+    const unsigned full = base + stages * C::kStageBytes + C::kPartBytes + C::kChunkBytes;
+    const unsigned empty = full + 8 * C::kMaxStages, tfull = empty + 8 * C::kMaxStages;
+    unsigned char* const tail = gen + (tfull + 8 - base);
+    unsigned* const tmem_slot = reinterpret_cast<unsigned*>(tail);
+    volatile int* const dead = reinterpret_cast<volatile int*>(tail + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        mbar_init(tfull, 1);
+        *dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch(&map_a);
+        tma_prefetch(&map_b);
+    }
+    if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), C::kTmemCols);
+    tcgen05_fence_before();
+    // (every block of the cluster has begun before another writes to it)
+    if (ranks > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    tcgen05_fence_after();
+    const unsigned tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const int tile = blockIdx.x / ranks;
+    const int b = tile / s.tiles;
+    int tm, tn;
+    tile_at<Epi::kSym, C::kBM / C::kBN>(s, tile - b * s.tiles, tm, tn);
+    const int m0 = tm * C::kBM, n0 = tn * kBN;
+    const int kb0 = (int)((long long)s.kblocks * rank / ranks);
+    const int kb1 = (int)((long long)s.kblocks * (rank + 1) / ranks);
+    const int ew = warp - 2, quarter = warp & 3;
+    constexpr int kUnits = kBN / 8;  // chunks of the tile: unit u has rows (u & 3), columns u >> 2
+    Place q;
+    q.b = b;
+    q.M = s.M;
+    q.N = s.N;
+    q.lane = lane;
+    q.off = tn / (C::kBM / C::kBN) != tm;
+    q.stage = chunks + ew * kWarpStage;
+    typename Epi::Pre pre;
+    // this warp's first unit: its own quarter where K is not split
+    int unit = ranks == 1 ? quarter : rank + ranks * ew;
+
+    if (warp == 0) {
+        int stage = 0;
+        unsigned phase = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(empty + 8 * stage, phase ^ 1, dead)) break;
+            if (elect_one()) {
+                mbar_expect(full + 8 * stage, C::kStageBytes);
+                load_stage<1, kBN>(base + stage * C::kStageBytes, &map_a, &map_b, s,
+                                   full + 8 * stage, m0, n0, kb * kBlockK, b);
+            }
+            __syncwarp();
+            if (++stage == stages) stage = 0, phase ^= 1;
+        }
+    } else if (warp == 1) {
+        int stage = 0;
+        unsigned phase = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(full + 8 * stage, phase, dead)) break;
+            tcgen05_fence_after();
+            if (elect_one()) {
+                multiply_stage<1>(tmem, base + stage * C::kStageBytes, s, kb > kb0);
+                mma_commit<1>(empty + 8 * stage);
+            }
+            __syncwarp();
+            if (++stage == stages) stage = 0, phase ^= 1;
+        }
+        if (elect_one()) mma_commit<1>(tfull);
+        __syncwarp();
+    } else {
+        q.row0 = m0 + (unit & 3) * 32;
+        q.col0 = n0 + (unit >> 2) * 32;
+        if (unit < kUnits && inside<Epi>(q)) Epi::prefetch(ep, q, pre);
+        const bool ok = warp_wait(tfull, 0, dead);
+        tcgen05_fence_after();
+        if (ok) {
+            for (int c = 0; c < kBN / 32; ++c) {
+                float v[32];
+                tmem_load32(tmem + ((unsigned)(quarter * 32) << 16) + 32 * c, v);
+                if (kb1 == kb0) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 }
-                if (row0 >= s.M || col0 >= s.N) continue;  // the same for the whole warp
-                Epi::regs(ep, s, b, row0 + lane, col0, v, tm != tn);
-                if constexpr (Epi::kRows) {
+                if (ranks == 1) {
+                    if (inside<Epi>(q)) Epi::apply(ep, q, pre, v);
+                    q.col0 += 32;
+                    if (c + 1 < kBN / 32 && inside<Epi>(q)) Epi::prefetch(ep, q, pre);
+                } else {
+                    // to slot [unit of the owner][from rank][8 x 32 lanes]
+                    const int u = c * 4 + quarter, owner = u % ranks, k = u / ranks;
+                    const unsigned at = map_rank(smem_u32(part + (k * ranks + rank) * 256 + lane), owner);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<float4*>(chunk + lane * kStageRow + j) =
-                            make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                    __syncwarp();
-                    const int lr = lane >> 3, col = col0 + (lane & 7) * 4;
-                    const int n = min(4, s.N - col);
-                    if (n > 0) {
-                        const typename Epi::Col cv = Epi::cols(ep, s, b, col, n);
-#pragma unroll
-                        for (int r = 0; r < 8; r += 4) {
-                            typename Epi::Aux aux[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const int row = row0 + (r + u) * 4 + lr;
-                                if (row < s.M) aux[u] = Epi::load(ep, s, b, row, col, n);
-                            }
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const int row = row0 + (r + u) * 4 + lr;
-                                const float4 a = *reinterpret_cast<const float4*>(
-                                    chunk + ((r + u) * 4 + lr) * kStageRow + (lane & 7) * 4);
-                                if (row < s.M) Epi::store(ep, s, b, row, col, n, a, aux[u], cv);
-                            }
-                        }
-                    }
-                    __syncwarp();
+                    for (int j = 0; j < 8; ++j)
+                        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         at + j * 512),
+                                     "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]),
+                                     "f"(v[4 * j + 3])
+                                     : "memory");
                 }
             }
         }
     }
     tcgen05_fence_before();
-    if constexpr (kPair == 2)
+    if (ranks > 1) {
         cluster_sync_all();
-    else
-        __syncthreads();
-    tcgen05_fence_after();
-    if (*dead) {
-        if (threadIdx.x == 0) atomicAdd(s.timeouts, 1u);
-        // copies and products in flight end within microseconds
-        const long long t0 = clock64();
-        while (clock64() - t0 < 4000000) {
+        if (ew >= 0) {
+            for (int k = ew; unit < kUnits; unit += ranks * C::kWarps, k += C::kWarps) {
+                q.row0 = m0 + (unit & 3) * 32;
+                q.col0 = n0 + (unit >> 2) * 32;
+                if (!inside<Epi>(q)) continue;
+                if (k != ew) Epi::prefetch(ep, q, pre);
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                for (int r = 0; r < ranks; ++r) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 x = part[(k * ranks + r) * 256 + j * 32 + lane];
+                        v[4 * j] += x.x;
+                        v[4 * j + 1] += x.y;
+                        v[4 * j + 2] += x.z;
+                        v[4 * j + 3] += x.w;
+                    }
+                }
+                Epi::apply(ep, q, pre, v);
+            }
         }
+        __syncthreads();
+    } else {
+        __syncthreads();
     }
-    if (warp == 1) tmem_free<kPair>(tmem, C::kTmemCols);
+    tcgen05_fence_after();
+    bury(dead, timeouts);
+    if (warp == 1) tmem_free<1>(tmem, C::kTmemCols);
 }
 
 // ------------------------------------------------------------- host side --
 
-// One operand of a product as the kernel loads it: `major` values contiguous
-// (K, or M / N when mn_major), `outer` rows of them, ld apart.
+// One operand of a product as the kernel loads it: `inner` values contiguous
+// (along K, or along M / N when mn_major), `outer` rows of them, ld apart.
 struct Operand {
     const void* data;
     long long inner, outer, ld, batch_stride;
     bool bf16;
     bool mn_major;
+};
+
+// One product D[M, N] = A[M, K] B[K, N], or a batch of them.
+struct Product {
+    Operand a, b;
+    int M, N, K, batch;
 };
 
 // Encodes the tensor map for boxes of 64 x box_rows; false when the driver
@@ -627,65 +1205,181 @@ inline unsigned instruction_desc(bool bf16, bool a_mn, bool b_mn, int m, int n) 
            ((unsigned)(m >> 4) << 24);
 }
 
-// Launches D = A B with the tile kPair * 128 x kBN.
-template <int kPair, int kBN, class Epi>
-cudaError_t launch_tile(const Operand& a, const Operand& b, int M, int N, int K, int batch,
-                        const typename Epi::Params& ep, cudaStream_t st) {
-    using C = Config<kPair, kBN>;
-    constexpr int kBM = kRowsPerCta * kPair;
-    static_assert(!Epi::kSym || kBM == kBN, "symmetric products use square tiles");
-    Shape s = {};
-    s.M = M;
-    s.N = N;
-    s.K = K;
-    s.batch = batch;
-    s.tiles_m = (M + kBM - 1) / kBM;
-    s.tiles_n = (N + kBN - 1) / kBN;
-    const long long tiles = Epi::kSym ? (long long)s.tiles_m * (s.tiles_m + 1) / 2
-                                      : (long long)s.tiles_m * s.tiles_n;
-    if (tiles * batch > 0x3FFFFFFF) return cudaErrorInvalidValue;
-    s.tiles = (int)tiles;
-    if (s.tiles * batch == 0) return cudaSuccess;
-    s.kblocks = (K + kBlockK - 1) / kBlockK;
-    s.group = 8;
-    s.a_mn = a.mn_major;
-    s.b_mn = b.mn_major;
-    s.idesc = instruction_desc(a.bf16, a.mn_major, b.mn_major, kBM, kBN);
-    CUtensorMap ma, mb;
-    if (K > 0) {
-        if (!encode_operand(&ma, a, batch, a.mn_major ? kBlockK : kRowsPerCta) ||
-            !encode_operand(&mb, b, batch, b.mn_major ? kBlockK : C::kBRows))
-            return cudaErrorInvalidValue;
-    } else {  // nothing is loaded
-        ma = CUtensorMap{};
-        mb = CUtensorMap{};
-    }
-    const int sms = device_sms();
-    s.timeouts = timeout_counter();
-    if (sms < 1 || s.timeouts == nullptr) return cudaErrorInvalidConfiguration;
-    auto* kernel = gemm_kernel<kPair, kBN, Epi>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::kSmem);
+// (a symmetric product's last tile row may hold a tile beyond its columns,
+// which computes nothing that is written)
+inline long long tile_count(long long M, long long N, int bm, int bn, bool sym) {
+    const long long tm = (M + bm - 1) / bm, tn = (N + bn - 1) / bn;
+    return sym ? tm * (tm + 1) / 2 * (bm / bn) : tm * tn;
+}
+
+inline cudaError_t shape_of(const Product& p, int bm, int bn, bool sym, Shape* s) {
+    *s = Shape{};
+    s->M = p.M;
+    s->N = p.N;
+    s->K = p.K;
+    s->tiles_m = (p.M + bm - 1) / bm;
+    s->tiles_n = (p.N + bn - 1) / bn;
+    const long long tiles = tile_count(p.M, p.N, bm, bn, sym);
+    if (tiles * p.batch > 0x0FFFFFFF) return cudaErrorInvalidValue;
+    s->tiles = (int)tiles;
+    s->total = (int)(tiles * p.batch);
+    s->kblocks = (p.K + kBlockK - 1) / kBlockK;
+    s->segment = s->kblocks > 0 ? s->kblocks : 1;
+    s->a_mn = p.a.mn_major;
+    s->b_mn = p.b.mn_major;
+    s->idesc = instruction_desc(p.a.bf16, p.a.mn_major, p.b.mn_major, bm, bn);
+    return cudaSuccess;
+}
+
+inline bool encode_product(const Product& p, int b_rows, CUtensorMap* ma, CUtensorMap* mb) {
+    *ma = CUtensorMap{};
+    *mb = CUtensorMap{};
+    if (p.K == 0) return true;  // nothing is loaded
+    return encode_operand(ma, p.a, p.batch, p.a.mn_major ? kBlockK : kRowsPerCta) &&
+           encode_operand(mb, p.b, p.batch, p.b.mn_major ? kBlockK : b_rows);
+}
+
+// Lets the kernel have all of an SM's shared memory, once per device.
+cudaError_t allow_smem(const void* kernel);
+
+template <class Kernel, class... Args>
+cudaError_t launch_cluster(Kernel* kernel, int blocks, int threads, int cluster, int smem,
+                           cudaStream_t st, const Args&... args) {
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel));
     if (e != cudaSuccess) return e;
-    const int slots = sms / kPair;
-    const int want = s.tiles * batch < slots ? s.tiles * batch : slots;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(want * kPair);
-    cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kPair;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, s, ep);
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
+}
+
+// One or two products in one launch of the pair kernel.  segment: K
+// blocks summed in tensor memory at a time (kPromote).
+template <class Epi, int kCount, bool kPromote>
+cudaError_t launch_pair(const Product* p, const typename Epi::Params* ep, int segment,
+                        cudaStream_t st) {
+    PairWork<Epi> w = {};
+    CUtensorMap m[4] = {};
+    // the product with the longer tiles first
+    const int first = kCount == 2 && p[kCount - 1].K > p[0].K ? 1 : 0;
+    for (int i = 0; i < kCount; ++i) {
+        const int from = i == 0 ? first : 1 - first;
+        const cudaError_t e = shape_of(p[from], Pair::kBM, Pair::kBN, Epi::kSym, &w.s[i]);
+        if (e != cudaSuccess) return e;
+        if (kPromote) w.s[i].segment = segment;
+        w.ep[i] = ep[from];
+        if (!encode_product(p[from], Pair::kBRows, &m[2 * i], &m[2 * i + 1]))
+            return cudaErrorInvalidValue;
+    }
+    const int sms = device_sms();
+    w.timeouts = timeout_counter();
+    if (sms < 2 || w.timeouts == nullptr) return cudaErrorInvalidConfiguration;
+    const int slots = sms / 2, total = w.s[0].total + w.s[1].total;
+    if (total == 0) return cudaSuccess;
+    const int pairs = total < slots ? total : slots;
+    if (w.s[1].total > 0 && w.s[0].total % pairs != 0)
+        w.extra = w.s[0].kblocks / (w.s[1].kblocks > 0 ? w.s[1].kblocks : 1);
+    return launch_cluster(pair_kernel<Epi, kCount, kPromote>, pairs * 2, kPairThreads, 2, Pair::kSmem, st, m[0], m[1],
+                          m[2], m[3], w);
+}
+
+template <int kBN, class Epi>
+cudaError_t launch_split(const Product& p, const typename Epi::Params& ep, int ranks,
+                         cudaStream_t st) {
+    using C = Split<kBN>;
+    Shape s;
+    const cudaError_t e = shape_of(p, C::kBM, C::kBN, Epi::kSym, &s);
+    if (e != cudaSuccess) return e;
+    if (s.total == 0) return cudaSuccess;
+    CUtensorMap ma, mb;
+    if (!encode_product(p, kBN, &ma, &mb)) return cudaErrorInvalidValue;
+    unsigned* timeouts = timeout_counter();
+    if (timeouts == nullptr) return cudaErrorInvalidConfiguration;
+    const int blocks = s.total * ranks;
+    const int stages = blocks <= device_sms() ? C::kManyStages : C::kFewStages;
+    return launch_cluster(split_kernel<kBN, Epi>, blocks, C::kThreads, ranks,
+                          C::kFixed + stages * C::kStageBytes, st, ma, mb, s, ep, timeouts, ranks,
+                          stages);
+}
+
+// How long a product takes, in microseconds, by a model of the two kernels
+// that was fitted to measurements of 1 to 512 tiles and K of 64 to 8192 on
+// operands in L2 (within 20 % of most): a fixed part, and for each wave of
+// tiles the larger of its K blocks' time and its epilogue's.
+//   pair kernel:   6.5 + waves of 76 x max(0.275 K blocks + 0.5, 3.2)
+//   split kernel:  1.5 + waves of 304 blocks x (2.3 + c K blocks of a rank)
+//                  (+ 0.7 where K is split), c = 0.21 with one block per SM
+//                  and 0.30 with two
+// e.g. 2048 x 2048 x 2048: 17 us (pair), 25 us (split); 512 x 512 x 2048:
+// 15.8 us and 6.1 us; 1024 x 1024 x 4096: 24 us and 14 us.
+inline double pair_us(const Product* p, int count, bool sym) {
+    double tile_us = 0.0, longest = 0.0;
+    long long total = 0;
+    const int slots = device_sms() / 2;
+    for (int i = 0; i < count; ++i) {
+        const long long tiles = tile_count(p[i].M, p[i].N, Pair::kBM, Pair::kBN, sym) * p[i].batch;
+        const double k = 0.275 * ((p[i].K + kBlockK - 1) / kBlockK) + 0.5;
+        const double each = k > 3.2 ? k : 3.2;
+        longest = each > longest ? each : longest;
+        tile_us += each * (double)tiles;
+        total += tiles;
+    }
+    if (count == 1) return 6.5 + longest * (double)((total + slots - 1) / slots);
+    const double even = tile_us / slots;
+    return 6.5 + (even > longest ? even : longest);
+}
+
+struct Plan {
+    double us;
+    int ranks;
+};
+
+// The split kernel's best number of ranks; limit > 0: at most so many K blocks
+// per rank (1e9 us where 8 ranks do not reach that).
+template <int kBN = 64>
+inline Plan plan_split(const Product& p, bool sym, int limit) {
+    using C = Split<kBN>;
+    const long long tiles = tile_count(p.M, p.N, C::kBM, kBN, sym) * p.batch;
+    const int kblocks = (p.K + kBlockK - 1) / kBlockK, sms = device_sms();
+    Plan best = {1e9, 1};
+    for (int ranks = 1; ranks <= 8; ranks *= 2) {
+        const int kb = (kblocks + ranks - 1) / ranks;
+        if (limit > 0 && kb > limit) continue;
+        const long long blocks = tiles * ranks;
+        const double c = blocks <= sms ? 0.21 : 0.30;
+        const double us = 1.5 + (double)((blocks + 2 * sms - 1) / (2 * sms)) * (2.3 + c * kb) +
+                          (ranks > 1 ? 0.7 : 0.0);
+        if (us < best.us) best = {us, ranks};
+    }
+    return best;
+}
+
+// Picks the kernel and the ranks.
+template <class Epi>
+cudaError_t launch(const Product& p, const typename Epi::Params& ep, cudaStream_t st) {
+    const Plan split = plan_split(p, Epi::kSym, 0);
+    if (split.us < pair_us(&p, 1, Epi::kSym)) return launch_split<64, Epi>(p, ep, split.ranks, st);
+    return launch_pair<Epi, 1, false>(&p, &ep, 0, st);
+}
+
+// A product with few columns: tiles 32 or 64 across.
+template <class Epi>
+cudaError_t launch_skinny(const Product& p, const typename Epi::Params& ep, cudaStream_t st) {
+    if (p.N <= 32) return launch_split<32, Epi>(p, ep, plan_split<32>(p, false, 0).ranks, st);
+    return launch_split<64, Epi>(p, ep, plan_split(p, false, 0).ranks, st);
 }
 
 }  // namespace gemm

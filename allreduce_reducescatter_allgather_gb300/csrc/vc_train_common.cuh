@@ -74,19 +74,34 @@ inline gemm::View view_of(const vc_matrix_t* m) {
     const uintptr_t bytes = v.f32 ? 16 : 8;
     v.vec = reinterpret_cast<uintptr_t>(m->data) % bytes == 0 && v.ld % 4 == 0 &&
             v.batch_stride % 4 == 0;
+    const long long per = v.f32 ? 4 : 8;
+    v.vec16 = reinterpret_cast<uintptr_t>(m->data) % 16 == 0 && v.ld % per == 0 &&
+              v.batch_stride % per == 0;
     return v;
 }
 
 inline size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Row length, in 16-bit values, of matrices laid out in the workspace.
-inline long long padded_ld(long long cols) { return (cols + 7) / 8 * 8; }
+// Row length, in 16-bit values, of matrices laid out in the workspace: whole
+// 32-byte sectors.
+inline long long padded_ld(long long cols) { return (cols + 15) / 16 * 16; }
 
 // ------------------------------------------------------------ activations --
 
-// __expf is good to a few units in the last place of float32 over the range
-// where its result matters here; the results are rounded to bf16.
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// exp2 and the reciprocal are the hardware's approximations, good to two units
+// in the last place of float32; the results are rounded to bf16.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float logistic(float z) { return rcp_fast(1.0f + exp2_fast(-kLog2e * z)); }
 
 constexpr float kGeluK = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
@@ -94,34 +109,95 @@ constexpr float kGeluC = 0.044715f;
 // max(z, 0), NaN kept.
 __device__ __forceinline__ float positive(float z) { return z <= 0.0f ? 0.0f : z; }
 
-__device__ __forceinline__ float act_value(float z, int act) {
-    switch (act) {
-    case VC_ACT_RELU: return positive(z);
-    case VC_ACT_RELU2: return positive(z) * positive(z);
-    case VC_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    // (1 + tanh u) / 2 is the logistic function of 2 u
-    case VC_ACT_GELU_TANH: return z * logistic(kGeluK * (z + kGeluC * z * z * z));
-    case VC_ACT_SILU: return z * logistic(z);
-    default: return z;
+// The activations in three families, so that a kernel holds the arithmetic of
+// one and no element branches: piecewise (none, relu, relu2), logistic (silu
+// and the tanh form of gelu, z / (1 + exp(-k z (1 + c z^2)))), and erf.
+enum { kFamilyPiecewise = 0, kFamilyLogistic = 1, kFamilyErf = 2 };
+
+inline int act_family(int act) {
+    return act == VC_ACT_GELU ? kFamilyErf
+           : act == VC_ACT_GELU_TANH || act == VC_ACT_SILU ? kFamilyLogistic : kFamilyPiecewise;
+}
+
+struct Act {
+    float k, c;      // logistic
+    int identity, square;  // piecewise: none, or max(z, 0) and its square
+};
+inline Act act_params(int act) {
+    Act a = {};
+    a.k = act == VC_ACT_GELU_TANH ? kGeluK : 1.0f;
+    a.c = act == VC_ACT_GELU_TANH ? kGeluC : 0.0f;
+    a.identity = act == VC_ACT_NONE;
+    a.square = act == VC_ACT_RELU2;
+    return a;
+}
+
+// erfc(x / sqrt(2)) / 2 = Phi(-x) for x >= 0, given e = exp(-x^2 / 2): the
+// rational approximation 7.1.26 of Abramowitz and Stegun, "Handbook of
+// Mathematical Functions", with their coefficients halved and p divided by
+// sqrt(2); its error is below 7.5e-8.
+constexpr float kTailP = 0.3275911f * 0.70710678118654752f;
+constexpr float kTail0 = 0.5f * 0.254829592f, kTail1 = 0.5f * -0.284496736f,
+                kTail2 = 0.5f * 1.421413741f, kTail3 = 0.5f * -1.453152027f,
+                kTail4 = 0.5f * 1.061405429f;
+__device__ __forceinline__ float2 normal_tail(float2 x, float2 e) {
+    const float2 d = gemm::fma2(x, gemm::both(kTailP), gemm::both(1.0f));
+    const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    float2 y = gemm::fma2(t, gemm::both(kTail4), gemm::both(kTail3));
+    y = gemm::fma2(t, y, gemm::both(kTail2));
+    y = gemm::fma2(t, y, gemm::both(kTail1));
+    y = gemm::fma2(t, y, gemm::both(kTail0));
+    return gemm::mul2(gemm::mul2(t, y), e);
+}
+// exp(-z^2 / 2)
+__device__ __forceinline__ float2 bell(float2 z) {
+    const float2 q = gemm::mul2(gemm::mul2(z, z), gemm::both(-0.5f * kLog2e));
+    return make_float2(exp2_fast(q.x), exp2_fast(q.y));
+}
+
+// Two values at a time: the epilogues are bound by instructions where K is
+// short, and paired arithmetic halves them.  Not called for the identity.
+template <int kFamily>
+__device__ __forceinline__ float2 act_value(float2 z, const Act& a) {
+    if constexpr (kFamily == kFamilyPiecewise) {
+        const float2 y = make_float2(positive(z.x), positive(z.y));
+        return a.square ? gemm::mul2(y, y) : y;
+    } else if constexpr (kFamily == kFamilyLogistic) {
+        // u = -log2(e) k z (1 + c z^2)
+        const float2 q = gemm::fma2(gemm::mul2(z, z), gemm::both(a.c), gemm::both(1.0f));
+        const float2 u = gemm::mul2(gemm::mul2(z, gemm::both(-kLog2e * a.k)), q);
+        const float2 d = gemm::add2(make_float2(exp2_fast(u.x), exp2_fast(u.y)), gemm::both(1.0f));
+        return gemm::mul2(z, make_float2(rcp_fast(d.x), rcp_fast(d.y)));
+    } else {
+        // max(z, 0) - |z| Phi(-|z|).  (|z| is cut at 30, where the tail is 0
+        // in float32, so that an infinity does not meet it.)
+        const float2 x = make_float2(fminf(fabsf(z.x), 30.0f), fminf(fabsf(z.y), 30.0f));
+        const float2 h = gemm::mul2(x, normal_tail(x, bell(z)));
+        return make_float2(fmaxf(z.x, 0.0f) - h.x, fmaxf(z.y, 0.0f) - h.y);
     }
 }
 
-__device__ __forceinline__ float act_slope(float z, int act) {
-    switch (act) {
-    case VC_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case VC_ACT_RELU2: return 2.0f * positive(z);
-    case VC_ACT_GELU:
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-               z * __expf(-0.5f * z * z) * 0.39894228040143268f;
-    case VC_ACT_GELU_TANH: {
-        const float s = logistic(kGeluK * (z + kGeluC * z * z * z));
-        return s + z * s * (1.0f - s) * kGeluK * (1.0f + 3.0f * kGeluC * z * z);
-    }
-    case VC_ACT_SILU: {
-        const float s = logistic(z);
-        return s * (1.0f + z * (1.0f - s));
-    }
-    default: return 1.0f;
+// act'(z); not called for the identity.
+template <int kFamily>
+__device__ __forceinline__ float2 act_slope(float2 z, const Act& a) {
+    if constexpr (kFamily == kFamilyPiecewise) {
+        return a.square ? make_float2(2.0f * positive(z.x), 2.0f * positive(z.y))
+                        : make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
+    } else if constexpr (kFamily == kFamilyLogistic) {
+        // with u = k z (1 + c z^2): s(u) + z s(u) (1 - s(u)) k (1 + 3 c z^2)
+        const float2 q = gemm::mul2(gemm::mul2(z, z), gemm::both(a.c));
+        const float2 u = gemm::mul2(gemm::mul2(z, gemm::both(a.k)), gemm::add2(q, gemm::both(1.0f)));
+        const float2 s = make_float2(logistic(u.x), logistic(u.y));
+        const float2 rest = make_float2(1.0f - s.x, 1.0f - s.y);
+        const float2 k = gemm::mul2(gemm::fma2(q, gemm::both(3.0f), gemm::both(1.0f)), gemm::both(a.k));
+        return gemm::mul2(s, gemm::fma2(gemm::mul2(z, rest), k, gemm::both(1.0f)));
+    } else {
+        // Phi(z) + z phi(z)
+        const float2 e = bell(z);
+        const float2 x = make_float2(fminf(fabsf(z.x), 30.0f), fminf(fabsf(z.y), 30.0f));
+        const float2 h = normal_tail(x, e);
+        const float2 phi = make_float2(z.x > 0.0f ? 1.0f - h.x : h.x, z.y > 0.0f ? 1.0f - h.y : h.y);
+        return gemm::fma2(gemm::mul2(z, gemm::both(0.39894228040143268f)), e, phi);
     }
 }
 

@@ -9,88 +9,157 @@ namespace train {
 namespace {
 
 using gemm::Operand;
+using gemm::Product;
 using gemm::Shape;
 using gemm::View;
 
 // ------------------------------------------------------------- epilogues --
 
-// y = act(acc + bias) + residual; z = acc + bias kept on request.
+using gemm::Place;
+
+// y = act(acc + bias) + residual; z = acc + bias kept on request.  kSwap: the
+// product is the transposed one, W x^T, so that a chunk's rows are y's columns.
+template <int kFamily, bool kSwap>
 struct EpiForward {
-    static constexpr bool kSym = false, kRows = true;
+    static constexpr bool kSym = false;
     struct Params {
         const __nv_bfloat16* bias;
         View residual, y, preact;
-        int has_residual, has_preact, act, bias_vec;
+        int has_residual, has_preact, bias_vec;
+        Act act;
     };
-    struct Col {
-        float4 bias;
+    struct Pre {
+        gemm::Chunk16 residual;  // as loaded, across the rows
+        gemm::Chunk16 bias;      // of the chunk's columns, the same in every lane
+        float one_bias;          // else: of the lane's column (kSwap: row)
     };
-    struct Aux {
-        float4 residual;
-    };
-    __device__ static void regs(const Params&, const Shape&, int, int, int, float (&)[32], bool) {}
-    __device__ static Col cols(const Params& p, const Shape&, int, int col, int n) {
-        Col c = {make_float4(0.f, 0.f, 0.f, 0.f)};
-        if (p.bias != nullptr) c.bias = gemm::load4(p.bias + col, n, p.bias_vec);
-        return c;
+    __device__ static bool bias_in_pieces(const Params& p, const Place& q) {
+        return !kSwap && p.bias_vec && q.whole();
     }
-    __device__ static Aux load(const Params& p, const Shape&, int, int row, int col, int n) {
-        Aux a = {make_float4(0.f, 0.f, 0.f, 0.f)};
-        if (p.has_residual) a.residual = gemm::view_load(p.residual, 0, row, col, n);
-        return a;
+    __device__ static void prefetch(const Params& p, const Place& q, Pre& pre) {
+        if (p.bias != nullptr) {
+            if (bias_in_pieces(p, q)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    pre.bias.u[i] = *reinterpret_cast<const uint4*>(p.bias + q.col0 + 8 * i);
+            } else {
+                const int at = kSwap ? q.row() : q.col0 + q.lane;
+                pre.one_bias = at < (kSwap ? q.M : q.N) ? __bfloat162float(p.bias[at]) : 0.0f;
+            }
+        }
+        if (!kSwap && p.has_residual && in_pieces(p.residual, q))
+            load_across(static_cast<const __nv_bfloat16*>(p.residual.data) + corner_of(p.residual, q),
+                        p.residual.ld * 2, q, pre.residual);
     }
-    __device__ static void store(const Params& p, const Shape&, int, int row, int col, int n,
-                                 float4 v, const Aux& a, const Col& c) {
-        v.x += c.bias.x;
-        v.y += c.bias.y;
-        v.z += c.bias.z;
-        v.w += c.bias.w;
-        if (p.has_preact) gemm::view_store(p.preact, 0, row, col, n, v);
-        v.x = act_value(v.x, p.act) + a.residual.x;
-        v.y = act_value(v.y, p.act) + a.residual.y;
-        v.z = act_value(v.z, p.act) + a.residual.z;
-        v.w = act_value(v.w, p.act) + a.residual.w;
-        gemm::view_store(p.y, 0, row, col, n, v);
+    __device__ static void apply(const Params& p, const Place& q, Pre& pre, float (&v)[32]) {
+        if (p.bias != nullptr) {
+            if (bias_in_pieces(p, q)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 f = pair_at(pre.bias, i, __nv_bfloat16());
+                    v[2 * i] += f.x;
+                    v[2 * i + 1] += f.y;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] += kSwap ? pre.one_bias : __shfl_sync(0xFFFFFFFFu, pre.one_bias, j);
+            }
+        }
+        if (p.has_preact) kSwap ? put_columns(p.preact, q, v) : put_rows(p.preact, q, v);
+        if (!p.act.identity) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                const float2 y = act_value<kFamily>(make_float2(v[j], v[j + 1]), p.act);
+                v[j] = y.x;
+                v[j + 1] = y.y;
+            }
+        }
+        if (p.has_residual) {
+            if (!kSwap && in_pieces(p.residual, q)) {
+                across_to_own(q, pre.residual);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 f = pair_at(pre.residual, i, __nv_bfloat16());
+                    v[2 * i] += f.x;
+                    v[2 * i + 1] += f.y;
+                }
+            } else {
+                float r[32];
+                kSwap ? get_columns(p.residual, q, r) : get_rows(p.residual, q, r);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += r[j];
+            }
+        }
+        kSwap ? put_columns(p.y, q, v) : put_rows(p.y, q, v);
     }
 };
 
 // out = acc, or out += acc.
+template <bool kSwap>
 struct EpiStore {
-    static constexpr bool kSym = false, kRows = true;
+    static constexpr bool kSym = false;
     struct Params {
         View out;
         int add;
     };
-    struct Col {};
-    struct Aux {
-        float4 old;
-    };
-    __device__ static void regs(const Params&, const Shape&, int, int, int, float (&)[32], bool) {}
-    __device__ static Col cols(const Params&, const Shape&, int, int, int) { return {}; }
-    __device__ static Aux load(const Params& p, const Shape&, int, int row, int col, int n) {
-        Aux a = {make_float4(0.f, 0.f, 0.f, 0.f)};
-        if (p.add) a.old = gemm::view_load(p.out, 0, row, col, n);
-        return a;
+    struct Pre {};
+    __device__ static void prefetch(const Params&, const Place&, Pre&) {}
+    __device__ static void apply(const Params& p, const Place& q, Pre&, float (&v)[32]) {
+        if (p.add) {
+            float old[32];
+            kSwap ? get_columns(p.out, q, old) : get_rows(p.out, q, old);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += old[j];
+        }
+        finish(p, q, v);
     }
-    __device__ static void store(const Params& p, const Shape&, int, int row, int col, int n,
-                                 float4 v, const Aux& a, const Col&) {
-        v.x += a.old.x;
-        v.y += a.old.y;
-        v.z += a.old.z;
-        v.w += a.old.w;
-        gemm::view_store(p.out, 0, row, col, n, v);
+    __device__ static void start(const Params& p, const Place& q, float (&v)[32]) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        if (p.add && gemm::inside<EpiStore>(q)) get_rows(p.out, q, v);
+    }
+    __device__ static void finish(const Params& p, const Place& q, const float (&v)[32]) {
+        kSwap ? put_columns(p.out, q, v) : put_rows(p.out, q, v);
     }
 };
 
-template <class Epi>
-cudaError_t product(const Operand& a, const Operand& b, int M, int N, int K,
-                    const typename Epi::Params& ep, cudaStream_t st) {
-    return gemm::launch_tile<1, 128, Epi>(a, b, M, N, K, 1, ep, st);
+// Up to this many rows of x the product is computed transposed: 128 rows of
+// the weight per tile and the rows of x across it, for a product that is
+// bound by reading the weight.
+constexpr int kSwapRows = 64;
+
+template <int kFamily, bool kSwap>
+cudaError_t forward(const Operand& x, const Operand& w, int M, int N, int K, const void* bias,
+                    const vc_matrix_t* residual, const vc_matrix_t* y, const vc_matrix_t* preact,
+                    vc_act_t act, cudaStream_t st) {
+    typename EpiForward<kFamily, kSwap>::Params ep = {};
+    ep.bias = static_cast<const __nv_bfloat16*>(bias);
+    ep.bias_vec = (reinterpret_cast<uintptr_t>(bias) & 15) == 0;
+    ep.residual = view_of(residual);
+    ep.y = view_of(y);
+    ep.preact = view_of(preact);
+    ep.has_residual = residual != nullptr;
+    ep.has_preact = preact != nullptr;
+    ep.act = act_params(act);
+    if constexpr (kSwap)
+        return gemm::launch_skinny<EpiForward<kFamily, true>>(Product{w, x, N, M, K, 1}, ep, st);
+    else
+        return gemm::launch<EpiForward<kFamily, false>>(Product{x, w, M, N, K, 1}, ep, st);
+}
+
+template <int kFamily>
+cudaError_t forward(const Operand& x, const Operand& w, int M, int N, int K, const void* bias,
+                    const vc_matrix_t* residual, const vc_matrix_t* y, const vc_matrix_t* preact,
+                    vc_act_t act, cudaStream_t st) {
+    return M <= kSwapRows
+               ? forward<kFamily, true>(x, w, M, N, K, bias, residual, y, preact, act, st)
+               : forward<kFamily, false>(x, w, M, N, K, bias, residual, y, preact, act, st);
 }
 
 // ------------------------------------------------------------ copy, dz, db --
 
-// A bf16 matrix copied to rows of ld_out values (a multiple of 8), so that
+// A bf16 matrix copied to rows of ld_out values (a multiple of 16), so that
 // TMA can read it.  One warp per row step; element-wise reads.
 __global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* src, long long ld,
                                                    __nv_bfloat16* dst, long long ld_out,
@@ -117,11 +186,13 @@ struct DzParams {
     long long ld_dz;
     float* sums;  // [gridDim.y][N], or NULL
     long long rows, cols;
-    int act;
+    int has_act;
+    Act act;
 };
 
 // dz = dy * act'(z) and the column sums of each block's rows.  A warp covers
 // 128 columns of a row; the block's eight warps take its rows in turn.
+template <int kFamily>
 __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzParams p) {
     __shared__ float4 part[8][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -134,12 +205,11 @@ __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzParam
         for (long long row = (long long)blockIdx.y * 8 + warp; row < p.rows;
              row += (long long)gridDim.y * 8) {
             float4 v = gemm::view_load(p.dy, 0, row, (int)col, n);
-            if (p.act != VC_ACT_NONE) {
+            if (p.has_act) {
                 const float4 z = gemm::view_load(p.preact, 0, row, (int)col, n);
-                v.x *= act_slope(z.x, p.act);
-                if (n > 1) v.y *= act_slope(z.y, p.act);
-                if (n > 2) v.z *= act_slope(z.z, p.act);
-                if (n > 3) v.w *= act_slope(z.w, p.act);
+                const float2 lo = act_slope<kFamily>(make_float2(z.x, z.y), p.act);
+                const float2 hi = act_slope<kFamily>(make_float2(z.z, z.w), p.act);
+                v = make_float4(v.x * lo.x, v.y * lo.y, v.z * hi.x, v.w * hi.y);
             }
             if (p.dz != nullptr) gemm::store4(p.dz + row * p.ld_dz + col, v, n, true);
             sum.x += v.x;
@@ -186,6 +256,9 @@ int dz_row_blocks(long long rows, long long cols) {
     const long long want = (152 * 8 + across - 1) / across;
     return (int)std::max(1ll, std::min(want, (rows + 31) / 32));
 }
+
+// K blocks (of 64) summed in tensor memory at a time for 32-bit gradients.
+constexpr int kSegment = 16;
 
 // ----------------------------------------------------------- the operands --
 
@@ -284,16 +357,18 @@ vc_status_t vc_linear_forward(const vc_matrix_t* x, const vc_matrix_t* weight, c
     if (ready_operand(x, &ws, st, &a.data, &a.ld) != cudaSuccess ||
         ready_operand(weight, &ws, st, &b.data, &b.ld) != cudaSuccess)
         return VC_ERR_CUDA;
-    EpiForward::Params ep = {};
-    ep.bias = static_cast<const __nv_bfloat16*>(bias);
-    ep.bias_vec = (reinterpret_cast<uintptr_t>(bias) & 7) == 0;
-    ep.residual = view_of(residual);
-    ep.y = view_of(y);
-    ep.preact = view_of(preact);
-    ep.has_residual = residual != nullptr;
-    ep.has_preact = preact != nullptr;
-    ep.act = act;
-    const cudaError_t e = product<EpiForward>(a, b, (int)M, (int)N, (int)K, ep, st);
+    cudaError_t e;
+    switch (act_family(act)) {
+    case kFamilyErf:
+        e = forward<kFamilyErf>(a, b, (int)M, (int)N, (int)K, bias, residual, y, preact, act, st);
+        break;
+    case kFamilyLogistic:
+        e = forward<kFamilyLogistic>(a, b, (int)M, (int)N, (int)K, bias, residual, y, preact, act, st);
+        break;
+    default:
+        e = forward<kFamilyPiecewise>(a, b, (int)M, (int)N, (int)K, bias, residual, y, preact, act,
+                                      st);
+    }
     return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
 }
 
@@ -364,8 +439,12 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
         p.sums = sums;
         p.rows = M;
         p.cols = N;
-        p.act = act;
-        e = launch_pdl(dz_kernel, dim3((unsigned)((N + 127) / 128), parts), dim3(256), st, p);
+        p.has_act = has_act;
+        p.act = act_params(act);
+        auto* kernel = act_family(act) == kFamilyErf        ? dz_kernel<kFamilyErf>
+                       : act_family(act) == kFamilyLogistic ? dz_kernel<kFamilyLogistic>
+                                                            : dz_kernel<kFamilyPiecewise>;
+        e = launch_pdl(kernel, dim3((unsigned)((N + 127) / 128), parts), dim3(256), st, p);
         if (e != cudaSuccess) return VC_ERR_CUDA;
         if (sums != nullptr) {
             e = launch_pdl(db_kernel, dim3((unsigned)((N + 255) / 256)), dim3(256), st,
@@ -374,18 +453,41 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
             if (e != cudaSuccess) return VC_ERR_CUDA;
         }
     }
+    Product p[2];
+    EpiStore<false>::Params ep[2];
+    int count = 0;
     if (dx != nullptr && M > 0 && K > 0) {
         Operand a = {dz, N, M, ld_dz, 0, true, false}, b = {nullptr, K, N, 0, 0, true, true};
         if (ready_operand(weight, &ws, st, &b.data, &b.ld) != cudaSuccess) return VC_ERR_CUDA;
-        EpiStore::Params ep = {view_of(dx), 0};
-        e = product<EpiStore>(a, b, (int)M, (int)K, (int)N, ep, st);
-        if (e != cudaSuccess) return VC_ERR_CUDA;
+        p[count] = {a, b, (int)M, (int)K, (int)N, 1};
+        ep[count++] = {view_of(dx), 0};
     }
     if (dweight != nullptr && N > 0 && K > 0) {
         Operand a = {dz, N, M, ld_dz, 0, true, true}, b = {nullptr, K, M, 0, 0, true, true};
         if (ready_operand(x, &ws, st, &b.data, &b.ld) != cudaSuccess) return VC_ERR_CUDA;
-        EpiStore::Params ep = {view_of(dweight), accumulate != 0};
-        e = product<EpiStore>(a, b, (int)N, (int)K, (int)M, ep, st);
+        p[count] = {a, b, (int)N, (int)K, (int)M, 1};
+        ep[count++] = {view_of(dweight), accumulate != 0};
+    }
+    if (count > 0) {
+        // 32-bit sums are not left to the tensor cores for longer than a segment
+        const bool promote = dweight != nullptr && dweight->dtype == VC_FLOAT32;
+        gemm::Plan plan[2];
+        double apart = 0.0;
+        for (int i = 0; i < count; ++i) {
+            const bool sums = promote && ep[i].out.f32;
+            plan[i] = gemm::plan_split(p[i], false, sums ? kSegment : 0);
+            apart += plan[i].us;
+        }
+        if (apart < gemm::pair_us(p, count, false)) {
+            for (int i = 0; i < count && e == cudaSuccess; ++i)
+                e = gemm::launch_split<64, EpiStore<false>>(p[i], ep[i], plan[i].ranks, st);
+        } else if (count == 2) {
+            e = promote ? gemm::launch_pair<EpiStore<false>, 2, true>(p, ep, kSegment, st)
+                        : gemm::launch_pair<EpiStore<false>, 2, false>(p, ep, 0, st);
+        } else {
+            e = promote ? gemm::launch_pair<EpiStore<false>, 1, true>(p, ep, kSegment, st)
+                        : gemm::launch_pair<EpiStore<false>, 1, false>(p, ep, 0, st);
+        }
         if (e != cudaSuccess) return VC_ERR_CUDA;
     }
     return VC_SUCCESS;

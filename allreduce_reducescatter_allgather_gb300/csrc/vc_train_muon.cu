@@ -31,6 +31,7 @@ namespace train {
 namespace {
 
 using gemm::Operand;
+using gemm::Product;
 using gemm::Shape;
 using gemm::View;
 
@@ -131,45 +132,62 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Prep
 
 // ------------------------------------------------------------- epilogues --
 
+using gemm::Place;
+
+// Matrices in the workspace have rows of whole chunks (layout_of), so that
+// chunks are accessed in 16-byte pieces whatever the matrix's size;
+// what lies beyond the matrix is written with zeros and read by nobody.
+
+// The mirrored chunk of a symmetric matrix, along its rows.
+__device__ __forceinline__ void put_mirror(__half* o, long long ld, const Place& q,
+                                           const float (&v)[32]) {
+    if (!q.off || q.row() >= q.M) return;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (q.col0 + j < q.N) o[(long long)(q.col0 + j) * ld + q.row()] = __float2half_rn(v[j]);
+}
+
+// The diagonal's value of this lane's row, if the chunk holds it (else 0); and
+// sets it to zero in the chunk.
+__device__ __forceinline__ float take_diagonal(const Place& q, float (&v)[32]) {
+    float d = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if (q.row() == q.col0 + j) {
+            d = v[j];
+            v[j] = 0.0f;
+        }
+    }
+    return d;
+}
+
 // A = X X^T: the diagonal to 32 bits, the rest to fp16 on both sides.
 struct EpiGram {
-    static constexpr bool kSym = true, kRows = true;
+    static constexpr bool kSym = true;
     struct Params {
         __half* o;
         float* d;
         long long ld, batch_stride;
         float scale;
     };
-    struct Col {};
-    struct Aux {};
-    __device__ static void regs(const Params& p, const Shape& s, int b, int row, int col0,
-                                float (&v)[32], bool off) {
-        __half* const o = p.o + (long long)b * p.batch_stride;
+    struct Pre {};
+    __device__ static void prefetch(const Params&, const Place&, Pre&) {}
+    __device__ static void apply(const Params& p, const Place& q, Pre&, float (&v)[32]) {
+        __half* const o = p.o + (long long)q.b * p.batch_stride;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            v[j] *= p.scale;
-            if (!off && row == col0 + j && row < s.M) {
-                p.d[(long long)b * s.M + row] = v[j];
-                v[j] = 0.0f;
-            }
+        for (int j = 0; j < 32; ++j) v[j] *= p.scale;
+        if (q.row0 == q.col0) {
+            const float d = take_diagonal(q, v);
+            if (q.row() < q.M) p.d[(long long)q.b * q.M + q.row()] = d;
         }
-        if (off && row < s.M) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (col0 + j < s.N) o[(col0 + j) * p.ld + row] = __float2half_rn(v[j]);
-        }
-    }
-    __device__ static Col cols(const Params&, const Shape&, int, int, int) { return {}; }
-    __device__ static Aux load(const Params&, const Shape&, int, int, int, int) { return {}; }
-    __device__ static void store(const Params& p, const Shape&, int b, int row, int col, int n,
-                                 float4 v, const Aux&, const Col&) {
-        gemm::store4(p.o + (long long)b * p.batch_stride + (long long)row * p.ld + col, v, n, true);
+        store_chunk(o + (long long)q.row0 * p.ld + q.col0, p.ld, q, v);
+        put_mirror(o, p.ld, q, v);
     }
 };
 
 // B = b A + c A^2 from the product O O of A's off-diagonal part.
 struct EpiPoly {
-    static constexpr bool kSym = true, kRows = true;
+    static constexpr bool kSym = true;
     struct Params {
         const __half* o;
         const float* d;
@@ -178,146 +196,119 @@ struct EpiPoly {
         long long ld, batch_stride;
         float cb, cc;
     };
-    struct Col {};
-    struct Aux {};
-    __device__ static void regs(const Params& p, const Shape& s, int b, int row, int col0,
-                                float (&v)[32], bool off) {
-        const __half* const o = p.o + (long long)b * p.batch_stride;
-        __half* const ob = p.ob + (long long)b * p.batch_stride;
-        const float* const d = p.d + (long long)b * s.M;
-        if (row < s.M) {
-            const float di = d[row];
-            float a[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j)  // the same value as o[row][col0 + j], read along rows
-                a[j] = col0 + j < s.N ? __half2float(o[(col0 + j) * p.ld + row]) : 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float dj = col0 + j < s.N ? d[col0 + j] : 0.0f;
-                if (!off && row == col0 + j) {
-                    p.db[(long long)b * s.M + row] = p.cb * di + p.cc * (di * di + v[j]);
-                    v[j] = 0.0f;
-                } else {
-                    v[j] = (p.cb + p.cc * (di + dj)) * a[j] + p.cc * v[j];
-                }
-            }
-            if (off) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (col0 + j < s.N) ob[(col0 + j) * p.ld + row] = __float2half_rn(v[j]);
-            }
-        }
+    struct Pre {
+        gemm::Chunk16 o;
+        float row, col;  // A's diagonal at the lane's row and at its column
+    };
+    __device__ static void prefetch(const Params& p, const Place& q, Pre& pre) {
+        const float* const d = p.d + (long long)q.b * q.M;
+        pre.col = q.col0 + q.lane < q.N ? d[q.col0 + q.lane] : 0.0f;
+        pre.row = q.row() < q.M ? d[q.row()] : 0.0f;
+        load_across(p.o + (long long)q.b * p.batch_stride + (long long)q.row0 * p.ld + q.col0, p.ld * 2,
+                    q, pre.o);
     }
-    __device__ static Col cols(const Params&, const Shape&, int, int, int) { return {}; }
-    __device__ static Aux load(const Params&, const Shape&, int, int, int, int) { return {}; }
-    __device__ static void store(const Params& p, const Shape&, int b, int row, int col, int n,
-                                 float4 v, const Aux&, const Col&) {
-        gemm::store4(p.ob + (long long)b * p.batch_stride + (long long)row * p.ld + col, v, n, true);
+    __device__ static void apply(const Params& p, const Place& q, Pre& pre, float (&v)[32]) {
+        __half* const ob = p.ob + (long long)q.b * p.batch_stride;
+        if (q.row0 == q.col0) {
+            const float d = take_diagonal(q, v);  // (O O)_ii
+            if (q.row() < q.M)
+                p.db[(long long)q.b * q.M + q.row()] = p.cb * pre.row + p.cc * (pre.row * pre.row + d);
+        }
+        across_to_own(q, pre.o);
+        const float k = fmaf(p.cc, pre.row, p.cb);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 a = pair_at(pre.o, i, __half());  // (0 on the diagonal)
+            const float k0 = fmaf(p.cc, __shfl_sync(0xFFFFFFFFu, pre.col, 2 * i), k);
+            const float k1 = fmaf(p.cc, __shfl_sync(0xFFFFFFFFu, pre.col, 2 * i + 1), k);
+            v[2 * i] = fmaf(k0, a.x, p.cc * v[2 * i]);
+            v[2 * i + 1] = fmaf(k1, a.y, p.cc * v[2 * i + 1]);
+        }
+        store_chunk(ob + (long long)q.row0 * p.ld + q.col0, p.ld, q, v);
+        put_mirror(ob, p.ld, q, v);
     }
 };
 
 // X <- (a + diag B) X + offdiag(B) X, and on the last pass the operator's
 // output instead of X.
-struct UpdateCommon {
+struct UpdateParams {
     const __half* hi;
     __half* lo;
     __half* hi_out;
-    const float* db;  // of B, [batch][r]
+    const float* db;  // diagonal of B, [batch][r]
     long long ld, batch_stride;
     float a;
     int tall;  // B stands on the right: its diagonal goes with the columns
     int r;
 };
-struct UpdateAux {
-    float4 x;
-    float row;
+struct UpdatePre {
+    gemm::Chunk16 hi, lo;
+    float k;  // a + B's diagonal at the lane's row, or at its column (tall)
 };
-struct UpdateCol {
-    float4 k;
-};
-__device__ __forceinline__ UpdateCol update_cols(const UpdateCommon& p, int b, int col, int n) {
-    UpdateCol c = {make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (p.tall) c.k = gemm::load4(p.db + (long long)b * p.r + col, n, false);
-    return c;
+__device__ __forceinline__ void update_prefetch(const UpdateParams& p, const Place& q, UpdatePre& pre) {
+    const int at = p.tall ? q.col0 + q.lane : q.row();
+    pre.k = at < p.r ? p.a + p.db[(long long)q.b * p.r + at] : 0.0f;
+    const long long x = (long long)q.b * p.batch_stride + (long long)q.row0 * p.ld + q.col0;
+    load_across(p.hi + x, p.ld * 2, q, pre.hi);
+    load_across(p.lo + x, p.ld * 2, q, pre.lo);
 }
-__device__ __forceinline__ UpdateAux update_load(const UpdateCommon& p, int b, int row, int col,
-                                                 int n) {
-    const long long at = (long long)b * p.batch_stride + (long long)row * p.ld + col;
-    const float4 h = gemm::load4(p.hi + at, n, true), l = gemm::load4(p.lo + at, n, true);
-    UpdateAux a;
-    a.x = make_float4(h.x + l.x, h.y + l.y, h.z + l.z, h.w + l.w);
-    a.row = p.a + (p.tall ? 0.0f : p.db[(long long)b * p.r + row]);
-    return a;
-}
-__device__ __forceinline__ float4 update_value(float4 v, const UpdateAux& a, const UpdateCol& c) {
-    return make_float4(fmaf(a.row + c.k.x, a.x.x, v.x), fmaf(a.row + c.k.y, a.x.y, v.y),
-                       fmaf(a.row + c.k.z, a.x.z, v.z), fmaf(a.row + c.k.w, a.x.w, v.w));
+__device__ __forceinline__ void update_apply(const UpdateParams& p, const Place& q, UpdatePre& pre,
+                                             float (&v)[32]) {
+    across_to_own(q, pre.hi);
+    across_to_own(q, pre.lo);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 h = pair_at(pre.hi, i, __half()), l = pair_at(pre.lo, i, __half());
+        const float k0 = __shfl_sync(0xFFFFFFFFu, pre.k, 2 * i);
+        const float k1 = __shfl_sync(0xFFFFFFFFu, pre.k, 2 * i + 1);
+        v[2 * i] = fmaf(p.tall ? k0 : pre.k, h.x + l.x, v[2 * i]);
+        v[2 * i + 1] = fmaf(p.tall ? k1 : pre.k, h.y + l.y, v[2 * i + 1]);
+    }
 }
 
 struct EpiUpdate {
-    static constexpr bool kSym = false, kRows = true;
-    using Params = UpdateCommon;
-    using Col = UpdateCol;
-    using Aux = UpdateAux;
-    __device__ static void regs(const Params&, const Shape&, int, int, int, float (&)[32], bool) {}
-    __device__ static Col cols(const Params& p, const Shape&, int b, int col, int n) {
-        return update_cols(p, b, col, n);
+    static constexpr bool kSym = false;
+    using Params = UpdateParams;
+    using Pre = UpdatePre;
+    __device__ static void prefetch(const Params& p, const Place& q, Pre& pre) {
+        update_prefetch(p, q, pre);
     }
-    __device__ static Aux load(const Params& p, const Shape&, int b, int row, int col, int n) {
-        return update_load(p, b, row, col, n);
-    }
-    __device__ static void store(const Params& p, const Shape&, int b, int row, int col, int n,
-                                 float4 v, const Aux& a, const Col& c) {
-        const float4 y = update_value(v, a, c);
-        const long long at = (long long)b * p.batch_stride + (long long)row * p.ld + col;
-        const float4 h = make_float4(__half2float(__float2half_rn(y.x)), __half2float(__float2half_rn(y.y)),
-                                     __half2float(__float2half_rn(y.z)), __half2float(__float2half_rn(y.w)));
-        gemm::store4(p.hi_out + at, h, n, true);
-        gemm::store4(p.lo + at, make_float4(y.x - h.x, y.y - h.y, y.z - h.z, y.w - h.w), n, true);
+    __device__ static void apply(const Params& p, const Place& q, Pre& pre, float (&v)[32]) {
+        update_apply(p, q, pre, v);
+        const long long at = (long long)q.b * p.batch_stride + (long long)q.row0 * p.ld + q.col0;
+        store_chunk(p.hi_out + at, p.ld, q, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
+        store_chunk(p.lo + at, p.ld, q, v);
     }
 };
 
 struct EpiFinal {
-    static constexpr bool kSym = false, kRows = true;
+    static constexpr bool kSym = false;
     struct Params {
-        UpdateCommon u;
+        UpdateParams u;
         View out;     // the output, or the weights
         int weights;  // out <- keep out + scale y, else out <- scale y
         float keep, scale;
     };
-    using Col = UpdateCol;
-    struct Aux {
-        UpdateAux u;
-        float4 w;
-    };
-    __device__ static void regs(const Params&, const Shape&, int, int, int, float (&)[32], bool) {}
-    __device__ static Col cols(const Params& p, const Shape&, int b, int col, int n) {
-        return update_cols(p.u, b, col, n);
+    using Pre = UpdatePre;
+    __device__ static void prefetch(const Params& p, const Place& q, Pre& pre) {
+        update_prefetch(p.u, q, pre);
     }
-    __device__ static Aux load(const Params& p, const Shape&, int b, int row, int col, int n) {
-        Aux a;
-        a.u = update_load(p.u, b, row, col, n);
-        a.w = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.weights) a.w = gemm::view_load(p.out, b, row, col, n);
-        return a;
-    }
-    __device__ static void store(const Params& p, const Shape&, int b, int row, int col, int n,
-                                 float4 v, const Aux& a, const Col& c) {
-        float4 y = update_value(v, a.u, c);
-        if (p.weights)
-            y = make_float4(fmaf(p.keep, a.w.x, p.scale * y.x), fmaf(p.keep, a.w.y, p.scale * y.y),
-                            fmaf(p.keep, a.w.z, p.scale * y.z), fmaf(p.keep, a.w.w, p.scale * y.w));
-        else
-            y = make_float4(p.scale * y.x, p.scale * y.y, p.scale * y.z, p.scale * y.w);
-        gemm::view_store(p.out, b, row, col, n, y);
+    __device__ static void apply(const Params& p, const Place& q, Pre& pre, float (&v)[32]) {
+        update_apply(p.u, q, pre, v);
+        if (p.weights) {
+            float w[32];
+            get_rows(p.out, q, w);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(p.keep, w[j], p.scale * v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= p.scale;
+        }
+        put_rows(p.out, q, v);
     }
 };
-
-template <class Epi>
-cudaError_t product(const Operand& a, const Operand& b, int M, int N, int K, int batch,
-                    const typename Epi::Params& ep, cudaStream_t st) {
-    return gemm::launch_tile<1, 128, Epi>(a, b, M, N, K, batch, ep, st);
-}
 
 // -------------------------------------------------------------- host side --
 
@@ -336,8 +327,8 @@ bool layout_of(long long batch, long long rows, long long cols, Layout* l) {
     if (rows * vpr > 0x7FFFFFFFll || batch * rows > 0x3FFFFFFFll) return false;
     l->r = std::min(rows, cols);
     l->c = std::max(rows, cols);
-    l->ldx = padded_ld(cols);
-    l->ldr = padded_ld(l->r);
+    l->ldx = (cols + 31) / 32 * 32;  // whole chunks of the epilogues
+    l->ldr = (l->r + 31) / 32 * 32;
     l->xs = rows * l->ldx;
     l->as = l->r * l->ldr;
     const long long want = (rows * vpr + 1023) / 1024, fit = std::max(1ll, 152 * 8 / std::max(1ll, batch));
@@ -394,21 +385,21 @@ cudaError_t iterate(const Layout& l, long long batch, long long rows, long long 
         xm.mn_major = true;
         EpiGram::Params gp = {oa, da, l.ldr, l.as, 1.0f / (size * size)};
         const Operand& side = tall ? xm : xk;
-        e = product<EpiGram>(side, side, r, r, c, nb, gp, st);
+        e = gemm::launch<EpiGram>(Product{side, side, r, r, c, nb}, gp, st);
         if (e != cudaSuccess) break;
         const Operand ao = {oa, r, r, l.ldr, l.as, false, false};
         EpiPoly::Params pp = {oa, da, ob, db, l.ldr, l.as, ns.b, ns.c};
-        e = product<EpiPoly>(ao, ao, r, r, r, nb, pp, st);
+        e = gemm::launch<EpiPoly>(Product{ao, ao, r, r, r, nb}, pp, st);
         if (e != cudaSuccess) break;
         const Operand bo = {ob, r, r, l.ldr, l.as, false, false};
-        const UpdateCommon u = {x[0], lo, x[1], db, l.ldx, l.xs, ns.a, tall, r};
+        const UpdateParams u = {x[0], lo, x[1], db, l.ldx, l.xs, ns.a, tall, r};
         const Operand &left = tall ? xk : bo, &right = tall ? bo : xm;
         if (i + 1 < ns.steps) {
-            e = product<EpiUpdate>(left, right, (int)rows, (int)cols, r, nb, u, st);
+            e = gemm::launch<EpiUpdate>(Product{left, right, (int)rows, (int)cols, r, nb}, u, st);
         } else {
             fin.u = u;
             fin.scale /= size;
-            e = product<EpiFinal>(left, right, (int)rows, (int)cols, r, nb, fin, st);
+            e = gemm::launch<EpiFinal>(Product{left, right, (int)rows, (int)cols, r, nb}, fin, st);
         }
         std::swap(x[0], x[1]);
     }

@@ -21,7 +21,7 @@ from __future__ import annotations
 import ctypes
 import math
 
-from ._binding import (_OnDevice, _stream, _torch, check_status, lib)
+from ._binding import _OnDevice, _torch, check_status, lib
 
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
 # Quintic whose repeated application takes singular values in (0, 1] to about 1.
@@ -188,10 +188,19 @@ class PreparedOperator:
 
     def __init__(self, fn, args, device, keep):
         self._fn, self._args, self._device, self._keep = fn, args, device, keep
+        self._index = device.index if device.index is not None else _torch().cuda.current_device()
 
     def __call__(self, stream=None):
-        with _OnDevice(self._device):
-            check_status(self._fn(*self._args, _stream(stream, self._device)))
+        cuda = _torch().cuda
+        # (short calls are bound by the host: the common case makes no objects)
+        raw = cuda.current_stream(self._index).cuda_stream if stream is None else stream.cuda_stream
+        if cuda.current_device() == self._index:
+            status = self._fn(*self._args, raw)
+        else:
+            with _OnDevice(self._device):
+                status = self._fn(*self._args, raw)
+        if status != 0:
+            check_status(status)
 
 
 # ------------------------------------------------------------- linear layer --
