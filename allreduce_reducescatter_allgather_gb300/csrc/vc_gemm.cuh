@@ -39,13 +39,8 @@ namespace gemm {
 
 constexpr int kBlockK = 64;            // 64 16-bit values: one 128-byte swizzle row
 constexpr int kRowsPerCta = 128;       // tensor-memory lanes
-constexpr int kChunkRow = 36;          // floats per row of an epilogue chunk (32 + 4: no bank
-                                       // conflicts in either direction)
 constexpr int kWarpStage = 2048;       // bytes of shared memory of an epilogue warp
 constexpr int kGroup = 8;              // tile rows walked together, for reuse in L2
-constexpr int kChunkRows = 8;          // rows of a chunk at a time
-constexpr int kEpilogueWarps = 8;
-constexpr int kPairThreads = 32 * (2 + kEpilogueWarps);
 constexpr int kSmemPerBlock = 232448;  // 227 KB
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 
@@ -54,7 +49,8 @@ struct Shape {
     int tiles_m, tiles_n;   // tiles of one product
     int tiles;              // tiles of one product that are computed
     int total;              // tiles of all products of the batch
-    int kblocks;            // ceil(K / 64)
+    int kblocks;            // K blocks summed: per_plane, for each plane of A
+    int per_plane;          // ceil(K / 64)
     int segment;            // K blocks summed in tensor memory at a time
     int a_mn, b_mn;         // operand is MN-major
     unsigned idesc;         // instruction descriptor
@@ -488,14 +484,19 @@ __device__ __forceinline__ unsigned packed(float a, float b, __half) {
     return *reinterpret_cast<const unsigned*>(&h);
 }
 template <class T>
-__device__ __forceinline__ void store_chunk(T* corner, long long ld, const Place& q,
-                                            const float (&v)[32]) {
+__device__ __forceinline__ Chunk16 packed_row(const float (&v)[32], T) {
     Chunk16 x;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         x.u[i] = make_uint4(packed(v[8 * i], v[8 * i + 1], T()), packed(v[8 * i + 2], v[8 * i + 3], T()),
                             packed(v[8 * i + 4], v[8 * i + 5], T()),
                             packed(v[8 * i + 6], v[8 * i + 7], T()));
+    return x;
+}
+template <class T>
+__device__ __forceinline__ void store_chunk(T* corner, long long ld, const Place& q,
+                                            const float (&v)[32]) {
+    Chunk16 x = packed_row(v, T());
     own_to_across(q, x);
     store_across(corner, ld * (long long)sizeof(T), q, x);
 }
@@ -508,96 +509,116 @@ __device__ __forceinline__ long long corner_of(const View& v, const Place& q) {
     return (long long)q.b * v.batch_stride + (long long)q.row0 * v.ld + q.col0;
 }
 
-// The chunk of a matrix, one row per lane: v[j] = X[row0 + lane][col0 + j].
-// All lanes call it.  Chunks that 16-byte pieces do not cover (odd row lengths,
-// the last columns) go through shared memory as floats, eight rows at a time.
-__device__ __forceinline__ void get_rows(const View& x, const Place& q, float (&v)[32]) {
-    if (in_pieces(x, q)) {
-        Chunk16 c;
-        if (x.f32) {
+// Chunks that 16-byte pieces do not cover (odd row lengths, the last columns)
+// take the same way through shared memory, but value by value on global
+// memory's side: 32 16-bit values of a row, or 16 floats of two rows, per
+// instruction.
+template <class T>
+__device__ __forceinline__ void load_values(const T* corner, long long ld, const Place& q, int cols,
+                                            Chunk16& x) {
+    constexpr int kAcross = 64 / sizeof(T), kRows = 32 / kAcross;
+    const int c = q.lane % kAcross, r0 = q.lane / kAcross;
+    const T* at = corner + r0 * ld + c;
+    __syncwarp();
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32 / kRows; i0 += 8) {
+        T v[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                load_across(static_cast<const float*>(x.data) + corner_of(x, q) + 16 * h, x.ld * 4, q, c);
-                across_to_own(q, c);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[16 * h + i] = __uint_as_float(word_of(c, i));
-            }
-        } else {
-            load_across(static_cast<const __nv_bfloat16*>(x.data) + corner_of(x, q), x.ld * 2, q, c);
-            across_to_own(q, c);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 f = pair_at(c, i, __nv_bfloat16());
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int r = (i0 + i) * kRows + r0;
+            if (c < cols && q.row0 + r < q.M) v[i] = at[(long long)(i0 + i) * kRows * ld];
         }
-        return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            reinterpret_cast<T*>(piece_of(q.stage, (i0 + i) * kRows + r0, c * (int)sizeof(T) / 16))
+                [c % (16 / sizeof(T))] = v[i];
     }
-    float* const chunk = reinterpret_cast<float*>(q.stage);
-    const int lr = q.lane >> 3, lc = (q.lane & 7) * 4, n = min(4, q.N - q.col0 - lc);
+    __syncwarp();
 #pragma unroll
-    for (int h = 0; h < 32 / kChunkRows; ++h) {
-        __syncwarp();
+    for (int i = 0; i < 4; ++i) x.u[i] = *piece_of(q.stage, q.lane, i);
+}
+template <class T>
+__device__ __forceinline__ void store_values(T* corner, long long ld, const Place& q, int cols,
+                                             const Chunk16& x) {
+    constexpr int kAcross = 64 / sizeof(T), kRows = 32 / kAcross;
+    const int c = q.lane % kAcross, r0 = q.lane / kAcross;
+    __syncwarp();
 #pragma unroll
-        for (int u = 0; u < kChunkRows / 4; ++u) {
-            const int r = 4 * u + lr, row = q.row0 + h * kChunkRows + r;
-            if (n > 0 && row < q.M)
-                *reinterpret_cast<float4*>(chunk + r * kChunkRow + lc) =
-                    view_load(x, q.b, row, q.col0 + lc, n);
+    for (int i = 0; i < 4; ++i) *piece_of(q.stage, q.lane, i) = x.u[i];
+    __syncwarp();
+    T* at = corner + r0 * ld + c;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32 / kRows; i0 += 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = (i0 + i) * kRows + r0;
+            const T v = reinterpret_cast<const T*>(
+                piece_of(q.stage, r, c * (int)sizeof(T) / 16))[c % (16 / sizeof(T))];
+            if (c < cols && q.row0 + r < q.M) at[(long long)(i0 + i) * kRows * ld] = v;
         }
-        __syncwarp();
-        if (q.lane / kChunkRows == h) {
+    }
+}
+
+// The chunk of a matrix, one row per lane: v[j] = X[row0 + lane][col0 + j].
+// All lanes call it.
+__device__ __forceinline__ void get_rows(const View& x, const Place& q, float (&v)[32]) {
+    Chunk16 c;
+    if (x.f32) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(
-                    chunk + (q.lane % kChunkRows) * kChunkRow + j);
-                v[j] = f.x;
-                v[j + 1] = f.y;
-                v[j + 2] = f.z;
-                v[j + 3] = f.w;
+        for (int h = 0; h < 2; ++h) {
+            const float* corner = static_cast<const float*>(x.data) + corner_of(x, q) + 16 * h;
+            if (in_pieces(x, q)) {
+                load_across(corner, x.ld * 4, q, c);
+                across_to_own(q, c);
+            } else {
+                load_values(corner, x.ld, q, q.N - q.col0 - 16 * h, c);
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[16 * h + i] = __uint_as_float(word_of(c, i));
+        }
+    } else {
+        const __nv_bfloat16* corner = static_cast<const __nv_bfloat16*>(x.data) + corner_of(x, q);
+        if (in_pieces(x, q)) {
+            load_across(corner, x.ld * 2, q, c);
+            across_to_own(q, c);
+        } else {
+            load_values(reinterpret_cast<const unsigned short*>(corner), x.ld, q, q.N - q.col0, c);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 f = pair_at(c, i, __nv_bfloat16());
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
         }
     }
 }
 
 __device__ __forceinline__ void put_rows(const View& x, const Place& q, const float (&v)[32]) {
-    if (in_pieces(x, q)) {
-        if (x.f32) {
+    Chunk16 c;
+    if (x.f32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                Chunk16 c;
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    c.u[i] = make_uint4(
-                        __float_as_uint(v[16 * h + 4 * i]), __float_as_uint(v[16 * h + 4 * i + 1]),
-                        __float_as_uint(v[16 * h + 4 * i + 2]), __float_as_uint(v[16 * h + 4 * i + 3]));
+            for (int i = 0; i < 4; ++i)
+                c.u[i] = make_uint4(
+                    __float_as_uint(v[16 * h + 4 * i]), __float_as_uint(v[16 * h + 4 * i + 1]),
+                    __float_as_uint(v[16 * h + 4 * i + 2]), __float_as_uint(v[16 * h + 4 * i + 3]));
+            float* corner = static_cast<float*>(x.data) + corner_of(x, q) + 16 * h;
+            if (in_pieces(x, q)) {
                 own_to_across(q, c);
-                store_across(static_cast<float*>(x.data) + corner_of(x, q) + 16 * h, x.ld * 4, q, c);
+                store_across(corner, x.ld * 4, q, c);
+            } else {
+                store_values(corner, x.ld, q, q.N - q.col0 - 16 * h, c);
             }
+        }
+    } else {
+        __nv_bfloat16* corner = static_cast<__nv_bfloat16*>(x.data) + corner_of(x, q);
+        c = packed_row(v, __nv_bfloat16());
+        if (in_pieces(x, q)) {
+            own_to_across(q, c);
+            store_across(corner, x.ld * 2, q, c);
         } else {
-            store_chunk(static_cast<__nv_bfloat16*>(x.data) + corner_of(x, q), x.ld, q, v);
-        }
-        return;
-    }
-    float* const chunk = reinterpret_cast<float*>(q.stage);
-    const int lr = q.lane >> 3, lc = (q.lane & 7) * 4, n = min(4, q.N - q.col0 - lc);
-#pragma unroll
-    for (int h = 0; h < 32 / kChunkRows; ++h) {
-        __syncwarp();
-        if (q.lane / kChunkRows == h) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<float4*>(chunk + (q.lane % kChunkRows) * kChunkRow + j) =
-                    make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int u = 0; u < kChunkRows / 4; ++u) {
-            const int r = 4 * u + lr, row = q.row0 + h * kChunkRows + r;
-            if (n > 0 && row < q.M)
-                view_store(x, q.b, row, q.col0 + lc, n,
-                           *reinterpret_cast<const float4*>(chunk + r * kChunkRow + lc));
+            store_values(reinterpret_cast<unsigned short*>(corner), x.ld, q, q.N - q.col0, c);
         }
     }
 }
@@ -634,6 +655,7 @@ __device__ __forceinline__ void put_columns(const View& x, const Place& q, const
 //   prefetch(p, q, pre)   starts these loads; called before the chunk's products are read
 //   apply(p, q, pre, v)   v[j] = D[row0 + lane][col0 + j]; all lanes call it
 // and, for sums that are promoted to registers,
+//   sums32(p)             whether the output is 32 bits wide
 //   start(p, q, sum)      the value that the sum begins with
 //   finish(p, q, sum)     stores it
 template <class Epi>
@@ -675,18 +697,21 @@ struct Ring {
     }
 };
 
-// One stage: 128 rows of A and kBRows of B, 64 values of K.
+// One stage: 128 rows of A and kBRows of B, K block kb of product b.  (Where A
+// is a sum of two planes, its blocks follow each other and B's are read again.)
 template <int kPair, int kBRows>
 __device__ __forceinline__ void load_stage(unsigned sa, const CUtensorMap* map_a,
                                            const CUtensorMap* map_b, const Shape& s, unsigned bar,
-                                           int m0, int n0, int k0, int b) {
+                                           int m0, int n0, int kb, int b) {
+    const int plane = kb >= s.per_plane;
+    const int k0 = (kb - (plane ? s.per_plane : 0)) * kBlockK;
     const unsigned sb = sa + kRowsPerCta * kBlockK * 2;
     if (s.a_mn) {
 #pragma unroll
         for (int i = 0; i < kRowsPerCta / 64; ++i)
-            tma_load<kPair>(sa + i * kBlockK * 128, map_a, bar, m0 + 64 * i, k0, b);
+            tma_load<kPair>(sa + i * kBlockK * 128, map_a, bar, m0 + 64 * i, k0, b + plane);
     } else {
-        tma_load<kPair>(sa, map_a, bar, k0, m0, b);
+        tma_load<kPair>(sa, map_a, bar, k0, m0, b + plane);
     }
     if (s.b_mn) {
 #pragma unroll
@@ -722,11 +747,15 @@ __device__ __forceinline__ void bury(volatile int* dead, unsigned* timeouts) {
 
 // ------------------------------------------------------------- pair kernel --
 
+template <bool kPromote>
 struct Pair {
     static constexpr int kBN = 256, kBM = 256;
+    // warps of the epilogue; sums in registers want more of them, with fewer columns each
+    static constexpr int kWarps = kPromote ? 16 : 8;
+    static constexpr int kThreads = 32 * (2 + kWarps);
     static constexpr int kBRows = kBN / 2;  // rows of B (columns of D) that a block loads
     static constexpr int kStageBytes = (kRowsPerCta + kBRows) * kBlockK * 2;
-    static constexpr int kChunkBytes = kEpilogueWarps * kWarpStage;
+    static constexpr int kChunkBytes = kWarps * kWarpStage;
     static constexpr int kBarBytes = 256;
     static constexpr int kStages = 6;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kChunkBytes + kBarBytes;
@@ -780,11 +809,11 @@ __device__ __forceinline__ bool work_item(const PairWork<Epi>& w, int slot, int 
 // cut accumulated sums off instead: measured 1e-6 relative, towards zero, for
 // sums of 1024 products, and growing with their number.)
 template <class Epi, int kCount, bool kPromote>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(Pair<kPromote>::kThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_b0,
             const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b1,
             const __grid_constant__ PairWork<Epi> w) {
-    using C = Pair;
+    using C = Pair<kPromote>;
     extern __shared__ unsigned char smem_raw[];
     const unsigned base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* const gen = smem_raw + (base - smem_u32(smem_raw));
@@ -807,7 +836,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull + 8 * i, 1);
-            mbar_init(tempty + 8 * i, 2 * kEpilogueWarps);
+            mbar_init(tempty + 8 * i, 2 * C::kWarps);
         }
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -844,8 +873,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ 
                     // both blocks' copies count on the leading block's barrier
                     if (leader) mbar_expect(full + 8 * ring.stage, 2 * C::kStageBytes);
                     load_stage<2, C::kBRows>(base + ring.stage * C::kStageBytes, ma, mb, s,
-                                             map_rank(full + 8 * ring.stage, 0), m0, n0,
-                                             kb * kBlockK, b);
+                                             map_rank(full + 8 * ring.stage, 0), m0, n0, kb, b);
                 }
                 __syncwarp();
                 ring.next();
@@ -891,9 +919,9 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ 
     } else {
         const int ew = warp - 2;
         const int quarter = warp & 3;  // the tensor-memory lanes this warp may read
-        const int half = ew >> 2;      // and its half of the columns
-        constexpr int kChunks = C::kBN / 64;
-        const unsigned lanes = tmem + ((unsigned)(quarter * 32) << 16) + half * (C::kBN / 2);
+        constexpr int kChunks = C::kBN / 32 / (C::kWarps / 4);
+        const int first_col = (ew >> 2) * kChunks * 32;  // its part of the columns
+        const unsigned lanes = tmem + ((unsigned)(quarter * 32) << 16) + first_col;
         const unsigned tempty_lead = map_rank(tempty, 0);
         Ring<2> acc;
         bool alive = true;
@@ -906,13 +934,16 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ 
             Place q;
             q.b = b;
             q.row0 = tm * C::kBM + (int)rank * kRowsPerCta + quarter * 32;
-            q.col0 = tn * C::kBN + half * (C::kBN / 2);
+            q.col0 = tn * C::kBN + first_col;
             q.M = s.M;
             q.N = s.N;
             q.lane = lane;
             q.off = tm != tn;
             q.stage = chunks + ew * kWarpStage;
+            bool summed = false;
             if constexpr (kPromote) {
+              if (s.segment < s.kblocks) {
+                summed = true;
                 float sum[kChunks][32];
                 Place at = q;
 #pragma unroll
@@ -927,10 +958,8 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ 
                     for (int c = 0; c < 2 * kChunks; ++c) {
                         float v[16];
                         tmem_load16(lanes + acc.stage * C::kBN + 16 * c, v);
-                        if (s.kblocks > 0) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) sum[c / 2][(c & 1) * 16 + j] += v[j];
-                        }
+                        for (int j = 0; j < 16; ++j) sum[c / 2][(c & 1) * 16 + j] += v[j];
                     }
                     tcgen05_fence_before();
                     __syncwarp();
@@ -942,7 +971,9 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ 
                 for (int c = 0; c < kChunks; ++c, q.col0 += 32) {
                     if (inside<Epi>(q)) Epi::finish(ep, q, sum[c]);
                 }
-            } else {
+              }
+            }
+            if (!summed) {
                 typename Epi::Pre pre;
                 if (inside<Epi>(q)) Epi::prefetch(ep, q, pre);
                 alive = warp_wait(tfull + 8 * acc.stage, acc.phase, dead);
@@ -1081,7 +1112,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             if (elect_one()) {
                 mbar_expect(full + 8 * stage, C::kStageBytes);
                 load_stage<1, kBN>(base + stage * C::kStageBytes, &map_a, &map_b, s,
-                                   full + 8 * stage, m0, n0, kb * kBlockK, b);
+                                   full + 8 * stage, m0, n0, kb, b);
             }
             __syncwarp();
             if (++stage == stages) stage = 0, phase ^= 1;
@@ -1179,11 +1210,13 @@ struct Operand {
     bool mn_major;
 };
 
-// One product D[M, N] = A[M, K] B[K, N], or a batch of them.
+// One product D[M, N] = A[M, K] B[K, N], or a batch of them; or, with planes =
+// 2 and a batch of one, D = (A_0 + A_1) B, A's planes batch_stride apart.
 struct Product {
     Operand a, b;
-    int M, N, K, batch;
+    int M, N, K, batch, planes;
 };
+inline int k_blocks(const Product& p) { return (p.K + kBlockK - 1) / kBlockK * p.planes; }
 
 // Encodes the tensor map for boxes of 64 x box_rows; false when the driver
 // refuses it.
@@ -1223,7 +1256,8 @@ inline cudaError_t shape_of(const Product& p, int bm, int bn, bool sym, Shape* s
     if (tiles * p.batch > 0x0FFFFFFF) return cudaErrorInvalidValue;
     s->tiles = (int)tiles;
     s->total = (int)(tiles * p.batch);
-    s->kblocks = (p.K + kBlockK - 1) / kBlockK;
+    s->per_plane = (p.K + kBlockK - 1) / kBlockK;
+    s->kblocks = k_blocks(p);
     s->segment = s->kblocks > 0 ? s->kblocks : 1;
     s->a_mn = p.a.mn_major;
     s->b_mn = p.b.mn_major;
@@ -1235,7 +1269,7 @@ inline bool encode_product(const Product& p, int b_rows, CUtensorMap* ma, CUtens
     *ma = CUtensorMap{};
     *mb = CUtensorMap{};
     if (p.K == 0) return true;  // nothing is loaded
-    return encode_operand(ma, p.a, p.batch, p.a.mn_major ? kBlockK : kRowsPerCta) &&
+    return encode_operand(ma, p.a, p.batch * p.planes, p.a.mn_major ? kBlockK : kRowsPerCta) &&
            encode_operand(mb, p.b, p.batch, p.b.mn_major ? kBlockK : b_rows);
 }
 
@@ -1267,21 +1301,23 @@ cudaError_t launch_cluster(Kernel* kernel, int blocks, int threads, int cluster,
 }
 
 // One or two products in one launch of the pair kernel.  segment: K
-// blocks summed in tensor memory at a time (kPromote).
+// blocks summed in tensor memory at a time for 32-bit outputs (kPromote).
 template <class Epi, int kCount, bool kPromote>
 cudaError_t launch_pair(const Product* p, const typename Epi::Params* ep, int segment,
                         cudaStream_t st) {
     PairWork<Epi> w = {};
     CUtensorMap m[4] = {};
     // the product with the longer tiles first
-    const int first = kCount == 2 && p[kCount - 1].K > p[0].K ? 1 : 0;
+    const int first = kCount == 2 && k_blocks(p[kCount - 1]) > k_blocks(p[0]) ? 1 : 0;
     for (int i = 0; i < kCount; ++i) {
         const int from = i == 0 ? first : 1 - first;
-        const cudaError_t e = shape_of(p[from], Pair::kBM, Pair::kBN, Epi::kSym, &w.s[i]);
+        const cudaError_t e = shape_of(p[from], Pair<false>::kBM, Pair<false>::kBN, Epi::kSym, &w.s[i]);
         if (e != cudaSuccess) return e;
-        if (kPromote) w.s[i].segment = segment;
+        if constexpr (kPromote) {
+            if (Epi::sums32(ep[from])) w.s[i].segment = segment;
+        }
         w.ep[i] = ep[from];
-        if (!encode_product(p[from], Pair::kBRows, &m[2 * i], &m[2 * i + 1]))
+        if (!encode_product(p[from], Pair<false>::kBRows, &m[2 * i], &m[2 * i + 1]))
             return cudaErrorInvalidValue;
     }
     const int sms = device_sms();
@@ -1292,7 +1328,8 @@ cudaError_t launch_pair(const Product* p, const typename Epi::Params* ep, int se
     const int pairs = total < slots ? total : slots;
     if (w.s[1].total > 0 && w.s[0].total % pairs != 0)
         w.extra = w.s[0].kblocks / (w.s[1].kblocks > 0 ? w.s[1].kblocks : 1);
-    return launch_cluster(pair_kernel<Epi, kCount, kPromote>, pairs * 2, kPairThreads, 2, Pair::kSmem, st, m[0], m[1],
+    return launch_cluster(pair_kernel<Epi, kCount, kPromote>, pairs * 2, Pair<kPromote>::kThreads,
+                          2, Pair<kPromote>::kSmem, st, m[0], m[1],
                           m[2], m[3], w);
 }
 
@@ -1330,8 +1367,8 @@ inline double pair_us(const Product* p, int count, bool sym) {
     long long total = 0;
     const int slots = device_sms() / 2;
     for (int i = 0; i < count; ++i) {
-        const long long tiles = tile_count(p[i].M, p[i].N, Pair::kBM, Pair::kBN, sym) * p[i].batch;
-        const double k = 0.275 * ((p[i].K + kBlockK - 1) / kBlockK) + 0.5;
+        const long long tiles = tile_count(p[i].M, p[i].N, Pair<false>::kBM, Pair<false>::kBN, sym) * p[i].batch;
+        const double k = 0.275 * k_blocks(p[i]) + 0.5;
         const double each = k > 3.2 ? k : 3.2;
         longest = each > longest ? each : longest;
         tile_us += each * (double)tiles;
@@ -1353,7 +1390,7 @@ template <int kBN = 64>
 inline Plan plan_split(const Product& p, bool sym, int limit) {
     using C = Split<kBN>;
     const long long tiles = tile_count(p.M, p.N, C::kBM, kBN, sym) * p.batch;
-    const int kblocks = (p.K + kBlockK - 1) / kBlockK, sms = device_sms();
+    const int kblocks = k_blocks(p), sms = device_sms();
     Plan best = {1e9, 1};
     for (int ranks = 1; ranks <= 8; ranks *= 2) {
         const int kb = (kblocks + ranks - 1) / ranks;

@@ -114,6 +114,7 @@ struct EpiStore {
         }
         finish(p, q, v);
     }
+    static bool sums32(const Params& p) { return p.out.f32; }
     __device__ static void start(const Params& p, const Place& q, float (&v)[32]) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
@@ -143,9 +144,9 @@ cudaError_t forward(const Operand& x, const Operand& w, int M, int N, int K, con
     ep.has_preact = preact != nullptr;
     ep.act = act_params(act);
     if constexpr (kSwap)
-        return gemm::launch_skinny<EpiForward<kFamily, true>>(Product{w, x, N, M, K, 1}, ep, st);
+        return gemm::launch_skinny<EpiForward<kFamily, true>>(Product{w, x, N, M, K, 1, 1}, ep, st);
     else
-        return gemm::launch<EpiForward<kFamily, false>>(Product{x, w, M, N, K, 1}, ep, st);
+        return gemm::launch<EpiForward<kFamily, false>>(Product{x, w, M, N, K, 1, 1}, ep, st);
 }
 
 template <int kFamily>
@@ -159,89 +160,142 @@ cudaError_t forward(const Operand& x, const Operand& w, int M, int N, int K, con
 
 // ------------------------------------------------------------ copy, dz, db --
 
-// A bf16 matrix copied to rows of ld_out values (a multiple of 16), so that
-// TMA can read it.  One warp per row step; element-wise reads.
-__global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* src, long long ld,
-                                                   __nv_bfloat16* dst, long long ld_out,
-                                                   long long rows, long long cols) {
+// bf16 matrices copied to rows of ld_out values (a multiple of 16), so that TMA
+// can read them; one or two in a launch.  A thread makes 16 bytes of a row.
+struct PackJob {
+    const unsigned short* src;
+    uint4* dst;
+    long long ld;
+    int rows, cols, pieces;  // pieces: of 8 values per row
+};
+struct PackJobs {
+    PackJob job[2];
+};
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackJobs jobs) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const long long warps = (long long)gridDim.x * 8;
-    for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
-        const __nv_bfloat16* s = src + r * ld;
-        __nv_bfloat16* d = dst + r * ld_out;
-        for (long long c = lane * 2; c < cols; c += 64) {
-            __nv_bfloat162 v;
-            v.x = s[c];
-            v.y = c + 1 < cols ? s[c + 1] : __float2bfloat16(0.0f);
-            *reinterpret_cast<__nv_bfloat162*>(d + c) = v;
-        }
+    const PackJob j = jobs.job[blockIdx.y];
+    const long long total = (long long)j.rows * j.pieces;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
+         i += (long long)gridDim.x * 256) {
+        const int row = (int)(i / j.pieces), col = (int)(i - (long long)row * j.pieces) * 8;
+        const unsigned short* s = j.src + row * j.ld + col;
+        unsigned v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = col + k < j.cols ? s[k] : 0u;
+        j.dst[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
 }
 
 struct DzParams {
     View dy, preact;
-    __nv_bfloat16* dz;  // NULL: not written
+    __nv_bfloat16* dz;       // NULL: not written
+    __nv_bfloat16* dz_rest;  // NULL, or receives what rounding dz left
     long long ld_dz;
     float* sums;  // [gridDim.y][N], or NULL
     long long rows, cols;
-    int has_act;
+    int has_act, vec16;
     Act act;
 };
 
+constexpr int kDzRows = 4;  // rows that a thread loads before it uses them
+
 // dz = dy * act'(z) and the column sums of each block's rows.  A warp covers
-// 128 columns of a row; the block's eight warps take its rows in turn.
+// 256 columns (8 per lane); the block's eight warps take groups of rows in
+// turn.
 template <int kFamily>
 __global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzParams p) {
-    __shared__ float4 part[8][32];
+    __shared__ float4 part[8][64];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long col = (long long)blockIdx.x * 128 + lane * 4;
-    const int n = (int)min(4ll, p.cols - col);
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (n > 0) {
-        for (long long row = (long long)blockIdx.y * 8 + warp; row < p.rows;
-             row += (long long)gridDim.y * 8) {
-            float4 v = gemm::view_load(p.dy, 0, row, (int)col, n);
-            if (p.has_act) {
-                const float4 z = gemm::view_load(p.preact, 0, row, (int)col, n);
-                const float2 lo = act_slope<kFamily>(make_float2(z.x, z.y), p.act);
-                const float2 hi = act_slope<kFamily>(make_float2(z.z, z.w), p.act);
-                v = make_float4(v.x * lo.x, v.y * lo.y, v.z * hi.x, v.w * hi.y);
+    const long long col = (long long)blockIdx.x * 256 + lane * 8;
+    const int n = (int)min(8ll, p.cols - col);
+    const bool vec = p.vec16 && n == 8;
+    float sum[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    const __nv_bfloat16* const dy = static_cast<const __nv_bfloat16*>(p.dy.data) + col;
+    const __nv_bfloat16* const z = static_cast<const __nv_bfloat16*>(p.preact.data) + col;
+    auto load8 = [&](const __nv_bfloat16* at) {
+        if (vec) return *reinterpret_cast<const uint4*>(at);
+        const unsigned short* s = reinterpret_cast<const unsigned short*>(at);
+        unsigned v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < n ? s[j] : 0u;
+        return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    };
+    auto low = [](unsigned w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); };
+    const long long step = (long long)gridDim.y * 8 * kDzRows;
+    for (long long row0 = ((long long)blockIdx.y * 8 + warp) * kDzRows; n > 0 && row0 < p.rows;
+         row0 += step) {
+        uint4 a[kDzRows], b[kDzRows];
+#pragma unroll
+        for (int u = 0; u < kDzRows; ++u) {
+            if (row0 + u >= p.rows) continue;
+            a[u] = load8(dy + (row0 + u) * p.dy.ld);
+            if (p.has_act) b[u] = load8(z + (row0 + u) * p.preact.ld);
+        }
+#pragma unroll
+        for (int u = 0; u < kDzRows; ++u) {
+            if (row0 + u >= p.rows) continue;
+            const unsigned aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+            const unsigned bw[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+            unsigned hi[4], rest[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 v = low(aw[j]);
+                if (p.has_act) {
+                    const float2 k = act_slope<kFamily>(low(bw[j]), p.act);
+                    v = make_float2(2 * j < n ? v.x * k.x : 0.0f, 2 * j + 1 < n ? v.y * k.y : 0.0f);
+                }
+                sum[2 * j] += v.x;
+                sum[2 * j + 1] += v.y;
+                hi[j] = gemm::packed(v.x, v.y, __nv_bfloat16());
+                const float2 h = low(hi[j]);
+                rest[j] = gemm::packed(v.x - h.x, v.y - h.y, __nv_bfloat16());
             }
-            if (p.dz != nullptr) gemm::store4(p.dz + row * p.ld_dz + col, v, n, true);
-            sum.x += v.x;
-            sum.y += v.y;
-            sum.z += v.z;
-            sum.w += v.w;
+            // (the buffers' rows are whole groups of 16 values)
+            if (p.dz != nullptr)
+                *reinterpret_cast<uint4*>(p.dz + (row0 + u) * p.ld_dz + col) =
+                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (p.dz_rest != nullptr)
+                *reinterpret_cast<uint4*>(p.dz_rest + (row0 + u) * p.ld_dz + col) =
+                    make_uint4(rest[0], rest[1], rest[2], rest[3]);
         }
     }
     if (p.sums == nullptr) return;
-    part[warp][lane] = sum;
+    part[warp][lane * 2] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    part[warp][lane * 2 + 1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
     __syncthreads();
-    if (warp == 0 && n > 0) {
-        for (int w = 1; w < 8; ++w) {
-            const float4 o = part[w][lane];
-            sum.x += o.x;
-            sum.y += o.y;
-            sum.z += o.z;
-            sum.w += o.w;
-        }
-        gemm::store4(p.sums + (long long)blockIdx.y * p.cols + col, sum, n, false);
+    const long long mine = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (mine < p.cols) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += reinterpret_cast<const float*>(part[w])[threadIdx.x];
+        p.sums[(long long)blockIdx.y * p.cols + mine] = t;
     }
 }
 
-// db (+)= the sum of the blocks' partial sums, in block order.
+// db (+)= the sum of the blocks' partial sums, in a fixed order: a block takes
+// 32 columns, its warps every eighth part.
 __global__ void __launch_bounds__(256) db_kernel(const float* sums, int parts, long long cols,
                                                  void* db, int f32, int add) {
+    __shared__ float part[8][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long col = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (col >= cols) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long col = (long long)blockIdx.x * 32 + lane;
     float v = 0.0f;
-    for (int i = 0; i < parts; ++i) v += sums[(long long)i * cols + col];
+    if (col < cols) {
+#pragma unroll 8
+        for (int i = warp; i < parts; i += 8) v += sums[(long long)i * cols + col];
+    }
+    part[warp][lane] = v;
+    __syncthreads();
+    if (warp != 0 || col >= cols) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v += part[w][lane];
     if (f32) {
         float* d = static_cast<float*>(db) + col;
         *d = add ? *d + v : v;
@@ -251,11 +305,18 @@ __global__ void __launch_bounds__(256) db_kernel(const float* sums, int parts, l
     }
 }
 
+// Blocks along the rows: enough for eight blocks per SM, each with a group of
+// rows for every warp.
 int dz_row_blocks(long long rows, long long cols) {
-    const long long across = (cols + 127) / 128;
+    const long long across = (cols + 255) / 256;
     const long long want = (152 * 8 + across - 1) / across;
-    return (int)std::max(1ll, std::min(want, (rows + 31) / 32));
+    return (int)std::max(1ll, std::min(want, (rows + 8 * kDzRows - 1) / (8 * kDzRows)));
 }
+
+// Batches of up to this many rows keep what rounding dz to bf16 leaves as a
+// second plane of the operand: their products are bound by the weight's bytes,
+// so that it costs nothing, and with few rows single roundings show.
+constexpr int kRestRows = 64;
 
 // K blocks (of 64) summed in tensor memory at a time for 32-bit gradients.
 constexpr int kSegment = 16;
@@ -270,22 +331,33 @@ size_t packed_bytes(const vc_matrix_t* m) {
     return operand_ready(m) ? 0 : round256((size_t)m->rows * padded_ld(m->cols) * 2);
 }
 
-// Where TMA reads the matrix: in place, or packed at *ws (advanced).
-cudaError_t ready_operand(const vc_matrix_t* m, unsigned char** ws, cudaStream_t st,
-                          const void** data, long long* ld) {
+// Where TMA reads the matrix: in place, or packed at *ws (advanced), for which
+// a job is added.
+void ready_operand(const vc_matrix_t* m, unsigned char** ws, PackJobs* jobs, int* count,
+                   Operand* o) {
     if (operand_ready(m) || m->rows == 0 || m->cols == 0) {
-        *data = m->data;
-        *ld = m->rows > 1 ? m->ld : padded_ld(m->cols);
-        return cudaSuccess;
+        o->data = m->data;
+        o->ld = m->rows > 1 ? m->ld : padded_ld(m->cols);
+        return;
     }
-    *data = *ws;
-    *ld = padded_ld(m->cols);
-    const int blocks = (int)std::min(152 * 8ll, (m->rows + 7) / 8);
-    const cudaError_t e = launch_pdl(
-        pack_kernel, dim3(blocks), dim3(256), st, static_cast<const __nv_bfloat16*>(m->data),
-        m->rows > 1 ? m->ld : 0, reinterpret_cast<__nv_bfloat16*>(*ws), *ld, m->rows, m->cols);
+    o->data = *ws;
+    o->ld = padded_ld(m->cols);
+    jobs->job[(*count)++] = {static_cast<const unsigned short*>(m->data),
+                             reinterpret_cast<uint4*>(*ws),
+                             m->rows > 1 ? m->ld : 0,
+                             (int)m->rows,
+                             (int)m->cols,
+                             (int)(o->ld / 8)};
     *ws += packed_bytes(m);
-    return e;
+}
+
+cudaError_t launch_pack(const PackJobs& jobs, int count, cudaStream_t st) {
+    if (count == 0) return cudaSuccess;
+    long long most = 0;
+    for (int i = 0; i < count; ++i)
+        most = std::max(most, (long long)jobs.job[i].rows * jobs.job[i].pieces);
+    const int blocks = (int)std::min(152 * 16ll, (most + 255) / 256);
+    return launch_pdl(pack_kernel, dim3(blocks, count), dim3(256), st, jobs);
 }
 
 bool is_bf16(const vc_matrix_t* m) { return m->dtype == VC_BFLOAT16; }
@@ -300,11 +372,15 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
     return need == 0 || (ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 15) == 0 && have >= need);
 }
 
+int dz_planes(long long rows, vc_act_t act) {
+    return act != VC_ACT_NONE && rows <= kRestRows ? 2 : 1;
+}
+
 size_t backward_workspace(const vc_matrix_t* dy, const vc_matrix_t* x, const vc_matrix_t* weight,
                           vc_act_t act, bool has_dbias) {
     size_t need = packed_bytes(x) + packed_bytes(weight);
     if (act != VC_ACT_NONE || !operand_ready(dy))
-        need += round256((size_t)dy->rows * padded_ld(dy->cols) * 2);
+        need += dz_planes(dy->rows, act) * round256((size_t)dy->rows * padded_ld(dy->cols) * 2);
     if (has_dbias) need += round256((size_t)dz_row_blocks(dy->rows, dy->cols) * dy->cols * 4);
     return need;
 }
@@ -354,9 +430,11 @@ vc_status_t vc_linear_forward(const vc_matrix_t* x, const vc_matrix_t* weight, c
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     Operand a = {nullptr, K, M, 0, 0, true, false}, b = {nullptr, K, N, 0, 0, true, false};
-    if (ready_operand(x, &ws, st, &a.data, &a.ld) != cudaSuccess ||
-        ready_operand(weight, &ws, st, &b.data, &b.ld) != cudaSuccess)
-        return VC_ERR_CUDA;
+    PackJobs jobs = {};
+    int packs = 0;
+    ready_operand(x, &ws, &jobs, &packs, &a);
+    ready_operand(weight, &ws, &jobs, &packs, &b);
+    if (launch_pack(jobs, packs, st) != cudaSuccess) return VC_ERR_CUDA;
     cudaError_t e;
     switch (act_family(act)) {
     case kFamilyErf:
@@ -418,6 +496,8 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
     const bool write_dz = has_act || !operand_ready(dy);
     const void* dz = dy->data;
     long long ld_dz = M > 1 ? dy->ld : padded_ld(N);
+    const int planes = dz_planes(M, act);
+    const long long plane = (long long)(round256((size_t)M * padded_ld(N) * 2) / 2);
     float* sums = nullptr;
     const int parts = dz_row_blocks(M, N);
     if (dbias != nullptr) {
@@ -427,7 +507,7 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
     if (write_dz) {
         dz = ws;
         ld_dz = padded_ld(N);
-        ws += round256((size_t)M * ld_dz * 2);
+        ws += planes * round256((size_t)M * ld_dz * 2);
     }
     cudaError_t e = cudaSuccess;
     if (N > 0 && (sums != nullptr || (write_dz && M > 0))) {
@@ -435,7 +515,9 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
         p.dy = view_of(dy);
         p.preact = view_of(has_act ? preact : nullptr);
         p.dz = write_dz ? static_cast<__nv_bfloat16*>(const_cast<void*>(dz)) : nullptr;
+        p.dz_rest = planes == 2 ? p.dz + plane : nullptr;
         p.ld_dz = ld_dz;
+        p.vec16 = p.dy.vec16 && (!has_act || p.preact.vec16);
         p.sums = sums;
         p.rows = M;
         p.cols = N;
@@ -444,10 +526,10 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
         auto* kernel = act_family(act) == kFamilyErf        ? dz_kernel<kFamilyErf>
                        : act_family(act) == kFamilyLogistic ? dz_kernel<kFamilyLogistic>
                                                             : dz_kernel<kFamilyPiecewise>;
-        e = launch_pdl(kernel, dim3((unsigned)((N + 127) / 128), parts), dim3(256), st, p);
+        e = launch_pdl(kernel, dim3((unsigned)((N + 255) / 256), parts), dim3(256), st, p);
         if (e != cudaSuccess) return VC_ERR_CUDA;
         if (sums != nullptr) {
-            e = launch_pdl(db_kernel, dim3((unsigned)((N + 255) / 256)), dim3(256), st,
+            e = launch_pdl(db_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), st,
                            (const float*)sums, parts, N, dbias, dbias_dtype == VC_FLOAT32 ? 1 : 0,
                            accumulate != 0 ? 1 : 0);
             if (e != cudaSuccess) return VC_ERR_CUDA;
@@ -455,19 +537,23 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
     }
     Product p[2];
     EpiStore<false>::Params ep[2];
-    int count = 0;
+    int count = 0, packs = 0;
+    PackJobs jobs = {};
     if (dx != nullptr && M > 0 && K > 0) {
-        Operand a = {dz, N, M, ld_dz, 0, true, false}, b = {nullptr, K, N, 0, 0, true, true};
-        if (ready_operand(weight, &ws, st, &b.data, &b.ld) != cudaSuccess) return VC_ERR_CUDA;
-        p[count] = {a, b, (int)M, (int)K, (int)N, 1};
+        const Operand a = {dz, N, M, ld_dz, plane, true, false};
+        Operand b = {nullptr, K, N, 0, 0, true, true};
+        ready_operand(weight, &ws, &jobs, &packs, &b);
+        p[count] = {a, b, (int)M, (int)K, (int)N, 1, planes};
         ep[count++] = {view_of(dx), 0};
     }
     if (dweight != nullptr && N > 0 && K > 0) {
-        Operand a = {dz, N, M, ld_dz, 0, true, true}, b = {nullptr, K, M, 0, 0, true, true};
-        if (ready_operand(x, &ws, st, &b.data, &b.ld) != cudaSuccess) return VC_ERR_CUDA;
-        p[count] = {a, b, (int)N, (int)K, (int)M, 1};
+        const Operand a = {dz, N, M, ld_dz, plane, true, true};
+        Operand b = {nullptr, K, M, 0, 0, true, true};
+        ready_operand(x, &ws, &jobs, &packs, &b);
+        p[count] = {a, b, (int)N, (int)K, (int)M, 1, planes};
         ep[count++] = {view_of(dweight), accumulate != 0};
     }
+    if (launch_pack(jobs, packs, st) != cudaSuccess) return VC_ERR_CUDA;
     if (count > 0) {
         // 32-bit sums are not left to the tensor cores for longer than a segment
         const bool promote = dweight != nullptr && dweight->dtype == VC_FLOAT32;

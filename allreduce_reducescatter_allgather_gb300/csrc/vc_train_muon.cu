@@ -385,21 +385,21 @@ cudaError_t iterate(const Layout& l, long long batch, long long rows, long long 
         xm.mn_major = true;
         EpiGram::Params gp = {oa, da, l.ldr, l.as, 1.0f / (size * size)};
         const Operand& side = tall ? xm : xk;
-        e = gemm::launch<EpiGram>(Product{side, side, r, r, c, nb}, gp, st);
+        e = gemm::launch<EpiGram>(Product{side, side, r, r, c, nb, 1}, gp, st);
         if (e != cudaSuccess) break;
         const Operand ao = {oa, r, r, l.ldr, l.as, false, false};
         EpiPoly::Params pp = {oa, da, ob, db, l.ldr, l.as, ns.b, ns.c};
-        e = gemm::launch<EpiPoly>(Product{ao, ao, r, r, r, nb}, pp, st);
+        e = gemm::launch<EpiPoly>(Product{ao, ao, r, r, r, nb, 1}, pp, st);
         if (e != cudaSuccess) break;
         const Operand bo = {ob, r, r, l.ldr, l.as, false, false};
         const UpdateParams u = {x[0], lo, x[1], db, l.ldx, l.xs, ns.a, tall, r};
         const Operand &left = tall ? xk : bo, &right = tall ? bo : xm;
         if (i + 1 < ns.steps) {
-            e = gemm::launch<EpiUpdate>(Product{left, right, (int)rows, (int)cols, r, nb}, u, st);
+            e = gemm::launch<EpiUpdate>(Product{left, right, (int)rows, (int)cols, r, nb, 1}, u, st);
         } else {
             fin.u = u;
             fin.scale /= size;
-            e = gemm::launch<EpiFinal>(Product{left, right, (int)rows, (int)cols, r, nb}, fin, st);
+            e = gemm::launch<EpiFinal>(Product{left, right, (int)rows, (int)cols, r, nb, 1}, fin, st);
         }
         std::swap(x[0], x[1]);
     }
