@@ -1,0 +1,258 @@
+"""The training-step ABI (include/vc_train.h) without a GPU: the library exports
+what the header declares, and rejects bad arguments before launching anything.
+
+As in test_abi_cpu.py, no call reaches a launch: validation fails first, or the
+launch hook (VC_TEST_FAIL_LAUNCH) turns the launch into VC_ERR_CUDA.  The fake
+device pointers are never dereferenced.
+"""
+from __future__ import annotations
+
+import ctypes
+import re
+import subprocess
+
+import pytest
+
+from conftest import ROOT
+
+SUCCESS, INVALID, UNSUPPORTED, ALIAS, CUDA = 0, 1, 2, 3, 4
+F32, BF16, I32 = 2, 3, 0
+GiB = 1 << 30
+NONE, RELU, GELU = 0, 1, 3
+
+
+@pytest.fixture(scope="module")
+def tr():
+    import __graft_entry__
+    __graft_entry__.build()
+    from allreduce_reducescatter_allgather_gb300 import training
+    training._lib()
+    return training
+
+
+@pytest.fixture(autouse=True)
+def no_launch(monkeypatch):
+    monkeypatch.setenv("VC_TEST_FAIL_LAUNCH", "1")
+
+
+def mat(tr, at, rows, cols, ld=None, dtype=BF16, batch=1, stride=None):
+    ld = cols if ld is None else ld
+    return tr.Matrix(at, batch, rows, cols, ld, rows * ld if stride is None else stride, dtype)
+
+
+def ref(m):
+    return ctypes.byref(m) if m is not None else None
+
+
+def header_functions():
+    text = (ROOT / "include" / "vc_train.h").read_text()
+    return sorted(set(re.findall(r"^\S.*?\b(vc_\w+)\s*\(", text, flags=re.M)))
+
+
+def test_library_exports_what_the_header_declares(tr):
+    assert header_functions() == sorted(tr.TRAIN_EXPORTS)
+    from allreduce_reducescatter_allgather_gb300._binding import LIB_PATH
+    out = subprocess.run(["nm", "-D", "--defined-only", str(LIB_PATH)], capture_output=True,
+                         text=True, check=True).stdout
+    exported = set(re.findall(r"\bT (vc_\w+)$", out, flags=re.M))
+    assert set(header_functions()) <= exported
+
+
+def forward(tr, x, w, y, bias=0, res=None, z=None, act=NONE, ws=0, size=0):
+    return tr._lib().vc_linear_forward(ref(x), ref(w), bias, ref(res), ref(y), ref(z), act, ws,
+                                       size, None)
+
+
+def test_forward_shapes_types_and_pointers(tr):
+    x, w, y = mat(tr, GiB, 10, 64), mat(tr, 2 * GiB, 24, 64), mat(tr, 3 * GiB, 10, 24)
+    assert forward(tr, x, w, y) == CUDA  # valid: the hook fires
+    assert forward(tr, None, w, y) == INVALID
+    assert forward(tr, x, None, y) == INVALID
+    assert forward(tr, x, w, None) == INVALID
+    assert forward(tr, mat(tr, 0, 10, 64), w, y) == INVALID          # null
+    assert forward(tr, mat(tr, GiB + 1, 10, 64), w, y) == INVALID    # not on an element
+    assert forward(tr, mat(tr, GiB, 10, 63), w, y) == INVALID        # K differs
+    assert forward(tr, x, w, mat(tr, 3 * GiB, 11, 24)) == INVALID    # M differs
+    assert forward(tr, x, w, mat(tr, 3 * GiB, 10, 23)) == INVALID    # N differs
+    assert forward(tr, x, w, mat(tr, 3 * GiB, 10, 24, dtype=F32)) == INVALID
+    assert forward(tr, mat(tr, GiB, 10, 64, dtype=I32), w, y) == INVALID
+    assert forward(tr, mat(tr, GiB, 10, 64, ld=63), w, y) == INVALID  # rows overlap
+    assert forward(tr, mat(tr, GiB, 10, 64, batch=2), w, y) == INVALID
+    assert forward(tr, mat(tr, GiB, -1, 64), w, y) == INVALID
+    assert forward(tr, x, w, y, act=6) == INVALID
+    assert forward(tr, x, w, y, act=-1) == INVALID
+    assert forward(tr, x, w, y, bias=4 * GiB + 1) == INVALID
+    assert forward(tr, x, w, y, res=mat(tr, 5 * GiB, 10, 25)) == INVALID
+    assert forward(tr, x, w, y, z=mat(tr, 5 * GiB, 9, 24)) == INVALID
+    # sizes beyond the kernels' coordinates, strides whose bytes would wrap
+    assert forward(tr, mat(tr, GiB, 1 << 31, 64), w, mat(tr, 3 * GiB, 1 << 31, 24)) == INVALID
+    assert forward(tr, mat(tr, GiB, 10, 64, ld=1 << 61), w, y) == INVALID
+
+
+def test_forward_aliases(tr):
+    x, w, y = mat(tr, GiB, 10, 64), mat(tr, 2 * GiB, 24, 64), mat(tr, 3 * GiB, 10, 24)
+    assert forward(tr, x, w, mat(tr, GiB, 10, 24)) == ALIAS
+    assert forward(tr, x, w, mat(tr, 2 * GiB + 100, 10, 24)) == ALIAS
+    assert forward(tr, x, w, y, bias=3 * GiB) == ALIAS
+    assert forward(tr, x, w, y, res=y) == CUDA  # in place
+    assert forward(tr, x, w, y, res=mat(tr, 3 * GiB + 2, 10, 24)) == ALIAS
+    assert forward(tr, x, w, mat(tr, 3 * GiB, 10, 24, ld=32), res=y) == ALIAS  # other rows
+    assert forward(tr, x, w, y, z=y) == ALIAS
+    assert forward(tr, x, w, y, z=mat(tr, GiB, 10, 24)) == ALIAS
+
+
+def test_forward_workspace(tr):
+    L = tr._lib()
+    y = mat(tr, 3 * GiB, 10, 24)
+    assert L.vc_linear_forward_workspace(ref(mat(tr, GiB, 10, 64)), ref(mat(tr, 2 * GiB, 24, 64))) == 0
+    assert L.vc_linear_forward_workspace(None, ref(mat(tr, 2 * GiB, 24, 64))) == 0
+    x, w = mat(tr, GiB, 10, 65), mat(tr, 2 * GiB, 24, 65)  # rows off 16 bytes
+    need = L.vc_linear_forward_workspace(ref(x), ref(w))
+    assert need >= (10 + 24) * 65 * 2
+    assert forward(tr, x, w, y, ws=6 * GiB, size=need) == CUDA
+    assert forward(tr, x, w, y, ws=6 * GiB, size=need - 1) == INVALID
+    assert forward(tr, x, w, y) == INVALID
+    assert forward(tr, x, w, y, ws=6 * GiB + 8, size=need) == INVALID
+    assert forward(tr, x, w, y, ws=3 * GiB, size=need) == ALIAS
+    # one row's length does not matter, a base off 16 bytes does
+    one = mat(tr, GiB, 1, 65)
+    assert L.vc_linear_forward_workspace(ref(one), ref(mat(tr, 2 * GiB, 24, 65))) < need
+    assert L.vc_linear_forward_workspace(ref(mat(tr, GiB + 2, 10, 64)),
+                                         ref(mat(tr, 2 * GiB, 24, 64))) > 0
+
+
+def test_forward_empty(tr):
+    w, y = mat(tr, 2 * GiB, 24, 64), mat(tr, 3 * GiB, 10, 24)
+    assert forward(tr, mat(tr, 0, 0, 64), w, mat(tr, 0, 0, 24)) == SUCCESS
+    assert forward(tr, mat(tr, GiB, 10, 64), mat(tr, 0, 0, 64), mat(tr, 0, 10, 0)) == SUCCESS
+    assert forward(tr, mat(tr, 0, 10, 0), mat(tr, 0, 24, 0), y) == CUDA  # K = 0: y = act(b) + r
+
+
+def backward(tr, dy, x, w, dx=None, dw=None, db=0, db_type=F32, z=None, act=NONE, acc=0,
+             ws=8 * GiB, size=GiB):
+    return tr._lib().vc_linear_backward(ref(dy), ref(x), ref(w), ref(z), act, ref(dx), ref(dw), db,
+                                        db_type, acc, ws, size, None)
+
+
+def test_backward_arguments(tr):
+    dy, x, w = mat(tr, GiB, 100, 24), mat(tr, 2 * GiB, 100, 64), mat(tr, 3 * GiB, 24, 64)
+    dx, dw = mat(tr, 4 * GiB, 100, 64), mat(tr, 5 * GiB, 24, 64, dtype=F32)
+    z = mat(tr, 6 * GiB, 100, 24)
+    assert backward(tr, dy, x, w, dx, dw, 7 * GiB) == CUDA
+    assert backward(tr, dy, x, w, dx) == CUDA
+    assert backward(tr, dy, x, w, dw=mat(tr, 5 * GiB, 24, 64)) == CUDA
+    assert backward(tr, dy, x, w) == SUCCESS  # nothing asked for
+    assert backward(tr, dy, x, w, dx, act=GELU) == INVALID  # needs preact
+    assert backward(tr, dy, x, w, dx, act=GELU, z=z) == CUDA
+    assert backward(tr, dy, x, w, dx, act=GELU, z=mat(tr, 6 * GiB, 100, 24, dtype=F32)) == INVALID
+    assert backward(tr, dy, x, w, mat(tr, 4 * GiB, 100, 64, dtype=F32)) == INVALID
+    assert backward(tr, dy, x, w, mat(tr, 4 * GiB, 100, 63)) == INVALID
+    assert backward(tr, dy, x, w, dw=mat(tr, 5 * GiB, 64, 24)) == INVALID
+    assert backward(tr, mat(tr, GiB, 99, 24), x, w, dx) == INVALID
+    assert backward(tr, dy, x, w, dx, db=7 * GiB, db_type=I32) == INVALID
+    assert backward(tr, dy, x, w, dx, db=7 * GiB + 2) == INVALID
+    assert backward(tr, dy, x, w, dx, db=7 * GiB + 2, db_type=BF16) == CUDA
+    assert backward(tr, dy, x, w, dx, act=9) == INVALID
+
+
+def test_backward_aliases_and_workspace(tr):
+    dy, x, w = mat(tr, GiB, 100, 24), mat(tr, 2 * GiB, 100, 64), mat(tr, 3 * GiB, 24, 64)
+    z = mat(tr, 6 * GiB, 100, 24)
+    assert backward(tr, dy, x, w, mat(tr, 2 * GiB, 100, 64)) == ALIAS  # dx over x
+    assert backward(tr, dy, x, w, mat(tr, GiB, 100, 64)) == ALIAS
+    assert backward(tr, dy, x, w, dw=mat(tr, 3 * GiB, 24, 64)) == ALIAS
+    assert backward(tr, dy, x, w, mat(tr, 4 * GiB, 100, 64),
+                    mat(tr, 4 * GiB + 16, 24, 64)) == ALIAS
+    assert backward(tr, dy, x, w, db=6 * GiB, act=GELU, z=z) == ALIAS
+    L = tr._lib()
+    need = L.vc_linear_backward_workspace(ref(dy), ref(x), ref(w), GELU, 1)
+    assert need >= 100 * 24 * 2 + 24 * 4
+    dx = mat(tr, 4 * GiB, 100, 64)
+    assert backward(tr, dy, x, w, dx, db=7 * GiB, act=GELU, z=z, size=need) == CUDA
+    assert backward(tr, dy, x, w, dx, db=7 * GiB, act=GELU, z=z, size=need - 1) == INVALID
+    assert backward(tr, dy, x, w, dx, db=7 * GiB, act=GELU, z=z, ws=2 * GiB, size=need) == ALIAS
+    # without an activation, a bias or odd rows nothing is needed
+    assert L.vc_linear_backward_workspace(ref(dy), ref(x), ref(w), NONE, 0) == 0
+    assert backward(tr, dy, x, w, dx, ws=0, size=0) == CUDA
+    # small batches keep dz's rounding remainder: a second plane
+    few = [mat(tr, GiB, 64, 24), mat(tr, 2 * GiB, 64, 64)]
+    more = [mat(tr, GiB, 65, 24), mat(tr, 2 * GiB, 65, 64)]
+    assert (L.vc_linear_backward_workspace(ref(few[0]), ref(few[1]), ref(w), GELU, 0)
+            > L.vc_linear_backward_workspace(ref(more[0]), ref(more[1]), ref(w), GELU, 0))
+
+
+def ns(tr, steps=5, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7):
+    return tr.NewtonSchulz(steps, a, b, c, eps)
+
+
+def ortho(tr, g, out, n=None, ws=8 * GiB, size=4 * GiB):
+    return tr._lib().vc_orthogonalize(ref(g), ref(out), ref(n or ns(tr)), ws, size, None)
+
+
+def test_orthogonalize_arguments(tr):
+    g, out = mat(tr, GiB, 100, 64, dtype=F32), mat(tr, 2 * GiB, 100, 64)
+    assert ortho(tr, g, out) == CUDA
+    assert ortho(tr, mat(tr, GiB, 100, 64), out) == CUDA
+    assert ortho(tr, out, out) == CUDA  # in place
+    assert ortho(tr, mat(tr, 2 * GiB + 2, 100, 64), out) == ALIAS
+    assert ortho(tr, mat(tr, GiB, 100, 64, dtype=I32), out) == INVALID
+    assert ortho(tr, g, mat(tr, 2 * GiB, 100, 64, dtype=F32)) == INVALID
+    assert ortho(tr, g, mat(tr, 2 * GiB, 64, 100)) == INVALID
+    assert ortho(tr, g, out, ns(tr, steps=0)) == INVALID
+    assert ortho(tr, g, out, ns(tr, steps=101)) == INVALID
+    assert ortho(tr, g, out, ns(tr, a=float("nan"))) == INVALID
+    assert ortho(tr, g, out, ns(tr, eps=-1.0)) == INVALID
+    assert ortho(tr, g, out, ws=0) == INVALID
+    assert ortho(tr, g, out, ws=8 * GiB + 16) == INVALID
+    assert ortho(tr, g, out, ws=GiB) == ALIAS
+    need = tr._lib().vc_orthogonalize_workspace(1, 100, 64)
+    assert need > 0
+    assert ortho(tr, g, out, size=need) == CUDA
+    assert ortho(tr, g, out, size=need - 1) == INVALID
+    assert ortho(tr, mat(tr, GiB, 100, 64, batch=3, stride=100 * 64 - 1),
+                 mat(tr, 2 * GiB, 100, 64, batch=3)) == INVALID  # matrices overlap
+    for shape in ((0, 100, 64), (1, 0, 64), (1, 100, 0)):
+        assert tr._lib().vc_orthogonalize_workspace(*shape) == 0
+        assert ortho(tr, mat(tr, 0, shape[1], shape[2], batch=shape[0]),
+                     mat(tr, 0, shape[1], shape[2], batch=shape[0]), ws=0, size=0) == SUCCESS
+    assert tr._lib().vc_orthogonalize_workspace(-1, 4, 4) == 0
+    assert tr._lib().vc_orthogonalize_workspace(1, 1 << 25, 4) == 0
+
+
+def muon(tr, w, g, m, ws=8 * GiB, size=4 * GiB, **kw):
+    args = tr.Muon(kw.get("lr", 0.1), kw.get("beta", 0.9), kw.get("wd", 0.0), kw.get("scale", 1.0),
+                   1, kw.get("ns", ns(tr)))
+    return tr._lib().vc_muon_step(ref(w), ref(g), ref(m), ctypes.byref(args), ws, size, None)
+
+
+def test_muon_arguments(tr):
+    w, g, m = (mat(tr, (1 + i) * GiB, 100, 64, dtype=F32) for i in range(3))
+    assert muon(tr, w, g, m) == CUDA
+    assert muon(tr, mat(tr, GiB, 100, 64), mat(tr, 2 * GiB, 100, 64), m) == CUDA
+    assert muon(tr, w, w, m) == ALIAS
+    assert muon(tr, w, g, g) == ALIAS
+    assert muon(tr, w, g, m, ws=2 * GiB) == ALIAS
+    assert muon(tr, w, mat(tr, 2 * GiB, 64, 100, dtype=F32), m) == INVALID
+    assert muon(tr, w, g, mat(tr, 3 * GiB, 100, 64, dtype=I32)) == INVALID
+    assert muon(tr, w, g, None) == INVALID
+    for bad in ({"lr": float("inf")}, {"beta": float("nan")}, {"wd": float("nan")},
+                {"scale": float("inf")}, {"ns": ns(tr, steps=0)}):
+        assert muon(tr, w, g, m, **bad) == INVALID
+    assert tr._lib().vc_muon_step(ref(w), ref(g), ref(m), None, 8 * GiB, GiB, None) == INVALID
+
+
+def test_timeouts_reports_errors(tr):
+    assert tr._lib().vc_train_timeouts(None) == INVALID
+    n = ctypes.c_uint(7)
+    assert tr._lib().vc_train_timeouts(ctypes.byref(n)) == CUDA
+
+
+def test_binding_refuses_host_tensors(tr):
+    torch = pytest.importorskip("torch")
+    t = torch.zeros(4, 4, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="not a CUDA tensor"):
+        tr.vc_linear_forward(t, t, t)
+    with pytest.raises(ValueError, match="not a CUDA tensor"):
+        tr.vc_orthogonalize(t, t)
+    with pytest.raises(TypeError, match="not a tensor"):
+        tr.vc_muon_step([1.0], t, t, lr=0.1)
