@@ -1232,7 +1232,7 @@ int device_sms();
 // The current device's count of waits that ran out; nullptr on error.
 unsigned* timeout_counter();
 
-inline unsigned instruction_desc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
+__host__ __device__ inline unsigned instruction_desc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
            ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((unsigned)(n >> 3) << 17) |
            ((unsigned)(m >> 4) << 24);

@@ -1,0 +1,428 @@
+// Newton-Schulz for matrices whose smaller side is at most 128: the whole
+// operator -- momentum, norm, every pass, the weight update -- in one kernel.
+//
+// X stays on the chip.  With r <= 128 rows (the smaller side; a tall matrix is
+// read and written transposed), a block holds up to 256 of X's columns in
+// shared memory, and a cluster of up to eight blocks up to 2048.  Per pass:
+//   A      each block multiplies its columns, X X^T, 128 x 128; the blocks add
+//          their parts through distributed shared memory (each owns some 32 x
+//          32 chunks of A, adds them in rank order, and sends the finished
+//          chunk, in fp16, to all);
+//   A^2    every block computes the whole of it, 128 x 128 x 128;
+//   B X    each block its own columns.
+// X's tile of 64 columns is 128 rows of 128 bytes, swizzled, which serves as
+// K-major operand of X X^T and as MN-major operand of B X alike.
+//
+// The alternative, a launch per product, spends 4 to 5 us on each of 15
+// products however small they are (128 x 256: 83 us); NEWT
+#pragma once
+
+#include "vc_train_common.cuh"
+
+namespace vc {
+namespace train {
+
+struct SmallParams {
+    gemm::View g, m, out;
+    int has_momentum, nesterov, weights, tall;
+    int r, c;       // smaller and larger side
+    int width;      // columns of X per block, a multiple of 64
+    int steps;
+    float beta, eps;
+    float ca, cb, cc;  // the polynomial
+    float size;        // X is stored times this
+    float keep, scale;  // out <- keep out + scale X, or scale X
+    unsigned* timeouts;
+};
+
+struct Small {
+    static constexpr int kThreads = 256, kMaxWidth = 256, kMaxRanks = 8, kRows = 128;
+    static constexpr int kAtom = 128 * 128;  // bytes of 64 columns
+    static constexpr int kHi = 0, kLo = 4 * kAtom, kO = 8 * kAtom, kParts = 10 * kAtom;
+    static constexpr int kVectors = 14 * kAtom;  // diagonals of A and B, norms, sums
+    static constexpr int kBar = kVectors + 1024 + 128;
+    static constexpr int kSmem = 1024 + kBar + 64;
+    static constexpr int kTmemCols = 512;  // 128 for A and A^2, up to 256 for B X
+    static_assert(kSmem <= gemm::kSmemPerBlock, "shared memory");
+};
+
+// Piece k (8 values) of row i of a swizzled tile of 64 columns.
+__device__ __forceinline__ uint4* small_piece(unsigned char* base, int i, int col) {
+    return reinterpret_cast<uint4*>(base + (col >> 6) * Small::kAtom + i * 128 +
+                                    ((((col & 63) >> 3) ^ (i & 7)) * 16));
+}
+__device__ __forceinline__ unsigned short* small_value(unsigned char* base, int i, int col) {
+    return reinterpret_cast<unsigned short*>(small_piece(base, i, col)) + (col & 7);
+}
+__device__ __forceinline__ void load_pieces(unsigned char* base, int i, int col, gemm::Chunk16& x) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x.u[k] = *small_piece(base, i, col + 8 * k);
+}
+__device__ __forceinline__ void store_pieces(unsigned char* base, int i, int col,
+                                             const gemm::Chunk16& x) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *small_piece(base, i, col + 8 * k) = x.u[k];
+}
+
+__device__ __forceinline__ uint64_t small_desc(unsigned addr, unsigned lead_bytes) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(lead_bytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void store_remote(unsigned at, uint4 v) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void store_remote(unsigned at, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
+// hi + lo with hi = x rounded to fp16.
+__device__ __forceinline__ void split_halves(const float (&x)[32], gemm::Chunk16& hi,
+                                             gemm::Chunk16& lo) {
+    hi = gemm::packed_row(x, __half());
+    float rest[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 h = gemm::pair_at(hi, i, __half());
+        rest[2 * i] = x[2 * i] - h.x;
+        rest[2 * i + 1] = x[2 * i + 1] - h.y;
+    }
+    lo = gemm::packed_row(rest, __half());
+}
+
+__global__ void __launch_bounds__(Small::kThreads, 1)
+ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
+    using S = Small;
+    extern __shared__ unsigned char smem_raw[];
+    const unsigned base = (gemm::smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char* const gen = smem_raw + (base - gemm::smem_u32(smem_raw));
+    unsigned char *const hi = gen + S::kHi, *const lo = gen + S::kLo, *const o = gen + S::kO;
+    float4* const parts = reinterpret_cast<float4*>(gen + S::kParts);
+    float* const d_a = reinterpret_cast<float*>(gen + S::kVectors);
+    float *const d_b = d_a + 128, *const norms = d_a + 256, *const sums = d_a + 264;
+    const unsigned bar = base + S::kBar;
+    unsigned* const tmem_slot = reinterpret_cast<unsigned*>(gen + S::kBar + 8);
+    volatile int* const dead = reinterpret_cast<volatile int*>(gen + S::kBar + 12);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)gemm::cluster_rank(), b = blockIdx.x / ranks;
+    const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+    const int j0 = rank * p.width, across = max(0, min(p.width, p.c - j0));
+
+    if (threadIdx.x == 0) {
+        gemm::mbar_init(bar, 1);
+        *dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) gemm::tmem_alloc<1>(gemm::smem_u32(tmem_slot), S::kTmemCols);
+    gemm::tcgen05_fence_before();
+    gemm::cluster_sync_all();
+    gemm::tcgen05_fence_after();
+    const unsigned tmem = *tmem_slot;
+    const unsigned lanes = tmem + ((unsigned)(quarter * 32) << 16);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- the update's values, as raw 32-bit floats in two 16-bit halves
+    float sum = 0.0f;
+    {
+        const int vecs = p.tall ? 32 : p.width / 4;
+        const int total = p.tall ? p.width * 32 : 128 * vecs;
+#pragma unroll 4
+        for (int at = threadIdx.x; at < total; at += S::kThreads) {
+            const int line = at / vecs, first = (at - line * vecs) * 4;
+            const int n = min(4, (p.tall ? p.r : across) - first);
+            const bool in = line < (p.tall ? across : p.r) && n > 0;
+            float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in) {
+                const long long grow = p.tall ? j0 + line : line;
+                const int gcol = p.tall ? first : j0 + first;
+                const float4 g = gemm::view_load(p.g, b, grow, gcol, n);
+                u = g;
+                if (p.has_momentum) {
+                    float4 m = gemm::view_load(p.m, b, grow, gcol, n);
+                    m = make_float4(fmaf(p.beta, m.x, g.x), fmaf(p.beta, m.y, g.y),
+                                    fmaf(p.beta, m.z, g.z), fmaf(p.beta, m.w, g.w));
+                    gemm::view_store(p.m, b, grow, gcol, n, m);
+                    if (!p.m.f32) {  // what was stored
+                        m.x = __bfloat162float(__float2bfloat16(m.x));
+                        m.y = __bfloat162float(__float2bfloat16(m.y));
+                        m.z = __bfloat162float(__float2bfloat16(m.z));
+                        m.w = __bfloat162float(__float2bfloat16(m.w));
+                    }
+                    u = p.nesterov ? make_float4(fmaf(p.beta, m.x, g.x), fmaf(p.beta, m.y, g.y),
+                                                 fmaf(p.beta, m.z, g.z), fmaf(p.beta, m.w, g.w))
+                                   : m;
+                }
+                sum += u.x * u.x + u.y * u.y + u.z * u.z + u.w * u.w;
+            }
+            const unsigned w[4] = {__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z),
+                                   __float_as_uint(u.w)};
+            if (p.tall) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    *small_value(hi, first + k, line) = (unsigned short)(w[k] >> 16);
+                    *small_value(lo, first + k, line) = (unsigned short)w[k];
+                }
+            } else {
+                *reinterpret_cast<uint2*>(small_value(hi, line, first)) =
+                    make_uint2((w[0] >> 16) | (w[1] & 0xFFFF0000u), (w[2] >> 16) | (w[3] & 0xFFFF0000u));
+                *reinterpret_cast<uint2*>(small_value(lo, line, first)) =
+                    make_uint2((w[0] & 0xFFFFu) | (w[1] << 16), (w[2] & 0xFFFFu) | (w[3] << 16));
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x < ranks) {
+        float s = 0.0f;
+        for (int w = 0; w < 8; ++w) s += sums[w];
+        store_remote(gemm::map_rank(gemm::smem_u32(norms + rank), threadIdx.x), s);
+    }
+    gemm::cluster_sync_all();
+    float square = 0.0f;
+    for (int i = 0; i < ranks; ++i) square += norms[i];
+    const float to_x = p.size / (sqrtf(square) + p.eps);
+
+    // ---- X_0, in place
+    const int chunks = p.width / 32;
+    for (int c = half; c < chunks; c += 2) {
+        gemm::Chunk16 h, l;
+        load_pieces(hi, row, 32 * c, h);
+        load_pieces(lo, row, 32 * c, l);
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const unsigned hw = gemm::word_of(h, i), lw = gemm::word_of(l, i);
+            x[2 * i] = __uint_as_float((hw << 16) | (lw & 0xFFFFu)) * to_x;
+            x[2 * i + 1] = __uint_as_float((hw & 0xFFFF0000u) | (lw >> 16)) * to_x;
+        }
+        split_halves(x, h, l);
+        store_pieces(hi, row, 32 * c, h);
+        store_pieces(lo, row, 32 * c, l);
+    }
+
+    const unsigned square_desc = gemm::instruction_desc(false, false, false, 128, 128);
+    const unsigned update_desc = gemm::instruction_desc(false, false, true, 128, p.width);
+    const float to_a = 1.0f / (p.size * p.size);
+    const int kuse = (p.r + 15) / 16;  // 16-deep steps over X's rows that are not padding
+    unsigned phase = 0;
+    // After the block's writes to shared memory: makes them visible to the
+    // matrix instructions that `issue` starts, and waits for these.
+    auto multiply = [&](auto issue) {
+        fence_async();
+        gemm::tcgen05_fence_before();
+        __syncthreads();
+        if (warp == 0) {
+            gemm::tcgen05_fence_after();
+            if (gemm::elect_one()) {
+                fence_async();
+                issue();
+                gemm::mma_commit<1>(bar);
+            }
+            __syncwarp();
+        }
+        gemm::warp_wait(bar, phase, dead);
+        phase ^= 1;
+        gemm::tcgen05_fence_after();
+    };
+
+    for (int step = 0; step < p.steps; ++step) {
+        // ---- A = X X^T
+        multiply([&] {
+            for (int k = 0; k < p.width / 16; ++k) {
+                const uint64_t d = small_desc(base + S::kHi + (k >> 2) * S::kAtom + (k & 3) * 32, 16);
+                gemm::mma_f16<1>(tmem, d, d, square_desc, k > 0);
+            }
+        });
+        // chunks of A: the diagonal in 32 bits, the rest in fp16
+        auto finish_chunk = [&](float (&v)[32], int i, int col0, gemm::Chunk16& out, float& diag) {
+            diag = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                v[j] *= to_a;
+                if (i == col0 + j) {
+                    diag = v[j];
+                    v[j] = 0.0f;
+                }
+            }
+            out = gemm::packed_row(v, __half());
+        };
+        for (int h = 0; h < 2; ++h) {
+            const int cc = half * 2 + h;  // chunk column
+            float v[32];
+            gemm::tmem_load32(lanes + 32 * cc, v);
+            if (ranks == 1) {
+                gemm::Chunk16 out;
+                float diag;
+                finish_chunk(v, row, 32 * cc, out, diag);
+                store_pieces(o, row, 32 * cc, out);
+                if (cc == quarter) d_a[row] = diag;
+            } else {
+                const int u = cc * 4 + quarter, owner = u % ranks, k = u / ranks;
+                const unsigned at = gemm::map_rank(
+                    gemm::smem_u32(parts + (k * ranks + rank) * 256 + lane), owner);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    store_remote(at + j * 512,
+                                 make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                            __float_as_uint(v[4 * j + 2]),
+                                            __float_as_uint(v[4 * j + 3])));
+            }
+        }
+        if (ranks > 1) {
+            gemm::cluster_sync_all();
+            for (int k = warp, u; (u = rank + ranks * k) < 16; k += 8) {
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                for (int from = 0; from < ranks; ++from) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 x = parts[(k * ranks + from) * 256 + j * 32 + lane];
+                        v[4 * j] += x.x;
+                        v[4 * j + 1] += x.y;
+                        v[4 * j + 2] += x.z;
+                        v[4 * j + 3] += x.w;
+                    }
+                }
+                const int i = (u & 3) * 32 + lane, col0 = (u >> 2) * 32;
+                gemm::Chunk16 out;
+                float diag;
+                finish_chunk(v, i, col0, out, diag);
+                for (int to = 0; to < ranks; ++to) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        store_remote(gemm::map_rank(gemm::smem_u32(small_piece(o, i, col0 + 8 * q)), to),
+                                     out.u[q]);
+                    if ((u & 3) == (u >> 2))
+                        store_remote(gemm::map_rank(gemm::smem_u32(d_a + i), to), diag);
+                }
+            }
+            fence_async();
+            gemm::cluster_sync_all();
+        }
+
+        // ---- B = b A + c A^2, over A's place
+        multiply([&] {
+            for (int k = 0; k < 8; ++k) {
+                const uint64_t d = small_desc(base + S::kO + (k >> 2) * S::kAtom + (k & 3) * 32, 16);
+                gemm::mma_f16<1>(tmem, d, d, square_desc, k > 0);
+            }
+        });
+        const float di = d_a[row];
+        for (int h = 0; h < 2; ++h) {
+            const int cc = half * 2 + h;
+            float v[32];
+            gemm::tmem_load32(lanes + 32 * cc, v);
+            gemm::Chunk16 a;
+            load_pieces(o, row, 32 * cc, a);
+            if (cc == quarter) {
+                float d = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    if (lane == j) {
+                        d = v[j];
+                        v[j] = 0.0f;
+                    }
+                }
+                d_b[row] = p.cb * di + p.cc * (di * di + d);
+            }
+            const float k0 = fmaf(p.cc, di, p.cb);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 x = gemm::pair_at(a, i, __half());
+                const float2 dj = *reinterpret_cast<const float2*>(d_a + 32 * cc + 2 * i);
+                v[2 * i] = fmaf(fmaf(p.cc, dj.x, k0), x.x, p.cc * v[2 * i]);
+                v[2 * i + 1] = fmaf(fmaf(p.cc, dj.y, k0), x.y, p.cc * v[2 * i + 1]);
+            }
+            store_pieces(o, row, 32 * cc, gemm::packed_row(v, __half()));
+        }
+
+        // ---- X <- (a + diag B) X + offdiag(B) X
+        multiply([&] {
+            for (int k = 0; k < kuse; ++k) {
+                const uint64_t da = small_desc(base + S::kO + (k >> 2) * S::kAtom + (k & 3) * 32, 16);
+                const uint64_t db = small_desc(base + S::kHi + k * 2048, S::kAtom);
+                gemm::mma_f16<1>(tmem + 128, da, db, update_desc, k > 0);
+            }
+        });
+        const float kx = p.ca + d_b[row];
+        for (int c = half; c < chunks; c += 2) {
+            float v[32];
+            gemm::tmem_load32(lanes + 128 + 32 * c, v);
+            gemm::Chunk16 h, l;
+            load_pieces(hi, row, 32 * c, h);
+            load_pieces(lo, row, 32 * c, l);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 a = gemm::pair_at(h, i, __half()), r = gemm::pair_at(l, i, __half());
+                v[2 * i] = fmaf(kx, a.x + r.x, v[2 * i]);
+                v[2 * i + 1] = fmaf(kx, a.y + r.y, v[2 * i + 1]);
+            }
+            if (step + 1 < p.steps) {
+                split_halves(v, h, l);
+                store_pieces(hi, row, 32 * c, h);
+                store_pieces(lo, row, 32 * c, l);
+            } else {
+                // (the parts' buffer is free: no block sends to another any more)
+                gemm::Place q;
+                q.b = b;
+                q.row0 = quarter * 32;
+                q.col0 = j0 + 32 * c;
+                q.M = p.r;
+                q.N = p.c;
+                q.lane = lane;
+                q.off = false;
+                q.stage = gen + S::kParts + warp * gemm::kWarpStage;
+                if (q.row0 >= q.M || q.col0 >= q.N) continue;
+                if (p.weights) {
+                    float w[32];
+                    if (p.tall)
+                        gemm::get_columns(p.out, q, w);
+                    else
+                        gemm::get_rows(p.out, q, w);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = fmaf(p.keep, w[j], p.scale * v[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= p.scale;
+                }
+                if (p.tall)
+                    gemm::put_columns(p.out, q, v);
+                else
+                    gemm::put_rows(p.out, q, v);
+            }
+        }
+    }
+    gemm::tcgen05_fence_before();
+    __syncthreads();
+    gemm::tcgen05_fence_after();
+    gemm::bury(dead, p.timeouts);
+    if (warp == 1) gemm::tmem_free<1>(tmem, S::kTmemCols);
+}
+
+// Blocks of a cluster for a larger side of c: 0 where eight do not hold it.
+inline int small_ranks(long long r, long long c) {
+    if (r > Small::kRows) return 0;
+    for (int ranks = 1; ranks <= Small::kMaxRanks; ranks *= 2)
+        if (c <= (long long)ranks * Small::kMaxWidth) return ranks;
+    return 0;
+}
+
+inline cudaError_t launch_small(SmallParams p, long long batch, int ranks, cudaStream_t st) {
+    p.width = ((p.c + ranks - 1) / ranks + 63) / 64 * 64;
+    p.timeouts = gemm::timeout_counter();
+    if (p.timeouts == nullptr) return cudaErrorInvalidConfiguration;
+    return gemm::launch_cluster(ns_small_kernel, (int)batch * ranks, Small::kThreads, ranks,
+                                Small::kSmem, st, p, ranks);
+}
+
+}  // namespace train
+}  // namespace vc

@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <math.h>
 
+#include "vc_ns_small.cuh"
 #include "vc_train_common.cuh"
 
 namespace vc {
@@ -361,6 +362,28 @@ cudaError_t iterate(const Layout& l, long long batch, long long rows, long long 
     int e2 = 0;  // X is stored times 2^e2, about sqrt(c)
     while (e2 < 12 && (1ll << (2 * e2)) < l.c) ++e2;
     const float size = (float)(1 << e2);
+    if (const int ranks = small_ranks(l.r, l.c)) {
+        SmallParams sp = {};
+        sp.g = p.g;
+        sp.m = p.m;
+        sp.out = fin.out;
+        sp.has_momentum = p.has_momentum;
+        sp.nesterov = p.nesterov;
+        sp.weights = fin.weights;
+        sp.tall = tall;
+        sp.r = (int)l.r;
+        sp.c = (int)l.c;
+        sp.steps = ns.steps;
+        sp.beta = p.beta;
+        sp.eps = ns.eps;
+        sp.ca = ns.a;
+        sp.cb = ns.b;
+        sp.cc = ns.c;
+        sp.size = size;
+        sp.keep = fin.keep;
+        sp.scale = fin.scale / size;
+        return launch_small(sp, batch, ranks, st);
+    }
     __half* x[2] = {reinterpret_cast<__half*>(ws + l.hi0), reinterpret_cast<__half*>(ws + l.hi1)};
     __half *const lo = reinterpret_cast<__half*>(ws + l.lo), *const oa = reinterpret_cast<__half*>(ws + l.a),
                   *const ob = reinterpret_cast<__half*>(ws + l.b);
