@@ -387,18 +387,38 @@ struct View {
     int vec;  // four values starting at a column that is a multiple of four are one aligned vector
     int vec16;  // rows are on 16 bytes
 };
+// Value by value, out of line: the code of the common case stays short, which
+// counts where a kernel runs it once (instructions come from L2 then).
+static __device__ __noinline__ float4 load_few(const void* p, int f32, int n) {
+    return f32 ? load4(static_cast<const float*>(p), n, false)
+               : load4(static_cast<const __nv_bfloat16*>(p), n, false);
+}
+static __device__ __noinline__ void store_few(void* p, int f32, int n, float4 x) {
+    if (f32)
+        store4(static_cast<float*>(p), x, n, false);
+    else
+        store4(static_cast<__nv_bfloat16*>(p), x, n, false);
+}
+// n <= 4 values of a row.
 __device__ __forceinline__ float4 view_load(const View& v, int b, long long row, int col, int n) {
-    const long long at = (long long)b * v.batch_stride + row * v.ld + col;
-    return v.f32 ? load4(static_cast<const float*>(v.data) + at, n, v.vec)
-                 : load4(static_cast<const __nv_bfloat16*>(v.data) + at, n, v.vec);
+    const char* p = static_cast<const char*>(v.data) +
+                    (((long long)b * v.batch_stride + row * v.ld + col) << (v.f32 ? 2 : 1));
+    if (!v.vec || n < 4) return load_few(p, v.f32, n);
+    if (v.f32) return *reinterpret_cast<const float4*>(p);
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
 }
 __device__ __forceinline__ void view_store(const View& v, int b, long long row, int col, int n,
                                            float4 x) {
-    const long long at = (long long)b * v.batch_stride + row * v.ld + col;
-    if (v.f32)
-        store4(static_cast<float*>(v.data) + at, x, n, v.vec);
+    char* p = static_cast<char*>(v.data) +
+              (((long long)b * v.batch_stride + row * v.ld + col) << (v.f32 ? 2 : 1));
+    if (!v.vec || n < 4)
+        store_few(p, v.f32, n, x);
+    else if (v.f32)
+        store4(reinterpret_cast<float*>(p), x, 4, true);
     else
-        store4(static_cast<__nv_bfloat16*>(v.data) + at, x, n, v.vec);
+        store4(reinterpret_cast<__nv_bfloat16*>(p), x, 4, true);
 }
 
 // ------------------------------------------------------------- epilogues --

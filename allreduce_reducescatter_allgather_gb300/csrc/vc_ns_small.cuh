@@ -36,11 +36,11 @@ struct SmallParams {
 };
 
 struct Small {
-    static constexpr int kThreads = 256, kMaxWidth = 256, kMaxRanks = 8, kRows = 128;
+    static constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxWidth = 256, kMaxRanks = 8, kRows = 128;
     static constexpr int kAtom = 128 * 128;  // bytes of 64 columns
     static constexpr int kHi = 0, kLo = 4 * kAtom, kO = 8 * kAtom, kParts = 10 * kAtom;
     static constexpr int kVectors = 14 * kAtom;  // diagonals of A and B, norms, sums
-    static constexpr int kBar = kVectors + 1024 + 128;
+    static constexpr int kBar = kVectors + 1024 + 192;
     static constexpr int kSmem = 1024 + kBar + 64;
     static constexpr int kTmemCols = 512;  // 128 for A and A^2, up to 256 for B X
     static_assert(kSmem <= gemm::kSmemPerBlock, "shared memory");
@@ -94,6 +94,18 @@ __device__ __forceinline__ void split_halves(const float (&x)[32], gemm::Chunk16
     lo = gemm::packed_row(rest, __half());
 }
 
+// beta m + g, of the momentum; with the new momentum for m, the Nesterov update.
+__device__ __forceinline__ float4 new_momentum(float beta, float4 g, float4 m) {
+    return make_float4(fmaf(beta, m.x, g.x), fmaf(beta, m.y, g.y), fmaf(beta, m.z, g.z),
+                       fmaf(beta, m.w, g.w));
+}
+// The value that a store into the matrix leaves there.
+__device__ __forceinline__ float4 as_stored(const gemm::View& v, float4 x) {
+    if (v.f32) return x;
+    return make_float4(__bfloat162float(__float2bfloat16(x.x)), __bfloat162float(__float2bfloat16(x.y)),
+                       __bfloat162float(__float2bfloat16(x.z)), __bfloat162float(__float2bfloat16(x.w)));
+}
+
 __global__ void __launch_bounds__(Small::kThreads, 1)
 ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
     using S = Small;
@@ -110,7 +122,8 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)gemm::cluster_rank(), b = blockIdx.x / ranks;
-    const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+    // a warp reads the tensor-memory lanes of its quarter; four warps share its columns
+    const int quarter = warp & 3, share = warp >> 2, row = quarter * 32 + lane;
     const int j0 = rank * p.width, across = max(0, min(p.width, p.c - j0));
 
     if (threadIdx.x == 0) {
@@ -130,36 +143,51 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
     // ---- the update's values, as raw 32-bit floats in two 16-bit halves
     float sum = 0.0f;
     {
+        // Groups of four values: `line` is a row of the stored matrix, `first` the
+        // group's place in it.  A warp takes neighbouring groups of a line; of
+        // a tall matrix, whose lines are X's columns, eight groups of four
+        // lines, since its values go to 32 rows of X and all of one column
+        // would meet in two of the memory's banks.  All loads of a batch come
+        // before its first store, so that a batch waits once.
         const int vecs = p.tall ? 32 : p.width / 4;
-        const int total = p.tall ? p.width * 32 : 128 * vecs;
-#pragma unroll 4
-        for (int at = threadIdx.x; at < total; at += S::kThreads) {
-            const int line = at / vecs, first = (at - line * vecs) * 4;
-            const int n = min(4, (p.tall ? p.r : across) - first);
-            const bool in = line < (p.tall ? across : p.r) && n > 0;
-            float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (in) {
-                const long long grow = p.tall ? j0 + line : line;
-                const int gcol = p.tall ? first : j0 + first;
-                const float4 g = gemm::view_load(p.g, b, grow, gcol, n);
-                u = g;
-                if (p.has_momentum) {
-                    float4 m = gemm::view_load(p.m, b, grow, gcol, n);
-                    m = make_float4(fmaf(p.beta, m.x, g.x), fmaf(p.beta, m.y, g.y),
-                                    fmaf(p.beta, m.z, g.z), fmaf(p.beta, m.w, g.w));
-                    gemm::view_store(p.m, b, grow, gcol, n, m);
-                    if (!p.m.f32) {  // what was stored
-                        m.x = __bfloat162float(__float2bfloat16(m.x));
-                        m.y = __bfloat162float(__float2bfloat16(m.y));
-                        m.z = __bfloat162float(__float2bfloat16(m.z));
-                        m.w = __bfloat162float(__float2bfloat16(m.w));
-                    }
-                    u = p.nesterov ? make_float4(fmaf(p.beta, m.x, g.x), fmaf(p.beta, m.y, g.y),
-                                                 fmaf(p.beta, m.z, g.z), fmaf(p.beta, m.w, g.w))
-                                   : m;
-                }
-                sum += u.x * u.x + u.y * u.y + u.z * u.z + u.w * u.w;
+        const int lines = p.tall ? p.width : S::kRows;
+        const int lines_in = p.tall ? across : p.r, cols_in = p.tall ? p.r : across;
+        const int row_at = p.tall ? j0 : 0, col_at = p.tall ? 0 : j0;
+        const int dline = p.tall ? S::kWarps : S::kThreads / vecs;
+        const int dvec = p.tall ? 0 : S::kThreads % vecs;
+        int line0 = p.tall ? (warp >> 2) * 4 + (lane >> 3) : threadIdx.x / vecs;
+        int vec0 = p.tall ? (warp & 3) * 8 + (lane & 7) : threadIdx.x % vecs;
+        constexpr int kBatch = 8;
+#pragma unroll 1
+        while (line0 < lines) {
+          float4 gs[kBatch], ms[kBatch];
+          int ls[kBatch], fs[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            ls[k] = line0;
+            fs[k] = vec0 * 4;
+            line0 += dline;
+            vec0 += dvec;
+            if (vec0 >= vecs) vec0 -= vecs, ++line0;
+            gs[k] = ms[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (ls[k] < lines_in && fs[k] < cols_in) {
+                const int n = min(4, cols_in - fs[k]);
+                gs[k] = gemm::view_load(p.g, b, row_at + ls[k], col_at + fs[k], n);
+                if (p.has_momentum) ms[k] = gemm::view_load(p.m, b, row_at + ls[k], col_at + fs[k], n);
             }
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int line = ls[k], first = fs[k];
+            if (line >= lines) continue;
+            float4 u = gs[k];
+            if (p.has_momentum && line < lines_in && first < cols_in) {
+                float4 m = new_momentum(p.beta, gs[k], ms[k]);
+                gemm::view_store(p.m, b, row_at + line, col_at + first, min(4, cols_in - first), m);
+                m = as_stored(p.m, m);
+                u = p.nesterov ? new_momentum(p.beta, gs[k], m) : m;
+            }
+            sum += u.x * u.x + u.y * u.y + u.z * u.z + u.w * u.w;  // 0 outside
             const unsigned w[4] = {__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z),
                                    __float_as_uint(u.w)};
             if (p.tall) {
@@ -174,6 +202,7 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
                 *reinterpret_cast<uint2*>(small_value(lo, line, first)) =
                     make_uint2((w[0] & 0xFFFFu) | (w[1] << 16), (w[2] & 0xFFFFu) | (w[3] << 16));
             }
+          }
         }
     }
 #pragma unroll
@@ -182,7 +211,7 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
     __syncthreads();
     if (threadIdx.x < ranks) {
         float s = 0.0f;
-        for (int w = 0; w < 8; ++w) s += sums[w];
+        for (int w = 0; w < S::kWarps; ++w) s += sums[w];
         store_remote(gemm::map_rank(gemm::smem_u32(norms + rank), threadIdx.x), s);
     }
     gemm::cluster_sync_all();
@@ -192,7 +221,7 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
 
     // ---- X_0, in place
     const int chunks = p.width / 32;
-    for (int c = half; c < chunks; c += 2) {
+    for (int c = share; c < chunks; c += 4) {
         gemm::Chunk16 h, l;
         load_pieces(hi, row, 32 * c, h);
         load_pieces(lo, row, 32 * c, l);
@@ -254,8 +283,8 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
             }
             out = gemm::packed_row(v, __half());
         };
-        for (int h = 0; h < 2; ++h) {
-            const int cc = half * 2 + h;  // chunk column
+        {
+            const int cc = share;  // chunk column
             float v[32];
             gemm::tmem_load32(lanes + 32 * cc, v);
             if (ranks == 1) {
@@ -278,7 +307,7 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
         }
         if (ranks > 1) {
             gemm::cluster_sync_all();
-            for (int k = warp, u; (u = rank + ranks * k) < 16; k += 8) {
+            for (int k = warp, u; (u = rank + ranks * k) < 16; k += S::kWarps) {
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 0.0f;
@@ -316,9 +345,9 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
                 gemm::mma_f16<1>(tmem, d, d, square_desc, k > 0);
             }
         });
-        const float di = d_a[row];
-        for (int h = 0; h < 2; ++h) {
-            const int cc = half * 2 + h;
+        {
+            const float di = d_a[row];
+            const int cc = share;
             float v[32];
             gemm::tmem_load32(lanes + 32 * cc, v);
             gemm::Chunk16 a;
@@ -354,7 +383,7 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
             }
         });
         const float kx = p.ca + d_b[row];
-        for (int c = half; c < chunks; c += 2) {
+        for (int c = share; c < chunks; c += 4) {
             float v[32];
             gemm::tmem_load32(lanes + 128 + 32 * c, v);
             gemm::Chunk16 h, l;

@@ -204,7 +204,7 @@ constexpr int kDzRows = 4;  // rows that a thread loads before it uses them
 // 256 columns (8 per lane); the block's eight warps take groups of rows in
 // turn.
 template <int kFamily>
-__global__ void __launch_bounds__(256) dz_kernel(const __grid_constant__ DzParams p) {
+__global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzParams p) {
     __shared__ float4 part[8][64];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -305,11 +305,11 @@ __global__ void __launch_bounds__(256) db_kernel(const float* sums, int parts, l
     }
 }
 
-// Blocks along the rows: enough for eight blocks per SM, each with a group of
-// rows for every warp.
+// Blocks along the rows: enough for the three blocks per SM that fit, each with
+// a group of rows at least for every warp.
 int dz_row_blocks(long long rows, long long cols) {
     const long long across = (cols + 255) / 256;
-    const long long want = (152 * 8 + across - 1) / across;
+    const long long want = (152 * 3 + across - 1) / across;
     return (int)std::max(1ll, std::min(want, (rows + 8 * kDzRows - 1) / (8 * kDzRows)));
 }
 

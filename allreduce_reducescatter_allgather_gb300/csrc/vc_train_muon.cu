@@ -51,12 +51,33 @@ struct PrepareParams {
     int rows, cols, vpr;         // vpr: groups of four columns per row
 };
 
-// The update's values: g, or the momentum, or g + beta momentum.
+// Groups of four columns that a thread loads before it stores the first.
+constexpr int kPrepareBatch = 4;
+
+struct Loaded {
+    float4 g, m;
+    unsigned row;
+    int col, n;  // n: columns of the group, 0 beyond the matrix
+};
+__device__ __forceinline__ void load_batch(const PrepareParams& p, int b, unsigned first,
+                                           Loaded (&x)[kPrepareBatch]) {
+    const unsigned total = (unsigned)p.rows * (unsigned)p.vpr;
+#pragma unroll
+    for (int k = 0; k < kPrepareBatch; ++k) {
+        const unsigned i = first + k * gridDim.x * 256;
+        x[k].g = x[k].m = make_float4(0.f, 0.f, 0.f, 0.f);
+        x[k].n = 0;
+        if (i >= total) continue;
+        x[k].row = i / (unsigned)p.vpr;
+        x[k].col = (int)(i - x[k].row * (unsigned)p.vpr) * 4;
+        x[k].n = min(4, p.cols - x[k].col);
+        x[k].g = gemm::view_load(p.g, b, x[k].row, x[k].col, x[k].n);
+        if (p.has_momentum) x[k].m = gemm::view_load(p.m, b, x[k].row, x[k].col, x[k].n);
+    }
+}
+// The update's value, m being the new momentum.
 __device__ __forceinline__ float4 update_of(const PrepareParams& p, float4 g, float4 m) {
-    if (!p.has_momentum) return g;
-    if (!p.nesterov) return m;
-    return make_float4(fmaf(p.beta, m.x, g.x), fmaf(p.beta, m.y, g.y), fmaf(p.beta, m.z, g.z),
-                       fmaf(p.beta, m.w, g.w));
+    return !p.has_momentum ? g : p.nesterov ? new_momentum(p.beta, g, m) : m;
 }
 
 __device__ __forceinline__ float block_sum(float v, float* tmp) {
@@ -71,10 +92,6 @@ __device__ __forceinline__ float block_sum(float v, float* tmp) {
     return s;
 }
 
-__device__ __forceinline__ float rounded(const View& v, float x) {
-    return v.f32 ? x : __bfloat162float(__float2bfloat16(x));
-}
-
 // M <- beta M + G, and this block's part of the sum of the update's squares.
 __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ PrepareParams p) {
     __shared__ float tmp[8];
@@ -83,22 +100,21 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ P
     const unsigned total = (unsigned)p.rows * (unsigned)p.vpr;
     const int b = blockIdx.y;
     float sum = 0.0f;
-    for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
-        const unsigned row = i / (unsigned)p.vpr;
-        const int col = (int)(i - row * (unsigned)p.vpr) * 4, n = min(4, p.cols - col);
-        const float4 g = gemm::view_load(p.g, b, row, col, n);
-        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.has_momentum) {
-            m = gemm::view_load(p.m, b, row, col, n);
-            m = make_float4(fmaf(p.beta, m.x, g.x), fmaf(p.beta, m.y, g.y),
-                            fmaf(p.beta, m.z, g.z), fmaf(p.beta, m.w, g.w));
-            gemm::view_store(p.m, b, row, col, n, m);
-            // the second pass reads what was stored
-            m = make_float4(rounded(p.m, m.x), rounded(p.m, m.y), rounded(p.m, m.z),
-                            rounded(p.m, m.w));
+    for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < total; i += kPrepareBatch * gridDim.x * 256) {
+        Loaded x[kPrepareBatch];
+        load_batch(p, b, i, x);
+#pragma unroll
+        for (int k = 0; k < kPrepareBatch; ++k) {
+            if (x[k].n == 0) continue;
+            float4 m = x[k].m;
+            if (p.has_momentum) {
+                m = new_momentum(p.beta, x[k].g, m);
+                gemm::view_store(p.m, b, x[k].row, x[k].col, x[k].n, m);
+                m = as_stored(p.m, m);
+            }
+            const float4 u = update_of(p, x[k].g, m);  // zero beyond n
+            sum += u.x * u.x + u.y * u.y + u.z * u.z + u.w * u.w;
         }
-        const float4 u = update_of(p, g, m);  // zero beyond n
-        sum += u.x * u.x + u.y * u.y + u.z * u.z + u.w * u.w;
     }
     sum = block_sum(sum, tmp);
     if (threadIdx.x == 0) p.parts[b * gridDim.x + blockIdx.x] = sum;
@@ -115,19 +131,21 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Prep
     float sum = 0.0f;
     for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) sum += p.parts[b * gridDim.x + i];
     const float scale = p.size / (sqrtf(block_sum(sum, tmp)) + p.eps);
-    for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
-        const unsigned row = i / (unsigned)p.vpr;
-        const int col = (int)(i - row * (unsigned)p.vpr) * 4, n = min(4, p.cols - col);
-        const float4 g = gemm::view_load(p.g, b, row, col, n);
-        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.has_momentum) m = gemm::view_load(p.m, b, row, col, n);
-        float4 u = update_of(p, g, m);
-        u = make_float4(u.x * scale, u.y * scale, u.z * scale, u.w * scale);
-        const long long at = (long long)b * p.batch_stride + (long long)row * p.ld + col;
-        const float4 hi = make_float4(__half2float(__float2half_rn(u.x)), __half2float(__float2half_rn(u.y)),
-                                      __half2float(__float2half_rn(u.z)), __half2float(__float2half_rn(u.w)));
-        gemm::store4(p.hi + at, hi, n, true);
-        gemm::store4(p.lo + at, make_float4(u.x - hi.x, u.y - hi.y, u.z - hi.z, u.w - hi.w), n, true);
+    for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < total; i += kPrepareBatch * gridDim.x * 256) {
+        Loaded x[kPrepareBatch];
+        load_batch(p, b, i, x);
+#pragma unroll
+        for (int k = 0; k < kPrepareBatch; ++k) {
+            if (x[k].n == 0) continue;
+            float4 u = update_of(p, x[k].g, x[k].m);
+            u = make_float4(u.x * scale, u.y * scale, u.z * scale, u.w * scale);
+            const long long at = (long long)b * p.batch_stride + (long long)x[k].row * p.ld + x[k].col;
+            const float2 h01 = __half22float2(__floats2half2_rn(u.x, u.y));
+            const float2 h23 = __half22float2(__floats2half2_rn(u.z, u.w));
+            gemm::store4(p.hi + at, make_float4(h01.x, h01.y, h23.x, h23.y), x[k].n, true);
+            gemm::store4(p.lo + at, make_float4(u.x - h01.x, u.y - h01.y, u.z - h23.x, u.w - h23.y),
+                         x[k].n, true);
+        }
     }
 }
 
@@ -332,7 +350,7 @@ bool layout_of(long long batch, long long rows, long long cols, Layout* l) {
     l->ldr = (l->r + 31) / 32 * 32;
     l->xs = rows * l->ldx;
     l->as = l->r * l->ldr;
-    const long long want = (rows * vpr + 1023) / 1024, fit = std::max(1ll, 152 * 8 / std::max(1ll, batch));
+    const long long want = (rows * vpr + 256 * kPrepareBatch - 1) / (256 * kPrepareBatch), fit = std::max(1ll, 152 * 8 / std::max(1ll, batch));
     l->parts = (int)std::max(1ll, std::min({want, fit, (long long)kMaxParts}));
     const size_t x = round256((size_t)batch * l->xs * 2), a = round256((size_t)batch * l->as * 2);
     const size_t d = round256((size_t)batch * l->r * 4);
