@@ -1,6 +1,7 @@
 // The linear layer with bias, activation and residual in its epilogue, and
 // its gradient.
 #include <algorithm>
+#include <type_traits>
 
 #include "vc_train_common.cuh"
 
@@ -19,20 +20,29 @@ using gemm::Place;
 
 // y = act(acc + bias) + residual; z = acc + bias kept on request.  kSwap: the
 // product is the transposed one, W x^T, so that a chunk's rows are y's columns.
-template <int kFamily, bool kSwap>
+template <int kFamily, bool kSwap, bool kResidual>
 struct EpiForward {
     static constexpr bool kSym = false;
     struct Params {
         const __nv_bfloat16* bias;
         View residual, y, preact;
-        int has_residual, has_preact, bias_vec;
+        int has_preact, bias_vec;
         Act act;
     };
-    struct Pre {
+    struct WithResidual {
         gemm::Chunk16 residual;  // as loaded, across the rows
-        gemm::Chunk16 bias;      // of the chunk's columns, the same in every lane
-        float one_bias;          // else: of the lane's column (kSwap: row)
     };
+    struct Without {};
+    struct Pre : std::conditional_t<kResidual && !kSwap, WithResidual, Without> {
+        gemm::Chunk16 bias;  // of the chunk's columns, the same in every lane
+        float one_bias;      // else: of the lane's column (kSwap: row)
+    };
+    __device__ static void add_residual(const Params& p, const Place& q, float (&v)[32]) {
+        float r[32];
+        kSwap ? get_columns(p.residual, q, r) : get_rows(p.residual, q, r);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += r[j];
+    }
     __device__ static bool bias_in_pieces(const Params& p, const Place& q) {
         return !kSwap && p.bias_vec && q.whole();
     }
@@ -47,9 +57,12 @@ struct EpiForward {
                 pre.one_bias = at < (kSwap ? q.M : q.N) ? __bfloat162float(p.bias[at]) : 0.0f;
             }
         }
-        if (!kSwap && p.has_residual && in_pieces(p.residual, q))
-            load_across(static_cast<const __nv_bfloat16*>(p.residual.data) + corner_of(p.residual, q),
-                        p.residual.ld * 2, q, pre.residual);
+        if constexpr (kResidual && !kSwap) {
+            if (in_pieces(p.residual, q))
+                load_across(static_cast<const __nv_bfloat16*>(p.residual.data) +
+                                corner_of(p.residual, q),
+                            p.residual.ld * 2, q, pre.residual);
+        }
     }
     __device__ static void apply(const Params& p, const Place& q, Pre& pre, float (&v)[32]) {
         if (p.bias != nullptr) {
@@ -75,8 +88,8 @@ struct EpiForward {
                 v[j + 1] = y.y;
             }
         }
-        if (p.has_residual) {
-            if (!kSwap && in_pieces(p.residual, q)) {
+        if constexpr (kResidual && !kSwap) {
+            if (in_pieces(p.residual, q)) {
                 across_to_own(q, pre.residual);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -85,11 +98,10 @@ struct EpiForward {
                     v[2 * i + 1] += f.y;
                 }
             } else {
-                float r[32];
-                kSwap ? get_columns(p.residual, q, r) : get_rows(p.residual, q, r);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += r[j];
+                add_residual(p, q, v);
             }
+        } else if constexpr (kResidual) {
+            add_residual(p, q, v);
         }
         kSwap ? put_columns(p.y, q, v) : put_rows(p.y, q, v);
     }
@@ -130,32 +142,39 @@ struct EpiStore {
 // bound by reading the weight.
 constexpr int kSwapRows = 64;
 
-template <int kFamily, bool kSwap>
-cudaError_t forward(const Operand& x, const Operand& w, int M, int N, int K, const void* bias,
-                    const vc_matrix_t* residual, const vc_matrix_t* y, const vc_matrix_t* preact,
-                    vc_act_t act, cudaStream_t st) {
-    typename EpiForward<kFamily, kSwap>::Params ep = {};
-    ep.bias = static_cast<const __nv_bfloat16*>(bias);
-    ep.bias_vec = (reinterpret_cast<uintptr_t>(bias) & 15) == 0;
-    ep.residual = view_of(residual);
-    ep.y = view_of(y);
-    ep.preact = view_of(preact);
-    ep.has_residual = residual != nullptr;
-    ep.has_preact = preact != nullptr;
-    ep.act = act_params(act);
+// The operands and options of a call.
+struct Forward {
+    Operand x, w;
+    int M, N, K;
+    const void* bias;
+    const vc_matrix_t *residual, *y, *preact;
+    vc_act_t act;
+};
+
+template <int kFamily, bool kSwap, bool kResidual>
+cudaError_t forward(const Forward& f, cudaStream_t st) {
+    using Epi = EpiForward<kFamily, kSwap, kResidual>;
+    typename Epi::Params ep = {};
+    ep.bias = static_cast<const __nv_bfloat16*>(f.bias);
+    ep.bias_vec = (reinterpret_cast<uintptr_t>(f.bias) & 15) == 0;
+    ep.residual = view_of(f.residual);
+    ep.y = view_of(f.y);
+    ep.preact = view_of(f.preact);
+    ep.has_preact = f.preact != nullptr;
+    ep.act = act_params(f.act);
     if constexpr (kSwap)
-        return gemm::launch_skinny<EpiForward<kFamily, true>>(Product{w, x, N, M, K, 1, 1}, ep, st);
+        return gemm::launch_skinny<Epi>(Product{f.w, f.x, f.N, f.M, f.K, 1, 1}, ep, st);
     else
-        return gemm::launch<EpiForward<kFamily, false>>(Product{x, w, M, N, K, 1, 1}, ep, st);
+        return gemm::launch<Epi>(Product{f.x, f.w, f.M, f.N, f.K, 1, 1}, ep, st);
 }
 
 template <int kFamily>
-cudaError_t forward(const Operand& x, const Operand& w, int M, int N, int K, const void* bias,
-                    const vc_matrix_t* residual, const vc_matrix_t* y, const vc_matrix_t* preact,
-                    vc_act_t act, cudaStream_t st) {
-    return M <= kSwapRows
-               ? forward<kFamily, true>(x, w, M, N, K, bias, residual, y, preact, act, st)
-               : forward<kFamily, false>(x, w, M, N, K, bias, residual, y, preact, act, st);
+cudaError_t forward(const Forward& f, cudaStream_t st) {
+    if (f.M <= kSwapRows)
+        return f.residual != nullptr ? forward<kFamily, true, true>(f, st)
+                                     : forward<kFamily, true, false>(f, st);
+    return f.residual != nullptr ? forward<kFamily, false, true>(f, st)
+                                 : forward<kFamily, false, false>(f, st);
 }
 
 // ------------------------------------------------------------ copy, dz, db --
@@ -435,17 +454,12 @@ vc_status_t vc_linear_forward(const vc_matrix_t* x, const vc_matrix_t* weight, c
     ready_operand(x, &ws, &jobs, &packs, &a);
     ready_operand(weight, &ws, &jobs, &packs, &b);
     if (launch_pack(jobs, packs, st) != cudaSuccess) return VC_ERR_CUDA;
+    const Forward f = {a, b, (int)M, (int)N, (int)K, bias, residual, y, preact, act};
     cudaError_t e;
     switch (act_family(act)) {
-    case kFamilyErf:
-        e = forward<kFamilyErf>(a, b, (int)M, (int)N, (int)K, bias, residual, y, preact, act, st);
-        break;
-    case kFamilyLogistic:
-        e = forward<kFamilyLogistic>(a, b, (int)M, (int)N, (int)K, bias, residual, y, preact, act, st);
-        break;
-    default:
-        e = forward<kFamilyPiecewise>(a, b, (int)M, (int)N, (int)K, bias, residual, y, preact, act,
-                                      st);
+    case kFamilyErf: e = forward<kFamilyErf>(f, st); break;
+    case kFamilyLogistic: e = forward<kFamilyLogistic>(f, st); break;
+    default: e = forward<kFamilyPiecewise>(f, st);
     }
     return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
 }
