@@ -42,6 +42,7 @@ constexpr int kRowsPerCta = 128;       // tensor-memory lanes
 constexpr int kWarpStage = 2048;       // bytes of shared memory of an epilogue warp
 constexpr int kGroup = 8;              // tile rows walked together, for reuse in L2
 constexpr int kSmemPerBlock = 232448;  // 227 KB
+constexpr int kSmemPerSm = 233472;     // 228 KB, of which each block takes 1 KB more than it asks for
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 
 struct Shape {
@@ -387,12 +388,7 @@ struct View {
     int vec;  // four values starting at a column that is a multiple of four are one aligned vector
     int vec16;  // rows are on 16 bytes
 };
-// Value by value, out of line: the code of the common case stays short, which
-// counts where a kernel runs it once (instructions come from L2 then).
-static __device__ __noinline__ float4 load_few(const void* p, int f32, int n) {
-    return f32 ? load4(static_cast<const float*>(p), n, false)
-               : load4(static_cast<const __nv_bfloat16*>(p), n, false);
-}
+// Value by value; the stores out of line, to keep the common case's code short.
 static __device__ __noinline__ void store_few(void* p, int f32, int n, float4 x) {
     if (f32)
         store4(static_cast<float*>(p), x, n, false);
@@ -403,7 +399,9 @@ static __device__ __noinline__ void store_few(void* p, int f32, int n, float4 x)
 __device__ __forceinline__ float4 view_load(const View& v, int b, long long row, int col, int n) {
     const char* p = static_cast<const char*>(v.data) +
                     (((long long)b * v.batch_stride + row * v.ld + col) << (v.f32 ? 2 : 1));
-    if (!v.vec || n < 4) return load_few(p, v.f32, n);
+    if (!v.vec || n < 4)
+        return v.f32 ? load4(reinterpret_cast<const float*>(p), n, false)
+                     : load4(reinterpret_cast<const __nv_bfloat16*>(p), n, false);
     if (v.f32) return *reinterpret_cast<const float4*>(p);
     const uint2 u = *reinterpret_cast<const uint2*>(p);
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
@@ -671,6 +669,7 @@ __device__ __forceinline__ void put_columns(const View& x, const Place& q, const
 // Epi: the operator's epilogue.
 //   kSym                  the product is symmetric: only the tiles on and
 //                         below the diagonal are computed
+//   odd(p)                whether a matrix it touches has rows off 16 bytes
 //   Pre                   what the epilogue of a chunk reads, as loaded
 //   prefetch(p, q, pre)   starts these loads; called before the chunk's products are read
 //   apply(p, q, pre, v)   v[j] = D[row0 + lane][col0 + j]; all lanes call it
@@ -1039,38 +1038,43 @@ template <int kTileN>
 struct Split {
     static constexpr int kBM = kRowsPerCta, kBN = kTileN;
     static constexpr int kStageBytes = (kRowsPerCta + kBN) * kBlockK * 2;
-    static constexpr int kWarps = 4;  // of the epilogue
+    static constexpr int kWarps = kBN == 128 ? 8 : 4;  // of the epilogue
     static constexpr int kThreads = 32 * (2 + kWarps);
-    // partial chunks that the cluster's blocks (up to 8) send to this one
-    static constexpr int kPartBytes = kBN < 64 ? 8 * 4096 : kRowsPerCta * kBN * 4;
+    static constexpr int kUnits = kBN / 8;  // 32 x 32 chunks of the tile
+    // Partial chunks that the cluster's blocks (1, 2, 4 or 8; with 128 columns
+    // also 3) send to this one.
+    static constexpr int kParts = kBN == 128 ? 18 : 8;
+    static constexpr int kPartBytes = kParts * 4096;
     static constexpr int kChunkBytes = kWarps * kWarpStage;
     static constexpr int kBarBytes = 256;
     static constexpr int kMaxStages = 8;
-    static constexpr int kFixed = 1024 + kPartBytes + kChunkBytes + kBarBytes;
+    static constexpr int kFixed = kPartBytes + kChunkBytes + kBarBytes;
     static constexpr int kTmemCols = kBN;
     // Two blocks fit an SM with few stages, so that one's set-up, or the
     // next launch's, runs beside the other's work; with one block per SM,
     // more stages cover the latency of the memory.
-    static constexpr int kFewStages = (kSmemPerBlock / 2 - 1024 - kFixed) / kStageBytes;
+    static constexpr int kBlocksPerSm = kBN == 128 ? 1 : 2;
+    static constexpr int kFewStages = (kSmemPerSm / kBlocksPerSm - 1024 - kFixed) / kStageBytes;
     static constexpr int kManyStages =
         (kSmemPerBlock - kFixed) / kStageBytes < kMaxStages ? (kSmemPerBlock - kFixed) / kStageBytes : kMaxStages;
     static_assert(kFewStages >= 2, "shared memory");
     static_assert((2 * kMaxStages + 1) * 8 + 8 <= kBarBytes, "barriers");
 };
 
-// A cluster of blocks computes one 128 x kBN tile; block `rank` takes the
-// rank-th part of K.  The tile's 32 x 32 chunks are shared out over the
+// A cluster of blocks computes one 128 x kBN tile; block `rank` takes K blocks
+// rank, rank + ranks, ... (neighbours in memory at about the same time).  The tile's 32 x 32 chunks are shared out over the
 // blocks: each sends its partial chunks to their owners, who add them in rank
 // order and run the epilogue.
 template <int kBN, class Epi>
-__global__ void __launch_bounds__(Split<kBN>::kThreads, 2)
+__global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kBlocksPerSm)
 split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep,
              unsigned* timeouts, int ranks, int stages) {
     using C = Split<kBN>;
-    extern __shared__ unsigned char smem_raw[];
-    const unsigned base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    unsigned char* const gen = smem_raw + (base - smem_u32(smem_raw));
+    // (aligned by its declaration: rounding up would cost a stage of two blocks)
+    extern __shared__ __align__(1024) unsigned char smem_aligned[];
+    const unsigned base = smem_u32(smem_aligned);
+    unsigned char* const gen = smem_aligned;
     float4* const part = reinterpret_cast<float4*>(gen + stages * C::kStageBytes);
     unsigned char* const chunks = gen + stages * C::kStageBytes + C::kPartBytes;
     const unsigned full = base + stages * C::kStageBytes + C::kPartBytes + C::kChunkBytes;
@@ -1087,7 +1091,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             mbar_init(empty + 8 * i, 1);
         }
         mbar_init(tfull, 1);
-        *dead = 0;
+        *dead = (base & 1023) != 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tma_prefetch(&map_a);
         tma_prefetch(&map_b);
@@ -1109,10 +1113,9 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     int tm, tn;
     tile_at<Epi::kSym, C::kBM / C::kBN>(s, tile - b * s.tiles, tm, tn);
     const int m0 = tm * C::kBM, n0 = tn * kBN;
-    const int kb0 = (int)((long long)s.kblocks * rank / ranks);
-    const int kb1 = (int)((long long)s.kblocks * (rank + 1) / ranks);
     const int ew = warp - 2, quarter = warp & 3;
-    constexpr int kUnits = kBN / 8;  // chunks of the tile: unit u has rows (u & 3), columns u >> 2
+    constexpr int kUnits = C::kUnits;  // unit u has rows (u & 3), columns u >> 2
+    constexpr int kShare = kBN / 32 / (C::kWarps / 4);  // chunk columns of a warp
     Place q;
     q.b = b;
     q.M = s.M;
@@ -1122,12 +1125,12 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     q.stage = chunks + ew * kWarpStage;
     typename Epi::Pre pre;
     // this warp's first unit: its own quarter where K is not split
-    int unit = ranks == 1 ? quarter : rank + ranks * ew;
+    int unit = ranks == 1 ? quarter + 4 * kShare * (ew >> 2) : rank + ranks * ew;
 
     if (warp == 0) {
         int stage = 0;
         unsigned phase = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = rank; kb < s.kblocks; kb += ranks) {
             if (!warp_wait(empty + 8 * stage, phase ^ 1, dead)) break;
             if (elect_one()) {
                 mbar_expect(full + 8 * stage, C::kStageBytes);
@@ -1140,11 +1143,11 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     } else if (warp == 1) {
         int stage = 0;
         unsigned phase = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = rank; kb < s.kblocks; kb += ranks) {
             if (!warp_wait(full + 8 * stage, phase, dead)) break;
             tcgen05_fence_after();
             if (elect_one()) {
-                multiply_stage<1>(tmem, base + stage * C::kStageBytes, s, kb > kb0);
+                multiply_stage<1>(tmem, base + stage * C::kStageBytes, s, kb >= ranks);
                 mma_commit<1>(empty + 8 * stage);
             }
             __syncwarp();
@@ -1159,17 +1162,18 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const bool ok = warp_wait(tfull, 0, dead);
         tcgen05_fence_after();
         if (ok) {
-            for (int c = 0; c < kBN / 32; ++c) {
+            for (int h = 0; h < kShare; ++h) {
+                const int c = (ew >> 2) * kShare + h;
                 float v[32];
                 tmem_load32(tmem + ((unsigned)(quarter * 32) << 16) + 32 * c, v);
-                if (kb1 == kb0) {
+                if (rank >= s.kblocks) {  // no K block: nothing was written
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 }
                 if (ranks == 1) {
                     if (inside<Epi>(q)) Epi::apply(ep, q, pre, v);
                     q.col0 += 32;
-                    if (c + 1 < kBN / 32 && inside<Epi>(q)) Epi::prefetch(ep, q, pre);
+                    if (h + 1 < kShare && inside<Epi>(q)) Epi::prefetch(ep, q, pre);
                 } else {
                     // to slot [unit of the owner][from rank][8 x 32 lanes]
                     const int u = c * 4 + quarter, owner = u % ranks, k = u / ranks;
@@ -1372,61 +1376,80 @@ cudaError_t launch_split(const Product& p, const typename Epi::Params& ep, int r
                           stages);
 }
 
-// How long a product takes, in microseconds, by a model of the two kernels
-// that was fitted to measurements of 1 to 512 tiles and K of 64 to 8192 on
-// operands in L2 (within 20 % of most): a fixed part, and for each wave of
-// tiles the larger of its K blocks' time and its epilogue's.
-//   pair kernel:   6.5 + waves of 76 x max(0.275 K blocks + 0.5, 3.2)
-//   split kernel:  1.5 + waves of 304 blocks x (2.3 + c K blocks of a rank)
-//                  (+ 0.7 where K is split), c = 0.21 with one block per SM
-//                  and 0.30 with two
-// e.g. 2048 x 2048 x 2048: 17 us (pair), 25 us (split); 512 x 512 x 2048:
+// How long a product takes, in microseconds, by a model of the kernels that was
+// fitted to measurements of 1 to 512 tiles and K of 64 to 8192 on operands in
+// L2 (within 20 % of most): a fixed part, and for each wave of tiles the larger
+// of its K blocks' time and its epilogue's, which is longer where a matrix's
+// rows are off 16 bytes (`odd`).
+//   pair kernel, 256 x 256:   6.5 + waves of 76 x max(0.275 K blocks + 0.5, 3.2)
+//   split kernel, 128 x 64:   1.5 + 2.3 waves of 304 + 0.2 (blocks per SM) K blocks
+//   split kernel, 128 x 128:  1.5 + waves of 152 x (2.8 + 0.28 K blocks)
+//                             (split: + 0.7 where K is)
+// e.g. 2048 x 2048 x 2048: 17 us (pair), 25 us (128 x 64); 512 x 512 x 2048:
 // 15.8 us and 6.1 us; 1024 x 1024 x 4096: 24 us and 14 us.
-inline double pair_us(const Product* p, int count, bool sym) {
+struct Plan {
+    double us;
+    int tile, ranks;  // 256: the pair kernel; 128, 64: the split kernel's columns
+};
+
+inline double pair_us(const Product* p, int count, bool sym, bool odd) {
     double tile_us = 0.0, longest = 0.0;
     long long total = 0;
     const int slots = device_sms() / 2;
     for (int i = 0; i < count; ++i) {
         const long long tiles = tile_count(p[i].M, p[i].N, Pair<false>::kBM, Pair<false>::kBN, sym) * p[i].batch;
-        const double k = 0.275 * k_blocks(p[i]) + 0.5;
-        const double each = k > 3.2 ? k : 3.2;
+        const double k = 0.275 * k_blocks(p[i]) + 0.5, epilogue = odd ? 9.0 : 3.2;
+        const double each = k > epilogue ? k : epilogue;
         longest = each > longest ? each : longest;
         tile_us += each * (double)tiles;
         total += tiles;
     }
-    if (count == 1) return 6.5 + longest * (double)((total + slots - 1) / slots);
+    const double fixed = odd ? 11.0 : 6.5;
+    if (count == 1) return fixed + longest * (double)((total + slots - 1) / slots);
     const double even = tile_us / slots;
-    return 6.5 + (even > longest ? even : longest);
+    return fixed + (even > longest ? even : longest);
 }
 
-struct Plan {
-    double us;
-    int ranks;
-};
-
-// The split kernel's best number of ranks; limit > 0: at most so many K blocks
-// per rank (1e9 us where 8 ranks do not reach that).
-inline Plan plan_split(const Product& p, bool sym, int limit) {
-    const long long tiles = tile_count(p.M, p.N, Split<64>::kBM, Split<64>::kBN, sym) * p.batch;
+// The split kernel's best tile and number of ranks; limit > 0: at most so many
+// K blocks per rank (1e9 us where 8 ranks do not reach that).
+inline Plan plan_split(const Product& p, bool sym, bool odd, int limit) {
     const int kblocks = k_blocks(p), sms = device_sms();
-    Plan best = {1e9, 1};
-    for (int ranks = 1; ranks <= 8; ranks *= 2) {
-        const int kb = (kblocks + ranks - 1) / ranks;
-        if (limit > 0 && kb > limit) continue;
-        const long long blocks = tiles * ranks;
-        const double c = blocks <= sms ? 0.21 : 0.30;
-        const double us = 1.5 + (double)((blocks + 2 * sms - 1) / (2 * sms)) * (2.3 + c * kb) +
-                          (ranks > 1 ? 0.7 : 0.0);
-        if (us < best.us) best = {us, ranks};
+    Plan best = {1e9, 64, 1};
+    for (int tile = 64; tile <= 128; tile += 64) {
+        const long long tiles = tile_count(p.M, p.N, kRowsPerCta, tile, sym) * p.batch;
+        for (int ranks = 1; ranks <= 8; ranks += ranks == 3 ? 1 : ranks > 3 ? 4 : 1) {
+            if (ranks == 3 && tile == 64) continue;
+            const int kb = (kblocks + ranks - 1) / ranks;
+            if (limit > 0 && kb > limit) continue;
+            const long long blocks = tiles * ranks;
+            const double epilogue = (odd ? 2.5 : 0.0) / ranks;
+            double us = 1.5 + (ranks > 1 ? 0.7 : 0.0);
+            if (tile == 64) {
+                const double per_sm = blocks > 2 * sms ? (double)blocks / sms
+                                                       : (double)((blocks + sms - 1) / sms);
+                us += (2.3 + epilogue) * (double)((blocks + 2 * sms - 1) / (2 * sms)) + 0.2 * per_sm * kb;
+            } else {
+                us += (2.8 + epilogue + 0.28 * kb) * (double)((blocks + sms - 1) / sms);
+            }
+            if (us < best.us) best = {us, tile, ranks};
+        }
     }
     return best;
 }
 
-// Picks the kernel and the ranks.
+template <class Epi>
+cudaError_t launch_planned(const Product& p, const typename Epi::Params& ep, const Plan& plan,
+                           cudaStream_t st) {
+    if (plan.tile == 128) return launch_split<128, Epi>(p, ep, plan.ranks, st);
+    return launch_split<64, Epi>(p, ep, plan.ranks, st);
+}
+
+// Picks the kernel, the tile and the ranks.
 template <class Epi>
 cudaError_t launch(const Product& p, const typename Epi::Params& ep, cudaStream_t st) {
-    const Plan split = plan_split(p, Epi::kSym, 0);
-    if (split.us < pair_us(&p, 1, Epi::kSym)) return launch_split<64, Epi>(p, ep, split.ranks, st);
+    const bool odd = Epi::odd(ep);
+    const Plan split = plan_split(p, Epi::kSym, odd, 0);
+    if (split.us < pair_us(&p, 1, Epi::kSym, odd)) return launch_planned<Epi>(p, ep, split, st);
     return launch_pair<Epi, 1, false>(&p, &ep, 0, st);
 }
 

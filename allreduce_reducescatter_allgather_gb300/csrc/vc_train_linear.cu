@@ -29,20 +29,17 @@ struct EpiForward {
         int has_preact, bias_vec;
         Act act;
     };
+    static bool odd(const Params& p) {
+        return !p.y.vec16 || (p.has_preact && !p.preact.vec16) || (kResidual && !p.residual.vec16);
+    }
     struct WithResidual {
-        gemm::Chunk16 residual;  // as loaded, across the rows
+        gemm::Chunk16 residual;  // across the rows, or, off 16 bytes, one row per lane
     };
     struct Without {};
     struct Pre : std::conditional_t<kResidual && !kSwap, WithResidual, Without> {
         gemm::Chunk16 bias;  // of the chunk's columns, the same in every lane
         float one_bias;      // else: of the lane's column (kSwap: row)
     };
-    __device__ static void add_residual(const Params& p, const Place& q, float (&v)[32]) {
-        float r[32];
-        kSwap ? get_columns(p.residual, q, r) : get_rows(p.residual, q, r);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += r[j];
-    }
     __device__ static bool bias_in_pieces(const Params& p, const Place& q) {
         return !kSwap && p.bias_vec && q.whole();
     }
@@ -62,6 +59,10 @@ struct EpiForward {
                 load_across(static_cast<const __nv_bfloat16*>(p.residual.data) +
                                 corner_of(p.residual, q),
                             p.residual.ld * 2, q, pre.residual);
+            else
+                load_values(static_cast<const unsigned short*>(p.residual.data) +
+                                corner_of(p.residual, q),
+                            p.residual.ld, q, q.N - q.col0, pre.residual);
         }
     }
     __device__ static void apply(const Params& p, const Place& q, Pre& pre, float (&v)[32]) {
@@ -89,19 +90,18 @@ struct EpiForward {
             }
         }
         if constexpr (kResidual && !kSwap) {
-            if (in_pieces(p.residual, q)) {
-                across_to_own(q, pre.residual);
+            if (in_pieces(p.residual, q)) across_to_own(q, pre.residual);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 f = pair_at(pre.residual, i, __nv_bfloat16());
-                    v[2 * i] += f.x;
-                    v[2 * i + 1] += f.y;
-                }
-            } else {
-                add_residual(p, q, v);
+            for (int i = 0; i < 16; ++i) {
+                const float2 f = pair_at(pre.residual, i, __nv_bfloat16());
+                v[2 * i] += f.x;
+                v[2 * i + 1] += f.y;
             }
         } else if constexpr (kResidual) {
-            add_residual(p, q, v);
+            float r[32];
+            get_columns(p.residual, q, r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += r[j];
         }
         kSwap ? put_columns(p.y, q, v) : put_rows(p.y, q, v);
     }
@@ -115,6 +115,7 @@ struct EpiStore {
         View out;
         int add;
     };
+    static bool odd(const Params& p) { return !p.out.vec16; }
     struct Pre {};
     __device__ static void prefetch(const Params&, const Place&, Pre&) {}
     __device__ static void apply(const Params& p, const Place& q, Pre&, float (&v)[32]) {
@@ -187,22 +188,66 @@ struct PackJob {
     long long ld;
     int rows, cols, pieces;  // pieces: of 8 values per row
 };
-struct PackJobs {
-    PackJob job[2];
+// db (+)= the sum of partial sums, in a fixed order.
+struct SumJob {
+    const float* sums;  // [parts][cols], or NULL
+    void* db;
+    int parts, cols, f32, add;
 };
-__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackJobs jobs) {
+__device__ __forceinline__ void store_db(const SumJob& j, int col, float v) {
+    if (j.f32) {
+        float* d = static_cast<float*>(j.db) + col;
+        *d = j.add ? *d + v : v;
+    } else {
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(j.db) + col;
+        *d = __float2bfloat16(j.add ? __bfloat162float(*d) + v : v);
+    }
+}
+
+// What has to be done before the products, in one launch: the blocks of row y
+// of the grid take job y, those of the last row the column sums (a block 32
+// columns at a time, its warps every eighth part).
+struct Jobs {
+    PackJob pack[2];
+    int packs;
+    SumJob sum;
+};
+__global__ void __launch_bounds__(256) jobs_kernel(const __grid_constant__ Jobs jobs) {
+    __shared__ float part[8][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const PackJob j = jobs.job[blockIdx.y];
-    const long long total = (long long)j.rows * j.pieces;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
-         i += (long long)gridDim.x * 256) {
-        const int row = (int)(i / j.pieces), col = (int)(i - (long long)row * j.pieces) * 8;
-        const unsigned short* s = j.src + row * j.ld + col;
-        unsigned v[8];
+    if ((int)blockIdx.y < jobs.packs) {
+        const PackJob j = jobs.pack[blockIdx.y];
+        const long long total = (long long)j.rows * j.pieces;
+        for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
+             i += (long long)gridDim.x * 256) {
+            const int row = (int)(i / j.pieces), col = (int)(i - (long long)row * j.pieces) * 8;
+            const unsigned short* s = j.src + row * j.ld + col;
+            unsigned v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = col + k < j.cols ? s[k] : 0u;
-        j.dst[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+            for (int k = 0; k < 8; ++k) v[k] = col + k < j.cols ? s[k] : 0u;
+            j.dst[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
+                                  v[6] | v[7] << 16);
+        }
+        return;
+    }
+    const SumJob& j = jobs.sum;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (long long first = (long long)blockIdx.x * 32; first < j.cols;
+         first += (long long)gridDim.x * 32) {
+        const long long col = first + lane;
+        float v = 0.0f;
+        if (col < j.cols) {
+#pragma unroll 8
+            for (int i = warp; i < j.parts; i += 8) v += j.sums[(long long)i * j.cols + col];
+        }
+        __syncthreads();
+        part[warp][lane] = v;
+        __syncthreads();
+        if (warp != 0 || col >= j.cols) continue;
+#pragma unroll
+        for (int w = 1; w < 8; ++w) v += part[w][lane];
+        store_db(j, (int)col, v);
     }
 }
 
@@ -212,6 +257,7 @@ struct DzParams {
     __nv_bfloat16* dz_rest;  // NULL, or receives what rounding dz left
     long long ld_dz;
     float* sums;  // [gridDim.y][N], or NULL
+    SumJob direct;  // with one row of blocks: where the sums go at once
     long long rows, cols;
     int has_act, vec16;
     Act act;
@@ -283,7 +329,7 @@ __global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzPa
                     make_uint4(rest[0], rest[1], rest[2], rest[3]);
         }
     }
-    if (p.sums == nullptr) return;
+    if (p.sums == nullptr && p.direct.db == nullptr) return;
     part[warp][lane * 2] = make_float4(sum[0], sum[1], sum[2], sum[3]);
     part[warp][lane * 2 + 1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
     __syncthreads();
@@ -292,35 +338,10 @@ __global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzPa
         float t = 0.0f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) t += reinterpret_cast<const float*>(part[w])[threadIdx.x];
-        p.sums[(long long)blockIdx.y * p.cols + mine] = t;
-    }
-}
-
-// db (+)= the sum of the blocks' partial sums, in a fixed order: a block takes
-// 32 columns, its warps every eighth part.
-__global__ void __launch_bounds__(256) db_kernel(const float* sums, int parts, long long cols,
-                                                 void* db, int f32, int add) {
-    __shared__ float part[8][32];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long col = (long long)blockIdx.x * 32 + lane;
-    float v = 0.0f;
-    if (col < cols) {
-#pragma unroll 8
-        for (int i = warp; i < parts; i += 8) v += sums[(long long)i * cols + col];
-    }
-    part[warp][lane] = v;
-    __syncthreads();
-    if (warp != 0 || col >= cols) return;
-#pragma unroll
-    for (int w = 1; w < 8; ++w) v += part[w][lane];
-    if (f32) {
-        float* d = static_cast<float*>(db) + col;
-        *d = add ? *d + v : v;
-    } else {
-        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(db) + col;
-        *d = __float2bfloat16(add ? __bfloat162float(*d) + v : v);
+        if (p.direct.db != nullptr)
+            store_db(p.direct, (int)mine, t);
+        else
+            p.sums[(long long)blockIdx.y * p.cols + mine] = t;
     }
 }
 
@@ -352,8 +373,7 @@ size_t packed_bytes(const vc_matrix_t* m) {
 
 // Where TMA reads the matrix: in place, or packed at *ws (advanced), for which
 // a job is added.
-void ready_operand(const vc_matrix_t* m, unsigned char** ws, PackJobs* jobs, int* count,
-                   Operand* o) {
+void ready_operand(const vc_matrix_t* m, unsigned char** ws, Jobs* jobs, Operand* o) {
     if (operand_ready(m) || m->rows == 0 || m->cols == 0) {
         o->data = m->data;
         o->ld = m->rows > 1 ? m->ld : padded_ld(m->cols);
@@ -361,22 +381,23 @@ void ready_operand(const vc_matrix_t* m, unsigned char** ws, PackJobs* jobs, int
     }
     o->data = *ws;
     o->ld = padded_ld(m->cols);
-    jobs->job[(*count)++] = {static_cast<const unsigned short*>(m->data),
-                             reinterpret_cast<uint4*>(*ws),
-                             m->rows > 1 ? m->ld : 0,
-                             (int)m->rows,
-                             (int)m->cols,
-                             (int)(o->ld / 8)};
+    jobs->pack[jobs->packs++] = {static_cast<const unsigned short*>(m->data),
+                                 reinterpret_cast<uint4*>(*ws),
+                                 m->rows > 1 ? m->ld : 0,
+                                 (int)m->rows,
+                                 (int)m->cols,
+                                 (int)(o->ld / 8)};
     *ws += packed_bytes(m);
 }
 
-cudaError_t launch_pack(const PackJobs& jobs, int count, cudaStream_t st) {
-    if (count == 0) return cudaSuccess;
-    long long most = 0;
-    for (int i = 0; i < count; ++i)
-        most = std::max(most, (long long)jobs.job[i].rows * jobs.job[i].pieces);
-    const int blocks = (int)std::min(152 * 16ll, (most + 255) / 256);
-    return launch_pdl(pack_kernel, dim3(blocks, count), dim3(256), st, jobs);
+cudaError_t launch_jobs(const Jobs& jobs, cudaStream_t st) {
+    const int rows = jobs.packs + (jobs.sum.sums != nullptr ? 1 : 0);
+    if (rows == 0) return cudaSuccess;
+    long long most = jobs.sum.sums != nullptr ? (jobs.sum.cols + 31) / 32 : 1;
+    for (int i = 0; i < jobs.packs; ++i)
+        most = std::max(most, ((long long)jobs.pack[i].rows * jobs.pack[i].pieces + 255) / 256);
+    const int blocks = (int)std::min(152 * 16ll, most);
+    return launch_pdl(jobs_kernel, dim3(blocks, rows), dim3(256), st, jobs);
 }
 
 bool is_bf16(const vc_matrix_t* m) { return m->dtype == VC_BFLOAT16; }
@@ -449,11 +470,10 @@ vc_status_t vc_linear_forward(const vc_matrix_t* x, const vc_matrix_t* weight, c
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     Operand a = {nullptr, K, M, 0, 0, true, false}, b = {nullptr, K, N, 0, 0, true, false};
-    PackJobs jobs = {};
-    int packs = 0;
-    ready_operand(x, &ws, &jobs, &packs, &a);
-    ready_operand(weight, &ws, &jobs, &packs, &b);
-    if (launch_pack(jobs, packs, st) != cudaSuccess) return VC_ERR_CUDA;
+    Jobs jobs = {};
+    ready_operand(x, &ws, &jobs, &a);
+    ready_operand(weight, &ws, &jobs, &b);
+    if (launch_jobs(jobs, st) != cudaSuccess) return VC_ERR_CUDA;
     const Forward f = {a, b, (int)M, (int)N, (int)K, bias, residual, y, preact, act};
     cudaError_t e;
     switch (act_family(act)) {
@@ -523,6 +543,7 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
         ld_dz = padded_ld(N);
         ws += planes * round256((size_t)M * ld_dz * 2);
     }
+    Jobs jobs = {};
     cudaError_t e = cudaSuccess;
     if (N > 0 && (sums != nullptr || (write_dz && M > 0))) {
         DzParams p = {};
@@ -532,7 +553,15 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
         p.dz_rest = planes == 2 ? p.dz + plane : nullptr;
         p.ld_dz = ld_dz;
         p.vec16 = p.dy.vec16 && (!has_act || p.preact.vec16);
-        p.sums = sums;
+        if (dbias != nullptr) {
+            const SumJob sum = {sums, dbias, parts, (int)N, dbias_dtype == VC_FLOAT32, accumulate != 0};
+            if (parts == 1) {
+                p.direct = sum;
+            } else {
+                p.sums = sums;
+                jobs.sum = sum;
+            }
+        }
         p.rows = M;
         p.cols = N;
         p.has_act = has_act;
@@ -542,45 +571,40 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
                                                             : dz_kernel<kFamilyPiecewise>;
         e = launch_pdl(kernel, dim3((unsigned)((N + 255) / 256), parts), dim3(256), st, p);
         if (e != cudaSuccess) return VC_ERR_CUDA;
-        if (sums != nullptr) {
-            e = launch_pdl(db_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), st,
-                           (const float*)sums, parts, N, dbias, dbias_dtype == VC_FLOAT32 ? 1 : 0,
-                           accumulate != 0 ? 1 : 0);
-            if (e != cudaSuccess) return VC_ERR_CUDA;
-        }
     }
     Product p[2];
     EpiStore<false>::Params ep[2];
-    int count = 0, packs = 0;
-    PackJobs jobs = {};
+    int count = 0;
     if (dx != nullptr && M > 0 && K > 0) {
         const Operand a = {dz, N, M, ld_dz, plane, true, false};
         Operand b = {nullptr, K, N, 0, 0, true, true};
-        ready_operand(weight, &ws, &jobs, &packs, &b);
+        ready_operand(weight, &ws, &jobs, &b);
         p[count] = {a, b, (int)M, (int)K, (int)N, 1, planes};
         ep[count++] = {view_of(dx), 0};
     }
     if (dweight != nullptr && N > 0 && K > 0) {
         const Operand a = {dz, N, M, ld_dz, plane, true, true};
         Operand b = {nullptr, K, M, 0, 0, true, true};
-        ready_operand(x, &ws, &jobs, &packs, &b);
+        ready_operand(x, &ws, &jobs, &b);
         p[count] = {a, b, (int)N, (int)K, (int)M, 1, planes};
         ep[count++] = {view_of(dweight), accumulate != 0};
     }
-    if (launch_pack(jobs, packs, st) != cudaSuccess) return VC_ERR_CUDA;
+    if (launch_jobs(jobs, st) != cudaSuccess) return VC_ERR_CUDA;
     if (count > 0) {
         // 32-bit sums are not left to the tensor cores for longer than a segment
         const bool promote = dweight != nullptr && dweight->dtype == VC_FLOAT32;
         gemm::Plan plan[2];
         double apart = 0.0;
+        bool odd = false;
         for (int i = 0; i < count; ++i) {
             const bool sums = promote && ep[i].out.f32;
-            plan[i] = gemm::plan_split(p[i], false, sums ? kSegment : 0);
+            plan[i] = gemm::plan_split(p[i], false, !ep[i].out.vec16, sums ? kSegment : 0);
+            odd = odd || !ep[i].out.vec16;
             apart += plan[i].us;
         }
-        if (apart < gemm::pair_us(p, count, false)) {
+        if (apart < gemm::pair_us(p, count, false, odd)) {
             for (int i = 0; i < count && e == cudaSuccess; ++i)
-                e = gemm::launch_split<64, EpiStore<false>>(p[i], ep[i], plan[i].ranks, st);
+                e = gemm::launch_planned<EpiStore<false>>(p[i], ep[i], plan[i], st);
         } else if (count == 2) {
             e = promote ? gemm::launch_pair<EpiStore<false>, 2, true>(p, ep, kSegment, st)
                         : gemm::launch_pair<EpiStore<false>, 2, false>(p, ep, 0, st);

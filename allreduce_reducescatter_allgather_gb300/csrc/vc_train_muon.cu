@@ -189,6 +189,7 @@ struct EpiGram {
         long long ld, batch_stride;
         float scale;
     };
+    static bool odd(const Params&) { return false; }
     struct Pre {};
     __device__ static void prefetch(const Params&, const Place&, Pre&) {}
     __device__ static void apply(const Params& p, const Place& q, Pre&, float (&v)[32]) {
@@ -215,6 +216,7 @@ struct EpiPoly {
         long long ld, batch_stride;
         float cb, cc;
     };
+    static bool odd(const Params&) { return false; }
     struct Pre {
         gemm::Chunk16 o;
         float row, col;  // A's diagonal at the lane's row and at its column
@@ -288,6 +290,7 @@ __device__ __forceinline__ void update_apply(const UpdateParams& p, const Place&
 struct EpiUpdate {
     static constexpr bool kSym = false;
     using Params = UpdateParams;
+    static bool odd(const Params&) { return false; }
     using Pre = UpdatePre;
     __device__ static void prefetch(const Params& p, const Place& q, Pre& pre) {
         update_prefetch(p, q, pre);
@@ -310,6 +313,7 @@ struct EpiFinal {
         int weights;  // out <- keep out + scale y, else out <- scale y
         float keep, scale;
     };
+    static bool odd(const Params& p) { return !p.out.vec16; }
     using Pre = UpdatePre;
     __device__ static void prefetch(const Params& p, const Place& q, Pre& pre) {
         update_prefetch(p.u, q, pre);
@@ -346,8 +350,8 @@ bool layout_of(long long batch, long long rows, long long cols, Layout* l) {
     if (rows * vpr > 0x7FFFFFFFll || batch * rows > 0x3FFFFFFFll) return false;
     l->r = std::min(rows, cols);
     l->c = std::max(rows, cols);
-    l->ldx = (cols + 31) / 32 * 32;  // whole chunks of the epilogues
-    l->ldr = (l->r + 31) / 32 * 32;
+    l->ldx = padded_ld(cols);  // whole chunks of the epilogues, too
+    l->ldr = padded_ld(l->r);
     l->xs = rows * l->ldx;
     l->as = l->r * l->ldr;
     const long long want = (rows * vpr + 256 * kPrepareBatch - 1) / (256 * kPrepareBatch), fit = std::max(1ll, 152 * 8 / std::max(1ll, batch));
