@@ -766,11 +766,10 @@ __device__ __forceinline__ void bury(volatile int* dead, unsigned* timeouts) {
 
 // ------------------------------------------------------------- pair kernel --
 
-template <bool kPromote>
+template <int kEpilogueWarps>
 struct Pair {
     static constexpr int kBN = 256, kBM = 256;
-    // warps of the epilogue; sums in registers want more of them, with fewer columns each
-    static constexpr int kWarps = kPromote ? 16 : 8;
+    static constexpr int kWarps = kEpilogueWarps;  // 8, or 16 with half the registers
     static constexpr int kThreads = 32 * (2 + kWarps);
     static constexpr int kBRows = kBN / 2;  // rows of B (columns of D) that a block loads
     static constexpr int kStageBytes = (kRowsPerCta + kBRows) * kBlockK * 2;
@@ -781,6 +780,12 @@ struct Pair {
     static constexpr int kTmemCols = 2 * kBN;  // two accumulators
     static_assert(kSmem <= kSmemPerBlock, "shared memory");
 };
+
+// Sums in registers want more warps, with fewer columns each (and fewer registers:
+// the Newton-Schulz update's epilogue is slower with 16, 17.7 -> 19.9 us at 4096
+// x 1024 x 1024).
+template <bool kPromote>
+struct PairFor : Pair<kPromote ? 16 : 8> {};
 
 // One or two products in one launch (the second one's tiles may be 0), whose
 // blocks then share the work of both: the first has the longer tiles.
@@ -828,11 +833,11 @@ __device__ __forceinline__ bool work_item(const PairWork<Epi>& w, int slot, int 
 // cut accumulated sums off instead: measured 1e-6 relative, towards zero, for
 // sums of 1024 products, and growing with their number.)
 template <class Epi, int kCount, bool kPromote>
-__global__ void __launch_bounds__(Pair<kPromote>::kThreads, 1)
+__global__ void __launch_bounds__(PairFor<kPromote>::kThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_b0,
             const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b1,
             const __grid_constant__ PairWork<Epi> w) {
-    using C = Pair<kPromote>;
+    using C = PairFor<kPromote>;
     extern __shared__ unsigned char smem_raw[];
     const unsigned base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* const gen = smem_raw + (base - smem_u32(smem_raw));
@@ -1335,13 +1340,13 @@ cudaError_t launch_pair(const Product* p, const typename Epi::Params* ep, int se
     const int first = kCount == 2 && k_blocks(p[kCount - 1]) > k_blocks(p[0]) ? 1 : 0;
     for (int i = 0; i < kCount; ++i) {
         const int from = i == 0 ? first : 1 - first;
-        const cudaError_t e = shape_of(p[from], Pair<false>::kBM, Pair<false>::kBN, Epi::kSym, &w.s[i]);
+        const cudaError_t e = shape_of(p[from], Pair<8>::kBM, Pair<8>::kBN, Epi::kSym, &w.s[i]);
         if (e != cudaSuccess) return e;
         if constexpr (kPromote) {
             if (Epi::sums32(ep[from])) w.s[i].segment = segment;
         }
         w.ep[i] = ep[from];
-        if (!encode_product(p[from], Pair<false>::kBRows, &m[2 * i], &m[2 * i + 1]))
+        if (!encode_product(p[from], Pair<8>::kBRows, &m[2 * i], &m[2 * i + 1]))
             return cudaErrorInvalidValue;
     }
     const int sms = device_sms();
@@ -1352,8 +1357,8 @@ cudaError_t launch_pair(const Product* p, const typename Epi::Params* ep, int se
     const int pairs = total < slots ? total : slots;
     if (w.s[1].total > 0 && w.s[0].total % pairs != 0)
         w.extra = w.s[0].kblocks / (w.s[1].kblocks > 0 ? w.s[1].kblocks : 1);
-    return launch_cluster(pair_kernel<Epi, kCount, kPromote>, pairs * 2, Pair<kPromote>::kThreads,
-                          2, Pair<kPromote>::kSmem, st, m[0], m[1],
+    return launch_cluster(pair_kernel<Epi, kCount, kPromote>, pairs * 2, PairFor<kPromote>::kThreads,
+                          2, PairFor<kPromote>::kSmem, st, m[0], m[1],
                           m[2], m[3], w);
 }
 
@@ -1397,14 +1402,14 @@ inline double pair_us(const Product* p, int count, bool sym, bool odd) {
     long long total = 0;
     const int slots = device_sms() / 2;
     for (int i = 0; i < count; ++i) {
-        const long long tiles = tile_count(p[i].M, p[i].N, Pair<false>::kBM, Pair<false>::kBN, sym) * p[i].batch;
+        const long long tiles = tile_count(p[i].M, p[i].N, Pair<8>::kBM, Pair<8>::kBN, sym) * p[i].batch;
         const double k = 0.275 * k_blocks(p[i]) + 0.5, epilogue = odd ? 9.0 : 3.2;
         const double each = k > epilogue ? k : epilogue;
         longest = each > longest ? each : longest;
         tile_us += each * (double)tiles;
         total += tiles;
     }
-    const double fixed = odd ? 11.0 : 6.5;
+    const double fixed = odd ? 8.0 : 6.5;
     if (count == 1) return fixed + longest * (double)((total + slots - 1) / slots);
     const double even = tile_us / slots;
     return fixed + (even > longest ? even : longest);

@@ -22,6 +22,9 @@
 namespace vc {
 namespace train {
 
+// Whether pass `step` reads X as two fp16 values.
+__host__ __device__ inline bool keeps_lo(int step, int steps) { return step == 0 || step < steps - 2; }
+
 struct SmallParams {
     gemm::View g, m, out;
     int has_momentum, nesterov, weights, tall;
@@ -388,17 +391,29 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
             gemm::tmem_load32(lanes + 128 + 32 * c, v);
             gemm::Chunk16 h, l;
             load_pieces(hi, row, 32 * c, h);
-            load_pieces(lo, row, 32 * c, l);
+            if (keeps_lo(step, p.steps)) {
+                load_pieces(lo, row, 32 * c, l);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 r = gemm::pair_at(l, i, __half());
+                    v[2 * i] = fmaf(kx, r.x, v[2 * i]);
+                    v[2 * i + 1] = fmaf(kx, r.y, v[2 * i + 1]);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float2 a = gemm::pair_at(h, i, __half()), r = gemm::pair_at(l, i, __half());
-                v[2 * i] = fmaf(kx, a.x + r.x, v[2 * i]);
-                v[2 * i + 1] = fmaf(kx, a.y + r.y, v[2 * i + 1]);
+                const float2 a = gemm::pair_at(h, i, __half());
+                v[2 * i] = fmaf(kx, a.x, v[2 * i]);
+                v[2 * i + 1] = fmaf(kx, a.y, v[2 * i + 1]);
             }
             if (step + 1 < p.steps) {
-                split_halves(v, h, l);
+                if (keeps_lo(step + 1, p.steps)) {
+                    split_halves(v, h, l);
+                    store_pieces(lo, row, 32 * c, l);
+                } else {
+                    h = gemm::packed_row(v, __half());
+                }
                 store_pieces(hi, row, 32 * c, h);
-                store_pieces(lo, row, 32 * c, l);
             } else {
                 // (the parts' buffer is free: no block sends to another any more)
                 gemm::Place q;

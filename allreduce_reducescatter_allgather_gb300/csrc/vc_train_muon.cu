@@ -21,6 +21,8 @@
 //     diag(B) X terms use both and the products the larger one.  Without it,
 //     directions with small singular values, which the iteration raises by
 //     up to 500, would be raised from the rounding noise of the large ones.
+//     In the last two passes, where what counts is near 1 and is raised no
+//     more, the larger value does alone.
 #include <algorithm>
 #include <math.h>
 
@@ -261,6 +263,7 @@ struct UpdateParams {
     float a;
     int tall;  // B stands on the right: its diagonal goes with the columns
     int r;
+    int read_lo, write_lo;
 };
 struct UpdatePre {
     gemm::Chunk16 hi, lo;
@@ -271,20 +274,24 @@ __device__ __forceinline__ void update_prefetch(const UpdateParams& p, const Pla
     pre.k = at < p.r ? p.a + p.db[(long long)q.b * p.r + at] : 0.0f;
     const long long x = (long long)q.b * p.batch_stride + (long long)q.row0 * p.ld + q.col0;
     load_across(p.hi + x, p.ld * 2, q, pre.hi);
-    load_across(p.lo + x, p.ld * 2, q, pre.lo);
+    if (p.read_lo) load_across(p.lo + x, p.ld * 2, q, pre.lo);
 }
 __device__ __forceinline__ void update_apply(const UpdateParams& p, const Place& q, UpdatePre& pre,
                                              float (&v)[32]) {
     across_to_own(q, pre.hi);
-    across_to_own(q, pre.lo);
+    if (p.read_lo) across_to_own(q, pre.lo);
+    auto add = [&](bool with_lo) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float2 h = pair_at(pre.hi, i, __half()), l = pair_at(pre.lo, i, __half());
-        const float k0 = __shfl_sync(0xFFFFFFFFu, pre.k, 2 * i);
-        const float k1 = __shfl_sync(0xFFFFFFFFu, pre.k, 2 * i + 1);
-        v[2 * i] = fmaf(p.tall ? k0 : pre.k, h.x + l.x, v[2 * i]);
-        v[2 * i + 1] = fmaf(p.tall ? k1 : pre.k, h.y + l.y, v[2 * i + 1]);
-    }
+        for (int i = 0; i < 16; ++i) {
+            float2 x = pair_at(pre.hi, i, __half());
+            if (with_lo) x = gemm::add2(x, pair_at(pre.lo, i, __half()));
+            const float k0 = p.tall ? __shfl_sync(0xFFFFFFFFu, pre.k, 2 * i) : pre.k;
+            const float k1 = p.tall ? __shfl_sync(0xFFFFFFFFu, pre.k, 2 * i + 1) : pre.k;
+            v[2 * i] = fmaf(k0, x.x, v[2 * i]);
+            v[2 * i + 1] = fmaf(k1, x.y, v[2 * i + 1]);
+        }
+    };
+    p.read_lo ? add(true) : add(false);
 }
 
 struct EpiUpdate {
@@ -299,6 +306,7 @@ struct EpiUpdate {
         update_apply(p, q, pre, v);
         const long long at = (long long)q.b * p.batch_stride + (long long)q.row0 * p.ld + q.col0;
         store_chunk(p.hi_out + at, p.ld, q, v);
+        if (!p.write_lo) return;
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] -= __half2float(__float2half_rn(v[j]));
         store_chunk(p.lo + at, p.ld, q, v);
@@ -437,7 +445,8 @@ cudaError_t iterate(const Layout& l, long long batch, long long rows, long long 
         e = gemm::launch<EpiPoly>(Product{ao, ao, r, r, r, nb, 1}, pp, st);
         if (e != cudaSuccess) break;
         const Operand bo = {ob, r, r, l.ldr, l.as, false, false};
-        const UpdateParams u = {x[0], lo, x[1], db, l.ldx, l.xs, ns.a, tall, r};
+        const UpdateParams u = {x[0], lo, x[1], db, l.ldx, l.xs, ns.a, tall, r, keeps_lo(i, ns.steps),
+                                keeps_lo(i + 1, ns.steps)};
         const Operand &left = tall ? xk : bo, &right = tall ? bo : xm;
         if (i + 1 < ns.steps) {
             e = gemm::launch<EpiUpdate>(Product{left, right, (int)rows, (int)cols, r, nb, 1}, u, st);
