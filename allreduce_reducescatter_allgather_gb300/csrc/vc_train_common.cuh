@@ -83,8 +83,7 @@ inline gemm::View view_of(const vc_matrix_t* m) {
 inline size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Row length, in 16-bit values, of operands laid out in the workspace: whole 128
-// bytes, the width of a TMA box (rows at other offsets make it read a line
-// more: a product of K = 7710 took 67 us instead of NEWT).
+// bytes, the width of a TMA box, whose rows then do not straddle lines.
 inline long long padded_ld(long long cols) { return (cols + 63) / 64 * 64; }
 
 // ------------------------------------------------------------ activations --

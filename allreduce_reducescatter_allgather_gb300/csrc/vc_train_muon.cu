@@ -50,36 +50,122 @@ struct PrepareParams {
     __half *hi, *lo;
     long long ld, batch_stride;  // of hi and lo
     float size, eps;             // X is stored times size / (norm + eps)
-    int rows, cols, vpr;         // vpr: groups of four columns per row
+    int rows, cols;
+    int lanes;  // lanes that share a row, a power of two; 8 columns each at a time
 };
 
-// Groups of four columns that a thread loads before it stores the first.
-constexpr int kPrepareBatch = 4;
-
-struct Loaded {
-    float4 g, m;
-    unsigned row;
-    int col, n;  // n: columns of the group, 0 beyond the matrix
+// Eight consecutive values of a row: n of them are there.
+struct Eight {
+    float v[8];
 };
-__device__ __forceinline__ void load_batch(const PrepareParams& p, int b, unsigned first,
-                                           Loaded (&x)[kPrepareBatch]) {
-    const unsigned total = (unsigned)p.rows * (unsigned)p.vpr;
+__device__ __forceinline__ Eight load_eight(const View& x, int b, long long row, int col, int n) {
+    Eight r;
+    const long long at = (long long)b * x.batch_stride + row * x.ld + col;
+    if (x.f32) {
+        const float* p = static_cast<const float*>(x.data) + at;
+        if (x.vec16 && n == 8) {
+            const float4 lo = *reinterpret_cast<const float4*>(p);
+            const float4 hi = *reinterpret_cast<const float4*>(p + 4);
+            return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+        }
 #pragma unroll
-    for (int k = 0; k < kPrepareBatch; ++k) {
-        const unsigned i = first + k * gridDim.x * 256;
-        x[k].g = x[k].m = make_float4(0.f, 0.f, 0.f, 0.f);
-        x[k].n = 0;
-        if (i >= total) continue;
-        x[k].row = i / (unsigned)p.vpr;
-        x[k].col = (int)(i - x[k].row * (unsigned)p.vpr) * 4;
-        x[k].n = min(4, p.cols - x[k].col);
-        x[k].g = gemm::view_load(p.g, b, x[k].row, x[k].col, x[k].n);
-        if (p.has_momentum) x[k].m = gemm::view_load(p.m, b, x[k].row, x[k].col, x[k].n);
+        for (int j = 0; j < 8; ++j) r.v[j] = j < n ? p[j] : 0.0f;
+    } else {
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x.data) + at;
+        if (x.vec16 && n == 8) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p);
+            const unsigned w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r.v[2 * j] = __uint_as_float(w[j] << 16);
+                r.v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+            return r;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.v[j] = j < n ? __bfloat162float(p[j]) : 0.0f;
+    }
+    return r;
+}
+// Stores them; r becomes what was stored.
+__device__ __forceinline__ void store_eight(const View& x, int b, long long row, int col, int n,
+                                            Eight& r) {
+    const long long at = (long long)b * x.batch_stride + row * x.ld + col;
+    if (x.f32) {
+        float* p = static_cast<float*>(x.data) + at;
+        if (x.vec16 && n == 8) {
+            *reinterpret_cast<float4*>(p) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) p[j] = r.v[j];
+        }
+    } else {
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(x.data) + at;
+        unsigned w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = gemm::packed(r.v[2 * j], r.v[2 * j + 1], __nv_bfloat16());
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r.v[2 * j] = __uint_as_float(w[j] << 16);
+            r.v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+        if (x.vec16 && n == 8) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) p[j] = __float2bfloat16(r.v[j]);
+        }
     }
 }
-// The update's value, m being the new momentum.
-__device__ __forceinline__ float4 update_of(const PrepareParams& p, float4 g, float4 m) {
-    return !p.has_momentum ? g : p.nesterov ? new_momentum(p.beta, g, m) : m;
+
+// beta m + g: the new momentum, or, with that for m, the Nesterov update.
+__device__ __forceinline__ Eight axpy(float beta, const Eight& m, const Eight& g) {
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.v[j] = fmaf(beta, m.v[j], g.v[j]);
+    return r;
+}
+
+// A thread's groups of eight columns, one after the other: along the rows that
+// its lanes take, `lanes` groups at a time.
+struct Groups {
+    int row, col, first_col, row_step, col_step;
+    __device__ __forceinline__ explicit Groups(const PrepareParams& p) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = 32 / p.lanes;
+        row = (blockIdx.x * 8 + warp) * per + lane / p.lanes;
+        col = first_col = (lane % p.lanes) * 8;
+        row_step = gridDim.x * 8 * per;
+        col_step = p.lanes * 8;
+    }
+    __device__ __forceinline__ void next(const PrepareParams& p) {
+        col += col_step;
+        if (col >= p.cols) col = first_col, row += row_step;
+    }
+};
+
+// Groups that a thread loads before it stores the first.
+constexpr int kPrepareBatch = 2;
+
+struct Loaded {
+    Eight g, m;
+    int row, col, n;  // n: values of the group, 0 beyond the matrix
+};
+__device__ __forceinline__ void load_batch(const PrepareParams& p, int b, Groups& at,
+                                           Loaded (&x)[kPrepareBatch]) {
+#pragma unroll
+    for (int k = 0; k < kPrepareBatch; ++k) {
+        x[k].row = at.row;
+        x[k].col = at.col;
+        x[k].n = at.row < p.rows ? max(0, min(8, p.cols - at.col)) : 0;
+        if (x[k].n > 0) {
+            x[k].g = load_eight(p.g, b, at.row, at.col, x[k].n);
+            if (p.has_momentum) x[k].m = load_eight(p.m, b, at.row, at.col, x[k].n);
+        }
+        at.next(p);
+    }
 }
 
 __device__ __forceinline__ float block_sum(float v, float* tmp) {
@@ -99,23 +185,22 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ P
     __shared__ float tmp[8];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const unsigned total = (unsigned)p.rows * (unsigned)p.vpr;
     const int b = blockIdx.y;
     float sum = 0.0f;
-    for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < total; i += kPrepareBatch * gridDim.x * 256) {
+    for (Groups at(p); at.row < p.rows;) {
         Loaded x[kPrepareBatch];
-        load_batch(p, b, i, x);
+        load_batch(p, b, at, x);
 #pragma unroll
         for (int k = 0; k < kPrepareBatch; ++k) {
             if (x[k].n == 0) continue;
-            float4 m = x[k].m;
+            Eight u = x[k].g;
             if (p.has_momentum) {
-                m = new_momentum(p.beta, x[k].g, m);
-                gemm::view_store(p.m, b, x[k].row, x[k].col, x[k].n, m);
-                m = as_stored(p.m, m);
+                Eight m = axpy(p.beta, x[k].m, x[k].g);
+                store_eight(p.m, b, x[k].row, x[k].col, x[k].n, m);
+                u = p.nesterov ? axpy(p.beta, m, x[k].g) : m;
             }
-            const float4 u = update_of(p, x[k].g, m);  // zero beyond n
-            sum += u.x * u.x + u.y * u.y + u.z * u.z + u.w * u.w;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fmaf(u.v[j], u.v[j], sum);  // 0 beyond n
         }
     }
     sum = block_sum(sum, tmp);
@@ -128,25 +213,29 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Prep
     __shared__ float tmp[8];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const unsigned total = (unsigned)p.rows * (unsigned)p.vpr;
     const int b = blockIdx.y;
     float sum = 0.0f;
     for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) sum += p.parts[b * gridDim.x + i];
     const float scale = p.size / (sqrtf(block_sum(sum, tmp)) + p.eps);
-    for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < total; i += kPrepareBatch * gridDim.x * 256) {
+    for (Groups at(p); at.row < p.rows;) {
         Loaded x[kPrepareBatch];
-        load_batch(p, b, i, x);
+        load_batch(p, b, at, x);
 #pragma unroll
         for (int k = 0; k < kPrepareBatch; ++k) {
             if (x[k].n == 0) continue;
-            float4 u = update_of(p, x[k].g, x[k].m);
-            u = make_float4(u.x * scale, u.y * scale, u.z * scale, u.w * scale);
-            const long long at = (long long)b * p.batch_stride + (long long)x[k].row * p.ld + x[k].col;
-            const float2 h01 = __half22float2(__floats2half2_rn(u.x, u.y));
-            const float2 h23 = __half22float2(__floats2half2_rn(u.z, u.w));
-            gemm::store4(p.hi + at, make_float4(h01.x, h01.y, h23.x, h23.y), x[k].n, true);
-            gemm::store4(p.lo + at, make_float4(u.x - h01.x, u.y - h01.y, u.z - h23.x, u.w - h23.y),
-                         x[k].n, true);
+            const Eight u = !p.has_momentum ? x[k].g : p.nesterov ? axpy(p.beta, x[k].m, x[k].g) : x[k].m;
+            unsigned hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = u.v[2 * j] * scale, c = u.v[2 * j + 1] * scale;
+                hi[j] = gemm::packed(a, c, __half());
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
+                lo[j] = gemm::packed(a - h.x, c - h.y, __half());
+            }
+            // (rows of hi and lo are whole groups; what lies beyond n is read by nobody)
+            const long long to = (long long)b * p.batch_stride + (long long)x[k].row * p.ld + x[k].col;
+            *reinterpret_cast<uint4*>(p.hi + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(p.lo + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
 }
@@ -347,22 +436,26 @@ struct Layout {
     long long r, c;        // smaller and larger side
     long long ldx, ldr;    // row lengths of X and of the r x r matrices
     long long xs, as;      // values from one matrix of the batch to the next
-    int parts;
+    int parts, lanes;
     size_t hi0, hi1, lo, a, b, da, db, sums, bytes;
 };
 
 bool layout_of(long long batch, long long rows, long long cols, Layout* l) {
     if (batch < 0 || rows < 0 || cols < 0) return false;
     if (batch > (1 << 16) - 1 || rows > (1ll << 24) || cols > (1ll << 24)) return false;
-    const long long vpr = (cols + 3) / 4;
-    if (rows * vpr > 0x7FFFFFFFll || batch * rows > 0x3FFFFFFFll) return false;
+    if (batch * rows > 0x3FFFFFFFll) return false;
     l->r = std::min(rows, cols);
     l->c = std::max(rows, cols);
     l->ldx = padded_ld(cols);  // whole chunks of the epilogues, too
     l->ldr = padded_ld(l->r);
     l->xs = rows * l->ldx;
     l->as = l->r * l->ldr;
-    const long long want = (rows * vpr + 256 * kPrepareBatch - 1) / (256 * kPrepareBatch), fit = std::max(1ll, 152 * 8 / std::max(1ll, batch));
+    l->lanes = 1;
+    while (l->lanes < 32 && l->lanes * 8 < cols) l->lanes *= 2;
+    const long long per_block = 8 * (32 / l->lanes);  // rows
+    // up to 8 blocks per SM over the batch
+    const long long want = (rows + per_block - 1) / per_block;
+    const long long fit = std::max(1ll, 152 * 8 / std::max(1ll, batch));
     l->parts = (int)std::max(1ll, std::min({want, fit, (long long)kMaxParts}));
     const size_t x = round256((size_t)batch * l->xs * 2), a = round256((size_t)batch * l->as * 2);
     const size_t d = round256((size_t)batch * l->r * 4);
@@ -427,7 +520,7 @@ cudaError_t iterate(const Layout& l, long long batch, long long rows, long long 
     p.eps = ns.eps;
     p.rows = (int)rows;
     p.cols = (int)cols;
-    p.vpr = (int)((cols + 3) / 4);
+    p.lanes = l.lanes;
     const dim3 grid(l.parts, (unsigned)batch);
     cudaError_t e = launch_pdl(momentum_kernel, grid, dim3(256), st, p);
     if (e == cudaSuccess) e = launch_pdl(scale_kernel, grid, dim3(256), st, p);

@@ -285,6 +285,20 @@ def test_backward_of_no_rows(env):
         assert (dw == 0).all() and (db == 0).all()
 
 
+def test_backward_of_no_features(env):
+    """No outputs: dx is zero; no inputs: db alone is left."""
+    torch, vc, dev = env
+    none = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=dev)  # noqa: E731
+    dx = torch.ones(30, 70, dtype=torch.bfloat16, device=dev)
+    vc.vc_linear_backward(none(30, 0), rand(torch, dev, 30, 70), none(0, 70), dx=dx,
+                          dweight=none(0, 70))
+    assert (dx == 0).all()
+    dy, db = rand(torch, dev, 30, 20), torch.empty(20, device=dev)
+    vc.vc_linear_backward(dy, none(30, 0), none(20, 0), dx=none(30, 0), dweight=none(20, 0),
+                          dbias=db)
+    check(db, dy.double().sum(0), 40 * 2.0 ** -24 * dy.double().abs().sum(0), "dbias")
+
+
 @pytest.mark.parametrize("name", ACTS[1:])
 def test_gradient_against_differences(env, name):
     """Along random directions the gradients agree with central differences of
