@@ -1070,26 +1070,42 @@ struct Split {
 // rank, rank + ranks, ... (neighbours in memory at about the same time).  The tile's 32 x 32 chunks are shared out over the
 // blocks: each sends its partial chunks to their owners, who add them in rank
 // order and run the epilogue.
-template <int kBN, class Epi>
+//
+// One or two products in a launch: clusters from `second` on work on the second.
+template <class Epi, int kCount>
+struct SplitWork {
+    Shape s[kCount];
+    typename Epi::Params ep[kCount];
+    int second, ranks, stages;
+    unsigned* timeouts;
+};
+
+template <int kBN, class Epi, int kCount>
 __global__ void __launch_bounds__(Split<kBN>::kThreads, Split<kBN>::kBlocksPerSm)
-split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-             const __grid_constant__ Shape s, const __grid_constant__ typename Epi::Params ep,
-             unsigned* timeouts, int ranks, int stages) {
+split_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_b0,
+             const __grid_constant__ CUtensorMap map_a1, const __grid_constant__ CUtensorMap map_b1,
+             const __grid_constant__ SplitWork<Epi, kCount> w) {
     using C = Split<kBN>;
     // (aligned by its declaration: rounding up would cost a stage of two blocks)
     extern __shared__ __align__(1024) unsigned char smem_aligned[];
     const unsigned base = smem_u32(smem_aligned);
     unsigned char* const gen = smem_aligned;
-    float4* const part = reinterpret_cast<float4*>(gen + stages * C::kStageBytes);
-    unsigned char* const chunks = gen + stages * C::kStageBytes + C::kPartBytes;
-    const unsigned full = base + stages * C::kStageBytes + C::kPartBytes + C::kChunkBytes;
+    float4* const part = reinterpret_cast<float4*>(gen + w.stages * C::kStageBytes);
+    unsigned char* const chunks = gen + w.stages * C::kStageBytes + C::kPartBytes;
+    const unsigned full = base + w.stages * C::kStageBytes + C::kPartBytes + C::kChunkBytes;
     const unsigned empty = full + 8 * C::kMaxStages, tfull = empty + 8 * C::kMaxStages;
     unsigned char* const tail = gen + (tfull + 8 - base);
     unsigned* const tmem_slot = reinterpret_cast<unsigned*>(tail);
     volatile int* const dead = reinterpret_cast<volatile int*>(tail + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
+    const int rank = (int)cluster_rank(), ranks = w.ranks, stages = w.stages;
+    const int cluster = blockIdx.x / ranks;
+    const int which = kCount == 2 && cluster >= w.second ? 1 : 0;
+    const Shape s = w.s[which];
+    const typename Epi::Params& ep = w.ep[which];
+    const CUtensorMap* const map_a = which ? &map_a1 : &map_a0;
+    const CUtensorMap* const map_b = which ? &map_b1 : &map_b0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
             mbar_init(full + 8 * i, 1);
@@ -1098,8 +1114,8 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         mbar_init(tfull, 1);
         *dead = (base & 1023) != 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        tma_prefetch(&map_a);
-        tma_prefetch(&map_b);
+        tma_prefetch(map_a);
+        tma_prefetch(map_b);
     }
     if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), C::kTmemCols);
     tcgen05_fence_before();
@@ -1113,7 +1129,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    const int tile = blockIdx.x / ranks;
+    const int tile = which ? cluster - w.second : cluster;
     const int b = tile / s.tiles;
     int tm, tn;
     tile_at<Epi::kSym, C::kBM / C::kBN>(s, tile - b * s.tiles, tm, tn);
@@ -1139,7 +1155,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             if (!warp_wait(empty + 8 * stage, phase ^ 1, dead)) break;
             if (elect_one()) {
                 mbar_expect(full + 8 * stage, C::kStageBytes);
-                load_stage<1, kBN>(base + stage * C::kStageBytes, &map_a, &map_b, s,
+                load_stage<1, kBN>(base + stage * C::kStageBytes, map_a, map_b, s,
                                    full + 8 * stage, m0, n0, kb, b);
             }
             __syncwarp();
@@ -1224,7 +1240,7 @@ split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         __syncthreads();
     }
     tcgen05_fence_after();
-    bury(dead, timeouts);
+    bury(dead, w.timeouts);
     if (warp == 1) tmem_free<1>(tmem, C::kTmemCols);
 }
 
@@ -1362,23 +1378,30 @@ cudaError_t launch_pair(const Product* p, const typename Epi::Params* ep, int se
                           m[2], m[3], w);
 }
 
-template <int kBN, class Epi>
-cudaError_t launch_split(const Product& p, const typename Epi::Params& ep, int ranks,
+template <int kBN, class Epi, int kCount>
+cudaError_t launch_split(const Product* p, const typename Epi::Params* ep, int ranks,
                          cudaStream_t st) {
     using C = Split<kBN>;
-    Shape s;
-    const cudaError_t e = shape_of(p, C::kBM, C::kBN, Epi::kSym, &s);
-    if (e != cudaSuccess) return e;
-    if (s.total == 0) return cudaSuccess;
-    CUtensorMap ma, mb;
-    if (!encode_product(p, kBN, &ma, &mb)) return cudaErrorInvalidValue;
-    unsigned* timeouts = timeout_counter();
-    if (timeouts == nullptr) return cudaErrorInvalidConfiguration;
-    const int blocks = s.total * ranks;
-    const int stages = blocks <= device_sms() ? C::kManyStages : C::kFewStages;
-    return launch_cluster(split_kernel<kBN, Epi>, blocks, C::kThreads, ranks,
-                          C::kFixed + stages * C::kStageBytes, st, ma, mb, s, ep, timeouts, ranks,
-                          stages);
+    SplitWork<Epi, kCount> w = {};
+    CUtensorMap m[4] = {};
+    int clusters = 0;
+    for (int i = 0; i < kCount; ++i) {
+        const cudaError_t e = shape_of(p[i], C::kBM, C::kBN, Epi::kSym, &w.s[i]);
+        if (e != cudaSuccess) return e;
+        if (!encode_product(p[i], kBN, &m[2 * i], &m[2 * i + 1])) return cudaErrorInvalidValue;
+        w.ep[i] = ep[i];
+        if (i == 0) w.second = w.s[0].total;
+        clusters += w.s[i].total;
+    }
+    if (clusters == 0) return cudaSuccess;
+    if (clusters > 0x0FFFFFFF) return cudaErrorInvalidValue;
+    const int blocks = clusters * ranks;
+    w.ranks = ranks;
+    w.stages = blocks <= device_sms() ? C::kManyStages : C::kFewStages;
+    w.timeouts = timeout_counter();
+    if (w.timeouts == nullptr) return cudaErrorInvalidConfiguration;
+    return launch_cluster(split_kernel<kBN, Epi, kCount>, blocks, C::kThreads, ranks,
+                          C::kFixed + w.stages * C::kStageBytes, st, m[0], m[1], m[2], m[3], w);
 }
 
 // How long a product takes, in microseconds, by a model of the kernels that was
@@ -1415,46 +1438,58 @@ inline double pair_us(const Product* p, int count, bool sym, bool odd) {
     return fixed + (even > longest ? even : longest);
 }
 
-// The split kernel's best tile and number of ranks; limit > 0: at most so many
-// K blocks per rank (1e9 us where 8 ranks do not reach that).
-inline Plan plan_split(const Product& p, bool sym, bool odd, int limit) {
-    const int kblocks = k_blocks(p), sms = device_sms();
+// The split kernel's best tile and number of ranks for one product or two in a
+// launch; limit[i] > 0: at most so many K blocks per rank of product i (1e9 us
+// where 8 ranks do not reach that).
+inline Plan plan_split(const Product* p, int count, bool sym, bool odd, const int* limit) {
+    const int sms = device_sms();
     Plan best = {1e9, 64, 1};
     for (int tile = 64; tile <= 128; tile += 64) {
-        const long long tiles = tile_count(p.M, p.N, kRowsPerCta, tile, sym) * p.batch;
         for (int ranks = 1; ranks <= 8; ranks += ranks == 3 ? 1 : ranks > 3 ? 4 : 1) {
             if (ranks == 3 && tile == 64) continue;
-            const int kb = (kblocks + ranks - 1) / ranks;
-            if (limit > 0 && kb > limit) continue;
-            const long long blocks = tiles * ranks;
+            long long blocks = 0;
+            double sum = 0.0;  // K blocks of all ranks
+            int most = 0;      // of one
+            bool fits = true;
+            for (int i = 0; i < count; ++i) {
+                const long long mine = tile_count(p[i].M, p[i].N, kRowsPerCta, tile, sym) * p[i].batch * ranks;
+                const int kb = (k_blocks(p[i]) + ranks - 1) / ranks;
+                fits = fits && (limit == nullptr || limit[i] == 0 || kb <= limit[i]);
+                blocks += mine;
+                sum += (double)mine * kb;
+                most = kb > most ? kb : most;
+            }
+            if (!fits) continue;
+            // blocks are shared out whole: up to two per SM the fullest one counts
+            const double per_sm = blocks > 2 * sms ? (double)blocks / sms
+                                                   : (double)((blocks + sms - 1) / sms);
+            const double even = blocks > 0 ? sum / (double)blocks * per_sm : 0.0;
+            const double kb = even > most ? even : most;
             const double epilogue = (odd ? 2.5 : 0.0) / ranks;
             double us = 1.5 + (ranks > 1 ? 0.7 : 0.0);
-            if (tile == 64) {
-                const double per_sm = blocks > 2 * sms ? (double)blocks / sms
-                                                       : (double)((blocks + sms - 1) / sms);
-                us += (2.3 + epilogue) * (double)((blocks + 2 * sms - 1) / (2 * sms)) + 0.2 * per_sm * kb;
-            } else {
-                us += (2.8 + epilogue + 0.28 * kb) * (double)((blocks + sms - 1) / sms);
-            }
+            if (tile == 64)
+                us += (2.3 + epilogue) * (double)((blocks + 2 * sms - 1) / (2 * sms)) + 0.2 * kb;
+            else
+                us += (2.8 + epilogue) * (double)((blocks + sms - 1) / sms) + 0.28 * kb;
             if (us < best.us) best = {us, tile, ranks};
         }
     }
     return best;
 }
 
-template <class Epi>
-cudaError_t launch_planned(const Product& p, const typename Epi::Params& ep, const Plan& plan,
+template <class Epi, int kCount>
+cudaError_t launch_planned(const Product* p, const typename Epi::Params* ep, const Plan& plan,
                            cudaStream_t st) {
-    if (plan.tile == 128) return launch_split<128, Epi>(p, ep, plan.ranks, st);
-    return launch_split<64, Epi>(p, ep, plan.ranks, st);
+    if (plan.tile == 128) return launch_split<128, Epi, kCount>(p, ep, plan.ranks, st);
+    return launch_split<64, Epi, kCount>(p, ep, plan.ranks, st);
 }
 
 // Picks the kernel, the tile and the ranks.
 template <class Epi>
 cudaError_t launch(const Product& p, const typename Epi::Params& ep, cudaStream_t st) {
     const bool odd = Epi::odd(ep);
-    const Plan split = plan_split(p, Epi::kSym, odd, 0);
-    if (split.us < pair_us(&p, 1, Epi::kSym, odd)) return launch_planned<Epi>(p, ep, split, st);
+    const Plan split = plan_split(&p, 1, Epi::kSym, odd, nullptr);
+    if (split.us < pair_us(&p, 1, Epi::kSym, odd)) return launch_planned<Epi, 1>(&p, &ep, split, st);
     return launch_pair<Epi, 1, false>(&p, &ep, 0, st);
 }
 
@@ -1468,8 +1503,8 @@ cudaError_t launch_skinny(const Product& p, const typename Epi::Params& ep, cuda
     const long long tiles = tile_count(p.M, 1, kRowsPerCta, 64, false);
     int ranks = 1;
     while (ranks < 8 && tiles * ranks * 2 <= device_sms() && ranks * 2 <= k_blocks(p)) ranks *= 2;
-    if (p.N <= 32) return launch_split<32, Epi>(p, ep, ranks, st);
-    return launch_split<64, Epi>(p, ep, ranks, st);
+    if (p.N <= 32) return launch_split<32, Epi, 1>(&p, &ep, ranks, st);
+    return launch_split<64, Epi, 1>(&p, &ep, ranks, st);
 }
 
 }  // namespace gemm

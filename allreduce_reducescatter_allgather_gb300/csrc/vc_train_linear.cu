@@ -593,18 +593,16 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
     if (count > 0) {
         // 32-bit sums are not left to the tensor cores for longer than a segment
         const bool promote = dweight != nullptr && dweight->dtype == VC_FLOAT32;
-        gemm::Plan plan[2];
-        double apart = 2.5 * (count - 1);  // what a second launch costs
+        int limit[2] = {0, 0};
         bool odd = false;
         for (int i = 0; i < count; ++i) {
-            const bool sums = promote && ep[i].out.f32;
-            plan[i] = gemm::plan_split(p[i], false, !ep[i].out.vec16, sums ? kSegment : 0);
+            if (ep[i].out.f32) limit[i] = kSegment;
             odd = odd || !ep[i].out.vec16;
-            apart += plan[i].us;
         }
-        if (apart < gemm::pair_us(p, count, false, odd)) {
-            for (int i = 0; i < count && e == cudaSuccess; ++i)
-                e = gemm::launch_planned<EpiStore<false>>(p[i], ep[i], plan[i], st);
+        const gemm::Plan plan = gemm::plan_split(p, count, false, odd, limit);
+        if (plan.us < gemm::pair_us(p, count, false, odd)) {
+            e = count == 2 ? gemm::launch_planned<EpiStore<false>, 2>(p, ep, plan, st)
+                           : gemm::launch_planned<EpiStore<false>, 1>(p, ep, plan, st);
         } else if (count == 2) {
             e = promote ? gemm::launch_pair<EpiStore<false>, 2, true>(p, ep, kSegment, st)
                         : gemm::launch_pair<EpiStore<false>, 2, false>(p, ep, 0, st);
