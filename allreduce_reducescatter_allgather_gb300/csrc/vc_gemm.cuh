@@ -54,6 +54,7 @@ struct Shape {
     int per_plane;          // ceil(K / 64)
     int segment;            // K blocks summed in tensor memory at a time
     int a_mn, b_mn;         // operand is MN-major
+    int planes_of_b;        // the operand that is a sum of planes is B, not A
     unsigned idesc;         // instruction descriptor
 };
 
@@ -716,28 +717,30 @@ struct Ring {
     }
 };
 
-// One stage: 128 rows of A and kBRows of B, K block kb of product b.  (Where A
-// is a sum of two planes, its blocks follow each other and B's are read again.)
+// One stage: 128 rows of A and kBRows of B, K block kb of product b.  (Where an
+// operand is a sum of two planes, its blocks follow each other and the other's
+// are read again.)
 template <int kPair, int kBRows>
 __device__ __forceinline__ void load_stage(unsigned sa, const CUtensorMap* map_a,
                                            const CUtensorMap* map_b, const Shape& s, unsigned bar,
                                            int m0, int n0, int kb, int b) {
     const int plane = kb >= s.per_plane;
     const int k0 = (kb - (plane ? s.per_plane : 0)) * kBlockK;
+    const int za = b + (plane & (s.planes_of_b ^ 1)), zb = b + (plane & s.planes_of_b);
     const unsigned sb = sa + kRowsPerCta * kBlockK * 2;
     if (s.a_mn) {
 #pragma unroll
         for (int i = 0; i < kRowsPerCta / 64; ++i)
-            tma_load<kPair>(sa + i * kBlockK * 128, map_a, bar, m0 + 64 * i, k0, b + plane);
+            tma_load<kPair>(sa + i * kBlockK * 128, map_a, bar, m0 + 64 * i, k0, za);
     } else {
-        tma_load<kPair>(sa, map_a, bar, k0, m0, b + plane);
+        tma_load<kPair>(sa, map_a, bar, k0, m0, za);
     }
     if (s.b_mn) {
 #pragma unroll
         for (int i = 0; i < (kBRows + 63) / 64; ++i)
-            tma_load<kPair>(sb + i * kBlockK * 128, map_b, bar, n0 + 64 * i, k0, b);
+            tma_load<kPair>(sb + i * kBlockK * 128, map_b, bar, n0 + 64 * i, k0, zb);
     } else {
-        tma_load<kPair>(sb, map_b, bar, k0, n0, b);
+        tma_load<kPair>(sb, map_b, bar, k0, n0, zb);
     }
 }
 
@@ -1256,10 +1259,12 @@ struct Operand {
 };
 
 // One product D[M, N] = A[M, K] B[K, N], or a batch of them; or, with planes =
-// 2 and a batch of one, D = (A_0 + A_1) B, A's planes batch_stride apart.
+// 2 and a batch of one, D = (A_0 + A_1) B, A's planes batch_stride apart (or, with
+// planes_of_b, A (B_0 + B_1)).
 struct Product {
     Operand a, b;
     int M, N, K, batch, planes;
+    bool planes_of_b = false;
 };
 inline int k_blocks(const Product& p) { return (p.K + kBlockK - 1) / kBlockK * p.planes; }
 
@@ -1306,6 +1311,7 @@ inline cudaError_t shape_of(const Product& p, int bm, int bn, bool sym, Shape* s
     s->segment = s->kblocks > 0 ? s->kblocks : 1;
     s->a_mn = p.a.mn_major;
     s->b_mn = p.b.mn_major;
+    s->planes_of_b = p.planes_of_b;
     s->idesc = instruction_desc(p.a.bf16, p.a.mn_major, p.b.mn_major, bm, bn);
     return cudaSuccess;
 }
@@ -1314,8 +1320,9 @@ inline bool encode_product(const Product& p, int b_rows, CUtensorMap* ma, CUtens
     *ma = CUtensorMap{};
     *mb = CUtensorMap{};
     if (p.K == 0) return true;  // nothing is loaded
-    return encode_operand(ma, p.a, p.batch * p.planes, p.a.mn_major ? kBlockK : kRowsPerCta) &&
-           encode_operand(mb, p.b, p.batch, p.b.mn_major ? kBlockK : b_rows);
+    const int pa = p.planes_of_b ? 1 : p.planes, pb = p.planes_of_b ? p.planes : 1;
+    return encode_operand(ma, p.a, p.batch * pa, p.a.mn_major ? kBlockK : kRowsPerCta) &&
+           encode_operand(mb, p.b, p.batch * pb, p.b.mn_major ? kBlockK : b_rows);
 }
 
 // Lets the kernel have all of an SM's shared memory, once per device.
@@ -1493,18 +1500,26 @@ cudaError_t launch(const Product& p, const typename Epi::Params& ep, cudaStream_
     return launch_pair<Epi, 1, false>(&p, &ep, 0, st);
 }
 
-// A product with few columns: tiles 32 or 64 across.  It is bound by reading A
-// once, so K is split until every SM has a block (with many stages in flight),
-// but not further: 32 columns, 4096 rows and K = 4096 from memory take 10.1 us
-// with 4 ranks (128 blocks of 6 stages) and 10.9 us with 8 (256 of 3), 17.8 us
-// with 1.
+// A product with few columns (up to 64): tiles 32 or 64 across.  It is bound by
+// reading A once, so K is split until every SM has a block (with many stages in
+// flight), but not further: 32 columns, 4096 rows and K = 4096 from memory take
+// 10.1 us with 4 ranks (128 blocks of 6 stages) and 10.9 us with 8 (256 of 3),
+// 17.8 us with 1.
+inline Plan plan_skinny(const Product& p) {
+    const long long tiles = (p.M + kRowsPerCta - 1) / kRowsPerCta;
+    const int sms = device_sms();
+    int ranks = 1;
+    while (ranks < 8 && tiles * ranks * 2 <= sms && ranks * 2 <= k_blocks(p)) ranks *= 2;
+    const double kb = (double)((k_blocks(p) + ranks - 1) / ranks);
+    return {3.8 + (ranks > 1 ? 0.7 : 0.0) + 0.2 * kb * (double)((tiles * ranks + sms - 1) / sms),
+            p.N <= 32 ? 32 : 64, ranks};
+}
+
 template <class Epi>
 cudaError_t launch_skinny(const Product& p, const typename Epi::Params& ep, cudaStream_t st) {
-    const long long tiles = tile_count(p.M, 1, kRowsPerCta, 64, false);
-    int ranks = 1;
-    while (ranks < 8 && tiles * ranks * 2 <= device_sms() && ranks * 2 <= k_blocks(p)) ranks *= 2;
-    if (p.N <= 32) return launch_split<32, Epi, 1>(&p, &ep, ranks, st);
-    return launch_split<64, Epi, 1>(&p, &ep, ranks, st);
+    const Plan plan = plan_skinny(p);
+    if (plan.tile == 32) return launch_split<32, Epi, 1>(&p, &ep, plan.ranks, st);
+    return launch_split<64, Epi, 1>(&p, &ep, plan.ranks, st);
 }
 
 }  // namespace gemm

@@ -248,6 +248,27 @@ def test_backward(env, m, n, k, i):
     check(db, want, bound + half * (want.abs() + bound), "dbias")
 
 
+@pytest.mark.parametrize("m", [1, 8, 33, 64])
+@pytest.mark.parametrize("n,k", [(4096, 256), (2113, 1000), (64, 3000), (300, 65)])
+@pytest.mark.parametrize("name", ["none", "gelu"])
+def test_backward_of_few_rows(env, m, n, k, name):
+    """dx by itself and with dW: the same values within the bounds, by
+    whichever kernel."""
+    torch, vc, dev = env
+    dy, z = rand(torch, dev, m, n, seed=1), rand(torch, dev, m, n, seed=2)
+    x, w = rand(torch, dev, m, k, seed=3), rand(torch, dev, n, k, seed=4, std=n ** -0.5)
+    dz = dy.double() * act(torch, z.double(), name)[1]
+    off = 0.0 if name == "none" else dy.double().abs() * 2.0 ** -19 + dz.abs() * 2.0 ** -16
+    want = dz @ w.double()
+    bound = accumulate_bound(2 * n, dz.abs() @ w.double().abs())
+    bound = bound + (0.0 if name == "none" else off @ w.double().abs())
+    for dw in (None, torch.empty(n, k, device=dev)):
+        dx = torch.full((m, k + 3), 9.0, dtype=torch.bfloat16, device=dev)
+        vc.vc_linear_backward(dy, x, w, dx=dx[:, :k], dweight=dw, preact=z, activation=name)
+        check(dx[:, :k], want, bound + BF16 * (want.abs() + bound), "dx")
+        assert (dx[:, k:] == 9).all()
+
+
 def test_backward_parts_alone_and_strided(env):
     """Each output by itself gives the same bits as all together; gradients are
     written into the views of a bucket, whose other values stay."""
