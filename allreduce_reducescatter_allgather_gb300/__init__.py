@@ -5,6 +5,10 @@ hand-written sm_103a kernels (libvc.so, C ABI in include/vc.h) that read the
 N buffers with 16-byte vector loads and reduce them in registers in a fixed
 order (ring, recursive halving or tree).  This package is the thin ctypes
 binding with the same names as the C entry points.
+
+Beside them, the operators of a data-parallel training step (include/vc_train.h,
+training.py): the linear layer, its gradient, Newton-Schulz orthogonalisation and
+the Muon step, on the tensor cores.
 """
 from ._binding import (  # noqa: F401
     BucketPlan,

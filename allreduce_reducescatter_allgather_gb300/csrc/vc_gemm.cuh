@@ -328,20 +328,6 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p, int n, bool vec)
     if (n > 3) v.w = __bfloat162float(p[3]);
     return v;
 }
-__device__ __forceinline__ float4 load4(const __half* p, int n, bool vec) {
-    if (vec && n == 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-        return make_float4(a.x, a.y, b.x, b.y);
-    }
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    v.x = __half2float(p[0]);
-    if (n > 1) v.y = __half2float(p[1]);
-    if (n > 2) v.z = __half2float(p[2]);
-    if (n > 3) v.w = __half2float(p[3]);
-    return v;
-}
 __device__ __forceinline__ void store4(float* p, float4 v, int n, bool vec) {
     if (vec && n == 4) {
         *reinterpret_cast<float4*>(p) = v;
@@ -366,21 +352,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v, int n, bool v
     if (n > 2) p[2] = b.x;
     if (n > 3) p[3] = b.y;
 }
-__device__ __forceinline__ void store4(__half* p, float4 v, int n, bool vec) {
-    const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-    if (vec && n == 4) {
-        uint2 u;
-        u.x = *reinterpret_cast<const unsigned*>(&a);
-        u.y = *reinterpret_cast<const unsigned*>(&b);
-        *reinterpret_cast<uint2*>(p) = u;
-        return;
-    }
-    p[0] = a.x;
-    if (n > 1) p[1] = a.y;
-    if (n > 2) p[2] = b.x;
-    if (n > 3) p[3] = b.y;
-}
-
 // A matrix that an epilogue reads or writes: float or bf16 by a flag.
 struct View {
     void* data;

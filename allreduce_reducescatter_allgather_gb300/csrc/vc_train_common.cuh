@@ -112,7 +112,7 @@ __device__ __forceinline__ float positive(float z) { return z <= 0.0f ? 0.0f : z
 // The activations in three families, so that a kernel holds the arithmetic of
 // one and no element branches: piecewise (none, relu, relu2), logistic (silu
 // and the tanh form of gelu, z / (1 + exp(-k z (1 + c z^2)))), and erf.
-enum { kFamilyPiecewise = 0, kFamilyLogistic = 1, kFamilyErf = 2 };
+enum { kFamilyPiecewise = 0, kFamilyLogistic = 1, kFamilyErf = 2, kNoActivation = 3 };
 
 inline int act_family(int act) {
     return act == VC_ACT_GELU ? kFamilyErf

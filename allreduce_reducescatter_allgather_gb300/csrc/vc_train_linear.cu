@@ -259,7 +259,7 @@ struct DzParams {
     float* sums;  // [gridDim.y][N], or NULL
     SumJob direct;  // with one row of blocks: where the sums go at once
     long long rows, cols;
-    int has_act, vec16;
+    int vec16;
     Act act;
 };
 
@@ -268,8 +268,9 @@ constexpr int kDzRows = 4;  // rows that a thread loads before it uses them
 // dz = dy * act'(z) and the column sums of each block's rows.  A warp covers
 // 256 columns (8 per lane); the block's eight warps take groups of rows in
 // turn.
+// kNoActivation: dz is dy, and the kernel needs half the registers.
 template <int kFamily>
-__global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzParams p) {
+__global__ void __launch_bounds__(256, kFamily == kNoActivation ? 6 : 3) dz_kernel(const __grid_constant__ DzParams p) {
     __shared__ float4 part[8][64];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -299,19 +300,18 @@ __global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzPa
         for (int u = 0; u < kDzRows; ++u) {
             if (row0 + u >= p.rows) continue;
             a[u] = load8(dy + (row0 + u) * p.dy.ld);
-            if (p.has_act) b[u] = load8(z + (row0 + u) * p.preact.ld);
+            if constexpr (kFamily != kNoActivation) b[u] = load8(z + (row0 + u) * p.preact.ld);
         }
 #pragma unroll
         for (int u = 0; u < kDzRows; ++u) {
             if (row0 + u >= p.rows) continue;
             const unsigned aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
-            const unsigned bw[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
             unsigned hi[4], rest[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float2 v = low(aw[j]);
-                if (p.has_act) {
-                    const float2 k = act_slope<kFamily>(low(bw[j]), p.act);
+                if constexpr (kFamily != kNoActivation) {
+                    const float2 k = act_slope<kFamily>(low(j == 0 ? b[u].x : j == 1 ? b[u].y : j == 2 ? b[u].z : b[u].w), p.act);
                     v = make_float2(2 * j < n ? v.x * k.x : 0.0f, 2 * j + 1 < n ? v.y * k.y : 0.0f);
                 }
                 sum[2 * j] += v.x;
@@ -345,11 +345,11 @@ __global__ void __launch_bounds__(256, 3) dz_kernel(const __grid_constant__ DzPa
     }
 }
 
-// Blocks along the rows: enough for the three blocks per SM that fit, each with
-// a group of rows at least for every warp.
-int dz_row_blocks(long long rows, long long cols) {
+// Blocks along the rows: enough for the three blocks per SM that fit (six
+// without an activation), each with a group of rows at least for every warp.
+int dz_row_blocks(long long rows, long long cols, vc_act_t act) {
     const long long across = (cols + 255) / 256;
-    const long long want = (152 * 3 + across - 1) / across;
+    const long long want = (152 * (act == VC_ACT_NONE ? 6 : 3) + across - 1) / across;
     return (int)std::max(1ll, std::min(want, (rows + 8 * kDzRows - 1) / (8 * kDzRows)));
 }
 
@@ -421,7 +421,7 @@ size_t backward_workspace(const vc_matrix_t* dy, const vc_matrix_t* x, const vc_
     size_t need = packed_bytes(x) + packed_bytes(weight);
     if (act != VC_ACT_NONE || !operand_ready(dy))
         need += dz_planes(dy->rows, act) * round256((size_t)dy->rows * padded_ld(dy->cols) * 2);
-    if (has_dbias) need += round256((size_t)dz_row_blocks(dy->rows, dy->cols) * dy->cols * 4);
+    if (has_dbias) need += round256((size_t)dz_row_blocks(dy->rows, dy->cols, act) * dy->cols * 4);
     return need;
 }
 
@@ -533,7 +533,7 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
     const int planes = dz_planes(M, act);
     const long long plane = (long long)(round256((size_t)M * padded_ld(N) * 2) / 2);
     float* sums = nullptr;
-    const int parts = dz_row_blocks(M, N);
+    const int parts = dz_row_blocks(M, N, act);
     if (dbias != nullptr) {
         sums = reinterpret_cast<float*>(ws);
         ws += round256((size_t)parts * N * 4);
@@ -564,9 +564,9 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
         }
         p.rows = M;
         p.cols = N;
-        p.has_act = has_act;
         p.act = act_params(act);
-        auto* kernel = act_family(act) == kFamilyErf        ? dz_kernel<kFamilyErf>
+        auto* kernel = !has_act                              ? dz_kernel<kNoActivation>
+                       : act_family(act) == kFamilyErf        ? dz_kernel<kFamilyErf>
                        : act_family(act) == kFamilyLogistic ? dz_kernel<kFamilyLogistic>
                                                             : dz_kernel<kFamilyPiecewise>;
         e = launch_pdl(kernel, dim3((unsigned)((N + 255) / 256), parts), dim3(256), st, p);

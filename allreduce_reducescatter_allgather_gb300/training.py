@@ -191,10 +191,13 @@ class PreparedOperator:
         self._index = device.index if device.index is not None else _torch().cuda.current_device()
 
     def __call__(self, stream=None):
-        cuda = _torch().cuda
+        torch = _torch()
         # (short calls are bound by the host: the common case makes no objects)
-        raw = cuda.current_stream(self._index).cuda_stream if stream is None else stream.cuda_stream
-        if cuda.current_device() == self._index:
+        if stream is None:
+            raw = torch._C._cuda_getCurrentRawStream(self._index)
+        else:
+            raw = stream.cuda_stream
+        if torch.cuda.current_device() == self._index:
             status = self._fn(*self._args, raw)
         else:
             with _OnDevice(self._device):
