@@ -318,7 +318,9 @@ __global__ void __launch_bounds__(256, kFamily == kNoActivation ? 6 : 3) dz_kern
                 sum[2 * j + 1] += v.y;
                 hi[j] = gemm::packed(v.x, v.y, __nv_bfloat16());
                 const float2 h = low(hi[j]);
-                rest[j] = gemm::packed(v.x - h.x, v.y - h.y, __nv_bfloat16());
+                // (nothing is left of an infinity, nor of what rounds to one)
+                rest[j] = gemm::packed(isinf(h.x) ? 0.0f : v.x - h.x, isinf(h.y) ? 0.0f : v.y - h.y,
+                                       __nv_bfloat16());
             }
             // (the buffers' rows are whole groups of 16 values)
             if (p.dz != nullptr)
