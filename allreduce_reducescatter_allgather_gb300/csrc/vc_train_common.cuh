@@ -109,6 +109,24 @@ constexpr float kGeluC = 0.044715f;
 // max(z, 0), NaN kept.
 __device__ __forceinline__ float positive(float z) { return z <= 0.0f ? 0.0f : z; }
 
+// z cut to at least, or at most, a value; NaN kept.  At infinities and where
+// squares of z overflow, the activations and their derivatives take their
+// limits: they are evaluated where the limit is reached in float32.
+__device__ __forceinline__ float2 at_least(float2 z, float a) {
+    float2 r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r.x) : "f"(z.x), "f"(a));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r.y) : "f"(z.y), "f"(a));
+    return r;
+}
+__device__ __forceinline__ float2 at_most(float2 z, float a) {
+    float2 r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r.x) : "f"(z.x), "f"(a));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r.y) : "f"(z.y), "f"(a));
+    return r;
+}
+constexpr float kLogisticFlat = 128.0f;  // exp(-128) is 0 beside 1, exp(128) infinite
+constexpr float kBellFlat = 30.0f;       // exp(-30^2 / 2) is 0
+
 // The activations in three families, so that a kernel holds the arithmetic of
 // one and no element branches: piecewise (none, relu, relu2), logistic (silu
 // and the tanh form of gelu, z / (1 + exp(-k z (1 + c z^2)))), and erf.
@@ -164,27 +182,28 @@ __device__ __forceinline__ float2 act_value(float2 z, const Act& a) {
         return a.square ? gemm::mul2(y, y) : y;
     } else if constexpr (kFamily == kFamilyLogistic) {
         // u = -log2(e) k z (1 + c z^2)
-        const float2 q = gemm::fma2(gemm::mul2(z, z), gemm::both(a.c), gemm::both(1.0f));
-        const float2 u = gemm::mul2(gemm::mul2(z, gemm::both(-kLog2e * a.k)), q);
+        const float2 y = at_least(z, -kLogisticFlat), x = at_most(y, kLogisticFlat);
+        const float2 q = gemm::fma2(gemm::mul2(x, x), gemm::both(a.c), gemm::both(1.0f));
+        const float2 u = gemm::mul2(gemm::mul2(x, gemm::both(-kLog2e * a.k)), q);
         const float2 d = gemm::add2(make_float2(exp2_fast(u.x), exp2_fast(u.y)), gemm::both(1.0f));
-        return gemm::mul2(z, make_float2(rcp_fast(d.x), rcp_fast(d.y)));
+        return gemm::mul2(y, make_float2(rcp_fast(d.x), rcp_fast(d.y)));
     } else {
-        // max(z, 0) - |z| Phi(-|z|).  (|z| is cut at 30, where the tail is 0
-        // in float32, so that an infinity does not meet it.)
-        const float2 x = make_float2(fminf(fabsf(z.x), 30.0f), fminf(fabsf(z.y), 30.0f));
+        // max(z, 0) - |z| Phi(-|z|)
+        const float2 x = make_float2(fminf(fabsf(z.x), kBellFlat), fminf(fabsf(z.y), kBellFlat));
         const float2 h = gemm::mul2(x, normal_tail(x, bell(z)));
         return make_float2(fmaxf(z.x, 0.0f) - h.x, fmaxf(z.y, 0.0f) - h.y);
     }
 }
 
-// act'(z); not called for the identity.
+// act'(v); not called for the identity.
 template <int kFamily>
-__device__ __forceinline__ float2 act_slope(float2 z, const Act& a) {
+__device__ __forceinline__ float2 act_slope(float2 v, const Act& a) {
     if constexpr (kFamily == kFamilyPiecewise) {
-        return a.square ? make_float2(2.0f * positive(z.x), 2.0f * positive(z.y))
-                        : make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
+        return a.square ? make_float2(2.0f * positive(v.x), 2.0f * positive(v.y))
+                        : make_float2(v.x > 0.0f ? 1.0f : 0.0f, v.y > 0.0f ? 1.0f : 0.0f);
     } else if constexpr (kFamily == kFamilyLogistic) {
         // with u = k z (1 + c z^2): s(u) + z s(u) (1 - s(u)) k (1 + 3 c z^2)
+        const float2 z = at_most(at_least(v, -kLogisticFlat), kLogisticFlat);
         const float2 q = gemm::mul2(gemm::mul2(z, z), gemm::both(a.c));
         const float2 u = gemm::mul2(gemm::mul2(z, gemm::both(a.k)), gemm::add2(q, gemm::both(1.0f)));
         const float2 s = make_float2(logistic(u.x), logistic(u.y));
@@ -193,8 +212,8 @@ __device__ __forceinline__ float2 act_slope(float2 z, const Act& a) {
         return gemm::mul2(s, gemm::fma2(gemm::mul2(z, rest), k, gemm::both(1.0f)));
     } else {
         // Phi(z) + z phi(z)
-        const float2 e = bell(z);
-        const float2 x = make_float2(fminf(fabsf(z.x), 30.0f), fminf(fabsf(z.y), 30.0f));
+        const float2 z = at_most(at_least(v, -kBellFlat), kBellFlat), e = bell(z);
+        const float2 x = make_float2(fabsf(z.x), fabsf(z.y));
         const float2 h = normal_tail(x, e);
         const float2 phi = make_float2(z.x > 0.0f ? 1.0f - h.x : h.x, z.y > 0.0f ? 1.0f - h.y : h.y);
         return gemm::fma2(gemm::mul2(z, gemm::both(0.39894228040143268f)), e, phi);

@@ -50,7 +50,8 @@ typedef struct {
 
 /* Activations.  RELU2 is max(z, 0)^2; GELU uses the error function,
  * GELU_TANH its tanh approximation with the constants sqrt(2/pi) and
- * 0.044715.  RELU's derivative at 0 is 0. */
+ * 0.044715.  RELU's derivative at 0 is 0.  At infinities an activation and its
+ * derivative take their limits (0 or z, 0 or 1, and RELU2 its square). */
 typedef enum {
     VC_ACT_NONE = 0,
     VC_ACT_RELU = 1,

@@ -7,11 +7,69 @@ from __future__ import annotations
 
 import pytest
 
-from test_training_gpu import env, rand
+from test_training_gpu import ACTS, BF16, act, env, rand
 
 pytestmark = pytest.mark.gpu
 
 assert env  # (the fixture; imported by name)
+
+# beyond what an activation bends: from here on it is z or 0 (or z^2)
+FAR = [2.0 ** 6, 1e4, 1e10, 1e13, 1e14, 1e18, 2e19, 1e25, 3e38]
+
+
+def far_values(torch, dev):
+    v = torch.tensor(FAR + [float("inf")], device=dev)
+    return torch.cat([v, -v]).to(torch.bfloat16)
+
+
+def limits(torch, z, name):
+    """Value and derivative: the formulas' up to 64, their limits beyond,
+    infinities included."""
+    up = z > 0
+    one, zero = torch.ones_like(z), torch.zeros_like(z)
+    if name == "none":
+        return z, one
+    if name == "relu2":
+        return torch.where(up, z * z, zero), torch.where(up, 2 * z, zero)
+    value, slope = act(torch, z.clamp(-64, 64), name)
+    near = z.abs() <= 64
+    return (torch.where(near, value, torch.where(up, z, zero)),
+            torch.where(near, slope, torch.where(up, one, zero)))
+
+
+def same(torch, got, want, what):
+    """Equal after bf16's rounding, signs of zeros aside, infinities too."""
+    off = (got.double() - want.to(torch.bfloat16).double()).abs()
+    both_infinite = got.isinf() & want.to(torch.bfloat16).isinf() & (got.double().sign() == want.sign())
+    ok = (off <= BF16 * want.abs()) | both_infinite
+    assert ok.all(), (what, got[~ok].tolist(), want[~ok].tolist())
+
+
+@pytest.mark.parametrize("repeat", [1, 20])  # up to 64 rows, and more
+@pytest.mark.parametrize("name", ACTS)
+def test_activations_far_out(env, name, repeat):
+    torch, vc, dev = env
+    z = far_values(torch, dev).repeat(repeat)
+    x = torch.zeros(z.numel(), 16, dtype=torch.bfloat16, device=dev)
+    x[:, 0] = z
+    w = torch.zeros(40, 16, dtype=torch.bfloat16, device=dev)
+    w[:, 0] = 1
+    y = torch.empty(z.numel(), 40, dtype=torch.bfloat16, device=dev)
+    vc.vc_linear_forward(x, w, y, activation=name)
+    value, slope = limits(torch, z.double(), name)
+    for column in (0, 31, 39):
+        same(torch, y[:, column], value, name)
+    x[:, 0] = float("nan")
+    vc.vc_linear_forward(x, w, y, activation=name)
+    assert y.isnan().all()
+    # one output feature, so that dx's first column is dz itself
+    one = torch.zeros(1, 16, dtype=torch.bfloat16, device=dev)
+    one[0, 0] = 1
+    dx = torch.empty_like(x)
+    dy = torch.ones(z.numel(), 1, dtype=torch.bfloat16, device=dev)
+    db = torch.empty(1, device=dev)
+    vc.vc_linear_backward(dy, x, one, dx=dx, dbias=db, preact=z[:, None].contiguous(), activation=name)
+    same(torch, dx[:, 0], slope, name + "'")
 
 
 @pytest.mark.parametrize("m", [8, 100])
