@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(256, kFamily == kNoActivation ? 6 : 3) dz_kern
 // Blocks along the rows: enough for the three blocks per SM that fit (six
 // without an activation), each with a group of rows at least for every warp.
 int dz_row_blocks(long long rows, long long cols, vc_act_t act) {
-    const long long across = (cols + 255) / 256;
+    const long long across = std::max(1ll, (cols + 255) / 256);
     const long long want = (152 * (act == VC_ACT_NONE ? 6 : 3) + across - 1) / across;
     return (int)std::max(1ll, std::min(want, (rows + 8 * kDzRows - 1) / (8 * kDzRows)));
 }

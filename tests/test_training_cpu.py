@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import re
 import subprocess
+import sys
 
 import pytest
 
@@ -179,6 +180,31 @@ def test_backward_aliases_and_workspace(tr):
     more = [mat(tr, GiB, 65, 24), mat(tr, 2 * GiB, 65, 64)]
     assert (L.vc_linear_backward_workspace(ref(few[0]), ref(few[1]), ref(w), GELU, 0)
             > L.vc_linear_backward_workspace(ref(more[0]), ref(more[1]), ref(w), GELU, 0))
+
+
+# Every side may be 0, with every output.  (In a process of its own: a division
+# by zero ends it.)
+EMPTY_SIDES = """
+import ctypes, itertools, sys
+sys.path.insert(0, sys.argv[1])
+from allreduce_reducescatter_allgather_gb300 import training as tr
+L, GiB = tr._lib(), 1 << 30
+mat = lambda at, r, c, t=3: ctypes.byref(tr.Matrix(at * GiB, 1, r, c, c, 0, t))
+for m, n, k, act, db in itertools.product((0, 10), (0, 24), (0, 64), (0, 3), (0, 1)):
+    dy, x, w, z = mat(1, m, n), mat(2, m, k), mat(3, n, k), mat(4, m, n)
+    need = L.vc_linear_backward_workspace(dy, x, w, act, db)
+    assert need < GiB, need
+    status = L.vc_linear_backward(dy, x, w, z, act, mat(5, m, k), mat(6, n, k, 2), 7 * GiB * db, 2,
+                                  0, 8 * GiB, GiB, None)
+    assert status == (0 if n == 0 and m * k == 0 else 4), (m, n, k, act, db, status)
+print("done")
+"""
+
+
+def test_backward_of_empty_sides(tr):
+    out = subprocess.run([sys.executable, "-c", EMPTY_SIDES, str(ROOT)], capture_output=True,
+                         text=True)
+    assert out.returncode == 0 and out.stdout.strip() == "done", (out.returncode, out.stderr)
 
 
 def ns(tr, steps=5, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7):
