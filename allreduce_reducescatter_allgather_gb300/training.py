@@ -154,13 +154,15 @@ def _ref(m):
 
 
 def _workspace(workspace, need, device, stream):
-    """The pointer and size to pass, and the tensor to keep until the call
-    has been enqueued.  A new one is allocated on the call's stream, so that
-    torch's allocator gives it out again only behind the call."""
+    """The pointer and size to pass, the tensor to keep until the call has
+    been enqueued, and it again where it is new.  A new one is allocated on the
+    call's stream, so that torch's allocator gives it out again only behind the
+    call."""
     torch = _torch()
-    if workspace is None:
+    new = workspace is None
+    if new:
         if need == 0:
-            return ctypes.c_void_p(0), 0, None
+            return ctypes.c_void_p(0), 0, None, None
         if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
         else:
@@ -172,7 +174,8 @@ def _workspace(workspace, need, device, stream):
             raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
         if workspace.data_ptr() % 256 != 0:
             raise ValueError("workspace is not aligned to 256 bytes")
-    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), workspace
+    return (ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), workspace,
+            workspace if new else None)
 
 
 class PreparedOperator:
@@ -184,11 +187,44 @@ class PreparedOperator:
         forward = prepare_linear_forward(x, weight, out, bias=b, activation="gelu")
         forward()                # on the current stream
         forward(stream=s)        # on another torch stream
+
+    A workspace that the handle has made itself follows it from stream to
+    stream: a call on another stream than the preparing one starts behind what
+    that one had to do when the workspace was allocated, and the allocator
+    gives the workspace to nobody else before the call has ended, even where
+    the handle is dropped meanwhile.  (The operands are the caller's to keep.)
+    A handle whose call was captured in a graph is kept as long as the graph.
     """
 
-    def __init__(self, fn, args, device, keep):
+    def __init__(self, fn, args, device, keep, made=None):
+        """made: the workspace, where it was allocated for this handle on the
+        current stream."""
         self._fn, self._args, self._device, self._keep = fn, args, device, keep
         self._index = device.index if device.index is not None else _torch().cuda.current_device()
+        self._made, self._stream, self._allocated = made, None, None
+        if made is not None:
+            torch = _torch()
+            self._stream = torch._C._cuda_getCurrentRawStream(self._index)
+            with _OnDevice(self._device):
+                if not torch.cuda.is_current_stream_capturing():
+                    self._allocated = torch.cuda.Event()
+                    self._allocated.record()
+
+    def _move(self, stream, raw):
+        """The workspace goes to another stream than that of the last call."""
+        torch = _torch()
+        with _OnDevice(self._device):
+            if stream is None:
+                stream = torch.cuda.current_stream()
+            with torch.cuda.stream(stream):
+                # (a stream under capture cannot wait for work outside of it;
+                # torch.cuda.graph waits for all work before it captures)
+                capturing = torch.cuda.is_current_stream_capturing()
+            if not capturing:
+                self._stream = raw
+                if self._allocated is not None:
+                    stream.wait_event(self._allocated)
+            self._made.record_stream(stream)
 
     def __call__(self, stream=None):
         torch = _torch()
@@ -197,6 +233,8 @@ class PreparedOperator:
             raw = torch._C._cuda_getCurrentRawStream(self._index)
         else:
             raw = stream.cuda_stream
+        if self._made is not None and raw != self._stream:
+            self._move(stream, raw)
         if torch.cuda.current_device() == self._index:
             status = self._fn(*self._args, raw)
         else:
@@ -204,6 +242,11 @@ class PreparedOperator:
                 status = self._fn(*self._args, raw)
         if status != 0:
             check_status(status)
+
+
+def _once(stream, fn, args, device, keep, made):
+    """One call, whose new workspace was allocated on its own stream."""
+    PreparedOperator(fn, args, device, keep)(stream)
 
 
 # ------------------------------------------------------------- linear layer --
@@ -237,11 +280,11 @@ def _forward(x, weight, out, bias, residual, preact, activation, workspace, stre
     act = _activation(activation)
     L = _lib()
     need = int(L.vc_linear_forward_workspace(_ref(xm), _ref(wm)))
-    ws, size, held = _workspace(workspace, need, dev, stream)
+    ws, size, held, made = _workspace(workspace, need, dev, stream)
     args = (_ref(xm), _ref(wm), ctypes.c_void_p(bias.data_ptr() if bias is not None else 0),
             _ref(rm), _ref(om), _ref(pm), act, ws, size)
     return L.vc_linear_forward, args, dev, (x, weight, out, bias, residual, preact, held,
-                                            xm, wm, om, rm, pm)
+                                            xm, wm, om, rm, pm), made
 
 
 def vc_linear_forward(x, weight, out, bias=None, residual=None, preact=None,
@@ -249,8 +292,7 @@ def vc_linear_forward(x, weight, out, bias=None, residual=None, preact=None,
     """out <- act(x W^T + bias) + residual, x [..., K], weight [N, K], out
     [..., N], all bfloat16.  preact receives x W^T + bias (for the backward
     pass).  residual may be out itself."""
-    PreparedOperator(*_forward(x, weight, out, bias, residual, preact, activation, workspace,
-                               stream))(stream)
+    _once(stream, *_forward(x, weight, out, bias, residual, preact, activation, workspace, stream))
 
 
 def prepare_linear_forward(x, weight, out, bias=None, residual=None, preact=None,
@@ -297,12 +339,12 @@ def _backward(dy, x, weight, dx, dweight, dbias, preact, activation, accumulate,
     L = _lib()
     need = int(L.vc_linear_backward_workspace(_ref(ym), _ref(xm), _ref(wm), act,
                                               int(dbias is not None)))
-    ws, size, held = _workspace(workspace, need, dev, stream)
+    ws, size, held, made = _workspace(workspace, need, dev, stream)
     args = (_ref(ym), _ref(xm), _ref(wm), _ref(pm), act, _ref(dxm), _ref(dwm),
             ctypes.c_void_p(dbias.data_ptr() if dbias is not None else 0),
             _code(dbias) if dbias is not None else 3, int(bool(accumulate)), ws, size)
     return L.vc_linear_backward, args, dev, (dy, x, weight, dx, dweight, dbias, preact, held,
-                                             ym, xm, wm, pm, dxm, dwm)
+                                             ym, xm, wm, pm, dxm, dwm), made
 
 
 def vc_linear_backward(dy, x, weight, dx=None, dweight=None, dbias=None, preact=None,
@@ -313,8 +355,8 @@ def vc_linear_backward(dy, x, weight, dx=None, dweight=None, dbias=None, preact=
     dbias are bfloat16 or float32 and may be views into a gradient bucket;
     accumulate adds to them.  The residual's gradient is dy itself.  dz is
     rounded to bfloat16 before the products."""
-    PreparedOperator(*_backward(dy, x, weight, dx, dweight, dbias, preact, activation, accumulate,
-                                workspace, stream))(stream)
+    _once(stream, *_backward(dy, x, weight, dx, dweight, dbias, preact, activation, accumulate,
+                             workspace, stream))
 
 
 def prepare_linear_backward(dy, x, weight, dx=None, dweight=None, dbias=None, preact=None,
@@ -352,9 +394,9 @@ def _orthogonalize(g, out, steps, coefficients, eps, workspace, stream):
     _same_shape("out", out, g)
     ns = _newton_schulz(steps, coefficients, eps)
     need = orthogonalize_workspace(g.shape)
-    ws, size, held = _workspace(workspace, need, g.device, stream)
+    ws, size, held, made = _workspace(workspace, need, g.device, stream)
     return _lib().vc_orthogonalize, (_ref(gm), _ref(om), _ref(ns), ws, size), g.device, (
-        g, out, held, gm, om, ns)
+        g, out, held, gm, om, ns), made
 
 
 def vc_orthogonalize(g, out, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7,
@@ -363,7 +405,7 @@ def vc_orthogonalize(g, out, steps: int = 5, coefficients=COEFFICIENTS, eps: flo
     X <- a X + (b A + c A^2) X, A = X X^T: each matrix of g [rows, cols] or
     [batch, rows, cols] (float32 or bfloat16) brought near the closest matrix
     with orthonormal rows (or columns).  out is bfloat16 and may be g."""
-    PreparedOperator(*_orthogonalize(g, out, steps, coefficients, eps, workspace, stream))(stream)
+    _once(stream, *_orthogonalize(g, out, steps, coefficients, eps, workspace, stream))
 
 
 def prepare_orthogonalize(g, out, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7,
@@ -375,8 +417,8 @@ def prepare_orthogonalize(g, out, steps: int = 5, coefficients=COEFFICIENTS, eps
 class PreparedMuon(PreparedOperator):
     """vc_muon_step on fixed buffers; the learning rate goes with each call."""
 
-    def __init__(self, fn, args, device, keep, muon):
-        super().__init__(fn, args, device, keep)
+    def __init__(self, fn, args, device, keep, made, muon):
+        super().__init__(fn, args, device, keep, made)
         self._muon = muon
 
     def __call__(self, lr: float, stream=None):
@@ -398,9 +440,9 @@ def _muon(weight, grad, momentum, beta, nesterov, weight_decay, scale, steps, co
     args = Muon(0.0, beta, weight_decay, scale, int(bool(nesterov)),
                 _newton_schulz(steps, coefficients, eps))
     need = orthogonalize_workspace(weight.shape)
-    ws, size, held = _workspace(workspace, need, weight.device, stream)
+    ws, size, held, made = _workspace(workspace, need, weight.device, stream)
     return (_lib().vc_muon_step, (_ref(wm), _ref(gm), _ref(mm), _ref(args), ws, size),
-            weight.device, (weight, grad, momentum, held, wm, gm, mm), args)
+            weight.device, (weight, grad, momentum, held, wm, gm, mm), made, args)
 
 
 def vc_muon_step(weight, grad, momentum, lr: float, beta: float = 0.95, nesterov: bool = True,
@@ -412,8 +454,10 @@ def vc_muon_step(weight, grad, momentum, lr: float, beta: float = 0.95, nesterov
     momentum are float32 or bfloat16, of one shape, [rows, cols] or
     [batch, rows, cols].  scale None: 0.2 sqrt(max(rows, cols)), which gives
     the update 0.2 a value in the root mean square."""
-    PreparedMuon(*_muon(weight, grad, momentum, beta, nesterov, weight_decay, scale, steps,
-                        coefficients, eps, workspace, stream))(lr, stream)
+    *call, args = _muon(weight, grad, momentum, beta, nesterov, weight_decay, scale, steps,
+                        coefficients, eps, workspace, stream)
+    args.lr = lr
+    _once(stream, *call)
 
 
 def prepare_muon_step(weight, grad, momentum, beta: float = 0.95, nesterov: bool = True,

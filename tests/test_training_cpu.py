@@ -282,3 +282,110 @@ def test_binding_refuses_host_tensors(tr):
         tr.vc_orthogonalize(t, t)
     with pytest.raises(TypeError, match="not a tensor"):
         tr.vc_muon_step([1.0], t, t, lr=0.1)
+
+
+class FakeCuda:
+    """What PreparedOperator asks of torch: streams by number, events, and a
+    log of what is done with them."""
+
+    def __init__(self):
+        self.log, self.now, self.capturing, self.device = [], 0, False, 0
+        fake = self
+
+        class Stream:
+            def __init__(self, raw):
+                self.cuda_stream = raw
+
+            def wait_event(self, event):
+                fake.log.append(("wait", self.cuda_stream, event.at))
+
+            def __enter__(self):
+                self.before, fake.now = fake.now, self.cuda_stream
+
+            def __exit__(self, *exc):
+                fake.now = self.before
+
+        class Event:
+            def record(self):
+                assert not fake.capturing
+                self.at = fake.now
+
+        class Cuda:
+            current_device = staticmethod(lambda: fake.device)
+            current_stream = staticmethod(lambda: Stream(fake.now))
+            is_current_stream_capturing = staticmethod(lambda: fake.capturing)
+            stream = staticmethod(lambda s: s)
+
+        class C:
+            _cuda_getCurrentRawStream = staticmethod(lambda index: fake.now)
+
+        self.Stream, Cuda.Event, self.cuda, self._C = Stream, Event, Cuda, C
+
+    def workspace(self):
+        fake = self
+
+        class Tensor:
+            def record_stream(self, stream):
+                fake.log.append(("record", stream.cuda_stream))
+        return Tensor()
+
+
+@pytest.fixture
+def fake_cuda(tr, monkeypatch):
+    import contextlib
+    fake = FakeCuda()
+    monkeypatch.setattr(tr, "_torch", lambda: fake)
+    monkeypatch.setattr(tr, "_OnDevice", lambda device: contextlib.nullcontext())
+    return fake
+
+
+def handle(tr, fake, made):
+    class Device:
+        index = 0
+    return tr.PreparedOperator(lambda stream: fake.log.append(("call", stream)) or 0, (), Device,
+                               (made,), made)
+
+
+def test_a_handles_workspace_follows_its_calls(tr, fake_cuda):
+    """On another stream than the preparing one, by argument or by a change of
+    the current stream, a call waits for what preceded the allocation and the
+    allocator learns of the stream, before the launch."""
+    fake = fake_cuda
+    fake.now = 7
+    call = handle(tr, fake, fake.workspace())
+    call()
+    call(stream=fake.Stream(7))
+    assert fake.log == [("call", 7), ("call", 7)]
+    fake.log.clear()
+    call(stream=fake.Stream(8))
+    call(stream=fake.Stream(8))
+    assert fake.log == [("wait", 8, 7), ("record", 8), ("call", 8), ("call", 8)]
+    fake.log.clear()
+    fake.now = 9
+    call()
+    assert fake.log == [("wait", 9, 7), ("record", 9), ("call", 9)]
+    assert fake.now == 9
+    # nothing to follow where the caller brought the workspace
+    fake.log.clear()
+    handle(tr, fake, None)(stream=fake.Stream(8))
+    assert fake.log == [("call", 8)]
+
+
+def test_a_handles_workspace_under_capture(tr, fake_cuda):
+    """A stream under capture waits for nothing outside of it, and no event is
+    recorded there."""
+    fake = fake_cuda
+    call = handle(tr, fake, fake.workspace())
+    fake.capturing = True
+    call(stream=fake.Stream(3))
+    assert fake.log == [("record", 3), ("call", 3)]
+    fake.log.clear()
+    fake.capturing = False
+    call(stream=fake.Stream(3))  # the same stream, after its capture
+    assert fake.log == [("wait", 3, 0), ("record", 3), ("call", 3)]
+    fake.log.clear()
+    fake.capturing = True
+    call = handle(tr, fake, fake.workspace())
+    fake.capturing = False
+    call(stream=fake.Stream(4))
+    assert fake.log == [("record", 4), ("call", 4)]

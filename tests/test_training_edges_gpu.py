@@ -91,3 +91,51 @@ def test_infinite_gradients_stay_infinite(env, m, name):
     assert torch.equal(dw2[3], x[5].float().sign() * inf)
     rows, features = torch.arange(m, device=dev) != 5, torch.arange(n, device=dev) != 3
     assert torch.equal(dx2[rows], dx[rows]) and torch.equal(dw2[features], dw[features])
+
+
+# -------------------------------------------------------------------- streams --
+
+@pytest.mark.parametrize("how", ["argument", "current"])
+def test_handle_dropped_while_another_stream_uses_its_workspace(env, how):
+    """A handle prepared on one stream and called on another: its workspace is
+    given to nobody else before that call has ended."""
+    torch, vc, dev = env
+    x, w = rand(torch, dev, 500, 301, seed=1), rand(torch, dev, 260, 301, seed=2)
+    want, y = (torch.empty(500, 260, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    vc.vc_linear_forward(x, w, want)
+    need = vc.linear_forward_workspace(x, w)
+    assert need > 0
+    side = torch.cuda.Stream(dev)
+    torch.cuda.synchronize()
+    call = vc.prepare_linear_forward(x, w, y)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        if how == "current":
+            call()
+    if how == "argument":
+        call(stream=side)
+    del call
+    # whoever allocates next on the first stream writes at once
+    for _ in range(4):
+        torch.empty(need, dtype=torch.uint8, device=dev).fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_handle_waits_for_the_stream_that_prepared_it(env):
+    """The workspace may hold a block that earlier work of the preparing
+    stream still uses: a call on another stream starts behind it."""
+    torch, vc, dev = env
+    x, w = rand(torch, dev, 500, 301, seed=1), rand(torch, dev, 260, 301, seed=2)
+    want, y = (torch.empty(500, 260, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    vc.vc_linear_forward(x, w, want)
+    need = vc.linear_forward_workspace(x, w)
+    side = torch.cuda.Stream(dev)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    block = torch.empty(need, dtype=torch.uint8, device=dev).fill_(255)
+    del block  # free for this stream's next allocation, though its fill is still to come
+    call = vc.prepare_linear_forward(x, w, y)
+    call(stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
