@@ -99,6 +99,8 @@ extern "C" vc_status_t vc_train_timeouts(unsigned* count) {
     if (v != nullptr && v[0] != '\0' && v[0] != '0') return VC_ERR_CUDA;
     const unsigned* p = vc::gemm::timeout_counter();
     if (p == nullptr) return VC_ERR_CUDA;
+    // (the copy alone would not wait for streams that do not block)
+    if (cudaDeviceSynchronize() != cudaSuccess) return VC_ERR_CUDA;
     return cudaMemcpy(count, p, sizeof *count, cudaMemcpyDeviceToHost) == cudaSuccess
                ? VC_SUCCESS
                : VC_ERR_CUDA;

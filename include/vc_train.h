@@ -128,8 +128,9 @@ vc_status_t vc_muon_step(const vc_matrix_t *weight, const vc_matrix_t *grad,
 /* Device-side waits of the product kernels are bounded (about two seconds
  * each).  *count receives how many blocks of the current device have given up
  * since the library was loaded: 0 unless something is broken, and any other
- * value means that results computed since are not valid.  Waits for the
- * device (it copies one word to the host). */
+ * value means that results computed since are not valid.  Waits for all
+ * streams of the device, then copies one word to the host; not to be called
+ * while a stream is captured. */
 vc_status_t vc_train_timeouts(unsigned *count);
 
 #ifdef __cplusplus

@@ -139,3 +139,12 @@ def test_handle_waits_for_the_stream_that_prepared_it(env):
     call(stream=side)
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+def test_timeouts_wait_for_every_stream(env):
+    torch, vc, dev = env
+    side = torch.cuda.Stream(dev)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    assert vc.train_timeouts() == 0
+    assert side.query()  # its work has ended
