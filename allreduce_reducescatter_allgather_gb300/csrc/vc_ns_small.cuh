@@ -29,6 +29,12 @@ namespace train {
 // Whether pass `step` reads X as two fp16 values.
 __host__ __device__ inline bool keeps_lo(int step, int steps) { return step == 0 || step < steps - 2; }
 
+// X_0 is the update times this; a zero matrix stays zero where eps is 0, too.
+__device__ __forceinline__ float x0_scale(float squares, float eps, float size) {
+    const float divisor = sqrtf(squares) + eps;
+    return divisor == 0.0f ? 0.0f : size / divisor;
+}
+
 struct SmallParams {
     gemm::View g, m, out;
     int has_momentum, nesterov, weights, tall;
@@ -224,7 +230,7 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
     gemm::cluster_sync_all();
     float square = 0.0f;
     for (int i = 0; i < ranks; ++i) square += norms[i];
-    const float to_x = p.size / (sqrtf(square) + p.eps);
+    const float to_x = x0_scale(square, p.eps, p.size);
 
     // ---- X_0, in place
     const int chunks = p.width / 32;

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Prep
     const int b = blockIdx.y;
     float sum = 0.0f;
     for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) sum += p.parts[b * gridDim.x + i];
-    const float scale = p.size / (sqrtf(block_sum(sum, tmp)) + p.eps);
+    const float scale = x0_scale(block_sum(sum, tmp), p.eps, p.size);
     for (Groups at(p); at.row < p.rows;) {
         Loaded x[kPrepareBatch];
         load_batch(p, b, at, x);

@@ -93,6 +93,22 @@ def test_infinite_gradients_stay_infinite(env, m, name):
     assert torch.equal(dx2[rows], dx[rows]) and torch.equal(dw2[features], dw[features])
 
 
+# ---------------------------------------------------------- orthogonalisation --
+
+@pytest.mark.parametrize("shape", [(64, 100), (100, 64), (300, 257), (3, 130, 200), (2, 40, 600)])
+def test_zero_matrices_without_eps(env, shape):
+    """A zero matrix gives zeros, and leaves the weight, whatever eps is."""
+    torch, vc, dev = env
+    g = torch.zeros(*shape, device=dev)
+    out = torch.full(shape, 5.0, dtype=torch.bfloat16, device=dev)
+    vc.vc_orthogonalize(g, out, eps=0.0)
+    assert (out == 0).all()
+    w = rand(torch, dev, *shape, dtype=torch.float32)
+    w0, m = w.clone(), torch.zeros_like(w)
+    vc.vc_muon_step(w, g, m, 0.1, eps=0.0)
+    assert torch.equal(w, w0) and (m == 0).all()
+
+
 # -------------------------------------------------------------------- streams --
 
 @pytest.mark.parametrize("how", ["argument", "current"])
