@@ -29,10 +29,44 @@ namespace train {
 // Whether pass `step` reads X as two fp16 values.
 __host__ __device__ inline bool keeps_lo(int step, int steps) { return step == 0 || step < steps - 2; }
 
-// X_0 is the update times this; a zero matrix stays zero where eps is 0, too.
-__device__ __forceinline__ float x0_scale(float squares, float eps, float size) {
-    const float divisor = sqrtf(squares) + eps;
-    return divisor == 0.0f ? 0.0f : size / divisor;
+// How a matrix enters the iteration.  Its X_0 has the norm n = norm / (norm + eps),
+// which bounds its singular values.  Where eps outweighs the norm, X_0 would
+// be too small for fp16; but then a pass is a multiplication by a as far as
+// the products' accuracy goes: b n^2 + c n^4 is at most 2^-12 of a.  Such
+// passes are left out and a goes into the scale, until n is above 2^-7 (where
+// fp16 loses 4e-5) or one pass is left.  If that one is linear too, X goes
+// through it in a unit of its own.
+struct Start {
+    float scale;  // the stored X_0 is the update times this; 0 for a zero matrix
+    float unit;   // of X: 1, or a power of two
+    int skip;     // passes left out
+    int linear;   // passes left out or linear: skip, or all of them
+};
+__device__ __forceinline__ Start start_of(float squares, float eps, float size, int steps, float a,
+                                          float b, float c) {
+    const float norm = sqrtf(squares), divisor = norm + eps;
+    if (norm == 0.0f) return {0.0f, 1.0f, 0, 0};
+    Start s = {size / divisor, 1.0f, 0, 0};
+    if (!(norm <= 0.0078125f * divisor)) return s;  // (NaN too)
+    // (in 64 bits: n and the powers of a pass float32's range)
+    double n = (double)norm / divisor, factor = 1.0;
+    auto linear = [&] {
+        const double q = n * n;
+        return n <= 0.0078125 && q * (fabs(b) + q * fabs(c)) <= 0.000244140625 * fabs(a);
+    };
+    while (s.skip < steps - 1 && linear()) {
+        ++s.skip;
+        factor *= a;
+        n *= fabs(a);
+    }
+    s.linear = s.skip;
+    if (linear()) {
+        s.linear = steps;
+        // n, or 2^-120, rounded up to a power of two
+        s.unit = __uint_as_float((__float_as_uint((float)fmax(n, 0x1p-120)) + 0x7FFFFFu) & 0x7F800000u);
+    }
+    s.scale = (float)((double)size / divisor * (factor / s.unit));
+    return s;
 }
 
 struct SmallParams {
@@ -43,7 +77,7 @@ struct SmallParams {
     int steps;
     float beta, eps;
     float ca, cb, cc;  // the polynomial
-    float size;        // X is stored times this
+    float size;        // X is stored times this / its unit
     float keep, scale;  // out <- keep out + scale X, or scale X
     unsigned* timeouts;
 };
@@ -52,7 +86,7 @@ struct Small {
     static constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxWidth = 256, kMaxRanks = 8, kRows = 128;
     static constexpr int kAtom = 128 * 128;  // bytes of 64 columns
     static constexpr int kHi = 0, kLo = 4 * kAtom, kO = 8 * kAtom, kParts = 10 * kAtom;
-    static constexpr int kVectors = 14 * kAtom;  // diagonals of A and B, norms, sums
+    static constexpr int kVectors = 14 * kAtom;  // diagonals of A and B, norms, sums, unit
     static constexpr int kBar = kVectors + 1024 + 192;
     static constexpr int kSmem = 1024 + kBar + 64;
     static constexpr int kTmemCols = 512;  // 128 for A and A^2, up to 256 for B X
@@ -129,6 +163,7 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
     float4* const parts = reinterpret_cast<float4*>(gen + S::kParts);
     float* const d_a = reinterpret_cast<float*>(gen + S::kVectors);
     float *const d_b = d_a + 128, *const norms = d_a + 256, *const sums = d_a + 264;
+    float* const unit = d_a + 280;
     const unsigned bar = base + S::kBar;
     unsigned* const tmem_slot = reinterpret_cast<unsigned*>(gen + S::kBar + 8);
     volatile int* const dead = reinterpret_cast<volatile int*>(gen + S::kBar + 12);
@@ -230,7 +265,8 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
     gemm::cluster_sync_all();
     float square = 0.0f;
     for (int i = 0; i < ranks; ++i) square += norms[i];
-    const float to_x = x0_scale(square, p.eps, p.size);
+    const Start start = start_of(square, p.eps, p.size, p.steps, p.ca, p.cb, p.cc);
+    const float to_x = start.scale;
 
     // ---- X_0, in place
     const int chunks = p.width / 32;
@@ -252,7 +288,9 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
 
     const unsigned square_desc = gemm::instruction_desc(false, false, false, 128, 128);
     const unsigned update_desc = gemm::instruction_desc(false, false, true, 128, p.width);
-    const float to_a = 1.0f / (p.size * p.size);
+    // (a linear pass takes A for 0)
+    const float to_a = start.linear == p.steps ? 0.0f : 1.0f / (p.size * p.size);
+    if (threadIdx.x == 0) *unit = start.unit;
     const int kuse = (p.r + 15) / 16;  // 16-deep steps over X's rows that are not padding
     unsigned phase = 0;
     // After the block's writes to shared memory: makes them visible to the
@@ -275,7 +313,7 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
         gemm::tcgen05_fence_after();
     };
 
-    for (int step = 0; step < p.steps; ++step) {
+    for (int step = start.skip; step < p.steps; ++step) {
         // ---- A = X X^T
         multiply([&] {
             for (int k = 0; k < p.width / 16; ++k) {
@@ -436,6 +474,7 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
                 q.off = false;
                 q.stage = gen + S::kParts + warp * gemm::kWarpStage;
                 if (q.row0 >= q.M || q.col0 >= q.N) continue;
+                const float scale = p.scale * *unit;
                 if (p.weights) {
                     float w[32];
                     if (p.tall)
@@ -443,10 +482,10 @@ ns_small_kernel(const __grid_constant__ SmallParams p, int ranks) {
                     else
                         gemm::get_rows(p.out, q, w);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = fmaf(p.keep, w[j], p.scale * v[j]);
+                    for (int j = 0; j < 32; ++j) v[j] = fmaf(p.keep, w[j], scale * v[j]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= p.scale;
+                    for (int j = 0; j < 32; ++j) v[j] *= scale;
                 }
                 if (p.tall)
                     gemm::put_columns(p.out, q, v);

@@ -13,7 +13,8 @@
 // 1e-3 of the exact iteration, below the bf16 rounding of the output (bf16
 // operands: 1e-2):
 //   - X is stored times a power of two near sqrt(c), so that its values are
-//     about 1 at the end and normal fp16 numbers at the start;
+//     about 1 at the end and normal fp16 numbers at the start (where eps
+//     outweighs the norm: struct Start);
 //   - the diagonals of A and B, which are far larger than the rest, are kept
 //     apart in 32 bits; with A = D + O,
 //       A^2 = D^2 + D O + O D + O^2,   B X = diag(B) X + offdiag(B) X;
@@ -49,7 +50,10 @@ struct PrepareParams {
     float* parts;  // [batch][gridDim.x]
     __half *hi, *lo;
     long long ld, batch_stride;  // of hi and lo
-    float size, eps;             // X is stored times size / (norm + eps)
+    float size, eps;             // X is stored times size
+    int steps;
+    float ca, cb, cc;
+    Start* starts;               // of each matrix
     int rows, cols;
     int lanes;  // lanes that share a row, a power of two; 8 columns each at a time
 };
@@ -207,8 +211,8 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ P
     if (threadIdx.x == 0) p.parts[b * gridDim.x + blockIdx.x] = sum;
 }
 
-// X_0 = update size / (norm + eps), as two fp16 values.  Every block adds up
-// the partial sums, in the same order.
+// X_0 = update size / (norm + eps), or what start_of makes of it, as two fp16
+// values.  Every block adds up the partial sums, in the same order.
 __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ PrepareParams p) {
     __shared__ float tmp[8];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -216,7 +220,9 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Prep
     const int b = blockIdx.y;
     float sum = 0.0f;
     for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) sum += p.parts[b * gridDim.x + i];
-    const float scale = x0_scale(block_sum(sum, tmp), p.eps, p.size);
+    const Start start = start_of(block_sum(sum, tmp), p.eps, p.size, p.steps, p.ca, p.cb, p.cc);
+    const float scale = start.scale;
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.starts[b] = start;
     for (Groups at(p); at.row < p.rows;) {
         Loaded x[kPrepareBatch];
         load_batch(p, b, at, x);
@@ -304,37 +310,46 @@ struct EpiPoly {
         const float* d;
         __half* ob;
         float* db;
+        const Start* starts;
         long long ld, batch_stride;
-        float cb, cc;
+        float ca, cb, cc;
+        int step;
     };
     static bool odd(const Params&) { return false; }
     struct Pre {
         gemm::Chunk16 o;
         float row, col;  // A's diagonal at the lane's row and at its column
+        int skip, linear;
     };
     __device__ static void prefetch(const Params& p, const Place& q, Pre& pre) {
         const float* const d = p.d + (long long)q.b * q.M;
         pre.col = q.col0 + q.lane < q.N ? d[q.col0 + q.lane] : 0.0f;
         pre.row = q.row() < q.M ? d[q.row()] : 0.0f;
+        pre.skip = p.starts[q.b].skip;
+        pre.linear = p.starts[q.b].linear;
         load_across(p.o + (long long)q.b * p.batch_stride + (long long)q.row0 * p.ld + q.col0, p.ld * 2,
                     q, pre.o);
     }
     __device__ static void apply(const Params& p, const Place& q, Pre& pre, float (&v)[32]) {
         __half* const ob = p.ob + (long long)q.b * p.batch_stride;
+        // a pass that is left out: a + B = 1; a linear one: B = 0
+        const bool none = p.step < pre.linear;
+        const float cb = none ? 0.0f : p.cb, cc = none ? 0.0f : p.cc;
         if (q.row0 == q.col0) {
             const float d = take_diagonal(q, v);  // (O O)_ii
             if (q.row() < q.M)
-                p.db[(long long)q.b * q.M + q.row()] = p.cb * pre.row + p.cc * (pre.row * pre.row + d);
+                p.db[(long long)q.b * q.M + q.row()] =
+                    p.step < pre.skip ? 1.0f - p.ca : cb * pre.row + cc * (pre.row * pre.row + d);
         }
         across_to_own(q, pre.o);
-        const float k = fmaf(p.cc, pre.row, p.cb);
+        const float k = fmaf(cc, pre.row, cb);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float2 a = pair_at(pre.o, i, __half());  // (0 on the diagonal)
-            const float k0 = fmaf(p.cc, __shfl_sync(0xFFFFFFFFu, pre.col, 2 * i), k);
-            const float k1 = fmaf(p.cc, __shfl_sync(0xFFFFFFFFu, pre.col, 2 * i + 1), k);
-            v[2 * i] = fmaf(k0, a.x, p.cc * v[2 * i]);
-            v[2 * i + 1] = fmaf(k1, a.y, p.cc * v[2 * i + 1]);
+            const float k0 = fmaf(cc, __shfl_sync(0xFFFFFFFFu, pre.col, 2 * i), k);
+            const float k1 = fmaf(cc, __shfl_sync(0xFFFFFFFFu, pre.col, 2 * i + 1), k);
+            v[2 * i] = fmaf(k0, a.x, cc * v[2 * i]);
+            v[2 * i + 1] = fmaf(k1, a.y, cc * v[2 * i + 1]);
         }
         store_chunk(ob + (long long)q.row0 * p.ld + q.col0, p.ld, q, v);
         put_mirror(ob, p.ld, q, v);
@@ -409,22 +424,27 @@ struct EpiFinal {
         View out;     // the output, or the weights
         int weights;  // out <- keep out + scale y, else out <- scale y
         float keep, scale;
+        const Start* starts;
     };
     static bool odd(const Params& p) { return !p.out.vec16; }
-    using Pre = UpdatePre;
+    struct Pre : UpdatePre {
+        float unit;
+    };
     __device__ static void prefetch(const Params& p, const Place& q, Pre& pre) {
         update_prefetch(p.u, q, pre);
+        pre.unit = p.starts[q.b].unit;
     }
     __device__ static void apply(const Params& p, const Place& q, Pre& pre, float (&v)[32]) {
         update_apply(p.u, q, pre, v);
+        const float scale = p.scale * pre.unit;
         if (p.weights) {
             float w[32];
             get_rows(p.out, q, w);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(p.keep, w[j], p.scale * v[j]);
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(p.keep, w[j], scale * v[j]);
         } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= p.scale;
+            for (int j = 0; j < 32; ++j) v[j] *= scale;
         }
         put_rows(p.out, q, v);
     }
@@ -437,7 +457,7 @@ struct Layout {
     long long ldx, ldr;    // row lengths of X and of the r x r matrices
     long long xs, as;      // values from one matrix of the batch to the next
     int parts, lanes;
-    size_t hi0, hi1, lo, a, b, da, db, sums, bytes;
+    size_t hi0, hi1, lo, a, b, da, db, sums, starts, bytes;
 };
 
 bool layout_of(long long batch, long long rows, long long cols, Layout* l) {
@@ -468,6 +488,7 @@ bool layout_of(long long batch, long long rows, long long cols, Layout* l) {
     l->da = at, at += d;
     l->db = at, at += d;
     l->sums = at, at += round256((size_t)batch * l->parts * 4);
+    l->starts = at, at += round256((size_t)batch * sizeof(Start));
     l->bytes = at;
     return true;
 }
@@ -518,6 +539,11 @@ cudaError_t iterate(const Layout& l, long long batch, long long rows, long long 
     p.batch_stride = l.xs;
     p.size = size;
     p.eps = ns.eps;
+    p.steps = ns.steps;
+    p.ca = ns.a;
+    p.cb = ns.b;
+    p.cc = ns.c;
+    p.starts = reinterpret_cast<Start*>(ws + l.starts);
     p.rows = (int)rows;
     p.cols = (int)cols;
     p.lanes = l.lanes;
@@ -534,7 +560,7 @@ cudaError_t iterate(const Layout& l, long long batch, long long rows, long long 
         e = gemm::launch<EpiGram>(Product{side, side, r, r, c, nb, 1}, gp, st);
         if (e != cudaSuccess) break;
         const Operand ao = {oa, r, r, l.ldr, l.as, false, false};
-        EpiPoly::Params pp = {oa, da, ob, db, l.ldr, l.as, ns.b, ns.c};
+        EpiPoly::Params pp = {oa, da, ob, db, p.starts, l.ldr, l.as, ns.a, ns.b, ns.c, i};
         e = gemm::launch<EpiPoly>(Product{ao, ao, r, r, r, nb, 1}, pp, st);
         if (e != cudaSuccess) break;
         const Operand bo = {ob, r, r, l.ldr, l.as, false, false};
@@ -546,6 +572,7 @@ cudaError_t iterate(const Layout& l, long long batch, long long rows, long long 
         } else {
             fin.u = u;
             fin.scale /= size;
+            fin.starts = p.starts;
             e = gemm::launch<EpiFinal>(Product{left, right, (int)rows, (int)cols, r, nb, 1}, fin, st);
         }
         std::swap(x[0], x[1]);

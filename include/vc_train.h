@@ -93,7 +93,9 @@ vc_status_t vc_linear_backward(const vc_matrix_t *dy, const vc_matrix_t *x,
 
 /* The Newton-Schulz iteration: `steps` (1 to 100) passes of the polynomial with the
  * coefficients a, b, c, after a division by the Frobenius norm plus eps.  The
- * squares of the values must have a sum that float32 holds. */
+ * squares of the values must have a sum that float32 holds: a norm from 1e-19
+ * to 1.8e19.  (Below, a matrix counts as zero.)  The norm may be far below
+ * eps. */
 typedef struct {
     int steps;
     float a, b, c;

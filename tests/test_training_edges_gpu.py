@@ -7,7 +7,7 @@ from __future__ import annotations
 
 import pytest
 
-from test_training_gpu import ACTS, BF16, act, env, rand
+from test_training_gpu import ACTS, BF16, COEF, ORTHO, act, env, ortho_exact, rand, relative
 
 pytestmark = pytest.mark.gpu
 
@@ -107,6 +107,69 @@ def test_zero_matrices_without_eps(env, shape):
     w0, m = w.clone(), torch.zeros_like(w)
     vc.vc_muon_step(w, g, m, 0.1, eps=0.0)
     assert torch.equal(w, w0) and (m == 0).all()
+
+
+SMALL = [1.0, 1e-2, 1e-4, 1e-6, 1e-9, 1e-12]  # |G| / eps
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 100), (100, 64), (300, 257), (257, 300), (96, 1500)])
+@pytest.mark.parametrize("eps", [1e-7, 1.0])
+def test_norms_below_eps(env, rows, cols, eps):
+    """Where eps is the larger part of the divisor, the result is as exact as
+    anywhere else.  (norms from 1e-19: their squares are float32s)"""
+    torch, vc, dev = env
+    g0 = rand(torch, dev, rows, cols, seed=3, dtype=torch.float32)
+    g0 /= g0.norm()
+    for steps, coef in ((5, COEF), (1, COEF), (12, (1.5, -0.5, 0.0)), (30, (1.9, -1.2, 0.3)),
+                        (2, (-3.0, 4.0, -1.5))):
+        tol = max(ORTHO, ORTHO * (steps / 5) ** 0.5)
+        for ratio in SMALL:
+            g = g0 * (eps * ratio)
+            out = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+            vc.vc_orthogonalize(g, out, steps=steps, coefficients=coef, eps=eps)
+            want = ortho_exact(torch, g, steps, coef, eps)
+            assert relative(out, want) < tol, (steps, coef, ratio)
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 100), (300, 257)])
+def test_scales_at_the_ends_of_float32(env, rows, cols):
+    torch, vc, dev = env
+    g = rand(torch, dev, rows, cols, seed=3, dtype=torch.float32)
+    g /= g.norm()
+    out = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+    for eps, scale in ((1e30, 1.0), (1e12, 1e-15), (1e12, 1e12), (0.0, 1e-18), (0.0, 1e18)):
+        vc.vc_orthogonalize(g * scale, out, eps=eps)
+        assert relative(out, ortho_exact(torch, g * scale, eps=eps)) < ORTHO, (eps, scale)
+    # what falls out of float32 on the way becomes 0, not NaN
+    for eps, coef, steps in ((3e38, COEF, 100), (1e-7, (0.01, 0.0, 0.0), 100), (1e30, (0.1, 0.0, 0.0), 9)):
+        vc.vc_orthogonalize(g * 1e-10, out, eps=eps, coefficients=coef, steps=steps)
+        want = ortho_exact(torch, g * 1e-10, steps, coef, eps)
+        assert ((out.double() - want).abs() <= BF16 * want.abs().max() + 1e-37).all(), (eps, coef)
+    # and what is not finite gives NaN everywhere
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for eps in (0.0, 1e-7, 1e9):
+            h = g.clone()
+            h[rows // 2, cols // 3] = bad
+            vc.vc_orthogonalize(h, out, eps=eps)
+            assert out.isnan().all(), (bad, eps)
+
+
+def test_norms_below_eps_beside_others(env):
+    """Matrices of a batch have their own scales; a Muon step too."""
+    torch, vc, dev = env
+    for rows, cols in ((60, 200), (260, 140)):
+        g = rand(torch, dev, 4, rows, cols, seed=5, dtype=torch.float32)
+        g /= g.norm(dim=(1, 2), keepdim=True)
+        g *= torch.tensor([1.0, 1e-10, 1e-4, 1e-16], device=dev)[:, None, None]
+        out = torch.empty(4, rows, cols, dtype=torch.bfloat16, device=dev)
+        vc.vc_orthogonalize(g, out)
+        want = ortho_exact(torch, g)
+        for i in range(4):
+            assert relative(out[i], want[i]) < ORTHO, i
+        w = torch.zeros_like(g)
+        vc.vc_muon_step(w, g, torch.zeros_like(g), 1.0, nesterov=False, scale=1.0)
+        for i in range(4):
+            assert relative(w[i], -want[i]) < ORTHO, i
 
 
 # -------------------------------------------------------------------- streams --
