@@ -35,23 +35,36 @@ inline bool valid_matrix(const vc_matrix_t* m) {
     return m->batch == 1 || (__int128)m->batch * m->batch_stride <= ((__int128)1 << 58);
 }
 
+// The bytes of an argument: rows of `width`, all of them whole pitches after the
+// first (pitch 0: one row).
 struct Span {
-    uintptr_t lo, hi;
+    uintptr_t lo, hi, width, pitch;
 };
-inline Span span_of(const vc_matrix_t* m) {
-    if (m == nullptr || m->batch == 0 || m->rows == 0 || m->cols == 0) return {0, 0};
-    const long long ld = m->rows > 1 ? m->ld : m->cols;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(m->data);
-    const long long last = (m->batch - 1) * (m->batch > 1 ? m->batch_stride : 0) +
-                           (m->rows - 1) * ld + m->cols;
-    return {lo, lo + (uintptr_t)last * elem_size(m->dtype)};
-}
 inline Span span_of(const void* p, size_t bytes) {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return p == nullptr ? Span{0, 0} : Span{lo, lo + bytes};
+    return p == nullptr ? Span{} : Span{lo, lo + bytes, bytes, 0};
 }
+inline Span span_of(const vc_matrix_t* m) {
+    if (m == nullptr || m->batch == 0 || m->rows == 0 || m->cols == 0) return {};
+    const uintptr_t es = elem_size(m->dtype), lo = reinterpret_cast<uintptr_t>(m->data);
+    // (sizes and strides were checked: nothing here passes 2^61)
+    const uintptr_t row = m->rows > 1 ? m->ld * es : 0, next = m->batch > 1 ? m->batch_stride * es : 0;
+    const uintptr_t width = m->cols * es;
+    const uintptr_t matrix = (m->rows - 1) * row + width, all = (m->batch - 1) * next + matrix;
+    if (row == 0) return {lo, lo + all, width, next};
+    if (next % row == 0) return {lo, lo + all, width, row};
+    // matrices that do not lie on one grid of rows: taken whole
+    return {lo, lo + all, matrix, next};
+}
+// Slices of one wider tensor interleave without an overlap: with the same
+// pitch, b's rows lie between a's where b's first byte falls, in a's pitch,
+// behind a's row, and b's row ends before a's next one.
 inline bool overlap(Span a, Span b) {
-    return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi;
+    if (!(a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi)) return false;
+    const uintptr_t pitch = a.pitch != 0 ? a.pitch : b.pitch;
+    if (pitch == 0 || (a.pitch != 0 && b.pitch != 0 && a.pitch != b.pitch)) return true;
+    const uintptr_t after = b.lo >= a.lo ? (b.lo - a.lo) % pitch : (pitch - (a.lo - b.lo) % pitch) % pitch;
+    return after < a.width || after + b.width > pitch;
 }
 // Exactly the same elements (an output that may stand in an input's place).
 inline bool same_matrix(const vc_matrix_t* a, const vc_matrix_t* b) {

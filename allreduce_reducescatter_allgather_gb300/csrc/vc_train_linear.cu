@@ -516,7 +516,7 @@ vc_status_t vc_linear_backward(const vc_matrix_t* dy, const vc_matrix_t* x,
     const Span outs[4] = {span_of(dx), span_of(dweight), span_of(dbias, (size_t)N * bias_size),
                           span_of(workspace, need)};
     const Span ins[4] = {span_of(dy), span_of(x), span_of(weight),
-                         has_act ? span_of(preact) : Span{0, 0}};
+                         has_act ? span_of(preact) : Span{}};
     for (int o = 0; o < 4; ++o) {
         for (int i = 0; i < 4; ++i)
             if (overlap(outs[o], ins[i])) return VC_ERR_ALIAS;

@@ -18,7 +18,8 @@
  * call returns; calls are asynchronous on `stream`; arguments are checked on
  * the host and a call that returns an error launches nothing; entry points
  * are thread-safe.  Outputs must not overlap inputs, except where a comment
- * says that they may be the same matrix.
+ * says that they may be the same matrix.  (Column slices of one wider tensor
+ * do not overlap.)
  *
  * Arithmetic.  Products run on the tensor cores with 16-bit operands and
  * 32-bit accumulators; biases, activations, residuals, norms, column sums and

@@ -284,6 +284,43 @@ def test_binding_refuses_host_tensors(tr):
         tr.vc_muon_step([1.0], t, t, lr=0.1)
 
 
+def test_slices_that_interleave_are_no_aliases(tr):
+    """Columns 0..63 and 64..87 of rows of 100 values share no element; one
+    column more, from either side, does."""
+    def x(first, n, ld=100, rows=10):
+        return mat(tr, GiB + 2 * first, rows, n, ld=ld)
+    def fwd(*a, ws=8 * GiB, size=GiB, **kw):
+        return forward(tr, *a, ws=ws, size=size, **kw)
+    w = mat(tr, 2 * GiB, 24, 64)
+    assert fwd(x(0, 64), w, x(64, 24)) == CUDA
+    assert fwd(x(36, 64), w, x(12, 24)) == CUDA
+    assert fwd(x(36, 64), w, x(100, 24)) == CUDA       # from the next row on
+    assert fwd(x(0, 64), w, x(63, 24)) == ALIAS
+    assert fwd(x(36, 64), w, x(13, 24)) == ALIAS
+    assert fwd(x(36, 64), w, x(77, 24)) == ALIAS       # reaches into the next row
+    assert fwd(x(0, 64), w, x(64, 24, ld=101)) == ALIAS  # rows drift over each other
+    assert fwd(x(0, 64), w, x(64, 24, ld=200)) == ALIAS
+    # one row, or a vector, between the rows of a matrix
+    one = mat(tr, GiB + 2 * 164, 1, 24, ld=0)
+    assert fwd(mat(tr, 3 * GiB, 1, 64), w, one, res=one) == CUDA
+    assert fwd(x(0, 64), w, mat(tr, 4 * GiB, 10, 24), bias=GiB + 2 * 164) == CUDA
+    assert fwd(mat(tr, 3 * GiB, 10, 64), w, x(0, 24), bias=GiB + 2 * 164) == CUDA
+    assert fwd(mat(tr, 3 * GiB, 10, 64), w, x(0, 24), bias=GiB + 2 * 176) == CUDA
+    assert fwd(mat(tr, 3 * GiB, 10, 64), w, x(0, 24), bias=GiB + 2 * 177) == ALIAS
+    assert fwd(mat(tr, 3 * GiB, 10, 64), w, x(0, 24), bias=GiB + 2 * 123) == ALIAS
+    # a workspace may not reach into a matrix's rows
+    odd, wo = mat(tr, 3 * GiB, 10, 65), mat(tr, 2 * GiB, 24, 65)
+    need = tr._lib().vc_linear_forward_workspace(ref(odd), ref(wo))
+    assert fwd(odd, wo, x(0, 24), ws=GiB + 128, size=need) == ALIAS
+
+    def three(first, stride=100 * 100, cols=30):
+        return mat(tr, GiB + 4 * first, 100, cols, ld=100, dtype=F32, batch=3, stride=stride)
+    assert muon(tr, three(0), three(30), three(60)) == CUDA
+    assert muon(tr, three(0), three(30), three(59)) == ALIAS
+    assert muon(tr, three(0), three(30, stride=100 * 101), three(60)) == CUDA
+    assert muon(tr, three(0), three(30, stride=100 * 101 + 1), three(60)) == ALIAS
+
+
 class FakeCuda:
     """What PreparedOperator asks of torch: streams by number, events, and a
     log of what is done with them."""

@@ -172,6 +172,39 @@ def test_norms_below_eps_beside_others(env):
             assert relative(w[i], -want[i]) < ORTHO, i
 
 
+# --------------------------------------------------------------------- slices --
+
+def test_slices_of_one_tensor_that_interleave(env):
+    """Inputs and outputs may be column slices of one wider tensor."""
+    torch, vc, dev = env
+    m, n, k = 70, 40, 48
+    for at in (0, 3, 8):
+        wide = rand(torch, dev, m, at + k + 2 * n + 9, seed=1)
+        before = wide.clone()
+        x, y, z = wide[:, at:at + k], wide[:, at + k:at + k + n], wide[:, at + k + n:at + k + 2 * n]
+        w = rand(torch, dev, n, k, seed=2)
+        y2, z2 = (torch.empty(m, n, dtype=torch.bfloat16, device=dev) for _ in range(2))
+        vc.vc_linear_forward(x.contiguous(), w, y2, preact=z2, activation="silu")
+        vc.vc_linear_forward(x, w, y, preact=z, activation="silu")
+        assert torch.equal(y, y2) and torch.equal(z, z2)
+        before[:, at + k:at + k + n] = y2
+        before[:, at + k + n:at + k + 2 * n] = z2
+        assert torch.equal(wide, before)
+        both = rand(torch, dev, m, 2 * k + at, seed=4)
+        x, dx = both[:, :k], both[:, k + at:]
+        dx2, dy = torch.empty(m, k, dtype=torch.bfloat16, device=dev), rand(torch, dev, m, n, seed=5)
+        vc.vc_linear_backward(dy, x.contiguous(), w, dx=dx2, preact=z2, activation="silu")
+        vc.vc_linear_backward(dy, x, w, dx=dx, preact=z, activation="silu")
+        assert torch.equal(dx, dx2)
+    for rows, cols in ((30, 50), (200, 150)):
+        wide = rand(torch, dev, 2, rows, 3 * cols, seed=6, dtype=torch.float32)
+        parts = [wide[:, :, i * cols:(i + 1) * cols] for i in range(3)]
+        alone = [p.contiguous() for p in parts]
+        vc.vc_muon_step(*parts, 0.1)
+        vc.vc_muon_step(*alone, 0.1)
+        assert all(torch.equal(a, b) for a, b in zip(parts, alone))
+
+
 # -------------------------------------------------------------------- streams --
 
 @pytest.mark.parametrize("how", ["argument", "current"])
