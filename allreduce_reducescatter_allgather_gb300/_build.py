@@ -22,8 +22,6 @@ LIB = LIBDIR / "libvc.so"
 
 SOURCES = ["vc_api.cu", "vc_reduce_dispatch.cu", "vc_noalloc.cu", "vc_copy.cu", "vc_bucket.cu",
            "vc_gemm.cu", "vc_train_linear.cu", "vc_train_muon.cu"]
-HEADERS = ["vc_device.cuh", "vc_launch.cuh", "vc_bucket_kernel.cuh", "vc_gemm.cuh",
-           "vc_train_common.cuh"]
 # vc_reduce_inst.cu compiled once per (element type, op, order group):
 # (object, -D flags).  Groups: 0 ring + recursive halving, 1 tree, 2 double
 # binary tree.  The integer types have group 0 only (ring): their results
@@ -56,13 +54,16 @@ def _cuda_lib_dir(nvcc: str) -> Path:
     return Path(nvcc).resolve().parent.parent / "lib64"
 
 
+def dependencies() -> list[Path]:
+    """Every file the library is built from: all sources and headers."""
+    return [*sorted(CSRC.glob("*.cu*")), *sorted(INCLUDE.glob("*.h")), Path(__file__)]
+
+
 def _stale() -> bool:
     if not LIB.exists():
         return True
     t = LIB.stat().st_mtime
-    deps = [CSRC / s for s in SOURCES + HEADERS + [INSTANCE_SOURCE, BUCKET_SOURCE]] + [
-        INCLUDE / "vc.h", INCLUDE / "vc_train.h", Path(__file__)]
-    return any(d.stat().st_mtime > t for d in deps)
+    return any(d.stat().st_mtime > t for d in dependencies())
 
 
 def build_library(force: bool = False, jobs: int | None = None) -> Path:

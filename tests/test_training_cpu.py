@@ -59,6 +59,27 @@ def test_library_exports_what_the_header_declares(tr):
     assert set(header_functions()) <= exported
 
 
+def test_an_edit_of_any_source_is_noticed(tr, monkeypatch, tmp_path):
+    """The library counts as old when any file that one of its sources
+    includes is newer."""
+    import os
+    from allreduce_reducescatter_allgather_gb300 import _build
+    included = set()
+    for f in _build.CSRC.iterdir():
+        assert f in _build.dependencies(), f.name
+        included |= set(re.findall(r'#include "(.*?)"', f.read_text()))
+    assert {"vc_ns_small.cuh", "vc_train.h"} <= included
+    assert included <= {f.name for f in _build.dependencies()}
+    lib = tmp_path / "lib.so"
+    lib.touch()
+    monkeypatch.setattr(_build, "LIB", lib)
+    newest = max(f.stat().st_mtime for f in _build.dependencies())
+    os.utime(lib, (newest, newest))
+    assert not _build._stale()
+    os.utime(lib, (newest - 1, newest - 1))
+    assert _build._stale()
+
+
 def forward(tr, x, w, y, bias=0, res=None, z=None, act=NONE, ws=0, size=0):
     return tr._lib().vc_linear_forward(ref(x), ref(w), bias, ref(res), ref(y), ref(z), act, ws,
                                        size, None)
