@@ -342,6 +342,40 @@ def test_slices_that_interleave_are_no_aliases(tr):
     assert muon(tr, three(0), three(30, stride=100 * 101 + 1), three(60)) == ALIAS
 
 
+class PlainMuon:
+    """vc_muon_step on the host; the ways in which it can be wrong."""
+
+    def __init__(self, fault=None):
+        self.fault = fault
+
+    def vc_muon_step(self, w, grad, m, lr, scale):
+        if self.fault == "nothing written":
+            return
+        m.copy_(0.95 * m + grad)
+        if self.fault == "momentum alone":
+            return
+        o = (m if self.fault == "no nesterov" else grad + 0.95 * m).double()
+        o = o / o.norm()
+        for _ in range(4 if self.fault == "a pass short" else 5):
+            a = o @ o.t()
+            o = 3.4445 * o + (-4.7750 * a + 2.0315 * (a @ a)) @ o
+        w.sub_((lr * scale * o * (1.01 if self.fault == "scale" else 1)).float())
+        if self.fault == "momentum":
+            m.mul_(1.001)
+
+
+@pytest.mark.parametrize("fault", [None, "nothing written", "momentum alone", "momentum",
+                                   "no nesterov", "a pass short", "scale"])
+def test_smoke_rejects_wrong_muon_steps(fault):
+    torch = pytest.importorskip("torch")
+    import __graft_entry__ as entry
+    if fault is None:
+        entry._check_muon(torch, PlainMuon(), torch.device("cpu"))
+        return
+    with pytest.raises(AssertionError):
+        entry._check_muon(torch, PlainMuon(fault), torch.device("cpu"))
+
+
 class FakeCuda:
     """What PreparedOperator asks of torch: streams by number, events, and a
     log of what is done with them."""
