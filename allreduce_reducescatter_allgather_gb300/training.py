@@ -5,7 +5,8 @@ step.
 Argument marshalling only, as for the collectives: tensors in, device
 pointers and a CUDA stream out to libvc.so.  Outputs are the caller's tensors;
 nothing is returned.  A `workspace` (a CUDA uint8 tensor of the size the
-*_workspace functions give) may be passed in; without one it comes from
+*_workspace functions give, on 16 bytes for the linear layer and on 256 for
+the others) may be passed in; without one it comes from
 torch's allocator, on the stream of the call.
 
 Matrices are tensors of two dimensions (three for a batch of them) whose last
@@ -153,7 +154,7 @@ def _ref(m):
     return ctypes.byref(m) if m is not None else None
 
 
-def _workspace(workspace, need, device, stream):
+def _workspace(workspace, need, device, stream, align):
     """The pointer and size to pass, the tensor to keep until the call has
     been enqueued, and it again where it is new.  A new one is allocated on the
     call's stream, so that torch's allocator gives it out again only behind the
@@ -172,8 +173,8 @@ def _workspace(workspace, need, device, stream):
         _tensor("workspace", workspace, (torch.uint8,), device)
         if not workspace.is_contiguous() or workspace.numel() < need:
             raise ValueError(f"workspace holds {workspace.numel()} bytes, {need} are needed")
-        if workspace.data_ptr() % 256 != 0:
-            raise ValueError("workspace is not aligned to 256 bytes")
+        if workspace.data_ptr() % align != 0:
+            raise ValueError(f"workspace is not aligned to {align} bytes")
     return (ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), workspace,
             workspace if new else None)
 
@@ -280,7 +281,7 @@ def _forward(x, weight, out, bias, residual, preact, activation, workspace, stre
     act = _activation(activation)
     L = _lib()
     need = int(L.vc_linear_forward_workspace(_ref(xm), _ref(wm)))
-    ws, size, held, made = _workspace(workspace, need, dev, stream)
+    ws, size, held, made = _workspace(workspace, need, dev, stream, 16)
     args = (_ref(xm), _ref(wm), ctypes.c_void_p(bias.data_ptr() if bias is not None else 0),
             _ref(rm), _ref(om), _ref(pm), act, ws, size)
     return L.vc_linear_forward, args, dev, (x, weight, out, bias, residual, preact, held,
@@ -339,7 +340,7 @@ def _backward(dy, x, weight, dx, dweight, dbias, preact, activation, accumulate,
     L = _lib()
     need = int(L.vc_linear_backward_workspace(_ref(ym), _ref(xm), _ref(wm), act,
                                               int(dbias is not None)))
-    ws, size, held, made = _workspace(workspace, need, dev, stream)
+    ws, size, held, made = _workspace(workspace, need, dev, stream, 16)
     args = (_ref(ym), _ref(xm), _ref(wm), _ref(pm), act, _ref(dxm), _ref(dwm),
             ctypes.c_void_p(dbias.data_ptr() if dbias is not None else 0),
             _code(dbias) if dbias is not None else 3, int(bool(accumulate)), ws, size)
@@ -394,7 +395,7 @@ def _orthogonalize(g, out, steps, coefficients, eps, workspace, stream):
     _same_shape("out", out, g)
     ns = _newton_schulz(steps, coefficients, eps)
     need = orthogonalize_workspace(g.shape)
-    ws, size, held, made = _workspace(workspace, need, g.device, stream)
+    ws, size, held, made = _workspace(workspace, need, g.device, stream, 256)
     return _lib().vc_orthogonalize, (_ref(gm), _ref(om), _ref(ns), ws, size), g.device, (
         g, out, held, gm, om, ns), made
 
@@ -440,7 +441,7 @@ def _muon(weight, grad, momentum, beta, nesterov, weight_decay, scale, steps, co
     args = Muon(0.0, beta, weight_decay, scale, int(bool(nesterov)),
                 _newton_schulz(steps, coefficients, eps))
     need = orthogonalize_workspace(weight.shape)
-    ws, size, held, made = _workspace(workspace, need, weight.device, stream)
+    ws, size, held, made = _workspace(workspace, need, weight.device, stream, 256)
     return (_lib().vc_muon_step, (_ref(wm), _ref(gm), _ref(mm), _ref(args), ws, size),
             weight.device, (weight, grad, momentum, held, wm, gm, mm), made, args)
 

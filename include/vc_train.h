@@ -63,7 +63,8 @@ typedef enum {
 } vc_act_t;
 
 /* Bytes of workspace that vc_linear_forward needs for these operands (0 where
- * both lie on 16 bytes); 0 too where they are invalid. */
+ * both lie on 16 bytes); 0 too where they are invalid.  The linear layer's
+ * workspaces are aligned to 16 bytes. */
 size_t vc_linear_forward_workspace(const vc_matrix_t *x, const vc_matrix_t *weight);
 
 /* y = act(x W^T + bias) + residual.  x [M, K], weight [N, K], y [M, N], all
@@ -104,7 +105,7 @@ typedef struct {
 } vc_newton_schulz_t;
 
 /* Bytes of workspace for matrices of these sizes (orthogonalize and muon
- * step); 0 where a size is invalid. */
+ * step), which is aligned to 256 bytes; 0 where a size is invalid. */
 size_t vc_orthogonalize_workspace(long long batch, long long rows, long long cols);
 
 /* out <- the orthogonalised g, each matrix of the batch by itself.  g float32

@@ -205,6 +205,31 @@ def test_slices_of_one_tensor_that_interleave(env):
         assert all(torch.equal(a, b) for a, b in zip(parts, alone))
 
 
+def test_alignment_of_given_workspaces(env):
+    """16 bytes for the linear layer, 256 for the rest, as the header says."""
+    torch, vc, dev = env
+    m, n, k = 70, 41, 51
+    x, w, dy = (rand(torch, dev, *s, seed=i) for i, s in enumerate(((m, k), (n, k), (m, n))))
+    y, y2, dx, dx2 = (torch.empty(m, c, dtype=torch.bfloat16, device=dev) for c in (n, n, k, k))
+    g = rand(torch, dev, 140, 150, seed=4)
+    out = torch.empty_like(g)
+    need = max(vc.linear_forward_workspace(x, w), vc.linear_backward_workspace(dy, x, w, "relu"),
+               vc.orthogonalize_workspace(g.shape))
+    big = torch.empty(need + 512, dtype=torch.uint8, device=dev)
+    vc.vc_linear_forward(x, w, y)
+    vc.vc_linear_backward(dy, x, w, dx=dx, preact=y, activation="relu")
+    for at in (16, 48, 256):
+        y2.zero_(), dx2.zero_()
+        vc.vc_linear_forward(x, w, y2, workspace=big[at:])
+        vc.vc_linear_backward(dy, x, w, dx=dx2, preact=y, activation="relu", workspace=big[at:])
+        assert torch.equal(y, y2) and torch.equal(dx, dx2)
+    vc.vc_orthogonalize(g, out, workspace=big[256:])
+    with pytest.raises(ValueError, match="aligned to 16 bytes"):
+        vc.vc_linear_forward(x, w, y, workspace=big[8:])
+    with pytest.raises(ValueError, match="aligned to 256 bytes"):
+        vc.vc_orthogonalize(g, out, workspace=big[128:])
+
+
 # -------------------------------------------------------------------- streams --
 
 @pytest.mark.parametrize("how", ["argument", "current"])
