@@ -1,8 +1,6 @@
 // Host side of the product kernel: tensor maps, and the count of waits that
-// ran out.
-#include <mutex>
-#include <set>
-#include <utility>
+// ran out.  Nothing here allocates or throws: C entry points call it.
+#include <atomic>
 
 #include "vc_gemm.cuh"
 #include "vc_train.h"
@@ -17,20 +15,21 @@ namespace {
 __device__ unsigned g_timeouts = 0;
 }
 
-// Looked up once per device (as sm_count does).
+constexpr int kMaxDevices = 64;
+
+// Looked up once per device (by two threads at once, if it so happens).
 unsigned* timeout_counter() {
-    constexpr int kMaxDevices = 64;
-    static std::mutex mu;
-    static unsigned* where[kMaxDevices] = {nullptr};
+    static std::atomic<unsigned*> where[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-    std::lock_guard<std::mutex> lock(mu);
-    if (where[dev] == nullptr) {
+    unsigned* at = where[dev].load(std::memory_order_relaxed);
+    if (at == nullptr) {
         void* p = nullptr;
         if (cudaGetSymbolAddress(&p, g_timeouts) != cudaSuccess) return nullptr;
-        where[dev] = static_cast<unsigned*>(p);
+        at = static_cast<unsigned*>(p);
+        where[dev].store(at, std::memory_order_relaxed);
     }
-    return where[dev];
+    return at;
 }
 
 int device_sms() { return sm_count(); }
@@ -45,31 +44,41 @@ typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void
 // cuTensorMapEncodeTiled through the runtime (the library does not link the
 // driver); looked up once.
 EncodeFn encoder() {
-    static std::once_flag once;
-    static EncodeFn fn = nullptr;
-    std::call_once(once, [] {
+    static std::atomic<EncodeFn> found;
+    EncodeFn fn = found.load(std::memory_order_relaxed);
+    if (fn == nullptr) {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult r;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
                                              &r) == cudaSuccess &&
             r == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<EncodeFn>(p);
-    });
+        found.store(fn, std::memory_order_relaxed);
+    }
     return fn;
 }
 
 }  // namespace
 
+// (a kernel that finds its places of the table taken sets its limit each time)
 cudaError_t allow_smem(const void* kernel) {
+    constexpr unsigned kPlaces = 256, kProbes = 16;
+    static std::atomic<const void*> done[kMaxDevices][kPlaces];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    static std::mutex mu;
-    static std::set<std::pair<int, const void*>> done;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count({dev, kernel}) != 0) return cudaSuccess;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    const unsigned first = (unsigned)(reinterpret_cast<uintptr_t>(kernel) >> 4) * 2654435761u >> 24;
+    unsigned i = 0;
+    const void* there = nullptr;
+    for (; i < kProbes; ++i) {
+        there = done[dev][(first + i) % kPlaces].load(std::memory_order_relaxed);
+        if (there == kernel) return cudaSuccess;
+        if (there == nullptr) break;
+    }
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerBlock);
-    if (e == cudaSuccess) done.insert({dev, kernel});
+    if (e == cudaSuccess && i < kProbes)
+        done[dev][(first + i) % kPlaces].compare_exchange_strong(there, kernel, std::memory_order_relaxed);
     return e;
 }
 

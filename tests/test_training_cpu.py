@@ -80,6 +80,19 @@ def test_an_edit_of_any_source_is_noticed(tr, monkeypatch, tmp_path):
     assert _build._stale()
 
 
+def test_entry_points_do_not_throw(tr):
+    """What the training operators are compiled to neither allocates host
+    memory nor throws: no exception can leave a C entry point."""
+    from allreduce_reducescatter_allgather_gb300 import _build
+    for stem in ("vc_gemm", "vc_train_linear", "vc_train_muon"):
+        out = subprocess.run(["nm", "-u", "-C", str(_build.BUILD / f"{stem}.o")],
+                             capture_output=True, text=True, check=True).stdout
+        assert "cudaLaunchKernel" in out or "cudaFuncSetAttribute" in out
+        bad = [line.split(" U ")[-1] for line in out.splitlines()
+               if re.search(r"operator new|throw|__once|_Rb_tree", line)]
+        assert not bad, (stem, bad)
+
+
 def forward(tr, x, w, y, bias=0, res=None, z=None, act=NONE, ws=0, size=0):
     return tr._lib().vc_linear_forward(ref(x), ref(w), bias, ref(res), ref(y), ref(z), act, ws,
                                        size, None)
