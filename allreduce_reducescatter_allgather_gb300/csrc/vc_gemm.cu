@@ -99,6 +99,28 @@ bool encode_operand(CUtensorMap* map, const Operand& o, int batch, int box_rows)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
+
+// A block whose warps wait, for about half a millisecond, for what never
+// comes, as a product kernel's would if a copy were lost: it gives up, ends
+// and counts itself.  For tests of the report (VC_TEST_WAIT_OUT).
+__global__ void __launch_bounds__(128) wait_out_kernel(unsigned* timeouts) {
+    __shared__ __align__(8) uint64_t barrier;
+    __shared__ int dead_word;
+    volatile int* const dead = &dead_word;
+    const unsigned bar = smem_u32(&barrier);
+    if (threadIdx.x == 0) {
+        mbar_init(bar, 1);
+        *dead = 0;
+    }
+    __syncthreads();
+    bool alive = true;
+    for (int i = 0; alive && i < 1000; ++i) alive = warp_wait(bar, 0, dead, 1000000);
+    __syncthreads();
+    bury(dead, timeouts);
+}
+
+}  // namespace
 }  // namespace gemm
 }  // namespace vc
 
@@ -108,6 +130,11 @@ extern "C" vc_status_t vc_train_timeouts(unsigned* count) {
     if (v != nullptr && v[0] != '\0' && v[0] != '0') return VC_ERR_CUDA;
     const unsigned* p = vc::gemm::timeout_counter();
     if (p == nullptr) return VC_ERR_CUDA;
+    const char* out = getenv("VC_TEST_WAIT_OUT");
+    if (out != nullptr && out[0] != '\0' && out[0] != '0') {
+        vc::gemm::wait_out_kernel<<<1, 128>>>(const_cast<unsigned*>(p));
+        if (cudaGetLastError() != cudaSuccess) return VC_ERR_CUDA;
+    }
     // (the copy alone would not wait for streams that do not block)
     if (cudaDeviceSynchronize() != cudaSuccess) return VC_ERR_CUDA;
     return cudaMemcpy(count, p, sizeof *count, cudaMemcpyDeviceToHost) == cudaSuccess

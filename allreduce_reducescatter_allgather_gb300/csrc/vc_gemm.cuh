@@ -121,12 +121,13 @@ __device__ __forceinline__ bool mbar_try(unsigned bar, unsigned parity) {
 
 // Waits for the barrier's phase; false when the block is dead or the wait
 // has run out (and the block is dead from then on).
-__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, volatile int* dead) {
+__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, volatile int* dead,
+                                          long long limit = kWaitCycles) {
     if (mbar_try(bar, parity)) return true;
     const long long t0 = clock64();
     while (!mbar_try(bar, parity)) {
         if (*dead) return false;
-        if (clock64() - t0 > kWaitCycles) {
+        if (clock64() - t0 > limit) {
             *dead = 1;
             return false;
         }
@@ -135,8 +136,9 @@ __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, volatil
 }
 
 // The same for a whole converged warp: every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(unsigned bar, unsigned parity, volatile int* dead) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, dead));
+__device__ __forceinline__ bool warp_wait(unsigned bar, unsigned parity, volatile int* dead,
+                                          long long limit = kWaitCycles) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, dead, limit));
 }
 
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {

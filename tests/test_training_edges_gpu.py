@@ -5,8 +5,12 @@ from the same arithmetic (bf16 keeps 8 significant bits).
 """
 from __future__ import annotations
 
+import subprocess
+import sys
+
 import pytest
 
+from conftest import ROOT
 from test_training_gpu import ACTS, BF16, COEF, ORTHO, act, env, ortho_exact, rand, relative
 
 pytestmark = pytest.mark.gpu
@@ -285,3 +289,30 @@ def test_timeouts_wait_for_every_stream(env):
         torch.cuda._sleep(200_000_000)
     assert vc.train_timeouts() == 0
     assert side.query()  # its work has ended
+
+
+# (in a process of its own: the count stays for as long as the library is loaded)
+WAIT_OUT = """
+import os, sys
+sys.path.insert(0, sys.argv[1])
+import torch
+import allreduce_reducescatter_allgather_gb300 as vc
+x = torch.randn(100, 64, device="cuda").bfloat16()
+y, z = (torch.empty(100, 100, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+vc.vc_linear_forward(x, x, y)
+assert vc.train_timeouts() == 0
+os.environ["VC_TEST_WAIT_OUT"] = "1"
+assert vc.train_timeouts() == 1
+assert vc.train_timeouts() == 2
+del os.environ["VC_TEST_WAIT_OUT"]
+assert vc.train_timeouts() == 2
+vc.vc_linear_forward(x, x, z)  # the context is as usable as before
+assert torch.equal(y, z) and torch.isfinite(z.float()).all()
+print("done")
+"""
+
+
+def test_a_wait_that_runs_out_is_counted(env):
+    out = subprocess.run([sys.executable, "-c", WAIT_OUT, str(ROOT)], capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "done", out.stderr
