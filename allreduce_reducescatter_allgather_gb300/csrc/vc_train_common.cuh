@@ -14,8 +14,10 @@ namespace train {
 
 inline int elem_size(vc_dtype_t dt) { return dt == VC_FLOAT32 ? 4 : dt == VC_BFLOAT16 ? 2 : 0; }
 
-// The largest extent of one dimension: tile and TMA coordinates are ints.
-constexpr long long kMaxExtent = 1ll << 30;
+// The largest extent of one dimension: tile and TMA coordinates are ints.  Of
+// all: no more than any memory holds, so that tiles can be counted in ints.
+// And of a row's pitch: TMA's stay below 2^40 bytes.
+constexpr long long kMaxExtent = 1ll << 30, kMaxElements = 1ll << 38, kMaxPitch = (1ll << 39) - 8;
 
 // A matrix argument: sizes, alignment, strides.  Empty matrices need no data.
 inline bool valid_matrix(const vc_matrix_t* m) {
@@ -25,8 +27,9 @@ inline bool valid_matrix(const vc_matrix_t* m) {
     if (m->batch < 0 || m->rows < 0 || m->cols < 0) return false;
     if (m->batch > kMaxExtent || m->rows > kMaxExtent || m->cols > kMaxExtent) return false;
     if (m->batch == 0 || m->rows == 0 || m->cols == 0) return true;
+    if ((__int128)m->batch * m->rows * m->cols > kMaxElements) return false;
     if (m->data == nullptr || reinterpret_cast<uintptr_t>(m->data) % es != 0) return false;
-    if (m->rows > 1 && (m->ld < m->cols || m->ld > (1ll << 40))) return false;
+    if (m->rows > 1 && (m->ld < m->cols || m->ld > kMaxPitch)) return false;
     const long long ld = m->rows > 1 ? m->ld : m->cols;
     const __int128 one = (__int128)(m->rows - 1) * ld + m->cols;
     if (one > ((__int128)1 << 58)) return false;

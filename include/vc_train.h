@@ -39,7 +39,8 @@ extern "C" {
  * data[k * batch_stride + i * ld + j].  ld >= cols (any value where rows <= 1);
  * batch_stride is not read where batch is 1 and covers a whole matrix
  * otherwise.  dtype is VC_FLOAT32 or VC_BFLOAT16; data is aligned to its
- * element.  Bases on 16 bytes with an ld of whole 16 bytes take the fastest
+ * element.  No side is above 2^30, no matrix or batch above 2^38 elements, no ld
+ * above 2^39 - 8.  Bases on 16 bytes with an ld of whole 16 bytes take the fastest
  * path; others are copied into the workspace first (tensor-core operands) or
  * accessed element by element (the rest). */
 typedef struct {

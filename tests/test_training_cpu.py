@@ -355,6 +355,19 @@ def test_slices_that_interleave_are_no_aliases(tr):
     assert muon(tr, three(0), three(30, stride=100 * 101 + 1), three(60)) == ALIAS
 
 
+def test_sizes_that_no_launch_could_take(tr):
+    """Refused before anything is launched: more tiles than ints count, rows
+    further apart than a tensor map can say."""
+    big, far = 1 << 20, (1 << 39) - 8
+    w = mat(tr, 2 * GiB, big, 8)
+    assert forward(tr, mat(tr, GiB, big, 8), w, mat(tr, 1 << 45, big, big)) == INVALID
+    assert forward(tr, mat(tr, GiB, big // 4, 8), w, mat(tr, 1 << 45, big // 4, big)) == CUDA
+    one = mat(tr, 3 * GiB, 10, 24)
+    assert forward(tr, mat(tr, 1 << 45, 10, 64, ld=far), mat(tr, 2 * GiB, 24, 64), one) == CUDA
+    assert forward(tr, mat(tr, 1 << 45, 10, 64, ld=far + 8), mat(tr, 2 * GiB, 24, 64), one) == INVALID
+    assert ortho(tr, mat(tr, GiB, 1 << 19, 1 << 19, batch=2), mat(tr, 1 << 45, 1 << 19, 1 << 19, batch=2)) == INVALID
+
+
 class PlainMuon:
     """vc_muon_step on the host; the ways in which it can be wrong."""
 
