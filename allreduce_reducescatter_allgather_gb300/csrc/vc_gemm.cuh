@@ -1386,9 +1386,13 @@ cudaError_t launch_split(const Product* p, const typename Epi::Params* ep, int r
 
 // How long a product takes, in microseconds, by a model of the kernels that was
 // fitted to measurements of 1 to 512 tiles and K of 64 to 8192 on operands in
-// L2 (within 20 % of most): a fixed part, and for each wave of tiles the larger
-// of its K blocks' time and its epilogue's, which is longer where a matrix's
-// rows are off 16 bytes (`odd`).
+// L2, with plain stores: a fixed part, and for each wave of tiles the larger of
+// its K blocks' time and its epilogue's, which is longer where a matrix's rows
+// are off 16 bytes (`odd`).  It is within 20 % of most of those, but too low
+// for the Newton-Schulz products, whose epilogues read and write more: of 4096 x
+// 1024, the update 11.4 us by the model and 19.4 measured, X^T X 9.5 and 12.5,
+// b A + c A^2 6.1 and 9.0; of 8 x 2048 x 8192 258 and 366, 149 and 176, 44 and
+// 55.  It is there to choose a kernel, not to predict a time.
 //   pair kernel, 256 x 256:   6.5 + waves of 76 x max(0.275 K blocks + 0.5, 3.2)
 //   split kernel, 128 x 64:   1.5 + 2.3 waves of 304 + 0.2 (blocks per SM) K blocks
 //   split kernel, 128 x 128:  1.5 + waves of 152 x (2.8 + 0.28 K blocks)

@@ -9,9 +9,12 @@
 //
 // Numbers.  The products' operands are fp16: their values are bounded (|X| at
 // most about 1.2 in the spectral norm), so fp16's 11 significant bits are
-// worth more than bf16's range.  Three measures keep the result within about
-// 1e-3 of the exact iteration, below the bf16 rounding of the output (bf16
-// operands: 1e-2):
+// worth more than bf16's range.  Three measures keep the result near the exact
+// iteration, beside 1.65e-3 of the norm for the bf16 rounding of the output:
+// 4e-4 to 1e-3 off for matrices of full rank (bf16 operands: 2e-2 to 3e-2), 2.5e-3
+// to 3.3e-3 for sums of few outer products (bf16: 0.1 to 1.9); 5e-3 was the worst
+// (rank one of 96 rows, matrices of a few values).  What is left are the
+// roundings of A and B, which coefficients of up to 4.8 raise in each pass:
 //   - X is stored times a power of two near sqrt(c), so that its values are
 //     about 1 at the end and normal fp16 numbers at the start (where eps
 //     outweighs the norm: struct Start);

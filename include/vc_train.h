@@ -87,7 +87,10 @@ size_t vc_linear_backward_workspace(const vc_matrix_t *dy, const vc_matrix_t *x,
  * NULL; dbias: N values of dbias_dtype (bfloat16 or float32), or NULL.  With
  * accumulate non-zero dweight and dbias are added to (in 32 bits, then
  * rounded), else overwritten.  dz is rounded to bfloat16 before the products
- * (a tensor-core operand); with VC_ACT_NONE dz is dy and nothing is rounded. */
+ * (a tensor-core operand), so that dx and dweight, of whatever type, are 1.7e-3
+ * of their norm off; batches of up to 64 rows keep the remainder of the rounding
+ * (2e-5); with VC_ACT_NONE dz is dy and nothing is rounded.  dbias sums dz in 32
+ * bits. */
 vc_status_t vc_linear_backward(const vc_matrix_t *dy, const vc_matrix_t *x,
                                const vc_matrix_t *weight, const vc_matrix_t *preact, vc_act_t act,
                                const vc_matrix_t *dx, const vc_matrix_t *dweight, void *dbias,
@@ -110,8 +113,11 @@ typedef struct {
 size_t vc_orthogonalize_workspace(long long batch, long long rows, long long cols);
 
 /* out <- the orthogonalised g, each matrix of the batch by itself.  g float32
- * or bfloat16, out bfloat16 (the products keep about 10 bits), of the same
- * sizes; out may be g (bfloat16).  A zero matrix gives zeros; a matrix with a
+ * or bfloat16, out bfloat16, of the same sizes; out may be g (bfloat16).  Before
+ * out's rounding the five default passes are within 1e-3 of the norm of the
+ * exact iteration for matrices of full rank, within 3.3e-3 for sums of few outer
+ * products; the worst measured is 5e-3 (rank one of 96 rows; matrices of a few
+ * values).  A zero matrix gives zeros; a matrix with a
  * value that is not finite gives NaN. */
 vc_status_t vc_orthogonalize(const vc_matrix_t *g, const vc_matrix_t *out,
                              const vc_newton_schulz_t *ns, void *workspace, size_t workspace_bytes,
@@ -135,7 +141,8 @@ vc_status_t vc_muon_step(const vc_matrix_t *weight, const vc_matrix_t *grad,
  * since the library was loaded: 0 unless something is broken, and any other
  * value means that results computed since are not valid.  Waits for all
  * streams of the device, then copies one word to the host; not to be called
- * while a stream is captured. */
+ * while a stream is captured.  (For tests: with VC_TEST_WAIT_OUT set to a
+ * non-zero value in the environment a block that gives up runs first.) */
 vc_status_t vc_train_timeouts(unsigned *count);
 
 #ifdef __cplusplus
