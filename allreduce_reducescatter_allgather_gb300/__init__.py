@@ -8,7 +8,9 @@ binding with the same names as the C entry points.
 
 Beside them, the operators of a data-parallel training step (include/vc_train.h,
 training.py): the linear layer, its gradient, Newton-Schulz orthogonalisation and
-the Muon step, on the tensor cores.
+the Muon step, on the tensor cores; and what a step has between and around the
+linear layers (include/vc_step.h, step.py): the embedding and its gradient, the
+norms around a block with its gate and residual, and gradient clipping.
 """
 from ._binding import (  # noqa: F401
     BucketPlan,
@@ -49,4 +51,19 @@ from .training import (  # noqa: F401
     vc_linear_forward,
     vc_muon_step,
     vc_orthogonalize,
+)
+from .step import (  # noqa: F401
+    ClipPlan,
+    GRAD_NORMS,
+    NORMS,
+    block_norm_backward_workspace,
+    embedding_backward_workspace,
+    prepare_block_norm_backward,
+    prepare_block_norm_forward,
+    prepare_embedding_backward,
+    prepare_embedding_forward,
+    vc_block_norm_backward,
+    vc_block_norm_forward,
+    vc_embedding_backward,
+    vc_embedding_forward,
 )

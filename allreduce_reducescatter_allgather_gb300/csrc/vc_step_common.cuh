@@ -1,0 +1,88 @@
+// What the entry points of vc_step.h share: rows of matrices eight values at a
+// time, sums over warps, and launches.
+#pragma once
+
+#include "vc_step.h"
+#include "vc_train_common.cuh"
+
+namespace vc {
+namespace step {
+
+using train::elem_size;
+using train::overlap;
+using train::round256;
+using train::same_matrix;
+using train::Span;
+using train::span_of;
+using train::test_launch_failure;
+using train::valid_matrix;
+
+constexpr int kSMs = 152;
+
+inline bool plain_matrix(const vc_matrix_t* m, long long rows, long long cols) {
+    return valid_matrix(m) && m->batch == 1 && m->rows == rows && m->cols == cols;
+}
+inline bool workspace_ok(const void* ws, size_t have, size_t need) {
+    return need == 0 || (ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && have >= need);
+}
+inline bool valid_dtype(vc_dtype_t d) { return d == VC_FLOAT32 || d == VC_BFLOAT16; }
+
+// A matrix as kernels take it.  vec: groups of eight columns start on 16 bytes in
+// every row.
+struct Rows {
+    void* data;
+    long long ld;
+    int f32, vec;
+};
+inline Rows rows_of(const vc_matrix_t* m) {
+    Rows r = {};
+    if (m == nullptr) return r;
+    r.data = m->data;
+    r.ld = m->rows > 1 ? m->ld : 0;
+    r.f32 = m->dtype == VC_FLOAT32;
+    r.vec = reinterpret_cast<uintptr_t>(m->data) % 16 == 0 && r.ld % (r.f32 ? 4 : 8) == 0;
+    return r;
+}
+
+struct Eight {
+    float v[8];
+};
+
+__device__ __forceinline__ Eight widen(uint4 u) {
+    Eight r;
+    const unsigned w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        r.v[2 * j] = __uint_as_float(w[j] << 16);
+        r.v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+    return r;
+}
+__device__ __forceinline__ unsigned narrow2(float a, float b) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const unsigned*>(&p);
+}
+__device__ __forceinline__ uint4 narrow(const Eight& r) {
+    return make_uint4(narrow2(r.v[0], r.v[1]), narrow2(r.v[2], r.v[3]), narrow2(r.v[4], r.v[5]),
+                      narrow2(r.v[6], r.v[7]));
+}
+
+// Sums of a whole warp, the same in every lane.
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_next() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace step
+}  // namespace vc

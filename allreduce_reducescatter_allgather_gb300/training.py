@@ -228,6 +228,9 @@ class PreparedOperator:
             self._made.record_stream(stream)
 
     def __call__(self, stream=None):
+        self._launch(self._fn, self._args, stream)
+
+    def _launch(self, fn, args, stream):
         torch = _torch()
         # (short calls are bound by the host: the common case makes no objects)
         if stream is None:
@@ -237,10 +240,10 @@ class PreparedOperator:
         if self._made is not None and raw != self._stream:
             self._move(stream, raw)
         if torch.cuda.current_device() == self._index:
-            status = self._fn(*self._args, raw)
+            status = fn(*args, raw)
         else:
             with _OnDevice(self._device):
-                status = self._fn(*self._args, raw)
+                status = fn(*args, raw)
         if status != 0:
             check_status(status)
 
