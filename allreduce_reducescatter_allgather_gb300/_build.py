@@ -22,7 +22,7 @@ LIB = LIBDIR / "libvc.so"
 
 SOURCES = ["vc_api.cu", "vc_reduce_dispatch.cu", "vc_noalloc.cu", "vc_copy.cu", "vc_bucket.cu",
            "vc_gemm.cu", "vc_train_linear.cu", "vc_train_muon.cu", "vc_step_embed.cu",
-           "vc_step_norm.cu", "vc_step_clip.cu"]
+           "vc_step_norm.cu", "vc_step_norm_grad.cu", "vc_step_clip.cu"]
 # vc_reduce_inst.cu compiled once per (element type, op, order group):
 # (object, -D flags).  Groups: 0 ring + recursive halving, 1 tree, 2 double
 # binary tree.  The integer types have group 0 only (ring): their results

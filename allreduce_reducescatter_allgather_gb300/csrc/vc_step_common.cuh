@@ -84,5 +84,28 @@ __device__ __forceinline__ void pdl_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// launch_pdl with dynamic shared memory.
+template <class... KArgs, class... Args>
+cudaError_t launch_pdl_shared(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t bytes, cudaStream_t st,
+                              Args&&... args) {
+    if (bytes > 48u << 10) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 }  // namespace step
 }  // namespace vc

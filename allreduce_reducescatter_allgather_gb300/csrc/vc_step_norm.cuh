@@ -1,0 +1,353 @@
+// vc_block_norm_forward / vc_block_norm_backward: the norm behind a block, its
+// gate, the residual and the norm before the next block in one pass over the rows.
+// Here: what both directions share.
+//
+//   u = post(h),  r = a x + act(gate) u,  n = pre(r)
+//
+// Every matrix is read or written once; the bound is their bytes.  A team of
+// threads (a warp for short rows, a whole block for long ones) holds a row in
+// registers, eight columns a thread and vector, between the sums that the norms
+// need.  Rows that are longer than a team can hold are read again for every sum
+// (from the caches), by kernels of their own.
+//
+// The gradient's column sums (weights, biases, a gate that rows share) stay in
+// registers over the rows of a team, which are neighbours, and go to the
+// workspace once; a second kernel adds those parts in order.  The statistics are
+// computed again from r and h, which the gradient reads anyway.
+#pragma once
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "vc_step_common.cuh"
+
+namespace vc {
+namespace step {
+
+enum { kGateNone = 0, kGateShared = 1, kGateFull = 2, kGateGroups = 3 };
+
+struct Affine {
+    Rows weight, bias;
+};
+
+struct NormParams {
+    // forward: h, x, gate -> r, n; backward: dr, dn, r, h, gate -> dx, dh, dgate
+    Rows h, x, gate, r, n, dr, dn, dx, dh, dgate;
+    Affine post, pre;
+    long long rows, group;  // rows that share a gate row
+    int cols, vec;
+    int gate_mode, sigmoid, accumulate;
+    float scale, eps, inv_cols;
+    // backward: parts[block][kind][padded], slots[team][2][padded]
+    float *parts, *slots;
+    long long padded;
+    int kinds;  // bits of enum kSum
+    int teams, blocks;
+    Affine dpost, dpre;
+};
+enum { kSumPre = 0, kSumPreBias = 1, kSumPost = 2, kSumPostBias = 3, kSumGate = 4, kSums = 5 };
+
+// ------------------------------------------------------------------- columns --
+
+// The columns of thread `lane` of a team in its v-th vector: eight neighbours on
+// 16 bytes, or every kTeam-th one.
+template <int kTeam>
+__device__ __forceinline__ int column(bool vec, int v, int lane, int j) {
+    return vec ? (v * kTeam + lane) * 8 + j : (v * 8 + j) * kTeam + lane;
+}
+
+template <int kTeam>
+__device__ __forceinline__ Eight load_f32(const void* data, long long at, bool vec, int v, int lane, int cols) {
+    const float* p = static_cast<const float*>(data) + at;
+    const int c = (v * kTeam + lane) * 8;
+    if (vec && c + 8 <= cols) {
+        const float4 lo = *reinterpret_cast<const float4*>(p + c), hi = *reinterpret_cast<const float4*>(p + c + 4);
+        return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+    }
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = column<kTeam>(vec, v, lane, j);
+        r.v[j] = k < cols ? p[k] : 0.0f;
+    }
+    return r;
+}
+template <int kTeam>
+__device__ __forceinline__ Eight load_bf16(const void* data, long long at, bool vec, int v, int lane, int cols) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(data) + at;
+    const int c = (v * kTeam + lane) * 8;
+    if (vec && c + 8 <= cols) return widen(*reinterpret_cast<const uint4*>(p + c));
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = column<kTeam>(vec, v, lane, j);
+        r.v[j] = k < cols ? __bfloat162float(p[k]) : 0.0f;
+    }
+    return r;
+}
+template <int kTeam>
+__device__ __forceinline__ Eight load_any(const Rows& x, long long row, bool vec, int v, int lane, int cols) {
+    return x.f32 ? load_f32<kTeam>(x.data, row * x.ld, vec, v, lane, cols)
+                 : load_bf16<kTeam>(x.data, row * x.ld, vec, v, lane, cols);
+}
+template <int kTeam>
+__device__ __forceinline__ Eight load_as(const Rows& x, bool f32, long long row, bool vec, int v, int lane, int cols) {
+    return f32 ? load_f32<kTeam>(x.data, row * x.ld, vec, v, lane, cols)
+               : load_bf16<kTeam>(x.data, row * x.ld, vec, v, lane, cols);
+}
+template <int kTeam>
+__device__ __forceinline__ void store_any(const Rows& x, bool f32, long long row, bool vec, int v, int lane,
+                                          int cols, const Eight& r) {
+    float* f = static_cast<float*>(x.data) + row * x.ld;
+    __nv_bfloat16* b = static_cast<__nv_bfloat16*>(x.data) + row * x.ld;
+    const int c = (v * kTeam + lane) * 8;
+    if (vec && c + 8 <= cols) {
+        if (f32) {
+            *reinterpret_cast<float4*>(f + c) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+            *reinterpret_cast<float4*>(f + c + 4) = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(b + c) = narrow(r);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = column<kTeam>(vec, v, lane, j);
+        if (k >= cols) continue;
+        if (f32)
+            f[k] = r.v[j];
+        else
+            b[k] = __float2bfloat16(r.v[j]);
+    }
+}
+
+// Eight columns of a row as they lie in memory, so that a thread can hold the next
+// row's while it computes with this one's: eight 32-bit words of float32, or of
+// bfloat16 four words of two (on 16 bytes) or eight of one.  Streams are read once:
+// they leave the first-level cache to the weights.
+struct Raw {
+    unsigned w[8];
+};
+template <int kTeam>
+__device__ __forceinline__ Raw load_raw(const Rows& x, bool f32, long long row, bool vec, int v, int lane, int cols) {
+    const long long at = row * x.ld;
+    const int c = (v * kTeam + lane) * 8;
+    Raw r;
+    if (vec && c + 8 <= cols) {
+        if (f32) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x.data) + at + c);
+            const uint4 lo = __ldcs(p), hi = __ldcs(p + 1);
+            r = {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+        } else {
+            const uint4 u = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.data) + at + c));
+            r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+        }
+        return r;
+    }
+    if (!f32 && vec)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.w[j] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = column<kTeam>(vec, v, lane, j);
+        if (f32) {
+            r.w[j] = k < cols ? __ldcs(static_cast<const unsigned*>(x.data) + at + k) : 0;
+        } else {
+            const unsigned u = k < cols ? __ldcs(static_cast<const unsigned short*>(x.data) + at + k) : 0;
+            if (vec)
+                r.w[j / 2] |= u << (j % 2 * 16);
+            else
+                r.w[j] = u;
+        }
+    }
+    return r;
+}
+__device__ __forceinline__ Eight widen_raw(const Raw& r, bool f32, bool vec) {
+    Eight e;
+    if (f32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e.v[j] = __uint_as_float(r.w[j]);
+    } else if (vec) {
+        e = widen(make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e.v[j] = __uint_as_float(r.w[j] << 16);
+    }
+    return e;
+}
+
+// ---------------------------------------------------------------------- sums --
+
+// Sums over a team; the team is a warp, or the whole block, whose calls then take
+// turns between two buffers, so that one barrier a call does.
+template <int kTeam>
+struct TeamSums {
+    static constexpr int kWarps = kTeam / 32;
+    float (*shared)[kWarps];  // [2 * 4][kWarps]
+    int turn;
+    template <int kN>
+    __device__ __forceinline__ void operator()(float (&v)[kN]) {
+        static_assert(kN <= 4, "a buffer has four rows");
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = warp_sum(v[i]);
+        if constexpr (kTeam > 32) {
+            float(*buf)[kWarps] = shared + turn * 4;
+            turn ^= 1;
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int i = 0; i < kN; ++i) buf[i][threadIdx.x >> 5] = v[i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                float s = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) s += buf[i][w];
+                v[i] = s;
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float gate_value(float g, bool sigmoid) {
+    return sigmoid ? train::logistic(g) : g;
+}
+__device__ __forceinline__ float gate_slope(float g, bool sigmoid) {
+    if (!sigmoid) return 1.0f;
+    const float s = train::logistic(g);
+    return s * train::logistic(-g);  // (1 - s would lose what is left of it near 1)
+}
+__device__ __forceinline__ long long gate_row(const NormParams& p, long long row) {
+    return p.gate_mode == kGateFull ? row : p.gate_mode == kGateGroups ? row / p.group : 0;
+}
+
+// The mean and 1 / sqrt(variance + eps) of the row in v (RMS: 0 and that of the
+// mean square).
+template <int kTeam, int kVecs, bool kLayer>
+__device__ __forceinline__ void statistics(const NormParams& p, const Eight (&v)[kVecs], bool vec,
+                                           int lane, TeamSums<kTeam>& sums, float& mean, float& rstd) {
+    mean = 0.0f;
+    if constexpr (kLayer) {
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[0] += v[i].v[j];
+        sums(s);
+        mean = s[0] * p.inv_cols;
+    }
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float d = v[i].v[j] - mean;
+            if (!kLayer || column<kTeam>(vec, i, lane, j) < p.cols) s[0] = fmaf(d, d, s[0]);
+        }
+    sums(s);
+    rstd = rsqrtf(fmaf(s[0], p.inv_cols, p.eps));
+}
+
+// Rows that are too long for registers: a block a row, in steps of 8 * kLong
+// columns, the inputs read again for every sum.
+constexpr int kLong = 512;
+
+template <bool kLayer, class F>
+__device__ __forceinline__ void long_statistics(const NormParams& p, TeamSums<kLong>& sums, int steps, int lane,
+                                                F load, float& mean, float& rstd) {
+    mean = 0.0f;
+    if constexpr (kLayer) {
+        float s[1] = {0.0f};
+        for (int i = 0; i < steps; ++i) {
+            const Eight v = load(i);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[0] += v.v[j];
+        }
+        sums(s);
+        mean = s[0] * p.inv_cols;
+    }
+    float s[1] = {0.0f};
+    for (int i = 0; i < steps; ++i) {
+        const Eight v = load(i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float d = v.v[j] - mean;
+            if (!kLayer || column<kLong>(p.vec, i, lane, j) < p.cols) s[0] = fmaf(d, d, s[0]);
+        }
+    }
+    sums(s);
+    rstd = rsqrtf(fmaf(s[0], p.inv_cols, p.eps));
+}
+
+__device__ __forceinline__ Eight normalised(const NormParams& p, const Affine& a, Eight v, float mean, float rstd,
+                                            int i, int lane) {
+    const Eight w = load_any<kLong>(a.weight, 0, p.vec, i, lane, p.cols);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v.v[j] = (v.v[j] - mean) * rstd * w.v[j];
+    if (a.bias.data != nullptr) {
+        const Eight b = load_any<kLong>(a.bias, 0, p.vec, i, lane, p.cols);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.v[j] += b.v[j];
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------- arguments --
+
+// A row of `cols` columns by `team` threads with `vecs` vectors each; team 0: the
+// kernels for long rows.
+struct Shape {
+    int team, vecs;
+};
+
+inline bool valid_affine(const vc_affine_t* a, bool needed) {
+    if (a == nullptr || a->weight == nullptr) return !needed && (a == nullptr || a->bias == nullptr);
+    const int es = elem_size(a->dtype);
+    return es != 0 && reinterpret_cast<uintptr_t>(a->weight) % es == 0 &&
+           reinterpret_cast<uintptr_t>(a->bias) % es == 0;
+}
+inline Rows vector_of(void* data, vc_dtype_t dtype) {
+    return {data, 0, dtype == VC_FLOAT32, reinterpret_cast<uintptr_t>(data) % 16 == 0};
+}
+inline Affine affine_of(const vc_affine_t* a) {
+    if (a == nullptr || (a->weight == nullptr && a->bias == nullptr)) return {};
+    return {vector_of(a->weight, a->dtype), vector_of(a->bias, a->dtype)};
+}
+inline bool valid_args(const vc_block_norm_t* a) {
+    return a != nullptr && (a->norm == VC_NORM_RMS || a->norm == VC_NORM_LAYER) &&
+           (a->gate_act == VC_GATE_NONE || a->gate_act == VC_GATE_SIGMOID) && a->eps >= 0.0f;
+}
+// [G, D] with G a divisor of the rows (any where there are none).
+inline bool valid_gate(const vc_matrix_t* g, long long rows, long long cols) {
+    return valid_matrix(g) && g->batch == 1 && g->cols == cols && g->rows > 0 && rows % g->rows == 0;
+}
+inline bool is_bf16(const vc_matrix_t* m) { return m->dtype == VC_BFLOAT16; }
+inline int mode_of(const vc_matrix_t* g, long long rows) {
+    return g == nullptr ? kGateNone : g->rows == 1 ? kGateShared : g->rows == rows ? kGateFull : kGateGroups;
+}
+inline Span span_of_vector(const void* p, vc_dtype_t dtype, long long cols) {
+    return span_of(p, (size_t)cols * elem_size(dtype));
+}
+
+inline void common_params(NormParams* p, const vc_matrix_t* gate, const vc_affine_t* post, const vc_affine_t* pre,
+                   const vc_block_norm_t* args, long long rows, long long cols) {
+    p->gate = rows_of(gate);
+    p->post = affine_of(post);
+    p->pre = affine_of(pre);
+    p->rows = rows;
+    p->cols = (int)cols;
+    p->gate_mode = mode_of(gate, rows);
+    p->group = gate == nullptr ? 1 : rows / gate->rows;
+    p->sigmoid = args->gate_act == VC_GATE_SIGMOID;
+    p->scale = args->residual_scale;
+    p->eps = args->eps;
+    p->inv_cols = (float)(1.0 / (double)cols);
+}
+// Whether all that is there lies on 16 bytes.
+inline bool all_vec(std::initializer_list<const Rows*> xs) {
+    bool vec = true;
+    for (const Rows* x : xs) vec = vec && (x->data == nullptr || x->vec);
+    return vec;
+}
+
+}  // namespace step
+}  // namespace vc

@@ -1,0 +1,694 @@
+// vc_block_norm_backward: from dr and dn to dx, dh, dgate and the column sums.
+#include "vc_step_norm.cuh"
+
+namespace vc {
+namespace step {
+namespace {
+
+// The rows of team t: a run of neighbours.
+__device__ __forceinline__ long long first_row(const NormParams& p, long long t) { return t * p.rows / p.teams; }
+
+// A team's sum of dr u over the rows of group g that it has: the whole of it goes to
+// dgate, a part to one of the team's two slots: 0 where the group started before
+// its rows, 1 where it goes on behind them.
+template <int kTeam>
+__device__ __forceinline__ void flush_gate(const NormParams& p, long long team, long long g, long long lo,
+                                           long long hi, bool vec, int v, int lane, Eight sum) {
+    const bool before = g * p.group < lo, behind = (g + 1) * p.group > hi;
+    if (before || behind) {
+        const Rows slot = {p.slots, p.padded, 1, 1};
+        store_any<kTeam>(slot, true, team * 2 + (before ? 0 : 1), vec, v, lane, p.cols, sum);
+        return;
+    }
+    const Eight gate = load_any<kTeam>(p.gate, g, vec, v, lane, p.cols);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum.v[j] *= gate_slope(gate.v[j], p.sigmoid);
+    if (p.accumulate) {
+        const Eight old = load_any<kTeam>(p.dgate, g, vec, v, lane, p.cols);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum.v[j] += old.v[j];
+    }
+    store_any<kTeam>(p.dgate, p.dgate.f32, g, vec, v, lane, p.cols, sum);
+}
+
+// A gate of its own for every element.
+template <int kTeam>
+__device__ __forceinline__ void store_gate(const NormParams& p, long long row, bool vec, int v, int lane, Eight d,
+                                           const Eight& gate) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d.v[j] *= gate_slope(gate.v[j], p.sigmoid);
+    if (p.accumulate) {
+        const Eight old = load_any<kTeam>(p.dgate, row, vec, v, lane, p.cols);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d.v[j] += old.v[j];
+    }
+    store_any<kTeam>(p.dgate, p.dgate.f32, row, vec, v, lane, p.cols, d);
+}
+
+constexpr int kBackwardThreads = 256;  // of a block of teams that are warps
+
+// One row after the other: the next row's loads are issued where this row's inputs
+// have been used up, before its last sum.  Blocks whose threads hold two vectors of a
+// row have no registers left for the column sums: those lie in shared memory, where
+// each thread adds to its own.
+template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
+__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam) backward_kernel(const __grid_constant__ NormParams p) {
+    constexpr int kThreads = kTeam == 32 ? kBackwardThreads : kTeam, kTeams = kThreads / kTeam;
+    // RMS norms have no biases
+    constexpr int kKept = kLayer ? 5 : 3;
+    constexpr int kPre = 0, kPost = 1, kGate = 2, kPreBias = 3, kPostBias = 4;
+    constexpr bool kInShared = kTeam > 32 && kVecs == 2;
+    __shared__ float shared[kTeam > 32 ? 8 : 1][kTeam / 32];
+    __shared__ float joined[kTeams > 1 ? kTeams : 1][kTeams > 1 ? 8 * kTeam * kVecs : 1];
+    extern __shared__ float4 columns[];  // [sum][vector][half][thread]
+    TeamSums<kTeam> sums = {shared, 0};
+    const int lane = threadIdx.x % kTeam;
+    const long long team = (long long)blockIdx.x * kTeams + threadIdx.x / kTeam;
+    const bool has_pre = p.dn.data != nullptr, has_post = p.post.weight.data != nullptr;
+    const bool has_h = p.h.data != nullptr;
+    const bool sums_gate = p.dgate.data != nullptr && (p.gate_mode == kGateShared || p.gate_mode == kGateGroups);
+    Eight kept[kInShared ? 1 : kKept][kInShared ? 1 : kVecs];
+    auto clear = [&](int k, int i) {
+        if constexpr (kInShared) {
+            float4* at = columns + (k * kVecs + i) * 2 * kTeam + lane;
+            at[0] = at[kTeam] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) kept[k][i].v[j] = 0.0f;
+        }
+    };
+    auto sum_of = [&](int k, int i) {
+        if constexpr (kInShared) {
+            const float4* at = columns + (k * kVecs + i) * 2 * kTeam + lane;
+            const float4 lo = at[0], hi = at[kTeam];
+            return Eight{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+        } else {
+            return kept[k][i];
+        }
+    };
+    auto add = [&](int k, int i, const Eight& d) {
+        if constexpr (kInShared) {
+            float4* at = columns + (k * kVecs + i) * 2 * kTeam + lane;
+            float4 lo = at[0], hi = at[kTeam];
+            lo.x += d.v[0], lo.y += d.v[1], lo.z += d.v[2], lo.w += d.v[3];
+            hi.x += d.v[4], hi.y += d.v[5], hi.z += d.v[6], hi.w += d.v[7];
+            at[0] = lo, at[kTeam] = hi;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) kept[k][i].v[j] += d.v[j];
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) clear(k, i);
+
+    Raw raw_dr[kVecs], raw_dn[kVecs], raw_r[kVecs], raw_h[kVecs], raw_gate[kVecs];
+    auto load = [&](long long row) {
+        if (has_pre)
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                raw_r[i] = load_raw<kTeam>(p.r, kStream32, row, kVec, i, lane, p.cols);
+                raw_dn[i] = load_raw<kTeam>(p.dn, false, row, kVec, i, lane, p.cols);
+            }
+        if (has_h)
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) raw_h[i] = load_raw<kTeam>(p.h, false, row, kVec, i, lane, p.cols);
+        if (p.dr.data != nullptr)
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) raw_dr[i] = load_raw<kTeam>(p.dr, kStream32, row, kVec, i, lane, p.cols);
+        if (p.gate_mode != kGateNone) {
+            const long long g = gate_row(p, row);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                raw_gate[i] = load_raw<kTeam>(p.gate, p.gate.f32, g, kVec, i, lane, p.cols);
+        }
+    };
+    pdl_next();
+    pdl_wait();
+    const long long lo = first_row(p, team), hi = first_row(p, team + 1);
+    long long group_end = p.gate_mode == kGateGroups ? (lo / p.group + 1) * p.group : 0;
+    if (lo < hi) load(lo);
+    for (long long row = lo; row < hi; ++row) {
+        // the statistics: with the means taken off first, in one sum for both norms
+        float mean = 0.0f, h_mean = 0.0f;
+        if constexpr (kLayer) {
+            float s[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const Eight r = widen_raw(raw_r[i], kStream32, kVec), h = widen_raw(raw_h[i], false, kVec);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (has_pre) s[0] += r.v[j];
+                    if (has_post) s[1] += h.v[j];
+                }
+            }
+            sums(s);
+            mean = s[0] * p.inv_cols;
+            h_mean = s[1] * p.inv_cols;
+        }
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            bool in[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) in[j] = !kLayer || column<kTeam>(kVec, i, lane, j) < p.cols;
+            if (has_pre) {
+                const Eight r = widen_raw(raw_r[i], kStream32, kVec), dn = widen_raw(raw_dn[i], false, kVec);
+                const Eight w = load_any<kTeam>(p.pre.weight, 0, kVec, i, lane, p.cols);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float c = in[j] ? r.v[j] - mean : 0.0f, d = w.v[j] * dn.v[j];
+                    s[0] = fmaf(c, c, s[0]);
+                    s[1] = fmaf(d, c, s[1]);
+                    if constexpr (kLayer) s[2] += d;
+                }
+            }
+            if (has_post) {
+                const Eight h = widen_raw(raw_h[i], false, kVec);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float c = in[j] ? h.v[j] - h_mean : 0.0f;
+                    s[3] = fmaf(c, c, s[3]);
+                }
+            }
+        }
+        if (has_pre || has_post) sums(s);
+        const float rstd = rsqrtf(fmaf(s[0], p.inv_cols, p.eps)), h_rstd = rsqrtf(fmaf(s[3], p.inv_cols, p.eps));
+        const float m2 = s[1] * p.inv_cols * rstd, m1 = s[2] * p.inv_cols;
+        Eight du[kVecs], hat[kVecs];
+        float t[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            Eight dr;
+            if (p.dr.data != nullptr) {
+                dr = widen_raw(raw_dr[i], kStream32, kVec);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dr.v[j] = 0.0f;
+            }
+            if (has_pre) {
+                const Eight r = widen_raw(raw_r[i], kStream32, kVec), dn = widen_raw(raw_dn[i], false, kVec);
+                const Eight w = load_any<kTeam>(p.pre.weight, 0, kVec, i, lane, p.cols);
+                Eight part;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float c = (r.v[j] - mean) * rstd;
+                    part.v[j] = dn.v[j] * c;
+                    dr.v[j] = fmaf(rstd, fmaf(w.v[j], dn.v[j], -m1) - c * m2, dr.v[j]);
+                }
+                add(kPre, i, part);
+                if constexpr (kLayer) add(kPreBias, i, dn);
+            }
+            if (p.dx.data != nullptr) {
+                Eight d;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d.v[j] = p.scale * dr.v[j];
+                store_any<kTeam>(p.dx, kStream32, row, kVec, i, lane, p.cols, d);
+            }
+            if (has_h) hat[i] = widen_raw(raw_h[i], false, kVec);
+            Eight w;
+            if (has_post) {
+                w = load_any<kTeam>(p.post.weight, 0, kVec, i, lane, p.cols);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) hat[i].v[j] = (hat[i].v[j] - h_mean) * h_rstd;
+            }
+            du[i] = dr;
+            if (p.gate_mode != kGateNone) {
+                const Eight gate = widen_raw(raw_gate[i], p.gate.f32, kVec);
+                if (p.dgate.data != nullptr) {
+                    Eight d = hat[i];
+                    if (has_post) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) d.v[j] *= w.v[j];
+                        if (kLayer && p.post.bias.data != nullptr) {
+                            const Eight b = load_any<kTeam>(p.post.bias, 0, kVec, i, lane, p.cols);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) d.v[j] += b.v[j];
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d.v[j] *= dr.v[j];
+                    if (sums_gate)
+                        add(kGate, i, d);
+                    else
+                        store_gate<kTeam>(p, row, kVec, i, lane, d, gate);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) du[i].v[j] *= gate_value(gate.v[j], p.sigmoid);
+            }
+            if (has_post) {
+                Eight part;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) part.v[j] = du[i].v[j] * hat[i].v[j];
+                add(kPost, i, part);
+                if constexpr (kLayer) add(kPostBias, i, du[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    t[0] = fmaf(part.v[j], w.v[j], t[0]);
+                    du[i].v[j] *= w.v[j];
+                    if constexpr (kLayer) t[1] += du[i].v[j];
+                }
+            }
+        }
+        // this row's inputs are used up
+        if (row + 1 < hi) load(row + 1);
+        if (p.gate_mode == kGateGroups && (row + 1 == group_end || row + 1 == hi)) {
+            if (sums_gate)
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    flush_gate<kTeam>(p, team, row / p.group, lo, hi, kVec, i, lane, sum_of(kGate, i));
+                    clear(kGate, i);
+                }
+            group_end += p.group;
+        }
+        if (p.dh.data == nullptr) continue;
+        if (has_post) {
+            sums(t);
+            const float h_m2 = t[0] * p.inv_cols, h_m1 = t[1] * p.inv_cols;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) du[i].v[j] = h_rstd * (du[i].v[j] - h_m1 - hat[i].v[j] * h_m2);
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.dh, false, row, kVec, i, lane, p.cols, du[i]);
+    }
+    // the column sums
+    const Rows parts = {p.parts, p.padded, 1, 1};
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int kind = k == kPre ? kSumPre : k == kPost ? kSumPost : k == kGate ? kSumGate
+                         : k == kPreBias ? kSumPreBias : kSumPostBias;
+        if (!(p.kinds >> kind & 1)) continue;
+        const long long at = (long long)blockIdx.x * kSums + kind;
+        if constexpr (kTeams == 1) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                store_any<kTeam>(parts, true, at, kVec, i, lane, p.cols, sum_of(k, i));
+        } else {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const Eight sum = sum_of(k, i);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    joined[threadIdx.x / kTeam][column<kTeam>(kVec, i, lane, j)] = sum.v[j];
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.cols; c += kThreads) {
+                float s = 0.0f;
+#pragma unroll
+                for (int t = 0; t < kTeams; ++t) s += joined[t][c];
+                p.parts[at * p.padded + c] = s;
+            }
+        }
+    }
+}
+
+// The same for rows too long for registers: the column sums lie in the block's
+// parts, where each thread adds to its own columns.
+template <bool kLayer, bool kStream32>
+__global__ void __launch_bounds__(kLong) backward_long_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float shared[8][kLong / 32];
+    TeamSums<kLong> sums = {shared, 0};
+    const int lane = threadIdx.x, steps = (p.cols + 8 * kLong - 1) / (8 * kLong);
+    const bool has_pre = p.dn.data != nullptr, has_post = p.post.weight.data != nullptr;
+    const bool sums_gate = p.dgate.data != nullptr && (p.gate_mode == kGateShared || p.gate_mode == kGateGroups);
+    const long long team = blockIdx.x;
+    pdl_next();
+    pdl_wait();
+    const long long lo = first_row(p, team), hi = first_row(p, team + 1);
+    const Rows parts = {p.parts, p.padded, 1, 1};
+    auto add = [&](int kind, bool fresh, int i, const Eight& d) {
+        const long long at = team * kSums + kind;
+        Eight s = d;
+        if (!fresh) {
+            const Eight old = load_f32<kLong>(parts.data, at * parts.ld, p.vec, i, lane, p.cols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s.v[j] += old.v[j];
+        }
+        store_any<kLong>(parts, true, at, p.vec, i, lane, p.cols, s);
+    };
+    for (long long row = lo; row < hi; ++row) {
+        auto load_h = [&](int i) { return load_bf16<kLong>(p.h.data, row * p.h.ld, p.vec, i, lane, p.cols); };
+        auto load_r = [&](int i) { return load_as<kLong>(p.r, kStream32, row, p.vec, i, lane, p.cols); };
+        auto load_dn = [&](int i) { return load_bf16<kLong>(p.dn.data, row * p.dn.ld, p.vec, i, lane, p.cols); };
+        float mean = 0.0f, rstd = 0.0f, m1 = 0.0f, m2 = 0.0f;
+        if (has_pre) {
+            long_statistics<kLayer>(p, sums, steps, lane, load_r, mean, rstd);
+            float s[2] = {0.0f, 0.0f};
+            for (int i = 0; i < steps; ++i) {
+                const Eight r = load_r(i), dn = load_dn(i), w = load_any<kLong>(p.pre.weight, 0, p.vec, i, lane, p.cols);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float d = w.v[j] * dn.v[j];
+                    s[0] = fmaf(d, (r.v[j] - mean) * rstd, s[0]);
+                    if constexpr (kLayer) s[1] += d;
+                }
+            }
+            sums(s);
+            m2 = s[0] * p.inv_cols;
+            m1 = s[1] * p.inv_cols;
+        }
+        auto load_dr = [&](int i) {
+            Eight dr = {{0, 0, 0, 0, 0, 0, 0, 0}};
+            if (p.dr.data != nullptr) dr = load_as<kLong>(p.dr, kStream32, row, p.vec, i, lane, p.cols);
+            if (has_pre) {
+                const Eight r = load_r(i), dn = load_dn(i), w = load_any<kLong>(p.pre.weight, 0, p.vec, i, lane, p.cols);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    dr.v[j] = fmaf(rstd, w.v[j] * dn.v[j] - m1 - (r.v[j] - mean) * rstd * m2, dr.v[j]);
+            }
+            return dr;
+        };
+        const long long g = gate_row(p, row);
+        auto load_gate = [&](int i) { return load_any<kLong>(p.gate, g, p.vec, i, lane, p.cols); };
+        float h_mean = 0.0f, h_rstd = 0.0f, h_m1 = 0.0f, h_m2 = 0.0f;
+        if (has_post) {
+            long_statistics<kLayer>(p, sums, steps, lane, load_h, h_mean, h_rstd);
+            float s[2] = {0.0f, 0.0f};
+            for (int i = 0; i < steps; ++i) {
+                Eight d = load_dr(i);
+                const Eight h = load_h(i), w = load_any<kLong>(p.post.weight, 0, p.vec, i, lane, p.cols);
+                if (p.gate_mode != kGateNone) {
+                    const Eight v = load_gate(i);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d.v[j] *= gate_value(v.v[j], p.sigmoid);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    d.v[j] *= w.v[j];
+                    s[0] = fmaf(d.v[j], (h.v[j] - h_mean) * h_rstd, s[0]);
+                    if constexpr (kLayer) s[1] += d.v[j];
+                }
+            }
+            sums(s);
+            h_m2 = s[0] * p.inv_cols;
+            h_m1 = s[1] * p.inv_cols;
+        }
+        const bool first = row == lo, group_first = first || (p.gate_mode == kGateGroups && row % p.group == 0);
+        const bool group_last = p.gate_mode == kGateGroups && ((row + 1) % p.group == 0 || row + 1 == hi);
+        // (dr and dn may be dx and dh: each column is read before it is written)
+        for (int i = 0; i < steps; ++i) {
+            Eight d = load_dr(i);
+            if (has_pre) {
+                const Eight r = load_r(i), dn = load_dn(i);
+                Eight t;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t.v[j] = dn.v[j] * (r.v[j] - mean) * rstd;
+                if (p.kinds >> kSumPre & 1) add(kSumPre, first, i, t);
+                if (p.kinds >> kSumPreBias & 1) add(kSumPreBias, first, i, dn);
+            }
+            if (p.dx.data != nullptr) {
+                Eight t;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t.v[j] = p.scale * d.v[j];
+                store_any<kLong>(p.dx, kStream32, row, p.vec, i, lane, p.cols, t);
+            }
+            Eight h;
+            if (p.h.data != nullptr) h = load_h(i);
+            if (p.gate_mode != kGateNone) {
+                const Eight v = load_gate(i);
+                if (p.dgate.data != nullptr) {
+                    Eight t = has_post ? normalised(p, p.post, h, h_mean, h_rstd, i, lane) : h;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) t.v[j] *= d.v[j];
+                    if (sums_gate) {
+                        add(kSumGate, group_first, i, t);
+                        if (group_last)
+                            flush_gate<kLong>(p, team, g, lo, hi, p.vec, i, lane,
+                                              load_f32<kLong>(parts.data, (team * kSums + kSumGate) * parts.ld,
+                                                              p.vec, i, lane, p.cols));
+                    } else {
+                        store_gate<kLong>(p, row, p.vec, i, lane, t, v);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d.v[j] *= gate_value(v.v[j], p.sigmoid);
+            }
+            if (has_post) {
+                const Eight w = load_any<kLong>(p.post.weight, 0, p.vec, i, lane, p.cols);
+                Eight t;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    h.v[j] = (h.v[j] - h_mean) * h_rstd;
+                    t.v[j] = d.v[j] * h.v[j];
+                }
+                if (p.kinds >> kSumPost & 1) add(kSumPost, first, i, t);
+                if (p.kinds >> kSumPostBias & 1) add(kSumPostBias, first, i, d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d.v[j] = h_rstd * (d.v[j] * w.v[j] - h_m1 - h.v[j] * h_m2);
+            }
+            if (p.dh.data != nullptr) store_any<kLong>(p.dh, false, row, p.vec, i, lane, p.cols, d);
+        }
+        __syncthreads();
+    }
+}
+
+// The parts of 32 columns, by 32 warps in turn: blocks y < kSums the column sums,
+// the others gate rows whose rows several teams have.
+constexpr int kJoinRows = 16;
+
+__global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float shared[32][33];
+    pdl_next();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long c = (long long)blockIdx.x * 32 + lane;
+    const bool live = c < p.cols;
+    // the sum over the warps, in warp 0
+    auto total = [&](float s) {
+        __syncthreads();
+        shared[warp][lane] = s;
+        __syncthreads();
+        float t = 0.0f;
+        if (warp == 0)
+            for (int w = 0; w < 32; ++w) t += shared[w][lane];
+        return t;
+    };
+    auto put = [&](const Rows& x, long long row, float s) {
+        if (warp != 0 || !live) return;
+        const long long at = row * x.ld + c;
+        if (x.f32) {
+            float* f = static_cast<float*>(x.data) + at;
+            *f = p.accumulate ? *f + s : s;
+        } else {
+            __nv_bfloat16* b = static_cast<__nv_bfloat16*>(x.data) + at;
+            *b = __float2bfloat16(p.accumulate ? __bfloat162float(*b) + s : s);
+        }
+    };
+    auto slope = [&](long long g) {
+        if (!live) return 0.0f;
+        const long long at = g * p.gate.ld + c;
+        return gate_slope(p.gate.f32 ? static_cast<const float*>(p.gate.data)[at]
+                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(p.gate.data)[at]),
+                          p.sigmoid);
+    };
+    const int kind = blockIdx.y;
+    if (kind < kSums) {
+        if (!(p.kinds >> kind & 1)) return;
+        float s = 0.0f;
+        if (live)
+#pragma unroll 4
+            for (int b = warp; b < p.blocks; b += 32) s += p.parts[((long long)b * kSums + kind) * p.padded + c];
+        s = total(s);
+        if (kind == kSumGate) s *= slope(0);
+        put(kind == kSumPre ? p.dpre.weight : kind == kSumPreBias ? p.dpre.bias
+            : kind == kSumPost ? p.dpost.weight : kind == kSumPostBias ? p.dpost.bias : p.dgate, 0, s);
+        return;
+    }
+    for (long long t = kind - kSums; t < p.teams; t += kJoinRows) {
+        // the group of the team's last row, where it starts there and goes on
+        const long long lo = first_row(p, t), hi = first_row(p, t + 1), g = (hi - 1) / p.group;
+        if (lo == hi || g * p.group < lo || (g + 1) * p.group <= hi) continue;
+        const long long last = ((g + 1) * p.group * p.teams - 1) / p.rows;  // the team of its last row
+        float s = 0.0f;
+        if (live)
+#pragma unroll 4
+            for (long long w = t + warp; w <= last; w += 32)
+                if (first_row(p, w) < first_row(p, w + 1))
+                    s += p.slots[(w * 2 + (w == t ? 1 : 0)) * p.padded + c];
+        s = total(s);
+        put(p.dgate, g, s * slope(g));
+    }
+}
+
+Shape backward_shape(int cols) {
+    if (cols <= 256) return {32, 1};
+    if (cols <= 512) return {32, 2};
+    if (cols <= 1024) return {128, 1};
+    if (cols <= 2048) return {256, 1};
+    if (cols <= 4096) return {512, 1};
+    if (cols <= 8192) return {512, 2};
+    return {0, 0};
+}
+
+// Blocks and teams of the gradient.
+struct Split {
+    Shape shape;
+    int blocks, teams, threads;
+    long long padded;
+};
+Split split_of(long long rows, long long cols) {
+    Split s = {};
+    s.shape = backward_shape((int)std::min(cols, 1ll << 20));
+    const int team = s.shape.team == 0 ? kLong : s.shape.team;
+    s.threads = team == 32 ? kBackwardThreads : team;
+    const int per = s.threads / team;
+    // four rows a team at least, so that the parts stay few beside the rows
+    const long long want = (rows + 4 * per - 1) / (4 * per);
+    s.blocks = (int)std::max(1ll, std::min(want, (long long)kSMs * std::max(1, 512 / s.threads)));
+    s.teams = s.blocks * per;
+    s.padded = (cols + 7) / 8 * 8;
+    return s;
+}
+
+template <bool kLayer, bool kStream32, bool kVec>
+cudaError_t launch_backward(const NormParams& p, const Split& s, cudaStream_t st) {
+    void (*kernel)(NormParams);
+    switch (s.shape.team * 4 + s.shape.vecs) {
+    case 32 * 4 + 1: kernel = backward_kernel<32, 1, kLayer, kStream32, kVec>; break;
+    case 32 * 4 + 2: kernel = backward_kernel<32, 2, kLayer, kStream32, kVec>; break;
+    case 128 * 4 + 1: kernel = backward_kernel<128, 1, kLayer, kStream32, kVec>; break;
+    case 256 * 4 + 1: kernel = backward_kernel<256, 1, kLayer, kStream32, kVec>; break;
+    case 512 * 4 + 1: kernel = backward_kernel<512, 1, kLayer, kStream32, kVec>; break;
+    case 512 * 4 + 2: kernel = backward_kernel<512, 2, kLayer, kStream32, kVec>; break;
+    default: kernel = backward_long_kernel<kLayer, kStream32>;
+    }
+    const bool shared = s.shape.team > 32 && s.shape.vecs == 2;
+    const size_t bytes = shared ? (size_t)(kLayer ? 5 : 3) * s.shape.team * s.shape.vecs * 32 : 0;
+    cudaError_t e = launch_pdl_shared(kernel, dim3(s.blocks), dim3(s.threads), bytes, st, p);
+    const bool groups = p.dgate.data != nullptr && p.gate_mode == kGateGroups;
+    if (e != cudaSuccess || (p.kinds == 0 && !groups)) return e;
+    const dim3 grid((unsigned)((p.cols + 31) / 32), kSums + (groups ? std::min(kJoinRows, s.teams) : 0));
+    return launch_pdl(finish_kernel, grid, dim3(1024), st, p);
+}
+template <bool kLayer, bool kStream32>
+cudaError_t launch_backward(const NormParams& p, const Split& s, cudaStream_t st) {
+    return p.vec ? launch_backward<kLayer, kStream32, true>(p, s, st)
+                 : launch_backward<kLayer, kStream32, false>(p, s, st);
+}
+
+}  // namespace
+}  // namespace step
+}  // namespace vc
+
+using namespace vc;
+using namespace vc::step;
+
+extern "C" {
+
+size_t vc_block_norm_backward_workspace(long long rows, long long cols, long long gates) {
+    if (rows <= 0 || rows > train::kMaxExtent || cols <= 0 || cols > train::kMaxExtent || gates < 0 ||
+        gates > rows)
+        return 0;
+    const Split s = split_of(rows, cols);
+    const size_t parts = (size_t)s.blocks * kSums * s.padded * 4;
+    const size_t slots = gates > 1 && gates < rows ? (size_t)s.teams * 2 * s.padded * 4 : 0;
+    return round256(parts) + round256(slots);
+}
+
+vc_status_t vc_block_norm_backward(const vc_block_norm_in_t* in, const vc_affine_t* post, const vc_affine_t* pre,
+                                   const vc_block_norm_t* args, const vc_block_norm_out_t* out, int accumulate,
+                                   void* workspace, size_t workspace_bytes, vc_stream_t stream) {
+    if (in == nullptr || out == nullptr || !valid_args(args)) return VC_ERR_INVALID_ARGUMENT;
+    const vc_matrix_t* shape = in->dr != nullptr ? in->dr : in->dn;
+    if (!valid_matrix(shape) || shape->batch != 1) return VC_ERR_INVALID_ARGUMENT;
+    const long long T = shape->rows, D = shape->cols;
+    const bool has_pre = in->dn != nullptr, has_post = post != nullptr && post->weight != nullptr;
+    const bool layer = args->norm == VC_NORM_LAYER;
+    auto bad = [&](const vc_matrix_t* m, bool bf16) {
+        return m != nullptr && (!plain_matrix(m, T, D) || (bf16 && !is_bf16(m)));
+    };
+    if (bad(in->dr, false) || bad(in->dn, true) || bad(in->r, false) || bad(in->h, true) || bad(out->dx, false) ||
+        bad(out->dh, true))
+        return VC_ERR_INVALID_ARGUMENT;
+    if (has_pre && in->r == nullptr) return VC_ERR_INVALID_ARGUMENT;
+    // one type for the residual stream
+    const vc_matrix_t* stream_like = in->dr != nullptr ? in->dr : in->r;
+    if ((has_pre && in->r->dtype != stream_like->dtype) ||
+        (out->dx != nullptr && out->dx->dtype != stream_like->dtype))
+        return VC_ERR_INVALID_ARGUMENT;
+    if (in->gate != nullptr && !valid_gate(in->gate, T, D)) return VC_ERR_INVALID_ARGUMENT;
+    if (out->dgate != nullptr && (in->gate == nullptr || !plain_matrix(out->dgate, in->gate->rows, D)))
+        return VC_ERR_INVALID_ARGUMENT;
+    if (!valid_affine(post, false) || !valid_affine(pre, has_pre)) return VC_ERR_INVALID_ARGUMENT;
+    auto bad_sum = [&](const vc_affine_t& s, bool there) {
+        if (s.weight == nullptr && s.bias == nullptr) return false;
+        const int es = elem_size(s.dtype);
+        return !there || es == 0 || reinterpret_cast<uintptr_t>(s.weight) % es != 0 ||
+               reinterpret_cast<uintptr_t>(s.bias) % es != 0 || (s.bias != nullptr && !layer);
+    };
+    if (bad_sum(out->dpre, has_pre) || bad_sum(out->dpost, has_post)) return VC_ERR_INVALID_ARGUMENT;
+    if ((post != nullptr && post->bias != nullptr && !layer) || (pre != nullptr && pre->bias != nullptr && !layer))
+        return VC_ERR_INVALID_ARGUMENT;
+    const bool post_work = has_post && (out->dh != nullptr || out->dgate != nullptr || out->dpost.weight != nullptr ||
+                                        out->dpost.bias != nullptr);
+    const bool needs_h = post_work || out->dgate != nullptr;
+    if (needs_h && in->h == nullptr) return VC_ERR_INVALID_ARGUMENT;
+    const long long gates = in->gate != nullptr ? in->gate->rows : 0;
+    const size_t need = T > 0 ? vc_block_norm_backward_workspace(T, D, gates) : 0;
+    if (!workspace_ok(workspace, workspace_bytes, need)) return VC_ERR_INVALID_ARGUMENT;
+    const vc_affine_t none = {};
+    const vc_affine_t &a = post != nullptr ? *post : none, &b = pre != nullptr ? *pre : none;
+    const Span outs[8] = {span_of(out->dx), span_of(out->dh), span_of(out->dgate),
+                          span_of_vector(out->dpost.weight, out->dpost.dtype, D),
+                          span_of_vector(out->dpost.bias, out->dpost.dtype, D),
+                          span_of_vector(out->dpre.weight, out->dpre.dtype, D),
+                          span_of_vector(out->dpre.bias, out->dpre.dtype, D), span_of(workspace, need)};
+    const Span ins[9] = {span_of(in->dr), span_of(in->dn), has_pre ? span_of(in->r) : Span{},
+                         needs_h ? span_of(in->h) : Span{}, span_of(in->gate),
+                         span_of_vector(a.weight, a.dtype, D), span_of_vector(a.bias, a.dtype, D),
+                         span_of_vector(b.weight, b.dtype, D), span_of_vector(b.bias, b.dtype, D)};
+    for (int o = 0; o < 8; ++o) {
+        for (int i = 0; i < 9; ++i)
+            if (overlap(outs[o], ins[i]) && !(o == 0 && i == 0 && same_matrix(out->dx, in->dr)) &&
+                !(o == 1 && i == 1 && same_matrix(out->dh, in->dn)))
+                return VC_ERR_ALIAS;
+        for (int q = 0; q < o; ++q)
+            if (overlap(outs[o], outs[q])) return VC_ERR_ALIAS;
+    }
+    if (D == 0) return VC_SUCCESS;
+    NormParams p = {};
+    p.dx = rows_of(out->dx);
+    p.dh = rows_of(out->dh);
+    p.dgate = rows_of(out->dgate);
+    p.dpost = affine_of(&out->dpost);
+    p.dpre = affine_of(&out->dpre);
+    p.kinds = (p.dpre.weight.data != nullptr) << kSumPre | (p.dpre.bias.data != nullptr) << kSumPreBias |
+              (p.dpost.weight.data != nullptr) << kSumPost | (p.dpost.bias.data != nullptr) << kSumPostBias |
+              (p.dgate.data != nullptr && mode_of(in->gate, T) == kGateShared) << kSumGate;
+    p.accumulate = accumulate != 0;
+    if (p.dx.data == nullptr && p.dh.data == nullptr && p.dgate.data == nullptr && p.kinds == 0) return VC_SUCCESS;
+    // (without rows, gate rows have none either, and the sums are zeros)
+    if (T == 0 && (p.kinds == 0 || accumulate)) return VC_SUCCESS;
+    if (test_launch_failure()) return VC_ERR_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    common_params(&p, in->gate, post, pre, args, T, D);
+    if (T == 0) {
+        const cudaError_t e = launch_pdl(finish_kernel, dim3((unsigned)((D + 31) / 32), kSums), dim3(1024), st, p);
+        return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
+    }
+    p.dr = rows_of(in->dr);
+    p.dn = rows_of(in->dn);
+    if (has_pre) p.r = rows_of(in->r);
+    if (needs_h) p.h = rows_of(in->h);
+    if (!post_work) p.post = {};
+    p.vec = all_vec({&p.h, &p.r, &p.gate, &p.dr, &p.dn, &p.dx, &p.dh, &p.dgate, &p.post.weight, &p.post.bias,
+                     &p.pre.weight});
+    const Split s = split_of(T, D);
+    p.blocks = s.blocks;
+    p.teams = s.teams;
+    p.padded = s.padded;
+    p.parts = static_cast<float*>(workspace);
+    p.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                       round256((size_t)s.blocks * kSums * s.padded * 4));
+    const bool f32 = stream_like->dtype == VC_FLOAT32;
+    const cudaError_t e = layer ? (f32 ? launch_backward<true, true>(p, s, st) : launch_backward<true, false>(p, s, st))
+                                : (f32 ? launch_backward<false, true>(p, s, st)
+                                       : launch_backward<false, false>(p, s, st));
+    return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
+}
+
+}  // extern "C"
