@@ -106,7 +106,7 @@ __device__ __forceinline__ double squares(const Held& h, bool f32) {
     for (int u = 0; u < kVecs; ++u) any |= h.v[u].x | h.v[u].y | h.v[u].z | h.v[u].w;
     if ((any & (f32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) return 0.0;
     double d = 0.0;
-    each_value(h, f32, [&](float x, int) { d = fma((double)x, (double)x, d); });
+    each_value(h, f32, [&](float x, int) { d = ::fma((double)x, (double)x, d); });
     return d;
 }
 

@@ -18,6 +18,7 @@ using train::test_launch_failure;
 using train::valid_matrix;
 
 constexpr int kSMs = 152;
+constexpr size_t kSharedLimit = 227u << 10;  // of a block; an SM has 1 KiB a block more
 
 inline bool plain_matrix(const vc_matrix_t* m, long long rows, long long cols) {
     return valid_matrix(m) && m->batch == 1 && m->rows == rows && m->cols == cols;
@@ -44,9 +45,69 @@ inline Rows rows_of(const vc_matrix_t* m) {
     return r;
 }
 
+// Eight values, computed two at a time.
 struct Eight {
     float v[8];
+    __device__ __forceinline__ float2 two(int j) const { return make_float2(v[2 * j], v[2 * j + 1]); }
+    __device__ __forceinline__ void set(int j, float2 x) { v[2 * j] = x.x, v[2 * j + 1] = x.y; }
 };
+__device__ __forceinline__ Eight zeros() { return {{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}}; }
+__device__ __forceinline__ Eight fma(const Eight& a, const Eight& b, const Eight& c) {
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.set(j, gemm::fma2(a.two(j), b.two(j), c.two(j)));
+    return r;
+}
+__device__ __forceinline__ Eight fma(float a, const Eight& b, const Eight& c) {
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.set(j, gemm::fma2(gemm::both(a), b.two(j), c.two(j)));
+    return r;
+}
+__device__ __forceinline__ Eight mul(const Eight& a, const Eight& b) {
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.set(j, gemm::mul2(a.two(j), b.two(j)));
+    return r;
+}
+__device__ __forceinline__ Eight mul(float a, const Eight& b) {
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.set(j, gemm::mul2(gemm::both(a), b.two(j)));
+    return r;
+}
+__device__ __forceinline__ Eight add(const Eight& a, const Eight& b) {
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.set(j, gemm::add2(a.two(j), b.two(j)));
+    return r;
+}
+__device__ __forceinline__ Eight add(float a, const Eight& b) {
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.set(j, gemm::add2(gemm::both(a), b.two(j)));
+    return r;
+}
+// s += a b, in two halves
+__device__ __forceinline__ void dot(float2& s, const Eight& a, const Eight& b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s = gemm::fma2(a.two(j), b.two(j), s);
+}
+__device__ __forceinline__ void total(float2& s, const Eight& a) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s = gemm::add2(s, a.two(j));
+}
+__device__ __forceinline__ float sum_of(float2 s) { return s.x + s.y; }
+
+// 16 bytes, of which the first `bytes` come from `from` and the others are zeros.
+__device__ __forceinline__ void copy16(uint4* to, const void* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the last kLeft groups of this thread's copies are there.
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
 __device__ __forceinline__ Eight widen(uint4 u) {
     Eight r;
@@ -88,7 +149,7 @@ __device__ __forceinline__ void pdl_next() {
 template <class... KArgs, class... Args>
 cudaError_t launch_pdl_shared(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t bytes, cudaStream_t st,
                               Args&&... args) {
-    if (bytes > 48u << 10) {
+    if (bytes > 24u << 10) {  // (with what the kernel has of its own, above 48 KiB)
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != cudaSuccess) return e;

@@ -6,37 +6,34 @@ namespace step {
 namespace {
 
 constexpr int kForwardThreads = 128;  // of a block of teams that are warps
+// Threads of an SM; half of them where rows come through registers.
+constexpr int kResident = 1024;
 
-// One row after the other: the next row's loads are issued where this row's inputs
-// have been used up, before its second sum.
+// One row after the other, the next one's inputs on their way meanwhile.
 template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
-__global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam) forward_kernel(const __grid_constant__ NormParams p) {
-    constexpr int kTeams = (kTeam == 32 ? kForwardThreads : kTeam) / kTeam;
+__global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam, (kVec ? kResident : kResident / 2) / (kTeam == 32 ? kForwardThreads : kTeam))
+    forward_kernel(const __grid_constant__ NormParams p) {
+    constexpr int kThreads = kTeam == 32 ? kForwardThreads : kTeam, kTeams = kThreads / kTeam;
+    constexpr int kH = 0, kX = 1, kGate = 2;
     __shared__ float shared[kTeam > 32 ? 8 : 1][kTeam / 32];
+    extern __shared__ uint4 ring[];
     TeamSums<kTeam> sums = {shared, 0};
     const int lane = threadIdx.x % kTeam;
-    Raw h[kVecs], x[kVecs], gate[kVecs];
+    const bool has_x = p.x.data != nullptr, full_gate = p.gate_mode == kGateFull;
+    Stream<kThreads, kTeam, kVecs, 3, kVec, kVec> in;
+    in.begin(ring);
+    in.array(kH, true, false);
+    in.array(kX, has_x, kStream32);
+    in.array(kGate, full_gate, p.gate.f32);
     auto load = [&](long long row) {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) h[i] = load_raw<kTeam>(p.h, false, row, kVec, i, lane, p.cols);
-        if (p.x.data != nullptr)
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) x[i] = load_raw<kTeam>(p.x, kStream32, row, kVec, i, lane, p.cols);
-        if (p.gate_mode != kGateNone) {
-            const long long g = gate_row(p, row);
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) gate[i] = load_raw<kTeam>(p.gate, p.gate.f32, g, kVec, i, lane, p.cols);
-        }
+        in.load(kH, p.h, row, lane, p.cols);
+        if (has_x) in.load(kX, p.x, row, lane, p.cols);
+        if (full_gate) in.load(kGate, p.gate, row, lane, p.cols);
     };
-    auto affine = [&](const Affine& a, Eight& u, int i, float mean, float rstd) {
-        const Eight w = load_any<kTeam>(a.weight, 0, kVec, i, lane, p.cols);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u.v[j] = (u.v[j] - mean) * rstd * w.v[j];
-        if (kLayer && a.bias.data != nullptr) {
-            const Eight b = load_any<kTeam>(a.bias, 0, kVec, i, lane, p.cols);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u.v[j] += b.v[j];
-        }
+    auto affine = [&](const Affine& a, const Eight& v, int i, float rstd) {
+        const Eight w = mul(rstd, load_any<kTeam>(a.weight, 0, kVec, i, lane, p.cols));
+        if (kLayer && a.bias.data != nullptr) return fma(v, w, load_any<kTeam>(a.bias, 0, kVec, i, lane, p.cols));
+        return mul(v, w);
     };
     pdl_next();
     pdl_wait();
@@ -44,41 +41,41 @@ __global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam) forward
     long long row = (long long)blockIdx.x * kTeams + threadIdx.x / kTeam;
     if (row < p.rows) load(row);
     for (; row < p.rows; row += step) {
+        if constexpr (kVec) {
+            copies_end();
+            copies_wait<0>();
+            in.stage ^= 1;
+            if (row + step < p.rows) load(row + step);
+        }
         Eight u[kVecs];
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) u[i] = widen_raw(h[i], false, kVec);
+        for (int i = 0; i < kVecs; ++i) u[i] = in.get(kH, i);
         if (p.post.weight.data != nullptr) {
-            float mean, rstd;
-            statistics<kTeam, kVecs, kLayer>(p, u, kVec, lane, sums, mean, rstd);
+            const float rstd = center<kTeam, kVecs, kLayer>(p, u, kVec, lane, sums);
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) affine(p.post, u[i], i, mean, rstd);
+            for (int i = 0; i < kVecs; ++i) u[i] = affine(p.post, u[i], i, rstd);
         }
-        if (p.gate_mode != kGateNone)
+        if (p.gate_mode != kGateNone) {
+            const long long g = gate_row(p, row);
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const Eight v = widen_raw(gate[i], p.gate.f32, kVec);
+            for (int i = 0; i < kVecs; ++i)
+                u[i] = mul(u[i], gate_value(full_gate ? in.get(kGate, i)
+                                                      : load_any<kTeam>(p.gate, g, kVec, i, lane, p.cols),
+                                            p.sigmoid));
+        }
+        if (has_x)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[i].v[j] *= gate_value(v.v[j], p.sigmoid);
-            }
-        if (p.x.data != nullptr)
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const Eight v = widen_raw(x[i], kStream32, kVec);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[i].v[j] = fmaf(p.scale, v.v[j], u[i].v[j]);
-            }
-        if (row + step < p.rows) load(row + step);
+            for (int i = 0; i < kVecs; ++i) u[i] = fma(p.scale, in.get(kX, i), u[i]);
+        if constexpr (!kVec)
+            if (row + step < p.rows) load(row + step);
         if (p.r.data != nullptr)
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.r, kStream32, row, kVec, i, lane, p.cols, u[i]);
         if (p.n.data == nullptr) continue;
-        float mean, rstd;
-        statistics<kTeam, kVecs, kLayer>(p, u, kVec, lane, sums, mean, rstd);
+        const float rstd = center<kTeam, kVecs, kLayer>(p, u, kVec, lane, sums);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            affine(p.pre, u[i], i, mean, rstd);
-            store_any<kTeam>(p.n, false, row, kVec, i, lane, p.cols, u[i]);
-        }
+        for (int i = 0; i < kVecs; ++i)
+            store_any<kTeam>(p.n, false, row, kVec, i, lane, p.cols, affine(p.pre, u[i], i, rstd));
     }
 }
 
@@ -136,8 +133,14 @@ cudaError_t launch_forward(const NormParams& p, cudaStream_t st) {
     const Shape s = forward_shape(p.cols);
     const int threads = s.team == 0 ? kLong : std::max(kForwardThreads, s.team);
     const int per = s.team == 0 ? 1 : threads / s.team;
+    size_t ring = 0;
+    if (s.team != 0 && kVec)
+        ring = (size_t)kStages * threads * s.vecs * 16 *
+               (1 + (p.x.data == nullptr ? 0 : kStream32 ? 2 : 1) + (p.gate_mode != kGateFull ? 0 : p.gate.f32 ? 2 : 1));
+    // as many blocks as an SM holds at a time
+    const int blocks = (int)std::min((size_t)((kVec ? kResident : kResident / 2) / threads), (kSharedLimit + 1024) / (ring + 2048));
     const long long want = (p.rows + per - 1) / per;
-    const dim3 grid((unsigned)std::min(want, (long long)kSMs * (1024 / threads)));
+    const dim3 grid((unsigned)std::min(want, (long long)kSMs * std::max(1, blocks)));
     void (*kernel)(NormParams);
     switch (s.team * 4 + s.vecs) {
     case 32 * 4 + 1: kernel = forward_kernel<32, 1, kLayer, kStream32, kVec>; break;
@@ -148,7 +151,7 @@ cudaError_t launch_forward(const NormParams& p, cudaStream_t st) {
     case 512 * 4 + 2: kernel = forward_kernel<512, 2, kLayer, kStream32, kVec>; break;
     default: kernel = forward_long_kernel<kLayer, kStream32>;
     }
-    return launch_pdl(kernel, grid, dim3(threads), st, p);
+    return launch_pdl_shared(kernel, grid, dim3(threads), ring, st, p);
 }
 template <bool kLayer, bool kStream32>
 cudaError_t launch_forward(const NormParams& p, cudaStream_t st) {

@@ -176,6 +176,66 @@ __device__ __forceinline__ Eight widen_raw(const Raw& r, bool f32, bool vec) {
     return e;
 }
 
+// The rows of up to five matrices as a team passes over them.  Rows on 16 bytes come
+// through shared memory: each thread copies its own columns of the next row
+// (asynchronously, so that they cost no registers on the way) while it works on this
+// one, and no other thread reads them.  Others are held in registers, from where the
+// last one has been used up.
+constexpr int kStages = 2;
+
+template <int kThreads, int kTeam, int kVecs, int kArrays, bool kVec, bool kRing>
+struct Stream {
+    uint4* ring;      // [stage][word][thread]
+    int words, stage; // of a row; the one that is read
+    int at[kArrays];  // an array's first word
+    bool f32[kArrays];
+    Raw raw[kRing ? 1 : kArrays][kRing ? 1 : kVecs];
+
+    __device__ __forceinline__ void begin(uint4* shared) {
+        ring = shared + threadIdx.x;
+        words = stage = 0;
+    }
+    __device__ __forceinline__ void array(int a, bool there, bool wide) {
+        at[a] = words;
+        f32[a] = wide;
+        if (there) words += kVecs * (wide ? 2 : 1);
+    }
+    __device__ __forceinline__ void load(int a, const Rows& x, long long row, int lane, int cols) {
+        if constexpr (kRing) {
+            const char* base = static_cast<const char*>(x.data) + row * x.ld * (f32[a] ? 4 : 2);
+            uint4* to = ring + ((stage ^ 1) * words + at[a]) * kThreads;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int c = (i * kTeam + lane) * 8;
+                if (f32[a]) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int bytes = max(0, min(16, (cols - c - half * 4) * 4));
+                        copy16(to + (i * 2 + half) * kThreads, base + (bytes ? (c + half * 4) * 4 : 0), bytes);
+                    }
+                } else {
+                    const int bytes = max(0, min(16, (cols - c) * 2));
+                    copy16(to + i * kThreads, base + (bytes ? c * 2 : 0), bytes);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) raw[a][i] = load_raw<kTeam>(x, f32[a], row, kVec, i, lane, cols);
+        }
+    }
+    __device__ __forceinline__ Eight get(int a, int i) const {
+        if constexpr (kRing) {
+            const uint4* from = ring + (stage * words + at[a]) * kThreads;
+            if (!f32[a]) return widen(from[i * kThreads]);
+            const uint4 lo = from[i * 2 * kThreads], hi = from[(i * 2 + 1) * kThreads];
+            return {{__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z), __uint_as_float(lo.w),
+                     __uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(hi.z), __uint_as_float(hi.w)}};
+        } else {
+            return widen_raw(raw[a][i], f32[a], kVec);
+        }
+    }
+};
+
 // ---------------------------------------------------------------------- sums --
 
 // Sums over a team; the team is a warp, or the whole block, whose calls then take
@@ -216,35 +276,47 @@ __device__ __forceinline__ float gate_slope(float g, bool sigmoid) {
     const float s = train::logistic(g);
     return s * train::logistic(-g);  // (1 - s would lose what is left of it near 1)
 }
+__device__ __forceinline__ Eight gate_value(const Eight& g, bool sigmoid) {
+    if (!sigmoid) return g;
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.v[j] = train::logistic(g.v[j]);
+    return r;
+}
 __device__ __forceinline__ long long gate_row(const NormParams& p, long long row) {
     return p.gate_mode == kGateFull ? row : p.gate_mode == kGateGroups ? row / p.group : 0;
 }
 
-// The mean and 1 / sqrt(variance + eps) of the row in v (RMS: 0 and that of the
-// mean square).
+// v minus its mean in the columns that are there, zeros beyond them.
+template <int kTeam>
+__device__ __forceinline__ Eight centered(const Eight& v, float mean, bool vec, int i, int lane, int cols) {
+    Eight r = add(-mean, v);
+    if (vec ? (i * kTeam + lane) * 8 + 8 > cols : true)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (column<kTeam>(vec, i, lane, j) >= cols) r.v[j] = 0.0f;
+    return r;
+}
+
+// Takes the row's mean off (LAYER) and returns 1 / sqrt(mean square + eps).
 template <int kTeam, int kVecs, bool kLayer>
-__device__ __forceinline__ void statistics(const NormParams& p, const Eight (&v)[kVecs], bool vec,
-                                           int lane, TeamSums<kTeam>& sums, float& mean, float& rstd) {
-    mean = 0.0f;
+__device__ __forceinline__ float center(const NormParams& p, Eight (&v)[kVecs], bool vec, int lane,
+                                        TeamSums<kTeam>& sums) {
     if constexpr (kLayer) {
-        float s[1] = {0.0f};
+        float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[0] += v[i].v[j];
+        for (int i = 0; i < kVecs; ++i) total(part, v[i]);
+        float s[1] = {sum_of(part)};
         sums(s);
-        mean = s[0] * p.inv_cols;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = centered<kTeam>(v[i], s[0] * p.inv_cols, vec, i, lane, p.cols);
     }
-    float s[1] = {0.0f};
+    float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float d = v[i].v[j] - mean;
-            if (!kLayer || column<kTeam>(vec, i, lane, j) < p.cols) s[0] = fmaf(d, d, s[0]);
-        }
+    for (int i = 0; i < kVecs; ++i) dot(part, v[i], v[i]);
+    float s[1] = {sum_of(part)};
     sums(s);
-    rstd = rsqrtf(fmaf(s[0], p.inv_cols, p.eps));
+    return rsqrtf(fmaf(s[0], p.inv_cols, p.eps));
 }
 
 // Rows that are too long for registers: a block a row, in steps of 8 * kLong

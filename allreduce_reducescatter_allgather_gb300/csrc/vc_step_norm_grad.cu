@@ -47,25 +47,32 @@ __device__ __forceinline__ void store_gate(const NormParams& p, long long row, b
 
 constexpr int kBackwardThreads = 256;  // of a block of teams that are warps
 
-// One row after the other: the next row's loads are issued where this row's inputs
-// have been used up, before its last sum.  Blocks whose threads hold two vectors of a
-// row have no registers left for the column sums: those lie in shared memory, where
-// each thread adds to its own.
+// One row after the other, the next one's inputs on their way meanwhile.  The column
+// sums of layer norms' long rows, and of long rows that come through registers, find
+// no registers: they lie in shared memory, where each thread adds to its own.
+template <int kTeam, int kVecs, bool kLayer, bool kVec>
+constexpr bool kThroughShared = kVec && !(kLayer && kVecs == 2 && kTeam > 32);
+
 template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
-__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam) backward_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam == 32 ? 1 : 512 / kTeam)
+    backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kBackwardThreads : kTeam, kTeams = kThreads / kTeam;
     // RMS norms have no biases
     constexpr int kKept = kLayer ? 5 : 3;
     constexpr int kPre = 0, kPost = 1, kGate = 2, kPreBias = 3, kPostBias = 4;
-    constexpr bool kInShared = kTeam > 32 && kVecs == 2;
+    constexpr bool kRing = kThroughShared<kTeam, kVecs, kLayer, kVec>;
+    constexpr bool kInShared = kTeam > 32 && kVecs == 2 && !kRing;
+    constexpr int kR = 0, kDn = 1, kH = 2, kDr = 3, kG = 4;
     __shared__ float shared[kTeam > 32 ? 8 : 1][kTeam / 32];
     __shared__ float joined[kTeams > 1 ? kTeams : 1][kTeams > 1 ? 8 * kTeam * kVecs : 1];
-    extern __shared__ float4 columns[];  // [sum][vector][half][thread]
+    extern __shared__ uint4 ring[];
+    float4* const columns = reinterpret_cast<float4*>(ring);  // [sum][vector][half][thread]
     TeamSums<kTeam> sums = {shared, 0};
     const int lane = threadIdx.x % kTeam;
     const long long team = (long long)blockIdx.x * kTeams + threadIdx.x / kTeam;
     const bool has_pre = p.dn.data != nullptr, has_post = p.post.weight.data != nullptr;
-    const bool has_h = p.h.data != nullptr;
+    const bool has_h = p.h.data != nullptr, has_dr = p.dr.data != nullptr;
+    const bool full_gate = p.gate_mode == kGateFull;
     const bool sums_gate = p.dgate.data != nullptr && (p.gate_mode == kGateShared || p.gate_mode == kGateGroups);
     Eight kept[kInShared ? 1 : kKept][kInShared ? 1 : kVecs];
     auto clear = [&](int k, int i) {
@@ -73,11 +80,10 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam) backwa
             float4* at = columns + (k * kVecs + i) * 2 * kTeam + lane;
             at[0] = at[kTeam] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) kept[k][i].v[j] = 0.0f;
+            kept[k][i] = zeros();
         }
     };
-    auto sum_of = [&](int k, int i) {
+    auto column_sum = [&](int k, int i) {
         if constexpr (kInShared) {
             const float4* at = columns + (k * kVecs + i) * 2 * kTeam + lane;
             const float4 lo = at[0], hi = at[kTeam];
@@ -86,43 +92,38 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam) backwa
             return kept[k][i];
         }
     };
-    auto add = [&](int k, int i, const Eight& d) {
+    // sum k += a b
+    auto add_product = [&](int k, int i, const Eight& a, const Eight& b) {
+        const Eight s = fma(a, b, column_sum(k, i));
         if constexpr (kInShared) {
             float4* at = columns + (k * kVecs + i) * 2 * kTeam + lane;
-            float4 lo = at[0], hi = at[kTeam];
-            lo.x += d.v[0], lo.y += d.v[1], lo.z += d.v[2], lo.w += d.v[3];
-            hi.x += d.v[4], hi.y += d.v[5], hi.z += d.v[6], hi.w += d.v[7];
-            at[0] = lo, at[kTeam] = hi;
+            at[0] = make_float4(s.v[0], s.v[1], s.v[2], s.v[3]);
+            at[kTeam] = make_float4(s.v[4], s.v[5], s.v[6], s.v[7]);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) kept[k][i].v[j] += d.v[j];
+            kept[k][i] = s;
         }
     };
+    const Eight ones = {{1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f}};
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) clear(k, i);
 
-    Raw raw_dr[kVecs], raw_dn[kVecs], raw_r[kVecs], raw_h[kVecs], raw_gate[kVecs];
+    Stream<kThreads, kTeam, kVecs, 5, kVec, kRing> in;
+    in.begin(ring);
+    in.array(kR, has_pre, kStream32);
+    in.array(kDn, has_pre, false);
+    in.array(kH, has_h, false);
+    in.array(kDr, has_dr, kStream32);
+    in.array(kG, full_gate, p.gate.f32);
     auto load = [&](long long row) {
-        if (has_pre)
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                raw_r[i] = load_raw<kTeam>(p.r, kStream32, row, kVec, i, lane, p.cols);
-                raw_dn[i] = load_raw<kTeam>(p.dn, false, row, kVec, i, lane, p.cols);
-            }
-        if (has_h)
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) raw_h[i] = load_raw<kTeam>(p.h, false, row, kVec, i, lane, p.cols);
-        if (p.dr.data != nullptr)
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) raw_dr[i] = load_raw<kTeam>(p.dr, kStream32, row, kVec, i, lane, p.cols);
-        if (p.gate_mode != kGateNone) {
-            const long long g = gate_row(p, row);
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i)
-                raw_gate[i] = load_raw<kTeam>(p.gate, p.gate.f32, g, kVec, i, lane, p.cols);
+        if (has_pre) {
+            in.load(kR, p.r, row, lane, p.cols);
+            in.load(kDn, p.dn, row, lane, p.cols);
         }
+        if (has_h) in.load(kH, p.h, row, lane, p.cols);
+        if (has_dr) in.load(kDr, p.dr, row, lane, p.cols);
+        if (full_gate) in.load(kG, p.gate, row, lane, p.cols);
     };
     pdl_next();
     pdl_wait();
@@ -130,146 +131,144 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam) backwa
     long long group_end = p.gate_mode == kGateGroups ? (lo / p.group + 1) * p.group : 0;
     if (lo < hi) load(lo);
     for (long long row = lo; row < hi; ++row) {
+        if constexpr (kRing) {
+            copies_end();
+            copies_wait<0>();
+            in.stage ^= 1;
+            if (row + 1 < hi) load(row + 1);
+        }
         // the statistics: with the means taken off first, in one sum for both norms
         float mean = 0.0f, h_mean = 0.0f;
         if constexpr (kLayer) {
-            float s[2] = {0.0f, 0.0f};
+            float2 a = make_float2(0.0f, 0.0f), b = a;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const Eight r = widen_raw(raw_r[i], kStream32, kVec), h = widen_raw(raw_h[i], false, kVec);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (has_pre) s[0] += r.v[j];
-                    if (has_post) s[1] += h.v[j];
-                }
+                if (has_pre) total(a, in.get(kR, i));
+                if (has_post) total(b, in.get(kH, i));
             }
+            float s[2] = {sum_of(a), sum_of(b)};
             sums(s);
             mean = s[0] * p.inv_cols;
             h_mean = s[1] * p.inv_cols;
         }
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        auto centered_r = [&](int i) {
+            const Eight r = in.get(kR, i);
+            return kLayer ? centered<kTeam>(r, mean, kVec, i, lane, p.cols) : r;
+        };
+        auto centered_h = [&](int i) {
+            const Eight h = in.get(kH, i);
+            return kLayer && has_post ? centered<kTeam>(h, h_mean, kVec, i, lane, p.cols) : h;
+        };
+        float rstd, h_rstd, m1 = 0.0f, m2;
+        {
+            float2 a = make_float2(0.0f, 0.0f), b = a, c = a, d = a;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            bool in[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) in[j] = !kLayer || column<kTeam>(kVec, i, lane, j) < p.cols;
-            if (has_pre) {
-                const Eight r = widen_raw(raw_r[i], kStream32, kVec), dn = widen_raw(raw_dn[i], false, kVec);
-                const Eight w = load_any<kTeam>(p.pre.weight, 0, kVec, i, lane, p.cols);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float c = in[j] ? r.v[j] - mean : 0.0f, d = w.v[j] * dn.v[j];
-                    s[0] = fmaf(c, c, s[0]);
-                    s[1] = fmaf(d, c, s[1]);
-                    if constexpr (kLayer) s[2] += d;
+            for (int i = 0; i < kVecs; ++i) {
+                if (has_pre) {
+                    const Eight r = centered_r(i);
+                    const Eight g = mul(load_any<kTeam>(p.pre.weight, 0, kVec, i, lane, p.cols), in.get(kDn, i));
+                    dot(a, r, r);
+                    dot(b, g, r);
+                    if constexpr (kLayer) total(c, g);
+                }
+                if (has_post) {
+                    const Eight h = centered_h(i);
+                    dot(d, h, h);
                 }
             }
-            if (has_post) {
-                const Eight h = widen_raw(raw_h[i], false, kVec);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float c = in[j] ? h.v[j] - h_mean : 0.0f;
-                    s[3] = fmaf(c, c, s[3]);
-                }
+            if constexpr (kLayer) {
+                float s[4] = {sum_of(a), sum_of(b), sum_of(d), sum_of(c)};
+                sums(s);
+                m1 = s[3] * p.inv_cols;
+                rstd = s[0], m2 = s[1], h_rstd = s[2];
+            } else {
+                float s[3] = {sum_of(a), sum_of(b), sum_of(d)};
+                sums(s);
+                rstd = s[0], m2 = s[1], h_rstd = s[2];
             }
         }
-        if (has_pre || has_post) sums(s);
-        const float rstd = rsqrtf(fmaf(s[0], p.inv_cols, p.eps)), h_rstd = rsqrtf(fmaf(s[3], p.inv_cols, p.eps));
-        const float m2 = s[1] * p.inv_cols * rstd, m1 = s[2] * p.inv_cols;
+        rstd = rsqrtf(fmaf(rstd, p.inv_cols, p.eps));
+        h_rstd = rsqrtf(fmaf(h_rstd, p.inv_cols, p.eps));
+        m2 *= p.inv_cols * rstd * rstd;
         Eight du[kVecs], hat[kVecs];
-        float t[2] = {0.0f, 0.0f};
+        float2 t1 = make_float2(0.0f, 0.0f), t2 = t1;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-            Eight dr;
-            if (p.dr.data != nullptr) {
-                dr = widen_raw(raw_dr[i], kStream32, kVec);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dr.v[j] = 0.0f;
-            }
+            Eight dr = has_dr ? in.get(kDr, i) : zeros();
             if (has_pre) {
-                const Eight r = widen_raw(raw_r[i], kStream32, kVec), dn = widen_raw(raw_dn[i], false, kVec);
+                const Eight r = mul(rstd, centered_r(i)), dn = in.get(kDn, i);
                 const Eight w = load_any<kTeam>(p.pre.weight, 0, kVec, i, lane, p.cols);
-                Eight part;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float c = (r.v[j] - mean) * rstd;
-                    part.v[j] = dn.v[j] * c;
-                    dr.v[j] = fmaf(rstd, fmaf(w.v[j], dn.v[j], -m1) - c * m2, dr.v[j]);
-                }
-                add(kPre, i, part);
-                if constexpr (kLayer) add(kPreBias, i, dn);
+                add_product(kPre, i, dn, r);
+                if constexpr (kLayer) add_product(kPreBias, i, dn, ones);
+                dr = fma(-m2, r, dr);
+                if constexpr (kLayer) dr = add(-m1 * rstd, dr);
+                dr = fma(mul(rstd, w), dn, dr);
             }
-            if (p.dx.data != nullptr) {
-                Eight d;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d.v[j] = p.scale * dr.v[j];
-                store_any<kTeam>(p.dx, kStream32, row, kVec, i, lane, p.cols, d);
-            }
-            if (has_h) hat[i] = widen_raw(raw_h[i], false, kVec);
+            if (p.dx.data != nullptr)
+                store_any<kTeam>(p.dx, kStream32, row, kVec, i, lane, p.cols, mul(p.scale, dr));
             Eight w;
+            if (has_h) hat[i] = centered_h(i);
             if (has_post) {
                 w = load_any<kTeam>(p.post.weight, 0, kVec, i, lane, p.cols);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) hat[i].v[j] = (hat[i].v[j] - h_mean) * h_rstd;
+                hat[i] = mul(h_rstd, hat[i]);
             }
             du[i] = dr;
             if (p.gate_mode != kGateNone) {
-                const Eight gate = widen_raw(raw_gate[i], p.gate.f32, kVec);
+                const Eight gate = full_gate ? in.get(kG, i)
+                                             : load_any<kTeam>(p.gate, gate_row(p, row), kVec, i, lane, p.cols);
                 if (p.dgate.data != nullptr) {
-                    Eight d = hat[i];
+                    Eight u = hat[i];
                     if (has_post) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) d.v[j] *= w.v[j];
-                        if (kLayer && p.post.bias.data != nullptr) {
-                            const Eight b = load_any<kTeam>(p.post.bias, 0, kVec, i, lane, p.cols);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) d.v[j] += b.v[j];
-                        }
+                        u = mul(u, w);
+                        if (kLayer && p.post.bias.data != nullptr)
+                            u = add(u, load_any<kTeam>(p.post.bias, 0, kVec, i, lane, p.cols));
                     }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) d.v[j] *= dr.v[j];
                     if (sums_gate)
-                        add(kGate, i, d);
+                        add_product(kGate, i, u, dr);
                     else
-                        store_gate<kTeam>(p, row, kVec, i, lane, d, gate);
+                        store_gate<kTeam>(p, row, kVec, i, lane, mul(u, dr), gate);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) du[i].v[j] *= gate_value(gate.v[j], p.sigmoid);
+                du[i] = mul(dr, gate_value(gate, p.sigmoid));
             }
             if (has_post) {
-                Eight part;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) part.v[j] = du[i].v[j] * hat[i].v[j];
-                add(kPost, i, part);
-                if constexpr (kLayer) add(kPostBias, i, du[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    t[0] = fmaf(part.v[j], w.v[j], t[0]);
-                    du[i].v[j] *= w.v[j];
-                    if constexpr (kLayer) t[1] += du[i].v[j];
-                }
+                add_product(kPost, i, du[i], hat[i]);
+                if constexpr (kLayer) add_product(kPostBias, i, du[i], ones);
+                du[i] = mul(du[i], w);
+                dot(t1, du[i], hat[i]);
+                if constexpr (kLayer) total(t2, du[i]);
             }
         }
-        // this row's inputs are used up
-        if (row + 1 < hi) load(row + 1);
+        // (this row's inputs are used up)
+        if constexpr (!kRing)
+            if (row + 1 < hi) load(row + 1);
         if (p.gate_mode == kGateGroups && (row + 1 == group_end || row + 1 == hi)) {
             if (sums_gate)
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    flush_gate<kTeam>(p, team, row / p.group, lo, hi, kVec, i, lane, sum_of(kGate, i));
+                    flush_gate<kTeam>(p, team, row / p.group, lo, hi, kVec, i, lane, column_sum(kGate, i));
                     clear(kGate, i);
                 }
             group_end += p.group;
         }
         if (p.dh.data == nullptr) continue;
         if (has_post) {
-            sums(t);
-            const float h_m2 = t[0] * p.inv_cols, h_m1 = t[1] * p.inv_cols;
+            float h_m2, h_m1 = 0.0f;
+            if constexpr (kLayer) {
+                float s[2] = {sum_of(t1), sum_of(t2)};
+                sums(s);
+                h_m2 = s[0], h_m1 = s[1];
+            } else {
+                float s[1] = {sum_of(t1)};
+                sums(s);
+                h_m2 = s[0];
+            }
+            h_m2 *= p.inv_cols * h_rstd;
+            h_m1 *= p.inv_cols * h_rstd;
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) du[i].v[j] = h_rstd * (du[i].v[j] - h_m1 - hat[i].v[j] * h_m2);
+            for (int i = 0; i < kVecs; ++i) {
+                du[i] = fma(-h_m2, hat[i], mul(h_rstd, du[i]));
+                if constexpr (kLayer) du[i] = add(-h_m1, du[i]);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.dh, false, row, kVec, i, lane, p.cols, du[i]);
@@ -285,12 +284,12 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam) backwa
         if constexpr (kTeams == 1) {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
-                store_any<kTeam>(parts, true, at, kVec, i, lane, p.cols, sum_of(k, i));
+                store_any<kTeam>(parts, true, at, kVec, i, lane, p.cols, column_sum(k, i));
         } else {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const Eight sum = sum_of(k, i);
+                const Eight sum = column_sum(k, i);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     joined[threadIdx.x / kTeam][column<kTeam>(kVec, i, lane, j)] = sum.v[j];
@@ -546,8 +545,20 @@ Split split_of(long long rows, long long cols) {
 
 template <bool kLayer, bool kStream32, bool kVec>
 cudaError_t launch_backward(const NormParams& p, const Split& s, cudaStream_t st) {
+    const bool ring = s.shape.team == 32 ? kVec : kVec && !(kLayer && s.shape.vecs == 2);
+    size_t bytes = 0;
+    if (s.shape.team != 0 && ring)
+        bytes = (size_t)kStages * s.threads * s.shape.vecs * 16 *
+                ((p.dn.data == nullptr ? 0 : kStream32 ? 3 : 2) + (p.h.data != nullptr) +
+                 (p.dr.data == nullptr ? 0 : kStream32 ? 2 : 1) +
+                 (p.gate_mode != kGateFull ? 0 : p.gate.f32 ? 2 : 1));
+    else if (s.shape.team > 32 && s.shape.vecs == 2)
+        bytes = (size_t)(kLayer ? 5 : 3) * s.shape.team * s.shape.vecs * 32;
+    // (four 32-bit words a column of two rows: a gate for every element beside a 32-bit stream)
+    const bool fits = bytes + 1024 <= kSharedLimit;
+    if (!fits) bytes = 0;
     void (*kernel)(NormParams);
-    switch (s.shape.team * 4 + s.shape.vecs) {
+    switch (fits ? s.shape.team * 4 + s.shape.vecs : 0) {
     case 32 * 4 + 1: kernel = backward_kernel<32, 1, kLayer, kStream32, kVec>; break;
     case 32 * 4 + 2: kernel = backward_kernel<32, 2, kLayer, kStream32, kVec>; break;
     case 128 * 4 + 1: kernel = backward_kernel<128, 1, kLayer, kStream32, kVec>; break;
@@ -556,8 +567,6 @@ cudaError_t launch_backward(const NormParams& p, const Split& s, cudaStream_t st
     case 512 * 4 + 2: kernel = backward_kernel<512, 2, kLayer, kStream32, kVec>; break;
     default: kernel = backward_long_kernel<kLayer, kStream32>;
     }
-    const bool shared = s.shape.team > 32 && s.shape.vecs == 2;
-    const size_t bytes = shared ? (size_t)(kLayer ? 5 : 3) * s.shape.team * s.shape.vecs * 32 : 0;
     cudaError_t e = launch_pdl_shared(kernel, dim3(s.blocks), dim3(s.threads), bytes, st, p);
     const bool groups = p.dgate.data != nullptr && p.gate_mode == kGateGroups;
     if (e != cudaSuccess || (p.kinds == 0 && !groups)) return e;
