@@ -15,13 +15,14 @@ __global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam, (kVec ?
     forward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kForwardThreads : kTeam, kTeams = kThreads / kTeam;
     constexpr int kH = 0, kX = 1, kGate = 2;
-    __shared__ float shared[kTeam > 32 ? 8 : 1][kTeam / 32];
+    __shared__ float shared[2 * kTeam / 32][4];
     extern __shared__ uint4 ring[];
     TeamSums<kTeam> sums = {shared, 0};
-    const int lane = threadIdx.x % kTeam;
+    const int lane = kTeams == 1 ? threadIdx.x : threadIdx.x % 32;
+    const int part = kTeams == 1 ? 0 : __shfl_sync(~0u, threadIdx.x / 32, 0);  // the team in the block
     const bool has_x = p.x.data != nullptr, full_gate = p.gate_mode == kGateFull;
     Stream<kThreads, kTeam, kVecs, 3, kVec, kVec> in;
-    in.begin(ring);
+    in.begin(ring, lane, p.cols);
     in.array(kH, true, false);
     in.array(kX, has_x, kStream32);
     in.array(kGate, full_gate, p.gate.f32);
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam, (kVec ?
     pdl_next();
     pdl_wait();
     const long long step = (long long)gridDim.x * kTeams;
-    long long row = (long long)blockIdx.x * kTeams + threadIdx.x / kTeam;
+    long long row = (long long)blockIdx.x * kTeams + part;
     if (row < p.rows) load(row);
     for (; row < p.rows; row += step) {
         if constexpr (kVec) {
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam, (kVec ?
 
 template <bool kLayer, bool kStream32>
 __global__ void __launch_bounds__(kLong) forward_long_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float shared[8][kLong / 32];
+    __shared__ float shared[2 * kLong / 32][4];
     TeamSums<kLong> sums = {shared, 0};
     const int lane = threadIdx.x, steps = (p.cols + 8 * kLong - 1) / (8 * kLong);
     pdl_next();

@@ -185,15 +185,26 @@ constexpr int kStages = 2;
 
 template <int kThreads, int kTeam, int kVecs, int kArrays, bool kVec, bool kRing>
 struct Stream {
-    uint4* ring;      // [stage][word][thread]
-    int words, stage; // of a row; the one that is read
-    int at[kArrays];  // an array's first word
+    uint4* ring;       // [stage][word][thread]
+    int words, stage;  // of a row; the one that is read
+    int at[kArrays];   // an array's first word
     bool f32[kArrays];
+    // what there is of the thread's columns, in bytes of 16 or 32 bits a value, and where
+    int bytes[kRing ? 3 : 1][kRing ? kVecs : 1], offset[kRing ? kVecs : 1];
     Raw raw[kRing ? 1 : kArrays][kRing ? 1 : kVecs];
 
-    __device__ __forceinline__ void begin(uint4* shared) {
+    __device__ __forceinline__ void begin(uint4* shared, int lane, int cols) {
         ring = shared + threadIdx.x;
         words = stage = 0;
+        if constexpr (kRing)
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int c = (i * kTeam + lane) * 8, n = cols - c;
+                bytes[0][i] = max(0, min(16, n * 2));
+                bytes[1][i] = max(0, min(16, n * 4));
+                bytes[2][i] = max(0, min(16, n * 4 - 16));
+                offset[i] = n > 0 ? c : 0;  // (nothing is read where there is nothing)
+            }
     }
     __device__ __forceinline__ void array(int a, bool there, bool wide) {
         at[a] = words;
@@ -202,21 +213,18 @@ struct Stream {
     }
     __device__ __forceinline__ void load(int a, const Rows& x, long long row, int lane, int cols) {
         if constexpr (kRing) {
-            const char* base = static_cast<const char*>(x.data) + row * x.ld * (f32[a] ? 4 : 2);
             uint4* to = ring + ((stage ^ 1) * words + at[a]) * kThreads;
+            if (f32[a]) {
+                const float* from = static_cast<const float*>(x.data) + row * x.ld;
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int c = (i * kTeam + lane) * 8;
-                if (f32[a]) {
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int bytes = max(0, min(16, (cols - c - half * 4) * 4));
-                        copy16(to + (i * 2 + half) * kThreads, base + (bytes ? (c + half * 4) * 4 : 0), bytes);
-                    }
-                } else {
-                    const int bytes = max(0, min(16, (cols - c) * 2));
-                    copy16(to + i * kThreads, base + (bytes ? c * 2 : 0), bytes);
+                for (int i = 0; i < kVecs; ++i) {
+                    copy16(to + i * 2 * kThreads, from + offset[i], bytes[1][i]);
+                    copy16(to + (i * 2 + 1) * kThreads, from + offset[i] + (bytes[2][i] ? 4 : 0), bytes[2][i]);
                 }
+            } else {
+                const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(x.data) + row * x.ld;
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) copy16(to + i * kThreads, from + offset[i], bytes[0][i]);
             }
         } else {
 #pragma unroll
@@ -236,34 +244,81 @@ struct Stream {
     }
 };
 
+// A vector of the row's length that is used in every row (a weight, a bias, the gate
+// of the rows at hand): in shared memory, in 32 bits, each thread's own columns, or
+// read where it lies.
+template <int kTeam, int kVecs, bool kVec, bool kHeld>
+struct Held {
+    float4* at;  // [vector][half][lane]
+    static constexpr bool kHolding = kHeld;
+    static constexpr int kBytes = kVecs * 2 * kTeam * 16;
+    __device__ __forceinline__ void put(int i, const Eight& x) const {
+        at[i * 2 * kTeam] = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
+        at[(i * 2 + 1) * kTeam] = make_float4(x.v[4], x.v[5], x.v[6], x.v[7]);
+    }
+    __device__ __forceinline__ void hold(const Rows& x, int lane, int cols) const {
+        if constexpr (kHeld)
+            if (x.data != nullptr)
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) put(i, load_any<kTeam>(x, 0, kVec, i, lane, cols));
+    }
+    __device__ __forceinline__ Eight get(const Rows& x, int i, int lane, int cols) const {
+        if constexpr (kHeld) {
+            const float4 lo = at[i * 2 * kTeam], hi = at[(i * 2 + 1) * kTeam];
+            return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+        } else {
+            return load_any<kTeam>(x, 0, kVec, i, lane, cols);
+        }
+    }
+};
+
 // ---------------------------------------------------------------------- sums --
 
-// Sums over a team; the team is a warp, or the whole block, whose calls then take
-// turns between two buffers, so that one barrier a call does.
+// Sums over a team of up to four values at a time.  A warp's lanes share the values
+// out while they add (of four values each lane keeps two, then one), the warps of a
+// block leave theirs in shared memory.  Calls take turns between two buffers there, so
+// that one barrier a call does.
 template <int kTeam>
 struct TeamSums {
     static constexpr int kWarps = kTeam / 32;
-    float (*shared)[kWarps];  // [2 * 4][kWarps]
+    float (*shared)[4];  // [2 * kWarps][4]
     int turn;
     template <int kN>
     __device__ __forceinline__ void operator()(float (&v)[kN]) {
-        static_assert(kN <= 4, "a buffer has four rows");
+        static_assert(kN <= 4, "a buffer has four columns");
+        constexpr int kP = kN == 3 ? 4 : kN;
+        const int lane = threadIdx.x & 31;
+        float c;
+        if constexpr (kP == 4) {
+            const bool high = lane & 16, odd = lane & 8;
+            const float v3 = kN == 4 ? v[kN - 1] : 0.0f;
+            float a = high ? v[2] : v[0], b = high ? v3 : v[1];
+            a += __shfl_xor_sync(~0u, high ? v[0] : v[2], 16);
+            b += __shfl_xor_sync(~0u, high ? v[1] : v3, 16);
+            c = (odd ? b : a) + __shfl_xor_sync(~0u, odd ? a : b, 8);
+        } else if constexpr (kP == 2) {
+            const bool high = lane & 16;
+            c = (high ? v[1] : v[0]) + __shfl_xor_sync(~0u, high ? v[0] : v[1], 16);
+        } else {
+            c = v[0];
+        }
 #pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = warp_sum(v[i]);
-        if constexpr (kTeam > 32) {
-            float(*buf)[kWarps] = shared + turn * 4;
+        for (int o = 16 / kP; o > 0; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
+        if constexpr (kTeam == 32) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[i] = __shfl_sync(~0u, c, i * (32 / kP));
+        } else {
+            float(*buf)[4] = shared + turn * kWarps;
             turn ^= 1;
-            if ((threadIdx.x & 31) == 0)
-#pragma unroll
-                for (int i = 0; i < kN; ++i) buf[i][threadIdx.x >> 5] = v[i];
+            if (lane % (32 / kP) == 0) buf[threadIdx.x >> 5][lane / (32 / kP)] = c;
             __syncthreads();
+            const int q = lane % kP, w = lane / kP;
+            c = w < kWarps ? buf[w][q] : 0.0f;
+            if constexpr (kWarps > 32 / kP) c += buf[w + 32 / kP][q];
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                float s = 0.0f;
+            for (int o = 16; o >= kP; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) s += buf[i][w];
-                v[i] = s;
-            }
+            for (int i = 0; i < kN; ++i) v[i] = __shfl_sync(~0u, c, i);
         }
     }
 };

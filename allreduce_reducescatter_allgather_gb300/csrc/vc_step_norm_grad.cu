@@ -6,7 +6,9 @@ namespace step {
 namespace {
 
 // The rows of team t: a run of neighbours.
-__device__ __forceinline__ long long first_row(const NormParams& p, long long t) { return t * p.rows / p.teams; }
+__device__ __forceinline__ long long first_row(const NormParams& p, long long t) {
+    return t < p.teams ? t * p.rows / p.teams : p.rows;
+}
 
 // A team's sum of dr u over the rows of group g that it has: the whole of it goes to
 // dgate, a part to one of the team's two slots: 0 where the group started before
@@ -53,8 +55,12 @@ constexpr int kBackwardThreads = 256;  // of a block of teams that are warps
 template <int kTeam, int kVecs, bool kLayer, bool kVec>
 constexpr bool kThroughShared = kVec && !(kLayer && kVecs == 2 && kTeam > 32);
 
+// Weights and the gate of the rows at hand are held in shared memory where there is room.
 template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
-__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam == 32 ? 1 : 512 / kTeam)
+constexpr bool kHolds = kThroughShared<kTeam, kVecs, kLayer, kVec> && !(kTeam == 512 && kVecs == 2 && kStream32);
+
+template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
+__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam == 32 ? 2 / kVecs : 512 / kTeam)
     backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kBackwardThreads : kTeam, kTeams = kThreads / kTeam;
     // RMS norms have no biases
@@ -63,13 +69,14 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
     constexpr bool kRing = kThroughShared<kTeam, kVecs, kLayer, kVec>;
     constexpr bool kInShared = kTeam > 32 && kVecs == 2 && !kRing;
     constexpr int kR = 0, kDn = 1, kH = 2, kDr = 3, kG = 4;
-    __shared__ float shared[kTeam > 32 ? 8 : 1][kTeam / 32];
+    __shared__ float shared[2 * kTeam / 32][4];
     __shared__ float joined[kTeams > 1 ? kTeams : 1][kTeams > 1 ? 8 * kTeam * kVecs : 1];
     extern __shared__ uint4 ring[];
     float4* const columns = reinterpret_cast<float4*>(ring);  // [sum][vector][half][thread]
     TeamSums<kTeam> sums = {shared, 0};
-    const int lane = threadIdx.x % kTeam;
-    const long long team = (long long)blockIdx.x * kTeams + threadIdx.x / kTeam;
+    const int lane = kTeams == 1 ? threadIdx.x : threadIdx.x % 32;
+    const int part = kTeams == 1 ? 0 : __shfl_sync(~0u, threadIdx.x / 32, 0);  // the team in the block
+    const long long team = (long long)blockIdx.x * kTeams + part;
     const bool has_pre = p.dn.data != nullptr, has_post = p.post.weight.data != nullptr;
     const bool has_h = p.h.data != nullptr, has_dr = p.dr.data != nullptr;
     const bool full_gate = p.gate_mode == kGateFull;
@@ -110,12 +117,16 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
         for (int i = 0; i < kVecs; ++i) clear(k, i);
 
     Stream<kThreads, kTeam, kVecs, 5, kVec, kRing> in;
-    in.begin(ring);
+    in.begin(ring, lane, p.cols);
     in.array(kR, has_pre, kStream32);
     in.array(kDn, has_pre, false);
     in.array(kH, has_h, false);
     in.array(kDr, has_dr, kStream32);
     in.array(kG, full_gate, p.gate.f32);
+    using Vector = Held<kTeam, kVecs, kVec, kHolds<kTeam, kVecs, kLayer, kStream32, kVec>>;
+    float4* const held = reinterpret_cast<float4*>(ring + kStages * in.words * kThreads) + lane;
+    const Vector pre = {held}, post = {held + Vector::kBytes / 16}, shift = {held + 2 * (Vector::kBytes / 16)},
+                 held_gate = {held + ((kLayer ? 3 : 2) + part) * (Vector::kBytes / 16)};  // (a team's own)
     auto load = [&](long long row) {
         if (has_pre) {
             in.load(kR, p.r, row, lane, p.cols);
@@ -130,7 +141,19 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
     const long long lo = first_row(p, team), hi = first_row(p, team + 1);
     long long group_end = p.gate_mode == kGateGroups ? (lo / p.group + 1) * p.group : 0;
     if (lo < hi) load(lo);
+    // (threads read what they have written themselves)
+    pre.hold(p.pre.weight, lane, p.cols);
+    post.hold(p.post.weight, lane, p.cols);
+    if constexpr (kLayer) shift.hold(p.post.bias, lane, p.cols);
+    long long g = p.gate_mode == kGateGroups ? lo / p.group : 0;  // the rows' gate
+    bool new_gate = p.gate_mode == kGateShared || p.gate_mode == kGateGroups;
     for (long long row = lo; row < hi; ++row) {
+        if (Vector::kHolding && new_gate) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                held_gate.put(i, gate_value(load_any<kTeam>(p.gate, g, kVec, i, lane, p.cols), p.sigmoid));
+            new_gate = false;
+        }
         if constexpr (kRing) {
             copies_end();
             copies_wait<0>();
@@ -166,7 +189,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
             for (int i = 0; i < kVecs; ++i) {
                 if (has_pre) {
                     const Eight r = centered_r(i);
-                    const Eight g = mul(load_any<kTeam>(p.pre.weight, 0, kVec, i, lane, p.cols), in.get(kDn, i));
+                    const Eight g = mul(pre.get(p.pre.weight, i, lane, p.cols), in.get(kDn, i));
                     dot(a, r, r);
                     dot(b, g, r);
                     if constexpr (kLayer) total(c, g);
@@ -197,7 +220,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
             Eight dr = has_dr ? in.get(kDr, i) : zeros();
             if (has_pre) {
                 const Eight r = mul(rstd, centered_r(i)), dn = in.get(kDn, i);
-                const Eight w = load_any<kTeam>(p.pre.weight, 0, kVec, i, lane, p.cols);
+                const Eight w = pre.get(p.pre.weight, i, lane, p.cols);
                 add_product(kPre, i, dn, r);
                 if constexpr (kLayer) add_product(kPreBias, i, dn, ones);
                 dr = fma(-m2, r, dr);
@@ -209,26 +232,31 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
             Eight w;
             if (has_h) hat[i] = centered_h(i);
             if (has_post) {
-                w = load_any<kTeam>(p.post.weight, 0, kVec, i, lane, p.cols);
+                w = post.get(p.post.weight, i, lane, p.cols);
                 hat[i] = mul(h_rstd, hat[i]);
             }
             du[i] = dr;
             if (p.gate_mode != kGateNone) {
-                const Eight gate = full_gate ? in.get(kG, i)
-                                             : load_any<kTeam>(p.gate, gate_row(p, row), kVec, i, lane, p.cols);
+                Eight gate, value;
+                if (full_gate || !Vector::kHolding) {
+                    gate = full_gate ? in.get(kG, i) : load_any<kTeam>(p.gate, g, kVec, i, lane, p.cols);
+                    value = gate_value(gate, p.sigmoid);
+                } else {
+                    value = held_gate.get(p.gate, i, lane, p.cols);
+                }
                 if (p.dgate.data != nullptr) {
                     Eight u = hat[i];
                     if (has_post) {
                         u = mul(u, w);
                         if (kLayer && p.post.bias.data != nullptr)
-                            u = add(u, load_any<kTeam>(p.post.bias, 0, kVec, i, lane, p.cols));
+                            u = add(u, shift.get(p.post.bias, i, lane, p.cols));
                     }
                     if (sums_gate)
                         add_product(kGate, i, u, dr);
                     else
                         store_gate<kTeam>(p, row, kVec, i, lane, mul(u, dr), gate);
                 }
-                du[i] = mul(dr, gate_value(gate, p.sigmoid));
+                du[i] = mul(dr, value);
             }
             if (has_post) {
                 add_product(kPost, i, du[i], hat[i]);
@@ -245,10 +273,12 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
             if (sums_gate)
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    flush_gate<kTeam>(p, team, row / p.group, lo, hi, kVec, i, lane, column_sum(kGate, i));
+                    flush_gate<kTeam>(p, team, g, lo, hi, kVec, i, lane, column_sum(kGate, i));
                     clear(kGate, i);
                 }
             group_end += p.group;
+            ++g;
+            new_gate = true;
         }
         if (p.dh.data == nullptr) continue;
         if (has_post) {
@@ -292,7 +322,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
                 const Eight sum = column_sum(k, i);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    joined[threadIdx.x / kTeam][column<kTeam>(kVec, i, lane, j)] = sum.v[j];
+                    joined[part][column<kTeam>(kVec, i, lane, j)] = sum.v[j];
             }
             __syncthreads();
             for (int c = threadIdx.x; c < p.cols; c += kThreads) {
@@ -309,7 +339,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
 // parts, where each thread adds to its own columns.
 template <bool kLayer, bool kStream32>
 __global__ void __launch_bounds__(kLong) backward_long_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float shared[8][kLong / 32];
+    __shared__ float shared[2 * kLong / 32][4];
     TeamSums<kLong> sums = {shared, 0};
     const int lane = threadIdx.x, steps = (p.cols + 8 * kLong - 1) / (8 * kLong);
     const bool has_pre = p.dn.data != nullptr, has_post = p.post.weight.data != nullptr;
@@ -497,19 +527,32 @@ __global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ No
             : kind == kSumPost ? p.dpost.weight : kind == kSumPostBias ? p.dpost.bias : p.dgate, 0, s);
         return;
     }
-    for (long long t = kind - kSums; t < p.teams; t += kJoinRows) {
-        // the group of the team's last row, where it starts there and goes on
-        const long long lo = first_row(p, t), hi = first_row(p, t + 1), g = (hi - 1) / p.group;
-        if (lo == hi || g * p.group < lo || (g + 1) * p.group <= hi) continue;
-        const long long last = ((g + 1) * p.group * p.teams - 1) / p.rows;  // the team of its last row
-        float s = 0.0f;
-        if (live)
+    // teams whose last row's group starts with them and goes on behind them
+    __shared__ int found[1025];
+    for (int t0 = kind - kSums; t0 < p.teams; t0 += kJoinRows * 1024) {
+        if (threadIdx.x == 0) found[1024] = 0;
+        __syncthreads();
+        const long long mine = t0 + (long long)threadIdx.x * kJoinRows;
+        if (mine < p.teams) {
+            const long long lo = first_row(p, mine), hi = first_row(p, mine + 1), g = (hi - 1) / p.group;
+            // (which place a team gets changes nothing but the order of work)
+            if (g * p.group >= lo && (g + 1) * p.group > hi) found[atomicAdd(&found[1024], 1)] = (int)mine;
+        }
+        __syncthreads();
+        const int n = found[1024];
+        for (int f = 0; f < n; ++f) {
+            const int t = found[f];
+            const long long g = (first_row(p, t + 1) - 1) / p.group;
+            const int last = (int)(((g + 1) * p.group * p.teams - 1) / p.rows);  // the team of its last row
+            float s = 0.0f;
+            if (live)
 #pragma unroll 4
-            for (long long w = t + warp; w <= last; w += 32)
-                if (first_row(p, w) < first_row(p, w + 1))
-                    s += p.slots[(w * 2 + (w == t ? 1 : 0)) * p.padded + c];
-        s = total(s);
-        put(p.dgate, g, s * slope(g));
+                for (int w = t + warp; w <= last; w += 32)
+                    s += p.slots[((long long)w * 2 + (w == t ? 1 : 0)) * p.padded + c];
+            s = total(s);
+            put(p.dgate, g, s * slope(g));
+        }
+        __syncthreads();
     }
 }
 
@@ -537,8 +580,8 @@ Split split_of(long long rows, long long cols) {
     const int per = s.threads / team;
     // four rows a team at least, so that the parts stay few beside the rows
     const long long want = (rows + 4 * per - 1) / (4 * per);
-    s.blocks = (int)std::max(1ll, std::min(want, (long long)kSMs * std::max(1, 512 / s.threads)));
-    s.teams = s.blocks * per;
+    s.blocks = (int)std::max(1ll, std::min(want, (long long)kSMs * (team == 32 ? 2 / s.shape.vecs : std::max(1, 512 / s.threads))));
+    s.teams = (int)std::min(rows, (long long)s.blocks * per);  // (the others have no rows)
     s.padded = (cols + 7) / 8 * 8;
     return s;
 }
@@ -554,7 +597,12 @@ cudaError_t launch_backward(const NormParams& p, const Split& s, cudaStream_t st
                  (p.gate_mode != kGateFull ? 0 : p.gate.f32 ? 2 : 1));
     else if (s.shape.team > 32 && s.shape.vecs == 2)
         bytes = (size_t)(kLayer ? 5 : 3) * s.shape.team * s.shape.vecs * 32;
-    // (four 32-bit words a column of two rows: a gate for every element beside a 32-bit stream)
+    // weights and gate that are held beside it
+    if (s.shape.team != 0 && ring && !(s.shape.team == 512 && s.shape.vecs == 2 && kStream32))
+        bytes += (size_t)((kLayer ? 3 : 2) * s.shape.team +
+                          (p.gate_mode == kGateShared || p.gate_mode == kGateGroups ? s.threads : 0)) *
+                 s.shape.vecs * 32;
+    // (what does not fit, as a 32-bit gate for every element of the longest rows, is read again)
     const bool fits = bytes + 1024 <= kSharedLimit;
     if (!fits) bytes = 0;
     void (*kernel)(NormParams);
