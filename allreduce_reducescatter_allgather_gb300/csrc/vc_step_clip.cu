@@ -23,7 +23,8 @@ namespace {
 constexpr int kClipThreads = 256;
 constexpr int kTileBytes = VC_CLIP_TILE_MAX_BYTES;
 constexpr int kVecs = kTileBytes / 16 / kClipThreads;  // 16-byte vectors of a thread
-constexpr int kMaxBlocks = kSMs * 8;
+constexpr int kResident = 6;  // blocks of an SM
+constexpr int kMaxBlocks = kSMs * kResident;
 
 int clip_blocks(int ntiles) { return std::max(1, std::min(ntiles, kMaxBlocks)); }
 
@@ -141,7 +142,7 @@ __device__ __forceinline__ int first_tile(int b, int blocks, int ntiles) {
 }
 
 template <bool kMax>
-__global__ void __launch_bounds__(kClipThreads) norm_kernel(const vc_clip_tile_t* tiles, int ntiles,
+__global__ void __launch_bounds__(kClipThreads, kResident) norm_kernel(const vc_clip_tile_t* tiles, int ntiles,
                                                             double* parts) {
     __shared__ double shared[kClipThreads / 32];
     pdl_next();
@@ -149,8 +150,12 @@ __global__ void __launch_bounds__(kClipThreads) norm_kernel(const vc_clip_tile_t
     const int end = first_tile(blockIdx.x + 1, gridDim.x, ntiles);
     double sum = 0.0;
     unsigned top = 0;
-    for (int i = first_tile(blockIdx.x, gridDim.x, ntiles); i < end; ++i) {
-        const vc_clip_tile_t t = tiles[i];
+    int i = first_tile(blockIdx.x, gridDim.x, ntiles);
+    vc_clip_tile_t next = {};
+    if (i < end) next = tiles[i];
+    for (; i < end; ++i) {
+        const vc_clip_tile_t t = next;
+        if (i + 1 < end) next = tiles[i + 1];
         Held h;
         load_tile(t, cut_of(t), h);
         if constexpr (kMax)
@@ -214,7 +219,7 @@ __device__ __forceinline__ void store_tile(const vc_clip_tile_t& t, const Cut& c
 }
 
 template <bool kMax, bool kClip>
-__global__ void __launch_bounds__(kClipThreads) clip_kernel(const vc_clip_tile_t* tiles, int ntiles,
+__global__ void __launch_bounds__(kClipThreads, kResident) clip_kernel(const vc_clip_tile_t* tiles, int ntiles,
                                                             const double* parts, int nparts,
                                                             float max_norm, float eps, float* norm) {
     __shared__ double shared[kClipThreads / 32];
@@ -226,8 +231,12 @@ __global__ void __launch_bounds__(kClipThreads) clip_kernel(const vc_clip_tile_t
         const float q = __fdiv_rn(max_norm, total + eps);
         const float scale = q >= 1.0f ? 1.0f : q;  // (a NaN stays one)
         const int begin = first_tile(blockIdx.x, gridDim.x, ntiles);
-        for (int i = first_tile(blockIdx.x + 1, gridDim.x, ntiles) - 1; i >= begin; --i) {
-            const vc_clip_tile_t t = tiles[i];
+        int i = first_tile(blockIdx.x + 1, gridDim.x, ntiles) - 1;
+        vc_clip_tile_t next = {};
+        if (i >= begin) next = tiles[i];
+        for (; i >= begin; --i) {
+            const vc_clip_tile_t t = next;
+            if (i > begin) next = tiles[i - 1];
             if (t.dst == nullptr || (scale == 1.0f && t.src == t.dst)) continue;
             const Cut c = cut_of(t);
             Held h;

@@ -128,6 +128,141 @@ __device__ __forceinline__ uint4 narrow(const Eight& r) {
                       narrow2(r.v[6], r.v[7]));
 }
 
+// ------------------------------------------------------------------- columns --
+
+// The columns of thread `lane` of a team in its v-th vector: eight neighbours on
+// 16 bytes, or every kTeam-th one.
+template <int kTeam>
+__device__ __forceinline__ int column(bool vec, int v, int lane, int j) {
+    return vec ? (v * kTeam + lane) * 8 + j : (v * 8 + j) * kTeam + lane;
+}
+
+template <int kTeam>
+__device__ __forceinline__ Eight load_f32(const void* data, long long at, bool vec, int v, int lane, int cols) {
+    const float* p = static_cast<const float*>(data) + at;
+    const int c = (v * kTeam + lane) * 8;
+    if (vec && c + 8 <= cols) {
+        const float4 lo = *reinterpret_cast<const float4*>(p + c), hi = *reinterpret_cast<const float4*>(p + c + 4);
+        return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+    }
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = column<kTeam>(vec, v, lane, j);
+        r.v[j] = k < cols ? p[k] : 0.0f;
+    }
+    return r;
+}
+template <int kTeam>
+__device__ __forceinline__ Eight load_bf16(const void* data, long long at, bool vec, int v, int lane, int cols) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(data) + at;
+    const int c = (v * kTeam + lane) * 8;
+    if (vec && c + 8 <= cols) return widen(*reinterpret_cast<const uint4*>(p + c));
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = column<kTeam>(vec, v, lane, j);
+        r.v[j] = k < cols ? __bfloat162float(p[k]) : 0.0f;
+    }
+    return r;
+}
+template <int kTeam>
+__device__ __forceinline__ Eight load_any(const Rows& x, long long row, bool vec, int v, int lane, int cols) {
+    return x.f32 ? load_f32<kTeam>(x.data, row * x.ld, vec, v, lane, cols)
+                 : load_bf16<kTeam>(x.data, row * x.ld, vec, v, lane, cols);
+}
+template <int kTeam>
+__device__ __forceinline__ Eight load_as(const Rows& x, bool f32, long long row, bool vec, int v, int lane, int cols) {
+    return f32 ? load_f32<kTeam>(x.data, row * x.ld, vec, v, lane, cols)
+               : load_bf16<kTeam>(x.data, row * x.ld, vec, v, lane, cols);
+}
+template <int kTeam>
+__device__ __forceinline__ void store_any(const Rows& x, bool f32, long long row, bool vec, int v, int lane,
+                                          int cols, const Eight& r) {
+    float* f = static_cast<float*>(x.data) + row * x.ld;
+    __nv_bfloat16* b = static_cast<__nv_bfloat16*>(x.data) + row * x.ld;
+    const int c = (v * kTeam + lane) * 8;
+    if (vec && c + 8 <= cols) {
+        if (f32) {
+            *reinterpret_cast<float4*>(f + c) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+            *reinterpret_cast<float4*>(f + c + 4) = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(b + c) = narrow(r);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = column<kTeam>(vec, v, lane, j);
+        if (k >= cols) continue;
+        if (f32)
+            f[k] = r.v[j];
+        else
+            b[k] = __float2bfloat16(r.v[j]);
+    }
+}
+
+// Eight columns of a row as they lie in memory, so that a thread can hold the next
+// row's while it computes with this one's: eight 32-bit words of float32, or of
+// bfloat16 four words of two (on 16 bytes) or eight of one.  kOnce: what is read once
+// leaves the caches to what is not.
+struct Raw {
+    unsigned w[8];
+};
+template <bool kOnce, class T>
+__device__ __forceinline__ T load_word(const T* p) {
+    return kOnce ? __ldcs(p) : *p;
+}
+template <int kTeam, bool kOnce = true>
+__device__ __forceinline__ Raw load_raw(const Rows& x, bool f32, long long row, bool vec, int v, int lane, int cols) {
+    const long long at = row * x.ld;
+    const int c = (v * kTeam + lane) * 8;
+    Raw r;
+    if (vec && c + 8 <= cols) {
+        if (f32) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x.data) + at + c);
+            const uint4 lo = load_word<kOnce>(p), hi = load_word<kOnce>(p + 1);
+            r = {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+        } else {
+            const uint4 u = load_word<kOnce>(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.data) + at + c));
+            r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+        }
+        return r;
+    }
+    if (!f32 && vec)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.w[j] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = column<kTeam>(vec, v, lane, j);
+        if (f32) {
+            r.w[j] = k < cols ? load_word<kOnce>(static_cast<const unsigned*>(x.data) + at + k) : 0;
+        } else {
+            const unsigned u = k < cols ? load_word<kOnce>(static_cast<const unsigned short*>(x.data) + at + k) : 0;
+            if (vec)
+                r.w[j / 2] |= u << (j % 2 * 16);
+            else
+                r.w[j] = u;
+        }
+    }
+    return r;
+}
+__device__ __forceinline__ Eight widen_raw(const Raw& r, bool f32, bool vec) {
+    Eight e;
+    if (f32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e.v[j] = __uint_as_float(r.w[j]);
+    } else if (vec) {
+        e = widen(make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e.v[j] = __uint_as_float(r.w[j] << 16);
+    }
+    return e;
+}
+
+// ---------------------------------------------------------------------- warps --
+
 // Sums of a whole warp, the same in every lane.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

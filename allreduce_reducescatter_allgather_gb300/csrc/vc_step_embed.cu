@@ -36,90 +36,58 @@ struct LookupParams {
     const void* ids;
     int wide;  // 64-bit ids
     Rows weight, out;
-    long long first, units;
+    long long first, tokens;
     unsigned long long rows;
-    int cols, per_row;  // units of a row
+    int cols, shift;  // log2 of the threads that share a row
     float scale;
 };
 
-// kVec: a unit is eight columns on 16 bytes (fewer at a row's end), else one.
-template <int kUnits, bool kVec>
-__global__ void __launch_bounds__(256) lookup_kernel(const __grid_constant__ LookupParams p) {
+constexpr int kLookupThreads = 256, kLookupUnits = 4;  // units of a thread in flight
+
+// A group of threads a token.  kVec: a unit is eight columns on 16 bytes (fewer at a
+// row's end), else one.
+template <bool kVec>
+__global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const __grid_constant__ LookupParams p) {
     pdl_next();
     pdl_wait();
-    const long long base = (long long)blockIdx.x * (256 * kUnits);
-    const long long t0 = base / p.per_row;
-    const unsigned c0 = (unsigned)(base - t0 * p.per_row);
-    long long token[kUnits];
-    unsigned long long row[kUnits];  // (below the table's start: far above its end)
-    int col[kUnits];
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        const unsigned at = u * 256 + threadIdx.x, c = c0 + at, t = c / (unsigned)p.per_row;
-        token[u] = base + at < p.units ? t0 + t : -1;
-        col[u] = (int)(c - t * p.per_row) * (kVec ? 8 : 1);
-        row[u] = token[u] >= 0 ? (unsigned long long)load_id(p.ids, p.wide, token[u]) -
-                                     (unsigned long long)p.first
-                               : ~0ull;
-    }
-    Eight v[kUnits];
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        const bool in = row[u] < p.rows;
-        const long long at = (in ? (long long)row[u] : 0) * p.weight.ld + col[u];
-        const float* f = static_cast<const float*>(p.weight.data) + at;
-        const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(p.weight.data) + at;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[u].v[j] = 0.0f;
-        if (!in) continue;
+    const int width = 1 << p.shift, lane = threadIdx.x & (width - 1), units = kVec ? (p.cols + 7) / 8 : p.cols;
+    const long long token = ((long long)blockIdx.x * kLookupThreads + threadIdx.x) >> p.shift;
+    if (token >= p.tokens) return;
+    const unsigned long long row =
+        (unsigned long long)load_id(p.ids, p.wide, token) - (unsigned long long)p.first;
+    const bool in = row < p.rows;  // (a row below the table's start is far above its end)
+    const long long from = in ? (long long)row : 0;
+    for (int u0 = lane; u0 < units; u0 += kLookupUnits * width) {
         if constexpr (kVec) {
-            const int n = p.cols - col[u];
-            if (n >= 8 && p.weight.f32) {
-                const float4 a = reinterpret_cast<const float4*>(f)[0];
-                const float4 c = reinterpret_cast<const float4*>(f)[1];
-                v[u] = {{a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w}};
-            } else if (n >= 8) {
-                v[u] = widen(*reinterpret_cast<const uint4*>(b));
-            } else {
+            Raw raw[kLookupUnits];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n) v[u].v[j] = p.weight.f32 ? f[j] : __bfloat162float(b[j]);
+            for (int u = 0; u < kLookupUnits; ++u)
+                if (in) raw[u] = load_raw<1, false>(p.weight, p.weight.f32, from, true, u0 + u * width, 0, p.cols);
+#pragma unroll
+            for (int u = 0; u < kLookupUnits; ++u) {
+                const Eight r = in ? mul(p.scale, widen_raw(raw[u], p.weight.f32, true)) : zeros();
+                if (u0 + u * width < units) store_any<1>(p.out, p.out.f32, token, true, u0 + u * width, 0, p.cols, r);
             }
         } else {
-            v[u].v[0] = p.weight.f32 ? *f : __bfloat162float(*b);
-        }
-    }
+            float v[kLookupUnits];
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        if (token[u] < 0) continue;
-        const bool in = row[u] < p.rows;
-        const long long at = token[u] * p.out.ld + col[u];
-        float* f = static_cast<float*>(p.out.data) + at;
-        __nv_bfloat16* b = static_cast<__nv_bfloat16*>(p.out.data) + at;
-        Eight r;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r.v[j] = in ? v[u].v[j] * p.scale : 0.0f;
-        if constexpr (kVec) {
-            const int n = p.cols - col[u];
-            if (n >= 8 && p.out.f32) {
-                reinterpret_cast<float4*>(f)[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-                reinterpret_cast<float4*>(f)[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
-            } else if (n >= 8) {
-                *reinterpret_cast<uint4*>(b) = narrow(r);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n) {
-                        if (p.out.f32)
-                            f[j] = r.v[j];
-                        else
-                            b[j] = __float2bfloat16(r.v[j]);
-                    }
+            for (int u = 0; u < kLookupUnits; ++u) {
+                const long long at = from * p.weight.ld + u0 + u * width;
+                v[u] = 0.0f;
+                if (in && u0 + u * width < units)
+                    v[u] = p.weight.f32 ? static_cast<const float*>(p.weight.data)[at]
+                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.weight.data)[at]);
             }
-        } else if (p.out.f32) {
-            *f = r.v[0];
-        } else {
-            *b = __float2bfloat16(r.v[0]);
+#pragma unroll
+            for (int u = 0; u < kLookupUnits; ++u) {
+                if (u0 + u * width >= units) continue;
+                const long long at = token * p.out.ld + u0 + u * width;
+                const float r = in ? v[u] * p.scale : 0.0f;
+                if (p.out.f32)
+                    static_cast<float*>(p.out.data)[at] = r;
+                else
+                    static_cast<__nv_bfloat16*>(p.out.data)[at] = __float2bfloat16(r);
+            }
         }
     }
 }
@@ -131,6 +99,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kItems = 8;           // of a thread at a time
 constexpr int kChunk = kSortThreads * kItems;
+constexpr int kFillClusters = 15;   // beside the one that sorts: all that run at a time
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kMarkRows = 16384;    // rows that a block marks at a time
 
@@ -173,15 +142,15 @@ struct SortShared {
 
 // Ranks the chunk's items among those of their warp with the same digit, and leaves
 // the counts of the warps before each in count[][], the chunk's in chunk[].
-__device__ void rank_chunk(SortShared& s, const uint2 (&item)[kItems], int begin, int end, int shift,
+__device__ void rank_chunk(SortShared& s, const uint2 (&item)[kItems], int each, int begin, int end, int shift,
                            unsigned mask, int (&rank)[kItems]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < kSortWarps * kBins / 2; i += kSortThreads)
-        reinterpret_cast<unsigned*>(s.count)[i] = 0;
-    __syncthreads();
+    for (int i = lane; i < kBins / 2; i += 32) reinterpret_cast<unsigned*>(s.count[warp])[i] = 0;
+    __syncwarp();
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-        const bool live = begin + warp * (kItems * 32) + k * 32 + lane < end;
+        if (k >= each) break;
+        const bool live = begin + (warp * each + k) * 32 + lane < end;
         const unsigned digit = live ? (item[k].x >> shift) & mask : kBins;
         const unsigned same = __match_any_sync(~0u, digit);
         const int before = live ? s.count[warp][digit] : 0;
@@ -194,6 +163,7 @@ __device__ void rank_chunk(SortShared& s, const uint2 (&item)[kItems], int begin
     __syncthreads();
     if (threadIdx.x <= mask) {
         unsigned sum = 0;
+#pragma unroll 8
         for (int w = 0; w < kSortWarps; ++w) {
             const unsigned n = s.count[w][threadIdx.x];
             s.count[w][threadIdx.x] = (unsigned short)sum;
@@ -210,6 +180,7 @@ __device__ void sort_tokens(const SortParams& p, SortShared& s) {
     const int lo = min((long long)p.tokens, (long long)me * each);
     const int hi = min((long long)p.tokens, (long long)(me + 1) * each);
     const bool once = each <= kChunk;
+    const int items = min(kItems, (each + kSortThreads - 1) / kSortThreads);  // of a thread
     const unsigned mask = (1u << p.bits) - 1;
     for (int pass = 0; pass < p.passes; ++pass) {
         // the last pass writes a
@@ -222,8 +193,8 @@ __device__ void sort_tokens(const SortParams& p, SortShared& s) {
         auto load = [&](int begin) {
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
-                const int i = begin + warp * (kItems * 32) + k * 32 + lane;
-                if (i >= hi)
+                const int i = begin + (warp * items + k) * 32 + lane;
+                if (k >= items || i >= hi)
                     item[k] = make_uint2(0, 0);
                 else
                     item[k] = pass == 0 ? make_uint2(key_of(p, i), i) : __ldcg(from + i);
@@ -232,7 +203,7 @@ __device__ void sort_tokens(const SortParams& p, SortShared& s) {
         if (threadIdx.x <= mask) s.total[threadIdx.x] = 0;
         for (int begin = lo; begin < hi || (once && begin == lo); begin += kChunk) {
             load(begin);
-            rank_chunk(s, item, begin, hi, shift, mask, rank);
+            rank_chunk(s, item, items, begin, hi, shift, mask, rank);
             if (threadIdx.x <= mask) s.total[threadIdx.x] += s.chunk[threadIdx.x];
             if (once) break;
         }
@@ -263,11 +234,11 @@ __device__ void sort_tokens(const SortParams& p, SortShared& s) {
         for (int begin = lo; begin < hi; begin += kChunk) {
             if (!once) {
                 load(begin);
-                rank_chunk(s, item, begin, hi, shift, mask, rank);
+                rank_chunk(s, item, items, begin, hi, shift, mask, rank);
             }
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
-                if (begin + warp * (kItems * 32) + k * 32 + lane >= hi) continue;
+                if (k >= items || begin + (warp * items + k) * 32 + lane >= hi) continue;
                 const unsigned digit = (item[k].x >> shift) & mask;
                 const unsigned at = s.base[digit] + s.count[warp][digit] + rank[k];
                 if (at < (unsigned)p.tokens) __stcg(to + at, item[k]);  // (ids that change meanwhile)
@@ -347,88 +318,22 @@ struct SumParams {
     float scale;
 };
 
-// Eight columns of a row: neighbours on 16 bytes, or every 32nd one.
-template <bool kVec>
-__device__ __forceinline__ Eight load_row(const Rows& x, long long row, int c0, int lane, int cols) {
-    const long long at = row * x.ld + c0;
-    const float* f = static_cast<const float*>(x.data) + at;
-    const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(x.data) + at;
-    Eight r;
-    if constexpr (kVec) {
-        const int c = lane * 8;
-        if (c0 + c + 8 <= cols) {
-            if (x.f32) {
-                const float4 lo = *reinterpret_cast<const float4*>(f + c),
-                             hi = *reinterpret_cast<const float4*>(f + c + 4);
-                return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
-            }
-            return widen(*reinterpret_cast<const uint4*>(b + c));
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int c = kVec ? lane * 8 + j : j * 32 + lane;
-        r.v[j] = c0 + c < cols ? (x.f32 ? f[c] : __bfloat162float(b[c])) : 0.0f;
-    }
-    return r;
-}
-template <bool kVec>
-__device__ __forceinline__ void store_row(const Rows& x, long long row, int c0, int lane, int cols,
-                                          const Eight& r) {
-    const long long at = row * x.ld + c0;
-    float* f = static_cast<float*>(x.data) + at;
-    __nv_bfloat16* b = static_cast<__nv_bfloat16*>(x.data) + at;
-    if constexpr (kVec) {
-        const int c = lane * 8;
-        if (c0 + c + 8 <= cols) {
-            if (x.f32) {
-                *reinterpret_cast<float4*>(f + c) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-                *reinterpret_cast<float4*>(f + c + 4) = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
-            } else {
-                *reinterpret_cast<uint4*>(b + c) = narrow(r);
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int c = kVec ? lane * 8 + j : j * 32 + lane;
-        if (c0 + c >= cols) continue;
-        if (x.f32)
-            f[c] = r.v[j];
-        else
-            b[c] = __float2bfloat16(r.v[j]);
-    }
-}
-
 // dW row (+)= scale * sum
 template <bool kVec>
-__device__ __forceinline__ void finish_row(const SumParams& p, unsigned row, int c0, int lane,
-                                           const Eight& sum) {
-    Eight r;
-    if (p.accumulate) {
-        r = load_row<kVec>(p.dw, row, c0, lane, p.cols);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r.v[j] = fmaf(p.scale, sum.v[j], r.v[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r.v[j] = p.scale * sum.v[j];
-    }
-    store_row<kVec>(p.dw, row, c0, lane, p.cols, r);
+__device__ __forceinline__ void finish_row(const SumParams& p, unsigned row, int slice, int lane, const Eight& sum) {
+    Eight r = mul(p.scale, sum);
+    if (p.accumulate) r = add(r, load_any<32>(p.dw, row, kVec, slice, lane, p.cols));
+    store_any<32>(p.dw, p.dw.f32, row, kVec, slice, lane, p.cols, r);
 }
 
-__device__ __forceinline__ float* part_at(const SumParams& p, int window, int last, int c0, int lane) {
-    return p.parts + ((long long)window * 2 + last) * p.padded + c0 + lane * 8;
-}
-
-template <int kWindow, bool kVec>
+template <int kWindow, bool kVec, bool kF32>
 __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_constant__ SumParams p) {
-    constexpr int kBatch = 8;  // rows in flight
+    constexpr int kBatch = kVec && !kF32 ? 8 : 4;  // rows in flight
     pdl_next();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const long long unit = (long long)blockIdx.x * kSumWarps + (threadIdx.x >> 5);
-    const int window = (int)(unit / p.slices), c0 = (int)(unit - (long long)window * p.slices) * kSlice;
+    const long long unit = (long long)blockIdx.x * kSumWarps + __shfl_sync(~0u, threadIdx.x / 32, 0);
+    const int window = (int)(unit / p.slices), slice = (int)(unit - (long long)window * p.slices);
     if (window >= p.windows) return;
     const int begin = window * kWindow;
     const uint2 none = make_uint2(p.rows, 0);
@@ -440,129 +345,100 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_consta
     }
     const unsigned before = begin > 0 ? p.sorted[begin - 1].x : p.rows;
     const unsigned after = p.tokens - begin > kWindow ? p.sorted[begin + kWindow].x : p.rows;
-    Eight sum;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum.v[j] = 0.0f;
+    Eight sum = zeros();
     unsigned row = __shfl_sync(~0u, mine[0].x, 0);
     bool first = true;
+    const Rows parts = {p.parts, p.padded, 1, 1};
     auto flush = [&](bool end) {
         if (row >= p.rows) return;
         const bool from = first && row == before, on = end && row == after;
-        if (from || on) {
-            float4* to = reinterpret_cast<float4*>(part_at(p, window, from ? 0 : 1, c0, lane));
-            to[0] = make_float4(sum.v[0], sum.v[1], sum.v[2], sum.v[3]);
-            to[1] = make_float4(sum.v[4], sum.v[5], sum.v[6], sum.v[7]);
-        } else {
-            finish_row<kVec>(p, row, c0, lane, sum);
-        }
+        if (from || on)
+            store_any<32>(parts, true, (long long)window * 2 + (from ? 0 : 1), kVec, slice, lane, p.cols, sum);
+        else
+            finish_row<kVec>(p, row, slice, lane, sum);
     };
 #pragma unroll 1
     for (int b = 0; b < kWindow; b += kBatch) {
-        Eight v[kBatch];
+        Raw v[kBatch];
         unsigned key[kBatch];
+        const uint2 from = kWindow > 32 && b >= 32 ? mine[(kWindow + 31) / 32 - 1] : mine[0];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const uint2 from = kWindow > 32 && b >= 32 ? mine[(kWindow + 31) / 32 - 1] : mine[0];
             key[i] = __shfl_sync(~0u, from.x, (b + i) & 31);
             const unsigned token = __shfl_sync(~0u, from.y, (b + i) & 31);
-            if (key[i] < p.rows) v[i] = load_row<kVec>(p.dy, token, c0, lane, p.cols);
+            if (key[i] < p.rows) v[i] = load_raw<32>(p.dy, kF32, token, kVec, slice, lane, p.cols);
         }
+        if (key[0] >= p.rows) break;  // (the tokens that are left out come last)
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             if (key[i] != row) {
                 flush(false);
                 first = false;
                 row = key[i];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum.v[j] = 0.0f;
+                sum = zeros();
             }
-            if (row < p.rows) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum.v[j] += v[i].v[j];
-            }
+            if (row < p.rows) sum = add(sum, widen_raw(v[i], kF32, kVec));
         }
     }
     flush(true);
 }
 
 // A row that starts in one window and goes on into others: its last partial sum
-// there and the first ones of the windows behind, by the warps of a block in
-// turn.  Blocks look for such rows among their windows.
-constexpr int kJoinWarps = 8, kJoinThreads = kJoinWarps * 32;
+// there and the first ones of the windows behind, a warp for 128 columns.
+constexpr int kJoinWarps = 8, kJoinColumns = 128;
 
 template <int kWindow, bool kVec>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ SumParams p) {
-    __shared__ int found[kJoinThreads + 1];
-    __shared__ int behind;
-    __shared__ float4 shared[kJoinWarps][64];
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ SumParams p) {
     pdl_next();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x * kSlice;
-    const int lo = (int)((long long)p.windows * blockIdx.y / gridDim.y);
-    const int hi = (int)((long long)p.windows * (blockIdx.y + 1) / gridDim.y);
+    const int lane = threadIdx.x & 31, chunks = (p.cols + kJoinColumns - 1) / kJoinColumns;
+    const long long unit = (long long)blockIdx.x * kJoinWarps + __shfl_sync(~0u, threadIdx.x / 32, 0);
+    const int start = (int)(unit / chunks);
+    if (start + 1 >= p.windows) return;
     auto key = [&](int window, int i) { return p.sorted[(long long)window * kWindow + i].x; };
-    for (int w0 = lo; w0 < hi; w0 += kJoinThreads) {
-        const int w = w0 + threadIdx.x;
-        bool starts = false;
-        if (w < hi && w + 1 < p.windows) {
-            const unsigned last = key(w, kWindow - 1);
-            starts = last < p.rows && key(w + 1, 0) == last &&
-                     !(key(w, 0) == last && w > 0 && p.sorted[(long long)w * kWindow - 1].x == last);
+    const unsigned row = key(start, kWindow - 1);
+    if (row >= p.rows || key(start + 1, 0) != row) return;
+    if (start > 0 && key(start, 0) == row && key(start - 1, kWindow - 1) == row) return;
+    int ends = start + 2;  // the first window behind that the row does not reach
+    for (;; ends += 32) {
+        const int u = ends + lane;
+        const unsigned other = __ballot_sync(~0u, u >= p.windows || key(u, 0) != row);
+        if (other != 0) {
+            ends += __ffs(other) - 1;
+            break;
         }
-        if (threadIdx.x == 0) found[kJoinThreads] = 0;
-        __syncthreads();
-        // (which slot a window gets changes nothing but the order of work)
-        if (starts) found[atomicAdd(&found[kJoinThreads], 1)] = w;
-        __syncthreads();
-        const int n = found[kJoinThreads];
-        for (int f = 0; f < n; ++f) {
-            const int start = found[f];
-            const unsigned row = key(start, kWindow - 1);
-            // windows behind that go on with the row
-            int ends = p.windows;
-            for (int u0 = start + 1; u0 < p.windows; u0 += kJoinThreads) {
-                __syncthreads();
-                if (threadIdx.x == 0) behind = p.windows;
-                __syncthreads();
-                const int u = u0 + threadIdx.x;
-                if (u < p.windows && key(u, 0) != row) atomicMin(&behind, u);
-                __syncthreads();
-                ends = behind;
-                if (ends < p.windows) break;
-            }
-            Eight sum;
+    }
+    const int c = (int)(unit - (long long)start * chunks) * kJoinColumns + lane * 4;
+    if (c >= p.cols) return;
+    const float* at = p.parts + ((long long)start * 2 + 1) * p.padded + c;
+    float4 sum = *reinterpret_cast<const float4*>(at);
+    at += p.padded;  // (the next window's first row)
+#pragma unroll 8
+    for (int u = start + 1; u < ends; ++u, at += 2 * p.padded) {
+        const float4 v = *reinterpret_cast<const float4*>(at);
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    const float s[4] = {sum.x, sum.y, sum.z, sum.w};
+    const long long to = (long long)row * p.dw.ld + c;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum.v[j] = 0.0f;
-#pragma unroll 4
-            for (int u = start + warp; u < ends; u += kJoinWarps) {
-                const float4* from =
-                    reinterpret_cast<const float4*>(part_at(p, u, u == start ? 1 : 0, c0, lane));
-                const float4 a = from[0], b = from[1];
-                sum.v[0] += a.x, sum.v[1] += a.y, sum.v[2] += a.z, sum.v[3] += a.w;
-                sum.v[4] += b.x, sum.v[5] += b.y, sum.v[6] += b.z, sum.v[7] += b.w;
-            }
-            __syncthreads();
-            shared[warp][lane * 2] = make_float4(sum.v[0], sum.v[1], sum.v[2], sum.v[3]);
-            shared[warp][lane * 2 + 1] = make_float4(sum.v[4], sum.v[5], sum.v[6], sum.v[7]);
-            __syncthreads();
-            if (warp == 0) {
-                for (int o = 1; o < kJoinWarps; ++o) {
-                    const float4 a = shared[o][lane * 2], b = shared[o][lane * 2 + 1];
-                    sum.v[0] += a.x, sum.v[1] += a.y, sum.v[2] += a.z, sum.v[3] += a.w;
-                    sum.v[4] += b.x, sum.v[5] += b.y, sum.v[6] += b.z, sum.v[7] += b.w;
-                }
-                finish_row<kVec>(p, row, c0, lane, sum);
-            }
+    for (int j = 0; j < 4; ++j) {
+        if (c + j >= p.cols) break;
+        if (p.dw.f32) {
+            float* f = static_cast<float*>(p.dw.data) + to + j;
+            *f = fmaf(p.scale, s[j], p.accumulate ? *f : 0.0f);
+        } else {
+            __nv_bfloat16* b = static_cast<__nv_bfloat16*>(p.dw.data) + to + j;
+            *b = __float2bfloat16(fmaf(p.scale, s[j], p.accumulate ? __bfloat162float(*b) : 0.0f));
         }
-        __syncthreads();
     }
 }
 
-// Tokens of a window: as many as leave a warp window for each of 32 warps an SM.
+// Tokens of a window: as many as leave a window for each of 12 warps an SM, each
+// of which has 4 KiB of rows in flight.
 int window_of(long long tokens, long long cols) {
     const long long slices = (cols + kSlice - 1) / kSlice;
     int w = 64;
-    while (w > 8 && (tokens + w - 1) / w * slices < kSMs * 32) w /= 2;
+    while (w > 8 && (tokens + w - 1) / w * slices < kSMs * 12) w /= 2;
     return w;
 }
 
@@ -586,11 +462,12 @@ BackwardSpace space_of(long long tokens, long long cols) {
 template <int kWindow, bool kVec>
 cudaError_t launch_sums(const SumParams& p, cudaStream_t st) {
     const long long units = (long long)p.windows * p.slices;
-    cudaError_t e = launch_pdl(sum_kernel<kWindow, kVec>, dim3((unsigned)((units + kSumWarps - 1) / kSumWarps)),
-                               dim3(kSumWarps * 32), st, p);
+    const long long joins = (long long)p.windows * ((p.cols + kJoinColumns - 1) / kJoinColumns);
+    cudaError_t e = launch_pdl(p.dy.f32 ? sum_kernel<kWindow, kVec, true> : sum_kernel<kWindow, kVec, false>,
+                               dim3((unsigned)((units + kSumWarps - 1) / kSumWarps)), dim3(kSumWarps * 32), st, p);
     if (e != cudaSuccess || p.windows == 1) return e;
-    const int across = std::max(1, std::min(p.windows, kSMs * 4 / std::min(p.slices, kSMs * 4)));
-    return launch_pdl(join_kernel<kWindow, kVec>, dim3(p.slices, across), dim3(kJoinThreads), st, p);
+    return launch_pdl(join_kernel<kWindow, kVec>, dim3((unsigned)((joins + kJoinWarps - 1) / kJoinWarps)),
+                      dim3(kJoinWarps * 32), st, p);
 }
 template <bool kVec>
 cudaError_t launch_sums(const SumParams& p, int window, cudaStream_t st) {
@@ -640,17 +517,18 @@ vc_status_t vc_embedding_forward(const void* ids, vc_dtype_t id_dtype, long long
     p.rows = weight->rows;
     p.cols = (int)weight->cols;
     p.scale = scale;
+    p.tokens = tokens;
     const bool vec = p.weight.vec && p.out.vec;
-    p.per_row = vec ? (p.cols + 7) / 8 : p.cols;
-    p.units = tokens * p.per_row;
-    // four units a thread where that still gives every SM its share
-    const bool many = p.units >= 4ll * 256 * kSMs * 4;
-    const long long blocks = (p.units + (many ? 1024 : 256) - 1) / (many ? 1024 : 256);
-    if (blocks > 0x7FFFFFFF) return VC_ERR_INVALID_ARGUMENT;
-    auto* kernel = many ? (vec ? lookup_kernel<4, true> : lookup_kernel<4, false>)
-                        : (vec ? lookup_kernel<1, true> : lookup_kernel<1, false>);
-    const cudaError_t e = launch_pdl(kernel, dim3((unsigned)blocks), dim3(256),
-                                     static_cast<cudaStream_t>(stream), p);
+    // a warp a row; half of one or less where that reaches over the row; up to a block
+    // where there are few rows, down to one unit a thread
+    const long long units = vec ? (p.cols + 7) / 8 : p.cols;
+    p.shift = 0;
+    while (p.shift < 8 && (1ll << p.shift) < units &&
+           (p.shift < 5 || (tokens << p.shift) < (long long)kSMs * 1024))
+        ++p.shift;
+    const long long blocks = ((tokens << p.shift) + kLookupThreads - 1) / kLookupThreads;
+    const cudaError_t e = launch_pdl(vec ? lookup_kernel<true> : lookup_kernel<false>, dim3((unsigned)blocks),
+                                     dim3(kLookupThreads), static_cast<cudaStream_t>(stream), p);
     return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
 }
 
@@ -708,7 +586,7 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
     s.pitch = dw.ld * es;
     s.vec = dw.vec;
     // blocks for the zeros: those of the clusters that fit beside the sorting one
-    const int fill = accumulate ? 0 : (int)std::min((long long)(kSMs / kCluster - 1), (V + 31) / 32) * kCluster;
+    const int fill = accumulate ? 0 : (int)std::min((long long)kFillClusters, (V + 31) / 32) * kCluster;
     cudaError_t e = launch_pdl(sort_kernel, dim3(kCluster + fill), dim3(kSortThreads), st, s);
     if (e != cudaSuccess) return VC_ERR_CUDA;
     if (tokens == 0) return VC_SUCCESS;
