@@ -25,6 +25,7 @@ constexpr int kTileBytes = VC_CLIP_TILE_MAX_BYTES;
 constexpr int kVecs = kTileBytes / 16 / kClipThreads;  // 16-byte vectors of a thread
 constexpr int kResident = 6;  // blocks of an SM
 constexpr int kMaxBlocks = kSMs * kResident;
+constexpr size_t kCacheBytes = 80u << 20;
 
 int clip_blocks(int ntiles) { return std::max(1, std::min(ntiles, kMaxBlocks)); }
 
@@ -64,13 +65,15 @@ __device__ __forceinline__ float load_value(const vc_clip_tile_t& t, int i) {
     return __bfloat162float(static_cast<const __nv_bfloat16*>(t.src)[i]);
 }
 
+// kOnce: not read again.
+template <bool kOnce>
 __device__ __forceinline__ void load_tile(const vc_clip_tile_t& t, const Cut& c, Held& h) {
     const char* base = static_cast<const char*>(t.src) + c.head * (t.flags & kTileF32 ? 4 : 2);
     const uint4* p = reinterpret_cast<const uint4*>(base);
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
         const int i = u * kClipThreads + threadIdx.x;
-        h.v[u] = i < c.vecs ? p[i] : make_uint4(0, 0, 0, 0);
+        h.v[u] = i < c.vecs ? load_word<kOnce>(p + i) : make_uint4(0, 0, 0, 0);
     }
     const int e = edge_of(t, c);
     h.edge = e >= 0 ? load_value(t, e) : 0.0f;
@@ -142,12 +145,13 @@ __device__ __forceinline__ int first_tile(int b, int blocks, int ntiles) {
 }
 
 template <bool kMax>
-__global__ void __launch_bounds__(kClipThreads, kResident) norm_kernel(const vc_clip_tile_t* tiles, int ntiles,
-                                                            double* parts) {
+__global__ void __launch_bounds__(kClipThreads, kResident)
+    norm_kernel(const vc_clip_tile_t* tiles, int ntiles, int again, double* parts) {
     __shared__ double shared[kClipThreads / 32];
     pdl_next();
     pdl_wait();
     const int end = first_tile(blockIdx.x + 1, gridDim.x, ntiles);
+    const int keep = end - again;  // the tiles from here on are read again
     double sum = 0.0;
     unsigned top = 0;
     int i = first_tile(blockIdx.x, gridDim.x, ntiles);
@@ -157,7 +161,10 @@ __global__ void __launch_bounds__(kClipThreads, kResident) norm_kernel(const vc_
         const vc_clip_tile_t t = next;
         if (i + 1 < end) next = tiles[i + 1];
         Held h;
-        load_tile(t, cut_of(t), h);
+        if (i < keep)
+            load_tile<true>(t, cut_of(t), h);
+        else
+            load_tile<false>(t, cut_of(t), h);
         if constexpr (kMax)
             top = max(top, largest(h, t.flags & kTileF32));
         else
@@ -197,7 +204,7 @@ __device__ __forceinline__ void store_tile(const vc_clip_tile_t& t, const Cut& c
             o[j] = f32 ? __float_as_uint(scale * __uint_as_float(w[j]))
                        : narrow2(scale * lo16(w[j]), scale * hi16(w[j]));
         if (vec) {
-            reinterpret_cast<uint4*>(base)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+            __stcs(reinterpret_cast<uint4*>(base) + i, make_uint4(o[0], o[1], o[2], o[3]));
         } else if (f32) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) reinterpret_cast<unsigned*>(base)[i * 4 + j] = o[j];
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(kClipThreads, kResident) clip_kernel(const vc_
             if (t.dst == nullptr || (scale == 1.0f && t.src == t.dst)) continue;
             const Cut c = cut_of(t);
             Held h;
-            load_tile(t, c, h);
+            load_tile<true>(t, c, h);
             store_tile(t, c, h, scale);
         }
     }
@@ -250,8 +257,10 @@ template <bool kMax>
 cudaError_t launch_clip(const vc_clip_tile_t* tiles, int ntiles, bool clip, float max_norm, float eps,
                         float* norm, double* parts, cudaStream_t st) {
     const int blocks = clip_blocks(ntiles);
+    // what the second-level cache can hold for the second kernel
+    const int again = clip ? (int)(kCacheBytes / kTileBytes / blocks) : 0;
     const cudaError_t e = launch_pdl(norm_kernel<kMax>, dim3(blocks), dim3(kClipThreads), st, tiles,
-                                     ntiles, parts);
+                                     ntiles, again, parts);
     if (e != cudaSuccess) return e;
     if (clip)
         return launch_pdl(clip_kernel<kMax, true>, dim3(blocks), dim3(kClipThreads), st, tiles, ntiles,

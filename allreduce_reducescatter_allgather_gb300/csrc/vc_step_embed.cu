@@ -7,12 +7,13 @@
 // Backward: dW_v (+)= s sum_{t: row(t) = v} dy_t in three launches, none of which
 // adds to memory that another block may add to:
 //
-//   sort   one cluster of blocks sorts (row, token) by row, keeping the tokens of a
-//          row in order: a radix sort of up to 9 bits a pass, whose ranks come from
-//          the lanes of a warp that share a digit, whose counts go through
-//          distributed shared memory.  It is bound by latency and needs few SMs; the
-//          other blocks of the same launch meanwhile write zeros to the rows that no
-//          token has (each marks the tokens of its own rows first).
+//   sort   one block (up to 4096 tokens) or one cluster of blocks sorts (row, token) by
+//          row, keeping the tokens of a row in order: a radix sort of up to 9 bits a
+//          pass, whose ranks come from the lanes of a warp that share a digit, and whose
+//          counts go through distributed shared memory in a cluster.  It is bound by
+//          latency and needs few SMs; the other blocks of the same launch meanwhile
+//          write zeros to the rows that no token has (each marks the tokens of its own
+//          rows first).
 //   sum    every warp takes a window of neighbours in the sorted order and 256
 //          columns: as many rows of dy to each, whatever the ids are.  Rows whose
 //          tokens all lie in the window are stored, the first and the last one,
@@ -99,6 +100,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kItems = 8;           // of a thread at a time
 constexpr int kChunk = kSortThreads * kItems;
+constexpr int kFewTokens = 4096;  // that one block sorts
 constexpr int kFillClusters = 15;   // beside the one that sorts: all that run at a time
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kMarkRows = 16384;    // rows that a block marks at a time
@@ -114,6 +116,7 @@ struct SortParams {
     char* out;
     long long row_bytes, pitch;
     int vec;                   // rows on 16 bytes
+    int fill, few;             // whether they are; one block sorts
 };
 
 __device__ __forceinline__ unsigned key_of(const SortParams& p, int t) {
@@ -135,45 +138,103 @@ __device__ __forceinline__ unsigned remote_load(const unsigned* at, int rank) {
     return v;
 }
 
+// Loops stay loops here: a launch runs each of them a few times only, and code that
+// has not run yet comes slowly (16 items unrolled took 7 us to the first sum).
 struct SortShared {
+    uint2 pair[kChunk];
+    unsigned short rank[kChunk];
     unsigned short count[kSortWarps][kBins];  // of a warp, then of the warps before
     unsigned chunk[kBins], total[kBins], base[kBins], scan[32];
 };
 
-// Ranks the chunk's items among those of their warp with the same digit, and leaves
-// the counts of the warps before each in count[][], the chunk's in chunk[].
-__device__ void rank_chunk(SortShared& s, const uint2 (&item)[kItems], int each, int begin, int end, int shift,
-                           unsigned mask, int (&rank)[kItems]) {
+// Ranks n items of the chunk, each of which has a place of 32 in a warp, among those of
+// their warp with the same digit; leaves the counts of the warps before each in
+// count[][], the chunk's in chunk[].
+__device__ __noinline__ void rank_chunk(SortShared& s, int items, int n, int shift, unsigned mask) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = lane; i < kBins / 2; i += 32) reinterpret_cast<unsigned*>(s.count[warp])[i] = 0;
+    for (int i = lane; i <= (int)mask / 2; i += 32) reinterpret_cast<unsigned*>(s.count[warp])[i] = 0;
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        if (k >= each) break;
-        const bool live = begin + (warp * each + k) * 32 + lane < end;
-        const unsigned digit = live ? (item[k].x >> shift) & mask : kBins;
-        const unsigned same = __match_any_sync(~0u, digit);
-        const int before = live ? s.count[warp][digit] : 0;
-        rank[k] = before + __popc(same & ((1u << lane) - 1));
+#pragma unroll 1
+    for (int k = 0; k < items; ++k) {
+        const int i = (warp * items + k) * 32 + lane;
+        const bool live = i < n;
+        const unsigned digit = live ? (s.pair[i].x >> shift) & mask : 0;
+        // the lanes with this digit, bit by bit (the instruction that finds them at once
+        // takes four times as long)
+        unsigned same = __ballot_sync(~0u, live);
+        for (unsigned bit = 1; bit <= mask; bit <<= 1) {
+            const unsigned with = __ballot_sync(~0u, digit & bit);
+            same &= digit & bit ? with : ~with;
+        }
+        const int before = s.count[warp][digit], ahead = __popc(same & ((1u << lane) - 1));
         __syncwarp();
-        if (live && (same & ((1u << lane) - 1)) == 0)
-            s.count[warp][digit] = (unsigned short)(before + __popc(same));
+        if (live) {
+            s.rank[i] = (unsigned short)(before + ahead);
+            if (ahead == 0) s.count[warp][digit] = (unsigned short)(before + __popc(same));
+        }
         __syncwarp();
     }
     __syncthreads();
     if (threadIdx.x <= mask) {
-        unsigned sum = 0;
-#pragma unroll 8
+        unsigned n[kSortWarps], sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) n[w] = s.count[w][threadIdx.x];
+#pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
-            const unsigned n = s.count[w][threadIdx.x];
             s.count[w][threadIdx.x] = (unsigned short)sum;
-            sum += n;
+            sum += n[w];
         }
         s.chunk[threadIdx.x] = sum;
     }
     __syncthreads();
 }
 
+// base[] <- the sum of `n` over the threads before, of the first mask + 1, plus `more`.
+__device__ __noinline__ void place_bins(SortShared& s, unsigned n, unsigned more, unsigned mask) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned m = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += m;
+    }
+    if (lane == 31) s.scan[warp] = sum;
+    __syncthreads();
+    const unsigned smaller = __reduce_add_sync(~0u, lane < warp ? s.scan[lane] : 0);
+    if (threadIdx.x <= mask) s.base[threadIdx.x] = smaller + sum - n + more;
+    __syncthreads();
+}
+
+// One block sorts up to a chunk of tokens without leaving its shared memory.
+__device__ void sort_few(const SortParams& p, SortShared& s, uint2* sorted) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int items = (p.tokens + kSortThreads - 1) / kSortThreads;
+    const unsigned mask = (1u << p.bits) - 1;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < p.tokens; i += kSortThreads) s.pair[i] = make_uint2(key_of(p, i), i);
+    __syncthreads();
+#pragma unroll 1
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.bits;
+        rank_chunk(s, items, p.tokens, shift, mask);
+        place_bins(s, threadIdx.x <= mask ? s.chunk[threadIdx.x] : 0, 0, mask);
+#pragma unroll 2
+        for (int k = 0; k < items; ++k) {
+            const int i = (warp * items + k) * 32 + lane;
+            if (i >= p.tokens) break;
+            const uint2 pair = s.pair[i];
+            const unsigned digit = (pair.x >> shift) & mask;
+            sorted[s.base[digit] + s.count[warp][digit] + s.rank[i]] = pair;
+        }
+        __syncthreads();
+        uint2* to = pass + 1 < p.passes ? s.pair : p.a;
+#pragma unroll 2
+        for (int i = threadIdx.x; i < p.tokens; i += kSortThreads) to[i] = sorted[i];
+        __syncthreads();
+    }
+}
+
+// A cluster sorts any number, each block a run of neighbours, chunk by chunk.
 __device__ void sort_tokens(const SortParams& p, SortShared& s) {
     const int me = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int each = (p.tokens + kCluster - 1) / kCluster;
@@ -182,30 +243,27 @@ __device__ void sort_tokens(const SortParams& p, SortShared& s) {
     const bool once = each <= kChunk;
     const int items = min(kItems, (each + kSortThreads - 1) / kSortThreads);  // of a thread
     const unsigned mask = (1u << p.bits) - 1;
+#pragma unroll 1
     for (int pass = 0; pass < p.passes; ++pass) {
         // the last pass writes a
         const bool into_a = ((p.passes - 1 - pass) & 1) == 0;
         const uint2* from = into_a ? p.b : p.a;
         uint2* to = into_a ? p.a : p.b;
         const int shift = pass * p.bits;
-        uint2 item[kItems];
-        int rank[kItems];
-        auto load = [&](int begin) {
-#pragma unroll
-            for (int k = 0; k < kItems; ++k) {
-                const int i = begin + (warp * items + k) * 32 + lane;
-                if (k >= items || i >= hi)
-                    item[k] = make_uint2(0, 0);
-                else
-                    item[k] = pass == 0 ? make_uint2(key_of(p, i), i) : __ldcg(from + i);
-            }
+        auto rank = [&](int begin) {
+            const int n = min(kChunk, hi - begin);
+            __syncthreads();  // (the last chunk is used up)
+#pragma unroll 4
+            for (int i = threadIdx.x; i < n; i += kSortThreads)
+                s.pair[i] = pass == 0 ? make_uint2(key_of(p, begin + i), begin + i) : __ldcg(from + begin + i);
+            __syncthreads();
+            rank_chunk(s, items, n, shift, mask);
         };
         if (threadIdx.x <= mask) s.total[threadIdx.x] = 0;
-        for (int begin = lo; begin < hi || (once && begin == lo); begin += kChunk) {
-            load(begin);
-            rank_chunk(s, item, items, begin, hi, shift, mask, rank);
+#pragma unroll 1
+        for (int begin = lo; begin < hi; begin += kChunk) {
+            rank(begin);
             if (threadIdx.x <= mask) s.total[threadIdx.x] += s.chunk[threadIdx.x];
-            if (once) break;
         }
         cluster_sync();
         // where each digit of this block starts: behind all smaller ones, and
@@ -219,29 +277,18 @@ __device__ void sort_tokens(const SortParams& p, SortShared& s) {
                 before += c < me ? n : 0;
             }
         }
-        unsigned sum = all;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned n = __shfl_up_sync(~0u, sum, o);
-            if (lane >= o) sum += n;
-        }
-        if (lane == 31) s.scan[warp] = sum;
-        __syncthreads();
-        unsigned smaller = 0;
-        for (int w = 0; w < kBins / 32; ++w) smaller += w < warp ? s.scan[w] : 0;
-        if (threadIdx.x <= mask) s.base[threadIdx.x] = smaller + sum - all + before;
-        __syncthreads();
+        place_bins(s, all, before, mask);
+#pragma unroll 1
         for (int begin = lo; begin < hi; begin += kChunk) {
-            if (!once) {
-                load(begin);
-                rank_chunk(s, item, items, begin, hi, shift, mask, rank);
-            }
-#pragma unroll
-            for (int k = 0; k < kItems; ++k) {
-                if (k >= items || begin + (warp * items + k) * 32 + lane >= hi) continue;
-                const unsigned digit = (item[k].x >> shift) & mask;
-                const unsigned at = s.base[digit] + s.count[warp][digit] + rank[k];
-                if (at < (unsigned)p.tokens) __stcg(to + at, item[k]);  // (ids that change meanwhile)
+            if (!once) rank(begin);
+#pragma unroll 2
+            for (int k = 0; k < items; ++k) {
+                const int i = (warp * items + k) * 32 + lane;
+                if (begin + i >= hi) break;
+                const uint2 pair = s.pair[i];
+                const unsigned digit = (pair.x >> shift) & mask;
+                const unsigned at = s.base[digit] + s.count[warp][digit] + s.rank[i];
+                if (at < (unsigned)p.tokens) __stcg(to + at, pair);  // (ids that change meanwhile)
             }
             if (!once) {
                 __syncthreads();
@@ -263,16 +310,10 @@ __device__ void fill_rows(const SortParams& p, unsigned* marks, int part, int pa
         const unsigned n = min(hi - at, (unsigned)kMarkRows);
         for (int i = threadIdx.x; i < kMarkRows / 32; i += kSortThreads) marks[i] = 0;
         __syncthreads();
-        for (int t0 = 0; t0 < p.tokens; t0 += kSortThreads * kItems) {
-            unsigned key[kItems];
-#pragma unroll
-            for (int k = 0; k < kItems; ++k) {
-                const int t = t0 + k * kSortThreads + threadIdx.x;
-                key[k] = t < p.tokens ? key_of(p, t) : p.rows;
-            }
-#pragma unroll
-            for (int k = 0; k < kItems; ++k)
-                if (key[k] - at < n) atomicOr(&marks[(key[k] - at) >> 5], 1u << ((key[k] - at) & 31));
+#pragma unroll 4
+        for (int t = threadIdx.x; t < p.tokens; t += kSortThreads) {
+            const unsigned i = key_of(p, t) - at;
+            if (i < n) atomicOr(&marks[i >> 5], 1u << (i & 31));
         }
         __syncthreads();
         for (unsigned i = warp; i < n; i += kSortWarps) {
@@ -282,7 +323,7 @@ __device__ void fill_rows(const SortParams& p, unsigned* marks, int part, int pa
             if (p.vec) {
                 done = p.row_bytes & ~15ll;
                 for (long long c = lane * 16; c < done; c += 512)
-                    *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+                    __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(0, 0, 0, 0));
             }
             for (long long c = done + lane * 2; c < p.row_bytes; c += 64)
                 *reinterpret_cast<unsigned short*>(row + c) = 0;
@@ -293,15 +334,21 @@ __device__ void fill_rows(const SortParams& p, unsigned* marks, int part, int pa
 
 __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kCluster, 1, 1)
     sort_kernel(const __grid_constant__ SortParams p) {
-    __shared__ SortShared s;
+    extern __shared__ uint4 shared[];
+    SortShared& s = *reinterpret_cast<SortShared*>(shared);
     pdl_next();
     pdl_wait();
-    if (blockIdx.x < kCluster)
+    const int sorters = p.few ? 1 : kCluster;
+    if (blockIdx.x >= sorters) {
+        if (p.fill) fill_rows(p, reinterpret_cast<unsigned*>(shared), blockIdx.x - sorters, gridDim.x - sorters);
+    } else if (p.few) {
+        sort_few(p, s, reinterpret_cast<uint2*>(&s + 1));
+    } else {
         sort_tokens(p, s);
-    else
-        fill_rows(p, reinterpret_cast<unsigned*>(&s), blockIdx.x - kCluster, gridDim.x - kCluster);
+    }
 }
 static_assert(sizeof(SortShared) >= kMarkRows / 8, "a block's marks fit");
+static_assert(kFewTokens <= kChunk && sizeof(SortShared) % 16 == 0, "pairs behind it are aligned");
 
 // ------------------------------------------------------------ sums by row --
 
@@ -318,21 +365,37 @@ struct SumParams {
     float scale;
 };
 
-// dW row (+)= scale * sum
+// dW row (+)= scale * sum.  What is added to 32-bit values is sent to memory, which
+// adds it once, and nobody waits for the old ones.
 template <bool kVec>
 __device__ __forceinline__ void finish_row(const SumParams& p, unsigned row, int slice, int lane, const Eight& sum) {
     Eight r = mul(p.scale, sum);
+    if (p.accumulate && p.dw.f32) {
+        float* to = static_cast<float*>(p.dw.data) + (long long)row * p.dw.ld;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = column<32>(kVec, slice, lane, j);
+            if (c < p.cols) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to + c), "f"(r.v[j]) : "memory");
+        }
+        return;
+    }
     if (p.accumulate) r = add(r, load_any<32>(p.dw, row, kVec, slice, lane, p.cols));
     store_any<32>(p.dw, p.dw.f32, row, kVec, slice, lane, p.cols, r);
 }
 
+// The rows of a window as one warp takes them: on 16 bytes through shared memory, where
+// each lane's own columns of kAhead rows are on their way; others by fours through
+// registers.
+constexpr int kAhead = 8;
+
 template <int kWindow, bool kVec, bool kF32>
 __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_constant__ SumParams p) {
-    constexpr int kBatch = kVec && !kF32 ? 8 : 4;  // rows in flight
+    constexpr int kBatch = 4, kWords = kF32 ? 2 : 1;
+    __shared__ uint4 ring[kSumWarps][kVec ? kAhead : 1][kVec ? kWords : 1][32];
     pdl_next();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long unit = (long long)blockIdx.x * kSumWarps + __shfl_sync(~0u, threadIdx.x / 32, 0);
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x / 32, 0);
+    const long long unit = (long long)blockIdx.x * kSumWarps + warp;
     const int window = (int)(unit / p.slices), slice = (int)(unit - (long long)window * p.slices);
     if (window >= p.windows) return;
     const int begin = window * kWindow;
@@ -345,42 +408,81 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_consta
     }
     const unsigned before = begin > 0 ? p.sorted[begin - 1].x : p.rows;
     const unsigned after = p.tokens - begin > kWindow ? p.sorted[begin + kWindow].x : p.rows;
+    auto key_at = [&](int j) { return __shfl_sync(~0u, kWindow > 32 && j >= 32 ? mine[(kWindow - 1) / 32].x : mine[0].x, j & 31); };
+    auto token_at = [&](int j) { return __shfl_sync(~0u, kWindow > 32 && j >= 32 ? mine[(kWindow - 1) / 32].y : mine[0].y, j & 31); };
     Eight sum = zeros();
-    unsigned row = __shfl_sync(~0u, mine[0].x, 0);
+    unsigned row = key_at(0);
     bool first = true;
     const Rows parts = {p.parts, p.padded, 1, 1};
     auto flush = [&](bool end) {
-        if (row >= p.rows) return;
         const bool from = first && row == before, on = end && row == after;
         if (from || on)
             store_any<32>(parts, true, (long long)window * 2 + (from ? 0 : 1), kVec, slice, lane, p.cols, sum);
         else
             finish_row<kVec>(p, row, slice, lane, sum);
     };
-#pragma unroll 1
-    for (int b = 0; b < kWindow; b += kBatch) {
-        Raw v[kBatch];
-        unsigned key[kBatch];
-        const uint2 from = kWindow > 32 && b >= 32 ? mine[(kWindow + 31) / 32 - 1] : mine[0];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            key[i] = __shfl_sync(~0u, from.x, (b + i) & 31);
-            const unsigned token = __shfl_sync(~0u, from.y, (b + i) & 31);
-            if (key[i] < p.rows) v[i] = load_raw<32>(p.dy, kF32, token, kVec, slice, lane, p.cols);
+    // the next token's row; false behind the last one (the tokens that are left out come last)
+    auto next = [&](unsigned key) {
+        if (key != row) {
+            flush(false);
+            first = false;
+            row = key;
+            sum = zeros();
         }
-        if (key[0] >= p.rows) break;  // (the tokens that are left out come last)
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (key[i] != row) {
-                flush(false);
-                first = false;
-                row = key[i];
-                sum = zeros();
+        return row < p.rows;
+    };
+    if (row >= p.rows) return;
+    if constexpr (kVec) {
+        const int c = (slice * 32 + lane) * 8, left = p.cols - c;
+        const int bytes = max(0, min(16, left * (kF32 ? 4 : 2))), more = max(0, min(16, left * 4 - 16));
+        const char* const base = static_cast<const char*>(p.dy.data) + (left > 0 ? (long long)c * (kF32 ? 4 : 2) : 0);
+        const long long pitch = p.dy.ld * (kF32 ? 4 : 2);
+        auto issue = [&](int j) {
+            if (j < kWindow && key_at(j) < p.rows) {
+                const char* from = base + token_at(j) * pitch;
+                uint4* to = &ring[warp][j % kAhead][0][lane];
+                copy16(to, from, bytes);
+                if constexpr (kF32) copy16(to + 32, from + (more ? 16 : 0), more);
             }
-            if (row < p.rows) sum = add(sum, widen_raw(v[i], kF32, kVec));
+            copies_end();
+        };
+#pragma unroll 1
+        for (int j = 0; j < kAhead; ++j) issue(j);
+#pragma unroll 1
+        for (int j = 0; j < kWindow; ++j) {
+            copies_wait<kAhead - 1>();
+            if (!next(key_at(j))) break;
+            const uint4(*at)[32] = ring[warp][j % kAhead];
+            if constexpr (kF32) {
+                const uint4 lo = at[0][lane], hi = at[kWords - 1][lane];
+                sum = add(sum, {{__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z),
+                                 __uint_as_float(lo.w), __uint_as_float(hi.x), __uint_as_float(hi.y),
+                                 __uint_as_float(hi.z), __uint_as_float(hi.w)}});
+            } else {
+                sum = add(sum, widen(at[0][lane]));
+            }
+            issue(j + kAhead);
+        }
+        copies_wait<0>();
+    } else {
+#pragma unroll 1
+        for (int b = 0; b < kWindow; b += kBatch) {
+            Raw v[kBatch];
+            unsigned key[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                key[i] = key_at(b + i);
+                const unsigned token = token_at(b + i);
+                if (key[i] < p.rows) v[i] = load_raw<32>(p.dy, kF32, token, kVec, slice, lane, p.cols);
+            }
+            bool more = true;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (more && (more = next(key[i]))) sum = add(sum, widen_raw(v[i], kF32, kVec));
+            if (!more) break;
         }
     }
-    flush(true);
+    if (row < p.rows) flush(true);
 }
 
 // A row that starts in one window and goes on into others: its last partial sum
@@ -413,7 +515,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const float* at = p.parts + ((long long)start * 2 + 1) * p.padded + c;
     float4 sum = *reinterpret_cast<const float4*>(at);
     at += p.padded;  // (the next window's first row)
-#pragma unroll 8
+#pragma unroll 16
     for (int u = start + 1; u < ends; ++u, at += 2 * p.padded) {
         const float4 v = *reinterpret_cast<const float4*>(at);
         sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
@@ -433,12 +535,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     }
 }
 
-// Tokens of a window: as many as leave a window for each of 12 warps an SM, each
-// of which has 4 KiB of rows in flight.
+// Tokens of a window: as many as leave a window for each of 12 warps an SM (each has
+// 4 KiB of rows in flight), or 512 windows: more would lengthen the joins of frequent
+// rows, whose windows are added one after the other.
 int window_of(long long tokens, long long cols) {
     const long long slices = (cols + kSlice - 1) / kSlice;
     int w = 64;
-    while (w > 8 && (tokens + w - 1) / w * slices < kSMs * 12) w /= 2;
+    while (w > 8 && (tokens + w - 1) / w < 512 && (tokens + w - 1) / w * slices < kSMs * 12) w /= 2;
     return w;
 }
 
@@ -586,8 +689,11 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
     s.pitch = dw.ld * es;
     s.vec = dw.vec;
     // blocks for the zeros: those of the clusters that fit beside the sorting one
+    s.few = tokens <= kFewTokens;
+    s.fill = !accumulate;
     const int fill = accumulate ? 0 : (int)std::min((long long)kFillClusters, (V + 31) / 32) * kCluster;
-    cudaError_t e = launch_pdl(sort_kernel, dim3(kCluster + fill), dim3(kSortThreads), st, s);
+    const size_t shared = sizeof(SortShared) + (s.few ? kFewTokens * sizeof(uint2) : 0);
+    cudaError_t e = launch_pdl_shared(sort_kernel, dim3(kCluster + fill), dim3(kSortThreads), shared, st, s);
     if (e != cudaSuccess) return VC_ERR_CUDA;
     if (tokens == 0) return VC_SUCCESS;
 

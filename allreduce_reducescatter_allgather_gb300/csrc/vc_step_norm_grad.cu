@@ -57,10 +57,10 @@ constexpr bool kThroughShared = kVec && !(kLayer && kVecs == 2 && kTeam > 32);
 
 // Weights and the gate of the rows at hand are held in shared memory where there is room.
 template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
-constexpr bool kHolds = kThroughShared<kTeam, kVecs, kLayer, kVec> && !(kTeam == 512 && kVecs == 2 && kStream32);
+constexpr bool kHolds = kTeam == 32 || kVecs == 1 || (kThroughShared<kTeam, kVecs, kLayer, kVec> && !kStream32);
 
 template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
-__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam == 32 ? 2 / kVecs : 512 / kTeam)
+__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam == 32 ? 2 / kVecs : 512 / kTeam) * (kLayer && !kVec && kVecs == 1 ? 3 : 4) / 4)
     backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kBackwardThreads : kTeam, kTeams = kThreads / kTeam;
     // RMS norms have no biases
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
     in.array(kDr, has_dr, kStream32);
     in.array(kG, full_gate, p.gate.f32);
     using Vector = Held<kTeam, kVecs, kVec, kHolds<kTeam, kVecs, kLayer, kStream32, kVec>>;
-    float4* const held = reinterpret_cast<float4*>(ring + kStages * in.words * kThreads) + lane;
+    float4* const held = reinterpret_cast<float4*>(ring + (kRing ? kStages * in.words * kThreads : 0)) + lane;
     const Vector pre = {held}, post = {held + Vector::kBytes / 16}, shift = {held + 2 * (Vector::kBytes / 16)},
                  held_gate = {held + ((kLayer ? 3 : 2) + part) * (Vector::kBytes / 16)};  // (a team's own)
     auto load = [&](long long row) {
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
         rstd = rsqrtf(fmaf(rstd, p.inv_cols, p.eps));
         h_rstd = rsqrtf(fmaf(h_rstd, p.inv_cols, p.eps));
         m2 *= p.inv_cols * rstd * rstd;
-        Eight du[kVecs], hat[kVecs];
+        Eight du[kVecs], kept_hat[kRing ? 1 : kVecs];
         float2 t1 = make_float2(0.0f, 0.0f), t2 = t1;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
@@ -229,12 +229,13 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
             }
             if (p.dx.data != nullptr)
                 store_any<kTeam>(p.dx, kStream32, row, kVec, i, lane, p.cols, mul(p.scale, dr));
-            Eight w;
-            if (has_h) hat[i] = centered_h(i);
+            Eight w, hat;
+            if (has_h) hat = centered_h(i);
             if (has_post) {
                 w = post.get(p.post.weight, i, lane, p.cols);
-                hat[i] = mul(h_rstd, hat[i]);
+                hat = mul(h_rstd, hat);
             }
+            if constexpr (!kRing) kept_hat[i] = hat;
             du[i] = dr;
             if (p.gate_mode != kGateNone) {
                 Eight gate, value;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
                     value = held_gate.get(p.gate, i, lane, p.cols);
                 }
                 if (p.dgate.data != nullptr) {
-                    Eight u = hat[i];
+                    Eight u = hat;
                     if (has_post) {
                         u = mul(u, w);
                         if (kLayer && p.post.bias.data != nullptr)
@@ -259,10 +260,10 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
                 du[i] = mul(dr, value);
             }
             if (has_post) {
-                add_product(kPost, i, du[i], hat[i]);
+                add_product(kPost, i, du[i], hat);
                 if constexpr (kLayer) add_product(kPostBias, i, du[i], ones);
                 du[i] = mul(du[i], w);
-                dot(t1, du[i], hat[i]);
+                dot(t1, du[i], hat);
                 if constexpr (kLayer) total(t2, du[i]);
             }
         }
@@ -296,7 +297,8 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, kTeam 
             h_m1 *= p.inv_cols * h_rstd;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                du[i] = fma(-h_m2, hat[i], mul(h_rstd, du[i]));
+                const Eight hat = kRing ? mul(h_rstd, centered_h(i)) : kept_hat[kRing ? 0 : i];
+                du[i] = fma(-h_m2, hat, mul(h_rstd, du[i]));
                 if constexpr (kLayer) du[i] = add(-h_m1, du[i]);
             }
         }
@@ -578,8 +580,8 @@ Split split_of(long long rows, long long cols) {
     const int team = s.shape.team == 0 ? kLong : s.shape.team;
     s.threads = team == 32 ? kBackwardThreads : team;
     const int per = s.threads / team;
-    // four rows a team at least, so that the parts stay few beside the rows
-    const long long want = (rows + 4 * per - 1) / (4 * per);
+    // two rows a team at least, so that the parts stay few beside the rows
+    const long long want = (rows + 2 * per - 1) / (2 * per);
     s.blocks = (int)std::max(1ll, std::min(want, (long long)kSMs * (team == 32 ? 2 / s.shape.vecs : std::max(1, 512 / s.threads))));
     s.teams = (int)std::min(rows, (long long)s.blocks * per);  // (the others have no rows)
     s.padded = (cols + 7) / 8 * 8;
@@ -598,7 +600,7 @@ cudaError_t launch_backward(const NormParams& p, const Split& s, cudaStream_t st
     else if (s.shape.team > 32 && s.shape.vecs == 2)
         bytes = (size_t)(kLayer ? 5 : 3) * s.shape.team * s.shape.vecs * 32;
     // weights and gate that are held beside it
-    if (s.shape.team != 0 && ring && !(s.shape.team == 512 && s.shape.vecs == 2 && kStream32))
+    if (s.shape.team == 32 || s.shape.vecs == 1 || (s.shape.team != 0 && ring && !kStream32))
         bytes += (size_t)((kLayer ? 3 : 2) * s.shape.team +
                           (p.gate_mode == kGateShared || p.gate_mode == kGateGroups ? s.threads : 0)) *
                  s.shape.vecs * 32;
