@@ -12,9 +12,10 @@
 //          pass, whose ranks come from the lanes of a warp that share a digit, and whose
 //          counts go through distributed shared memory in a cluster.  It is bound by
 //          latency and needs few SMs; the other blocks of the same launch meanwhile
-//          write zeros to the rows that no token has (each marks the tokens of its own
-//          rows first).
-//   sum    every warp takes a window of neighbours in the sorted order and 256
+//          mark the rows that tokens have, and write zeros to as many of the others
+//          as they have time for.
+//   sum    writes zeros to the rest of those, in blocks among the summing ones: writes
+//          alone reach 4.0 TB/s, together with reads 6.8.  Every summing warp takes a window of neighbours in the sorted order and 256
 //          columns: as many rows of dy to each, whatever the ids are.  Rows whose
 //          tokens all lie in the window are stored, the first and the last one,
 //          where they go on beyond it, left as partial sums.
@@ -105,6 +106,23 @@ constexpr int kFillClusters = 15;   // beside the one that sorts: all that run a
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kMarkRows = 16384;    // rows that a block marks at a time
 
+// Rows to be set to zero.
+struct ZeroRows {
+    char* out;
+    long long row_bytes, pitch;
+    int vec;  // rows on 16 bytes
+};
+__device__ __forceinline__ void zero_row(const ZeroRows& z, unsigned row, int lane) {
+    char* at = z.out + (long long)row * z.pitch;
+    long long done = 0;
+    if (z.vec) {
+        done = z.row_bytes & ~15ll;
+        for (long long c = lane * 16; c < done; c += 512)
+            __stcs(reinterpret_cast<uint4*>(at + c), make_uint4(0, 0, 0, 0));
+    }
+    for (long long c = done + lane * 2; c < z.row_bytes; c += 64) *reinterpret_cast<unsigned short*>(at + c) = 0;
+}
+
 struct SortParams {
     const void* ids;
     int wide;
@@ -112,11 +130,12 @@ struct SortParams {
     unsigned rows;             // also the key of tokens that are left out
     int tokens, passes, bits;  // bits of a pass
     uint2 *a, *b;              // (row, token); the last pass writes a
-    // the rows that no token has are set to zero, by the blocks that do not sort
-    char* out;
-    long long row_bytes, pitch;
-    int vec;                   // rows on 16 bytes
-    int fill, few;             // whether they are; one block sorts
+    // the rows that no token has: below `split` the blocks that do not sort set them to
+    // zero, from there on they leave marks
+    ZeroRows zero;
+    unsigned split;
+    unsigned* marks;           // a bit a row from split on: a token has it
+    int fill, few;             // whether there is any of that; one block sorts
 };
 
 __device__ __forceinline__ unsigned key_of(const SortParams& p, int t) {
@@ -301,34 +320,33 @@ __device__ void sort_tokens(const SortParams& p, SortShared& s) {
     }
 }
 
-// Zeros to those of this block's rows that no token has.
-__device__ void fill_rows(const SortParams& p, unsigned* marks, int part, int parts) {
-    const unsigned lo = (unsigned)((unsigned long long)p.rows * part / parts);
-    const unsigned hi = (unsigned)((unsigned long long)p.rows * (part + 1) / parts);
+// This block's share of the rows below split, which it sets to zero where no token has
+// them, and of the others, which it marks.  One pass over the ids for both.
+__device__ void clear_rows(const SortParams& p, unsigned* marks, int part, int parts) {
+    const unsigned behind = p.rows - p.split, words = (behind + 31) / 32;
+    unsigned a = (unsigned)((unsigned long long)p.split * part / parts);
+    const unsigned a_end = (unsigned)((unsigned long long)p.split * (part + 1) / parts);
+    unsigned b = (unsigned)((unsigned long long)words * part / parts) * 32;
+    const unsigned b_end = min(behind, (unsigned)((unsigned long long)words * (part + 1) / parts) * 32);
+    unsigned* const marks_b = marks + kMarkRows / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (unsigned at = lo; at < hi; at += kMarkRows) {
-        const unsigned n = min(hi - at, (unsigned)kMarkRows);
-        for (int i = threadIdx.x; i < kMarkRows / 32; i += kSortThreads) marks[i] = 0;
+    while (a < a_end || b < b_end) {
+        const unsigned na = min(a_end - a, (unsigned)kMarkRows), nb = b < b_end ? min(b_end - b, (unsigned)kMarkRows) : 0;
+        for (int i = threadIdx.x; i < 2 * kMarkRows / 32; i += kSortThreads) marks[i] = 0;
         __syncthreads();
 #pragma unroll 4
         for (int t = threadIdx.x; t < p.tokens; t += kSortThreads) {
-            const unsigned i = key_of(p, t) - at;
-            if (i < n) atomicOr(&marks[i >> 5], 1u << (i & 31));
+            const unsigned key = key_of(p, t), i = key - a, j = key - p.split - b;
+            if (i < na) atomicOr(&marks[i >> 5], 1u << (i & 31));
+            if (j < nb) atomicOr(&marks_b[j >> 5], 1u << (j & 31));
         }
         __syncthreads();
-        for (unsigned i = warp; i < n; i += kSortWarps) {
-            if (marks[i >> 5] >> (i & 31) & 1) continue;
-            char* row = p.out + (long long)(at + i) * p.pitch;
-            long long done = 0;
-            if (p.vec) {
-                done = p.row_bytes & ~15ll;
-                for (long long c = lane * 16; c < done; c += 512)
-                    __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(0, 0, 0, 0));
-            }
-            for (long long c = done + lane * 2; c < p.row_bytes; c += 64)
-                *reinterpret_cast<unsigned short*>(row + c) = 0;
-        }
+        for (unsigned i = threadIdx.x; i < (nb + 31) / 32; i += kSortThreads) p.marks[b / 32 + i] = marks_b[i];
+        for (unsigned i = warp; i < na; i += kSortWarps)
+            if (!(marks[i >> 5] >> (i & 31) & 1)) zero_row(p.zero, a + i, lane);
         __syncthreads();
+        a += na;
+        b += nb;
     }
 }
 
@@ -340,14 +358,14 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kCluster, 1,
     pdl_wait();
     const int sorters = p.few ? 1 : kCluster;
     if (blockIdx.x >= sorters) {
-        if (p.fill) fill_rows(p, reinterpret_cast<unsigned*>(shared), blockIdx.x - sorters, gridDim.x - sorters);
+        if (p.fill) clear_rows(p, reinterpret_cast<unsigned*>(shared), blockIdx.x - sorters, gridDim.x - sorters);
     } else if (p.few) {
         sort_few(p, s, reinterpret_cast<uint2*>(&s + 1));
     } else {
         sort_tokens(p, s);
     }
 }
-static_assert(sizeof(SortShared) >= kMarkRows / 8, "a block's marks fit");
+static_assert(sizeof(SortShared) >= 2 * kMarkRows / 8, "a block's marks fit");
 static_assert(kFewTokens <= kChunk && sizeof(SortShared) % 16 == 0, "pairs behind it are aligned");
 
 // ------------------------------------------------------------ sums by row --
@@ -363,7 +381,20 @@ struct SumParams {
     unsigned rows;
     int tokens, windows, slices, cols, accumulate;
     float scale;
+    // rows from split on whose mark is not set become zero
+    ZeroRows zero;
+    const unsigned* marks;
+    unsigned split;
+    int zero_rows;                       // of a block
+    unsigned zero_blocks, sum_blocks;    // of the launch
 };
+
+__device__ __forceinline__ void zero_unmarked(const SumParams& p, unsigned block) {
+    const unsigned first = block * p.zero_rows, behind = p.rows - p.split;
+    const int lane = threadIdx.x & 31;
+    for (unsigned i = first + threadIdx.x / 32; i < min(behind, first + p.zero_rows); i += kSumWarps)
+        if (!(p.marks[i >> 5] >> (i & 31) & 1)) zero_row(p.zero, p.split + i, lane);
+}
 
 // dW row (+)= scale * sum.  What is added to 32-bit values is sent to memory, which
 // adds it once, and nobody waits for the old ones.
@@ -394,8 +425,12 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_consta
     __shared__ uint4 ring[kSumWarps][kVec ? kAhead : 1][kVec ? kWords : 1][32];
     pdl_next();
     pdl_wait();
+    // the zeroing blocks lie evenly among the others
+    const unsigned zeroing = (unsigned)((unsigned long long)blockIdx.x * p.zero_blocks / gridDim.x);
+    if ((unsigned)((unsigned long long)(blockIdx.x + 1) * p.zero_blocks / gridDim.x) != zeroing)
+        return zero_unmarked(p, zeroing);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x / 32, 0);
-    const long long unit = (long long)blockIdx.x * kSumWarps + warp;
+    const long long unit = (long long)(blockIdx.x - zeroing) * kSumWarps + warp;
     const int window = (int)(unit / p.slices), slice = (int)(unit - (long long)window * p.slices);
     if (window >= p.windows) return;
     const int begin = window * kWindow;
@@ -498,10 +533,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const int start = (int)(unit / chunks);
     if (start + 1 >= p.windows) return;
     auto key = [&](int window, int i) { return p.sorted[(long long)window * kWindow + i].x; };
-    const unsigned row = key(start, kWindow - 1);
-    if (row >= p.rows || key(start + 1, 0) != row) return;
-    if (start > 0 && key(start, 0) == row && key(start - 1, kWindow - 1) == row) return;
-    int ends = start + 2;  // the first window behind that the row does not reach
+    const unsigned row = key(start, kWindow - 1), front = key(start, 0);
+    const unsigned back = start > 0 ? key(start - 1, kWindow - 1) : p.rows;
+    int ends = start + 1;  // the first window behind that the row does not reach
     for (;; ends += 32) {
         const int u = ends + lane;
         const unsigned other = __ballot_sync(~0u, u >= p.windows || key(u, 0) != row);
@@ -510,6 +544,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
             break;
         }
     }
+    if (row >= p.rows || ends == start + 1 || (front == row && back == row)) return;
     const int c = (int)(unit - (long long)start * chunks) * kJoinColumns + lane * 4;
     if (c >= p.cols) return;
     const float* at = p.parts + ((long long)start * 2 + 1) * p.padded + c;
@@ -535,39 +570,39 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     }
 }
 
-// Tokens of a window: as many as leave a window for each of 12 warps an SM (each has
-// 4 KiB of rows in flight), or 512 windows: more would lengthen the joins of frequent
-// rows, whose windows are added one after the other.
+// Tokens of a window: as many as leave a window for each of 24 warps an SM, or 1024
+// windows: more would lengthen the joins of frequent rows, whose windows are added
+// one after the other.
 int window_of(long long tokens, long long cols) {
     const long long slices = (cols + kSlice - 1) / kSlice;
     int w = 64;
-    while (w > 8 && (tokens + w - 1) / w < 512 && (tokens + w - 1) / w * slices < kSMs * 12) w /= 2;
+    while (w > 8 && (tokens + w - 1) / w < 1024 && (tokens + w - 1) / w * slices < kSMs * 24) w /= 2;
     return w;
 }
 
 constexpr long long kMaxTokens = train::kMaxExtent;  // (sums with a block's share fit ints)
 
 struct BackwardSpace {
-    size_t pairs, parts;
+    size_t pairs, parts, marks;
     int window;
     long long windows, slices;
 };
-BackwardSpace space_of(long long tokens, long long cols) {
+BackwardSpace space_of(long long tokens, long long rows, long long cols) {
     BackwardSpace s = {};
     s.window = window_of(tokens, cols);
     s.windows = (tokens + s.window - 1) / s.window;
     s.slices = (cols + kSlice - 1) / kSlice;
     s.pairs = round256((size_t)tokens * sizeof(uint2));
-    s.parts = (size_t)s.windows * 2 * s.slices * kSlice * 4;
+    s.parts = round256((size_t)s.windows * 2 * s.slices * kSlice * 4);
+    s.marks = round256((size_t)(rows + 31) / 32 * 4);
     return s;
 }
 
 template <int kWindow, bool kVec>
 cudaError_t launch_sums(const SumParams& p, cudaStream_t st) {
-    const long long units = (long long)p.windows * p.slices;
     const long long joins = (long long)p.windows * ((p.cols + kJoinColumns - 1) / kJoinColumns);
     cudaError_t e = launch_pdl(p.dy.f32 ? sum_kernel<kWindow, kVec, true> : sum_kernel<kWindow, kVec, false>,
-                               dim3((unsigned)((units + kSumWarps - 1) / kSumWarps)), dim3(kSumWarps * 32), st, p);
+                               dim3(p.sum_blocks + p.zero_blocks), dim3(kSumWarps * 32), st, p);
     if (e != cudaSuccess || p.windows == 1) return e;
     return launch_pdl(join_kernel<kWindow, kVec>, dim3((unsigned)((joins + kJoinWarps - 1) / kJoinWarps)),
                       dim3(kJoinWarps * 32), st, p);
@@ -640,8 +675,8 @@ size_t vc_embedding_backward_workspace(long long tokens, long long rows, long lo
         cols > train::kMaxExtent)
         return 0;
     if (tokens == 0 || rows == 0 || cols == 0) return 0;
-    const BackwardSpace s = space_of(tokens, cols);
-    return 2 * s.pairs + round256(s.parts);
+    const BackwardSpace s = space_of(tokens, rows, cols);
+    return 2 * s.pairs + s.parts + s.marks;
 }
 
 vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dtype_t id_dtype,
@@ -662,9 +697,9 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
             if (overlap(o, i)) return VC_ERR_ALIAS;
     if (overlap(outs[0], outs[1])) return VC_ERR_ALIAS;
     if (V == 0 || D == 0 || (tokens == 0 && accumulate)) return VC_SUCCESS;
-    const BackwardSpace sp = space_of(tokens, D);
-    if (sp.windows * sp.slices > 0x7FFFFFFFll * kSumWarps || sp.slices > 0x7FFFFFFF)
-        return VC_ERR_INVALID_ARGUMENT;
+    const BackwardSpace sp = space_of(tokens, V, D);
+    const long long sum_blocks = (sp.windows * sp.slices + kSumWarps - 1) / kSumWarps;
+    if (sum_blocks > 1ll << 30) return VC_ERR_INVALID_ARGUMENT;
     if (test_launch_failure()) return VC_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -684,10 +719,12 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
     s.b = reinterpret_cast<uint2*>(ws + sp.pairs);
     const Rows dw = rows_of(dweight);
     const int es = elem_size(dweight->dtype);
-    s.out = static_cast<char*>(dw.data);
-    s.row_bytes = D * es;
-    s.pitch = dw.ld * es;
-    s.vec = dw.vec;
+    s.zero = {static_cast<char*>(dw.data), D * es, dw.ld * es, dw.vec};
+    // what can be zeroed while the tokens are sorted (13 us for 16384 of them, 28 us for
+    // 65536), at 4 TB/s
+    const long long early = tokens == 0 ? V : ((8ll << 20) + 1200 * tokens) / (D * es);
+    s.split = (unsigned)std::min(V, early);
+    s.marks = reinterpret_cast<unsigned*>(ws + 2 * sp.pairs + sp.parts);
     // blocks for the zeros: those of the clusters that fit beside the sorting one
     s.few = tokens <= kFewTokens;
     s.fill = !accumulate;
@@ -710,6 +747,15 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
     p.cols = (int)D;
     p.accumulate = accumulate != 0;
     p.scale = scale;
+    p.sum_blocks = (unsigned)sum_blocks;
+    if (!accumulate && s.split < s.rows) {
+        // 64 KiB a block
+        p.zero = s.zero;
+        p.marks = s.marks;
+        p.split = s.split;
+        p.zero_rows = (int)std::max(4ll, std::min(32ll, (64ll << 10) / (D * es)));
+        p.zero_blocks = (s.rows - s.split + p.zero_rows - 1) / p.zero_rows;
+    }
     e = p.dy.vec && p.dw.vec ? launch_sums<true>(p, sp.window, st) : launch_sums<false>(p, sp.window, st);
     return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
 }

@@ -185,7 +185,8 @@ struct TeamSums {
             __syncthreads();
             const int q = lane % kP, w = lane / kP;
             c = w < kWarps ? buf[w][q] : 0.0f;
-            if constexpr (kWarps > 32 / kP) c += buf[w + 32 / kP][q];
+#pragma unroll
+            for (int more = 32 / kP; more < kWarps; more += 32 / kP) c += buf[w + more][q];
 #pragma unroll
             for (int o = 16; o >= kP; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
 #pragma unroll
