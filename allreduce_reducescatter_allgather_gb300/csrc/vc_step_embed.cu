@@ -370,7 +370,9 @@ static_assert(kFewTokens <= kChunk && sizeof(SortShared) % 16 == 0, "pairs behin
 
 // ------------------------------------------------------------ sums by row --
 
-constexpr int kSlice = 256;  // columns of a warp
+// Columns of a warp, a vector a lane.  (Two vectors a lane halve the warps that wait
+// for one token after the other: 14.4 -> 19.6 us for 16384 x 1024.)
+constexpr int kVectors = 1, kSlice = 256 * kVectors;
 constexpr int kSumWarps = 4;
 
 struct SumParams {
@@ -396,33 +398,31 @@ __device__ __forceinline__ void zero_unmarked(const SumParams& p, unsigned block
         if (!(p.marks[i >> 5] >> (i & 31) & 1)) zero_row(p.zero, p.split + i, lane);
 }
 
-// dW row (+)= scale * sum.  What is added to 32-bit values is sent to memory, which
-// adds it once, and nobody waits for the old ones.
+// dW row (+)= scale * sum, vector v.  What is added to 32-bit values is sent to memory,
+// which adds it once, and nobody waits for the old ones.
 template <bool kVec>
-__device__ __forceinline__ void finish_row(const SumParams& p, unsigned row, int slice, int lane, const Eight& sum) {
+__device__ __forceinline__ void finish_row(const SumParams& p, unsigned row, int v, int lane, const Eight& sum) {
     Eight r = mul(p.scale, sum);
     if (p.accumulate && p.dw.f32) {
         float* to = static_cast<float*>(p.dw.data) + (long long)row * p.dw.ld;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = column<32>(kVec, slice, lane, j);
+            const int c = column<32>(kVec, v, lane, j);
             if (c < p.cols) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to + c), "f"(r.v[j]) : "memory");
         }
         return;
     }
-    if (p.accumulate) r = add(r, load_any<32>(p.dw, row, kVec, slice, lane, p.cols));
-    store_any<32>(p.dw, p.dw.f32, row, kVec, slice, lane, p.cols, r);
+    if (p.accumulate) r = add(r, load_any<32>(p.dw, row, kVec, v, lane, p.cols));
+    store_any<32>(p.dw, p.dw.f32, row, kVec, v, lane, p.cols, r);
 }
 
 // The rows of a window as one warp takes them: on 16 bytes through shared memory, where
-// each lane's own columns of kAhead rows are on their way; others by fours through
+// each lane's own columns of the next rows are on their way; others by fours through
 // registers.
-constexpr int kAhead = 8;
-
 template <int kWindow, bool kVec, bool kF32>
 __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_constant__ SumParams p) {
-    constexpr int kBatch = 4, kWords = kF32 ? 2 : 1;
-    __shared__ uint4 ring[kSumWarps][kVec ? kAhead : 1][kVec ? kWords : 1][32];
+    constexpr int kWords = kF32 ? 2 : 1, kAhead = 8 / kWords, kBatch = 4, kPairs = (kWindow + 31) / 32;
+    __shared__ uint4 ring[kSumWarps][kVec ? kAhead : 1][kVec ? kVectors * kWords : 1][32];
     pdl_next();
     pdl_wait();
     // the zeroing blocks lie evenly among the others
@@ -434,90 +434,120 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_consta
     const int window = (int)(unit / p.slices), slice = (int)(unit - (long long)window * p.slices);
     if (window >= p.windows) return;
     const int begin = window * kWindow;
-    const uint2 none = make_uint2(p.rows, 0);
-    uint2 mine[(kWindow + 31) / 32];
+    uint2 mine[kPairs];
 #pragma unroll
-    for (int i = 0; i < (kWindow + 31) / 32; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
         const int t = begin + i * 32 + lane;
-        mine[i] = i * 32 + lane < kWindow && t < p.tokens ? p.sorted[t] : none;
+        mine[i] = i * 32 + lane < kWindow && t < p.tokens ? p.sorted[t] : make_uint2(p.rows, 0);
     }
     const unsigned before = begin > 0 ? p.sorted[begin - 1].x : p.rows;
     const unsigned after = p.tokens - begin > kWindow ? p.sorted[begin + kWindow].x : p.rows;
-    auto key_at = [&](int j) { return __shfl_sync(~0u, kWindow > 32 && j >= 32 ? mine[(kWindow - 1) / 32].x : mine[0].x, j & 31); };
-    auto token_at = [&](int j) { return __shfl_sync(~0u, kWindow > 32 && j >= 32 ? mine[(kWindow - 1) / 32].y : mine[0].y, j & 31); };
-    Eight sum = zeros();
+    auto key_at = [&](int j) { return __shfl_sync(~0u, kPairs > 1 && j >= 32 ? mine[kPairs - 1].x : mine[0].x, j & 31); };
+    auto token_at = [&](int j) { return __shfl_sync(~0u, kPairs > 1 && j >= 32 ? mine[kPairs - 1].y : mine[0].y, j & 31); };
+    // how many tokens there are (those that are left out come last), and which ones
+    // start a row
+    int live = 0;
+    unsigned starts[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        live += __popc(__ballot_sync(~0u, mine[i].x < p.rows));
+        unsigned last = __shfl_up_sync(~0u, mine[i].x, 1);
+        const unsigned other = __shfl_sync(~0u, mine[0].x, i == 0 ? 0 : 31);
+        if (lane == 0) last = other;
+        starts[i] = __ballot_sync(~0u, mine[i].x != last);
+    }
+    if (live == 0) return;
+    Eight sum[kVectors];
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) sum[i] = zeros();
     unsigned row = key_at(0);
     bool first = true;
     const Rows parts = {p.parts, p.padded, 1, 1};
     auto flush = [&](bool end) {
         const bool from = first && row == before, on = end && row == after;
-        if (from || on)
-            store_any<32>(parts, true, (long long)window * 2 + (from ? 0 : 1), kVec, slice, lane, p.cols, sum);
-        else
-            finish_row<kVec>(p, row, slice, lane, sum);
-    };
-    // the next token's row; false behind the last one (the tokens that are left out come last)
-    auto next = [&](unsigned key) {
-        if (key != row) {
-            flush(false);
-            first = false;
-            row = key;
-            sum = zeros();
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) {
+            const int v = slice * kVectors + i;
+            if (from || on)
+                store_any<32>(parts, true, (long long)window * 2 + (from ? 0 : 1), kVec, v, lane, p.cols, sum[i]);
+            else
+                finish_row<kVec>(p, row, v, lane, sum[i]);
         }
-        return row < p.rows;
     };
-    if (row >= p.rows) return;
+    auto next = [&](int j) {
+        if (!((kPairs > 1 && j >= 32 ? starts[kPairs - 1] : starts[0]) >> (j & 31) & 1)) return;
+        flush(false);
+        first = false;
+        row = key_at(j);
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) sum[i] = zeros();
+    };
     if constexpr (kVec) {
-        const int c = (slice * 32 + lane) * 8, left = p.cols - c;
-        const int bytes = max(0, min(16, left * (kF32 ? 4 : 2))), more = max(0, min(16, left * 4 - 16));
-        const char* const base = static_cast<const char*>(p.dy.data) + (left > 0 ? (long long)c * (kF32 ? 4 : 2) : 0);
         const long long pitch = p.dy.ld * (kF32 ? 4 : 2);
+        const char* base[kVectors];
+        int bytes[kVectors], more[kVectors];
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) {
+            const int c = ((slice * kVectors + i) * 32 + lane) * 8, left = p.cols - c;
+            bytes[i] = max(0, min(16, left * (kF32 ? 4 : 2)));
+            more[i] = max(0, min(16, left * 4 - 16));
+            base[i] = static_cast<const char*>(p.dy.data) + (left > 0 ? (long long)c * (kF32 ? 4 : 2) : 0);
+        }
         auto issue = [&](int j) {
-            if (j < kWindow && key_at(j) < p.rows) {
-                const char* from = base + token_at(j) * pitch;
+            if (j < live) {
+                const long long at = token_at(j) * pitch;
                 uint4* to = &ring[warp][j % kAhead][0][lane];
-                copy16(to, from, bytes);
-                if constexpr (kF32) copy16(to + 32, from + (more ? 16 : 0), more);
+#pragma unroll
+                for (int i = 0; i < kVectors; ++i) {
+                    copy16(to + i * kWords * 32, base[i] + at, bytes[i]);
+                    if constexpr (kF32) copy16(to + (i * kWords + 1) * 32, base[i] + at + (more[i] ? 16 : 0), more[i]);
+                }
             }
             copies_end();
         };
 #pragma unroll 1
         for (int j = 0; j < kAhead; ++j) issue(j);
 #pragma unroll 1
-        for (int j = 0; j < kWindow; ++j) {
+        for (int j = 0; j < live; ++j) {
             copies_wait<kAhead - 1>();
-            if (!next(key_at(j))) break;
+            next(j);
             const uint4(*at)[32] = ring[warp][j % kAhead];
-            if constexpr (kF32) {
-                const uint4 lo = at[0][lane], hi = at[kWords - 1][lane];
-                sum = add(sum, {{__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z),
-                                 __uint_as_float(lo.w), __uint_as_float(hi.x), __uint_as_float(hi.y),
-                                 __uint_as_float(hi.z), __uint_as_float(hi.w)}});
-            } else {
-                sum = add(sum, widen(at[0][lane]));
+#pragma unroll
+            for (int i = 0; i < kVectors; ++i) {
+                if constexpr (kF32) {
+                    const uint4 lo = at[i * kWords][lane], hi = at[i * kWords + kWords - 1][lane];
+                    sum[i] = add(sum[i], {{__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z),
+                                           __uint_as_float(lo.w), __uint_as_float(hi.x), __uint_as_float(hi.y),
+                                           __uint_as_float(hi.z), __uint_as_float(hi.w)}});
+                } else {
+                    sum[i] = add(sum[i], widen(at[i][lane]));
+                }
             }
             issue(j + kAhead);
         }
         copies_wait<0>();
     } else {
 #pragma unroll 1
-        for (int b = 0; b < kWindow; b += kBatch) {
-            Raw v[kBatch];
-            unsigned key[kBatch];
+        for (int b = 0; b < live; b += kBatch) {
+            Raw v[kBatch][kVectors];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                key[i] = key_at(b + i);
-                const unsigned token = token_at(b + i);
-                if (key[i] < p.rows) v[i] = load_raw<32>(p.dy, kF32, token, kVec, slice, lane, p.cols);
+            for (int k = 0; k < kBatch; ++k) {
+                const unsigned token = token_at(b + k);
+                if (b + k < live)
+#pragma unroll
+                    for (int i = 0; i < kVectors; ++i)
+                        v[k][i] = load_raw<32>(p.dy, kF32, token, kVec, slice * kVectors + i, lane, p.cols);
             }
-            bool more = true;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (more && (more = next(key[i]))) sum = add(sum, widen_raw(v[i], kF32, kVec));
-            if (!more) break;
+            for (int k = 0; k < kBatch; ++k) {
+                if (b + k >= live) break;
+                next(b + k);
+#pragma unroll
+                for (int i = 0; i < kVectors; ++i) sum[i] = add(sum[i], widen_raw(v[k][i], kF32, kVec));
+            }
         }
     }
-    if (row < p.rows) flush(true);
+    flush(true);
 }
 
 // A row that starts in one window and goes on into others: its last partial sum
@@ -722,7 +752,7 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
     s.zero = {static_cast<char*>(dw.data), D * es, dw.ld * es, dw.vec};
     // what can be zeroed while the tokens are sorted (13 us for 16384 of them, 28 us for
     // 65536), at 4 TB/s
-    const long long early = tokens == 0 ? V : ((8ll << 20) + 1200 * tokens) / (D * es);
+    const long long early = tokens == 0 ? V : ((16ll << 20) + 1400 * tokens) / (D * es);
     s.split = (unsigned)std::min(V, early);
     s.marks = reinterpret_cast<unsigned*>(ws + 2 * sp.pairs + sp.parts);
     // blocks for the zeros: those of the clusters that fit beside the sorting one
