@@ -156,11 +156,17 @@ __device__ __forceinline__ unsigned remote_load(const unsigned* at, int rank) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(address) : "memory");
     return v;
 }
+__device__ __forceinline__ void remote_store(uint2* at, unsigned rank, uint2 v) {
+    unsigned address;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(address) : "r"((unsigned)__cvta_generic_to_shared(at)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(address), "r"(v.x), "r"(v.y) : "memory");
+}
 
 // Loops stay loops here: a launch runs each of them a few times only, and code that
 // has not run yet comes slowly (16 items unrolled took 7 us to the first sum).
 struct SortShared {
-    uint2 pair[kChunk];
+    uint2 pair[2][kChunk];
     unsigned short rank[kChunk];
     unsigned short count[kSortWarps][kBins];  // of a warp, then of the warps before
     unsigned chunk[kBins], total[kBins], base[kBins], scan[32];
@@ -169,7 +175,8 @@ struct SortShared {
 // Ranks n items of the chunk, each of which has a place of 32 in a warp, among those of
 // their warp with the same digit; leaves the counts of the warps before each in
 // count[][], the chunk's in chunk[].
-__device__ __noinline__ void rank_chunk(SortShared& s, int items, int n, int shift, unsigned mask) {
+__device__ __noinline__ void rank_chunk(SortShared& s, const uint2* pairs, int items, int n, int shift,
+                                        unsigned mask) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = lane; i <= (int)mask / 2; i += 32) reinterpret_cast<unsigned*>(s.count[warp])[i] = 0;
     __syncwarp();
@@ -177,7 +184,7 @@ __device__ __noinline__ void rank_chunk(SortShared& s, int items, int n, int shi
     for (int k = 0; k < items; ++k) {
         const int i = (warp * items + k) * 32 + lane;
         const bool live = i < n;
-        const unsigned digit = live ? (s.pair[i].x >> shift) & mask : 0;
+        const unsigned digit = live ? (pairs[i].x >> shift) & mask : 0;
         // the lanes with this digit, bit by bit (the instruction that finds them at once
         // takes four times as long)
         unsigned same = __ballot_sync(~0u, live);
@@ -225,42 +232,95 @@ __device__ __noinline__ void place_bins(SortShared& s, unsigned n, unsigned more
 }
 
 // One block sorts up to a chunk of tokens without leaving its shared memory.
-__device__ void sort_few(const SortParams& p, SortShared& s, uint2* sorted) {
+__device__ void sort_few(const SortParams& p, SortShared& s) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int items = (p.tokens + kSortThreads - 1) / kSortThreads;
     const unsigned mask = (1u << p.bits) - 1;
 #pragma unroll 2
-    for (int i = threadIdx.x; i < p.tokens; i += kSortThreads) s.pair[i] = make_uint2(key_of(p, i), i);
+    for (int i = threadIdx.x; i < p.tokens; i += kSortThreads) s.pair[0][i] = make_uint2(key_of(p, i), i);
     __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * p.bits;
-        rank_chunk(s, items, p.tokens, shift, mask);
+        const uint2* from = s.pair[pass & 1];
+        uint2* to = s.pair[(pass & 1) ^ 1];
+        rank_chunk(s, from, items, p.tokens, shift, mask);
         place_bins(s, threadIdx.x <= mask ? s.chunk[threadIdx.x] : 0, 0, mask);
 #pragma unroll 2
         for (int k = 0; k < items; ++k) {
             const int i = (warp * items + k) * 32 + lane;
             if (i >= p.tokens) break;
-            const uint2 pair = s.pair[i];
+            const uint2 pair = from[i];
             const unsigned digit = (pair.x >> shift) & mask;
-            sorted[s.base[digit] + s.count[warp][digit] + s.rank[i]] = pair;
+            to[s.base[digit] + s.count[warp][digit] + s.rank[i]] = pair;
         }
         __syncthreads();
-        uint2* to = pass + 1 < p.passes ? s.pair : p.a;
+    }
 #pragma unroll 2
-        for (int i = threadIdx.x; i < p.tokens; i += kSortThreads) to[i] = sorted[i];
-        __syncthreads();
+    for (int i = threadIdx.x; i < p.tokens; i += kSortThreads) p.a[i] = s.pair[p.passes & 1][i];
+}
+
+// Where this block's digits start: behind all smaller ones of the cluster, and behind
+// those of the blocks before.
+__device__ __forceinline__ void place_cluster(SortShared& s, unsigned mask) {
+    cluster_sync();
+    unsigned all = 0, before = 0;
+    if (threadIdx.x <= mask) {
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c) {
+            const unsigned n = remote_load(&s.total[threadIdx.x], c);
+            all += n;
+            before += c < (int)blockIdx.x ? n : 0;
+        }
+    }
+    place_bins(s, all, before, mask);
+}
+
+// A cluster sorts up to a chunk for each block: the pairs go from block to block.
+__device__ void sort_chunks(const SortParams& p, SortShared& s) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int each = (p.tokens + kCluster - 1) / kCluster;
+    const int lo = min(p.tokens, (int)blockIdx.x * each), n = min(each, p.tokens - lo);
+    const int items = (each + kSortThreads - 1) / kSortThreads;
+    const unsigned mask = (1u << p.bits) - 1;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < n; i += kSortThreads) s.pair[0][i] = make_uint2(key_of(p, lo + i), lo + i);
+    __syncthreads();
+#pragma unroll 1
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.bits;
+        const uint2* from = s.pair[pass & 1];
+        uint2* to = s.pair[(pass & 1) ^ 1];
+        rank_chunk(s, from, items, n, shift, mask);
+        if (threadIdx.x <= mask) s.total[threadIdx.x] = s.chunk[threadIdx.x];
+        place_cluster(s, mask);
+        const bool last = pass + 1 == p.passes;
+#pragma unroll 2
+        for (int k = 0; k < items; ++k) {
+            const int i = (warp * items + k) * 32 + lane;
+            if (i >= n) break;
+            const uint2 pair = from[i];
+            const unsigned digit = (pair.x >> shift) & mask;
+            const unsigned at = s.base[digit] + s.count[warp][digit] + s.rank[i];
+            if (last) {
+                p.a[at] = pair;
+            } else {
+                const unsigned block = at / each;
+                remote_store(to + (at - block * each), block, pair);
+            }
+        }
+        // (also before a block ends whose totals others read)
+        cluster_sync();
     }
 }
 
-// A cluster sorts any number, each block a run of neighbours, chunk by chunk.
+// A cluster sorts any number, each block a run of neighbours, chunk by chunk, through
+// the workspace.
 __device__ void sort_tokens(const SortParams& p, SortShared& s) {
     const int me = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int each = (p.tokens + kCluster - 1) / kCluster;
     const int lo = min((long long)p.tokens, (long long)me * each);
     const int hi = min((long long)p.tokens, (long long)(me + 1) * each);
-    const bool once = each <= kChunk;
-    const int items = min(kItems, (each + kSortThreads - 1) / kSortThreads);  // of a thread
     const unsigned mask = (1u << p.bits) - 1;
 #pragma unroll 1
     for (int pass = 0; pass < p.passes; ++pass) {
@@ -274,9 +334,9 @@ __device__ void sort_tokens(const SortParams& p, SortShared& s) {
             __syncthreads();  // (the last chunk is used up)
 #pragma unroll 4
             for (int i = threadIdx.x; i < n; i += kSortThreads)
-                s.pair[i] = pass == 0 ? make_uint2(key_of(p, begin + i), begin + i) : __ldcg(from + begin + i);
+                s.pair[0][i] = pass == 0 ? make_uint2(key_of(p, begin + i), begin + i) : __ldcg(from + begin + i);
             __syncthreads();
-            rank_chunk(s, items, n, shift, mask);
+            rank_chunk(s, s.pair[0], kItems, n, shift, mask);
         };
         if (threadIdx.x <= mask) s.total[threadIdx.x] = 0;
 #pragma unroll 1
@@ -284,35 +344,21 @@ __device__ void sort_tokens(const SortParams& p, SortShared& s) {
             rank(begin);
             if (threadIdx.x <= mask) s.total[threadIdx.x] += s.chunk[threadIdx.x];
         }
-        cluster_sync();
-        // where each digit of this block starts: behind all smaller ones, and
-        // behind those of the blocks before
-        unsigned all = 0, before = 0;
-        if (threadIdx.x <= mask) {
-#pragma unroll
-            for (int c = 0; c < kCluster; ++c) {
-                const unsigned n = remote_load(&s.total[threadIdx.x], c);
-                all += n;
-                before += c < me ? n : 0;
-            }
-        }
-        place_bins(s, all, before, mask);
+        place_cluster(s, mask);
 #pragma unroll 1
         for (int begin = lo; begin < hi; begin += kChunk) {
-            if (!once) rank(begin);
+            rank(begin);
 #pragma unroll 2
-            for (int k = 0; k < items; ++k) {
-                const int i = (warp * items + k) * 32 + lane;
+            for (int k = 0; k < kItems; ++k) {
+                const int i = (warp * kItems + k) * 32 + lane;
                 if (begin + i >= hi) break;
-                const uint2 pair = s.pair[i];
+                const uint2 pair = s.pair[0][i];
                 const unsigned digit = (pair.x >> shift) & mask;
                 const unsigned at = s.base[digit] + s.count[warp][digit] + s.rank[i];
                 if (at < (unsigned)p.tokens) __stcg(to + at, pair);  // (ids that change meanwhile)
             }
-            if (!once) {
-                __syncthreads();
-                if (threadIdx.x <= mask) s.base[threadIdx.x] += s.chunk[threadIdx.x];
-            }
+            __syncthreads();
+            if (threadIdx.x <= mask) s.base[threadIdx.x] += s.chunk[threadIdx.x];
         }
         // what was written is read by other blocks; totals are rewritten
         __threadfence();
@@ -360,13 +406,15 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kCluster, 1,
     if (blockIdx.x >= sorters) {
         if (p.fill) clear_rows(p, reinterpret_cast<unsigned*>(shared), blockIdx.x - sorters, gridDim.x - sorters);
     } else if (p.few) {
-        sort_few(p, s, reinterpret_cast<uint2*>(&s + 1));
+        sort_few(p, s);
+    } else if (p.tokens <= kCluster * kChunk) {
+        sort_chunks(p, s);
     } else {
         sort_tokens(p, s);
     }
 }
 static_assert(sizeof(SortShared) >= 2 * kMarkRows / 8, "a block's marks fit");
-static_assert(kFewTokens <= kChunk && sizeof(SortShared) % 16 == 0, "pairs behind it are aligned");
+static_assert(kFewTokens <= kChunk && sizeof(SortShared) + 1024 <= kSharedLimit, "what a block has");
 
 // ------------------------------------------------------------ sums by row --
 
@@ -551,52 +599,92 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_consta
 }
 
 // A row that starts in one window and goes on into others: its last partial sum
-// there and the first ones of the windows behind, a warp for 128 columns.
-constexpr int kJoinWarps = 8, kJoinColumns = 128;
+// there and the first ones of the windows behind, for 128 columns.  A warp looks after
+// a window; where the row goes on for long, all warps of the block share its windows.
+// (The windows of a block are neighbours, of which few have such a row; the columns of
+// one window are different blocks'.)
+constexpr int kJoinWarps = 8, kJoinColumns = 128, kJoinLong = 16;
 
 template <int kWindow, bool kVec>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ SumParams p) {
+    __shared__ int spans[kJoinWarps];  // windows behind that a long row reaches, or 0
+    __shared__ float4 part[kJoinWarps][32];
     pdl_next();
     pdl_wait();
-    const int lane = threadIdx.x & 31, chunks = (p.cols + kJoinColumns - 1) / kJoinColumns;
-    const long long unit = (long long)blockIdx.x * kJoinWarps + __shfl_sync(~0u, threadIdx.x / 32, 0);
-    const int start = (int)(unit / chunks);
-    if (start + 1 >= p.windows) return;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x / 32, 0);
+    const int first = blockIdx.x * kJoinWarps, c = blockIdx.y * kJoinColumns + lane * 4;
     auto key = [&](int window, int i) { return p.sorted[(long long)window * kWindow + i].x; };
-    const unsigned row = key(start, kWindow - 1), front = key(start, 0);
-    const unsigned back = start > 0 ? key(start - 1, kWindow - 1) : p.rows;
-    int ends = start + 1;  // the first window behind that the row does not reach
-    for (;; ends += 32) {
-        const int u = ends + lane;
-        const unsigned other = __ballot_sync(~0u, u >= p.windows || key(u, 0) != row);
-        if (other != 0) {
-            ends += __ffs(other) - 1;
-            break;
-        }
-    }
-    if (row >= p.rows || ends == start + 1 || (front == row && back == row)) return;
-    const int c = (int)(unit - (long long)start * chunks) * kJoinColumns + lane * 4;
-    if (c >= p.cols) return;
-    const float* at = p.parts + ((long long)start * 2 + 1) * p.padded + c;
-    float4 sum = *reinterpret_cast<const float4*>(at);
-    at += p.padded;  // (the next window's first row)
-#pragma unroll 16
-    for (int u = start + 1; u < ends; ++u, at += 2 * p.padded) {
-        const float4 v = *reinterpret_cast<const float4*>(at);
-        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-    }
-    const float s[4] = {sum.x, sum.y, sum.z, sum.w};
-    const long long to = (long long)row * p.dw.ld + c;
+    // the partial sums of the windows from `begin` on, every step-th one, eight in flight
+    auto add_up = [&](int begin, int end, int step, float4 sum) {
+        constexpr int kBatch = 8;
+        const long long pitch = (long long)step * 2 * p.padded;
+        const float* at = p.parts + (long long)begin * 2 * p.padded + c;
+        for (int u = begin; u < end; u += kBatch * step, at += kBatch * pitch) {
+            float4 v[kBatch];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (c + j >= p.cols) break;
-        if (p.dw.f32) {
-            float* f = static_cast<float*>(p.dw.data) + to + j;
-            *f = fmaf(p.scale, s[j], p.accumulate ? *f : 0.0f);
-        } else {
-            __nv_bfloat16* b = static_cast<__nv_bfloat16*>(p.dw.data) + to + j;
-            *b = __float2bfloat16(fmaf(p.scale, s[j], p.accumulate ? __bfloat162float(*b) : 0.0f));
+            for (int k = 0; k < kBatch; ++k)
+                v[k] = u + k * step < end ? *reinterpret_cast<const float4*>(at + k * pitch)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) sum.x += v[k].x, sum.y += v[k].y, sum.z += v[k].z, sum.w += v[k].w;
         }
+        return sum;
+    };
+    auto store = [&](unsigned row, float4 sum) {
+        const float s[4] = {sum.x, sum.y, sum.z, sum.w};
+        const long long to = (long long)row * p.dw.ld + c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (c + j >= p.cols) break;
+            if (p.dw.f32) {
+                float* f = static_cast<float*>(p.dw.data) + to + j;
+                *f = fmaf(p.scale, s[j], p.accumulate ? *f : 0.0f);
+            } else {
+                __nv_bfloat16* b = static_cast<__nv_bfloat16*>(p.dw.data) + to + j;
+                *b = __float2bfloat16(fmaf(p.scale, s[j], p.accumulate ? __bfloat162float(*b) : 0.0f));
+            }
+        }
+    };
+    auto last_part = [&](int window) {
+        return *reinterpret_cast<const float4*>(p.parts + ((long long)window * 2 + 1) * p.padded + c);
+    };
+    const int start = first + warp;
+    int span = 0;
+    if (start + 1 < p.windows) {
+        const unsigned row = key(start, kWindow - 1), front = key(start, 0);
+        const unsigned back = start > 0 ? key(start - 1, kWindow - 1) : p.rows;
+        for (int u = start + 1 + lane;; u += 32) {
+            const unsigned other = __ballot_sync(~0u, u >= p.windows || key(u, 0) != row);
+            if (other != 0) {
+                span += __ffs(other) - 1;
+                break;
+            }
+            span += 32;
+        }
+        if (row >= p.rows || (front == row && back == row)) span = 0;
+        if (span > 0 && span <= kJoinLong && c < p.cols)
+            store(row, add_up(start + 1, start + 1 + span, 1, last_part(start)));
+    }
+    if (lane == 0) spans[warp] = span > kJoinLong ? span : 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const int n = spans[w], from = first + w;
+        if (n == 0) continue;
+        const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c < p.padded)
+            part[warp][lane] = add_up(from + 1 + warp, from + 1 + n, kJoinWarps, warp == 0 ? last_part(from) : none);
+        __syncthreads();
+        if (warp == 0 && c < p.cols) {
+            float4 sum = part[0][lane];
+#pragma unroll
+            for (int o = 1; o < kJoinWarps; ++o) {
+                const float4 v = part[o][lane];
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+            }
+            store(key(from, kWindow - 1), sum);
+        }
+        __syncthreads();
     }
 }
 
@@ -630,11 +718,11 @@ BackwardSpace space_of(long long tokens, long long rows, long long cols) {
 
 template <int kWindow, bool kVec>
 cudaError_t launch_sums(const SumParams& p, cudaStream_t st) {
-    const long long joins = (long long)p.windows * ((p.cols + kJoinColumns - 1) / kJoinColumns);
     cudaError_t e = launch_pdl(p.dy.f32 ? sum_kernel<kWindow, kVec, true> : sum_kernel<kWindow, kVec, false>,
                                dim3(p.sum_blocks + p.zero_blocks), dim3(kSumWarps * 32), st, p);
     if (e != cudaSuccess || p.windows == 1) return e;
-    return launch_pdl(join_kernel<kWindow, kVec>, dim3((unsigned)((joins + kJoinWarps - 1) / kJoinWarps)),
+    return launch_pdl(join_kernel<kWindow, kVec>,
+                      dim3((p.windows + kJoinWarps - 1) / kJoinWarps, (p.cols + kJoinColumns - 1) / kJoinColumns),
                       dim3(kJoinWarps * 32), st, p);
 }
 template <bool kVec>
@@ -759,8 +847,7 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
     s.few = tokens <= kFewTokens;
     s.fill = !accumulate;
     const int fill = accumulate ? 0 : (int)std::min((long long)kFillClusters, (V + 31) / 32) * kCluster;
-    const size_t shared = sizeof(SortShared) + (s.few ? kFewTokens * sizeof(uint2) : 0);
-    cudaError_t e = launch_pdl_shared(sort_kernel, dim3(kCluster + fill), dim3(kSortThreads), shared, st, s);
+    cudaError_t e = launch_pdl_shared(sort_kernel, dim3(kCluster + fill), dim3(kSortThreads), sizeof(SortShared), st, s);
     if (e != cudaSuccess) return VC_ERR_CUDA;
     if (tokens == 0) return VC_SUCCESS;
 
