@@ -4,13 +4,17 @@
 // Two kernels, both over the plan's tiles of up to 16 KiB: the first sums squares
 // (or takes the largest magnitude) and leaves one value a block, the second adds
 // those in a fixed order, in every block by itself, and scales.  The bound is the
-// gradients' bytes.
+// gradients' bytes, which clipping reads twice where they are more than the second-
+// level cache holds.  (Small sets in one launch of one cluster, whose blocks read each
+// other's sums, took 10 us with 16 blocks and 6.2 with 8, where these two take 5.0.)
 //
-// Squares are added in 32 bits over a tile's 16 or 32 values of a thread and in 64
-// bits from there on.  float32's range does not hold the squares of its own
-// values: where a thread's sum over a tile leaves [2^-90, 2^120] it is computed
-// again, in 64 bits, from the registers that still hold the values.  (At a sum of
-// 2^-90 or more, squares below 2^-126, which lose digits, do not count.)
+// Squares are added in 32 bits over a tile's 16 or 32 values of a thread, and from there
+// on as pairs of 32-bit values that keep what the additions round off (48 bits; this
+// GPU adds two 64-bit values a clock and SM: a block's 64-bit sum took 9 us).
+// float32's range does not hold the squares of its own values: where a thread's sum
+// over a tile leaves [2^-90, 2^90] it is computed again, in 64 bits, from the registers
+// that still hold the values, and added apart.  (At a sum of 2^-90 or more, squares
+// below 2^-126, which lose digits, do not count.)
 #include <algorithm>
 #include <math.h>
 
@@ -23,13 +27,14 @@ namespace {
 constexpr int kClipThreads = 256;
 constexpr int kTileBytes = VC_CLIP_TILE_MAX_BYTES;
 constexpr int kVecs = kTileBytes / 16 / kClipThreads;  // 16-byte vectors of a thread
-constexpr int kResident = 6;  // blocks of an SM
+constexpr int kResident = 4;  // blocks of an SM
 constexpr int kMaxBlocks = kSMs * kResident;
 constexpr size_t kCacheBytes = 80u << 20;
 
 int clip_blocks(int ntiles) { return std::max(1, std::min(ntiles, kMaxBlocks)); }
 
-enum { kTileF32 = 1 };
+// kAllInPlace: all tiles of the plan are (so that nothing is to be done where c = 1).
+enum { kTileF32 = 1, kAllInPlace = 2 };
 
 // A tile's values as a thread holds them: up to kVecs vectors of 16 bytes from
 // the first 16-byte boundary on, and at most one value before or behind them.
@@ -100,18 +105,33 @@ __device__ __forceinline__ void each_value(const Held& h, bool f32, F f) {
     f(h.edge, 0);
 }
 
-__device__ __forceinline__ double squares(const Held& h, bool f32) {
+// A sum of squares: s + c, where |c| is at most half a step of s, and what is out of
+// their range.  Of the largest magnitude: its bits in s.
+struct __align__(16) Part {
+    float s, c;
+    double rest;
+};
+constexpr float kLeast = 0x1p-90f, kMost = 0x1p90f;
+
+// s + c += x + d
+__device__ __forceinline__ void add_pair(float& s, float& c, float x, float d) {
+    const float t = s + x, b = t - s;
+    c += ((s - (t - b)) + (x - b)) + d;
+    s = t;
+}
+
+__device__ __forceinline__ void squares(const Held& h, bool f32, Part& p) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     each_value(h, f32, [&](float x, int j) { s[j] = fmaf(x, x, s[j]); });
     const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-    if (sum >= 0x1p-90f && sum <= 0x1p120f) return sum;
+    if (sum >= kLeast && sum <= kMost) return add_pair(p.s, p.c, sum, 0.0f);
     unsigned any = __float_as_uint(h.edge);
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) any |= h.v[u].x | h.v[u].y | h.v[u].z | h.v[u].w;
-    if ((any & (f32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) return 0.0;
+    if ((any & (f32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) return;
     double d = 0.0;
     each_value(h, f32, [&](float x, int) { d = ::fma((double)x, (double)x, d); });
-    return d;
+    p.rest += d;
 }
 
 // The largest magnitude as float32 bits, which order like the values; a NaN's
@@ -122,20 +142,36 @@ __device__ __forceinline__ unsigned largest(const Held& h, bool f32) {
     return m;
 }
 
-// The block's sum or maximum, in thread 0 (and in all threads with `all`).
+// The sum or maximum of the warp's parts, in every lane.
 template <bool kMax>
-__device__ double block_total(double v, double* shared) {
-    unsigned long long bits = (unsigned long long)v;  // (kMax: an integer below 2^31)
-    if constexpr (kMax)
-        v = (double)__reduce_max_sync(~0u, (unsigned)bits);
-    else
-        v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+__device__ __forceinline__ Part warp_total(Part p) {
+    if constexpr (kMax) {
+        p.s = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(p.s)));
+    } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float s = __shfl_xor_sync(~0u, p.s, o), c = __shfl_xor_sync(~0u, p.c, o);
+            // (in the same order in both lanes, for the same bits)
+            const bool low = (threadIdx.x & o) == 0;
+            float t = low ? p.s : s, d = low ? p.c : c;
+            add_pair(t, d, low ? s : p.s, low ? c : p.c);
+            p.s = t, p.c = d;
+        }
+        if (__any_sync(~0u, p.rest != 0.0)) p.rest = warp_sum(p.rest);  // (NaN: too)
+    }
+    return p;
+}
+// The block's, in every thread.
+template <bool kMax>
+__device__ Part block_total(Part p, Part* shared) {
+    p = warp_total<kMax>(p);
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    if (lane == 0) shared[threadIdx.x >> 5] = p;
     __syncthreads();
-    double t = shared[0];
-    for (int w = 1; w < kClipThreads / 32; ++w) t = kMax ? fmax(t, shared[w]) : t + shared[w];
+    p = lane < warps ? shared[lane] : Part{0.0f, 0.0f, 0.0};
+    p = warp_total<kMax>(p);
     __syncthreads();
-    return t;
+    return p;
 }
 
 // Block b's tiles: a run of neighbours, so that the second kernel, which takes
@@ -146,43 +182,52 @@ __device__ __forceinline__ int first_tile(int b, int blocks, int ntiles) {
 
 template <bool kMax>
 __global__ void __launch_bounds__(kClipThreads, kResident)
-    norm_kernel(const vc_clip_tile_t* tiles, int ntiles, int again, double* parts) {
-    __shared__ double shared[kClipThreads / 32];
+    norm_kernel(const vc_clip_tile_t* tiles, int ntiles, int again, Part* parts) {
+    __shared__ Part shared[kClipThreads / 32];
     pdl_next();
     pdl_wait();
     const int end = first_tile(blockIdx.x + 1, gridDim.x, ntiles);
     const int keep = end - again;  // the tiles from here on are read again
-    double sum = 0.0;
-    unsigned top = 0;
+    Part sum = {0.0f, 0.0f, 0.0};
     int i = first_tile(blockIdx.x, gridDim.x, ntiles);
+    // a tile is on its way while the one before it is summed, and the place of the next
     vc_clip_tile_t next = {};
-    if (i < end) next = tiles[i];
-    for (; i < end; ++i) {
-        const vc_clip_tile_t t = next;
-        if (i + 1 < end) next = tiles[i + 1];
-        Held h;
-        if (i < keep)
-            load_tile<true>(t, cut_of(t), h);
+    Held coming;
+    auto load = [&](int at) {
+        if (at < keep)
+            load_tile<true>(next, cut_of(next), coming);
         else
-            load_tile<false>(t, cut_of(t), h);
-        if constexpr (kMax)
-            top = max(top, largest(h, t.flags & kTileF32));
-        else
-            sum += squares(h, t.flags & kTileF32);
+            load_tile<false>(next, cut_of(next), coming);
+    };
+    if (i < end) {
+        next = tiles[i];
+        load(i);
     }
-    const double total = block_total<kMax>(kMax ? (double)top : sum, shared);
-    if (threadIdx.x == 0) parts[blockIdx.x] = total;
+    for (; i < end; ++i) {
+        const bool f32 = next.flags & kTileF32;
+        const Held h = coming;
+        if (i + 1 < end) {
+            next = tiles[i + 1];
+            load(i + 1);
+        }
+        if constexpr (kMax)
+            sum.s = __uint_as_float(max(__float_as_uint(sum.s), largest(h, f32)));
+        else
+            squares(h, f32, sum);
+    }
+    sum = block_total<kMax>(sum, shared);
+    if (threadIdx.x == 0) parts[blockIdx.x] = sum;
 }
 
 template <bool kMax>
-__device__ __forceinline__ float total_norm(const double* parts, int nparts, double* shared) {
-    double v = 0.0;
-    for (int i = threadIdx.x; i < nparts; i += kClipThreads) {
-        const double p = parts[i];
-        v = kMax ? fmax(v, p) : v + p;
-    }
-    v = block_total<kMax>(v, shared);
-    return kMax ? __uint_as_float((unsigned)v) : (float)sqrt(v);
+__device__ __forceinline__ float norm_of(const Part& p) {
+    if (kMax) return p.s;
+    if (p.rest == 0.0) return __fsqrt_rn(p.s);  // (c is below half a step)
+    return (float)sqrt((double)p.s + (double)p.c + p.rest);
+}
+__device__ __forceinline__ float scale_of(float norm, float max_norm, float eps) {
+    const float q = __fdiv_rn(max_norm, norm + eps);
+    return q >= 1.0f ? 1.0f : q;  // (a NaN stays one)
 }
 
 // c x, rounded to the tile's type, where the plan says.
@@ -227,35 +272,48 @@ __device__ __forceinline__ void store_tile(const vc_clip_tile_t& t, const Cut& c
 
 template <bool kMax, bool kClip>
 __global__ void __launch_bounds__(kClipThreads, kResident) clip_kernel(const vc_clip_tile_t* tiles, int ntiles,
-                                                            const double* parts, int nparts,
+                                                            const Part* parts, int nparts,
                                                             float max_norm, float eps, float* norm) {
-    __shared__ double shared[kClipThreads / 32];
+    __shared__ Part shared[kClipThreads / 32];
     pdl_next();
     pdl_wait();
-    const float total = total_norm<kMax>(parts, nparts, shared);
+    Part all = {0.0f, 0.0f, 0.0};
+    for (int i = threadIdx.x; i < nparts; i += kClipThreads) {
+        const Part p = parts[i];
+        if constexpr (kMax) {
+            all.s = __uint_as_float(max(__float_as_uint(all.s), __float_as_uint(p.s)));
+        } else {
+            add_pair(all.s, all.c, p.s, p.c);
+            if (p.rest != 0.0) all.rest += p.rest;
+        }
+    }
+    const float total = norm_of<kMax>(block_total<kMax>(all, shared));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
     if constexpr (kClip) {
-        const float q = __fdiv_rn(max_norm, total + eps);
-        const float scale = q >= 1.0f ? 1.0f : q;  // (a NaN stays one)
+        const float scale = scale_of(total, max_norm, eps);
         const int begin = first_tile(blockIdx.x, gridDim.x, ntiles);
         int i = first_tile(blockIdx.x + 1, gridDim.x, ntiles) - 1;
-        vc_clip_tile_t next = {};
-        if (i >= begin) next = tiles[i];
+        if (i < begin) return;
+        vc_clip_tile_t next = tiles[i];
+        if (scale == 1.0f && next.flags & kAllInPlace) return;
+        Held coming;
+        load_tile<true>(next, cut_of(next), coming);
         for (; i >= begin; --i) {
             const vc_clip_tile_t t = next;
-            if (i > begin) next = tiles[i - 1];
+            const Held h = coming;
+            if (i > begin) {
+                next = tiles[i - 1];
+                load_tile<true>(next, cut_of(next), coming);
+            }
             if (t.dst == nullptr || (scale == 1.0f && t.src == t.dst)) continue;
-            const Cut c = cut_of(t);
-            Held h;
-            load_tile<true>(t, c, h);
-            store_tile(t, c, h, scale);
+            store_tile(t, cut_of(t), h, scale);
         }
     }
 }
 
 template <bool kMax>
 cudaError_t launch_clip(const vc_clip_tile_t* tiles, int ntiles, bool clip, float max_norm, float eps,
-                        float* norm, double* parts, cudaStream_t st) {
+                        float* norm, Part* parts, cudaStream_t st) {
     const int blocks = clip_blocks(ntiles);
     // what the second-level cache can hold for the second kernel
     const int again = clip ? (int)(kCacheBytes / kTileBytes / blocks) : 0;
@@ -264,9 +322,9 @@ cudaError_t launch_clip(const vc_clip_tile_t* tiles, int ntiles, bool clip, floa
     if (e != cudaSuccess) return e;
     if (clip)
         return launch_pdl(clip_kernel<kMax, true>, dim3(blocks), dim3(kClipThreads), st, tiles, ntiles,
-                          (const double*)parts, blocks, max_norm, eps, norm);
+                          (const Part*)parts, blocks, max_norm, eps, norm);
     return launch_pdl(clip_kernel<kMax, false>, dim3(1), dim3(kClipThreads), st, tiles, ntiles,
-                      (const double*)parts, blocks, max_norm, eps, norm);
+                      (const Part*)parts, blocks, max_norm, eps, norm);
 }
 
 vc_status_t run_clip(const vc_clip_tile_t* dev_tiles, int ntiles, vc_grad_norm_t kind, bool clip,
@@ -285,7 +343,7 @@ vc_status_t run_clip(const vc_clip_tile_t* dev_tiles, int ntiles, vc_grad_norm_t
     if (overlap(table, out) || overlap(table, ws) || overlap(out, ws)) return VC_ERR_ALIAS;
     if (test_launch_failure()) return VC_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    double* parts = static_cast<double*>(workspace);
+    Part* parts = static_cast<Part*>(workspace);
     const cudaError_t e =
         kind == VC_GRAD_NORM_MAX
             ? launch_clip<true>(dev_tiles, ntiles, clip, max_norm, eps, norm, parts, st)
@@ -362,11 +420,14 @@ vc_status_t vc_clip_plan(const void* const* grads, void* const* outs, const size
             t.index = n++;
         }
     }
+    bool in_place = outs != nullptr;
+    for (int i = 0; i < n && in_place; ++i) in_place = tiles[i].src == tiles[i].dst;
+    for (int i = 0; i < n && in_place; ++i) tiles[i].flags |= kAllInPlace;
     return outs != nullptr && tiles_alias(tiles, n) ? VC_ERR_ALIAS : VC_SUCCESS;
 }
 
 size_t vc_clip_workspace(int ntiles) {
-    return ntiles < 0 ? 0 : round256(sizeof(double) * clip_blocks(ntiles));
+    return ntiles < 0 ? 0 : round256(sizeof(Part) * clip_blocks(ntiles));
 }
 
 vc_status_t vc_grad_norm(const vc_clip_tile_t* dev_tiles, int ntiles, vc_grad_norm_t kind,

@@ -280,6 +280,29 @@ __device__ __forceinline__ void pdl_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// ------------------------------------------------------------------- clusters --
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+// What lies at `at` in block `rank` of the cluster.
+__device__ __forceinline__ unsigned remote_address(const void* at, unsigned rank) {
+    unsigned address;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(address) : "r"((unsigned)__cvta_generic_to_shared(at)), "r"(rank));
+    return address;
+}
+__device__ __forceinline__ unsigned remote_load(const unsigned* at, unsigned rank) {
+    unsigned v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote_address(at, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void remote_store(uint2* at, unsigned rank, uint2 v) {
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};"
+                 ::"r"(remote_address(at, rank)), "r"(v.x), "r"(v.y) : "memory");
+}
+
 // launch_pdl with dynamic shared memory.
 template <class... KArgs, class... Args>
 cudaError_t launch_pdl_shared(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t bytes, cudaStream_t st,

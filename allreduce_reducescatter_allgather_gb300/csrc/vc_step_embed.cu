@@ -145,24 +145,6 @@ __device__ __forceinline__ unsigned key_of(const SortParams& p, int t) {
     return live ? (unsigned)row : p.rows;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-                 ::: "memory");
-}
-__device__ __forceinline__ unsigned remote_load(const unsigned* at, int rank) {
-    unsigned address, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(address) : "r"((unsigned)__cvta_generic_to_shared(at)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(address) : "memory");
-    return v;
-}
-__device__ __forceinline__ void remote_store(uint2* at, unsigned rank, uint2 v) {
-    unsigned address;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(address) : "r"((unsigned)__cvta_generic_to_shared(at)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(address), "r"(v.x), "r"(v.y) : "memory");
-}
-
 // Loops stay loops here: a launch runs each of them a few times only, and code that
 // has not run yet comes slowly (16 items unrolled took 7 us to the first sum).
 struct SortShared {

@@ -131,7 +131,8 @@ vc_status_t vc_block_norm_backward(const vc_block_norm_in_t *in, const vc_affine
 /* ---- the norm of all gradients, and clipping ------------------------------ */
 
 /* One tile of a plan: `count` consecutive elements of a gradient at src, and
- * where they go (NULL: nowhere).  flags bit 0: float32 (else bfloat16). */
+ * where they go (NULL: nowhere).  flags bit 0: float32 (else bfloat16); bit 1: all
+ * tiles of the plan are in place. */
 typedef struct {
     const void *src;
     void *dst;
