@@ -303,9 +303,9 @@ __device__ __forceinline__ void remote_store(uint2* at, unsigned rank, uint2 v) 
                  ::"r"(remote_address(at, rank)), "r"(v.x), "r"(v.y) : "memory");
 }
 
-// launch_pdl with dynamic shared memory.
+// launch_pdl with dynamic shared memory, and clusters of `span` blocks.
 template <class... KArgs, class... Args>
-cudaError_t launch_pdl_shared(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t bytes, cudaStream_t st,
+cudaError_t launch_pdl_shared(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t bytes, int span, cudaStream_t st,
                               Args&&... args) {
     if (bytes > 24u << 10) {  // (with what the kernel has of its own, above 48 KiB)
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -317,11 +317,14 @@ cudaError_t launch_pdl_shared(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = span;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = span > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -378,7 +378,7 @@ __device__ void clear_rows(const SortParams& p, unsigned* marks, int part, int p
     }
 }
 
-__global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kCluster, 1, 1)
+__global__ void __launch_bounds__(kSortThreads, 1)
     sort_kernel(const __grid_constant__ SortParams p) {
     extern __shared__ uint4 shared[];
     SortShared& s = *reinterpret_cast<SortShared*>(shared);
@@ -829,7 +829,7 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
     s.few = tokens <= kFewTokens;
     s.fill = !accumulate;
     const int fill = accumulate ? 0 : (int)std::min((long long)kFillClusters, (V + 31) / 32) * kCluster;
-    cudaError_t e = launch_pdl_shared(sort_kernel, dim3(kCluster + fill), dim3(kSortThreads), sizeof(SortShared), st, s);
+    cudaError_t e = launch_pdl_shared(sort_kernel, dim3(kCluster + fill), dim3(kSortThreads), sizeof(SortShared), kCluster, st, s);
     if (e != cudaSuccess) return VC_ERR_CUDA;
     if (tokens == 0) return VC_SUCCESS;
 

@@ -10,19 +10,22 @@ constexpr int kForwardThreads = 128;  // of a block of teams that are warps
 constexpr int kResident = 1024;
 
 // One row after the other, the next one's inputs on their way meanwhile.
-template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
+template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec, bool kSpan = false>
 __global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam, (kVec ? kResident : kResident / 2) / (kTeam == 32 ? kForwardThreads : kTeam))
     forward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kForwardThreads : kTeam, kTeams = kThreads / kTeam;
     constexpr int kH = 0, kX = 1, kGate = 2;
-    __shared__ float shared[2 * kTeam / 32][4];
+    using Sums = TeamSums<kTeam, kSpan>;
+    __shared__ float shared[2 * Sums::kAll][4];
     extern __shared__ uint4 ring[];
-    TeamSums<kTeam> sums = {shared, 0};
+    __shared__ SpanShared signals;
+    Sums sums = {shared, 0, p.span, &signals, 0};
+    const int v0 = kSpan ? blockIdx.x % p.span * kVecs : 0;  // the block's first vector
     const int lane = kTeams == 1 ? threadIdx.x : threadIdx.x % 32;
     const int part = kTeams == 1 ? 0 : __shfl_sync(~0u, threadIdx.x / 32, 0);  // the team in the block
     const bool has_x = p.x.data != nullptr, full_gate = p.gate_mode == kGateFull;
     Stream<kThreads, kTeam, kVecs, 3, kVec, kVec> in;
-    in.begin(ring, lane, p.cols);
+    in.begin(ring, v0, lane, p.cols);
     in.array(kH, true, false);
     in.array(kX, has_x, kStream32);
     in.array(kGate, full_gate, p.gate.f32);
@@ -32,14 +35,16 @@ __global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam, (kVec ?
         if (full_gate) in.load(kGate, p.gate, row, lane, p.cols);
     };
     auto affine = [&](const Affine& a, const Eight& v, int i, float rstd) {
-        const Eight w = mul(rstd, load_any<kTeam>(a.weight, 0, kVec, i, lane, p.cols));
-        if (kLayer && a.bias.data != nullptr) return fma(v, w, load_any<kTeam>(a.bias, 0, kVec, i, lane, p.cols));
+        const Eight w = mul(rstd, load_any<kTeam>(a.weight, 0, kVec, v0 + i, lane, p.cols));
+        if (kLayer && a.bias.data != nullptr) return fma(v, w, load_any<kTeam>(a.bias, 0, kVec, v0 + i, lane, p.cols));
         return mul(v, w);
     };
+    if constexpr (kSpan) sums.begin();
     pdl_next();
     pdl_wait();
-    const long long step = (long long)gridDim.x * kTeams;
-    long long row = (long long)blockIdx.x * kTeams + part;
+    const int span = kSpan ? p.span : 1;
+    const long long step = (long long)(gridDim.x / span) * kTeams;
+    long long row = (long long)(blockIdx.x / span) * kTeams + part;
     if (row < p.rows) load(row);
     for (; row < p.rows; row += step) {
         if constexpr (kVec) {
@@ -52,7 +57,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam, (kVec ?
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) u[i] = in.get(kH, i);
         if (p.post.weight.data != nullptr) {
-            const float rstd = center<kTeam, kVecs, kLayer>(p, u, kVec, lane, sums);
+            const float rstd = center<kVecs, kLayer>(p, u, kVec, v0, lane, sums);
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) u[i] = affine(p.post, u[i], i, rstd);
         }
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam, (kVec ?
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
                 u[i] = mul(u[i], gate_value(full_gate ? in.get(kGate, i)
-                                                      : load_any<kTeam>(p.gate, g, kVec, i, lane, p.cols),
+                                                      : load_any<kTeam>(p.gate, g, kVec, v0 + i, lane, p.cols),
                                             p.sigmoid));
         }
         if (has_x)
@@ -71,19 +76,21 @@ __global__ void __launch_bounds__(kTeam == 32 ? kForwardThreads : kTeam, (kVec ?
             if (row + step < p.rows) load(row + step);
         if (p.r.data != nullptr)
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.r, kStream32, row, kVec, i, lane, p.cols, u[i]);
+            for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.r, kStream32, row, kVec, v0 + i, lane, p.cols, u[i]);
         if (p.n.data == nullptr) continue;
-        const float rstd = center<kTeam, kVecs, kLayer>(p, u, kVec, lane, sums);
+        const float rstd = center<kVecs, kLayer>(p, u, kVec, v0, lane, sums);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i)
-            store_any<kTeam>(p.n, false, row, kVec, i, lane, p.cols, affine(p.pre, u[i], i, rstd));
+            store_any<kTeam>(p.n, false, row, kVec, v0 + i, lane, p.cols, affine(p.pre, u[i], i, rstd));
     }
+    if constexpr (kSpan) sums.end(p.timeouts);
 }
 
+// Longer rows.
 template <bool kLayer, bool kStream32>
 __global__ void __launch_bounds__(kLong) forward_long_kernel(const __grid_constant__ NormParams p) {
     __shared__ float shared[2 * kLong / 32][4];
-    TeamSums<kLong> sums = {shared, 0};
+    TeamSums<kLong, false> sums = {shared, 0, 1, nullptr, 0};
     const int lane = threadIdx.x, steps = (p.cols + 8 * kLong - 1) / (8 * kLong);
     pdl_next();
     pdl_wait();
@@ -121,41 +128,47 @@ __global__ void __launch_bounds__(kLong) forward_long_kernel(const __grid_consta
 }
 
 Shape forward_shape(int cols) {
-    if (cols <= 256) return {32, 1};
-    if (cols <= 512) return {32, 2};
-    if (cols <= 1024) return {128, 1};
-    if (cols <= 2048) return {128, 2};
-    if (cols <= 4096) return {256, 2};
-    if (cols <= 8192) return {512, 2};
-    return {0, 0};
+    if (cols <= 256) return {32, 1, 1};
+    if (cols <= 512) return {32, 2, 1};
+    if (cols <= 1024) return {128, 1, 1};
+    if (cols <= 2048) return {128, 2, 1};
+    if (cols <= 4096) return {256, 2, 1};
+    if (cols <= 8192 * kMaxSpan) return {512, 2, (cols + 8191) / 8192};
+    return {0, 0, 1};
 }
 template <bool kLayer, bool kStream32, bool kVec>
-cudaError_t launch_forward(const NormParams& p, cudaStream_t st) {
+cudaError_t launch_forward(NormParams& p, cudaStream_t st) {
     const Shape s = forward_shape(p.cols);
     const int threads = s.team == 0 ? kLong : std::max(kForwardThreads, s.team);
     const int per = s.team == 0 ? 1 : threads / s.team;
-    size_t ring = 0;
-    if (s.team != 0 && kVec)
-        ring = (size_t)kStages * threads * s.vecs * 16 *
-               (1 + (p.x.data == nullptr ? 0 : kStream32 ? 2 : 1) + (p.gate_mode != kGateFull ? 0 : p.gate.f32 ? 2 : 1));
-    // as many blocks as an SM holds at a time
-    const int blocks = (int)std::min((size_t)((kVec ? kResident : kResident / 2) / threads), (kSharedLimit + 1024) / (ring + 2048));
-    const long long want = (p.rows + per - 1) / per;
-    const dim3 grid((unsigned)std::min(want, (long long)kSMs * std::max(1, blocks)));
-    void (*kernel)(NormParams);
+    // 16-byte words a thread has of a vector of the inputs of one row
+    const size_t words = 1 + (p.x.data == nullptr ? 0 : kStream32 ? 2 : 1) +
+                         (p.gate_mode != kGateFull ? 0 : p.gate.f32 ? 2 : 1);
+    const size_t bytes = kVec ? kStages * words * s.vecs * threads * 16 : 0;
+    p.span = s.span;
+    if (s.span > 1 && (p.timeouts = gemm::timeout_counter()) == nullptr) return cudaErrorInvalidValue;
+    void (*kernel)(NormParams) = nullptr;
     switch (s.team * 4 + s.vecs) {
     case 32 * 4 + 1: kernel = forward_kernel<32, 1, kLayer, kStream32, kVec>; break;
     case 32 * 4 + 2: kernel = forward_kernel<32, 2, kLayer, kStream32, kVec>; break;
     case 128 * 4 + 1: kernel = forward_kernel<128, 1, kLayer, kStream32, kVec>; break;
     case 128 * 4 + 2: kernel = forward_kernel<128, 2, kLayer, kStream32, kVec>; break;
     case 256 * 4 + 2: kernel = forward_kernel<256, 2, kLayer, kStream32, kVec>; break;
-    case 512 * 4 + 2: kernel = forward_kernel<512, 2, kLayer, kStream32, kVec>; break;
+    case 512 * 4 + 2:
+        kernel = s.span > 1 ? forward_kernel<512, 2, kLayer, kStream32, kVec, true>
+                            : forward_kernel<512, 2, kLayer, kStream32, kVec>;
+        break;
     default: kernel = forward_long_kernel<kLayer, kStream32>;
     }
-    return launch_pdl_shared(kernel, grid, dim3(threads), ring, st, p);
+    // as many blocks as an SM holds at a time
+    const int blocks = std::max(1, (int)std::min((size_t)((kVec || s.team == 0 ? kResident : kResident / 2) / threads),
+                                                 (kSharedLimit + 1024) / (bytes + 2048 + (s.span > 1 ? 4096 : 0))));
+    const long long want = (p.rows + per - 1) / per;
+    const long long most = s.span > 1 ? clusters_of(s.span, blocks) : (long long)kSMs * blocks;
+    return launch_pdl_shared(kernel, dim3((unsigned)(std::min(want, most) * s.span)), dim3(threads), bytes, s.span, st, p);
 }
 template <bool kLayer, bool kStream32>
-cudaError_t launch_forward(const NormParams& p, cudaStream_t st) {
+cudaError_t launch_forward(NormParams& p, cudaStream_t st) {
     return p.vec ? launch_forward<kLayer, kStream32, true>(p, st) : launch_forward<kLayer, kStream32, false>(p, st);
 }
 

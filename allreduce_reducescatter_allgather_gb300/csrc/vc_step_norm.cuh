@@ -43,6 +43,8 @@ struct NormParams {
     long long padded;
     int kinds;  // bits of enum kSum
     int teams, blocks;
+    int span;  // blocks of a cluster that share a row
+    unsigned* timeouts;
     Affine dpost, dpre;
 };
 enum { kSumPre = 0, kSumPreBias = 1, kSumPost = 2, kSumPostBias = 3, kSumGate = 4, kSums = 5 };
@@ -60,17 +62,19 @@ struct Stream {
     int words, stage;  // of a row; the one that is read
     int at[kArrays];   // an array's first word
     bool f32[kArrays];
+    int v0;            // the block's first vector
     // what there is of the thread's columns, in bytes of 16 or 32 bits a value, and where
     int bytes[kRing ? 3 : 1][kRing ? kVecs : 1], offset[kRing ? kVecs : 1];
     Raw raw[kRing ? 1 : kArrays][kRing ? 1 : kVecs];
 
-    __device__ __forceinline__ void begin(uint4* shared, int lane, int cols) {
+    __device__ __forceinline__ void begin(uint4* shared, int first, int lane, int cols) {
         ring = shared + threadIdx.x;
         words = stage = 0;
+        v0 = first;
         if constexpr (kRing)
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const int c = (i * kTeam + lane) * 8, n = cols - c;
+                const int c = ((v0 + i) * kTeam + lane) * 8, n = cols - c;
                 bytes[0][i] = max(0, min(16, n * 2));
                 bytes[1][i] = max(0, min(16, n * 4));
                 bytes[2][i] = max(0, min(16, n * 4 - 16));
@@ -99,7 +103,7 @@ struct Stream {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) raw[a][i] = load_raw<kTeam>(x, f32[a], row, kVec, i, lane, cols);
+            for (int i = 0; i < kVecs; ++i) raw[a][i] = load_raw<kTeam>(x, f32[a], row, kVec, v0 + i, lane, cols);
         }
     }
     __device__ __forceinline__ Eight get(int a, int i) const {
@@ -116,30 +120,23 @@ struct Stream {
 };
 
 // A vector of the row's length that is used in every row (a weight, a bias, the gate
-// of the rows at hand): in shared memory, in 32 bits, each thread's own columns, or
-// read where it lies.
-template <int kTeam, int kVecs, bool kVec, bool kHeld>
+// of the rows at hand): in shared memory, in 32 bits, each thread's own columns.
+template <int kTeam, int kVecs, bool kVec>
 struct Held {
-    float4* at;  // [vector][half][lane]
-    static constexpr bool kHolding = kHeld;
     static constexpr int kBytes = kVecs * 2 * kTeam * 16;
+    float4* at;  // [vector][half][lane]
     __device__ __forceinline__ void put(int i, const Eight& x) const {
         at[i * 2 * kTeam] = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
         at[(i * 2 + 1) * kTeam] = make_float4(x.v[4], x.v[5], x.v[6], x.v[7]);
     }
-    __device__ __forceinline__ void hold(const Rows& x, int lane, int cols) const {
-        if constexpr (kHeld)
-            if (x.data != nullptr)
+    __device__ __forceinline__ void hold(const Rows& x, int v0, int lane, int cols) const {
+        if (x.data != nullptr)
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i) put(i, load_any<kTeam>(x, 0, kVec, i, lane, cols));
+            for (int i = 0; i < kVecs; ++i) put(i, load_any<kTeam>(x, 0, kVec, v0 + i, lane, cols));
     }
-    __device__ __forceinline__ Eight get(const Rows& x, int i, int lane, int cols) const {
-        if constexpr (kHeld) {
-            const float4 lo = at[i * 2 * kTeam], hi = at[(i * 2 + 1) * kTeam];
-            return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
-        } else {
-            return load_any<kTeam>(x, 0, kVec, i, lane, cols);
-        }
+    __device__ __forceinline__ Eight get(int i) const {
+        const float4 lo = at[i * 2 * kTeam], hi = at[(i * 2 + 1) * kTeam];
+        return {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
     }
 };
 
@@ -147,13 +144,42 @@ struct Held {
 
 // Sums over a team of up to four values at a time.  A warp's lanes share the values
 // out while they add (of four values each lane keeps two, then one), the warps of a
-// block leave theirs in shared memory.  Calls take turns between two buffers there, so
-// that one barrier a call does.
-template <int kTeam>
+// block leave theirs in shared memory, those of a cluster in that of every block.
+// Calls take turns between two buffers there, so that one wait a call does.
+//
+// In a cluster the values bring their own signal: they are counted on a barrier of the
+// block that they go to.  (The cluster's own barrier also waits for all that its blocks
+// have stored to memory: 1.4 us a call.)  Its waits are bounded as those of the
+// products' kernels are: a block whose wait runs out goes on without, and is counted.
+constexpr int kMaxSpan = 8;  // blocks of a cluster that share a row
+
+struct SpanShared {
+    unsigned long long barrier[2];
+    int dead;
+};
+
+template <int kTeam, bool kSpan>
 struct TeamSums {
-    static constexpr int kWarps = kTeam / 32;
-    float (*shared)[4];  // [2 * kWarps][4]
-    int turn;
+    static constexpr int kWarps = kTeam / 32, kAll = kWarps * (kSpan ? kMaxSpan : 1);
+    float (*shared)[4];  // [2 * kAll][4]
+    int turn, span;      // blocks that share a row
+    SpanShared* signals;
+    unsigned parity;
+    // Of a cluster: before the first call, and after the last one.
+    __device__ __forceinline__ void begin() {
+        const unsigned bar = gemm::smem_u32(signals->barrier);
+        if (threadIdx.x == 0) {
+            signals->dead = 0;
+            gemm::mbar_init(bar, 1);
+            gemm::mbar_init(bar + 8, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        cluster_sync();
+    }
+    __device__ __forceinline__ void end(unsigned* timeouts) {
+        if (threadIdx.x == 0 && *static_cast<volatile int*>(&signals->dead)) atomicAdd(timeouts, 1u);
+        cluster_sync();  // (no block leaves while others still send to it)
+    }
     template <int kN>
     __device__ __forceinline__ void operator()(float (&v)[kN]) {
         static_assert(kN <= 4, "a buffer has four columns");
@@ -179,14 +205,35 @@ struct TeamSums {
 #pragma unroll
             for (int i = 0; i < kN; ++i) v[i] = __shfl_sync(~0u, c, i * (32 / kP));
         } else {
-            float(*buf)[4] = shared + turn * kWarps;
-            turn ^= 1;
-            if (lane % (32 / kP) == 0) buf[threadIdx.x >> 5][lane / (32 / kP)] = c;
-            __syncthreads();
+            float(*buf)[4] = shared + turn * kAll;
             const int q = lane % kP, w = lane / kP;
-            c = w < kWarps ? buf[w][q] : 0.0f;
+            if constexpr (kSpan) {
+                const unsigned bar = gemm::smem_u32(&signals->barrier[turn]);
+                if (lane % (32 / kP) == 0) {
+                    const float* at = &buf[blockIdx.x % span * kWarps + (threadIdx.x >> 5)][lane / (32 / kP)];
+                    for (int r = 0; r < span; ++r)
+                        asm volatile(
+                            "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                                remote_address(at, r)),
+                            "r"(__float_as_uint(c)), "r"(remote_address(&signals->barrier[turn], r))
+                            : "memory");
+                }
+                if (threadIdx.x == 0) gemm::mbar_expect(bar, kWarps * span * kP * 4);
+                gemm::warp_wait(bar, parity >> turn & 1, &signals->dead);
+                parity ^= 1u << turn;
+            } else {
+                if (lane % (32 / kP) == 0) buf[threadIdx.x >> 5][lane / (32 / kP)] = c;
+                __syncthreads();
+            }
+            turn ^= 1;
+            const int warps = kSpan ? kWarps * span : kWarps;
+            c = w < warps ? buf[w][q] : 0.0f;
+            if constexpr (kSpan) {
+                for (int more = w + 32 / kP; more < warps; more += 32 / kP) c += buf[more][q];
+            } else {
 #pragma unroll
-            for (int more = 32 / kP; more < kWarps; more += 32 / kP) c += buf[w + more][q];
+                for (int more = 32 / kP; more < kWarps; more += 32 / kP) c += buf[w + more][q];
+            }
 #pragma unroll
             for (int o = 16; o >= kP; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
 #pragma unroll
@@ -226,9 +273,9 @@ __device__ __forceinline__ Eight centered(const Eight& v, float mean, bool vec, 
 }
 
 // Takes the row's mean off (LAYER) and returns 1 / sqrt(mean square + eps).
-template <int kTeam, int kVecs, bool kLayer>
-__device__ __forceinline__ float center(const NormParams& p, Eight (&v)[kVecs], bool vec, int lane,
-                                        TeamSums<kTeam>& sums) {
+template <int kVecs, bool kLayer, int kTeam, bool kSpan>
+__device__ __forceinline__ float center(const NormParams& p, Eight (&v)[kVecs], bool vec, int v0, int lane,
+                                        TeamSums<kTeam, kSpan>& sums) {
     if constexpr (kLayer) {
         float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -236,7 +283,7 @@ __device__ __forceinline__ float center(const NormParams& p, Eight (&v)[kVecs], 
         float s[1] = {sum_of(part)};
         sums(s);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) v[i] = centered<kTeam>(v[i], s[0] * p.inv_cols, vec, i, lane, p.cols);
+        for (int i = 0; i < kVecs; ++i) v[i] = centered<kTeam>(v[i], s[0] * p.inv_cols, vec, v0 + i, lane, p.cols);
     }
     float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -246,12 +293,12 @@ __device__ __forceinline__ float center(const NormParams& p, Eight (&v)[kVecs], 
     return rsqrtf(fmaf(s[0], p.inv_cols, p.eps));
 }
 
-// Rows that are too long for registers: a block a row, in steps of 8 * kLong
-// columns, the inputs read again for every sum.
+// Rows that are too long for a cluster's registers: a block a row, in steps of 8 *
+// kLong columns, the inputs read again for every sum.
 constexpr int kLong = 512;
 
 template <bool kLayer, class F>
-__device__ __forceinline__ void long_statistics(const NormParams& p, TeamSums<kLong>& sums, int steps, int lane,
+__device__ __forceinline__ void long_statistics(const NormParams& p, TeamSums<kLong, false>& sums, int steps, int lane,
                                                 F load, float& mean, float& rstd) {
     mean = 0.0f;
     if constexpr (kLayer) {
@@ -292,11 +339,15 @@ __device__ __forceinline__ Eight normalised(const NormParams& p, const Affine& a
 
 // ---------------------------------------------------------------- arguments --
 
-// A row of `cols` columns by `team` threads with `vecs` vectors each; team 0: the
-// kernels for long rows.
+// A row of `cols` columns by `team` threads of each of `span` blocks, with `vecs`
+// vectors each; team 0: the kernels for the longest rows.
 struct Shape {
-    int team, vecs;
+    int team, vecs, span;
 };
+
+// Clusters of this many blocks that run at a time, with `per_sm` blocks on an SM: of
+// each of eight groups of SMs 18 are counted on.
+inline int clusters_of(int span, int per_sm) { return 8 * (18 * per_sm / span); }
 
 inline bool valid_affine(const vc_affine_t* a, bool needed) {
     if (a == nullptr || a->weight == nullptr) return !needed && (a == nullptr || a->bias == nullptr);

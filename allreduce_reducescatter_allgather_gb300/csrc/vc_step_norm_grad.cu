@@ -49,81 +49,49 @@ __device__ __forceinline__ void store_gate(const NormParams& p, long long row, b
 
 constexpr int kBackwardThreads = 256;  // of a block of teams that are warps
 
-// One row after the other, the next one's inputs on their way meanwhile.  The column
-// sums of layer norms' long rows, and of long rows that come through registers, find
-// no registers: they lie in shared memory, where each thread adds to its own.
-template <int kTeam, int kVecs, bool kLayer, bool kVec>
-constexpr bool kThroughShared = kVec && !(kLayer && kVecs == 2 && kTeam > 32);
+// One row after the other, the next one's inputs on their way meanwhile, the column sums
+// in registers.
 
-// Weights and the gate of the rows at hand are held in shared memory where there is room.
-template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
-constexpr bool kHolds = kTeam == 32 || kVecs == 1 || (kThroughShared<kTeam, kVecs, kLayer, kVec> && !kStream32);
-
-template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec>
+template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec, bool kSpan = false>
 __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam == 32 ? 2 / kVecs : 512 / kTeam) * (kLayer && !kVec && kVecs == 1 ? 3 : 4) / 4)
     backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kBackwardThreads : kTeam, kTeams = kThreads / kTeam;
     // RMS norms have no biases
     constexpr int kKept = kLayer ? 5 : 3;
     constexpr int kPre = 0, kPost = 1, kGate = 2, kPreBias = 3, kPostBias = 4;
-    constexpr bool kRing = kThroughShared<kTeam, kVecs, kLayer, kVec>;
-    constexpr bool kInShared = kTeam > 32 && kVecs == 2 && !kRing;
+    constexpr bool kRing = kVec;
     constexpr int kR = 0, kDn = 1, kH = 2, kDr = 3, kG = 4;
-    __shared__ float shared[2 * kTeam / 32][4];
+    using Sums = TeamSums<kTeam, kSpan>;
+    __shared__ float shared[2 * Sums::kAll][4];
     __shared__ float joined[kTeams > 1 ? kTeams : 1][kTeams > 1 ? 8 * kTeam * kVecs : 1];
     extern __shared__ uint4 ring[];
-    float4* const columns = reinterpret_cast<float4*>(ring);  // [sum][vector][half][thread]
-    TeamSums<kTeam> sums = {shared, 0};
+    __shared__ SpanShared signals;
+    Sums sums = {shared, 0, p.span, &signals, 0};
+    const int v0 = kSpan ? blockIdx.x % p.span * kVecs : 0;  // the block's first vector
     const int lane = kTeams == 1 ? threadIdx.x : threadIdx.x % 32;
     const int part = kTeams == 1 ? 0 : __shfl_sync(~0u, threadIdx.x / 32, 0);  // the team in the block
-    const long long team = (long long)blockIdx.x * kTeams + part;
+    const long long block = kSpan ? blockIdx.x / p.span : blockIdx.x, team = block * kTeams + part;
     const bool has_pre = p.dn.data != nullptr, has_post = p.post.weight.data != nullptr;
     const bool has_h = p.h.data != nullptr, has_dr = p.dr.data != nullptr;
     const bool full_gate = p.gate_mode == kGateFull;
     const bool sums_gate = p.dgate.data != nullptr && (p.gate_mode == kGateShared || p.gate_mode == kGateGroups);
-    Eight kept[kInShared ? 1 : kKept][kInShared ? 1 : kVecs];
-    auto clear = [&](int k, int i) {
-        if constexpr (kInShared) {
-            float4* at = columns + (k * kVecs + i) * 2 * kTeam + lane;
-            at[0] = at[kTeam] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        } else {
-            kept[k][i] = zeros();
-        }
-    };
-    auto column_sum = [&](int k, int i) {
-        if constexpr (kInShared) {
-            const float4* at = columns + (k * kVecs + i) * 2 * kTeam + lane;
-            const float4 lo = at[0], hi = at[kTeam];
-            return Eight{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
-        } else {
-            return kept[k][i];
-        }
-    };
+    Eight kept[kKept][kVecs];
     // sum k += a b
-    auto add_product = [&](int k, int i, const Eight& a, const Eight& b) {
-        const Eight s = fma(a, b, column_sum(k, i));
-        if constexpr (kInShared) {
-            float4* at = columns + (k * kVecs + i) * 2 * kTeam + lane;
-            at[0] = make_float4(s.v[0], s.v[1], s.v[2], s.v[3]);
-            at[kTeam] = make_float4(s.v[4], s.v[5], s.v[6], s.v[7]);
-        } else {
-            kept[k][i] = s;
-        }
-    };
+    auto add_product = [&](int k, int i, const Eight& a, const Eight& b) { kept[k][i] = fma(a, b, kept[k][i]); };
     const Eight ones = {{1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f}};
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) clear(k, i);
+        for (int i = 0; i < kVecs; ++i) kept[k][i] = zeros();
 
     Stream<kThreads, kTeam, kVecs, 5, kVec, kRing> in;
-    in.begin(ring, lane, p.cols);
+    in.begin(ring, v0, lane, p.cols);
     in.array(kR, has_pre, kStream32);
     in.array(kDn, has_pre, false);
     in.array(kH, has_h, false);
     in.array(kDr, has_dr, kStream32);
     in.array(kG, full_gate, p.gate.f32);
-    using Vector = Held<kTeam, kVecs, kVec, kHolds<kTeam, kVecs, kLayer, kStream32, kVec>>;
+    using Vector = Held<kTeam, kVecs, kVec>;
     float4* const held = reinterpret_cast<float4*>(ring + (kRing ? kStages * in.words * kThreads : 0)) + lane;
     const Vector pre = {held}, post = {held + Vector::kBytes / 16}, shift = {held + 2 * (Vector::kBytes / 16)},
                  held_gate = {held + ((kLayer ? 3 : 2) + part) * (Vector::kBytes / 16)};  // (a team's own)
@@ -136,22 +104,23 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam
         if (has_dr) in.load(kDr, p.dr, row, lane, p.cols);
         if (full_gate) in.load(kG, p.gate, row, lane, p.cols);
     };
+    if constexpr (kSpan) sums.begin();
     pdl_next();
     pdl_wait();
     const long long lo = first_row(p, team), hi = first_row(p, team + 1);
     long long group_end = p.gate_mode == kGateGroups ? (lo / p.group + 1) * p.group : 0;
     if (lo < hi) load(lo);
     // (threads read what they have written themselves)
-    pre.hold(p.pre.weight, lane, p.cols);
-    post.hold(p.post.weight, lane, p.cols);
-    if constexpr (kLayer) shift.hold(p.post.bias, lane, p.cols);
+    pre.hold(p.pre.weight, v0, lane, p.cols);
+    post.hold(p.post.weight, v0, lane, p.cols);
+    if constexpr (kLayer) shift.hold(p.post.bias, v0, lane, p.cols);
     long long g = p.gate_mode == kGateGroups ? lo / p.group : 0;  // the rows' gate
     bool new_gate = p.gate_mode == kGateShared || p.gate_mode == kGateGroups;
     for (long long row = lo; row < hi; ++row) {
-        if (Vector::kHolding && new_gate) {
+        if (new_gate) {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
-                held_gate.put(i, gate_value(load_any<kTeam>(p.gate, g, kVec, i, lane, p.cols), p.sigmoid));
+                held_gate.put(i, gate_value(load_any<kTeam>(p.gate, g, kVec, v0 + i, lane, p.cols), p.sigmoid));
             new_gate = false;
         }
         if constexpr (kRing) {
@@ -176,11 +145,11 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam
         }
         auto centered_r = [&](int i) {
             const Eight r = in.get(kR, i);
-            return kLayer ? centered<kTeam>(r, mean, kVec, i, lane, p.cols) : r;
+            return kLayer ? centered<kTeam>(r, mean, kVec, v0 + i, lane, p.cols) : r;
         };
         auto centered_h = [&](int i) {
             const Eight h = in.get(kH, i);
-            return kLayer && has_post ? centered<kTeam>(h, h_mean, kVec, i, lane, p.cols) : h;
+            return kLayer && has_post ? centered<kTeam>(h, h_mean, kVec, v0 + i, lane, p.cols) : h;
         };
         float rstd, h_rstd, m1 = 0.0f, m2;
         {
@@ -189,7 +158,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam
             for (int i = 0; i < kVecs; ++i) {
                 if (has_pre) {
                     const Eight r = centered_r(i);
-                    const Eight g = mul(pre.get(p.pre.weight, i, lane, p.cols), in.get(kDn, i));
+                    const Eight g = mul(pre.get(i), in.get(kDn, i));
                     dot(a, r, r);
                     dot(b, g, r);
                     if constexpr (kLayer) total(c, g);
@@ -220,7 +189,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam
             Eight dr = has_dr ? in.get(kDr, i) : zeros();
             if (has_pre) {
                 const Eight r = mul(rstd, centered_r(i)), dn = in.get(kDn, i);
-                const Eight w = pre.get(p.pre.weight, i, lane, p.cols);
+                const Eight w = pre.get(i);
                 add_product(kPre, i, dn, r);
                 if constexpr (kLayer) add_product(kPreBias, i, dn, ones);
                 dr = fma(-m2, r, dr);
@@ -228,34 +197,34 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam
                 dr = fma(mul(rstd, w), dn, dr);
             }
             if (p.dx.data != nullptr)
-                store_any<kTeam>(p.dx, kStream32, row, kVec, i, lane, p.cols, mul(p.scale, dr));
+                store_any<kTeam>(p.dx, kStream32, row, kVec, v0 + i, lane, p.cols, mul(p.scale, dr));
             Eight w, hat;
             if (has_h) hat = centered_h(i);
             if (has_post) {
-                w = post.get(p.post.weight, i, lane, p.cols);
+                w = post.get(i);
                 hat = mul(h_rstd, hat);
             }
             if constexpr (!kRing) kept_hat[i] = hat;
             du[i] = dr;
             if (p.gate_mode != kGateNone) {
                 Eight gate, value;
-                if (full_gate || !Vector::kHolding) {
-                    gate = full_gate ? in.get(kG, i) : load_any<kTeam>(p.gate, g, kVec, i, lane, p.cols);
+                if (full_gate) {
+                    gate = in.get(kG, i);
                     value = gate_value(gate, p.sigmoid);
                 } else {
-                    value = held_gate.get(p.gate, i, lane, p.cols);
+                    value = held_gate.get(i);
                 }
                 if (p.dgate.data != nullptr) {
                     Eight u = hat;
                     if (has_post) {
                         u = mul(u, w);
                         if (kLayer && p.post.bias.data != nullptr)
-                            u = add(u, shift.get(p.post.bias, i, lane, p.cols));
+                            u = add(u, shift.get(i));
                     }
                     if (sums_gate)
                         add_product(kGate, i, u, dr);
                     else
-                        store_gate<kTeam>(p, row, kVec, i, lane, mul(u, dr), gate);
+                        store_gate<kTeam>(p, row, kVec, v0 + i, lane, mul(u, dr), gate);
                 }
                 du[i] = mul(dr, value);
             }
@@ -274,8 +243,8 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam
             if (sums_gate)
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    flush_gate<kTeam>(p, team, g, lo, hi, kVec, i, lane, column_sum(kGate, i));
-                    clear(kGate, i);
+                    flush_gate<kTeam>(p, team, g, lo, hi, kVec, v0 + i, lane, kept[kGate][i]);
+                    kept[kGate][i] = zeros();
                 }
             group_end += p.group;
             ++g;
@@ -303,8 +272,9 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam
             }
         }
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.dh, false, row, kVec, i, lane, p.cols, du[i]);
+        for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.dh, false, row, kVec, v0 + i, lane, p.cols, du[i]);
     }
+    if constexpr (kSpan) sums.end(p.timeouts);
     // the column sums
     const Rows parts = {p.parts, p.padded, 1, 1};
 #pragma unroll
@@ -312,19 +282,18 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam
         const int kind = k == kPre ? kSumPre : k == kPost ? kSumPost : k == kGate ? kSumGate
                          : k == kPreBias ? kSumPreBias : kSumPostBias;
         if (!(p.kinds >> kind & 1)) continue;
-        const long long at = (long long)blockIdx.x * kSums + kind;
+        const long long at = block * kSums + kind;
         if constexpr (kTeams == 1) {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
-                store_any<kTeam>(parts, true, at, kVec, i, lane, p.cols, column_sum(k, i));
+                store_any<kTeam>(parts, true, at, kVec, v0 + i, lane, p.cols, kept[k][i]);
         } else {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const Eight sum = column_sum(k, i);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    joined[part][column<kTeam>(kVec, i, lane, j)] = sum.v[j];
+                    joined[part][column<kTeam>(kVec, i, lane, j)] = kept[k][i].v[j];
             }
             __syncthreads();
             for (int c = threadIdx.x; c < p.cols; c += kThreads) {
@@ -337,12 +306,12 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam
     }
 }
 
-// The same for rows too long for registers: the column sums lie in the block's
-// parts, where each thread adds to its own columns.
+// The longest rows, read again for every pass (from the second-level cache); the column sums lie in the block's parts, where each thread adds to its own
+// columns.
 template <bool kLayer, bool kStream32>
 __global__ void __launch_bounds__(kLong) backward_long_kernel(const __grid_constant__ NormParams p) {
     __shared__ float shared[2 * kLong / 32][4];
-    TeamSums<kLong> sums = {shared, 0};
+    TeamSums<kLong, false> sums = {shared, 0, 1, nullptr, 0};
     const int lane = threadIdx.x, steps = (p.cols + 8 * kLong - 1) / (8 * kLong);
     const bool has_pre = p.dn.data != nullptr, has_post = p.post.weight.data != nullptr;
     const bool sums_gate = p.dgate.data != nullptr && (p.gate_mode == kGateShared || p.gate_mode == kGateGroups);
@@ -477,6 +446,32 @@ __global__ void __launch_bounds__(kLong) backward_long_kernel(const __grid_const
     }
 }
 
+// A group of rows that several teams have, from the one that has its first row to the
+// one that has its last.
+struct Spanning {
+    int first, last, group;
+};
+constexpr int kJoinTeams = 256;  // that are looked at together
+
+// The spanning groups that start with the teams t0, t0 + step, ... of kJoinTeams; their
+// number.
+__device__ __forceinline__ int find_spanning(const NormParams& p, int t0, int step, Spanning* found) {
+    int* const count = &found[kJoinTeams].first;
+    if (threadIdx.x == 0) *count = 0;
+    __syncthreads();
+    const long long t = t0 + (long long)threadIdx.x * step;
+    if (threadIdx.x < kJoinTeams && t < p.teams) {
+        const long long lo = first_row(p, t), hi = first_row(p, t + 1), g = (hi - 1) / p.group;
+        if (g * p.group >= lo && (g + 1) * p.group > hi) {
+            // (which place a group gets changes nothing but the order of work)
+            const long long last = ((g + 1) * p.group * p.teams - 1) / p.rows;
+            found[atomicAdd(count, 1)] = {(int)t, (int)last, (int)g};
+        }
+    }
+    __syncthreads();
+    return *count;
+}
+
 // The parts of 32 columns, by 32 warps in turn: blocks y < kSums the column sums,
 // the others gate rows whose rows several teams have.
 constexpr int kJoinRows = 16;
@@ -529,43 +524,63 @@ __global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ No
             : kind == kSumPost ? p.dpost.weight : kind == kSumPostBias ? p.dpost.bias : p.dgate, 0, s);
         return;
     }
-    // teams whose last row's group starts with them and goes on behind them
-    __shared__ int found[1025];
-    for (int t0 = kind - kSums; t0 < p.teams; t0 += kJoinRows * 1024) {
-        if (threadIdx.x == 0) found[1024] = 0;
-        __syncthreads();
-        const long long mine = t0 + (long long)threadIdx.x * kJoinRows;
-        if (mine < p.teams) {
-            const long long lo = first_row(p, mine), hi = first_row(p, mine + 1), g = (hi - 1) / p.group;
-            // (which place a team gets changes nothing but the order of work)
-            if (g * p.group >= lo && (g + 1) * p.group > hi) found[atomicAdd(&found[1024], 1)] = (int)mine;
-        }
-        __syncthreads();
-        const int n = found[1024];
+    // few groups, of many teams each
+    __shared__ Spanning found[kJoinTeams + 1];
+    for (int t0 = kind - kSums; t0 < p.teams; t0 += kJoinRows * kJoinTeams) {
+        const int n = find_spanning(p, t0, kJoinRows, found);
         for (int f = 0; f < n; ++f) {
-            const int t = found[f];
-            const long long g = (first_row(p, t + 1) - 1) / p.group;
-            const int last = (int)(((g + 1) * p.group * p.teams - 1) / p.rows);  // the team of its last row
             float s = 0.0f;
             if (live)
 #pragma unroll 4
-                for (int w = t + warp; w <= last; w += 32)
-                    s += p.slots[((long long)w * 2 + (w == t ? 1 : 0)) * p.padded + c];
+                for (int w = found[f].first + warp; w <= found[f].last; w += 32)
+                    s += p.slots[((long long)w * 2 + (w == found[f].first ? 1 : 0)) * p.padded + c];
             s = total(s);
-            put(p.dgate, g, s * slope(g));
+            put(p.dgate, found[f].group, s * slope(found[f].group));
         }
         __syncthreads();
     }
 }
 
-Shape backward_shape(int cols) {
-    if (cols <= 256) return {32, 1};
-    if (cols <= 512) return {32, 2};
-    if (cols <= 1024) return {128, 1};
-    if (cols <= 2048) return {256, 1};
-    if (cols <= 4096) return {512, 1};
-    if (cols <= 8192) return {512, 2};
-    return {0, 0};
+// Many groups, of a few teams each: a thread a column.
+__global__ void __launch_bounds__(kJoinTeams) gates_kernel(const __grid_constant__ NormParams p) {
+    __shared__ Spanning found[kJoinTeams + 1];
+    pdl_next();
+    pdl_wait();
+    const long long c = (long long)blockIdx.x * kJoinTeams + threadIdx.x;
+    for (int t0 = blockIdx.y; t0 < p.teams; t0 += gridDim.y * kJoinTeams) {
+        const int n = find_spanning(p, t0, gridDim.y, found);
+        if (c < p.cols)
+#pragma unroll 2
+            for (int f = 0; f < n; ++f) {
+                const Spanning s = found[f];
+                float sum = p.slots[((long long)s.first * 2 + 1) * p.padded + c];
+                for (int w = s.first + 1; w <= s.last; ++w) sum += p.slots[(long long)w * 2 * p.padded + c];
+                const long long from = (long long)s.group * p.gate.ld + c, to = (long long)s.group * p.dgate.ld + c;
+                sum *= gate_slope(p.gate.f32 ? static_cast<const float*>(p.gate.data)[from]
+                                             : __bfloat162float(static_cast<const __nv_bfloat16*>(p.gate.data)[from]),
+                                  p.sigmoid);
+                if (p.dgate.f32) {
+                    float* f32 = static_cast<float*>(p.dgate.data) + to;
+                    *f32 = p.accumulate ? *f32 + sum : sum;
+                } else {
+                    __nv_bfloat16* b16 = static_cast<__nv_bfloat16*>(p.dgate.data) + to;
+                    *b16 = __float2bfloat16(p.accumulate ? __bfloat162float(*b16) + sum : sum);
+                }
+            }
+        __syncthreads();
+    }
+}
+
+// in_two: rows of up to 8192 values by two vectors a thread.
+Shape backward_shape(int cols, bool in_two) {
+    if (cols <= 256) return {32, 1, 1};
+    if (cols <= 512) return {32, 2, 1};
+    if (cols <= 1024) return {128, 1, 1};
+    if (cols <= 2048) return {256, 1, 1};
+    if (cols <= 4096) return {512, 1, 1};
+    if (cols <= 8192 && in_two) return {512, 2, 1};
+    if (cols <= 4096 * kMaxSpan) return {512, 1, (cols + 4095) / 4096};
+    return {0, 0, 1};
 }
 
 // Blocks and teams of the gradient.
@@ -574,57 +589,67 @@ struct Split {
     int blocks, teams, threads;
     long long padded;
 };
-Split split_of(long long rows, long long cols) {
+Split split_of(long long rows, long long cols, bool in_two) {
     Split s = {};
-    s.shape = backward_shape((int)std::min(cols, 1ll << 20));
+    s.shape = backward_shape((int)std::min(cols, 1ll << 20), in_two);
     const int team = s.shape.team == 0 ? kLong : s.shape.team;
     s.threads = team == 32 ? kBackwardThreads : team;
     const int per = s.threads / team;
     // two rows a team at least, so that the parts stay few beside the rows
     const long long want = (rows + 2 * per - 1) / (2 * per);
-    s.blocks = (int)std::max(1ll, std::min(want, (long long)kSMs * (team == 32 ? 2 / s.shape.vecs : std::max(1, 512 / s.threads))));
+    const long long most = s.shape.span > 1 ? clusters_of(s.shape.span, 1)
+                           : (long long)kSMs * (team == 32 ? 2 / s.shape.vecs : std::max(1, 512 / s.threads));
+    s.blocks = (int)std::max(1ll, std::min(want, most));  // or clusters
     s.teams = (int)std::min(rows, (long long)s.blocks * per);  // (the others have no rows)
     s.padded = (cols + 7) / 8 * 8;
     return s;
 }
 
 template <bool kLayer, bool kStream32, bool kVec>
-cudaError_t launch_backward(const NormParams& p, const Split& s, cudaStream_t st) {
-    const bool ring = s.shape.team == 32 ? kVec : kVec && !(kLayer && s.shape.vecs == 2);
-    size_t bytes = 0;
-    if (s.shape.team != 0 && ring)
-        bytes = (size_t)kStages * s.threads * s.shape.vecs * 16 *
-                ((p.dn.data == nullptr ? 0 : kStream32 ? 3 : 2) + (p.h.data != nullptr) +
-                 (p.dr.data == nullptr ? 0 : kStream32 ? 2 : 1) +
-                 (p.gate_mode != kGateFull ? 0 : p.gate.f32 ? 2 : 1));
-    else if (s.shape.team > 32 && s.shape.vecs == 2)
-        bytes = (size_t)(kLayer ? 5 : 3) * s.shape.team * s.shape.vecs * 32;
-    // weights and gate that are held beside it
-    if (s.shape.team == 32 || s.shape.vecs == 1 || (s.shape.team != 0 && ring && !kStream32))
-        bytes += (size_t)((kLayer ? 3 : 2) * s.shape.team +
-                          (p.gate_mode == kGateShared || p.gate_mode == kGateGroups ? s.threads : 0)) *
-                 s.shape.vecs * 32;
-    // (what does not fit, as a 32-bit gate for every element of the longest rows, is read again)
-    const bool fits = bytes + 1024 <= kSharedLimit;
-    if (!fits) bytes = 0;
-    void (*kernel)(NormParams);
-    switch (fits ? s.shape.team * 4 + s.shape.vecs : 0) {
+cudaError_t launch_backward(NormParams& p, const Split& s, cudaStream_t st) {
+    // 16-byte words a thread has of a vector of the inputs of one row
+    const size_t words = (p.dn.data == nullptr ? 0 : kStream32 ? 3 : 2) + (p.h.data != nullptr) +
+                         (p.dr.data == nullptr ? 0 : kStream32 ? 2 : 1) +
+                         (p.gate_mode != kGateFull ? 0 : p.gate.f32 ? 2 : 1);
+    const bool summed_gate =
+        p.dgate.data != nullptr && (p.gate_mode == kGateShared || p.gate_mode == kGateGroups);
+    const bool groups = summed_gate && p.gate_mode == kGateGroups;
+    // two rows' inputs; held weights and gates
+    size_t bytes = kVec ? kStages * words * s.shape.vecs * s.threads * 16 : 0;
+    bytes += (size_t)((kLayer ? 3 : 2) * s.shape.team +
+                      (p.gate_mode == kGateShared || p.gate_mode == kGateGroups ? s.threads : 0)) *
+             s.shape.vecs * 32;
+    p.span = s.shape.span;
+    if (p.span > 1 && (p.timeouts = gemm::timeout_counter()) == nullptr) return cudaErrorInvalidValue;
+    void (*kernel)(NormParams) = nullptr;
+    switch (s.shape.team * 4 + s.shape.vecs) {
     case 32 * 4 + 1: kernel = backward_kernel<32, 1, kLayer, kStream32, kVec>; break;
     case 32 * 4 + 2: kernel = backward_kernel<32, 2, kLayer, kStream32, kVec>; break;
     case 128 * 4 + 1: kernel = backward_kernel<128, 1, kLayer, kStream32, kVec>; break;
     case 256 * 4 + 1: kernel = backward_kernel<256, 1, kLayer, kStream32, kVec>; break;
-    case 512 * 4 + 1: kernel = backward_kernel<512, 1, kLayer, kStream32, kVec>; break;
-    case 512 * 4 + 2: kernel = backward_kernel<512, 2, kLayer, kStream32, kVec>; break;
-    default: kernel = backward_long_kernel<kLayer, kStream32>;
+    case 512 * 4 + 1:
+        kernel = s.shape.span > 1 ? backward_kernel<512, 1, kLayer, kStream32, kVec, true>
+                                  : backward_kernel<512, 1, kLayer, kStream32, kVec>;
+        break;
+    case 512 * 4 + 2: kernel = backward_kernel<512, 2, false, false, true>; break;
+    default: kernel = backward_long_kernel<kLayer, kStream32>; bytes = 0;
     }
-    cudaError_t e = launch_pdl_shared(kernel, dim3(s.blocks), dim3(s.threads), bytes, st, p);
-    const bool groups = p.dgate.data != nullptr && p.gate_mode == kGateGroups;
+    cudaError_t e = launch_pdl_shared(kernel, dim3(s.blocks * s.shape.span), dim3(s.threads), bytes, s.shape.span, st, p);
     if (e != cudaSuccess || (p.kinds == 0 && !groups)) return e;
-    const dim3 grid((unsigned)((p.cols + 31) / 32), kSums + (groups ? std::min(kJoinRows, s.teams) : 0));
-    return launch_pdl(finish_kernel, grid, dim3(1024), st, p);
+    const unsigned across = (unsigned)((p.cols + 31) / 32);
+    const long long per_group = s.teams / (p.rows / p.group);  // teams
+    const bool few = groups && per_group > 16;
+    if (p.kinds != 0 || few) {
+        e = launch_pdl(finish_kernel, dim3(across, kSums + (few ? std::min(kJoinRows, s.teams) : 0)), dim3(1024), st, p);
+        if (e != cudaSuccess) return e;
+    }
+    if (groups && !few)
+        e = launch_pdl(gates_kernel, dim3((p.cols + kJoinTeams - 1) / kJoinTeams, std::min(64, s.teams)),
+                       dim3(kJoinTeams), st, p);
+    return e;
 }
 template <bool kLayer, bool kStream32>
-cudaError_t launch_backward(const NormParams& p, const Split& s, cudaStream_t st) {
+cudaError_t launch_backward(NormParams& p, const Split& s, cudaStream_t st) {
     return p.vec ? launch_backward<kLayer, kStream32, true>(p, s, st)
                  : launch_backward<kLayer, kStream32, false>(p, s, st);
 }
@@ -642,9 +667,10 @@ size_t vc_block_norm_backward_workspace(long long rows, long long cols, long lon
     if (rows <= 0 || rows > train::kMaxExtent || cols <= 0 || cols > train::kMaxExtent || gates < 0 ||
         gates > rows)
         return 0;
-    const Split s = split_of(rows, cols);
-    const size_t parts = (size_t)s.blocks * kSums * s.padded * 4;
-    const size_t slots = gates > 1 && gates < rows ? (size_t)s.teams * 2 * s.padded * 4 : 0;
+    // (of the two ways that rows of up to 8192 values may take, the one that needs more)
+    const Split a = split_of(rows, cols, false), s = split_of(rows, cols, true);
+    const size_t parts = (size_t)std::max(a.blocks, s.blocks) * kSums * s.padded * 4;
+    const size_t slots = gates > 1 && gates < rows ? (size_t)std::max(a.teams, s.teams) * 2 * s.padded * 4 : 0;
     return round256(parts) + round256(slots);
 }
 
@@ -736,7 +762,11 @@ vc_status_t vc_block_norm_backward(const vc_block_norm_in_t* in, const vc_affine
     if (!post_work) p.post = {};
     p.vec = all_vec({&p.h, &p.r, &p.gate, &p.dr, &p.dn, &p.dx, &p.dh, &p.dgate, &p.post.weight, &p.post.bias,
                      &p.pre.weight});
-    const Split s = split_of(T, D);
+    // (RMS norms of 16-bit streams on 16 bytes have the registers; not with a gate in 32
+    // bits for every element, whose rows would not find their place in shared memory)
+    const bool in_two = p.vec && !layer && stream_like->dtype == VC_BFLOAT16 &&
+                        !(p.gate_mode == kGateFull && p.gate.f32);
+    const Split s = split_of(T, D, in_two);
     p.blocks = s.blocks;
     p.teams = s.teams;
     p.padded = s.padded;

@@ -38,7 +38,8 @@ def env():
     import allreduce_reducescatter_allgather_gb300 as vc
     dev = torch.device("cuda:0")
     torch.cuda.set_device(dev)
-    return torch, vc, dev
+    yield torch, vc, dev
+    assert vc.train_timeouts() == 0
 
 
 def dt(torch, name):
@@ -456,6 +457,18 @@ def test_block_forward_widths(env, cols, stream, norm):
         b = Block(torch, dev, rows, cols, norm, stream, gates=gates_of(GATES[(cols + i) % 4], rows),
                   bias=norm == "layer", act=("none", "sigmoid")[i])
         check_forward(env, b)
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("cols", [32768, 33000, 40001, 65536, 70004])
+def test_block_longest_rows(env, cols, norm):
+    """Rows at the ends of what a cluster of blocks shares, and beyond."""
+    for i, gate in enumerate(GATES):
+        stream = ("bf16", "f32")[i % 2]
+        b = Block(env[0], env[2], 6, cols, norm, stream, gates_of(gate, 6), True, norm == "layer",
+                  ("none", "sigmoid")[i // 2])
+        check_forward(env, b)
+        check_backward(env, b)
 
 
 @pytest.mark.parametrize("norm", ["rms", "layer"])
