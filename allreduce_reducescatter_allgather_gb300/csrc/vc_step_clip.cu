@@ -358,9 +358,9 @@ bool tiles_alias(vc_clip_tile_t* tiles, int n) {
         return (uintptr_t)t.count * (t.flags & kTileF32 ? 4 : 2);
     };
     auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
-    std::sort(tiles, tiles + n, [&](const vc_clip_tile_t& a, const vc_clip_tile_t& b) {
-        return at(a.dst) < at(b.dst);
-    });
+    auto by_place = [&](const vc_clip_tile_t& a, const vc_clip_tile_t& b) { return at(a.dst) < at(b.dst); };
+    const bool sorted = std::is_sorted(tiles, tiles + n, by_place);
+    if (!sorted) std::sort(tiles, tiles + n, by_place);
     bool bad = false;
     for (int i = 0; i + 1 < n; ++i) bad = bad || at(tiles[i].dst) + bytes(tiles[i]) > at(tiles[i + 1].dst);
     for (int i = 0; i < n && !bad; ++i) {
@@ -371,8 +371,9 @@ bool tiles_alias(vc_clip_tile_t* tiles, int n) {
         for (; o != tiles + n && at(o->dst) < hi && !bad; ++o)
             bad = !(o == tiles + i && at(o->dst) == lo);
     }
-    std::sort(tiles, tiles + n,
-              [](const vc_clip_tile_t& a, const vc_clip_tile_t& b) { return a.index < b.index; });
+    if (!sorted)
+        std::sort(tiles, tiles + n,
+                  [](const vc_clip_tile_t& a, const vc_clip_tile_t& b) { return a.index < b.index; });
     return bad;
 }
 

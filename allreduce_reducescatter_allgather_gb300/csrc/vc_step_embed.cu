@@ -110,17 +110,17 @@ constexpr int kMarkRows = 16384;    // rows that a block marks at a time
 struct ZeroRows {
     char* out;
     long long row_bytes, pitch;
-    int vec;  // rows on 16 bytes
 };
 __device__ __forceinline__ void zero_row(const ZeroRows& z, unsigned row, int lane) {
-    char* at = z.out + (long long)row * z.pitch;
-    long long done = 0;
-    if (z.vec) {
-        done = z.row_bytes & ~15ll;
-        for (long long c = lane * 16; c < done; c += 512)
-            __stcs(reinterpret_cast<uint4*>(at + c), make_uint4(0, 0, 0, 0));
-    }
-    for (long long c = done + lane * 2; c < z.row_bytes; c += 64) *reinterpret_cast<unsigned short*>(at + c) = 0;
+    char* const at = z.out + (long long)row * z.pitch;
+    // 16 bytes at a time between the first and the last 16-byte boundary
+    const long long head = min(z.row_bytes, (long long)(-reinterpret_cast<uintptr_t>(at) & 15));
+    const long long done = head + ((z.row_bytes - head) & ~15ll);
+    for (long long c = head + lane * 16; c < done; c += 512)
+        __stcs(reinterpret_cast<uint4*>(at + c), make_uint4(0, 0, 0, 0));
+    const int edge = lane * 2;  // (of less than 16 bytes each, in elements of two bytes)
+    if (edge < head) *reinterpret_cast<unsigned short*>(at + edge) = 0;
+    if (done + edge < z.row_bytes) *reinterpret_cast<unsigned short*>(at + done + edge) = 0;
 }
 
 struct SortParams {
@@ -680,6 +680,8 @@ int window_of(long long tokens, long long cols) {
     return w;
 }
 
+constexpr long long kMaxColumns = 1 << 22;
+static_assert(kMaxColumns / kJoinColumns <= 65535, "a grid's second extent");
 constexpr long long kMaxTokens = train::kMaxExtent;  // (sums with a block's share fit ints)
 
 struct BackwardSpace {
@@ -772,7 +774,7 @@ vc_status_t vc_embedding_forward(const void* ids, vc_dtype_t id_dtype, long long
 
 size_t vc_embedding_backward_workspace(long long tokens, long long rows, long long cols) {
     if (tokens < 0 || tokens > kMaxTokens || rows < 0 || rows > train::kMaxExtent || cols < 0 ||
-        cols > train::kMaxExtent)
+        cols > kMaxColumns)
         return 0;
     if (tokens == 0 || rows == 0 || cols == 0) return 0;
     const BackwardSpace s = space_of(tokens, rows, cols);
@@ -787,6 +789,7 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
         dy->cols != dweight->cols || !valid_ids(ids, id_dtype, dy->rows, first))
         return VC_ERR_INVALID_ARGUMENT;
     const long long tokens = dy->rows, V = dweight->rows, D = dweight->cols;
+    if (D > kMaxColumns) return VC_ERR_INVALID_ARGUMENT;
     const size_t need = vc_embedding_backward_workspace(tokens, V, D);
     if (!workspace_ok(workspace, workspace_bytes, need)) return VC_ERR_INVALID_ARGUMENT;
     const Span outs[2] = {span_of(dweight), span_of(workspace, need)};
@@ -819,7 +822,7 @@ vc_status_t vc_embedding_backward(const vc_matrix_t* dy, const void* ids, vc_dty
     s.b = reinterpret_cast<uint2*>(ws + sp.pairs);
     const Rows dw = rows_of(dweight);
     const int es = elem_size(dweight->dtype);
-    s.zero = {static_cast<char*>(dw.data), D * es, dw.ld * es, dw.vec};
+    s.zero = {static_cast<char*>(dw.data), D * es, dw.ld * es};
     // what can be zeroed while the tokens are sorted (13 us for 16384 of them, 28 us for
     // 65536), at 4 TB/s
     const long long early = tokens == 0 ? V : ((16ll << 20) + 1400 * tokens) / (D * es);

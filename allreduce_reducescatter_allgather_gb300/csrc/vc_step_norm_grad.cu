@@ -49,11 +49,15 @@ __device__ __forceinline__ void store_gate(const NormParams& p, long long row, b
 
 constexpr int kBackwardThreads = 256;  // of a block of teams that are warps
 
+// Blocks on an SM; one less of four where layer norms' rows come through registers.
+template <int kTeam, int kVecs, bool kCrowded>
+constexpr int backward_resident = kTeam == 32 ? 2 / kVecs : kTeam == 128 && kCrowded ? 3 : 512 / kTeam;
+
 // One row after the other, the next one's inputs on their way meanwhile, the column sums
 // in registers.
 
 template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec, bool kSpan = false>
-__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, (kTeam == 32 ? 2 / kVecs : 512 / kTeam) * (kLayer && !kVec && kVecs == 1 ? 3 : 4) / 4)
+__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, backward_resident<kTeam, kVecs, kLayer && !kVec>)
     backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kBackwardThreads : kTeam, kTeams = kThreads / kTeam;
     // RMS norms have no biases
@@ -589,7 +593,7 @@ struct Split {
     int blocks, teams, threads;
     long long padded;
 };
-Split split_of(long long rows, long long cols, bool in_two) {
+Split split_of(long long rows, long long cols, bool in_two, bool crowded) {
     Split s = {};
     s.shape = backward_shape((int)std::min(cols, 1ll << 20), in_two);
     const int team = s.shape.team == 0 ? kLong : s.shape.team;
@@ -598,7 +602,9 @@ Split split_of(long long rows, long long cols, bool in_two) {
     // two rows a team at least, so that the parts stay few beside the rows
     const long long want = (rows + 2 * per - 1) / (2 * per);
     const long long most = s.shape.span > 1 ? clusters_of(s.shape.span, 1)
-                           : (long long)kSMs * (team == 32 ? 2 / s.shape.vecs : std::max(1, 512 / s.threads));
+                           : (long long)kSMs * (team == 32                ? 2 / s.shape.vecs
+                                               : team == 128 && crowded ? 3
+                                                                        : 512 / s.threads);
     s.blocks = (int)std::max(1ll, std::min(want, most));  // or clusters
     s.teams = (int)std::min(rows, (long long)s.blocks * per);  // (the others have no rows)
     s.padded = (cols + 7) / 8 * 8;
@@ -667,8 +673,8 @@ size_t vc_block_norm_backward_workspace(long long rows, long long cols, long lon
     if (rows <= 0 || rows > train::kMaxExtent || cols <= 0 || cols > train::kMaxExtent || gates < 0 ||
         gates > rows)
         return 0;
-    // (of the two ways that rows of up to 8192 values may take, the one that needs more)
-    const Split a = split_of(rows, cols, false), s = split_of(rows, cols, true);
+    // (of the ways that rows of such a length may take, the one that needs most)
+    const Split a = split_of(rows, cols, false, false), s = split_of(rows, cols, true, false);
     const size_t parts = (size_t)std::max(a.blocks, s.blocks) * kSums * s.padded * 4;
     const size_t slots = gates > 1 && gates < rows ? (size_t)std::max(a.teams, s.teams) * 2 * s.padded * 4 : 0;
     return round256(parts) + round256(slots);
@@ -766,7 +772,7 @@ vc_status_t vc_block_norm_backward(const vc_block_norm_in_t* in, const vc_affine
     // bits for every element, whose rows would not find their place in shared memory)
     const bool in_two = p.vec && !layer && stream_like->dtype == VC_BFLOAT16 &&
                         !(p.gate_mode == kGateFull && p.gate.f32);
-    const Split s = split_of(T, D, in_two);
+    const Split s = split_of(T, D, in_two, layer && !p.vec);
     p.blocks = s.blocks;
     p.teams = s.teams;
     p.padded = s.padded;

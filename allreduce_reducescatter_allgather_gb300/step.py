@@ -415,7 +415,7 @@ class ClipPlan(PreparedOperator):
         check_status(L.vc_clip_plan(*tables, tiles, ntiles.value, ctypes.byref(ntiles)))
         self.ntiles = ntiles.value
         # the table and the workspace are one allocation, which follows the calls' streams
-        table = torch.frombuffer(bytearray(bytes(tiles)), dtype=torch.uint8)
+        table = torch.frombuffer(tiles, dtype=torch.uint8)
         at = -(-table.numel() // 256) * 256
         size = int(L.vc_clip_workspace(self.ntiles))
         ws, _, held, made = _workspace(None, at + size, dev, None, 256)

@@ -53,8 +53,9 @@ size_t vc_embedding_backward_workspace(long long tokens, long long rows, long lo
  * row of dweight is written: with zeros where no token is, unless `accumulate` is
  * non-zero, which adds to the rows that tokens have and leaves the others as they
  * are.  dy and dweight float32 or bfloat16, each by itself.  The tokens are sorted by
- * row first, so that no row is written twice, whatever the ids are.  At most 2^30
- * tokens. */
+ * row first, so that no block adds to another's sums, whatever the ids are.  At most 2^30
+ * tokens and 2^22 columns.  (Where accumulate adds to float32 values, sums below 2^-126
+ * become 0.) */
 vc_status_t vc_embedding_backward(const vc_matrix_t *dy, const void *ids, vc_dtype_t id_dtype,
                                   long long first, long long padding, float scale,
                                   const vc_matrix_t *dweight, int accumulate, void *workspace,
@@ -87,7 +88,8 @@ typedef struct {
  * is that of the T / G rows from g T / G on (G = 1: one vector for all; G = T:
  * a value for every element).  r or n NULL: not stored; n needs pre->weight.  n is computed
  * from r in 32 bits, before its rounding.  r may be x itself and n may be h
- * itself.  post and pre may be NULL where there is no such norm. */
+ * itself.  post and pre may be NULL where there is no such norm.  The squares of a row's
+ * values must have a sum that float32 holds. */
 vc_status_t vc_block_norm_forward(const vc_matrix_t *h, const vc_matrix_t *x,
                                   const vc_matrix_t *gate, const vc_affine_t *post,
                                   const vc_affine_t *pre, const vc_block_norm_t *args,
@@ -163,7 +165,8 @@ typedef enum { VC_GRAD_NORM_L2 = 0, VC_GRAD_NORM_MAX = 1 } vc_grad_norm_t;
 /* Bytes of workspace for both of the following. */
 size_t vc_clip_workspace(int ntiles);
 
-/* *norm (device memory) <- the norm of the planned gradients.  dev_tiles: DEVICE
+/* *norm (device memory, outside of the gradients and outputs; not checked) <- the norm
+ * of the planned gradients.  dev_tiles: DEVICE
  * array of the ntiles tiles (16-byte aligned), as planned: tables that differ from the
  * planned ones are undefined behaviour, as for any device copy.  No tiles: 0. */
 vc_status_t vc_grad_norm(const vc_clip_tile_t *dev_tiles, int ntiles, vc_grad_norm_t kind,

@@ -136,8 +136,8 @@ vc_status_t vc_muon_step(const vc_matrix_t *weight, const vc_matrix_t *grad,
                          const vc_matrix_t *momentum, const vc_muon_t *args, void *workspace,
                          size_t workspace_bytes, vc_stream_t stream);
 
-/* Device-side waits of the product kernels are bounded (about two seconds
- * each).  *count receives how many blocks of the current device have given up
+/* Device-side waits of the product kernels, and of the block norms' clusters of
+ * vc_step.h, are bounded (about two seconds each).  *count receives how many blocks of the current device have given up
  * since the library was loaded: 0 unless something is broken, and any other
  * value means that results computed since are not valid.  Waits for all
  * streams of the device, then copies one word to the host; not to be called

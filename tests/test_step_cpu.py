@@ -131,7 +131,11 @@ def test_embedding_backward_arguments(st):
     assert L.vc_embedding_backward_workspace(-1, 100, 64) == 0
     assert L.vc_embedding_backward_workspace(10, 1 << 31, 64) == 0
     assert L.vc_embedding_backward_workspace((1 << 30) + 1, 100, 64) == 0
-    assert L.vc_embedding_backward_workspace(1 << 30, 1 << 30, 1 << 30) > 0
+    assert L.vc_embedding_backward_workspace(1 << 30, 1 << 30, 1 << 22) > 0
+    # more columns than a grid covers
+    assert L.vc_embedding_backward_workspace(10, 100, (1 << 22) + 1) == 0
+    wide = mat(st, 40 * GiB, 1, (1 << 22) + 8)
+    assert scatter(st, mat(st, GiB, 1, (1 << 22) + 8), wide) == INVALID
 
 
 # -------------------------------------------------------------- block norms --

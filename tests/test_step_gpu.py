@@ -878,6 +878,58 @@ def test_refusals(env):
             call()
 
 
+# ------------------------------------------------------------------- far rows --
+
+def test_tables_beyond_32_bit_offsets(env):
+    """A table of 2^31 and more elements: its last rows are looked up, and their
+    gradients land there and nowhere else."""
+    torch, vc, dev = env
+    cols = 4096
+    rows = 2 ** 31 // cols + 300
+    w = torch.zeros(rows, cols, dtype=torch.bfloat16, device=dev)
+    last = rand(torch, dev, 64, cols)
+    w[-64:] = last
+    ids = torch.arange(rows - 64, rows, device=dev).flip(0)
+    out = torch.empty(64, cols, dtype=torch.bfloat16, device=dev)
+    vc.vc_embedding_forward(ids, w, out)
+    assert torch.equal(out, last.flip(0))
+    w.fill_(3)
+    vc.vc_embedding_backward(last, ids, w)
+    assert torch.equal(w[-64:], last.flip(0))
+    assert not w[:-64].any()
+    vc.vc_embedding_backward(last, ids, w, accumulate=True)
+    assert torch.equal(w[-64:], last.flip(0) * 2) and not w[:-64].any()
+
+
+def test_rows_beyond_32_bit_offsets(env):
+    torch, vc, dev = env
+    cols = 4096
+    rows = 2 ** 31 // cols + 40
+    h = torch.zeros(rows, cols, dtype=torch.bfloat16, device=dev)
+    h[-40:] = rand(torch, dev, 40, cols)
+    w = rand(torch, dev, cols, mean=1.0)
+    n, few = torch.empty_like(h), torch.empty(40, cols, dtype=torch.bfloat16, device=dev)
+    vc.vc_block_norm_forward(h, n=n, pre=w)
+    vc.vc_block_norm_forward(h[-40:], n=few, pre=w)
+    assert torch.equal(n[-40:], few) and not n[:-40].any()
+    dx, dpre = torch.empty_like(h), torch.empty(cols, device=dev)
+    fx, fpre = torch.empty_like(few), torch.empty(cols, device=dev)
+    vc.vc_block_norm_backward(dr=h, dn=h, r=h, dx=dx, pre=w, dpre=dpre)
+    vc.vc_block_norm_backward(dr=h[-40:], dn=h[-40:], r=h[-40:], dx=fx, pre=w, dpre=fpre)
+    assert torch.equal(dx[-40:], fx) and not dx[:-40].any()
+    assert ((dpre - fpre).abs() <= 80 * U * (h[-40:].double().square().sum(0) * 40)).all()
+
+
+def test_gradients_beyond_32_bit_offsets(env):
+    torch, vc, dev = env
+    g = torch.zeros(2 ** 31 + 100, dtype=torch.bfloat16, device=dev)
+    g[-100:] = 4
+    norm = torch.empty((), device=dev)
+    plan = vc.ClipPlan([g])
+    plan.clip(10.0, norm, eps=0.0)
+    assert norm.item() == 40 and g[-100:].eq(1).all() and not g[:-100].any()
+
+
 # ------------------------------------------------------- streams and graphs --
 
 def test_replays_of_a_graph_see_new_inputs(env):
