@@ -102,7 +102,7 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kItems = 8;           // of a thread at a time
 constexpr int kChunk = kSortThreads * kItems;
 constexpr int kFewTokens = 4096;  // that one block sorts
-constexpr int kFillClusters = 15;   // beside the one that sorts: all that run at a time
+constexpr int kFillClusters = 14;   // beside the one that sorts: 15 run at a time
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kMarkRows = 16384;    // rows that a block marks at a time
 

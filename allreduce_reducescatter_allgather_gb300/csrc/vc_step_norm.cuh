@@ -144,7 +144,7 @@ struct Held {
 
 // Sums over a team of up to four values at a time.  A warp's lanes share the values
 // out while they add (of four values each lane keeps two, then one), the warps of a
-// block leave theirs in shared memory, those of a cluster in that of every block.
+// block leave theirs in shared memory, the blocks of a cluster in that of every one.
 // Calls take turns between two buffers there, so that one wait a call does.
 //
 // In a cluster the values bring their own signal: they are counted on a barrier of the
@@ -160,7 +160,7 @@ struct SpanShared {
 
 template <int kTeam, bool kSpan>
 struct TeamSums {
-    static constexpr int kWarps = kTeam / 32, kAll = kWarps * (kSpan ? kMaxSpan : 1);
+    static constexpr int kWarps = kTeam / 32, kAll = kWarps + (kSpan ? kMaxSpan : 0);
     float (*shared)[4];  // [2 * kAll][4]
     int turn, span;      // blocks that share a row
     SpanShared* signals;
@@ -207,37 +207,38 @@ struct TeamSums {
         } else {
             float(*buf)[4] = shared + turn * kAll;
             const int q = lane % kP, w = lane / kP;
+            if (lane % (32 / kP) == 0) buf[threadIdx.x >> 5][lane / (32 / kP)] = c;
+            __syncthreads();
+            c = w < kWarps ? buf[w][q] : 0.0f;
+#pragma unroll
+            for (int more = 32 / kP; more < kWarps; more += 32 / kP)
+                if (w + more < kWarps) c += buf[w + more][q];
+#pragma unroll
+            for (int o = 16; o >= kP; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
             if constexpr (kSpan) {
+                // one lane a value sends the block's to every block
+                float(*all)[4] = buf + kWarps;
                 const unsigned bar = gemm::smem_u32(&signals->barrier[turn]);
-                if (lane % (32 / kP) == 0) {
-                    const float* at = &buf[blockIdx.x % span * kWarps + (threadIdx.x >> 5)][lane / (32 / kP)];
+                if (threadIdx.x < kP)
                     for (int r = 0; r < span; ++r)
                         asm volatile(
                             "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
-                                remote_address(at, r)),
+                                remote_address(&all[blockIdx.x % span][q], r)),
                             "r"(__float_as_uint(c)), "r"(remote_address(&signals->barrier[turn], r))
                             : "memory");
-                }
-                if (threadIdx.x == 0) gemm::mbar_expect(bar, kWarps * span * kP * 4);
+                if (threadIdx.x == 0) gemm::mbar_expect(bar, span * kP * 4);
                 gemm::warp_wait(bar, parity >> turn & 1, &signals->dead);
                 parity ^= 1u << turn;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) v[i] = 0.0f;
+                for (int r = 0; r < span; ++r)
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) v[i] += all[r][i];
             } else {
-                if (lane % (32 / kP) == 0) buf[threadIdx.x >> 5][lane / (32 / kP)] = c;
-                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kN; ++i) v[i] = __shfl_sync(~0u, c, i);
             }
             turn ^= 1;
-            const int warps = kSpan ? kWarps * span : kWarps;
-            c = w < warps ? buf[w][q] : 0.0f;
-            if constexpr (kSpan) {
-                for (int more = w + 32 / kP; more < warps; more += 32 / kP) c += buf[more][q];
-            } else {
-#pragma unroll
-                for (int more = 32 / kP; more < kWarps; more += 32 / kP) c += buf[w + more][q];
-            }
-#pragma unroll
-            for (int o = 16; o >= kP; o >>= 1) c += __shfl_xor_sync(~0u, c, o);
-#pragma unroll
-            for (int i = 0; i < kN; ++i) v[i] = __shfl_sync(~0u, c, i);
         }
     }
 };
@@ -345,9 +346,13 @@ struct Shape {
     int team, vecs, span;
 };
 
-// Clusters of this many blocks that run at a time, with `per_sm` blocks on an SM: of
-// each of eight groups of SMs 18 are counted on.
-inline int clusters_of(int span, int per_sm) { return 8 * (18 * per_sm / span); }
+// Clusters of `span` blocks that run at a time on a GB300, with one or two blocks on an SM
+// (what its occupancy query says: a cluster's SMs are of one group).
+inline int clusters_of(int span, int per_sm) {
+    constexpr int kOne[kMaxSpan + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+    constexpr int kTwo[kMaxSpan + 1] = {0, 304, 152, 97, 74, 58, 46, 38, 36};
+    return (per_sm > 1 ? kTwo : kOne)[span];
+}
 
 inline bool valid_affine(const vc_affine_t* a, bool needed) {
     if (a == nullptr || a->weight == nullptr) return !needed && (a == nullptr || a->bias == nullptr);

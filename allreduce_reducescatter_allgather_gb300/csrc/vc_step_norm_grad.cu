@@ -49,15 +49,23 @@ __device__ __forceinline__ void store_gate(const NormParams& p, long long row, b
 
 constexpr int kBackwardThreads = 256;  // of a block of teams that are warps
 
-// Blocks on an SM; one less of four where layer norms' rows come through registers.
-template <int kTeam, int kVecs, bool kCrowded>
-constexpr int backward_resident = kTeam == 32 ? 2 / kVecs : kTeam == 128 && kCrowded ? 3 : 512 / kTeam;
+// Blocks on an SM: 16 to 20 warps with 100 to 128 registers a thread, fewer where layer
+// norms' rows come through registers (crowded).
+__host__ __device__ constexpr int resident_blocks(int team, bool crowded) {
+    return team == 32    ? 2
+           : team == 64  ? (crowded ? 6 : 8)
+           : team == 128 ? (crowded ? 3 : 4)
+           : team == 192 ? 2
+           : team == 256 ? 2
+           : team == 320 ? (crowded ? 1 : 2)
+                         : 1;
+}
 
 // One row after the other, the next one's inputs on their way meanwhile, the column sums
 // in registers.
 
 template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec, bool kSpan = false>
-__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, backward_resident<kTeam, kVecs, kLayer && !kVec>)
+__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, resident_blocks(kTeam, kLayer && !kVec))
     backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kBackwardThreads : kTeam, kTeams = kThreads / kTeam;
     // RMS norms have no biases
@@ -577,10 +585,8 @@ __global__ void __launch_bounds__(kJoinTeams) gates_kernel(const __grid_constant
 
 // in_two: rows of up to 8192 values by two vectors a thread.
 Shape backward_shape(int cols, bool in_two) {
-    if (cols <= 256) return {32, 1, 1};
-    if (cols <= 512) return {32, 2, 1};
-    if (cols <= 1024) return {128, 1, 1};
-    if (cols <= 2048) return {256, 1, 1};
+    for (int team : {32, 64, 128, 192, 256, 320})
+        if (cols <= team * 8) return {team, 1, 1};
     if (cols <= 4096) return {512, 1, 1};
     if (cols <= 8192 && in_two) return {512, 2, 1};
     if (cols <= 4096 * kMaxSpan) return {512, 1, (cols + 4095) / 4096};
@@ -602,9 +608,7 @@ Split split_of(long long rows, long long cols, bool in_two, bool crowded) {
     // two rows a team at least, so that the parts stay few beside the rows
     const long long want = (rows + 2 * per - 1) / (2 * per);
     const long long most = s.shape.span > 1 ? clusters_of(s.shape.span, 1)
-                           : (long long)kSMs * (team == 32                ? 2 / s.shape.vecs
-                                               : team == 128 && crowded ? 3
-                                                                        : 512 / s.threads);
+                                            : (long long)kSMs * resident_blocks(team, crowded);
     s.blocks = (int)std::max(1ll, std::min(want, most));  // or clusters
     s.teams = (int)std::min(rows, (long long)s.blocks * per);  // (the others have no rows)
     s.padded = (cols + 7) / 8 * 8;
@@ -630,8 +634,10 @@ cudaError_t launch_backward(NormParams& p, const Split& s, cudaStream_t st) {
     void (*kernel)(NormParams) = nullptr;
     switch (s.shape.team * 4 + s.shape.vecs) {
     case 32 * 4 + 1: kernel = backward_kernel<32, 1, kLayer, kStream32, kVec>; break;
-    case 32 * 4 + 2: kernel = backward_kernel<32, 2, kLayer, kStream32, kVec>; break;
+    case 64 * 4 + 1: kernel = backward_kernel<64, 1, kLayer, kStream32, kVec>; break;
     case 128 * 4 + 1: kernel = backward_kernel<128, 1, kLayer, kStream32, kVec>; break;
+    case 192 * 4 + 1: kernel = backward_kernel<192, 1, kLayer, kStream32, kVec>; break;
+    case 320 * 4 + 1: kernel = backward_kernel<320, 1, kLayer, kStream32, kVec>; break;
     case 256 * 4 + 1: kernel = backward_kernel<256, 1, kLayer, kStream32, kVec>; break;
     case 512 * 4 + 1:
         kernel = s.shape.span > 1 ? backward_kernel<512, 1, kLayer, kStream32, kVec, true>
