@@ -89,9 +89,10 @@ def build_library(force: bool = False, jobs: int | None = None) -> Path:
     jobs_list = [(Path(s).stem, s, []) for s in SOURCES]
     jobs_list += [(stem, INSTANCE_SOURCE, defs) for stem, defs in INSTANCES]
     jobs_list += [(stem, BUCKET_SOURCE, defs) for stem, defs in BUCKET_INSTANCES]
-    # the longest units first (the bucket slices, then the double tree, tree
-    # and ring slices, then the rest), so the pool finishes together
-    jobs_list.sort(key=lambda j: -3 if j[1] == BUCKET_SOURCE
+    # the longest units first (the gradient of the block norms and the bucket slices,
+    # then the double tree, tree and ring slices, then the rest), so the pool finishes
+    # together
+    jobs_list.sort(key=lambda j: -4 if j[1] == "vc_step_norm_grad.cu" else -3 if j[1] == BUCKET_SOURCE
                    else (-int(j[0][-1]) if j[1] == INSTANCE_SOURCE else 1))
     jobs = jobs or max(1, os.cpu_count() or 4)
     with ThreadPoolExecutor(max_workers=jobs) as ex:

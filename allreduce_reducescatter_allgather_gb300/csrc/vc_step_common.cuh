@@ -204,16 +204,16 @@ __device__ __forceinline__ void store_any(const Rows& x, bool f32, long long row
 
 // Eight columns of a row as they lie in memory, so that a thread can hold the next
 // row's while it computes with this one's: eight 32-bit words of float32, or of
-// bfloat16 four words of two (on 16 bytes) or eight of one.  kOnce: what is read once
-// leaves the caches to what is not.
+// bfloat16 four words of two (on 16 bytes) or eight of one.
 struct Raw {
     unsigned w[8];
 };
+// kOnce: what is read once leaves the caches to what is not.
 template <bool kOnce, class T>
 __device__ __forceinline__ T load_word(const T* p) {
     return kOnce ? __ldcs(p) : *p;
 }
-template <int kTeam, bool kOnce = true>
+template <int kTeam>
 __device__ __forceinline__ Raw load_raw(const Rows& x, bool f32, long long row, bool vec, int v, int lane, int cols) {
     const long long at = row * x.ld;
     const int c = (v * kTeam + lane) * 8;
@@ -221,10 +221,10 @@ __device__ __forceinline__ Raw load_raw(const Rows& x, bool f32, long long row, 
     if (vec && c + 8 <= cols) {
         if (f32) {
             const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x.data) + at + c);
-            const uint4 lo = load_word<kOnce>(p), hi = load_word<kOnce>(p + 1);
+            const uint4 lo = load_word<true>(p), hi = load_word<true>(p + 1);
             r = {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
         } else {
-            const uint4 u = load_word<kOnce>(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.data) + at + c));
+            const uint4 u = load_word<true>(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.data) + at + c));
             r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
         }
         return r;
@@ -236,9 +236,9 @@ __device__ __forceinline__ Raw load_raw(const Rows& x, bool f32, long long row, 
     for (int j = 0; j < 8; ++j) {
         const int k = column<kTeam>(vec, v, lane, j);
         if (f32) {
-            r.w[j] = k < cols ? load_word<kOnce>(static_cast<const unsigned*>(x.data) + at + k) : 0;
+            r.w[j] = k < cols ? load_word<true>(static_cast<const unsigned*>(x.data) + at + k) : 0;
         } else {
-            const unsigned u = k < cols ? load_word<kOnce>(static_cast<const unsigned short*>(x.data) + at + k) : 0;
+            const unsigned u = k < cols ? load_word<true>(static_cast<const unsigned short*>(x.data) + at + k) : 0;
             if (vec)
                 r.w[j / 2] |= u << (j % 2 * 16);
             else
@@ -263,12 +263,7 @@ __device__ __forceinline__ Eight widen_raw(const Raw& r, bool f32, bool vec) {
 
 // ---------------------------------------------------------------------- warps --
 
-// Sums of a whole warp, the same in every lane.
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-    return v;
-}
+// The sum of a whole warp, the same in every lane.
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);

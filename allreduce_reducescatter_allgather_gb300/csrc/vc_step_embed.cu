@@ -2,7 +2,8 @@
 // token, and the sum of the tokens' gradients by row.
 //
 // Forward: y_t = s W[id_t - first].  One 16-byte vector of a row a thread, four
-// of them in flight; bound by the bytes of y and of the rows.
+// of them in flight; bound by the bytes of y and of the rows: 65536 x 4096 from a table
+// of 131072 rows take 117 us (6.05 TB/s), 8 x 1024 take 4.0 us, the launch.
 //
 // Backward: dW_v (+)= s sum_{t: row(t) = v} dy_t in three launches, none of which
 // adds to memory that another block may add to:
@@ -15,12 +16,18 @@
 //          mark the rows that tokens have, and write zeros to as many of the others
 //          as they have time for.
 //   sum    writes zeros to the rest of those, in blocks among the summing ones: writes
-//          alone reach 4.0 TB/s, together with reads 6.8.  Every summing warp takes a window of neighbours in the sorted order and 256
-//          columns: as many rows of dy to each, whatever the ids are.  Rows whose
-//          tokens all lie in the window are stored, the first and the last one,
-//          where they go on beyond it, left as partial sums.
+//          alone reach 4.0 TB/s, together with reads 6.8.  Every summing warp takes a
+//          window of neighbours in the sorted order and 256 columns: as many rows of dy
+//          to each, whatever the ids are.  Rows whose tokens all lie in the window are
+//          stored, the first and the last one, where they go on beyond it, left as
+//          partial sums.  Bound by the bytes of dy and dW.
 //   join   adds the partial sums of rows that span windows, in order.
+//
+// 65536 x 4096 into 131072 rows take 271 us (5.8 TB/s), 16384 x 1024 into 32000 rows 32
+// us, of which the sort is 13, and 1003 x 517 into 5003 rows 12 us: three launches that
+// wait for one another.
 #include <algorithm>
+#include <type_traits>
 
 #include "vc_step_common.cuh"
 
@@ -46,50 +53,78 @@ struct LookupParams {
 
 constexpr int kLookupThreads = 256, kLookupUnits = 4;  // units of a thread in flight
 
-// A group of threads a token.  kVec: a unit is eight columns on 16 bytes (fewer at a
-// row's end), else one.
-template <bool kVec>
+// A group of threads a token.  Rows on 16 bytes eight columns at a time, others one (12352
+// x 1735 of those take 28 us, 29 % of the floor).  A kernel for each pair of types:
+// with all in one 65536 x 4096 took 123 us, with these 117.
+template <bool kVec, bool kFrom32, bool kTo32>
 __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const __grid_constant__ LookupParams p) {
+    using From = std::conditional_t<kFrom32, float, __nv_bfloat16>;
+    using To = std::conditional_t<kTo32, float, __nv_bfloat16>;
     pdl_next();
     pdl_wait();
-    const int width = 1 << p.shift, lane = threadIdx.x & (width - 1), units = kVec ? (p.cols + 7) / 8 : p.cols;
+    const int width = 1 << p.shift, lane = threadIdx.x & (width - 1);
     const long long token = ((long long)blockIdx.x * kLookupThreads + threadIdx.x) >> p.shift;
     if (token >= p.tokens) return;
     const unsigned long long row =
         (unsigned long long)load_id(p.ids, p.wide, token) - (unsigned long long)p.first;
     const bool in = row < p.rows;  // (a row below the table's start is far above its end)
-    const long long from = in ? (long long)row : 0;
-    for (int u0 = lane; u0 < units; u0 += kLookupUnits * width) {
-        if constexpr (kVec) {
-            Raw raw[kLookupUnits];
+    const From* const from = static_cast<const From*>(p.weight.data) + (in ? (long long)row : 0) * p.weight.ld;
+    To* const to = static_cast<To*>(p.out.data) + token * p.out.ld;
+    int done = 0;  // columns
+    if constexpr (kVec) {
+        const int units = p.cols / 8;
+        done = units * 8;
+        for (int u0 = lane; u0 < units; u0 += kLookupUnits * width) {
+            uint4 raw[kLookupUnits][kFrom32 ? 2 : 1];
 #pragma unroll
             for (int u = 0; u < kLookupUnits; ++u)
-                if (in) raw[u] = load_raw<1, false>(p.weight, p.weight.f32, from, true, u0 + u * width, 0, p.cols);
-#pragma unroll
-            for (int u = 0; u < kLookupUnits; ++u) {
-                const Eight r = in ? mul(p.scale, widen_raw(raw[u], p.weight.f32, true)) : zeros();
-                if (u0 + u * width < units) store_any<1>(p.out, p.out.f32, token, true, u0 + u * width, 0, p.cols, r);
-            }
-        } else {
-            float v[kLookupUnits];
-#pragma unroll
-            for (int u = 0; u < kLookupUnits; ++u) {
-                const long long at = from * p.weight.ld + u0 + u * width;
-                v[u] = 0.0f;
-                if (in && u0 + u * width < units)
-                    v[u] = p.weight.f32 ? static_cast<const float*>(p.weight.data)[at]
-                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.weight.data)[at]);
-            }
+                if (in && u0 + u * width < units) {
+                    const uint4* at = reinterpret_cast<const uint4*>(from + (u0 + u * width) * 8);
+                    raw[u][0] = at[0];
+                    if constexpr (kFrom32) raw[u][1] = at[1];
+                }
 #pragma unroll
             for (int u = 0; u < kLookupUnits; ++u) {
                 if (u0 + u * width >= units) continue;
-                const long long at = token * p.out.ld + u0 + u * width;
-                const float r = in ? v[u] * p.scale : 0.0f;
-                if (p.out.f32)
-                    static_cast<float*>(p.out.data)[at] = r;
-                else
-                    static_cast<__nv_bfloat16*>(p.out.data)[at] = __float2bfloat16(r);
+                Eight r = zeros();
+                if (in) {
+                    if constexpr (kFrom32)
+                        r = {{__uint_as_float(raw[u][0].x), __uint_as_float(raw[u][0].y), __uint_as_float(raw[u][0].z),
+                              __uint_as_float(raw[u][0].w), __uint_as_float(raw[u][1].x), __uint_as_float(raw[u][1].y),
+                              __uint_as_float(raw[u][1].z), __uint_as_float(raw[u][1].w)}};
+                    else
+                        r = widen(raw[u][0]);
+                    r = mul(p.scale, r);
+                }
+                To* at = to + (u0 + u * width) * 8;
+                if constexpr (kTo32) {
+                    reinterpret_cast<float4*>(at)[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+                    reinterpret_cast<float4*>(at)[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+                } else {
+                    *reinterpret_cast<uint4*>(at) = narrow(r);
+                }
             }
+        }
+    }
+    auto value = [&](int c) {
+        if constexpr (kFrom32)
+            return from[c];
+        else
+            return __bfloat162float(from[c]);
+    };
+    for (int c0 = done + lane; c0 < p.cols; c0 += kLookupUnits * width) {
+        float v[kLookupUnits];
+#pragma unroll
+        for (int u = 0; u < kLookupUnits; ++u) v[u] = in && c0 + u * width < p.cols ? value(c0 + u * width) : 0.0f;
+#pragma unroll
+        for (int u = 0; u < kLookupUnits; ++u) {
+            const int c = c0 + u * width;
+            if (c >= p.cols) continue;
+            const float r = in ? v[u] * p.scale : 0.0f;
+            if constexpr (kTo32)
+                to[c] = r;
+            else
+                to[c] = __float2bfloat16(r);
         }
     }
 }
@@ -447,8 +482,9 @@ __device__ __forceinline__ void finish_row(const SumParams& p, unsigned row, int
 }
 
 // The rows of a window as one warp takes them: on 16 bytes through shared memory, where
-// each lane's own columns of the next rows are on their way; others by fours through
-// registers.
+// each lane's own columns of the next rows are on their way (128 bytes a lane);
+// others by fours through registers.  16384 x 4096 into 32768 rows: 65 us for 116 MB read
+// and 205 written, from cold caches.
 template <int kWindow, bool kVec, bool kF32>
 __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_constant__ SumParams p) {
     constexpr int kWords = kF32 ? 2 : 1, kAhead = 8 / kWords, kBatch = 4, kPairs = (kWindow + 31) / 32;
@@ -584,7 +620,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_consta
 // there and the first ones of the windows behind, for 128 columns.  A warp looks after
 // a window; where the row goes on for long, all warps of the block share its windows.
 // (The windows of a block are neighbours, of which few have such a row; the columns of
-// one window are different blocks'.)
+// one window are different blocks'.)  7.7 us for 256 windows of 4096 columns.
 constexpr int kJoinWarps = 8, kJoinColumns = 128, kJoinLong = 16;
 
 template <int kWindow, bool kVec>
@@ -767,8 +803,19 @@ vc_status_t vc_embedding_forward(const void* ids, vc_dtype_t id_dtype, long long
            (p.shift < 5 || (tokens << p.shift) < (long long)kSMs * 1024))
         ++p.shift;
     const long long blocks = ((tokens << p.shift) + kLookupThreads - 1) / kLookupThreads;
-    const cudaError_t e = launch_pdl(vec ? lookup_kernel<true> : lookup_kernel<false>, dim3((unsigned)blocks),
-                                     dim3(kLookupThreads), static_cast<cudaStream_t>(stream), p);
+    void (*kernel)(LookupParams);
+    switch (vec * 4 + p.weight.f32 * 2 + p.out.f32) {
+    case 0: kernel = lookup_kernel<false, false, false>; break;
+    case 1: kernel = lookup_kernel<false, false, true>; break;
+    case 2: kernel = lookup_kernel<false, true, false>; break;
+    case 3: kernel = lookup_kernel<false, true, true>; break;
+    case 4: kernel = lookup_kernel<true, false, false>; break;
+    case 5: kernel = lookup_kernel<true, false, true>; break;
+    case 6: kernel = lookup_kernel<true, true, false>; break;
+    default: kernel = lookup_kernel<true, true, true>;
+    }
+    const cudaError_t e = launch_pdl(kernel, dim3((unsigned)blocks), dim3(kLookupThreads),
+                                     static_cast<cudaStream_t>(stream), p);
     return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
 }
 

@@ -5,10 +5,11 @@
 //   u = post(h),  r = a x + act(gate) u,  n = pre(r)
 //
 // Every matrix is read or written once; the bound is their bytes.  A team of
-// threads (a warp for short rows, a whole block for long ones) holds a row in
-// registers, eight columns a thread and vector, between the sums that the norms
-// need.  Rows that are longer than a team can hold are read again for every sum
-// (from the caches), by kernels of their own.
+// threads (a warp for short rows, a whole block or a cluster of blocks for long ones)
+// holds a row, eight columns a thread and vector, between the sums that the norms
+// need: in registers, or in shared memory where it has come through that.  Rows that
+// are longer than a cluster can hold (65536 values, 32768 in the gradient) are read
+// again for every sum (from the caches), by kernels of their own.
 //
 // The gradient's column sums (weights, biases, a gate that rows share) stay in
 // registers over the rows of a team, which are neighbours, and go to the

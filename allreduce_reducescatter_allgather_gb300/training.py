@@ -473,8 +473,9 @@ def prepare_muon_step(weight, grad, momentum, beta: float = 0.95, nesterov: bool
 
 
 def train_timeouts() -> int:
-    """Blocks of product kernels on the current device whose bounded waits
-    ran out since the library was loaded: 0 unless something is broken.
+    """Blocks on the current device, of product kernels and of clusters that
+    share a row of a block norm, whose bounded waits ran out since the library
+    was loaded: 0 unless something is broken.
     Waits for the device."""
     n = ctypes.c_uint(0)
     check_status(_lib().vc_train_timeouts(ctypes.byref(n)))

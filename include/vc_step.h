@@ -16,7 +16,7 @@
  * launches nothing; entry points are thread-safe.  Outputs must not overlap
  * inputs, except where a comment says that they may be the same matrix.
  *
- * Arithmetic is in 32 bits (sums over many gradients in 64) and rounded once
+ * Arithmetic is in 32 bits (the sums of clipping keep 48) and rounded once
  * where a value is stored.  The same call on the same inputs gives the same
  * bits: no sum depends on the order in which blocks run.
  */
@@ -158,8 +158,8 @@ vc_status_t vc_clip_plan(const void *const *grads, void *const *outs, const size
                          const vc_dtype_t *dtypes, int ntensors, vc_clip_tile_t *tiles,
                          int max_tiles, int *ntiles);
 
-/* L2: sqrt of the sum of squares, in 64 bits, so that no value of the gradients' types
- * is too large or too small.  MAX: the largest magnitude. */
+/* L2: sqrt of the sum of squares, which no value of the gradients' types is too large or
+ * too small for: squares that float32 does not hold are added in 64 bits.  MAX: the largest magnitude. */
 typedef enum { VC_GRAD_NORM_L2 = 0, VC_GRAD_NORM_MAX = 1 } vc_grad_norm_t;
 
 /* Bytes of workspace for both of the following. */

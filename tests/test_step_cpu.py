@@ -56,7 +56,7 @@ def test_library_exports_what_the_header_declares(st):
 def test_entry_points_do_not_throw(st):
     """Nothing in the host code allocates or throws."""
     from allreduce_reducescatter_allgather_gb300 import _build
-    for stem in ("vc_step_embed", "vc_step_norm", "vc_step_clip"):
+    for stem in ("vc_step_embed", "vc_step_norm", "vc_step_norm_grad", "vc_step_clip"):
         out = subprocess.run(["nm", "-u", "-C", str(_build.BUILD / f"{stem}.o")],
                              capture_output=True, text=True, check=True).stdout
         assert "cudaLaunchKernel" in out
