@@ -107,9 +107,11 @@ struct Stream {
             for (int i = 0; i < kVecs; ++i) raw[a][i] = load_raw<kTeam>(x, f32[a], row, kVec, v0 + i, lane, cols);
         }
     }
+    // kOther: from the stage that loads write to.
+    template <bool kOther = false>
     __device__ __forceinline__ Eight get(int a, int i) const {
         if constexpr (kRing) {
-            const uint4* from = ring + (stage * words + at[a]) * kThreads;
+            const uint4* from = ring + ((kOther ? stage ^ 1 : stage) * words + at[a]) * kThreads;
             if (!f32[a]) return widen(from[i * kThreads]);
             const uint4 lo = from[i * 2 * kThreads], hi = from[(i * 2 + 1) * kThreads];
             return {{__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z), __uint_as_float(lo.w),

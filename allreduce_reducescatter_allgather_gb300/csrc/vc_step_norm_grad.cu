@@ -108,14 +108,91 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
     float4* const held = reinterpret_cast<float4*>(ring + (kRing ? kStages * in.words * kThreads : 0)) + lane;
     const Vector pre = {held}, post = {held + Vector::kBytes / 16}, shift = {held + 2 * (Vector::kBytes / 16)},
                  held_gate = {held + ((kLayer ? 3 : 2) + part) * (Vector::kBytes / 16)};  // (a team's own)
-    auto load = [&](long long row) {
+    // what a row needs until its dr is there, and what it needs to the end
+    auto load_early = [&](long long row) {
         if (has_pre) {
             in.load(kR, p.r, row, lane, p.cols);
             in.load(kDn, p.dn, row, lane, p.cols);
         }
-        if (has_h) in.load(kH, p.h, row, lane, p.cols);
         if (has_dr) in.load(kDr, p.dr, row, lane, p.cols);
         if (full_gate) in.load(kG, p.gate, row, lane, p.cols);
+    };
+    auto load_late = [&](long long row) {
+        if (has_h) in.load(kH, p.h, row, lane, p.cols);
+    };
+    auto load = [&](long long row) {
+        load_early(row);
+        load_late(row);
+    };
+    // A row's statistics, in two steps: the totals that a layer norm needs for its means,
+    // and the products.
+    struct Stats {
+        float mean = 0.0f, h_mean = 0.0f, rstd = 0.0f, h_rstd = 0.0f, m1 = 0.0f, m2 = 0.0f;
+    };
+    auto centered_r = [&](const Stats& s, int i) {
+        const Eight r = in.get(kR, i);
+        return kLayer ? centered<kTeam>(r, s.mean, kVec, v0 + i, lane, p.cols) : r;
+    };
+    auto centered_h = [&](const Stats& s, const Eight& h, int i) {
+        return kLayer && has_post ? centered<kTeam>(h, s.h_mean, kVec, v0 + i, lane, p.cols) : h;
+    };
+    auto add_totals = [&](float& r, float& h) {
+        float2 a = make_float2(0.0f, 0.0f), b = a;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            if (has_pre) total(a, in.get(kR, i));
+            if (has_post) total(b, in.get(kH, i));
+        }
+        r = sum_of(a), h = sum_of(b);
+    };
+    auto add_products = [&](const Stats& s, float& r, float& gr, float& h, float& g) {
+        float2 a = make_float2(0.0f, 0.0f), b = a, c = a, d = a;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            if (has_pre) {
+                const Eight r = centered_r(s, i);
+                const Eight g = mul(pre.get(i), in.get(kDn, i));
+                dot(a, r, r);
+                dot(b, g, r);
+                if constexpr (kLayer) total(c, g);
+            }
+            if (has_post) {
+                const Eight h = centered_h(s, in.get(kH, i), i);
+                dot(d, h, h);
+            }
+        }
+        r = sum_of(a), gr = sum_of(b), h = sum_of(d), g = sum_of(c);
+    };
+    auto set_products = [&](Stats& s, float r, float gr, float h, float g) {
+        s.rstd = rsqrtf(fmaf(r, p.inv_cols, p.eps));
+        s.h_rstd = rsqrtf(fmaf(h, p.inv_cols, p.eps));
+        s.m2 = gr * (p.inv_cols * s.rstd * s.rstd);
+        s.m1 = g * p.inv_cols;
+    };
+    auto sum_products = [&](Stats& s) {
+        float r, gr, h, g;
+        add_products(s, r, gr, h, g);
+        if constexpr (kLayer) {
+            float v[4] = {r, gr, h, g};
+            sums(v);
+            set_products(s, v[0], v[1], v[2], v[3]);
+        } else {
+            float v[3] = {r, gr, h};
+            sums(v);
+            set_products(s, v[0], v[1], v[2], 0.0f);
+        }
+    };
+    auto statistics = [&] {
+        Stats s;
+        if constexpr (kLayer) {
+            float v[2];
+            add_totals(v[0], v[1]);
+            sums(v);
+            s.mean = v[0] * p.inv_cols;
+            s.h_mean = v[1] * p.inv_cols;
+        }
+        sum_products(s);
+        return s;
     };
     if constexpr (kSpan) sums.begin();
     pdl_next();
@@ -123,12 +200,23 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
     const long long lo = first_row(p, team), hi = first_row(p, team + 1);
     long long group_end = p.gate_mode == kGateGroups ? (lo / p.group + 1) * p.group : 0;
     if (lo < hi) load(lo);
+    if constexpr (kRing) {
+        copies_end();
+        in.stage ^= 1;
+        if (lo + 1 < hi) load(lo + 1);
+        copies_end();
+    }
     // (threads read what they have written themselves)
     pre.hold(p.pre.weight, v0, lane, p.cols);
     post.hold(p.post.weight, v0, lane, p.cols);
     if constexpr (kLayer) shift.hold(p.post.bias, v0, lane, p.cols);
     long long g = p.gate_mode == kGateGroups ? lo / p.group : 0;  // the rows' gate
     bool new_gate = p.gate_mode == kGateShared || p.gate_mode == kGateGroups;
+    Stats now;  // the row's
+    if constexpr (kRing) {
+        copies_wait<1>();
+        if (lo < hi) now = statistics();
+    }
     for (long long row = lo; row < hi; ++row) {
         if (new_gate) {
 #pragma unroll
@@ -136,86 +224,28 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
                 held_gate.put(i, gate_value(load_any<kTeam>(p.gate, g, kVec, v0 + i, lane, p.cols), p.sigmoid));
             new_gate = false;
         }
-        if constexpr (kRing) {
-            copies_end();
-            copies_wait<0>();
-            in.stage ^= 1;
-            if (row + 1 < hi) load(row + 1);
-        }
-        // the statistics: with the means taken off first, in one sum for both norms
-        float mean = 0.0f, h_mean = 0.0f;
-        if constexpr (kLayer) {
-            float2 a = make_float2(0.0f, 0.0f), b = a;
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                if (has_pre) total(a, in.get(kR, i));
-                if (has_post) total(b, in.get(kH, i));
-            }
-            float s[2] = {sum_of(a), sum_of(b)};
-            sums(s);
-            mean = s[0] * p.inv_cols;
-            h_mean = s[1] * p.inv_cols;
-        }
-        auto centered_r = [&](int i) {
-            const Eight r = in.get(kR, i);
-            return kLayer ? centered<kTeam>(r, mean, kVec, v0 + i, lane, p.cols) : r;
-        };
-        auto centered_h = [&](int i) {
-            const Eight h = in.get(kH, i);
-            return kLayer && has_post ? centered<kTeam>(h, h_mean, kVec, v0 + i, lane, p.cols) : h;
-        };
-        float rstd, h_rstd, m1 = 0.0f, m2;
-        {
-            float2 a = make_float2(0.0f, 0.0f), b = a, c = a, d = a;
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                if (has_pre) {
-                    const Eight r = centered_r(i);
-                    const Eight g = mul(pre.get(i), in.get(kDn, i));
-                    dot(a, r, r);
-                    dot(b, g, r);
-                    if constexpr (kLayer) total(c, g);
-                }
-                if (has_post) {
-                    const Eight h = centered_h(i);
-                    dot(d, h, h);
-                }
-            }
-            if constexpr (kLayer) {
-                float s[4] = {sum_of(a), sum_of(b), sum_of(d), sum_of(c)};
-                sums(s);
-                m1 = s[3] * p.inv_cols;
-                rstd = s[0], m2 = s[1], h_rstd = s[2];
-            } else {
-                float s[3] = {sum_of(a), sum_of(b), sum_of(d)};
-                sums(s);
-                rstd = s[0], m2 = s[1], h_rstd = s[2];
-            }
-        }
-        rstd = rsqrtf(fmaf(rstd, p.inv_cols, p.eps));
-        h_rstd = rsqrtf(fmaf(h_rstd, p.inv_cols, p.eps));
-        m2 *= p.inv_cols * rstd * rstd;
+        if constexpr (!kRing) now = statistics();
         Eight du[kVecs], kept_hat[kRing ? 1 : kVecs];
         float2 t1 = make_float2(0.0f, 0.0f), t2 = t1;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             Eight dr = has_dr ? in.get(kDr, i) : zeros();
             if (has_pre) {
-                const Eight r = mul(rstd, centered_r(i)), dn = in.get(kDn, i);
+                const Eight r = mul(now.rstd, centered_r(now, i)), dn = in.get(kDn, i);
                 const Eight w = pre.get(i);
                 add_product(kPre, i, dn, r);
                 if constexpr (kLayer) add_product(kPreBias, i, dn, ones);
-                dr = fma(-m2, r, dr);
-                if constexpr (kLayer) dr = add(-m1 * rstd, dr);
-                dr = fma(mul(rstd, w), dn, dr);
+                dr = fma(-now.m2, r, dr);
+                if constexpr (kLayer) dr = add(-now.m1 * now.rstd, dr);
+                dr = fma(mul(now.rstd, w), dn, dr);
             }
             if (p.dx.data != nullptr)
                 store_any<kTeam>(p.dx, kStream32, row, kVec, v0 + i, lane, p.cols, mul(p.scale, dr));
             Eight w, hat;
-            if (has_h) hat = centered_h(i);
+            if (has_h) hat = centered_h(now, in.get(kH, i), i);
             if (has_post) {
                 w = post.get(i);
-                hat = mul(h_rstd, hat);
+                hat = mul(now.h_rstd, hat);
             }
             if constexpr (!kRing) kept_hat[i] = hat;
             du[i] = dr;
@@ -263,29 +293,61 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
             ++g;
             new_gate = true;
         }
-        if (p.dh.data == nullptr) continue;
-        if (has_post) {
-            float h_m2, h_m1 = 0.0f;
+        // dh's sums, and the next row's: in one
+        float s1 = sum_of(t1), s2 = sum_of(t2);
+        Stats next;
+        if constexpr (kRing) {
+            in.stage ^= 1;
+            if (row + 2 < hi) load_early(row + 2);
+            copies_end();
+            copies_wait<1>();
+            const bool more = row + 1 < hi;
             if constexpr (kLayer) {
-                float s[2] = {sum_of(t1), sum_of(t2)};
-                sums(s);
-                h_m2 = s[0], h_m1 = s[1];
+                float v[4] = {s1, s2, 0.0f, 0.0f};
+                if (more) add_totals(v[2], v[3]);
+                sums(v);
+                s1 = v[0], s2 = v[1];
+                next.mean = v[2] * p.inv_cols;
+                next.h_mean = v[3] * p.inv_cols;
             } else {
-                float s[1] = {sum_of(t1)};
-                sums(s);
-                h_m2 = s[0];
+                float v[4] = {s1, 0.0f, 0.0f, 0.0f}, none;
+                if (more) add_products(next, v[1], v[2], v[3], none);
+                sums(v);
+                s1 = v[0];
+                set_products(next, v[1], v[2], v[3], 0.0f);
             }
-            h_m2 *= p.inv_cols * h_rstd;
-            h_m1 *= p.inv_cols * h_rstd;
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const Eight hat = kRing ? mul(h_rstd, centered_h(i)) : kept_hat[kRing ? 0 : i];
-                du[i] = fma(-h_m2, hat, mul(h_rstd, du[i]));
-                if constexpr (kLayer) du[i] = add(-h_m1, du[i]);
+        } else if (has_post && p.dh.data != nullptr) {
+            if constexpr (kLayer) {
+                float v[2] = {s1, s2};
+                sums(v);
+                s1 = v[0], s2 = v[1];
+            } else {
+                float v[1] = {s1};
+                sums(v);
+                s1 = v[0];
             }
         }
+        if (p.dh.data != nullptr) {
+            if (has_post) {
+                const float h_m2 = s1 * (p.inv_cols * now.h_rstd), h_m1 = s2 * (p.inv_cols * now.h_rstd);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.dh, false, row, kVec, v0 + i, lane, p.cols, du[i]);
+                for (int i = 0; i < kVecs; ++i) {
+                    const Eight hat = kRing ? mul(now.h_rstd, centered_h(now, in.template get<true>(kH, i), i))
+                                            : kept_hat[kRing ? 0 : i];
+                    du[i] = fma(-h_m2, hat, mul(now.h_rstd, du[i]));
+                    if constexpr (kLayer) du[i] = add(-h_m1, du[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.dh, false, row, kVec, v0 + i, lane, p.cols, du[i]);
+        }
+        if constexpr (kRing) {
+            if (row + 2 < hi) load_late(row + 2);
+            copies_end();
+            if constexpr (kLayer)
+                if (row + 1 < hi) sum_products(next);
+            now = next;
+        }
     }
     if constexpr (kSpan) sums.end(p.timeouts);
     // the column sums
