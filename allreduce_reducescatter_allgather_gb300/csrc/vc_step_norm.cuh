@@ -38,6 +38,7 @@ struct NormParams {
     long long rows, group;  // rows that share a gate row
     int cols, vec;
     int gate_mode, sigmoid, accumulate;
+    int stream_gate;  // backward: a gate for every element comes as the other matrices do
     float scale, eps, inv_cols;
     // backward: parts[block][kind][padded], slots[team][2][padded]
     float *parts, *slots;
@@ -50,11 +51,97 @@ struct NormParams {
 };
 enum { kSumPre = 0, kSumPreBias = 1, kSumPost = 2, kSumPostBias = 3, kSumGate = 4, kSums = 5 };
 
+// Eight neighbours of a row of any alignment, outside of the kernels' streams.
+template <int kTeam>
+__device__ __forceinline__ Eight load_near(const Rows& x, long long row, int v, int lane, int cols) {
+    if (x.vec) return load_any<kTeam>(x, row, true, v, lane, cols);
+    const int c = (v * kTeam + lane) * 8;
+    const long long at = row * x.ld + c;
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        r.v[j] = c + j >= cols ? 0.0f
+                 : x.f32       ? static_cast<const float*>(x.data)[at + j]
+                               : __bfloat162float(static_cast<const __nv_bfloat16*>(x.data)[at + j]);
+    return r;
+}
+
+// 16 bytes from byte `off` (even, below 16) of 32 on; 32 from byte `off` (a multiple of
+// 4) of 48 on.
+__device__ __forceinline__ uint4 cut16(uint4 lo, uint4 hi, unsigned off) {
+    unsigned w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int j = 0; j < 6; ++j) w[j] = off & 8 ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = off & 4 ? w[j + 1] : w[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], (off & 2) * 8);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ Eight cut32(uint4 a, uint4 b, uint4 c, unsigned off) {
+    unsigned w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int j = 0; j < 10; ++j) w[j] = off & 8 ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 9; ++j) w[j] = off & 4 ? w[j + 1] : w[j];
+    Eight r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.v[j] = __uint_as_float(w[j]);
+    return r;
+}
+
+// Eight neighbours to a row of any alignment, by a whole warp.  Off 16 bytes, each lane
+// stores the 16-byte words that its first values end, with the last ones of the lane
+// before it; what no word of the warp covers goes value by value.  (Value by value all
+// of it is eight accesses of 16 sectors each.)
+template <int kTeam>
+__device__ __forceinline__ void store_near(const Rows& x, bool f32, long long row, int v, int lane, int cols,
+                                           const Eight& r) {
+    const int es = f32 ? 4 : 2, c = (v * kTeam + lane) * 8, l = lane & 31;
+    char* const to = static_cast<char*>(x.data) + (row * x.ld + c) * es;
+    const unsigned off = (unsigned)reinterpret_cast<uintptr_t>(to) & 15;
+    if (off == 0) return store_any<kTeam>(x, f32, row, true, v, lane, cols, r);
+    const int first = 8 - (int)off / es;  // of the lane's values, in its own words
+    const bool own = l > 0 && c + first <= cols, next = l < 31 && c + 8 + first <= cols;
+    if (f32) {
+        uint4 before, a, b;
+        a = make_uint4(__float_as_uint(r.v[0]), __float_as_uint(r.v[1]), __float_as_uint(r.v[2]), __float_as_uint(r.v[3]));
+        b = make_uint4(__float_as_uint(r.v[4]), __float_as_uint(r.v[5]), __float_as_uint(r.v[6]), __float_as_uint(r.v[7]));
+        before.x = __shfl_up_sync(~0u, b.x, 1), before.y = __shfl_up_sync(~0u, b.y, 1);
+        before.z = __shfl_up_sync(~0u, b.z, 1), before.w = __shfl_up_sync(~0u, b.w, 1);
+        const Eight o = cut32(before, a, b, 16 - off);
+        if (own) {
+            float4* const at = reinterpret_cast<float4*>(to - off);
+            at[0] = make_float4(o.v[0], o.v[1], o.v[2], o.v[3]);
+            at[1] = make_float4(o.v[4], o.v[5], o.v[6], o.v[7]);
+        }
+    } else {
+        const uint4 a = narrow(r);
+        uint4 before;
+        before.x = __shfl_up_sync(~0u, a.x, 1), before.y = __shfl_up_sync(~0u, a.y, 1);
+        before.z = __shfl_up_sync(~0u, a.z, 1), before.w = __shfl_up_sync(~0u, a.w, 1);
+        const uint4 o = cut16(before, a, 16 - off);
+        if (own) *reinterpret_cast<uint4*>(to - off) = o;
+    }
+    if (own && next) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if ((j < first ? own : next) || c + j >= cols) continue;
+        if (f32)
+            reinterpret_cast<float*>(to)[j] = r.v[j];
+        else
+            reinterpret_cast<__nv_bfloat16*>(to)[j] = __float2bfloat16(r.v[j]);
+    }
+}
+
 // The rows of up to five matrices as a team passes over them.  Rows on 16 bytes come
-// through shared memory: each thread copies its own columns of the next row
+// through shared memory (kRing): each thread copies its own columns of the next row
 // (asynchronously, so that they cost no registers on the way) while it works on this
 // one, and no other thread reads them.  Others are held in registers, from where the
-// last one has been used up.
+// last one has been used up, or where there are too few of those come through shared
+// memory as well (kRing without kVec): the thread copies the 16-byte words that its
+// columns lie in, two or three, and shifts them when it reads them.  The words' other
+// bytes are read but not used.
 constexpr int kStages = 2;
 
 template <int kThreads, int kTeam, int kVecs, int kArrays, bool kVec, bool kRing>
@@ -66,11 +153,13 @@ struct Stream {
     int v0;            // the block's first vector
     // what there is of the thread's columns, in bytes of 16 or 32 bits a value, and where
     int bytes[kRing ? 3 : 1][kRing ? kVecs : 1], offset[kRing ? kVecs : 1];
+    unsigned here, there;  // four bits an array: the row's byte in a 16-byte word
     Raw raw[kRing ? 1 : kArrays][kRing ? 1 : kVecs];
 
     __device__ __forceinline__ void begin(uint4* shared, int first, int lane, int cols) {
         ring = shared + threadIdx.x;
         words = stage = 0;
+        here = there = 0;
         v0 = first;
         if constexpr (kRing)
 #pragma unroll
@@ -82,13 +171,35 @@ struct Stream {
                 offset[i] = n > 0 ? c : 0;  // (nothing is read where there is nothing)
             }
     }
-    __device__ __forceinline__ void array(int a, bool there, bool wide) {
+    __device__ __forceinline__ void array(int a, bool present, bool wide) {
         at[a] = words;
         f32[a] = wide;
-        if (there) words += kVecs * (wide ? 2 : 1);
+        if (present) words += kVecs * ((wide ? 2 : 1) + (kRing && !kVec));
     }
     __device__ __forceinline__ void load(int a, const Rows& x, long long row, int lane, int cols) {
-        if constexpr (kRing) {
+        if constexpr (kRing && !kVec) {
+            uint4* const to = ring + ((stage ^ 1) * words + at[a]) * kThreads;
+            const char* const from = static_cast<const char*>(x.data) + row * x.ld * (f32[a] ? 4 : 2);
+            // (eight columns are whole words: the same for all of the row)
+            const unsigned off = (unsigned)reinterpret_cast<uintptr_t>(from) & 15;
+            there = (there & ~(15u << 4 * a)) | off << 4 * a;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int n = f32[a] ? bytes[1][i] + bytes[2][i] : bytes[0][i], end = n > 0 ? n + (int)off : 0;
+                const char* const first = from + offset[i] * (f32[a] ? 4 : 2) - off;
+                auto word = [&](int w, int k) {
+                    copy16(to + w * kThreads, first + (end > 16 * k ? 16 * k : 0), max(0, min(16, end - 16 * k)));
+                };
+                if (f32[a]) {
+                    word(i * 3, 0);
+                    word(i * 3 + 1, 1);
+                    word(i * 3 + 2, 2);
+                } else {
+                    word(i * 2, 0);
+                    word(i * 2 + 1, 1);
+                }
+            }
+        } else if constexpr (kRing) {
             uint4* to = ring + ((stage ^ 1) * words + at[a]) * kThreads;
             if (f32[a]) {
                 const float* from = static_cast<const float*>(x.data) + row * x.ld;
@@ -107,11 +218,26 @@ struct Stream {
             for (int i = 0; i < kVecs; ++i) raw[a][i] = load_raw<kTeam>(x, f32[a], row, kVec, v0 + i, lane, cols);
         }
     }
+    // What has been loaded is read from here on.
+    __device__ __forceinline__ void turn() {
+        stage ^= 1;
+        if constexpr (kRing && !kVec) {
+            const unsigned h = here;
+            here = there;
+            there = h;
+        }
+    }
     // kOther: from the stage that loads write to.
     template <bool kOther = false>
     __device__ __forceinline__ Eight get(int a, int i) const {
         if constexpr (kRing) {
             const uint4* from = ring + ((kOther ? stage ^ 1 : stage) * words + at[a]) * kThreads;
+            if constexpr (!kVec) {
+                const unsigned off = (kOther ? there : here) >> 4 * a & 15;
+                if (!f32[a]) return widen(cut16(from[i * 2 * kThreads], from[(i * 2 + 1) * kThreads], off));
+                from += i * 3 * kThreads;
+                return cut32(from[0], from[kThreads], from[2 * kThreads], off);
+            }
             if (!f32[a]) return widen(from[i * kThreads]);
             const uint4 lo = from[i * 2 * kThreads], hi = from[(i * 2 + 1) * kThreads];
             return {{__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z), __uint_as_float(lo.w),
@@ -124,7 +250,7 @@ struct Stream {
 
 // A vector of the row's length that is used in every row (a weight, a bias, the gate
 // of the rows at hand): in shared memory, in 32 bits, each thread's own columns.
-template <int kTeam, int kVecs, bool kVec>
+template <int kTeam, int kVecs, class Access>
 struct Held {
     static constexpr int kBytes = kVecs * 2 * kTeam * 16;
     float4* at;  // [vector][half][lane]
@@ -135,7 +261,7 @@ struct Held {
     __device__ __forceinline__ void hold(const Rows& x, int v0, int lane, int cols) const {
         if (x.data != nullptr)
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) put(i, load_any<kTeam>(x, 0, kVec, v0 + i, lane, cols));
+            for (int i = 0; i < kVecs; ++i) put(i, Access{v0 + i, lane, cols}.load(x, 0));
     }
     __device__ __forceinline__ Eight get(int i) const {
         const float4 lo = at[i * 2 * kTeam], hi = at[(i * 2 + 1) * kTeam];

@@ -1,4 +1,6 @@
 // vc_block_norm_backward: from dr and dn to dx, dh, dgate and the column sums.
+#include <type_traits>
+
 #include "vc_step_norm.cuh"
 
 namespace vc {
@@ -13,39 +15,79 @@ __device__ __forceinline__ long long first_row(const NormParams& p, long long t)
 // A team's sum of dr u over the rows of group g that it has: the whole of it goes to
 // dgate, a part to one of the team's two slots: 0 where the group started before
 // its rows, 1 where it goes on behind them.
-template <int kTeam>
+template <class Access>
 __device__ __forceinline__ void flush_gate(const NormParams& p, long long team, long long g, long long lo,
-                                           long long hi, bool vec, int v, int lane, Eight sum) {
+                                           long long hi, const Access& access, Eight sum) {
     const bool before = g * p.group < lo, behind = (g + 1) * p.group > hi;
-    if (before || behind) {
-        const Rows slot = {p.slots, p.padded, 1, 1};
-        store_any<kTeam>(slot, true, team * 2 + (before ? 0 : 1), vec, v, lane, p.cols, sum);
-        return;
-    }
-    const Eight gate = load_any<kTeam>(p.gate, g, vec, v, lane, p.cols);
+    if (before || behind) return access.part({p.slots, p.padded, 1, 1}, team * 2 + (before ? 0 : 1), sum);
+    const Eight gate = access.load(p.gate, g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum.v[j] *= gate_slope(gate.v[j], p.sigmoid);
     if (p.accumulate) {
-        const Eight old = load_any<kTeam>(p.dgate, g, vec, v, lane, p.cols);
+        const Eight old = access.load(p.dgate, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum.v[j] += old.v[j];
     }
-    store_any<kTeam>(p.dgate, p.dgate.f32, g, vec, v, lane, p.cols, sum);
+    access.store(p.dgate, p.dgate.f32, g, sum);
 }
 
 // A gate of its own for every element.
-template <int kTeam>
-__device__ __forceinline__ void store_gate(const NormParams& p, long long row, bool vec, int v, int lane, Eight d,
+template <class Access>
+__device__ __forceinline__ void store_gate(const NormParams& p, long long row, const Access& access, Eight d,
                                            const Eight& gate) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) d.v[j] *= gate_slope(gate.v[j], p.sigmoid);
     if (p.accumulate) {
-        const Eight old = load_any<kTeam>(p.dgate, row, vec, v, lane, p.cols);
+        const Eight old = access.load(p.dgate, row);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d.v[j] += old.v[j];
     }
-    store_any<kTeam>(p.dgate, p.dgate.f32, row, vec, v, lane, p.cols, d);
+    access.store(p.dgate, p.dgate.f32, row, d);
 }
+
+// How a thread reads and writes its columns of vector v: neighbours of rows of any
+// alignment,
+template <int kTeam>
+struct Near {
+    int v, lane, cols;
+    __device__ __forceinline__ Eight load(const Rows& x, long long row) const {
+        return load_near<kTeam>(x, row, v, lane, cols);
+    }
+    __device__ __forceinline__ void store(const Rows& x, bool f32, long long row, const Eight& r) const {
+        store_near<kTeam>(x, f32, row, v, lane, cols, r);
+    }
+    __device__ __forceinline__ void part(const Rows& x, long long row, const Eight& r) const {
+        store_any<kTeam>(x, true, row, true, v, lane, cols, r);
+    }
+};
+// neighbours of rows on 16 bytes or else every kTeam-th one,
+template <int kTeam, bool kVec>
+struct Plain {
+    int v, lane, cols;
+    __device__ __forceinline__ Eight load(const Rows& x, long long row) const {
+        return load_any<kTeam>(x, row, kVec, v, lane, cols);
+    }
+    __device__ __forceinline__ void store(const Rows& x, bool f32, long long row, const Eight& r) const {
+        store_any<kTeam>(x, f32, row, kVec, v, lane, cols, r);
+    }
+    __device__ __forceinline__ void part(const Rows& x, long long row, const Eight& r) const {
+        store_any<kTeam>(x, true, row, kVec, v, lane, cols, r);
+    }
+};
+// and the same known at run time.
+struct Long {
+    bool vec;
+    int v, lane, cols;
+    __device__ __forceinline__ Eight load(const Rows& x, long long row) const {
+        return load_any<kLong>(x, row, vec, v, lane, cols);
+    }
+    __device__ __forceinline__ void store(const Rows& x, bool f32, long long row, const Eight& r) const {
+        store_any<kLong>(x, f32, row, vec, v, lane, cols, r);
+    }
+    __device__ __forceinline__ void part(const Rows& x, long long row, const Eight& r) const {
+        store_any<kLong>(x, true, row, vec, v, lane, cols, r);
+    }
+};
 
 constexpr int kBackwardThreads = 256;  // of a block of teams that are warps
 
@@ -57,8 +99,18 @@ __host__ __device__ constexpr int resident_blocks(int team, bool crowded) {
            : team == 128 ? (crowded ? 3 : 4)
            : team == 192 ? 2
            : team == 256 ? 2
-           : team == 320 ? (crowded ? 1 : 2)
+           : team == 320 ? 2
                          : 1;
+}
+
+// Rows off 16 bytes: in registers, strided over the team, or by the larger teams shifted
+// out of shared memory.  (The registers do not hold the next row beside the sums of a
+// layer norm, and with spilled ones a row waits for the next one's loads: 9120 x 4095 took
+// 213 us in registers, RMS, and 482, layer norm, 9120 x 4100 479 and 1487.  Shifted they
+// take 176, 250, 354 and 545.  9120 x 1021 took 49 and 61 us in registers, 53 and 93
+// shifted.)
+__host__ __device__ constexpr bool shifted(int team, bool layer, bool vec) {
+    return !vec && (team == 512 || (team == 256 && layer));
 }
 
 // One row after the other, the next one's inputs on their way meanwhile, the column sums
@@ -72,7 +124,8 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
     // RMS norms have no biases
     constexpr int kKept = kLayer ? 5 : 3;
     constexpr int kPre = 0, kPost = 1, kGate = 2, kPreBias = 3, kPostBias = 4;
-    constexpr bool kRing = kVec;
+    constexpr bool kShift = shifted(kTeam, kLayer, kVec), kRing = kVec || kShift;
+    using Access = std::conditional_t<kShift, Near<kTeam>, Plain<kTeam, kVec>>;
     constexpr int kR = 0, kDn = 1, kH = 2, kDr = 3, kG = 4;
     using Sums = TeamSums<kTeam, kSpan>;
     __shared__ float shared[2 * Sums::kAll][4];
@@ -86,7 +139,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
     const long long block = kSpan ? blockIdx.x / p.span : blockIdx.x, team = block * kTeams + part;
     const bool has_pre = p.dn.data != nullptr, has_post = p.post.weight.data != nullptr;
     const bool has_h = p.h.data != nullptr, has_dr = p.dr.data != nullptr;
-    const bool full_gate = p.gate_mode == kGateFull;
+    const bool full_gate = p.gate_mode == kGateFull, stream_gate = full_gate && (!kShift || p.stream_gate);
     const bool sums_gate = p.dgate.data != nullptr && (p.gate_mode == kGateShared || p.gate_mode == kGateGroups);
     Eight kept[kKept][kVecs];
     // sum k += a b
@@ -103,8 +156,8 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
     in.array(kDn, has_pre, false);
     in.array(kH, has_h, false);
     in.array(kDr, has_dr, kStream32);
-    in.array(kG, full_gate, p.gate.f32);
-    using Vector = Held<kTeam, kVecs, kVec>;
+    in.array(kG, stream_gate, kVecs == 1 && p.gate.f32);  // (two vectors: not with one in 32 bits)
+    using Vector = Held<kTeam, kVecs, Access>;
     float4* const held = reinterpret_cast<float4*>(ring + (kRing ? kStages * in.words * kThreads : 0)) + lane;
     const Vector pre = {held}, post = {held + Vector::kBytes / 16}, shift = {held + 2 * (Vector::kBytes / 16)},
                  held_gate = {held + ((kLayer ? 3 : 2) + part) * (Vector::kBytes / 16)};  // (a team's own)
@@ -115,7 +168,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
             in.load(kDn, p.dn, row, lane, p.cols);
         }
         if (has_dr) in.load(kDr, p.dr, row, lane, p.cols);
-        if (full_gate) in.load(kG, p.gate, row, lane, p.cols);
+        if (stream_gate) in.load(kG, p.gate, row, lane, p.cols);
     };
     auto load_late = [&](long long row) {
         if (has_h) in.load(kH, p.h, row, lane, p.cols);
@@ -131,10 +184,10 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
     };
     auto centered_r = [&](const Stats& s, int i) {
         const Eight r = in.get(kR, i);
-        return kLayer ? centered<kTeam>(r, s.mean, kVec, v0 + i, lane, p.cols) : r;
+        return kLayer ? centered<kTeam>(r, s.mean, kRing, v0 + i, lane, p.cols) : r;
     };
     auto centered_h = [&](const Stats& s, const Eight& h, int i) {
-        return kLayer && has_post ? centered<kTeam>(h, s.h_mean, kVec, v0 + i, lane, p.cols) : h;
+        return kLayer && has_post ? centered<kTeam>(h, s.h_mean, kRing, v0 + i, lane, p.cols) : h;
     };
     auto add_totals = [&](float& r, float& h) {
         float2 a = make_float2(0.0f, 0.0f), b = a;
@@ -202,7 +255,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
     if (lo < hi) load(lo);
     if constexpr (kRing) {
         copies_end();
-        in.stage ^= 1;
+        in.turn();
         if (lo + 1 < hi) load(lo + 1);
         copies_end();
     }
@@ -221,7 +274,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
         if (new_gate) {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
-                held_gate.put(i, gate_value(load_any<kTeam>(p.gate, g, kVec, v0 + i, lane, p.cols), p.sigmoid));
+                held_gate.put(i, gate_value(Access{v0 + i, lane, p.cols}.load(p.gate, g), p.sigmoid));
             new_gate = false;
         }
         if constexpr (!kRing) now = statistics();
@@ -240,7 +293,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
                 dr = fma(mul(now.rstd, w), dn, dr);
             }
             if (p.dx.data != nullptr)
-                store_any<kTeam>(p.dx, kStream32, row, kVec, v0 + i, lane, p.cols, mul(p.scale, dr));
+                Access{v0 + i, lane, p.cols}.store(p.dx, kStream32, row, mul(p.scale, dr));
             Eight w, hat;
             if (has_h) hat = centered_h(now, in.get(kH, i), i);
             if (has_post) {
@@ -252,7 +305,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
             if (p.gate_mode != kGateNone) {
                 Eight gate, value;
                 if (full_gate) {
-                    gate = in.get(kG, i);
+                    gate = stream_gate ? in.get(kG, i) : Access{v0 + i, lane, p.cols}.load(p.gate, row);
                     value = gate_value(gate, p.sigmoid);
                 } else {
                     value = held_gate.get(i);
@@ -267,7 +320,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
                     if (sums_gate)
                         add_product(kGate, i, u, dr);
                     else
-                        store_gate<kTeam>(p, row, kVec, v0 + i, lane, mul(u, dr), gate);
+                        store_gate(p, row, Access{v0 + i, lane, p.cols}, mul(u, dr), gate);
                 }
                 du[i] = mul(dr, value);
             }
@@ -286,7 +339,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
             if (sums_gate)
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    flush_gate<kTeam>(p, team, g, lo, hi, kVec, v0 + i, lane, kept[kGate][i]);
+                    flush_gate(p, team, g, lo, hi, Access{v0 + i, lane, p.cols}, kept[kGate][i]);
                     kept[kGate][i] = zeros();
                 }
             group_end += p.group;
@@ -297,7 +350,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
         float s1 = sum_of(t1), s2 = sum_of(t2);
         Stats next;
         if constexpr (kRing) {
-            in.stage ^= 1;
+            in.turn();
             if (row + 2 < hi) load_early(row + 2);
             copies_end();
             copies_wait<1>();
@@ -339,7 +392,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) store_any<kTeam>(p.dh, false, row, kVec, v0 + i, lane, p.cols, du[i]);
+            for (int i = 0; i < kVecs; ++i) Access{v0 + i, lane, p.cols}.store(p.dh, false, row, du[i]);
         }
         if constexpr (kRing) {
             if (row + 2 < hi) load_late(row + 2);
@@ -361,7 +414,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
         if constexpr (kTeams == 1) {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i)
-                store_any<kTeam>(parts, true, at, kVec, v0 + i, lane, p.cols, kept[k][i]);
+                Access{v0 + i, lane, p.cols}.part(parts, at, kept[k][i]);
         } else {
             __syncthreads();
 #pragma unroll
@@ -492,11 +545,11 @@ __global__ void __launch_bounds__(kLong) backward_long_kernel(const __grid_const
                     if (sums_gate) {
                         add(kSumGate, group_first, i, t);
                         if (group_last)
-                            flush_gate<kLong>(p, team, g, lo, hi, p.vec, i, lane,
-                                              load_f32<kLong>(parts.data, (team * kSums + kSumGate) * parts.ld,
-                                                              p.vec, i, lane, p.cols));
+                            flush_gate(p, team, g, lo, hi, Long{p.vec != 0, i, lane, p.cols},
+                                       load_f32<kLong>(parts.data, (team * kSums + kSumGate) * parts.ld, p.vec, i,
+                                                       lane, p.cols));
                     } else {
-                        store_gate<kLong>(p, row, p.vec, i, lane, t, v);
+                        store_gate(p, row, Long{p.vec != 0, i, lane, p.cols}, t, v);
                     }
                 }
 #pragma unroll
@@ -647,10 +700,12 @@ __global__ void __launch_bounds__(kJoinTeams) gates_kernel(const __grid_constant
     }
 }
 
-// in_two: rows of up to 8192 values by two vectors a thread.
-Shape backward_shape(int cols, bool in_two) {
-    for (int team : {32, 64, 128, 192, 256, 320})
+// vec: on 16 bytes (rows that are not leave 320 threads too few registers: 9120 x 2300
+// 364 us, RMS).  in_two: rows of up to 8192 values by two vectors a thread.
+Shape backward_shape(int cols, bool vec, bool in_two) {
+    for (int team : {32, 64, 128, 192, 256})
         if (cols <= team * 8) return {team, 1, 1};
+    if (cols <= 2560 && vec) return {320, 1, 1};
     if (cols <= 4096) return {512, 1, 1};
     if (cols <= 8192 && in_two) return {512, 2, 1};
     if (cols <= 4096 * kMaxSpan) return {512, 1, (cols + 4095) / 4096};
@@ -663,9 +718,9 @@ struct Split {
     int blocks, teams, threads;
     long long padded;
 };
-Split split_of(long long rows, long long cols, bool in_two, bool crowded) {
+Split split_of(long long rows, long long cols, bool vec, bool in_two, bool crowded) {
     Split s = {};
-    s.shape = backward_shape((int)std::min(cols, 1ll << 20), in_two);
+    s.shape = backward_shape((int)std::min(cols, 1ll << 20), vec, in_two);
     const int team = s.shape.team == 0 ? kLong : s.shape.team;
     s.threads = team == 32 ? kBackwardThreads : team;
     const int per = s.threads / team;
@@ -681,18 +736,23 @@ Split split_of(long long rows, long long cols, bool in_two, bool crowded) {
 
 template <bool kLayer, bool kStream32, bool kVec>
 cudaError_t launch_backward(NormParams& p, const Split& s, cudaStream_t st) {
-    // 16-byte words a thread has of a vector of the inputs of one row
-    const size_t words = (p.dn.data == nullptr ? 0 : kStream32 ? 3 : 2) + (p.h.data != nullptr) +
-                         (p.dr.data == nullptr ? 0 : kStream32 ? 2 : 1) +
-                         (p.gate_mode != kGateFull ? 0 : p.gate.f32 ? 2 : 1);
-    const bool summed_gate =
-        p.dgate.data != nullptr && (p.gate_mode == kGateShared || p.gate_mode == kGateGroups);
-    const bool groups = summed_gate && p.gate_mode == kGateGroups;
+    const bool groups = p.dgate.data != nullptr && p.gate_mode == kGateGroups;
+    const bool shift = shifted(s.shape.team, kLayer, kVec), ring = kVec || shift;
+    // 16-byte words a thread has of a vector of a matrix
+    auto words = [&](bool present, bool f32) -> size_t { return !present ? 0 : 1 + f32 + shift; };
+    const size_t rows = words(p.dn.data != nullptr, kStream32) + words(p.dn.data != nullptr, false) +
+                        words(p.h.data != nullptr, false) + words(p.dr.data != nullptr, kStream32);
+    const size_t gate = words(p.gate_mode == kGateFull, p.gate.f32);
     // two rows' inputs; held weights and gates
-    size_t bytes = kVec ? kStages * words * s.shape.vecs * s.threads * 16 : 0;
-    bytes += (size_t)((kLayer ? 3 : 2) * s.shape.team +
-                      (p.gate_mode == kGateShared || p.gate_mode == kGateGroups ? s.threads : 0)) *
-             s.shape.vecs * 32;
+    auto shared = [&](size_t words) {
+        return (ring ? kStages * words * s.shape.vecs * s.threads * 16 : 0) +
+               (size_t)((kLayer ? 3 : 2) * s.shape.team +
+                        (p.gate_mode == kGateShared || p.gate_mode == kGateGroups ? s.threads : 0)) *
+                   s.shape.vecs * 32;
+    };
+    // (shifted rows in 32 bits leave no place for a gate of as many values)
+    p.stream_gate = shared(rows + gate) + 2048 <= kSharedLimit;
+    size_t bytes = shared(rows + (p.stream_gate ? gate : 0));
     p.span = s.shape.span;
     if (p.span > 1 && (p.timeouts = gemm::timeout_counter()) == nullptr) return cudaErrorInvalidValue;
     void (*kernel)(NormParams) = nullptr;
@@ -701,7 +761,7 @@ cudaError_t launch_backward(NormParams& p, const Split& s, cudaStream_t st) {
     case 64 * 4 + 1: kernel = backward_kernel<64, 1, kLayer, kStream32, kVec>; break;
     case 128 * 4 + 1: kernel = backward_kernel<128, 1, kLayer, kStream32, kVec>; break;
     case 192 * 4 + 1: kernel = backward_kernel<192, 1, kLayer, kStream32, kVec>; break;
-    case 320 * 4 + 1: kernel = backward_kernel<320, 1, kLayer, kStream32, kVec>; break;
+    case 320 * 4 + 1: kernel = backward_kernel<320, 1, kLayer, kStream32, true>; break;
     case 256 * 4 + 1: kernel = backward_kernel<256, 1, kLayer, kStream32, kVec>; break;
     case 512 * 4 + 1:
         kernel = s.shape.span > 1 ? backward_kernel<512, 1, kLayer, kStream32, kVec, true>
@@ -744,7 +804,7 @@ size_t vc_block_norm_backward_workspace(long long rows, long long cols, long lon
         gates > rows)
         return 0;
     // (of the ways that rows of such a length may take, the one that needs most)
-    const Split a = split_of(rows, cols, false, false), s = split_of(rows, cols, true, false);
+    const Split a = split_of(rows, cols, true, false, false), s = split_of(rows, cols, true, true, false);
     const size_t parts = (size_t)std::max(a.blocks, s.blocks) * kSums * s.padded * 4;
     const size_t slots = gates > 1 && gates < rows ? (size_t)std::max(a.teams, s.teams) * 2 * s.padded * 4 : 0;
     return round256(parts) + round256(slots);
@@ -842,7 +902,7 @@ vc_status_t vc_block_norm_backward(const vc_block_norm_in_t* in, const vc_affine
     // bits for every element, whose rows would not find their place in shared memory)
     const bool in_two = p.vec && !layer && stream_like->dtype == VC_BFLOAT16 &&
                         !(p.gate_mode == kGateFull && p.gate.f32);
-    const Split s = split_of(T, D, in_two, layer && !p.vec);
+    const Split s = split_of(T, D, p.vec, in_two, layer && !p.vec);
     p.blocks = s.blocks;
     p.teams = s.teams;
     p.padded = s.padded;
