@@ -115,9 +115,12 @@ __host__ __device__ constexpr bool shifted(int team, bool layer, bool vec) {
 
 // One row after the other, the next one's inputs on their way meanwhile, the column sums
 // in registers, which are what bounds how many warps an SM has: 16384 x 8192 (1.61 GB) take
-// 340 us, 4.7 TB/s, with one block of 16 warps an SM, half of whose issue slots are used.
-// (h^ is computed again for dh: two vectors a thread have no registers to keep it, 372 us.)
-template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec, bool kSpan = false>
+// 276 us, 5.85 TB/s, with one block of 16 warps an SM.  A row's last sums and the next
+// row's statistics are one exchange (two: 340 us).  h^ is computed again for dh: two
+// vectors a thread have no registers to keep it.  kGates: a gate for every element or for
+// groups of rows; two vectors a thread have a kernel without that, whose code leaves them
+// no register spilled (with it 309 to 417 us, as the compiler chose which ones).
+template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec, bool kSpan = false, bool kGates = true>
 __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, resident_blocks(kTeam, kLayer && !kVec))
     backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kBackwardThreads : kTeam, kTeams = kThreads / kTeam;
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
     const long long block = kSpan ? blockIdx.x / p.span : blockIdx.x, team = block * kTeams + part;
     const bool has_pre = p.dn.data != nullptr, has_post = p.post.weight.data != nullptr;
     const bool has_h = p.h.data != nullptr, has_dr = p.dr.data != nullptr;
-    const bool full_gate = p.gate_mode == kGateFull, stream_gate = full_gate && (!kShift || p.stream_gate);
+    const bool full_gate = kGates && p.gate_mode == kGateFull, stream_gate = full_gate && (!kShift || p.stream_gate);
     const bool sums_gate = p.dgate.data != nullptr && (p.gate_mode == kGateShared || p.gate_mode == kGateGroups);
     Eight kept[kKept][kVecs];
     // sum k += a b
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
                     }
                     if (sums_gate)
                         add_product(kGate, i, u, dr);
-                    else
+                    else if constexpr (kGates)
                         store_gate(p, row, Access{v0 + i, lane, p.cols}, mul(u, dr), gate);
                 }
                 du[i] = mul(dr, value);
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, reside
         // (this row's inputs are used up)
         if constexpr (!kRing)
             if (row + 1 < hi) load(row + 1);
-        if (p.gate_mode == kGateGroups && (row + 1 == group_end || row + 1 == hi)) {
+        if (kGates && p.gate_mode == kGateGroups && (row + 1 == group_end || row + 1 == hi)) {
             if (sums_gate)
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
@@ -767,7 +770,11 @@ cudaError_t launch_backward(NormParams& p, const Split& s, cudaStream_t st) {
         kernel = s.shape.span > 1 ? backward_kernel<512, 1, kLayer, kStream32, kVec, true>
                                   : backward_kernel<512, 1, kLayer, kStream32, kVec>;
         break;
-    case 512 * 4 + 2: kernel = backward_kernel<512, 2, false, false, true>; break;
+    case 512 * 4 + 2:
+        kernel = p.gate_mode == kGateNone || p.gate_mode == kGateShared
+                     ? backward_kernel<512, 2, false, false, true, false, false>
+                     : backward_kernel<512, 2, false, false, true>;
+        break;
     default: kernel = backward_long_kernel<kLayer, kStream32>; bytes = 0;
     }
     cudaError_t e = launch_pdl_shared(kernel, dim3(s.blocks * s.shape.span), dim3(s.threads), bytes, s.shape.span, st, p);
