@@ -522,8 +522,22 @@ def test_block_backward_groups(env, rows, groups, cols):
     check_backward(env, b)
 
 
-@pytest.mark.parametrize("cols", [64, 130, 1040, 8300])
-@pytest.mark.parametrize("gap,offset", [(8, 0), (8, 8), (3, 0), (0, 1)])
+@pytest.mark.parametrize("norm,stream", [("rms", "bf16"), ("layer", "f32")])
+@pytest.mark.parametrize("gate_type", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [1801, 2304, 2600, 4095, 5120, 8191, 8192])
+def test_block_gates_of_wide_rows(env, cols, gate_type, norm, stream):
+    """Gates for every element and for groups, where rows with them do and do not fit in
+    shared memory."""
+    torch, vc, dev = env
+    for gates in (40, 4):
+        b = Block(torch, dev, 40, cols, norm, stream, gates, bias=norm == "layer", act="sigmoid",
+                  gate_type=gate_type)
+        check_forward(env, b)
+        check_backward(env, b, gate_type, accumulate=gates == 4)
+
+
+@pytest.mark.parametrize("cols", [64, 130, 1040, 1801, 2301, 4099, 8300])
+@pytest.mark.parametrize("gap,offset", [(8, 0), (8, 8), (3, 0), (0, 1), (0, 3)])
 def test_block_strides(env, cols, gap, offset):
     """Rows of wider tensors, on and off 16 bytes; nothing beside them is written."""
     torch, vc, dev = env
