@@ -91,15 +91,18 @@ struct Long {
 
 constexpr int kBackwardThreads = 256;  // of a block of teams that are warps
 
-// Blocks on an SM: 16 to 20 warps with 100 to 128 registers a thread, fewer where layer
-// norms' rows come through registers (crowded).
-__host__ __device__ constexpr int resident_blocks(int team, bool crowded) {
+// Blocks on an SM: 16 to 20 warps with 100 to 128 registers a thread, fewer where a layer
+// norm's rows come through registers, or are 32 bits wide beside 96 registers (16384 x 2560,
+// 16 gate rows: 282 us with two blocks of 320 threads, 230 with one; of 16 bits, one gate
+// row: 180 and 197).
+__host__ __device__ constexpr int resident_blocks(int team, bool layer, bool f32, bool vec) {
+    const bool crowded = layer && (team == 320 ? f32 : !vec);
     return team == 32    ? 2
            : team == 64  ? (crowded ? 6 : 8)
            : team == 128 ? (crowded ? 3 : 4)
            : team == 192 ? 2
            : team == 256 ? 2
-           : team == 320 ? 2
+           : team == 320 ? (crowded ? 1 : 2)
                          : 1;
 }
 
@@ -121,7 +124,7 @@ __host__ __device__ constexpr bool shifted(int team, bool layer, bool vec) {
 // groups of rows; two vectors a thread have a kernel without that, whose code leaves them
 // no register spilled (with it 309 to 417 us, as the compiler chose which ones).
 template <int kTeam, int kVecs, bool kLayer, bool kStream32, bool kVec, bool kSpan = false, bool kGates = true>
-__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, resident_blocks(kTeam, kLayer && !kVec))
+__global__ void __launch_bounds__(kTeam == 32 ? kBackwardThreads : kTeam, resident_blocks(kTeam, kLayer, kStream32, kVec))
     backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int kThreads = kTeam == 32 ? kBackwardThreads : kTeam, kTeams = kThreads / kTeam;
     // RMS norms have no biases
@@ -721,7 +724,7 @@ struct Split {
     int blocks, teams, threads;
     long long padded;
 };
-Split split_of(long long rows, long long cols, bool vec, bool in_two, bool crowded) {
+Split split_of(long long rows, long long cols, bool in_two, bool layer, bool f32, bool vec) {
     Split s = {};
     s.shape = backward_shape((int)std::min(cols, 1ll << 20), vec, in_two);
     const int team = s.shape.team == 0 ? kLong : s.shape.team;
@@ -730,7 +733,7 @@ Split split_of(long long rows, long long cols, bool vec, bool in_two, bool crowd
     // two rows a team at least, so that the parts stay few beside the rows
     const long long want = (rows + 2 * per - 1) / (2 * per);
     const long long most = s.shape.span > 1 ? clusters_of(s.shape.span, 1)
-                                            : (long long)kSMs * resident_blocks(team, crowded);
+                                            : (long long)kSMs * resident_blocks(team, layer, f32, vec);
     s.blocks = (int)std::max(1ll, std::min(want, most));  // or clusters
     s.teams = (int)std::min(rows, (long long)s.blocks * per);  // (the others have no rows)
     s.padded = (cols + 7) / 8 * 8;
@@ -811,7 +814,7 @@ size_t vc_block_norm_backward_workspace(long long rows, long long cols, long lon
         gates > rows)
         return 0;
     // (of the ways that rows of such a length may take, the one that needs most)
-    const Split a = split_of(rows, cols, true, false, false), s = split_of(rows, cols, true, true, false);
+    const Split a = split_of(rows, cols, false, false, false, true), s = split_of(rows, cols, true, false, false, true);
     const size_t parts = (size_t)std::max(a.blocks, s.blocks) * kSums * s.padded * 4;
     const size_t slots = gates > 1 && gates < rows ? (size_t)std::max(a.teams, s.teams) * 2 * s.padded * 4 : 0;
     return round256(parts) + round256(slots);
@@ -909,7 +912,7 @@ vc_status_t vc_block_norm_backward(const vc_block_norm_in_t* in, const vc_affine
     // bits for every element, whose rows would not find their place in shared memory)
     const bool in_two = p.vec && !layer && stream_like->dtype == VC_BFLOAT16 &&
                         !(p.gate_mode == kGateFull && p.gate.f32);
-    const Split s = split_of(T, D, p.vec, in_two, layer && !p.vec);
+    const Split s = split_of(T, D, in_two, layer, stream_like->dtype == VC_FLOAT32, p.vec);
     p.blocks = s.blocks;
     p.teams = s.teams;
     p.padded = s.padded;
