@@ -46,6 +46,7 @@ struct NormParams {
     int kinds;  // bits of enum kSum
     int teams, blocks;
     int span;  // blocks of a cluster that share a row
+    long long gates;  // rows of dgate, where there are no rows
     unsigned* timeouts;
     Affine dpost, dpre;
 };

@@ -608,7 +608,8 @@ __device__ __forceinline__ int find_spanning(const NormParams& p, int t0, int st
 
 // The parts of 32 columns, by 32 warps in turn: blocks y < kSums the column sums,
 // the others gate rows whose rows several teams have.  11.6 us for three sums of 152
-// parts of 8192 columns, from cold caches; latency.
+// parts of 8192 columns, from cold caches; latency.  Without rows the column sums are
+// zeros, and the others write those to the gates' gradient.
 constexpr int kJoinRows = 16;
 
 __global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ NormParams p) {
@@ -647,6 +648,17 @@ __global__ void __launch_bounds__(1024) finish_kernel(const __grid_constant__ No
                           p.sigmoid);
     };
     const int kind = blockIdx.y;
+    if (kind >= kSums && p.rows == 0) {
+        // no gate has any row: sums of nothing
+        for (long long g = (kind - kSums) * 32 + warp; live && g < p.gates; g += 32 * (gridDim.y - kSums)) {
+            const long long at = g * p.dgate.ld + c;
+            if (p.dgate.f32)
+                static_cast<float*>(p.dgate.data)[at] = 0.0f;
+            else
+                static_cast<__nv_bfloat16*>(p.dgate.data)[at] = __float2bfloat16(0.0f);
+        }
+        return;
+    }
     if (kind < kSums) {
         if (!(p.kinds >> kind & 1)) return;
         float s = 0.0f;
@@ -892,13 +904,17 @@ vc_status_t vc_block_norm_backward(const vc_block_norm_in_t* in, const vc_affine
               (p.dgate.data != nullptr && mode_of(in->gate, T) == kGateShared) << kSumGate;
     p.accumulate = accumulate != 0;
     if (p.dx.data == nullptr && p.dh.data == nullptr && p.dgate.data == nullptr && p.kinds == 0) return VC_SUCCESS;
-    // (without rows, gate rows have none either, and the sums are zeros)
-    if (T == 0 && (p.kinds == 0 || accumulate)) return VC_SUCCESS;
+    // (without rows all sums are zeros)
+    if (T == 0 && accumulate) return VC_SUCCESS;
+    if (T == 0) p.kinds &= ~(1 << kSumGate);  // (all gates are written alike)
+    if (T == 0 && p.kinds == 0 && p.dgate.data == nullptr) return VC_SUCCESS;
     if (test_launch_failure()) return VC_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     common_params(&p, in->gate, post, pre, args, T, D);
     if (T == 0) {
-        const cudaError_t e = launch_pdl(finish_kernel, dim3((unsigned)((D + 31) / 32), kSums), dim3(1024), st, p);
+        p.gates = p.dgate.data != nullptr ? gates : 0;
+        const unsigned more = (unsigned)std::min((long long)kJoinRows, (p.gates + 31) / 32);
+        const cudaError_t e = launch_pdl(finish_kernel, dim3((unsigned)((D + 31) / 32), kSums + more), dim3(1024), st, p);
         return e == cudaSuccess ? VC_SUCCESS : VC_ERR_CUDA;
     }
     p.dr = rows_of(in->dr);

@@ -1,0 +1,53 @@
+"""Calls of the embedding, block norms and clipping at the ends of what they allow, and beside
+each other."""
+from __future__ import annotations
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import allreduce_reducescatter_allgather_gb300 as vc
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    yield torch, vc, dev
+    assert vc.train_timeouts() == 0
+
+
+def rand(torch, dev, *shape, seed=0, dtype=None):
+    g = torch.Generator(device=dev).manual_seed(2000 + seed)
+    return torch.randn(*shape, generator=g, device=dev).to(dtype or torch.bfloat16)
+
+
+# --------------------------------------------------------------- block norms --
+
+@pytest.mark.parametrize("gates", [1, 3, 40])
+@pytest.mark.parametrize("act", ["none", "sigmoid"])
+@pytest.mark.parametrize("grad", ["bfloat16", "float32"])
+@pytest.mark.parametrize("cols", [5, 130, 4100])
+def test_gates_without_rows(env, cols, grad, act, gates):
+    """A sum over no rows is zero, whatever the gate is, and adds nothing."""
+    torch, vc, dev = env
+    none, w = torch.empty(0, cols, dtype=torch.bfloat16, device=dev), rand(torch, dev, cols)
+    gate = rand(torch, dev, gates, cols)
+    gate[0, 0] = float("nan")
+    whole = torch.full((gates + 2, cols + 3), 3.0, dtype=getattr(torch, grad), device=dev)
+    dgate, dpre = whole[1:-1, :cols], torch.full((cols,), 3.0, device=dev)
+    plain = dict(h=none, dr=none, gate=gate, dgate=dgate, gate_act=act)
+    both = dict(dn=none, r=none, pre=w, dpre=dpre, **plain)
+    for kw in (plain, both):
+        vc.vc_block_norm_backward(accumulate=True, **kw)
+        assert whole.eq(3).all() and dpre.eq(3).all()
+    for kw in (plain, both):
+        whole.fill_(3)
+        vc.vc_block_norm_backward(**kw)
+        assert dgate.eq(0).all()
+        assert whole[0].eq(3).all() and whole[-1].eq(3).all() and whole[:, cols:].eq(3).all()
+        assert dpre.eq(0 if kw is both else 3).all()
