@@ -195,6 +195,7 @@ vc_status_t vc_block_norm_forward(const vc_matrix_t* h, const vc_matrix_t* x, co
         return VC_ERR_INVALID_ARGUMENT;
     if (x != nullptr && r != nullptr && x->dtype != r->dtype) return VC_ERR_INVALID_ARGUMENT;
     if (!valid_affine(post, false) || !valid_affine(pre, n != nullptr)) return VC_ERR_INVALID_ARGUMENT;
+    if (args->norm != VC_NORM_LAYER && (has_bias(post) || has_bias(pre))) return VC_ERR_INVALID_ARGUMENT;
     const Span outs[2] = {span_of(r), span_of(n)};
     if (overlap(outs[0], outs[1])) return VC_ERR_ALIAS;
     const vc_affine_t none = {};

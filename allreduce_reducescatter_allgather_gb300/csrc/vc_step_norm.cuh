@@ -490,6 +490,7 @@ inline bool valid_affine(const vc_affine_t* a, bool needed) {
     return es != 0 && reinterpret_cast<uintptr_t>(a->weight) % es == 0 &&
            reinterpret_cast<uintptr_t>(a->bias) % es == 0;
 }
+inline bool has_bias(const vc_affine_t* a) { return a != nullptr && a->bias != nullptr; }
 inline Rows vector_of(void* data, vc_dtype_t dtype) {
     return {data, 0, dtype == VC_FLOAT32, reinterpret_cast<uintptr_t>(data) % 16 == 0};
 }

@@ -864,8 +864,7 @@ vc_status_t vc_block_norm_backward(const vc_block_norm_in_t* in, const vc_affine
                reinterpret_cast<uintptr_t>(s.bias) % es != 0 || (s.bias != nullptr && !layer);
     };
     if (bad_sum(out->dpre, has_pre) || bad_sum(out->dpost, has_post)) return VC_ERR_INVALID_ARGUMENT;
-    if ((post != nullptr && post->bias != nullptr && !layer) || (pre != nullptr && pre->bias != nullptr && !layer))
-        return VC_ERR_INVALID_ARGUMENT;
+    if (!layer && (has_bias(post) || has_bias(pre))) return VC_ERR_INVALID_ARGUMENT;
     const bool post_work = has_post && (out->dh != nullptr || out->dgate != nullptr || out->dpost.weight != nullptr ||
                                         out->dpost.bias != nullptr);
     const bool needs_h = post_work || out->dgate != nullptr;

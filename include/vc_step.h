@@ -63,7 +63,7 @@ vc_status_t vc_embedding_backward(const vc_matrix_t *dy, const void *ids, vc_dty
 
 /* ---- norms around a block ------------------------------------------------ */
 
-/* RMS: v / sqrt(mean(v^2) + eps) * w (+ b).  LAYER: the same of v - mean(v). */
+/* RMS: v / sqrt(mean(v^2) + eps) * w.  LAYER: the same of v - mean(v), (+ b). */
 typedef enum { VC_NORM_RMS = 0, VC_NORM_LAYER = 1 } vc_norm_t;
 typedef enum { VC_GATE_NONE = 0, VC_GATE_SIGMOID = 1 } vc_gate_t;
 
@@ -75,7 +75,8 @@ typedef struct {
 } vc_block_norm_t;
 
 /* A norm's weight and bias (D values each, contiguous, of one type: float32 or
- * bfloat16).  weight NULL: there is no such norm (and bias is NULL too). */
+ * bfloat16).  weight NULL: there is no such norm (and bias is NULL too).  RMS norms
+ * have no bias: calls with one are refused. */
 typedef struct {
     void *weight, *bias;
     vc_dtype_t dtype;

@@ -30,6 +30,22 @@ def mat(st, at, rows, cols, dtype=BF16):
     return st.Matrix(at, 1, rows, cols, cols, rows * cols, dtype)
 
 
+@pytest.mark.parametrize("cols", [64, 70000])
+def test_rms_norms_have_no_bias(st, cols):
+    """Of any width, before or behind a block, in both directions; layer norms have."""
+    L = st._lib()
+    h, r, n = (mat(st, (k + 1) * GiB, 12, cols) for k in range(3))
+    weight, biased = st.Affine(8 * GiB, None, BF16), st.Affine(9 * GiB, 10 * GiB, BF16)
+    by = ctypes.byref
+    for post, pre in ((biased, weight), (weight, biased), (biased, biased), (weight, weight)):
+        args = st.BlockNorm(0, 0, 1.0, 1e-6)
+        want = CUDA if post is weight and pre is weight else INVALID
+        call = (by(h), None, None, by(post), by(pre), by(args), by(r), by(n), None)
+        assert L.vc_block_norm_forward(*call) == want
+        args.norm = 1
+        assert L.vc_block_norm_forward(*call) == CUDA
+
+
 @pytest.mark.parametrize("gates", [1, 3])
 def test_gates_without_rows_reach_a_launch(st, gates):
     """The gradient of a gate that no row has is zeros, and has to be written."""
