@@ -116,11 +116,14 @@ struct __align__(16) Part {
 };
 constexpr float kLeast = 0x1p-90f, kMost = 0x1p90f;
 
-// s + c += x + d
+// s + c += x + d, for s and x of one sign.  What the addition of s and x rounds off joins c, and
+// their sum is split again, so that c never grows to more than half a step of s (left to
+// itself it becomes the whole error of a 32-bit sum: 1.3e-6 of the norm of 2 GB of equal values).
 __device__ __forceinline__ void add_pair(float& s, float& c, float x, float d) {
     const float t = s + x, b = t - s;
-    c += ((s - (t - b)) + (x - b)) + d;
-    s = t;
+    const float e = c + (((s - (t - b)) + (x - b)) + d);
+    s = t + e;
+    c = e - (s - t);
 }
 
 __device__ __forceinline__ void squares(const Held& h, bool f32, Part& p) {

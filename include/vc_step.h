@@ -16,9 +16,10 @@
  * launches nothing; entry points are thread-safe.  Outputs must not overlap
  * inputs, except where a comment says that they may be the same matrix.
  *
- * Arithmetic is in 32 bits (the sums of clipping keep 48) and rounded once
- * where a value is stored.  The same call on the same inputs gives the same
- * bits: no sum depends on the order in which blocks run.
+ * Arithmetic is in 32 bits and rounded once where a value is stored.  (Clipping adds
+ * squares in 32 bits over at most 33 values, and those sums as pairs of 32-bit values,
+ * which keep 48 bits.)  The same call on the same inputs gives the same bits: no sum
+ * depends on the order in which blocks run.
  */
 #ifndef VC_STEP_H
 #define VC_STEP_H
@@ -160,7 +161,8 @@ vc_status_t vc_clip_plan(const void *const *grads, void *const *outs, const size
                          int max_tiles, int *ntiles);
 
 /* L2: sqrt of the sum of squares, which no value of the gradients' types is too large or
- * too small for: squares that float32 does not hold are added in 64 bits.  MAX: the largest magnitude. */
+ * too small for: a sum of up to 33 squares that leaves [2^-90, 2^90] is taken in 64 bits.
+ * MAX: the largest magnitude. */
 typedef enum { VC_GRAD_NORM_L2 = 0, VC_GRAD_NORM_MAX = 1 } vc_grad_norm_t;
 
 /* Bytes of workspace for both of the following. */

@@ -6,6 +6,8 @@ import pytest
 
 pytestmark = pytest.mark.gpu
 
+U = 2.0 ** -24
+
 
 @pytest.fixture(scope="module")
 def env():
@@ -24,6 +26,31 @@ def env():
 def rand(torch, dev, *shape, seed=0, dtype=None):
     g = torch.Generator(device=dev).manual_seed(2000 + seed)
     return torch.randn(*shape, generator=g, device=dev).to(dtype or torch.bfloat16)
+
+
+# ------------------------------------------------------------------ clipping --
+
+@pytest.mark.parametrize("values", [500_002_816, 2 ** 31])
+@pytest.mark.parametrize("eleven_bits", [1543, 1913])
+def test_long_sums_of_equal_squares(env, values, eleven_bits):
+    """Equal values round every addition of a plain sum the same way.  A value of 11 bits
+    has a square of 22, of which four and sixteen add up exactly in 32 bits; tiles of
+    4096 such values are all full.  From there on sums are pairs, each addition of which
+    is off by less than 2^-44, and fewer than 2^12 follow one another.  That leaves the rounding
+    to 32 bits (u of the sum, half of it in the root) and the root's: 2 u."""
+    torch, vc, dev = env
+    assert values % 4096 == 0
+    value = eleven_bits / 2048
+    g = torch.full((values,), value, device=dev)
+    norm, want = torch.empty(1, device=dev), value * values ** 0.5
+    plan = vc.ClipPlan([g])
+    plan.norm(norm)
+    assert abs(norm.item() - want) <= 2 * U * want, norm.item() / want - 1
+    norm.fill_(0)
+    plan.clip(2 * want, norm)
+    assert abs(norm.item() - want) <= 2 * U * want
+    del plan, g
+    torch.cuda.empty_cache()
 
 
 # --------------------------------------------------------------- block norms --
