@@ -76,7 +76,11 @@ cudaError_t allow_smem(const void* kernel) {
         if (there == kernel) return cudaSuccess;
         if (there == nullptr) break;
     }
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerBlock);
+    cudaFuncAttributes has;
+    e = cudaFuncGetAttributes(&has, kernel);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemPerBlock - (int)has.sharedSizeBytes);
     if (e == cudaSuccess && i < kProbes)
         done[dev][(first + i) % kPlaces].compare_exchange_strong(there, kernel, std::memory_order_relaxed);
     return e;

@@ -1298,7 +1298,9 @@ inline bool encode_product(const Product& p, int b_rows, CUtensorMap* ma, CUtens
            encode_operand(mb, p.b, p.batch * pb, p.b.mn_major ? kBlockK : b_rows);
 }
 
-// Lets the kernel have all of an SM's shared memory, once per device.
+// Lets the kernel have all of an SM's shared memory that it does not have of its own, once
+// per device.  (One limit for all of its launches: a limit of each launch's own size
+// would refuse a larger one of another host thread.)
 cudaError_t allow_smem(const void* kernel);
 
 template <class Kernel, class... Args>

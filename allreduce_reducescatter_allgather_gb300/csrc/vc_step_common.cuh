@@ -303,8 +303,7 @@ template <class... KArgs, class... Args>
 cudaError_t launch_pdl_shared(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t bytes, int span, cudaStream_t st,
                               Args&&... args) {
     if (bytes > 24u << 10) {  // (with what the kernel has of its own, above 48 KiB)
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        const cudaError_t e = gemm::allow_smem(reinterpret_cast<const void*>(kernel));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

@@ -2,6 +2,8 @@
 each other."""
 from __future__ import annotations
 
+import threading
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +80,58 @@ def test_gates_without_rows(env, cols, grad, act, gates):
         assert dgate.eq(0).all()
         assert whole[0].eq(3).all() and whole[-1].eq(3).all() and whole[:, cols:].eq(3).all()
         assert dpre.eq(0 if kw is both else 3).all()
+
+
+def test_threads_with_other_operands(env):
+    """Host threads that call one kernel with more and fewer operands, which need more and
+    less shared memory, do not take it from each other."""
+    torch, vc, dev = env
+    rows, cols = 4, 4096
+    f = lambda i: rand(torch, dev, rows, cols, seed=i, dtype=torch.float32)  # noqa: E731
+    h, dn, w = rand(torch, dev, rows, cols), rand(torch, dev, rows, cols, seed=1), rand(torch, dev, cols)
+    x, gate, r, dr = f(2), f(3), f(4), f(5)
+
+    def calls():
+        """Forward and backward with few operands and with many, of one kernel each."""
+        o = [torch.empty_like(x) for _ in range(4)]
+        b = [torch.empty_like(h) for _ in range(2)]
+        few = (vc.prepare_block_norm_forward(h, r=o[0], x=x),
+               vc.prepare_block_norm_backward(dr=dr, dn=dn, r=r, dx=o[1], pre=w))
+        many = (vc.prepare_block_norm_forward(h, r=o[2], x=x, gate=gate, post=w, pre=w, n=b[0]),
+                vc.prepare_block_norm_backward(h, b[1], dr=dr, dn=dn, r=r, dx=o[3], gate=gate, post=w,
+                                               pre=w))
+        return few, many, o, b
+
+    few, many, want, want_b = calls()
+    for c in (*few, *many):
+        c()
+    torch.cuda.synchronize()
+    errors, outs = [], []
+    start = threading.Barrier(4)
+
+    def work(k):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                f_, m_, o, b = calls()
+                outs.append((o, b))
+                mine = m_ if k % 2 else f_
+                start.wait(60)
+                for _ in range(4000):
+                    for c in mine:
+                        c()
+                for c in (*f_, *m_):
+                    c()
+            stream.synchronize()
+        except Exception as e:  # reported below, on the main thread
+            errors.append((k, e))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for o, b in outs:
+        assert all(torch.equal(p, q) for p, q in zip(o + b, want + want_b))
