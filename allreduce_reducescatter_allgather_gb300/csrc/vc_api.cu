@@ -204,11 +204,11 @@ int sm_count() {
     static std::mutex mu;
     static int count[kMaxDevices] = {0};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
+    if (reported(cudaGetDevice(&dev)) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
     std::lock_guard<std::mutex> lock(mu);
     if (count[dev] == 0) {
         int v = 0;
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        if (reported(cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
             return -1;
         count[dev] = v;
     }

@@ -22,6 +22,8 @@
 
 #include <type_traits>
 
+#include "vc_error.cuh"
+
 namespace vc {
 
 constexpr int kMaxRanks = 64;
@@ -1496,9 +1498,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStre
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return reported(cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...));
 }
 
 // Launchers by element type (vc_reduce_dispatch.cu, which picks the slice of

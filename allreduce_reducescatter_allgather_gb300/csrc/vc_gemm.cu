@@ -21,11 +21,11 @@ constexpr int kMaxDevices = 64;
 unsigned* timeout_counter() {
     static std::atomic<unsigned*> where[kMaxDevices];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+    if (reported(cudaGetDevice(&dev)) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
     unsigned* at = where[dev].load(std::memory_order_relaxed);
     if (at == nullptr) {
         void* p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_timeouts) != cudaSuccess) return nullptr;
+        if (reported(cudaGetSymbolAddress(&p, g_timeouts)) != cudaSuccess) return nullptr;
         at = static_cast<unsigned*>(p);
         where[dev].store(at, std::memory_order_relaxed);
     }
@@ -65,7 +65,7 @@ cudaError_t allow_smem(const void* kernel) {
     constexpr unsigned kPlaces = 256, kProbes = 16;
     static std::atomic<const void*> done[kMaxDevices][kPlaces];
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = reported(cudaGetDevice(&dev));
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     const unsigned first = (unsigned)(reinterpret_cast<uintptr_t>(kernel) >> 4) * 2654435761u >> 24;
@@ -77,10 +77,10 @@ cudaError_t allow_smem(const void* kernel) {
         if (there == nullptr) break;
     }
     cudaFuncAttributes has;
-    e = cudaFuncGetAttributes(&has, kernel);
+    e = reported(cudaFuncGetAttributes(&has, kernel));
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemPerBlock - (int)has.sharedSizeBytes);
+    e = reported(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kSmemPerBlock - (int)has.sharedSizeBytes));
     if (e == cudaSuccess && i < kProbes)
         done[dev][(first + i) % kPlaces].compare_exchange_strong(there, kernel, std::memory_order_relaxed);
     return e;
@@ -140,8 +140,8 @@ extern "C" vc_status_t vc_train_timeouts(unsigned* count) {
         if (cudaGetLastError() != cudaSuccess) return VC_ERR_CUDA;
     }
     // (the copy alone would not wait for streams that do not block)
-    if (cudaDeviceSynchronize() != cudaSuccess) return VC_ERR_CUDA;
-    return cudaMemcpy(count, p, sizeof *count, cudaMemcpyDeviceToHost) == cudaSuccess
+    if (vc::reported(cudaDeviceSynchronize()) != cudaSuccess) return VC_ERR_CUDA;
+    return vc::reported(cudaMemcpy(count, p, sizeof *count, cudaMemcpyDeviceToHost)) == cudaSuccess
                ? VC_SUCCESS
                : VC_ERR_CUDA;
 }

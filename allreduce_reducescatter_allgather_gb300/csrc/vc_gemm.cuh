@@ -34,6 +34,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "vc_error.cuh"
+
 namespace vc {
 namespace gemm {
 
@@ -1322,9 +1324,7 @@ cudaError_t launch_cluster(Kernel* kernel, int blocks, int threads, int cluster,
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return reported(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 // One or two products in one launch of the pair kernel.  segment: K

@@ -35,11 +35,11 @@ void* g_scratch_addr[kMaxDevices] = {};
 // the first call on each device, with that device current.
 vc_status_t scratch_address(void** out) {
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return VC_ERR_CUDA;
+    if (reported(cudaGetDevice(&dev)) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return VC_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_setup_mu);
     if (g_scratch_addr[dev] == nullptr) {
         void* p = nullptr;
-        const cudaError_t e = cudaGetSymbolAddress(&p, noalloc_scratch);
+        const cudaError_t e = reported(cudaGetSymbolAddress(&p, noalloc_scratch));
         if (e != cudaSuccess || p == nullptr) return VC_ERR_CUDA;
         g_scratch_addr[dev] = p;
     }

@@ -319,8 +319,7 @@ cudaError_t launch_pdl_shared(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = span > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return reported(cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...));
 }
 
 }  // namespace step

@@ -2,6 +2,7 @@
 each other."""
 from __future__ import annotations
 
+import ctypes
 import threading
 
 import pytest
@@ -135,3 +136,52 @@ def test_threads_with_other_operands(env):
     assert not errors, errors
     for o, b in outs:
         assert all(torch.equal(p, q) for p, q in zip(o + b, want + want_b))
+
+
+# ----------------------------------------------------------- failed launches --
+
+def test_a_failed_launch_leaves_no_error_behind(env):
+    """A launch that the runtime refuses (here on a stream whose capture has been
+    invalidated) is reported by its own call alone, and not again by the next one that asks
+    the runtime for its last error.  An error that the program has left itself is not taken
+    for a launch's."""
+    torch, vc, dev = env
+    rt = ctypes.CDLL("libcudart.so.13")
+    x, w = rand(torch, dev, 4, 4096), rand(torch, dev, 16, 4096)
+    out, y = torch.empty_like(x), torch.empty(4, 16, dtype=torch.bfloat16, device=dev)
+    wide = [t.float() for t in (x, x)]
+    ids = torch.zeros(4, dtype=torch.int64, device=dev)
+    torch.cuda.synchronize()
+    raw = ctypes.c_void_p()
+    assert rt.cudaStreamCreateWithFlags(ctypes.byref(raw), 1) == 0
+    stream = torch.cuda.ExternalStream(raw.value, device=dev)
+    calls = {
+        "embedding": vc.prepare_embedding_forward(ids, w, out),
+        "block": vc.prepare_block_norm_forward(x, r=wide[0], x=wide[1], pre=w[0], n=out),
+        "linear": vc.prepare_linear_forward(x, w, y),
+        "all_reduce": lambda stream: vc.vc_all_reduce([x, out], stream=stream),
+    }
+    torch.cuda.synchronize()
+    left = {}
+    for name, call in calls.items():
+        assert rt.cudaStreamBeginCapture(raw, 2) == 0  # relaxed
+        assert rt.cudaStreamSynchronize(raw) != 0      # not allowed: ends the capture's validity
+        rt.cudaGetLastError()
+        with pytest.raises(vc.VcError):
+            call(stream=stream)
+        left[name] = rt.cudaPeekAtLastError()
+        rt.cudaGetLastError()
+        graph = ctypes.c_void_p()
+        assert rt.cudaStreamEndCapture(raw, ctypes.byref(graph)) != 0
+        rt.cudaGetLastError()
+    assert rt.cudaStreamDestroy(raw) == 0
+    assert not any(left.values()), left
+    assert rt.cudaSetDevice(1 << 20) != 0  # leaves its error
+    try:
+        for name, call in calls.items():
+            call(stream=torch.cuda.current_stream())
+            left[name] = rt.cudaPeekAtLastError()
+    finally:
+        rt.cudaGetLastError()
+    assert all(left.values()), left
+    torch.cuda.synchronize()
