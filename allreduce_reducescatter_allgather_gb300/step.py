@@ -8,6 +8,7 @@ bytes) may be passed in, and the prepare_* functions check fixed buffers once.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import math
 
@@ -385,6 +386,8 @@ class ClipPlan(PreparedOperator):
         plan = ClipPlan(grads)
         plan.clip(1.0, norm)      # norm: a float32 CUDA tensor of one value
         plan.norm(norm)           # the norm alone
+
+    norm lies outside of the gradients and outputs.
     """
 
     def __init__(self, grads, out=None):
@@ -422,13 +425,26 @@ class ClipPlan(PreparedOperator):
         held[:table.numel()].copy_(table)
         self._table = (ws, self.ntiles)
         self._space = (ctypes.c_void_p(ws.value + at), size)
+        # the memory that a call reads and writes, as runs in order that do not overlap
+        self._starts, self._ends = [], []
+        for lo, hi in sorted({(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                              for t in (*grads, *outs) if t.numel()}):
+            if self._ends and lo <= self._ends[-1]:
+                self._ends[-1] = max(self._ends[-1], hi)
+            else:
+                self._starts.append(lo)
+                self._ends.append(hi)
         super().__init__(None, (), dev, (grads, outs, held), made)
 
     def _norm_pointer(self, norm):
         _tensor("norm", norm, (_torch().float32,), self._keep[0][0].device)
         if norm.numel() != 1:
             raise ValueError(f"norm holds {norm.numel()} elements, expected 1")
-        return ctypes.c_void_p(norm.data_ptr())
+        at = norm.data_ptr()
+        run = bisect.bisect_left(self._starts, at + 4) - 1
+        if run >= 0 and self._ends[run] > at:
+            raise ValueError("norm lies in a gradient or an output")
+        return ctypes.c_void_p(at)
 
     def norm(self, norm, kind: str = "l2", stream=None):
         """norm <- the 2-norm ("l2") of the gradients, or their largest magnitude

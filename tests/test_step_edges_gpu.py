@@ -56,6 +56,33 @@ def test_long_sums_of_equal_squares(env, values, eleven_bits):
     torch.cuda.empty_cache()
 
 
+def test_norm_inside_of_what_is_read_or_written(env):
+    """Refused before anything is launched; neighbours are not."""
+    torch, vc, dev = env
+    flat, other = torch.ones(3000, device=dev), torch.ones(3000, device=dev)
+    grads, out = [flat[8:1000], flat[1000:1000], flat[1004:2000]], [other[0:992], other[992:992], other[992:1988]]
+    half = torch.ones(100, dtype=torch.bfloat16, device=dev)
+    elsewhere, in_place = vc.ClipPlan(grads, out), vc.ClipPlan(grads + [half])
+    bad = [flat[k:k + 1] for k in (8, 500, 999, 1004, 1999)]
+    for plan, inside in ((elsewhere, bad + [other[k:k + 1] for k in (0, 991, 992, 1987)]),
+                         (in_place, bad + [half[98:].view(torch.float32)])):
+        for norm in inside:
+            for call in (plan.norm, lambda n: plan.clip(1.0, n), lambda n: plan(1.0, n)):
+                with pytest.raises(ValueError, match="norm lies in"):
+                    call(norm)
+    torch.cuda.synchronize()
+    assert flat.eq(1).all() and other.eq(1).all() and half.eq(1).all()
+    want = (992 + 996) ** 0.5  # (the sum is exact)
+    for norm in [flat[k:k + 1] for k in (7, 1000, 1003, 2000)] + [other[1988:1989]]:
+        elsewhere.norm(norm)
+        assert abs(norm.item() - want) <= 2 * U * want
+        norm.fill_(1)
+    for norm in (flat[7:8], flat[1000], other[0:1]):
+        in_place.norm(norm)
+        assert abs(norm.item() - 2088 ** 0.5) <= 2 * U * 2088 ** 0.5
+        norm.fill_(1)
+
+
 # --------------------------------------------------------------- block norms --
 
 @pytest.mark.parametrize("gates", [1, 3, 40])
