@@ -156,7 +156,7 @@ def _embedding_backward(dy, ids, dweight, scale, first, padding, accumulate, wor
     ptr, code, tokens = _ids(ids, dev)
     ym = _matrix("dy", dy, _float_types(), dev)
     _shape("dy", ym, tokens, wm.cols)
-    if padding is not None and int(padding) < 0:
+    if padding is not None and not 0 <= int(padding) < 1 << 63:  # (what an id can be)
         raise ValueError(f"padding is {padding}, expected an id")
     need = embedding_backward_workspace(tokens, wm.rows, wm.cols)
     ws, size, held, made = _workspace(workspace, need, dev, stream, 256)

@@ -31,6 +31,21 @@ def rand(torch, dev, *shape, seed=0, dtype=None):
     return torch.randn(*shape, generator=g, device=dev).to(dtype or torch.bfloat16)
 
 
+# ---------------------------------------------------------------- embedding --
+
+def test_padding_beyond_64_bits(env):
+    """Not taken for the id that its low 64 bits are."""
+    torch, vc, dev = env
+    ids, dy = torch.tensor([5, 2 ** 63 - 1], device=dev), torch.ones(2, 8, device=dev)
+    for padding in (2 ** 63, 2 ** 64, 2 ** 64 + 5):
+        dw = torch.full((10, 8), 3.0, device=dev)
+        with pytest.raises(ValueError, match="expected an id"):
+            vc.vc_embedding_backward(dy, ids, dw, padding=padding)
+        assert dw.eq(3).all()
+    vc.vc_embedding_backward(dy, ids, dw, padding=2 ** 63 - 1)
+    assert dw[5].eq(1).all() and dw.sum().item() == 8
+
+
 # ------------------------------------------------------------------ clipping --
 
 @pytest.mark.parametrize("values", [500_002_816, 2 ** 31])
