@@ -136,7 +136,10 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kItems = 8;           // of a thread at a time
 constexpr int kChunk = kSortThreads * kItems;
-constexpr int kFewTokens = 4096;  // that one block sorts
+// Tokens that one block sorts (256 columns, by one block and by the cluster: 256 tokens
+// 11.3 and 13.0 us, 1024 12.0 and 13.4, 2048 13.2 and 13.9, 3000 16.4 and 15.9, 4096 17.2 and
+// 15.4, 6000 21.0 and 16.8).
+constexpr int kFewTokens = 4096;
 constexpr int kFillClusters = 14;   // beside the one that sorts: 15 run at a time
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kMarkRows = 16384;    // rows that a block marks at a time
@@ -621,6 +624,9 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_kernel(const __grid_consta
 // a window; where the row goes on for long, all warps of the block share its windows.
 // (The windows of a block are neighbours, of which few have such a row; the columns of
 // one window are different blocks'.)  7.7 us for 256 windows of 4096 columns.
+// kJoinLong: the windows up to which a warp does it alone (the gradient of 16384 x 1024 whose
+// rows have 4 windows each: 24.7 us by a warp, 27.6 by the block; 16: 25.2 and 25.7; 32: 26.7 and
+// 25.2; 128: 39.4 and 31.3).
 constexpr int kJoinWarps = 8, kJoinColumns = 128, kJoinLong = 16;
 
 template <int kWindow, bool kVec>

@@ -131,6 +131,9 @@ __global__ void __launch_bounds__(kLong) forward_long_kernel(const __grid_consta
     }
 }
 
+// The smallest shape that holds the row: with the next one 9120 x 256, RMS, take 6.6 us for 4.7,
+// x 512 14.5 for 6.2, x 1024 23.2 for 13.4, x 2048 46.6 for 26.1, x 4096 91.2 for 51.3, and layer
+// norms as much more.
 Shape forward_shape(int cols) {
     if (cols <= 256) return {32, 1, 1};
     if (cols <= 512) return {32, 2, 1};

@@ -378,8 +378,13 @@ class ClipPlan(PreparedOperator):
     """The norm of many gradients taken as one vector, and clipping to it: `grads`
     are contiguous float32 or bfloat16 tensors of one device (matrices and biases, views
     into buckets, the ranks' shards of a ReduceScatter), `out` where the clipped ones
-    go (None: in place).  Planned once (checks, aliasing, tiles); a call is two
-    launches.  The plan keeps the tensors' addresses: make a new one if they change.
+    go (None: in place).  No two gradients share memory where `out` is None, and no two
+    outputs do: a weight that is tied is given once.  A call is two launches.  The plan keeps
+    the tensors' addresses: make a new one if they change.  Planning (checks, aliasing, a table
+    of the tensors' parts of 16 KiB, its copy to the GPU) takes longer than a call: 0.1 ms
+    for 2 MB in 4 tensors, 1.4 ms for 368 MB in 145, 5 ms for 2.1 GB, 13 ms where the
+    tensors do not follow one another in memory.  So gradients that keep their places from step
+    to step (views into buckets) are planned once.
     Calls of one plan that may overlap on the GPU share its workspace and must be
     ordered by the caller.
 
