@@ -442,14 +442,15 @@ class ClipPlan(PreparedOperator):
         super().__init__(None, (), dev, (grads, outs, held), made)
 
     def _norm_pointer(self, norm):
-        _tensor("norm", norm, (_torch().float32,), self._keep[0][0].device)
+        # (before every call: with as few objects as it can do with)
+        _tensor("norm", norm, (_torch().float32,), self._device)
         if norm.numel() != 1:
             raise ValueError(f"norm holds {norm.numel()} elements, expected 1")
         at = norm.data_ptr()
         run = bisect.bisect_left(self._starts, at + 4) - 1
         if run >= 0 and self._ends[run] > at:
             raise ValueError("norm lies in a gradient or an output")
-        return ctypes.c_void_p(at)
+        return at
 
     def norm(self, norm, kind: str = "l2", stream=None):
         """norm <- the 2-norm ("l2") of the gradients, or their largest magnitude
